@@ -434,6 +434,179 @@ nm_status nm_obs_prune(const void *W_bf16, const float *H, int64_t rows, int64_t
  */
 nm_status nm_obs_release_workspace(void);
 
+/*
+ * ---- A paged KV cache in 4 bits and the attention over it ----
+ *
+ * What a decoding program needs between nm_spmv_qkv and the o projection (the
+ * pages prune only the linear layers: ai.info summary, "Methodology in Plain
+ * English" step 4). Grouped-query attention, causal, head_dim 64 or 128.
+ *
+ * Values: each group of 64 channels of one token and kv head is held as 64
+ * codes c of 4 bits and two fp16 parameters:
+ *     s   = fp16(bf16((max x - min x) * (1/15)))   (eight significant bits)
+ *     mid = fp16(min x + 8 s)
+ *     c   = clamp(rint((x - mid) / s), -8, 7) + 8     (8 when s = 0)
+ *     the value it stands for: mid + s (c - 8)
+ * in fp32 arithmetic (1/15 rounded to fp32), one rounding per operation. Finite |x| above 32768
+ * saturates. When k or v of a token holds a NaN or an infinity in one kv
+ * head, that head's K parameters become NaN (so every query that attends the
+ * token gives NaN) and its v is held finite (NaN as 0, infinities saturated),
+ * so that a query that does not attend it never sees it.
+ *
+ * Layout: the pool is [n_pages] pages; a page is [n_layers][n_kv_heads]
+ * [page_tokens / 16] cells of 16 tokens; with D = head_dim, G = D / 64, a cell
+ * of 16 (D + 8 G) bytes holds
+ *   K codes  [16 tokens][4 t][G groups][8 bytes]: byte b holds channels
+ *            64 g + 16 t + 2 b (low four bits) and + 1 (high four bits);
+ *   V codes  [G groups][8 e][4 t][2 p][2 f][2 r][2 bytes]: byte b holds channels
+ *            64 g + 8 e + 4 f + 2 b and + 1 of token 8 p + 2 t + r;
+ *   K params fp16 [16 tokens][G][s, mid];
+ *   V params fp16 [8 token pairs][G][s of both tokens, mid of both].
+ *
+ * Bookkeeping (device int32, written by the calls below):
+ *   info   [16]: [0] free pages; [1] result of the last nm_kv4_reserve or
+ *          nm_kv4_fork: 0 done, n > 0: n pages were lacking, -1: refused (an id
+ *          out of range or twice in the list, a destination that is not empty,
+ *          a sequence past max_pages) -- nothing is changed unless it is 0;
+ *          [2] pages moved by the last nm_kv4_compact; the rest is zero.
+ *   lens   [max_seqs]: tokens of each sequence.
+ *   refs   [n_pages]: how many table entries name the page (0: free).
+ *   tables [max_seqs][max_pages]: the pages of each sequence in order; -1 beyond.
+ * Only full pages are shared between sequences, so an append never writes a
+ * page that another sequence reads.
+ *
+ * Conventions, beside those at the top of this file:
+ *   - seqs: device int32 [n_seqs], rows of `tables`; NULL: 0 .. n_seqs - 1.
+ *   - starts: device int32 [n_seqs + 1], starts[0] = 0: the new tokens of the
+ *     i-th listed sequence are rows starts[i] .. starts[i+1] - 1 of the token
+ *     arrays; NULL: one token each (n_tokens = n_seqs).
+ *   - Token arrays are bf16 [n_tokens][heads][head_dim] with a token stride in
+ *     elements (a multiple of 8, at least heads * head_dim), so that slices of a
+ *     fused row can be passed. n_seqs is at most 1024; heads, pages and layers
+ *     any count that fits the tables.
+ *   - New tokens are the last ones of their sequence: nm_kv4_reserve has made
+ *     room for them and raised lens; token j of n_new is at position
+ *     lens - n_new + j.
+ *   - The tables are checked on the device: an id, length, start or page out
+ *     of range is not followed (a token at such a place is neither written nor
+ *     attended, its row gives zeros) and nm_device_status reports NM_ERR_BOUNDS.
+ *   - workspace: device memory of nm_kv4_workspace_bytes(), 256-byte aligned and
+ *     zeroed once before its first use (nm_kv4_init does). Calls with the same
+ *     workspace, or that change the same bookkeeping, must not overlap on the
+ *     GPU; calls with caches of their own may.
+ *   - All calls are asynchronous, allocate nothing but the library's per-device
+ *     scratch (for its status word), and can be captured in a CUDA graph.
+ */
+typedef struct nm_kv4_cache {
+    void *pool;          /* device, n_pages * nm_kv4_page_bytes() bytes, 128-byte aligned */
+    int64_t n_pages;
+    int32_t page_tokens; /* 16, 32, 64 or 128 */
+    int32_t n_layers;
+    int32_t n_kv_heads;
+    int32_t head_dim;    /* 64 or 128 */
+    int32_t max_seqs;
+    int32_t max_pages;   /* pages of one sequence at most */
+    int32_t *info;       /* device int32 [16] */
+    int32_t *lens;       /* device int32 [max_seqs] */
+    int32_t *refs;       /* device int32 [n_pages] */
+    int32_t *tables;     /* device int32 [max_seqs][max_pages] */
+    void *workspace;
+    int64_t workspace_bytes;
+} nm_kv4_cache;
+
+/* Bytes of one page, and of the workspace of a cache with this head_dim and
+ * page count; 0 for sizes that the calls refuse. */
+int64_t nm_kv4_page_bytes(int page_tokens, int n_layers, int n_kv_heads, int head_dim);
+int64_t nm_kv4_workspace_bytes(int64_t n_pages, int head_dim);
+
+/* Empties the cache: lens, refs and info cleared (all pages free), tables -1,
+ * the workspace's counters zeroed. The pool is left as it is. */
+nm_status nm_kv4_init(const nm_kv4_cache *cache, void *stream);
+
+/*
+ * nm_kv4_reserve -- makes room for new tokens: lens[s] grows by the sequence's
+ * new tokens, and pages are added to its table as it needs them. Free pages are
+ * taken lowest index first, in the order of the list. All or nothing: info[1].
+ */
+nm_status nm_kv4_reserve(const nm_kv4_cache *cache, const int32_t *seqs, const int32_t *starts, int n_seqs,
+                         void *stream);
+
+/*
+ * nm_kv4_fork -- dst[i] (empty) becomes a copy of src[i]: the full pages are
+ * shared (refs + 1); the cells of the partial last page that hold tokens are
+ * copied, in every layer, into a page of its own (lowest free page first, in
+ * the order of the list). One source may be forked several times in a call; a
+ * sequence cannot be both. All or nothing: info[1].
+ */
+nm_status nm_kv4_fork(const nm_kv4_cache *cache, const int32_t *src, const int32_t *dst, int n, void *stream);
+
+/* nm_kv4_free -- empties the listed sequences (refs - 1 for each of their
+ * pages; those that reach 0 are free). An empty sequence may be listed. */
+nm_status nm_kv4_free(const nm_kv4_cache *cache, const int32_t *seqs, int n, void *stream);
+
+/*
+ * nm_kv4_compact -- moves pages so that the n in use are pages 0 .. n-1: the
+ * k-th free page below n takes the contents and references of the k-th used
+ * page at or above n, and the tables follow. A pool can then be cut or grown.
+ */
+nm_status nm_kv4_compact(const nm_kv4_cache *cache, void *stream);
+
+/*
+ * nm_kv4_copy_pages -- copies whole pages: page src_pages[i] of `src` to page
+ * dst_pages[i] of `dst` (which may be the same cache, or another with the same
+ * page bytes). No page may be both a source and a destination, or twice a
+ * destination. Only the pools are touched. A page out of range is skipped.
+ */
+nm_status nm_kv4_copy_pages(const nm_kv4_cache *src, const int32_t *src_pages, const nm_kv4_cache *dst,
+                            const int32_t *dst_pages, int64_t n, void *stream);
+
+/*
+ * nm_kv4_append -- writes the new tokens' k and v to the cache of one layer,
+ * rotating k, and rotates q.
+ *   k, v : bf16 [n_tokens][n_kv_heads][head_dim] (read).
+ *   q    : bf16 [n_tokens][n_q_heads][head_dim] (read) or NULL; q_out: the same
+ *          shape (written; may be q itself, with the same stride).
+ *   rope : fp32 [rope_rows][head_dim], 16-byte aligned, row p: cos of the
+ *          head_dim / 2 angles of position p, then sin; NULL: no rotation (q, if
+ *          given, is copied). Channels i and i + head_dim / 2 are turned together:
+ *          (a cos - b sin, b cos + a sin), each operation rounded to fp32. k goes
+ *          into the codes from fp32; q is rounded to bf16.
+ * A position at or past rope_rows is reported as NM_ERR_BOUNDS; its token is not
+ * written and its q_out row is zero.
+ */
+nm_status nm_kv4_append(const nm_kv4_cache *cache, int layer, const int32_t *seqs, const int32_t *starts, int n_seqs,
+                        int64_t n_tokens, const void *k_bf16, int64_t k_stride, const void *v_bf16, int64_t v_stride,
+                        const void *q_bf16, int64_t q_stride, int n_q_heads, void *q_out_bf16, int64_t q_out_stride,
+                        const float *rope, int64_t rope_rows, void *stream);
+
+/*
+ * nm_kv4_read -- the values that the cache holds for the last tokens of each
+ * sequence (as many as starts says), k and v each [n_tokens][n_kv_heads]
+ * [head_dim] contiguous in bf16, or fp32 with f32 != 0; either may be NULL.
+ */
+nm_status nm_kv4_read(const nm_kv4_cache *cache, int layer, const int32_t *seqs, const int32_t *starts, int n_seqs,
+                      int64_t n_tokens, void *k, void *v, int f32, void *stream);
+
+/*
+ * nm_kv4_attention -- attention of the new tokens over the cache of one layer.
+ *   q   : bf16 [n_tokens][n_q_heads][head_dim] (read), n_q_heads a multiple of
+ *         n_kv_heads, at most 64 of them to a kv head.
+ *   out : bf16, as q (written). lse: fp32 [n_tokens][n_q_heads] or NULL.
+ *   A query at position p attends positions 0 .. p of its sequence:
+ *     out = sum_t e^(scale q.k_t) v_t / sum_t e^(scale q.k_t),
+ *     lse = log sum_t e^(scale q.k_t).
+ *   A query with nothing to attend gives out 0 and lse -inf.
+ *   max_new: a bound on the new tokens of one sequence that the caller expects; it
+ *   chooses the kernel, any value >= 1 gives the same results to rounding.
+ * Scores are exact products with fp32 sums; the softmax statistics, its sums
+ * and the output are held in fp32, the weights are rounded to fp16 for the
+ * product with v. The order of the sums depends on the lengths and the device
+ * alone: results repeat bit for bit.
+ */
+nm_status nm_kv4_attention(const nm_kv4_cache *cache, int layer, const int32_t *seqs, const int32_t *starts,
+                           int n_seqs, int64_t n_tokens, int64_t max_new, const void *q_bf16, int64_t q_stride,
+                           int n_q_heads, float scale, void *out_bf16, int64_t out_stride, float *lse, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

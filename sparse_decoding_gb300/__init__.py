@@ -43,7 +43,10 @@ EXPORTS = ("nm_abi_version", "nm_status_str", "nm_pack_host", "nm_select", "nm_p
            "nm_spmv_f32out", "dense_gemv", "dense_gemv_f32out", "nm_spmv_stack", "dense_gemv_stack",
            "nm_device_status", "nm_spmv_noalloc", "nm_stack_plan_create", "nm_stack_plan_run",
            "nm_stack_plan_destroy", "nm_pack_swiglu", "nm_spmv_swiglu", "nm_obs_hessian", "nm_obs_prune",
-           "nm_spmv_f32out_atomic", "nm_select_pack", "nm_spmv_qkv", "nm_obs_release_workspace")
+           "nm_spmv_f32out_atomic", "nm_select_pack", "nm_spmv_qkv", "nm_obs_release_workspace",
+           "nm_kv4_page_bytes", "nm_kv4_workspace_bytes", "nm_kv4_init", "nm_kv4_reserve", "nm_kv4_fork",
+           "nm_kv4_free", "nm_kv4_compact", "nm_kv4_copy_pages", "nm_kv4_append", "nm_kv4_read",
+           "nm_kv4_attention")
 
 
 class NmError(RuntimeError):
@@ -58,6 +61,15 @@ class NmLinear(ctypes.Structure):
                 ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("flags", ctypes.c_uint32), ("y_k", ctypes.c_void_p),
                 ("y_v", ctypes.c_void_p), ("rows_q", ctypes.c_int64), ("rows_k", ctypes.c_int64)]
+
+
+class NmKv4Cache(ctypes.Structure):
+    """Mirror of ``nm_kv4_cache`` in include/nmspmv.h."""
+    _fields_ = [("pool", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_tokens", ctypes.c_int32),
+                ("n_layers", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("max_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("info", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("tables", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -98,6 +110,17 @@ def lib() -> ctypes.CDLL:
         "nm_obs_hessian": ([p, i64, i64, p, i32, p], i32),
         "nm_obs_prune": ([p, p, i64, i64, i32, i32, ctypes.c_float, ctypes.c_uint, p, p, p, p], i32),
         "nm_obs_release_workspace": ([], i32),
+        "nm_kv4_page_bytes": ([i32, i32, i32, i32], i64),
+        "nm_kv4_workspace_bytes": ([i64, i32], i64),
+        "nm_kv4_init": ([p, p], i32),
+        "nm_kv4_reserve": ([p, p, p, i32, p], i32),
+        "nm_kv4_fork": ([p, p, p, i32, p], i32),
+        "nm_kv4_free": ([p, p, i32, p], i32),
+        "nm_kv4_compact": ([p, p], i32),
+        "nm_kv4_copy_pages": ([p, p, p, p, i64, p], i32),
+        "nm_kv4_append": ([p, i32, p, p, i32, i64, p, i64, p, i64, p, i64, i32, p, i64, p, i64, p], i32),
+        "nm_kv4_read": ([p, i32, p, p, i32, i64, p, p, i32, p], i32),
+        "nm_kv4_attention": ([p, i32, p, p, i32, i64, i64, p, i64, i32, ctypes.c_float, p, i64, p, p], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -402,3 +425,192 @@ def obs_prune(W: torch.Tensor, H: torch.Tensor, N: int, M: int, percdamp: float 
 def obs_release_workspace():
     """Return the memory the OBS calls keep for their workspaces on the current device."""
     _check(lib().nm_obs_release_workspace(), "nm_obs_release_workspace")
+
+
+# --- the 4-bit paged KV cache ---------------------------------------------------------
+
+def _pad4(n: int) -> int:
+    return (n + 3) // 4 * 4
+
+
+class Kv4Cache:
+    """A paged KV cache in 4 bits (``nm_kv4_*``): grouped-query attention's keys and values of
+    every layer, in pages of ``page_tokens`` tokens (16, 32, 64 or 128), head_dim 64 or 128.
+
+    ``pool`` (uint8 [n_pages][page bytes]) holds the pages and ``book`` (int32) the bookkeeping:
+    the views ``info`` [16], ``lens`` [max_seqs], ``refs`` [n_pages] and ``tables``
+    [max_seqs][max_pages] (see include/nmspmv.h). Both are made here, empty, or taken over as
+    they are. All calls are asynchronous on the current stream; calls on one cache must not
+    overlap on the GPU. ``seqs`` (int32, CUDA) names the sequences of a call, None: 0, 1, ...;
+    ``starts`` (int32 [n + 1], CUDA) bounds each one's new tokens in the token tensors, None: one
+    token each. Token tensors are bf16 [tokens][heads][head_dim] or [tokens][heads * head_dim];
+    the token stride is free.
+    """
+
+    def __init__(self, n_pages: int, page_tokens: int, n_layers: int, n_kv_heads: int, head_dim: int, max_seqs: int,
+                 max_pages: int, device: Optional[torch.device] = None, pool: Optional[torch.Tensor] = None,
+                 book: Optional[torch.Tensor] = None):
+        L = lib()
+        per = L.nm_kv4_page_bytes(page_tokens, n_layers, n_kv_heads, head_dim)
+        if per == 0 or n_pages < 0 or max_seqs < 0 or max_pages < 0:
+            raise NmError(NM_ERR_UNSUPPORTED, "Kv4Cache")
+        given = pool if pool is not None else book
+        device = given.device if given is not None else torch.device(device if device is not None else "cuda")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.n_pages, self.page_tokens = device, n_pages, page_tokens
+        self.n_layers, self.n_kv_heads, self.head_dim = n_layers, n_kv_heads, head_dim
+        ints = self.book_ints(n_pages, max_seqs, max_pages)
+        fresh = book is None
+        self.pool = torch.empty(n_pages, per, dtype=torch.uint8, device=device) if pool is None else \
+            _cuda(pool, torch.uint8, "pool")
+        self.book = torch.empty(ints, dtype=torch.int32, device=device) if fresh else _cuda(book, torch.int32, "book")
+        if tuple(self.pool.shape) != (n_pages, per) or self.book.numel() != ints:
+            raise ValueError(f"pool must be [{n_pages}][{per}] and book have {ints} ints")
+        if self.pool.device != device or self.book.device != device:
+            raise ValueError("pool and book must be on one device")
+        a = 16 + _pad4(max_seqs)
+        b = a + _pad4(n_pages)
+        self.info, self.lens, self.refs = self.book[:16], self.book[16:16 + max_seqs], self.book[a:a + n_pages]
+        self.tables = self.book[b:b + max_seqs * max_pages].view(max_seqs, max_pages)
+        self._work = torch.zeros(L.nm_kv4_workspace_bytes(n_pages, head_dim), dtype=torch.uint8, device=device)
+        base = self.book.data_ptr()
+        self._c = NmKv4Cache(self.pool.data_ptr(), n_pages, page_tokens, n_layers, n_kv_heads, head_dim, max_seqs,
+                             max_pages, base, base + 64, base + 4 * a, base + 4 * b, self._work.data_ptr(),
+                             self._work.numel())
+        self._ref = ctypes.byref(self._c)
+        if fresh:
+            _check(L.nm_kv4_init(self._ref, self._s()), "nm_kv4_init")
+
+    @staticmethod
+    def book_ints(n_pages: int, max_seqs: int, max_pages: int) -> int:
+        """Ints of ``book``: info, lens, refs and tables, each padded to a multiple of four."""
+        return 16 + _pad4(max_seqs) + _pad4(n_pages) + _pad4(max_seqs * max_pages)
+
+    def _s(self) -> int:
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError(f"the cache is on {self.device}: make it the current device")
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def _ids(self, t: Optional[torch.Tensor], name: str):
+        if t is None:
+            return None
+        _cuda(t, torch.int32, name)
+        if t.device != self.device or t.dim() != 1:
+            raise ValueError(f"{name} must be one-dimensional on {self.device}")
+        return t.data_ptr()
+
+    def _batch(self, seqs, starts, n_tokens=None):
+        """(seqs pointer, starts pointer, n_seqs) of a call."""
+        n = starts.numel() - 1 if starts is not None else seqs.numel() if seqs is not None else n_tokens
+        if n is None or n < 0 or (seqs is not None and seqs.numel() != n) or \
+                (starts is None and n_tokens is not None and n != n_tokens):
+            raise ValueError("seqs, starts and the token count do not agree")
+        return self._ids(seqs, "seqs"), self._ids(starts, "starts"), n
+
+    def _tokens(self, t: torch.Tensor, name: str):
+        """(pointer, token stride, heads) of a token tensor."""
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != self.device:
+            raise TypeError(f"{name} must be a bfloat16 tensor on {self.device}")
+        D = self.head_dim
+        if t.dim() == 3 and t.shape[2] == D and t.stride(2) == 1 and (t.stride(1) == D or t.shape[1] == 1):
+            heads = t.shape[1]
+        elif t.dim() == 2 and t.shape[1] % D == 0 and t.stride(1) == 1:
+            heads = t.shape[1] // D
+        else:
+            raise ValueError(f"{name} must be [tokens][heads][{D}] or [tokens][heads * {D}], contiguous in a token")
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * D, heads
+
+    def reserve(self, seqs: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
+                n: Optional[int] = None) -> None:
+        """Room for the new tokens of each sequence (``n`` sequences with both None): lens grow, pages
+        are added. All or nothing; ``info[1]`` (on the device) tells."""
+        p, st, m = self._batch(seqs, starts, n)
+        _check(lib().nm_kv4_reserve(self._ref, p, st, m, self._s()), "nm_kv4_reserve")
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor) -> None:
+        """The empty sequences dst become copies of src, sharing its full pages. ``info[1]`` tells."""
+        if src.numel() != dst.numel():
+            raise ValueError("src and dst must have the same length")
+        _check(lib().nm_kv4_fork(self._ref, self._ids(src, "src"), self._ids(dst, "dst"), src.numel(), self._s()),
+               "nm_kv4_fork")
+
+    def free(self, seqs: torch.Tensor) -> None:
+        """Empties the listed sequences."""
+        _check(lib().nm_kv4_free(self._ref, self._ids(seqs, "seqs"), seqs.numel(), self._s()), "nm_kv4_free")
+
+    def compact(self) -> None:
+        """Moves the pages in use to the front of the pool; the tables follow."""
+        _check(lib().nm_kv4_compact(self._ref, self._s()), "nm_kv4_compact")
+
+    def copy_pages(self, src_pages: torch.Tensor, dst_pages: torch.Tensor, dst: Optional["Kv4Cache"] = None) -> None:
+        """Copies whole pages of this pool to pages of ``dst``'s (default: this one)."""
+        dst = self if dst is None else dst
+        if src_pages.numel() != dst_pages.numel() or dst.device != self.device:
+            raise ValueError("page lists must have the same length, and the caches one device")
+        _check(lib().nm_kv4_copy_pages(self._ref, self._ids(src_pages, "src_pages"), dst._ref,
+                                       self._ids(dst_pages, "dst_pages"), src_pages.numel(), self._s()),
+               "nm_kv4_copy_pages")
+
+    def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, q: Optional[torch.Tensor] = None,
+               rope: Optional[torch.Tensor] = None, seqs: Optional[torch.Tensor] = None,
+               starts: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None):
+        """Writes the new tokens' k (rotated by ``rope``, fp32 [positions][head_dim]: cos, then sin) and v to
+        the cache; returns q rotated (None without q). q_out may be q itself."""
+        kp, ks, kh = self._tokens(k, "k")
+        vp, vs, vh = self._tokens(v, "v")
+        T = k.shape[0]
+        if kh != self.n_kv_heads or vh != kh or v.shape[0] != T:
+            raise ValueError(f"k and v must have {self.n_kv_heads} heads and the same tokens")
+        qp = op = None
+        qs = os_ = qh = 0
+        if q is not None:
+            qp, qs, qh = self._tokens(q, "q")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            op, os_, oh = self._tokens(q_out, "q_out")
+            if q.shape[0] != T or q_out.shape[0] != T or oh != qh:
+                raise ValueError("q and q_out must have the tokens of k, and the same heads")
+        rp, rows = None, 0
+        if rope is not None:
+            _cuda(rope, torch.float32, "rope")
+            if rope.dim() != 2 or rope.shape[1] != self.head_dim or rope.device != self.device:
+                raise ValueError(f"rope must be [positions][{self.head_dim}] on {self.device}")
+            rp, rows = rope.data_ptr(), rope.shape[0]
+        sp, st, n = self._batch(seqs, starts, T if starts is None else None)
+        _check(lib().nm_kv4_append(self._ref, layer, sp, st, n, T, kp, ks, vp, vs, qp, qs, qh, op, os_, rp, rows,
+                                   self._s()), "nm_kv4_append")
+        return q_out if q is not None else None
+
+    def read(self, layer: int, n_tokens: int, seqs: Optional[torch.Tensor] = None,
+             starts: Optional[torch.Tensor] = None, f32: bool = False):
+        """The values held for the last tokens of each sequence: (k, v), [n_tokens][n_kv_heads][head_dim]
+        in bf16 (fp32 with f32)."""
+        sp, st, n = self._batch(seqs, starts, n_tokens if starts is None else None)
+        shape = (n_tokens, self.n_kv_heads, self.head_dim)
+        dt = torch.float32 if f32 else torch.bfloat16
+        k, v = torch.empty(shape, dtype=dt, device=self.device), torch.empty(shape, dtype=dt, device=self.device)
+        _check(lib().nm_kv4_read(self._ref, layer, sp, st, n, n_tokens, k.data_ptr(), v.data_ptr(), int(f32),
+                                 self._s()), "nm_kv4_read")
+        return k, v
+
+    def attention(self, layer: int, q: torch.Tensor, seqs: Optional[torch.Tensor] = None,
+                  starts: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
+                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse: bool = False):
+        """Causal attention of the new tokens' q over the cache of one layer; bf16, shaped as q.
+
+        ``max_new``: the most new tokens a sequence has, where the caller knows (it chooses the kernel only).
+        ``scale`` defaults to head_dim ** -0.5. lse=True: (out, lse), lse fp32 [tokens][heads]."""
+        qp, qs, qh = self._tokens(q, "q")
+        T = q.shape[0]
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        op, os_, oh = self._tokens(out, "out")
+        if out.shape[0] != T or oh != qh:
+            raise ValueError("out must have q's tokens and heads")
+        sp, st, n = self._batch(seqs, starts, T if starts is None else None)
+        ls = torch.empty(T, qh, dtype=torch.float32, device=q.device) if lse else None
+        _check(lib().nm_kv4_attention(self._ref, layer, sp, st, n, T, max(T, 1) if max_new is None else max_new, qp,
+                                      qs, qh, self.head_dim ** -0.5 if scale is None else scale, op, os_,
+                                      ls.data_ptr() if lse else None, self._s()), "nm_kv4_attention")
+        return (out, ls) if lse else out

@@ -4,21 +4,10 @@
 #include <new>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "kernels.h"
 #include "streamk.cuh"
 
 namespace nm {
-
-// An NVTX range over one C entry point (visible in a timeline profiler; a
-// no-op when no tool is attached).
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
 
 constexpr int kMaxDevices = 64;
 

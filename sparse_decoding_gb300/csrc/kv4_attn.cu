@@ -1,0 +1,580 @@
+// kv4_attn.cu -- attention of few queries over the 4-bit paged cache (decode
+// steps and drafted tokens).
+//
+// For one sequence and kv head, the rows are its queries times the query heads
+// that share the kv head; a tile holds 8 NT of them. A warp takes the cache one
+// cell (16 tokens) at a time:
+//
+//   S^T [16 tokens][rows] = codes(K) Q^T      m16n8k16, A = codes - 8 as fp16
+//   s = (scale_t S^T + mid_t sum(q)) per group of 64 channels, in fp32
+//   p = 2^(s - m + 6)                         m: the row's running maximum
+//   O^T [channels][rows] += V^T P^T           A = V as fp16, B = P as fp16
+//
+// The codes are exact in fp16, q is made so by a power of two per row, and the
+// scale is applied in fp32, so scores carry fp32 rounding only. V's values are
+// rounded once to fp16 (2^-11), like the weights p. m is raised only when a score
+// passes it by 2^8 (p <= 2^14 stays inside fp16, and weights down to 2^-30 of
+// the largest keep a digit): the warp votes per cell instead of reducing.
+//
+// The layout of a cell is the operands' own: lane l reads 16 bytes at 16 l, so K
+// and V need no transposition on the way to the registers.
+//
+// The cells of all (sequence, kv head, tile) segments are one line, cut evenly
+// over the CTAs of one wave, whatever the lengths; a CTA's warps take the cells of
+// a piece in turn and are joined in shared memory. A segment that was cut is
+// joined by the last of its CTAs, in CTA order, from the workspace.
+#include <mutex>
+#include <type_traits>
+
+#include "kv4.cuh"
+
+namespace nm {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int64_t kMinShare = 16; // cells of a CTA at least: two for each warp
+constexpr float kShift = 6.0f;    // p = 2^(s - m + kShift)
+constexpr float kSlack = 8.0f;    // a score may pass m by this much
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *(__half2 *)&x; }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *(uint32_t *)&x; }
+
+// Nibble N (0..3) of both halves of w, minus `bias`, as two fp16 numbers: the
+// bits under an exponent of 2^10 are 1024 + n (or 1024 + 16 n), so the result is
+// exact.
+template <int N> __device__ __forceinline__ __half2 nibble(uint32_t w, float bias)
+{
+    const uint32_t x = N >= 2 ? w >> 8 : w;
+    if (N % 2 == 0)
+        return __hadd2(as_half2((x & 0x000F000Fu) | 0x64006400u), __float2half2_rn(-1024.0f - bias));
+    return __hfma2(as_half2((x & 0x00F000F0u) | 0x64006400u), __float2half2_rn(0.0625f),
+                   __float2half2_rn(-64.0f - bias));
+}
+
+// A cell in a lane's registers.
+template <int D> struct CellRegs {
+    static constexpr int G = Kv4Cell<D>::G;
+    uint32_t k[2][2 * G]; // tokens g, g + 8: 16 channels of each group
+    uint32_t v[G][4];     // (quad 0, pair 0), (quad 1, pair 0), (quad 0, pair 1), (quad 1, pair 1)
+    uint32_t kp[2][G];    // tokens g, g + 8: (s, mid)
+    uint32_t vp[2][2 * G]; // token pairs t, t + 4: per group (s, s), (mid, mid)
+};
+
+template <int D> __device__ __forceinline__ void load_cell(CellRegs<D> &r, const uint8_t *cell, int lane)
+{
+    using C = Kv4Cell<D>;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (D == 128) {
+            const uint4 x = ldg_nc128(cell + e * 512 + lane * 16);
+            r.k[e][0] = x.x;
+            r.k[e][1] = x.y;
+            r.k[e][2 * C::G - 2] = x.z;
+            r.k[e][2 * C::G - 1] = x.w;
+            const uint2 p = *(const uint2 *)(cell + C::kKp + (g + 8 * e) * 8);
+            r.kp[e][0] = p.x;
+            r.kp[e][C::G - 1] = p.y;
+            const uint4 q = *(const uint4 *)(cell + C::kVp + (t + 4 * e) * 16);
+            r.vp[e][0] = q.x;
+            r.vp[e][1] = q.y;
+            r.vp[e][2 * C::G - 2] = q.z;
+            r.vp[e][2 * C::G - 1] = q.w;
+        } else {
+            const uint2 x = *(const uint2 *)(cell + e * 256 + lane * 8);
+            r.k[e][0] = x.x;
+            r.k[e][1] = x.y;
+            r.kp[e][0] = *(const uint32_t *)(cell + C::kKp + (g + 8 * e) * 4);
+            const uint2 q = *(const uint2 *)(cell + C::kVp + (t + 4 * e) * 8);
+            r.vp[e][0] = q.x;
+            r.vp[e][1] = q.y;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < C::G; ++e) {
+        const uint4 x = ldg_nc128(cell + C::kV + e * 512 + lane * 16);
+        r.v[e][0] = x.x;
+        r.v[e][1] = x.y;
+        r.v[e][2] = x.z;
+        r.v[e][3] = x.w;
+    }
+}
+
+struct AttnArgs {
+    int layer, ratio; // ratio: query heads of one kv head
+    int n_q_heads;
+    const uint16_t *q;
+    int64_t q_stride;
+    float scale;
+    uint16_t *out;
+    int64_t out_stride;
+    float *lse;
+    uint32_t *counters;
+    float *partials;
+};
+
+// Floats of one part in the workspace: m and l of each row, then O.
+template <int D, int NT> constexpr int part_floats() { return 8 * NT * (D + 2); }
+
+template <int D, int NT> struct Smem {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kPitch = D + 4;
+    // [kWarps][kRows] m, l; [kWarps][kRows][kPitch] o
+    static constexpr int kMerge = kWarps * kRows * (2 + kPitch) * 4;
+};
+
+__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+    attn_rows_kernel(const Kv4 c, const Kv4Batch b, const AttnArgs a)
+{
+    constexpr int G = Kv4Cell<D>::G;
+    constexpr int RT = 8 * NT;
+    constexpr int KS = 4 * G; // k-steps of 16 channels
+    using SM = Smem<D, NT>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *const sm_m = (float *)smem, *const sm_l = sm_m + kWarps * RT, *const sm_o = sm_l + kWarps * RT;
+    int64_t *const pre = (int64_t *)(smem + SM::kMerge);     // [n_seqs + 1]
+    Kv4Seq *const seqs = (Kv4Seq *)(pre + b.n_seqs + 1);     // [n_seqs]
+    __shared__ uint32_t s_last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+
+    // the segments of each sequence, and where they start on the line of cells
+    for (int i = tid; i < b.n_seqs; i += kThreads) {
+        const Kv4Seq s = kv4_seq(c, b, i, blockIdx.x == 0);
+        seqs[i] = s;
+        const int64_t cells = s.n_new == 0 ? 0 : s.len > 0 ? (s.len + kKv4Cell - 1) / kKv4Cell : 1;
+        pre[i + 1] = cells * ceil_div((int64_t)s.n_new * a.ratio, RT) * c.n_kv_heads;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int64_t sum = 0;
+        for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
+            int64_t x = i0 + lane < b.n_seqs ? pre[i0 + lane + 1] : 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            if (i0 + lane < b.n_seqs)
+                pre[i0 + lane + 1] = sum + x;
+            sum += __shfl_sync(~0u, x, 31);
+        }
+        if (lane == 0)
+            pre[0] = 0;
+    }
+    __syncthreads();
+    const int64_t total = pre[b.n_seqs];
+    int64_t share = ceil_div(total, gridDim.x);
+    share = share < kMinShare ? kMinShare : share;
+    const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share < total ? lo + share : total;
+
+    for (int64_t pos = lo; pos < hi;) {
+        int i;
+        {
+            int l = 0, h = b.n_seqs; // pre[l] <= pos < pre[h]
+            while (h - l > 1) {
+                const int m = (l + h) >> 1;
+                if (pre[m] <= pos)
+                    l = m;
+                else
+                    h = m;
+            }
+            i = l;
+        }
+        const Kv4Seq s = seqs[i];
+        const int cells = s.len > 0 ? (s.len + kKv4Cell - 1) / kKv4Cell : 1;
+        const int64_t seg = (pos - pre[i]) / cells;
+        const int64_t seg_lo = pre[i] + seg * cells, seg_hi = seg_lo + cells;
+        const int c0 = (int)(pos - seg_lo);
+        const int c1 = (int)((hi < seg_hi ? hi : seg_hi) - seg_lo);
+        const int64_t tiles = ceil_div((int64_t)s.n_new * a.ratio, RT);
+        const int head = (int)(seg / tiles);
+        const int64_t row0 = (seg % tiles) * RT;        // first row of the tile
+        const int64_t rows = (int64_t)s.n_new * a.ratio; // rows of the sequence and kv head
+
+        // Q as the B operand: row g of each n-tile, channels 64 grp + 16 t ..
+        uint32_t qb[NT][KS][2];
+        float rowscale[NT][2], qsum[NT][2][G];
+        int limit[NT][2]; // tokens that rows 2 t, 2 t + 1 attend
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int64_t row = row0 + 8 * j + g;
+            float x[G][16];
+            float top = 0.0f;
+            if (row < rows) {
+                const int64_t token = s.first + row / a.ratio;
+                const uint16_t *q = a.q + token * a.q_stride + ((int64_t)head * a.ratio + row % a.ratio) * D;
+#pragma unroll
+                for (int e = 0; e < G; ++e)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const uint4 w = ldg_nc128(q + 64 * e + 16 * t + 8 * f);
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            x[e][8 * f + 2 * n] = bf16lo_to_f32(ws[n]);
+                            x[e][8 * f + 2 * n + 1] = bf16hi_to_f32(ws[n]);
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int e = 0; e < G; ++e)
+#pragma unroll
+                    for (int n = 0; n < 16; ++n)
+                        x[e][n] = 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+                    top = fmaxf(top, fabsf(x[e][n]));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            // 2^-e brings the row's largest magnitude into [1, 2): exact in fp16
+            // but for parts below 2^-24 of it
+            uint32_t e2 = (__float_as_uint(top) >> 23) & 0xFFu;
+            e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
+            const float down = __uint_as_float((254u - e2) << 23), up = __uint_as_float(e2 << 23);
+            float sums[G];
+#pragma unroll
+            for (int e = 0; e < G; ++e) {
+                sums[e] = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    x[e][n] = __half2float(__float2half_rn(x[e][n] * down));
+                    sums[e] += x[e][n];
+                }
+                sums[e] += __shfl_xor_sync(~0u, sums[e], 1);
+                sums[e] += __shfl_xor_sync(~0u, sums[e], 2);
+                // word f of 8 channels: nibble pairs (0,4),(1,5) and (2,6),(3,7) are two k-steps
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float *y = &x[e][8 * f + 2 * h];
+                        qb[j][4 * e + 2 * f + h][0] = pack_half2(y[0], y[4]);
+                        qb[j][4 * e + 2 * f + h][1] = pack_half2(y[1], y[5]);
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int from = (2 * t + n) * 4;
+                rowscale[j][n] = __shfl_sync(~0u, up, from) * (a.scale * kLog2e);
+#pragma unroll
+                for (int e = 0; e < G; ++e)
+                    qsum[j][n][e] = __shfl_sync(~0u, sums[e], from);
+                const int64_t r = row0 + 8 * j + 2 * t + n;
+                limit[j][n] = r < rows ? s.len - s.n_new + (int)(r / a.ratio) + 1 : 0;
+            }
+        }
+
+        float o[NT][G][4][4] = {}; // [n-tile][group][m-tile][fragment]
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.0f;
+
+        const int shift = c.page_shift - 4;
+        for (int cell = c0 + warp; cell < c1; cell += kWarps) {
+            if (s.len == 0)
+                break;
+            const int page = kv4_page(c, s.row, cell >> shift);
+            if (page < 0) {
+                if (lane == 0)
+                    kv4_bad(c);
+                continue;
+            }
+            CellRegs<D> r;
+            load_cell<D>(r, c.pool + kv4_cell_offset<D>(c, page, a.layer, head, cell & ((1 << shift) - 1)), lane);
+            const int tok = cell * kKv4Cell;
+
+            // scores
+            float acc[NT][G][4] = {};
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    uint32_t af[2][4];
+                    const uint32_t w0 = r.k[0][2 * e + f], w1 = r.k[1][2 * e + f];
+                    af[0][0] = as_u32(nibble<0>(w0, 8.0f));
+                    af[0][1] = as_u32(nibble<0>(w1, 8.0f));
+                    af[0][2] = as_u32(nibble<1>(w0, 8.0f));
+                    af[0][3] = as_u32(nibble<1>(w1, 8.0f));
+                    af[1][0] = as_u32(nibble<2>(w0, 8.0f));
+                    af[1][1] = as_u32(nibble<2>(w1, 8.0f));
+                    af[1][2] = as_u32(nibble<3>(w0, 8.0f));
+                    af[1][3] = as_u32(nibble<3>(w1, 8.0f));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+                            mma16816(acc[j][e], af[h], qb[j][4 * e + 2 * f + h][0], qb[j][4 * e + 2 * f + h][1]);
+                }
+            float ks[2][G], km[2][G];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < G; ++e) {
+                    ks[u][e] = __low2float(as_half2(r.kp[u][e]));
+                    km[u][e] = __high2float(as_half2(r.kp[u][e]));
+                }
+            float sc[NT][4];
+            bool above = false;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int u = f >> 1, n = f & 1; // token g + 8 u, row 2 t + n
+                    float x = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < G; ++e)
+                        x = fmaf(ks[u][e], acc[j][e][f], fmaf(km[u][e], qsum[j][n][e], x));
+                    x *= rowscale[j][n];
+                    sc[j][f] = tok + g + 8 * u < limit[j][n] ? x : -INFINITY;
+                    above |= sc[j][f] > m[j][n] + kSlack;
+                }
+            if (__any_sync(~0u, above)) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        float x = fmaxf(m[j][n], fmaxf(sc[j][n], sc[j][n + 2]));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                        const float by = x == m[j][n] ? 1.0f : exp2_approx(m[j][n] - x);
+                        m[j][n] = x;
+                        l[j][n] *= by;
+#pragma unroll
+                        for (int e = 0; e < G; ++e)
+#pragma unroll
+                            for (int i4 = 0; i4 < 4; ++i4) {
+                                o[j][e][i4][n] *= by;
+                                o[j][e][i4][n + 2] *= by;
+                            }
+                    }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float p[4];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int n = f & 1;
+                    const float x = exp2_approx(sc[j][f] - (m[j][n] - kShift));
+                    p[f] = sc[j][f] == -INFINITY ? 0.0f : x;
+                    l[j][n] += p[f];
+                }
+                pb[j][0] = transpose8x8(pack_half2(p[0], p[1]));
+                pb[j][1] = transpose8x8(pack_half2(p[2], p[3]));
+            }
+
+            // O^T += V^T P^T; tokens past the sequence's end hold anything: their V is taken as 0
+            if (tok + kKv4Cell > s.len) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int first = tok + 8 * u + 2 * t;
+                    const uint32_t keep = (first < s.len ? 0x0000FFFFu : 0u) | (first + 1 < s.len ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int e = 0; e < 2 * G; ++e)
+                        r.vp[u][e] &= keep;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < G; ++e) {
+                const __half2 s0 = as_half2(r.vp[0][2 * e]), m0 = as_half2(r.vp[0][2 * e + 1]);
+                const __half2 s1 = as_half2(r.vp[1][2 * e]), m1 = as_half2(r.vp[1][2 * e + 1]);
+                const auto tile = [&](auto nib) {
+                    constexpr int N = decltype(nib)::value;
+                    uint32_t af[4];
+                    af[0] = as_u32(__hfma2(nibble<N>(r.v[e][0], 8.0f), s0, m0));
+                    af[1] = as_u32(__hfma2(nibble<N>(r.v[e][1], 8.0f), s0, m0));
+                    af[2] = as_u32(__hfma2(nibble<N>(r.v[e][2], 8.0f), s1, m1));
+                    af[3] = as_u32(__hfma2(nibble<N>(r.v[e][3], 8.0f), s1, m1));
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        mma16816(o[j][e][N], af, pb[j][0], pb[j][1]);
+                };
+                tile(std::integral_constant<int, 0>{});
+                tile(std::integral_constant<int, 1>{});
+                tile(std::integral_constant<int, 2>{});
+                tile(std::integral_constant<int, 3>{});
+            }
+        }
+
+        // the warp's part to shared memory: rows 2 t, 2 t + 1, channels 64 e + 8 g ..
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float x = l[j][n];
+                x += __shfl_xor_sync(~0u, x, 4);
+                x += __shfl_xor_sync(~0u, x, 8);
+                x += __shfl_xor_sync(~0u, x, 16);
+                const int row = 8 * j + 2 * t + n;
+                if (g == 0) {
+                    sm_m[warp * RT + row] = m[j][n];
+                    sm_l[warp * RT + row] = x;
+                }
+                float *dst = sm_o + (warp * RT + row) * SM::kPitch + 8 * g;
+#pragma unroll
+                for (int e = 0; e < G; ++e) {
+                    *(float4 *)(dst + 64 * e) =
+                        make_float4(o[j][e][0][n], o[j][e][1][n], o[j][e][2][n], o[j][e][3][n]);
+                    *(float4 *)(dst + 64 * e + 4) =
+                        make_float4(o[j][e][0][n + 2], o[j][e][1][n + 2], o[j][e][2][n + 2], o[j][e][3][n + 2]);
+                }
+            }
+        __syncthreads();
+
+        // joined over the warps; four channels of a row to a thread
+        const auto store = [&](int row, int ch, const float4 &x, float M, float L) {
+            const int64_t r = row0 + row;
+            if (r >= rows)
+                return;
+            const int64_t token = s.first + r / a.ratio, h = (int64_t)head * a.ratio + r % a.ratio;
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            uint2 w;
+            w.x = f32_to_bf16_rn(x.x * inv) | ((uint32_t)f32_to_bf16_rn(x.y * inv) << 16);
+            w.y = f32_to_bf16_rn(x.z * inv) | ((uint32_t)f32_to_bf16_rn(x.w * inv) << 16);
+            *(uint2 *)(a.out + token * a.out_stride + h * D + ch) = w;
+            if (a.lse && ch == 0)
+                a.lse[token * a.n_q_heads + h] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * kLn2;
+        };
+        const bool whole = c0 == 0 && c1 == cells;
+        float *part = nullptr;
+        if (!whole)
+            part = a.partials + ((int64_t)blockIdx.x * 2 + (pos == lo ? 0 : 1)) * part_floats<D, NT>();
+        for (int x = tid; x < RT * (D / 4); x += kThreads) {
+            const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
+            float M = -INFINITY, L = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                M = fmaxf(M, sm_m[w * RT + row]);
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = sm_m[w * RT + row];
+                const float f = mw == M ? 1.0f : exp2_approx(mw - M);
+                const float4 z = *(const float4 *)(sm_o + (w * RT + row) * SM::kPitch + ch);
+                L = fmaf(f, sm_l[w * RT + row], L);
+                y.x = fmaf(f, z.x, y.x);
+                y.y = fmaf(f, z.y, y.y);
+                y.z = fmaf(f, z.z, y.z);
+                y.w = fmaf(f, z.w, y.w);
+            }
+            if (whole) {
+                store(row, ch, y, M, L);
+            } else {
+                if (ch == 0) {
+                    part[row] = M;
+                    part[RT + row] = L;
+                }
+                *(float4 *)(part + 2 * RT + row * D + ch) = y;
+            }
+        }
+        if (!whole) {
+            // the segment's CTAs are first .. last; the last one to arrive joins their parts in order
+            const int first = (int)(seg_lo / share), last = (int)((seg_hi - 1) / share);
+            __syncthreads();
+            if (tid == 0) {
+                const uint32_t n = (uint32_t)(last - first);
+                s_last = atom_add_acq_rel_gpu(a.counters + first, 1u) == n;
+                if (s_last)
+                    a.counters[first] = 0; // for the next launch
+            }
+            __syncthreads();
+            if (s_last) {
+                for (int x = tid; x < RT * (D / 4); x += kThreads) {
+                    const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
+                    const auto at = [&](int k) {
+                        return a.partials + ((int64_t)k * 2 + (k > first || seg_lo == (int64_t)first * share ? 0 : 1)) *
+                                                part_floats<D, NT>();
+                    };
+                    float M = -INFINITY, L = 0.0f;
+                    for (int k = first; k <= last; ++k)
+                        M = fmaxf(M, ldcg_f32(at(k) + row));
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = first; k <= last; ++k) {
+                        const float *p = at(k);
+                        const float mk = ldcg_f32(p + row);
+                        const float f = mk == M ? 1.0f : exp2_approx(mk - M);
+                        const float4 z = __ldcg((const float4 *)(p + 2 * RT + row * D + ch));
+                        L = fmaf(f, ldcg_f32(p + RT + row), L);
+                        y.x = fmaf(f, z.x, y.x);
+                        y.y = fmaf(f, z.y, y.y);
+                        y.z = fmaf(f, z.z, y.z);
+                        y.w = fmaf(f, z.w, y.w);
+                    }
+                    store(row, ch, y, M, L);
+                }
+            }
+        }
+        __syncthreads(); // the parts' shared memory is free again
+        pos += c1 - c0;
+    }
+}
+
+template <int D, int NT> nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, int num_sms, cudaStream_t st)
+{
+    const size_t smem = Smem<D, NT>::kMerge + (size_t)(b.n_seqs + 1) * 8 + (size_t)b.n_seqs * sizeof(Kv4Seq);
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(attn_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    Smem<D, NT>::kMerge + kKv4MaxSeqs * 24 + 8);
+    });
+    if (attr != cudaSuccess)
+        return NM_ERR_CUDA;
+    const unsigned grid = (unsigned)(num_sms * (NT == 1 ? 2 : 1));
+    attn_rows_kernel<D, NT><<<grid, kThreads, smem, st>>>(c, b, a);
+    return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
+}
+
+} // namespace
+
+// Parts of two CTAs to an SM with 8 rows, or of one with 16: two each.
+size_t kv4_partial_bytes(int head_dim) { return (size_t)kKv4Counters / 2 * 2 * 8 * (head_dim + 2) * 4; }
+
+nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &at, int64_t max_new, const Kv4Work &w,
+                               int num_sms, cudaStream_t st)
+{
+    const AttnArgs a{at.layer, at.n_q_heads / c.n_kv_heads, at.n_q_heads, (const uint16_t *)at.q, at.q_stride,
+                     at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials};
+    const bool one = max_new * a.ratio <= 8;
+    if (c.head_dim == 128)
+        return one ? launch_rows<128, 1>(c, b, a, num_sms, st) : launch_rows<128, 2>(c, b, a, num_sms, st);
+    return one ? launch_rows<64, 1>(c, b, a, num_sms, st) : launch_rows<64, 2>(c, b, a, num_sms, st);
+}
+
+} // namespace nm
