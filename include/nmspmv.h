@@ -490,8 +490,8 @@ nm_status nm_obs_release_workspace(void);
  *   - The tables are checked on the device: an id, length, start or page out
  *     of range is not followed (a token at such a place is neither written nor
  *     attended, its row gives zeros) and nm_device_status reports NM_ERR_BOUNDS.
- *   - workspace: device memory of nm_kv4_workspace_bytes(), 256-byte aligned and
- *     zeroed once before its first use (nm_kv4_init does). Calls with the same
+ *   - workspace: device memory of nm_kv4_workspace_bytes(), 256-byte aligned, its
+ *     first 8192 bytes zeroed once before its first use (nm_kv4_init does). Calls with the same
  *     workspace, or that change the same bookkeeping, must not overlap on the
  *     GPU; calls with caches of their own may.
  *   - All calls are asynchronous, allocate nothing but the library's per-device

@@ -473,7 +473,8 @@ class Kv4Cache:
         b = a + _pad4(n_pages)
         self.info, self.lens, self.refs = self.book[:16], self.book[16:16 + max_seqs], self.book[a:a + n_pages]
         self.tables = self.book[b:b + max_seqs * max_pages].view(max_seqs, max_pages)
-        self._work = torch.zeros(L.nm_kv4_workspace_bytes(n_pages, head_dim), dtype=torch.uint8, device=device)
+        self._work = torch.empty(L.nm_kv4_workspace_bytes(n_pages, head_dim), dtype=torch.uint8, device=device)
+        self._work[:8192].zero_()  # the join counters
         base = self.book.data_ptr()
         self._c = NmKv4Cache(self.pool.data_ptr(), n_pages, page_tokens, n_layers, n_kv_heads, head_dim, max_seqs,
                              max_pages, base, base + 64, base + 4 * a, base + 4 * b, self._work.data_ptr(),

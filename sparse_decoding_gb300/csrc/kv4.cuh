@@ -148,6 +148,10 @@ struct Kv4Attn {
     int64_t out_stride;
     float *lse;
 };
+constexpr int kKv4PromptCtas = 160; // CTAs of the prompt kernel at most
+size_t kv4_prompt_partial_bytes(int head_dim);
+nm_status kv4_launch_prompt(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a, const Kv4Work &w, int num_sms,
+                            cudaStream_t st);
 nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a, int64_t max_new, const Kv4Work &w,
                                int num_sms, cudaStream_t st);
 

@@ -564,13 +564,20 @@ template <int D, int NT> nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, 
 } // namespace
 
 // Parts of two CTAs to an SM with 8 rows, or of one with 16: two each.
-size_t kv4_partial_bytes(int head_dim) { return (size_t)kKv4Counters / 2 * 2 * 8 * (head_dim + 2) * 4; }
+size_t kv4_partial_bytes(int head_dim)
+{
+    const size_t rows = (size_t)kKv4Counters / 2 * 2 * 8 * (head_dim + 2) * 4;
+    const size_t prompt = kv4_prompt_partial_bytes(head_dim);
+    return rows > prompt ? rows : prompt;
+}
 
 nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &at, int64_t max_new, const Kv4Work &w,
                                int num_sms, cudaStream_t st)
 {
     const AttnArgs a{at.layer, at.n_q_heads / c.n_kv_heads, at.n_q_heads, (const uint16_t *)at.q, at.q_stride,
                      at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials};
+    if (max_new * a.ratio > 32)
+        return kv4_launch_prompt(c, b, at, w, num_sms, st);
     const bool one = max_new * a.ratio <= 8;
     if (c.head_dim == 128)
         return one ? launch_rows<128, 1>(c, b, a, num_sms, st) : launch_rows<128, 2>(c, b, a, num_sms, st);

@@ -1,0 +1,820 @@
+// kv4_prompt.cu -- attention of many queries over the 4-bit paged cache
+// (prompts), on the 5th-generation tensor cores.
+//
+// For one sequence and kv head the rows are its new tokens times the query heads
+// that share the kv head. A CTA works on a pair of 128-row tiles at a time and
+// walks the tokens they see in blocks of 128:
+//
+//   S = Q K^T      tcgen05.mma, Q and K in shared memory, S in tensor memory
+//   P = 2^(S r - m + 6)  one row per thread, written back to tensor memory as fp16
+//   O += P V       tcgen05.mma, P from tensor memory, V^T in shared memory
+//
+// Both operands of S are exact in fp16: q is scaled by a power of two per row,
+// and a key is s (c - 8) with a scale of eight significant bits (the format's
+// reason for it), so s (c - 8) needs eleven. The groups' middles enter as one more
+// k-step of 16: [sum q of the group, in two fp16 parts] x [mid, mid]. Scores
+// then carry fp32 rounding only, as in the kernel for few rows.
+//
+// Roles (13 warps): two softmax warpgroups, one per tile (a thread owns a row: no
+// reductions across threads; it also loads and scales its row of Q, rescales and
+// stores its row of O); one warpgroup that unpacks the cache into two stages of K
+// and of V^T (both tiles use them); one thread that issues the MMAs. While one
+// tile is in its softmax, the other's MMAs run. The running maximum is raised only
+// when a score passes it by 2^8, so O is rarely rescaled. The next block's bytes are
+// in the unpacking threads' registers before the current one is written.
+//
+// The blocks of all (sequence, kv head, pair) segments are one line, cut evenly
+// over one CTA per SM; a segment that was cut is joined, row by row, by the last
+// of its CTAs, in CTA order.
+//
+// All waits are bounded; one that runs out sets NM_ERR_TIMEOUT and the kernel
+// frees its tensor memory and returns.
+#include <mutex>
+
+#include "kv4.cuh"
+
+namespace nm {
+namespace {
+
+constexpr int kSoft = 256;     // softmax threads: two tiles of 128 rows
+constexpr int kUnpack = 128;   // unpacking threads
+constexpr int kThreads = kSoft + kUnpack + 32;
+constexpr int kBlock = 128;    // tokens of a block
+constexpr int kMinShare = 2;   // blocks of a CTA at least
+constexpr int kSub = 128 * 128; // bytes of 128 rows of 64 fp16
+constexpr int kExtra = 128 * 32; // bytes of 128 rows of 16 fp16
+constexpr float kShift = 6.0f, kSlack = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int D> struct Cfg {
+    static constexpr int G = D / 64;
+    static constexpr int kQ = G * kSub + kExtra; // a tile of Q, and a stage of K
+    static constexpr int kV = 2 * D * 128;       // a stage of V^T: two halves of 64 tokens
+    static constexpr int kOffK = 2 * kQ, kOffV = kOffK + 2 * kQ, kTiles = kOffV + 2 * kV;
+    static constexpr int kPart = 128 * (D + 2);  // floats of a tile's part
+};
+
+// ---- tensor memory and tensor cores (PTX ISA, tcgen05) ------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// D (tensor memory) (+)= A (shared memory) B (shared memory)^T
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+// D (tensor memory) (+)= A (tensor memory) B (shared memory)^T
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+// 32 columns of this thread's lane; the caller waits.
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+                   "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+                   "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
+// Shared-memory descriptor of a K-major tile with rows of SW bytes under the
+// SW-byte swizzle, 8-row groups 8 SW bytes apart (layout type 2: 128 bytes, 6: 32).
+template <int SW> __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr)
+{
+    static_assert(SW == 128 || SW == 32, "swizzle width");
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)((8 * SW) >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)(SW == 128 ? 2 : 6) << 61;
+}
+// kind::f16, A and B fp16 and K-major, D fp32, M = 128.
+template <int N> constexpr uint32_t kIdesc = (1u << 4) | ((N >> 3) << 17) | ((128 >> 4) << 24);
+
+__device__ __forceinline__ void arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *(__half2 *)&x; }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *(uint32_t *)&x; }
+// Nibble N of both halves of w, minus 8: exact (see kv4_attn.cu).
+template <int N> __device__ __forceinline__ __half2 nibble8(uint32_t w)
+{
+    const uint32_t x = N >= 2 ? w >> 8 : w;
+    if (N % 2 == 0)
+        return __hadd2(as_half2((x & 0x000F000Fu) | 0x64006400u), __float2half2_rn(-1032.0f));
+    return __hfma2(as_half2((x & 0x00F000F0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
+}
+
+struct PromptArgs {
+    int layer, ratio, n_q_heads;
+    const uint16_t *q;
+    int64_t q_stride;
+    float scale;
+    uint16_t *out;
+    int64_t out_stride;
+    float *lse;
+    uint32_t *counters;
+    float *partials;
+};
+
+// Tokens that tile `tile` of a sequence sees at most (its last row's), 0 for a
+// tile without tokens; tt: tokens of a tile.
+__device__ __forceinline__ int tile_limit(const Kv4Seq &s, int64_t tile, int tt)
+{
+    if (tile * tt >= s.n_new)
+        return 0;
+    const int64_t last = (tile + 1) * tt < s.n_new ? (tile + 1) * tt : s.n_new;
+    const int64_t n = s.len - s.n_new + last;
+    return n > 0 ? (int)n : 0;
+}
+__device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlock - 1) / kBlock; }
+// Blocks of a pair of tiles (one at least, so that rows that see nothing are answered).
+__device__ __forceinline__ int pair_blocks(const Kv4Seq &s, int64_t pair, int tt)
+{
+    const int a = blocks_of(tile_limit(s, 2 * pair, tt)), b = blocks_of(tile_limit(s, 2 * pair + 1, tt));
+    const int n = a > b ? a : b;
+    return n > 0 ? n : 1;
+}
+__device__ __forceinline__ int64_t pairs_of(const Kv4Seq &s, int tt)
+{
+    return ((int64_t)s.n_new + 2 * tt - 1) / (2 * tt);
+}
+
+// A place on the line of blocks.
+struct Place {
+    int seq, head, pair, block;
+};
+
+// What the roles of a CTA agree on about one piece of work.
+struct Piece {
+    Kv4Seq s;
+    int seq, head, pair, b0, nblk, total; // blocks [b0, b0 + nblk) of the pair's total
+    int n[2];                             // of those, how many each tile takes
+    int64_t seg_lo;                       // the segment's first place on the line
+};
+
+__device__ __forceinline__ Piece piece_at(const Kv4 &c, const Kv4Batch &b, const Place &p, int64_t pos, int64_t hi,
+                                          int tt)
+{
+    Piece w;
+    w.s = kv4_seq(c, b, p.seq, false);
+    w.seq = p.seq;
+    w.head = p.head;
+    w.pair = p.pair;
+    w.b0 = p.block;
+    w.total = pair_blocks(w.s, p.pair, tt);
+    w.seg_lo = pos - p.block;
+    const int64_t left = hi - pos;
+    w.nblk = w.total - w.b0 < left ? w.total - w.b0 : (int)left;
+    for (int k = 0; k < 2; ++k) {
+        const int n = blocks_of(tile_limit(w.s, 2 * (int64_t)p.pair + k, tt)) - w.b0;
+        w.n[k] = n < 0 ? 0 : n > w.nblk ? w.nblk : n;
+    }
+    return w;
+}
+
+// The place after a piece that ends its segment.
+__device__ __forceinline__ void next_segment(const Kv4 &c, const Kv4Batch &b, const Piece &w, int tt, Place *p)
+{
+    p->block = 0;
+    if (++p->pair < pairs_of(w.s, tt))
+        return;
+    p->pair = 0;
+    if (++p->head < c.n_kv_heads)
+        return;
+    p->head = 0;
+    do
+        ++p->seq;
+    while (p->seq < b.n_seqs && kv4_seq(c, b, p->seq, false).n_new == 0);
+}
+
+struct Shared {
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint32_t tmem;
+    uint32_t last[2];
+    int64_t total, share;
+    Place start;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, const Kv4Batch b, const PromptArgs a)
+{
+    using C = Cfg<D>;
+    constexpr int G = C::G;
+    extern __shared__ __align__(1024) uint8_t dsmem[];
+    __shared__ Shared sh;
+    uint8_t *const base = dsmem + ((1024u - (smem_addr(dsmem) & 1023u)) & 1023u);
+    const uint32_t tiles = smem_addr(base);
+    int64_t *const pre = (int64_t *)(base + C::kTiles); // [n_seqs + 1]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tt = 128 / a.ratio; // tokens of a tile
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh.k_full[i]), kUnpack);
+            mbar_init(smem_addr(&sh.v_full[i]), kUnpack);
+            mbar_init(smem_addr(&sh.k_empty[i]), 1);
+            mbar_init(smem_addr(&sh.v_empty[i]), 1);
+            mbar_init(smem_addr(&sh.q_full[i]), 128);
+            mbar_init(smem_addr(&sh.p_full[i]), 128);
+            mbar_init(smem_addr(&sh.s_full[i]), 1);
+            mbar_init(smem_addr(&sh.o_full[i]), 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 12)
+        tmem_alloc(smem_addr(&sh.tmem), 512);
+
+    // blocks of each sequence (a warp to a sequence), then where each starts on the line
+    for (int i = warp; i < b.n_seqs; i += kThreads / 32) {
+        const Kv4Seq s = kv4_seq(c, b, i, blockIdx.x == 0 && lane == 0);
+        int64_t n = 0;
+        for (int64_t j = lane; j < pairs_of(s, tt); j += 32)
+            n += pair_blocks(s, j, tt);
+        for (int o = 16; o; o >>= 1)
+            n += __shfl_xor_sync(~0u, n, o);
+        if (lane == 0)
+            pre[i + 1] = n * c.n_kv_heads;
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 0) {
+        int64_t sum = 0;
+        for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
+            int64_t x = i0 + lane < b.n_seqs ? pre[i0 + lane + 1] : 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            if (i0 + lane < b.n_seqs)
+                pre[i0 + lane + 1] = sum + x;
+            sum += __shfl_sync(~0u, x, 31);
+        }
+        if (lane == 0)
+            pre[0] = 0;
+        __syncwarp();
+        const int64_t total = sum;
+        int64_t share = (total + gridDim.x - 1) / gridDim.x;
+        share = share < kMinShare ? kMinShare : share;
+        const int64_t pos = (int64_t)blockIdx.x * share;
+        Place p{};
+        if (pos < total) {
+            int l = 0, h = b.n_seqs;
+            while (h - l > 1) {
+                const int m = (l + h) >> 1;
+                if (pre[m] <= pos)
+                    l = m;
+                else
+                    h = m;
+            }
+            p.seq = l;
+            const Kv4Seq s = kv4_seq(c, b, l, false);
+            const int64_t per = (pre[l + 1] - pre[l]) / c.n_kv_heads;
+            p.head = (int)((pos - pre[l]) / per);
+            int64_t left = (pos - pre[l]) % per;
+            // the pair that holds block `left` of the head's line
+            for (int64_t j0 = 0;; j0 += 32) {
+                const int64_t j = j0 + lane;
+                const int n = j < pairs_of(s, tt) ? pair_blocks(s, j, tt) : 0;
+                int64_t x = n;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(~0u, x, o);
+                    if (lane >= o)
+                        x += y;
+                }
+                const uint32_t in = __ballot_sync(~0u, left < x && left >= x - n);
+                if (in || j0 + 32 >= pairs_of(s, tt)) {
+                    const int who = in ? __ffs(in) - 1 : 0;
+                    p.pair = (int)(j0 + who);
+                    p.block = (int)(left - (__shfl_sync(~0u, x, who) - __shfl_sync(~0u, n, who)));
+                    break;
+                }
+                left -= __shfl_sync(~0u, x, 31);
+            }
+        }
+        if (lane == 0) {
+            sh.total = total;
+            sh.share = share;
+            sh.start = p;
+        }
+    }
+    __syncthreads();
+    const uint32_t tmem = sh.tmem;
+    const int64_t share = sh.share;
+    const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share < sh.total ? lo + share : sh.total;
+    bool dead = false;
+    const auto wait = [&](uint64_t &bar, uint32_t parity) {
+        return mbar_wait_bounded(smem_addr(&bar), parity & 1u, c.status, dead);
+    };
+    Place at = sh.start;
+
+    if (warp < 8) {
+        // ---- softmax: a row per thread ----
+        const int k = warp >> 2;          // the tile
+        const int row = tid & 127;
+        const uint32_t q_tile = tiles + k * C::kQ;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lanes + k * 128, t_o = tmem + lanes + 256 + k * 128;
+        uint32_t n_s = 0, n_o = 0; // blocks and pieces of this tile so far
+        for (int64_t pos = lo; pos < hi;) {
+            const Piece w = piece_at(c, b, at, pos, hi, tt);
+            const int64_t tile = 2 * (int64_t)w.pair + k;
+            const int64_t token = tile * tt + row / a.ratio; // of the sequence's new ones
+            const bool valid = row < tt * a.ratio && token < w.s.n_new;
+            const int limit = valid ? w.s.len - w.s.n_new + (int)token + 1 : 0;
+            const int head = w.head * a.ratio + row % a.ratio;
+
+            // the row of Q: scaled by a power of two, channels in the order of the unpacked keys
+            float rs;
+            {
+                uint4 x[D / 8];
+                const uint16_t *q = a.q + (w.s.first + token) * a.q_stride + (int64_t)head * D;
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    x[i] = valid ? ldg_nc128(q + 8 * i) : make_uint4(0, 0, 0, 0);
+                    const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        top = max(top, ws[n] & 0x7FFF0000u);
+                        top = max(top, (ws[n] << 16) & 0x7FFF0000u);
+                    }
+                }
+                uint32_t e2 = top >> 23;
+                e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
+                const float up = __uint_as_float(e2 << 23);
+                float down = __uint_as_float((254u - e2) << 23);
+                rs = up * (fabsf(a.scale) * kLog2e);
+                if (a.scale < 0.0f)
+                    down = -down;
+                uint32_t ext[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 v = x[8 * g + i];
+                        const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+                        float y[8];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            y[2 * n] = __half2float(__float2half_rn(bf16lo_to_f32(ws[n]) * down));
+                            y[2 * n + 1] = __half2float(__float2half_rn(bf16hi_to_f32(ws[n]) * down));
+                            sum += y[2 * n] + y[2 * n + 1];
+                        }
+                        sts128(q_tile + g * kSub + row * 128 + ((i ^ (row & 7)) << 4), pack_half2(y[0], y[4]),
+                               pack_half2(y[1], y[5]), pack_half2(y[2], y[6]), pack_half2(y[3], y[7]));
+                    }
+                    const float part = __half2float(__float2half_rn(sum));
+                    ext[g] = pack_half2(part, sum - part);
+                }
+                const uint32_t e_row = q_tile + G * kSub + row * 32, flip = (row >> 2) & 1;
+                sts128(e_row + (flip << 4), ext[0], ext[1], 0, 0);
+                sts128(e_row + ((flip ^ 1) << 4), 0, 0, 0, 0);
+                fence_proxy_async_smem();
+                arrive(smem_addr(&sh.q_full[k]));
+            }
+
+            float m = -INFINITY, l = 0.0f;
+            for (int i = 0; i < w.n[k]; ++i, ++n_s) {
+                wait(sh.s_full[k], n_s);
+                fence_after();
+                const int vis = limit - (w.b0 + i) * kBlock; // columns this row sees
+                const bool all = __all_sync(~0u, vis >= kBlock);
+                float mx = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t r[32];
+                    ld32(t_s + 32 * h, r);
+                    wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        mx = all || 32 * h + e < vis ? fmaxf(mx, __uint_as_float(r[e])) : mx;
+                }
+                mx = mx == -INFINITY ? mx : mx * rs;
+                if (__any_sync(~0u, mx > m + kSlack)) {
+                    const float mn = fmaxf(m, mx);
+                    const float f = mn == m ? 1.0f : exp2_approx(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (i > 0) {
+#pragma unroll
+                        for (int h = 0; h < D / 32; ++h) {
+                            uint32_t r[32];
+                            ld32(t_o + 32 * h, r);
+                            wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                            st16(t_o + 32 * h, r);
+                            st16(t_o + 32 * h + 16, r + 16);
+                        }
+                    }
+                }
+                const float off = kShift - (m == -INFINITY ? 0.0f : m);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t r[32], p[16];
+                    ld32(t_s + 32 * h, r);
+                    wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float x = exp2_approx(fmaf(__uint_as_float(r[e]), rs, off));
+                        float y = exp2_approx(fmaf(__uint_as_float(r[e + 1]), rs, off));
+                        x = all || 32 * h + e < vis ? x : 0.0f;
+                        y = all || 32 * h + e + 1 < vis ? y : 0.0f;
+                        l += x + y;
+                        p[e / 2] = pack_half2(x, y);
+                    }
+                    st16(t_s + 16 * h, p);
+                }
+                wait_st();
+                fence_before();
+                arrive(smem_addr(&sh.p_full[k]));
+            }
+
+            // the tile's rows of O
+            if (w.n[k] > 0) {
+                wait(sh.o_full[k], n_o);
+                ++n_o;
+                fence_after();
+            }
+            const auto store = [&](int ch, const float (&x)[32], float M, float L) {
+                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                uint16_t *o = a.out + (w.s.first + token) * a.out_stride + (int64_t)head * D + ch;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        y[n] = f32_to_bf16_rn(x[e + 2 * n] * inv) |
+                               ((uint32_t)f32_to_bf16_rn(x[e + 2 * n + 1] * inv) << 16);
+                    *(uint4 *)(o + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+                if (a.lse && ch == 0)
+                    a.lse[(w.s.first + token) * a.n_q_heads + head] =
+                        L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * kLn2;
+            };
+            const bool whole = w.b0 == 0 && w.nblk == w.total;
+            float *part = nullptr;
+            if (!whole) {
+                part = a.partials + (((int64_t)blockIdx.x * 2 + (pos == lo ? 0 : 1)) * 2 + k) * C::kPart;
+                part[row] = m;
+                part[128 + row] = l;
+            }
+#pragma unroll
+            for (int h = 0; h < D / 32; ++h) {
+                uint32_t r[32];
+                float x[32];
+                if (w.n[k] > 0) {
+                    ld32(t_o + 32 * h, r);
+                    wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    x[e] = w.n[k] > 0 ? __uint_as_float(r[e]) : 0.0f;
+                if (whole) {
+                    if (valid)
+                        store(32 * h, x, m, l);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *(float4 *)(part + 256 + row * D + 32 * h + e) =
+                            make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                }
+            }
+            if (!whole) {
+                // the last CTA of the segment to arrive joins the parts of this tile, in CTA order
+                const int first = (int)(w.seg_lo / share), last = (int)((w.seg_lo + w.total - 1) / share);
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
+                if (row == 0) {
+                    const uint32_t done = atom_add_acq_rel_gpu(a.counters + 2 * first + k, 1u);
+                    sh.last[k] = done == (uint32_t)(last - first);
+                    if (sh.last[k])
+                        a.counters[2 * first + k] = 0; // for the next launch
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
+                if (sh.last[k] && valid) {
+                    const auto of = [&](int z) {
+                        const int slot = z > first || w.seg_lo == (int64_t)first * share ? 0 : 1;
+                        return a.partials + (((int64_t)z * 2 + slot) * 2 + k) * C::kPart;
+                    };
+                    float M = -INFINITY, L = 0.0f;
+                    for (int z = first; z <= last; ++z)
+                        M = fmaxf(M, ldcg_f32(of(z) + row));
+                    for (int z = first; z <= last; ++z) {
+                        const float mz = ldcg_f32(of(z) + row);
+                        L = fmaf(mz == M ? 1.0f : exp2_approx(mz - M), ldcg_f32(of(z) + 128 + row), L);
+                    }
+#pragma unroll 1
+                    for (int h = 0; h < D / 32; ++h) {
+                        float x[32] = {};
+                        for (int z = first; z <= last; ++z) {
+                            const float mz = ldcg_f32(of(z) + row);
+                            const float f = mz == M ? 1.0f : exp2_approx(mz - M);
+                            const float4 *o = (const float4 *)(of(z) + 256 + row * D + 32 * h);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 y = __ldcg(o + e);
+                                x[4 * e] = fmaf(f, y.x, x[4 * e]);
+                                x[4 * e + 1] = fmaf(f, y.y, x[4 * e + 1]);
+                                x[4 * e + 2] = fmaf(f, y.z, x[4 * e + 2]);
+                                x[4 * e + 3] = fmaf(f, y.w, x[4 * e + 3]);
+                            }
+                        }
+                        store(32 * h, x, M, L);
+                    }
+                }
+            }
+            fence_before(); // the next piece's MMAs overwrite O only after this thread's Q arrives
+            pos += w.nblk;
+            if (pos < hi)
+                next_segment(c, b, w, tt, &at);
+        }
+    } else if (warp < 12) {
+        // ---- unpacking: 128 threads fill K and V^T of a block ----
+        const int u = tid - kSoft;
+        uint32_t n = 0; // blocks so far
+        for (int64_t pos = lo; pos < hi;) {
+            const Piece w = piece_at(c, b, at, pos, hi, tt);
+            const int cells = (w.s.len + kKv4Cell - 1) / kKv4Cell;
+            for (int i = 0; i < w.nblk; ++i, ++n) {
+                const int st = n & 1;
+                const int blk = w.b0 + i;
+                // lane z < 8: the place of cell z of the block, in 128-byte units; ~0 for none
+                uint32_t place = ~0u;
+                {
+                    const int cell = blk * 8 + (lane & 7);
+                    if (cell < cells) {
+                        const int page = kv4_page(c, w.s.row, cell >> (c.page_shift - 4));
+                        if (page >= 0)
+                            place = (uint32_t)(kv4_cell_offset<D>(c, page, a.layer, w.head,
+                                                                  cell & ((1 << (c.page_shift - 4)) - 1)) >> 7);
+                        else if (u < 8)
+                            kv4_bad(c);
+                    }
+                }
+                const uint32_t ks = tiles + C::kOffK + st * C::kQ, vs = tiles + C::kOffV + st * C::kV;
+                // K: 16-byte pieces (8 at D = 64): row 32 j + u / 4, channels 16 (u % 4) .. of each group
+                if (n >= 2)
+                    wait(sh.k_empty[st], (n >> 1) - 1);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = 32 * j + (u >> 2), t = u & 3;
+                    const uint32_t where = __shfl_sync(~0u, place, row >> 4);
+                    uint32_t wk[2 * G] = {}, pr[G] = {};
+                    if (where != ~0u) {
+                        const uint8_t *cell = c.pool + ((int64_t)where << 7);
+                        const uint8_t *src = cell + (row & 15) * (D / 2) + t * 8 * G;
+                        if (D == 128) {
+                            const uint4 x = ldg_nc128(src);
+                            wk[0] = x.x;
+                            wk[1] = x.y;
+                            wk[2 * G - 2] = x.z;
+                            wk[2 * G - 1] = x.w;
+                            const uint2 p = *(const uint2 *)(cell + Kv4Cell<D>::kKp + (row & 15) * 8);
+                            pr[0] = p.x;
+                            pr[G - 1] = p.y;
+                        } else {
+                            const uint2 x = *(const uint2 *)src;
+                            wk[0] = x.x;
+                            wk[1] = x.y;
+                            pr[0] = *(const uint32_t *)(cell + Kv4Cell<D>::kKp + (row & 15) * 4);
+                        }
+                    }
+                    uint32_t mids[2] = {0, 0};
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const __half2 s = __low2half2(as_half2(pr[g]));
+                        mids[g] = as_u32(__high2half2(as_half2(pr[g])));
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const uint32_t x = wk[2 * g + f];
+                            sts128(ks + g * kSub + row * 128 + (((2 * t + f) ^ (row & 7)) << 4),
+                                   as_u32(__hmul2(nibble8<0>(x), s)), as_u32(__hmul2(nibble8<1>(x), s)),
+                                   as_u32(__hmul2(nibble8<2>(x), s)), as_u32(__hmul2(nibble8<3>(x), s)));
+                        }
+                    }
+                    if (t < 2) { // the k-step of the middles: two 16-byte halves of the row
+                        const uint32_t e = ks + G * kSub + row * 32 + ((t ^ ((row >> 2) & 1)) << 4);
+                        sts128(e, t ? 0 : mids[0], t ? 0 : mids[1], 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+                arrive(smem_addr(&sh.k_full[st]));
+                // V^T: unit (cell, group, e, p): 8 channels 64 g + 8 e .., tokens 8 p .. of the cell
+                if (n >= 2)
+                    wait(sh.v_empty[st], (n >> 1) - 1);
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    const int p = u & 1, e = (u >> 3) & 7;
+                    const int half = G == 2 ? j : u >> 6, g = G == 2 ? u >> 6 : 0;
+                    const int cell_i = half * 4 + ((u >> 1) & 3);
+                    const uint32_t where = __shfl_sync(~0u, place, cell_i);
+                    uint2 x[4] = {}, pr[4] = {};
+                    if (where != ~0u) {
+                        const uint8_t *cell = c.pool + ((int64_t)where << 7);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            x[t] = *(const uint2 *)(cell + Kv4Cell<D>::kV + g * 512 + e * 64 + t * 16 + p * 8);
+                            pr[t] = *(const uint2 *)(cell + Kv4Cell<D>::kVp + ((4 * p + t) * G + g) * 8);
+                        }
+                    }
+                    const int tok = blk * kBlock + cell_i * 16 + 8 * p; // past the end V is 0, whatever is there
+                    if (tok + 8 > w.s.len) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t keep = (tok + 2 * t < w.s.len ? 0x0000FFFFu : 0u) |
+                                                  (tok + 2 * t + 1 < w.s.len ? 0xFFFF0000u : 0u);
+                            pr[t].x &= keep;
+                            pr[t].y &= keep;
+                        }
+                    }
+                    const uint32_t dst = vs + half * (D * 128) + (64 * g + 8 * e) * 128;
+                    const int chunk = 2 * ((u >> 1) & 3) + p;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t y[4][4]; // [nibble][token pair]
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t wv = q ? x[t].y : x[t].x;
+                            const __half2 s = as_half2(pr[t].x), mid = as_half2(pr[t].y);
+                            y[0][t] = as_u32(__hfma2(nibble8<0>(wv), s, mid));
+                            y[1][t] = as_u32(__hfma2(nibble8<1>(wv), s, mid));
+                            y[2][t] = as_u32(__hfma2(nibble8<2>(wv), s, mid));
+                            y[3][t] = as_u32(__hfma2(nibble8<3>(wv), s, mid));
+                        }
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int r = 4 * q + z; // row & 7
+                            sts128(dst + r * 128 + ((chunk ^ r) << 4), y[z][0], y[z][1], y[z][2], y[z][3]);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                arrive(smem_addr(&sh.v_full[st]));
+            }
+            pos += w.nblk;
+            if (pos < hi)
+                next_segment(c, b, w, tt, &at);
+        }
+    } else if (lane == 0) {
+        // ---- the MMAs ----
+        uint32_t n = 0, n_p[2] = {0, 0}, piece = 0;
+        const auto scores = [&](int k, uint32_t blk) { // S of tile k
+            const uint32_t q = tiles + k * C::kQ, kk = tiles + C::kOffK + (blk & 1) * C::kQ;
+            const uint32_t d = tmem + k * 128;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mma_ss(d, smem_desc<128>(q + g * kSub + 32 * x), smem_desc<128>(kk + g * kSub + 32 * x),
+                           kIdesc<128>, g + x > 0);
+            mma_ss(d, smem_desc<32>(q + G * kSub), smem_desc<32>(kk + G * kSub), kIdesc<128>, true);
+            commit(smem_addr(&sh.s_full[k]));
+        };
+        const auto values = [&](int k, uint32_t blk, bool accumulate) { // O of tile k
+            const uint32_t v = tiles + C::kOffV + (blk & 1) * C::kV;
+            const uint32_t d = tmem + 256 + k * 128, p = tmem + k * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mma_ts(d, p + 8 * (4 * h + x), smem_desc<128>(v + h * (D * 128) + 32 * x), kIdesc<D>,
+                           accumulate || h + x > 0);
+        };
+        for (int64_t pos = lo; pos < hi; ++piece) {
+            const Piece w = piece_at(c, b, at, pos, hi, tt);
+            wait(sh.q_full[0], piece);
+            wait(sh.q_full[1], piece);
+            wait(sh.k_full[n & 1], n >> 1);
+            fence_after();
+            for (int k = 0; k < 2; ++k)
+                if (w.n[k] > 0)
+                    scores(k, n);
+            commit(smem_addr(&sh.k_empty[n & 1]));
+            for (int i = 0; i < w.nblk; ++i, ++n) {
+                const bool more = i + 1 < w.nblk;
+                wait(sh.v_full[n & 1], n >> 1);
+                for (int k = 0; k < 2; ++k) {
+                    if (i < w.n[k]) {
+                        wait(sh.p_full[k], n_p[k]);
+                        ++n_p[k];
+                        fence_after();
+                        values(k, n, i > 0);
+                        if (i == w.n[k] - 1)
+                            commit(smem_addr(&sh.o_full[k]));
+                    }
+                    if (k == 1)
+                        commit(smem_addr(&sh.v_empty[n & 1]));
+                    if (more) {
+                        if (k == 0)
+                            wait(sh.k_full[(n + 1) & 1], (n + 1) >> 1);
+                        fence_after();
+                        if (i + 1 < w.n[k])
+                            scores(k, n + 1);
+                        if (k == 1)
+                            commit(smem_addr(&sh.k_empty[(n + 1) & 1]));
+                    }
+                }
+            }
+            pos += w.nblk;
+            if (pos < hi)
+                next_segment(c, b, w, tt, &at);
+        }
+        // before leaving, the MMAs in flight end (bounded): the last stages are released
+        if (n > 0) {
+            wait(sh.k_empty[(n - 1) & 1], (n - 1) >> 1);
+            wait(sh.v_empty[(n - 1) & 1], (n - 1) >> 1);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        __syncwarp();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D> nm_status launch(const Kv4 &c, const Kv4Batch &b, const PromptArgs &a, int grid, cudaStream_t st)
+{
+    constexpr size_t kMax = Cfg<D>::kTiles + 1024 + (kKv4MaxSeqs + 1) * 8;
+    static_assert(kMax + sizeof(Shared) <= 227 * 1024, "shared memory");
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMax);
+    });
+    if (attr != cudaSuccess)
+        return NM_ERR_CUDA;
+    const size_t smem = Cfg<D>::kTiles + 1024 + (size_t)(b.n_seqs + 1) * 8;
+    attn_prompt_kernel<D><<<grid, kThreads, smem, st>>>(c, b, a);
+    return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
+}
+
+} // namespace
+
+size_t kv4_prompt_partial_bytes(int head_dim) { return (size_t)kKv4PromptCtas * 4 * 128 * (head_dim + 2) * 4; }
+
+nm_status kv4_launch_prompt(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &at, const Kv4Work &w, int num_sms,
+                            cudaStream_t st)
+{
+    const PromptArgs a{at.layer, at.n_q_heads / c.n_kv_heads, at.n_q_heads, (const uint16_t *)at.q, at.q_stride,
+                       at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials};
+    const int grid = num_sms < kKv4PromptCtas ? num_sms : kKv4PromptCtas;
+    return c.head_dim == 128 ? launch<128>(c, b, a, grid, st) : launch<64>(c, b, a, grid, st);
+}
+
+} // namespace nm
