@@ -72,20 +72,30 @@ __device__ __forceinline__ void commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// D (tensor memory) (+)= A (shared memory) B (shared memory)^T
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+// Shared-memory descriptor of a K-major tile with rows of SW bytes under the
+// SW-byte swizzle, 8-row groups 8 SW bytes apart (layout type 2: 128 bytes, 6: 32):
+// its high word, and its low word without the address (in 16-byte units).
+template <int SW>
+constexpr uint32_t kDescHi = ((8 * SW) >> 4) | (1u << 14) | ((SW == 128 ? 2u : SW == 32 ? 6u : 8u) << 29);
+constexpr uint32_t kDescLo = 1u << 16;
+
+// D (tensor memory) (+)= A (shared memory) B (shared memory)^T; a, b: the low words
+template <int SW>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi<SW>)
                  : "memory");
 }
 // D (tensor memory) (+)= A (tensor memory) B (shared memory)^T
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "mov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi<128>)
                  : "memory");
 }
 // 32 columns of this thread's lane; the caller waits.
@@ -101,6 +111,38 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32])
                    "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(taddr));
 }
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+                   "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+// Two fp32 numbers in one register pair: a b + c, a + b.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r)
@@ -112,14 +154,6 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r)
                  : "memory");
 }
 
-// Shared-memory descriptor of a K-major tile with rows of SW bytes under the
-// SW-byte swizzle, 8-row groups 8 SW bytes apart (layout type 2: 128 bytes, 6: 32).
-template <int SW> __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr)
-{
-    static_assert(SW == 128 || SW == 32, "swizzle width");
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)((8 * SW) >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)(SW == 128 ? 2 : 6) << 61;
-}
 // kind::f16, A and B fp16 and K-major, D fp32, M = 128.
 template <int N> constexpr uint32_t kIdesc = (1u << 4) | ((N >> 3) << 17) | ((128 >> 4) << 24);
 
@@ -152,6 +186,137 @@ template <int N> __device__ __forceinline__ __half2 nibble8(uint32_t w)
     if (N % 2 == 0)
         return __hadd2(as_half2((x & 0x000F000Fu) | 0x64006400u), __float2half2_rn(-1032.0f));
     return __hfma2(as_half2((x & 0x00F000F0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
+}
+
+// What an unpacking thread u holds of a block. K: four 16-byte pieces (8 bytes at
+// D = 64): row 32 j + u / 4, channels 16 (u % 4) .. of each group.
+template <int D> struct RawK {
+    uint32_t w[4][2 * Cfg<D>::G], p[4][Cfg<D>::G];
+};
+// V: units (cell, group, e, p): channels 64 g + 8 e .., tokens 8 p .. of the cell.
+template <int D> struct RawV {
+    uint2 w[Cfg<D>::G][4], p[Cfg<D>::G][4];
+};
+template <int D> __device__ __forceinline__ void unit_of(int u, int j, int *cell, int *g)
+{
+    *cell = (Cfg<D>::G == 2 ? j : u >> 6) * 4 + ((u >> 1) & 3);
+    *g = Cfg<D>::G == 2 ? u >> 6 : 0;
+}
+
+template <int D> __device__ __forceinline__ void load_k(RawK<D> &r, const uint8_t *pool, uint32_t place, int u)
+{
+    constexpr int G = Cfg<D>::G;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int row = 32 * j + (u >> 2), t = u & 3;
+        const uint32_t where = __shfl_sync(~0u, place, row >> 4);
+        const uint8_t *cell = pool + ((int64_t)where << 7);
+        const uint8_t *src = cell + (row & 15) * (D / 2) + t * 8 * G;
+        const bool have = where != ~0u;
+        if (D == 128) {
+            const uint4 x = have ? ldg_nc128(src) : make_uint4(0, 0, 0, 0);
+            r.w[j][0] = x.x;
+            r.w[j][1] = x.y;
+            r.w[j][2 * G - 2] = x.z;
+            r.w[j][2 * G - 1] = x.w;
+            const uint2 p = have ? *(const uint2 *)(cell + Kv4Cell<D>::kKp + (row & 15) * 8) : make_uint2(0, 0);
+            r.p[j][0] = p.x;
+            r.p[j][G - 1] = p.y;
+        } else {
+            const uint2 x = have ? *(const uint2 *)src : make_uint2(0, 0);
+            r.w[j][0] = x.x;
+            r.w[j][1] = x.y;
+            r.p[j][0] = have ? *(const uint32_t *)(cell + Kv4Cell<D>::kKp + (row & 15) * 4) : 0u;
+        }
+    }
+}
+template <int D> __device__ __forceinline__ void unpack_k(const RawK<D> &r, uint32_t ks, int u)
+{
+    constexpr int G = Cfg<D>::G;
+    const int t = u & 3;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int row = 32 * j + (u >> 2);
+        uint32_t mids[2] = {0, 0};
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const __half2 s = __low2half2(as_half2(r.p[j][g]));
+            mids[g] = as_u32(__high2half2(as_half2(r.p[j][g])));
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const uint32_t x = r.w[j][2 * g + f];
+                sts128(ks + g * kSub + row * 128 + (((2 * t + f) ^ (row & 7)) << 4), as_u32(__hmul2(nibble8<0>(x), s)),
+                       as_u32(__hmul2(nibble8<1>(x), s)), as_u32(__hmul2(nibble8<2>(x), s)),
+                       as_u32(__hmul2(nibble8<3>(x), s)));
+            }
+        }
+        if (t < 2) // the k-step of the middles: two 16-byte halves of the row
+            sts128(ks + G * kSub + row * 32 + ((t ^ ((row >> 2) & 1)) << 4), t ? 0 : mids[0], t ? 0 : mids[1], 0, 0);
+    }
+}
+template <int D> __device__ __forceinline__ void load_v(RawV<D> &r, const uint8_t *pool, uint32_t place, int u)
+{
+    constexpr int G = Cfg<D>::G;
+    const int p = u & 1, e = (u >> 3) & 7;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+        int cell_i, g;
+        unit_of<D>(u, j, &cell_i, &g);
+        const uint32_t where = __shfl_sync(~0u, place, cell_i);
+        const uint8_t *cell = pool + ((int64_t)where << 7);
+        const bool have = where != ~0u;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            r.w[j][t] = have ? *(const uint2 *)(cell + Kv4Cell<D>::kV + g * 512 + e * 64 + t * 16 + p * 8)
+                             : make_uint2(0, 0);
+            r.p[j][t] = have ? *(const uint2 *)(cell + Kv4Cell<D>::kVp + ((4 * p + t) * G + g) * 8) : make_uint2(0, 0);
+        }
+    }
+}
+// left: tokens of the sequence from the block's first on; past them V is 0, whatever is there.
+template <int D> __device__ __forceinline__ void unpack_v(const RawV<D> &r, uint32_t vs, int u, int left)
+{
+    constexpr int G = Cfg<D>::G;
+    const int p = u & 1, e = (u >> 3) & 7;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+        int cell_i, g;
+        unit_of<D>(u, j, &cell_i, &g);
+        uint2 pr[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            pr[t] = r.p[j][t];
+        const int tok = cell_i * 16 + 8 * p;
+        if (tok + 8 > left) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t keep =
+                    (tok + 2 * t < left ? 0x0000FFFFu : 0u) | (tok + 2 * t + 1 < left ? 0xFFFF0000u : 0u);
+                pr[t].x &= keep;
+                pr[t].y &= keep;
+            }
+        }
+        const uint32_t dst = vs + (cell_i >> 2) * (D * 128) + (64 * g + 8 * e) * 128;
+        const int chunk = 2 * (cell_i & 3) + p;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t y[4][4]; // [nibble][token pair]
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t wv = q ? r.w[j][t].y : r.w[j][t].x;
+                const __half2 s = as_half2(pr[t].x), mid = as_half2(pr[t].y);
+                y[0][t] = as_u32(__hfma2(nibble8<0>(wv), s, mid));
+                y[1][t] = as_u32(__hfma2(nibble8<1>(wv), s, mid));
+                y[2][t] = as_u32(__hfma2(nibble8<2>(wv), s, mid));
+                y[3][t] = as_u32(__hfma2(nibble8<3>(wv), s, mid));
+            }
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const int rr = 4 * q + z; // row & 7
+                sts128(dst + rr * 128 + ((chunk ^ rr) << 4), y[z][0], y[z][1], y[z][2], y[z][3]);
+            }
+        }
+    }
 }
 
 struct PromptArgs {
@@ -198,7 +363,7 @@ struct Place {
 struct Piece {
     Kv4Seq s;
     int seq, head, pair, b0, nblk, total; // blocks [b0, b0 + nblk) of the pair's total
-    int n[2];                             // of those, how many each tile takes
+    int n0, n1;                           // of those, how many each tile takes
     int64_t seg_lo;                       // the segment's first place on the line
 };
 
@@ -215,10 +380,10 @@ __device__ __forceinline__ Piece piece_at(const Kv4 &c, const Kv4Batch &b, const
     w.seg_lo = pos - p.block;
     const int64_t left = hi - pos;
     w.nblk = w.total - w.b0 < left ? w.total - w.b0 : (int)left;
-    for (int k = 0; k < 2; ++k) {
-        const int n = blocks_of(tile_limit(w.s, 2 * (int64_t)p.pair + k, tt)) - w.b0;
-        w.n[k] = n < 0 ? 0 : n > w.nblk ? w.nblk : n;
-    }
+    const int n0 = blocks_of(tile_limit(w.s, 2 * (int64_t)p.pair, tt)) - w.b0;
+    const int n1 = blocks_of(tile_limit(w.s, 2 * (int64_t)p.pair + 1, tt)) - w.b0;
+    w.n0 = n0 < 0 ? 0 : n0 > w.nblk ? w.nblk : n0;
+    w.n1 = n1 < 0 ? 0 : n1 > w.nblk ? w.nblk : n1;
     return w;
 }
 
@@ -371,6 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         for (int64_t pos = lo; pos < hi;) {
             const Piece w = piece_at(c, b, at, pos, hi, tt);
             const int64_t tile = 2 * (int64_t)w.pair + k;
+            const int nk = k ? w.n1 : w.n0;
             const int64_t token = tile * tt + row / a.ratio; // of the sequence's new ones
             const bool valid = row < tt * a.ratio && token < w.s.n_new;
             const int limit = valid ? w.s.len - w.s.n_new + (int)token + 1 : 0;
@@ -379,13 +545,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             // the row of Q: scaled by a power of two, channels in the order of the unpacked keys
             float rs;
             {
-                uint4 x[D / 8];
                 const uint16_t *q = a.q + (w.s.first + token) * a.q_stride + (int64_t)head * D;
                 uint32_t top = 0;
-#pragma unroll
+#pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
-                    x[i] = valid ? ldg_nc128(q + 8 * i) : make_uint4(0, 0, 0, 0);
-                    const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    const uint4 x = valid ? ldg_nc128(q + 8 * i) : make_uint4(0, 0, 0, 0);
+                    const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         top = max(top, ws[n] & 0x7FFF0000u);
@@ -396,16 +561,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
                 const float up = __uint_as_float(e2 << 23);
                 float down = __uint_as_float((254u - e2) << 23);
-                rs = up * (fabsf(a.scale) * kLog2e);
+                rs = fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f); // above 0, so that masked scores stay -inf
                 if (a.scale < 0.0f)
                     down = -down;
-                uint32_t ext[4] = {0, 0, 0, 0};
+                uint32_t ext[2] = {0, 0};
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     float sum = 0.0f;
-#pragma unroll
+#pragma unroll 2
                     for (int i = 0; i < 8; ++i) {
-                        const uint4 v = x[8 * g + i];
+                        const uint4 v = valid ? ldg_nc128(q + 64 * g + 8 * i) : make_uint4(0, 0, 0, 0);
                         const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
                         float y[8];
 #pragma unroll
@@ -427,66 +592,101 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 arrive(smem_addr(&sh.q_full[k]));
             }
 
-            float m = -INFINITY, l = 0.0f;
-            for (int i = 0; i < w.n[k]; ++i, ++n_s) {
+            // rows that see nothing of the piece need no maximum
+            float m = limit > w.b0 * kBlock ? -INFINITY : 0.0f, l = 0.0f;
+            for (int i = 0; i < nk; ++i, ++n_s) {
                 wait(sh.s_full[k], n_s);
                 fence_after();
                 const int vis = limit - (w.b0 + i) * kBlock; // columns this row sees
-                const bool all = __all_sync(~0u, vis >= kBlock);
-                float mx = -INFINITY;
+                if (!__all_sync(~0u, vis >= kBlock)) {
+                    // the others become -inf in place: only the last blocks of a row come here
+#pragma unroll 1
+                    for (int h = 0; h < 8; ++h) {
+                        uint32_t r[16];
+                        ld16(t_s + 16 * h, r);
+                        wait_ld();
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t r[32];
-                    ld32(t_s + 32 * h, r);
-                    wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        mx = all || 32 * h + e < vis ? fmaxf(mx, __uint_as_float(r[e])) : mx;
+                        for (int e = 0; e < 16; ++e)
+                            r[e] = 16 * h + e < vis ? r[e] : 0xFF800000u;
+                        st16(t_s + 16 * h, r);
+                    }
+                    wait_st();
                 }
-                mx = mx == -INFINITY ? mx : mx * rs;
-                if (__any_sync(~0u, mx > m + kSlack)) {
-                    const float mn = fmaxf(m, mx);
-                    const float f = mn == m ? 1.0f : exp2_approx(m - mn);
-                    m = mn;
-                    l *= f;
-                    if (i > 0) {
-#pragma unroll
-                        for (int h = 0; h < D / 32; ++h) {
-                            uint32_t r[32];
-                            ld32(t_o + 32 * h, r);
+                uint32_t p[64];
+                bool find = __any_sync(~0u, m == -INFINITY); // the first block: its maximum first
+                for (;;) {
+                    if (find) {
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int h = 0; h < 8; ++h) {
+                            uint32_t r[16];
+                            ld16(t_s + 16 * h, r);
                             wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                            st16(t_o + 32 * h, r);
-                            st16(t_o + 32 * h + 16, r + 16);
+                            for (int e = 0; e < 16; ++e)
+                                mx = fmaxf(mx, __uint_as_float(r[e]));
+                        }
+                        const float mn = fmaxf(m, mx * rs);
+                        const float f = mn == m ? 1.0f : exp2_approx(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (i > 0) {
+#pragma unroll 1
+                            for (int h = 0; h < D / 16; ++h) {
+                                uint32_t r[16];
+                                ld16(t_o + 16 * h, r);
+                                wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                                st16(t_o + 16 * h, r);
+                            }
                         }
                     }
-                }
-                const float off = kShift - (m == -INFINITY ? 0.0f : m);
+                    const float off = kShift - (m == -INFINITY ? 0.0f : m);
+                    const uint64_t rs2 = pair(rs, rs), off2 = pair(off, off);
+                    uint64_t sum2 = 0;
+                    float mx = -INFINITY;
+                    uint32_t r[2][16];
+                    ld16(t_s, r[0]);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t r[32], p[16];
-                    ld32(t_s + 32 * h, r);
-                    wait_ld();
+                    for (int h = 0; h < 8; ++h) {
+                        wait_ld();
+                        if (h < 7)
+                            ld16(t_s + 16 * (h + 1), r[(h + 1) & 1]);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float x = exp2_approx(fmaf(__uint_as_float(r[e]), rs, off));
-                        float y = exp2_approx(fmaf(__uint_as_float(r[e + 1]), rs, off));
-                        x = all || 32 * h + e < vis ? x : 0.0f;
-                        y = all || 32 * h + e + 1 < vis ? y : 0.0f;
-                        l += x + y;
-                        p[e / 2] = pack_half2(x, y);
+                        for (int e = 0; e < 16; e += 2) {
+                            float x, y;
+                            unpair(fma2(pair(__uint_as_float(r[h & 1][e]), __uint_as_float(r[h & 1][e + 1])), rs2, off2),
+                                   x, y);
+                            mx = fmaxf(fmaxf(mx, x), y);
+                            x = exp2_approx(x);
+                            y = exp2_approx(y);
+                            sum2 = add2(sum2, pair(x, y));
+                            p[8 * h + e / 2] = pack_half2(x, y);
+                        }
                     }
-                    st16(t_s + 16 * h, p);
+                    // a score passed the running maximum by more than the slack: raise it and take them again
+                    find = __any_sync(~0u, mx > kShift + kSlack);
+                    if (!find) {
+                        float x, y;
+                        unpair(sum2, x, y);
+                        l += x + y;
+                        break;
+                    }
                 }
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    st16(t_s + 16 * h, p + 16 * h);
                 wait_st();
                 fence_before();
                 arrive(smem_addr(&sh.p_full[k]));
             }
+            if (l == 0.0f)
+                m = -INFINITY; // nothing seen
 
             // the tile's rows of O
-            if (w.n[k] > 0) {
+            if (nk > 0) {
                 wait(sh.o_full[k], n_o);
                 ++n_o;
                 fence_after();
@@ -514,17 +714,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 part[row] = m;
                 part[128 + row] = l;
             }
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
                 uint32_t r[32];
                 float x[32];
-                if (w.n[k] > 0) {
+                if (nk > 0) {
                     ld32(t_o + 32 * h, r);
                     wait_ld();
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    x[e] = w.n[k] > 0 ? __uint_as_float(r[e]) : 0.0f;
+                    x[e] = nk > 0 ? __uint_as_float(r[e]) : 0.0f;
                 if (whole) {
                     if (valid)
                         store(32 * h, x, m, l);
@@ -586,188 +786,128 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
     } else if (warp < 12) {
         // ---- unpacking: 128 threads fill K and V^T of a block ----
         const int u = tid - kSoft;
-        uint32_t n = 0; // blocks so far
-        for (int64_t pos = lo; pos < hi;) {
-            const Piece w = piece_at(c, b, at, pos, hi, tt);
-            const int cells = (w.s.len + kKv4Cell - 1) / kKv4Cell;
-            for (int i = 0; i < w.nblk; ++i, ++n) {
-                const int st = n & 1;
-                const int blk = w.b0 + i;
-                // lane z < 8: the place of cell z of the block, in 128-byte units; ~0 for none
-                uint32_t place = ~0u;
-                {
-                    const int cell = blk * 8 + (lane & 7);
-                    if (cell < cells) {
-                        const int page = kv4_page(c, w.s.row, cell >> (c.page_shift - 4));
-                        if (page >= 0)
-                            place = (uint32_t)(kv4_cell_offset<D>(c, page, a.layer, w.head,
-                                                                  cell & ((1 << (c.page_shift - 4)) - 1)) >> 7);
-                        else if (u < 8)
-                            kv4_bad(c);
-                    }
-                }
-                const uint32_t ks = tiles + C::kOffK + st * C::kQ, vs = tiles + C::kOffV + st * C::kV;
-                // K: 16-byte pieces (8 at D = 64): row 32 j + u / 4, channels 16 (u % 4) .. of each group
-                if (n >= 2)
-                    wait(sh.k_empty[st], (n >> 1) - 1);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = 32 * j + (u >> 2), t = u & 3;
-                    const uint32_t where = __shfl_sync(~0u, place, row >> 4);
-                    uint32_t wk[2 * G] = {}, pr[G] = {};
-                    if (where != ~0u) {
-                        const uint8_t *cell = c.pool + ((int64_t)where << 7);
-                        const uint8_t *src = cell + (row & 15) * (D / 2) + t * 8 * G;
-                        if (D == 128) {
-                            const uint4 x = ldg_nc128(src);
-                            wk[0] = x.x;
-                            wk[1] = x.y;
-                            wk[2 * G - 2] = x.z;
-                            wk[2 * G - 1] = x.w;
-                            const uint2 p = *(const uint2 *)(cell + Kv4Cell<D>::kKp + (row & 15) * 8);
-                            pr[0] = p.x;
-                            pr[G - 1] = p.y;
-                        } else {
-                            const uint2 x = *(const uint2 *)src;
-                            wk[0] = x.x;
-                            wk[1] = x.y;
-                            pr[0] = *(const uint32_t *)(cell + Kv4Cell<D>::kKp + (row & 15) * 4);
-                        }
-                    }
-                    uint32_t mids[2] = {0, 0};
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const __half2 s = __low2half2(as_half2(pr[g]));
-                        mids[g] = as_u32(__high2half2(as_half2(pr[g])));
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            const uint32_t x = wk[2 * g + f];
-                            sts128(ks + g * kSub + row * 128 + (((2 * t + f) ^ (row & 7)) << 4),
-                                   as_u32(__hmul2(nibble8<0>(x), s)), as_u32(__hmul2(nibble8<1>(x), s)),
-                                   as_u32(__hmul2(nibble8<2>(x), s)), as_u32(__hmul2(nibble8<3>(x), s)));
-                        }
-                    }
-                    if (t < 2) { // the k-step of the middles: two 16-byte halves of the row
-                        const uint32_t e = ks + G * kSub + row * 32 + ((t ^ ((row >> 2) & 1)) << 4);
-                        sts128(e, t ? 0 : mids[0], t ? 0 : mids[1], 0, 0);
-                    }
-                }
-                fence_proxy_async_smem();
-                arrive(smem_addr(&sh.k_full[st]));
-                // V^T: unit (cell, group, e, p): 8 channels 64 g + 8 e .., tokens 8 p .. of the cell
-                if (n >= 2)
-                    wait(sh.v_empty[st], (n >> 1) - 1);
-#pragma unroll
-                for (int j = 0; j < G; ++j) {
-                    const int p = u & 1, e = (u >> 3) & 7;
-                    const int half = G == 2 ? j : u >> 6, g = G == 2 ? u >> 6 : 0;
-                    const int cell_i = half * 4 + ((u >> 1) & 3);
-                    const uint32_t where = __shfl_sync(~0u, place, cell_i);
-                    uint2 x[4] = {}, pr[4] = {};
-                    if (where != ~0u) {
-                        const uint8_t *cell = c.pool + ((int64_t)where << 7);
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            x[t] = *(const uint2 *)(cell + Kv4Cell<D>::kV + g * 512 + e * 64 + t * 16 + p * 8);
-                            pr[t] = *(const uint2 *)(cell + Kv4Cell<D>::kVp + ((4 * p + t) * G + g) * 8);
-                        }
-                    }
-                    const int tok = blk * kBlock + cell_i * 16 + 8 * p; // past the end V is 0, whatever is there
-                    if (tok + 8 > w.s.len) {
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const uint32_t keep = (tok + 2 * t < w.s.len ? 0x0000FFFFu : 0u) |
-                                                  (tok + 2 * t + 1 < w.s.len ? 0xFFFF0000u : 0u);
-                            pr[t].x &= keep;
-                            pr[t].y &= keep;
-                        }
-                    }
-                    const uint32_t dst = vs + half * (D * 128) + (64 * g + 8 * e) * 128;
-                    const int chunk = 2 * ((u >> 1) & 3) + p;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t y[4][4]; // [nibble][token pair]
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const uint32_t wv = q ? x[t].y : x[t].x;
-                            const __half2 s = as_half2(pr[t].x), mid = as_half2(pr[t].y);
-                            y[0][t] = as_u32(__hfma2(nibble8<0>(wv), s, mid));
-                            y[1][t] = as_u32(__hfma2(nibble8<1>(wv), s, mid));
-                            y[2][t] = as_u32(__hfma2(nibble8<2>(wv), s, mid));
-                            y[3][t] = as_u32(__hfma2(nibble8<3>(wv), s, mid));
-                        }
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const int r = 4 * q + z; // row & 7
-                            sts128(dst + r * 128 + ((chunk ^ r) << 4), y[z][0], y[z][1], y[z][2], y[z][3]);
-                        }
-                    }
-                }
-                fence_proxy_async_smem();
-                arrive(smem_addr(&sh.v_full[st]));
+        Piece w{};
+        int64_t pos = lo;
+        int i = 0; // the block being fetched: block b0 + i of the piece
+        RawK<D> rk;
+        RawV<D> rv;
+        int len = 0, blk = 0; // of the block in rk and rv
+        uint32_t place = ~0u;
+        // lane z < 8: the place of cell z of the block to fetch, in 128-byte units; ~0 for none
+        const auto find = [&]() {
+            const int cell = (w.b0 + i) * 8 + (lane & 7);
+            place = ~0u;
+            if (cell * kKv4Cell < w.s.len) {
+                const int page = kv4_page(c, w.s.row, cell >> (c.page_shift - 4));
+                if (page >= 0)
+                    place = (uint32_t)(kv4_cell_offset<D>(c, page, a.layer, w.head,
+                                                          cell & ((1 << (c.page_shift - 4)) - 1)) >> 7);
+                else if (u < 8)
+                    kv4_bad(c);
             }
-            pos += w.nblk;
-            if (pos < hi)
-                next_segment(c, b, w, tt, &at);
+        };
+        if (pos < hi) {
+            w = piece_at(c, b, at, pos, hi, tt);
+            find();
+            load_k<D>(rk, c.pool, place, u);
+            load_v<D>(rv, c.pool, place, u);
+        }
+        for (uint32_t n = 0; pos < hi; ++n) {
+            len = w.s.len;
+            blk = w.b0 + i;
+            // the next block
+            if (++i == w.nblk) {
+                pos += w.nblk;
+                i = 0;
+                if (pos < hi) {
+                    next_segment(c, b, w, tt, &at);
+                    w = piece_at(c, b, at, pos, hi, tt);
+                }
+            }
+            const bool more = pos < hi;
+            if (more)
+                find();
+            const int st = n & 1;
+            if (n >= 2)
+                wait(sh.k_empty[st], (n >> 1) - 1);
+            unpack_k<D>(rk, tiles + C::kOffK + st * C::kQ, u);
+            fence_proxy_async_smem();
+            arrive(smem_addr(&sh.k_full[st]));
+            if (more)
+                load_k<D>(rk, c.pool, place, u);
+            if (n >= 2)
+                wait(sh.v_empty[st], (n >> 1) - 1);
+            unpack_v<D>(rv, tiles + C::kOffV + st * C::kV, u, len - blk * kBlock);
+            fence_proxy_async_smem();
+            arrive(smem_addr(&sh.v_full[st]));
+            if (more)
+                load_v<D>(rv, c.pool, place, u);
         }
     } else if (lane == 0) {
         // ---- the MMAs ----
-        uint32_t n = 0, n_p[2] = {0, 0}, piece = 0;
+        uint32_t n = 0, n_p0 = 0, n_p1 = 0, piece = 0;
+        const uint32_t desc0 = kDescLo | (tiles >> 4);
         const auto scores = [&](int k, uint32_t blk) { // S of tile k
-            const uint32_t q = tiles + k * C::kQ, kk = tiles + C::kOffK + (blk & 1) * C::kQ;
+            const uint32_t q = desc0 + k * (C::kQ >> 4), kk = desc0 + (C::kOffK >> 4) + (blk & 1) * (C::kQ >> 4);
             const uint32_t d = tmem + k * 128;
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    mma_ss(d, smem_desc<128>(q + g * kSub + 32 * x), smem_desc<128>(kk + g * kSub + 32 * x),
-                           kIdesc<128>, g + x > 0);
-            mma_ss(d, smem_desc<32>(q + G * kSub), smem_desc<32>(kk + G * kSub), kIdesc<128>, true);
+                    mma_ss<128>(d, q + ((g * kSub + 32 * x) >> 4), kk + ((g * kSub + 32 * x) >> 4), kIdesc<128>, g + x);
+            mma_ss<32>(d, q + ((G * kSub) >> 4), kk + ((G * kSub) >> 4), kIdesc<128>, 1);
             commit(smem_addr(&sh.s_full[k]));
         };
         const auto values = [&](int k, uint32_t blk, bool accumulate) { // O of tile k
-            const uint32_t v = tiles + C::kOffV + (blk & 1) * C::kV;
+            const uint32_t v = desc0 + (C::kOffV >> 4) + (blk & 1) * (C::kV >> 4);
             const uint32_t d = tmem + 256 + k * 128, p = tmem + k * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    mma_ts(d, p + 8 * (4 * h + x), smem_desc<128>(v + h * (D * 128) + 32 * x), kIdesc<D>,
-                           accumulate || h + x > 0);
+                    mma_ts(d, p + 8 * (4 * h + x), v + ((h * (D * 128) + 32 * x) >> 4), kIdesc<D>,
+                           h + x > 0 ? 1u : (uint32_t)accumulate);
         };
         for (int64_t pos = lo; pos < hi; ++piece) {
             const Piece w = piece_at(c, b, at, pos, hi, tt);
+            const int n0 = w.n0, n1 = w.n1;
             wait(sh.q_full[0], piece);
             wait(sh.q_full[1], piece);
             wait(sh.k_full[n & 1], n >> 1);
             fence_after();
-            for (int k = 0; k < 2; ++k)
-                if (w.n[k] > 0)
-                    scores(k, n);
+            if (n0 > 0)
+                scores(0, n);
+            if (n1 > 0)
+                scores(1, n);
             commit(smem_addr(&sh.k_empty[n & 1]));
             for (int i = 0; i < w.nblk; ++i, ++n) {
                 const bool more = i + 1 < w.nblk;
                 wait(sh.v_full[n & 1], n >> 1);
-                for (int k = 0; k < 2; ++k) {
-                    if (i < w.n[k]) {
-                        wait(sh.p_full[k], n_p[k]);
-                        ++n_p[k];
-                        fence_after();
-                        values(k, n, i > 0);
-                        if (i == w.n[k] - 1)
-                            commit(smem_addr(&sh.o_full[k]));
-                    }
-                    if (k == 1)
-                        commit(smem_addr(&sh.v_empty[n & 1]));
-                    if (more) {
-                        if (k == 0)
-                            wait(sh.k_full[(n + 1) & 1], (n + 1) >> 1);
-                        fence_after();
-                        if (i + 1 < w.n[k])
-                            scores(k, n + 1);
-                        if (k == 1)
-                            commit(smem_addr(&sh.k_empty[(n + 1) & 1]));
-                    }
+                if (i < n0) {
+                    wait(sh.p_full[0], n_p0++);
+                    fence_after();
+                    values(0, n, i > 0);
+                    if (i == n0 - 1)
+                        commit(smem_addr(&sh.o_full[0]));
+                }
+                if (more) {
+                    wait(sh.k_full[(n + 1) & 1], (n + 1) >> 1);
+                    fence_after();
+                    if (i + 1 < n0)
+                        scores(0, n + 1);
+                }
+                if (i < n1) {
+                    wait(sh.p_full[1], n_p1++);
+                    fence_after();
+                    values(1, n, i > 0);
+                    if (i == n1 - 1)
+                        commit(smem_addr(&sh.o_full[1]));
+                }
+                commit(smem_addr(&sh.v_empty[n & 1]));
+                if (more) {
+                    if (i + 1 < n1)
+                        scores(1, n + 1);
+                    commit(smem_addr(&sh.k_empty[(n + 1) & 1]));
                 }
             }
             pos += w.nblk;
