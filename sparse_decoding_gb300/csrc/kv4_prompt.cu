@@ -68,9 +68,16 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols)
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void commit(uint32_t bar)
+// The instructions that one thread issues are predicated (on `one`) instead of
+// branched around: the MMA warp's control flow stays uniform, so that descriptors
+// live in uniform registers. In a branch of one lane each MMA waited for their
+// transfer (about 130 cycles between MMAs of 64).
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t one)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+                 "r"(one)
+                 : "memory");
 }
 // Shared-memory descriptor of a K-major tile with rows of SW bytes under the
 // SW-byte swizzle, 8-row groups 8 SW bytes apart (layout type 2: 128 bytes, 6: 32):
@@ -81,21 +88,23 @@ constexpr uint32_t kDescLo = 1u << 16;
 
 // D (tensor memory) (+)= A (shared memory) B (shared memory)^T; a, b: the low words
 template <int SW>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t one)
 {
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %6, 0;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi<SW>)
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi<SW>), "r"(one)
                  : "memory");
 }
 // D (tensor memory) (+)= A (tensor memory) B (shared memory)^T
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t one)
 {
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %6, 0;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "mov.b64 y, {%2, %5};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi<128>)
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi<128>), "r"(one)
                  : "memory");
 }
 // 32 columns of this thread's lane; the caller waits.
@@ -319,6 +328,16 @@ template <int D> __device__ __forceinline__ void unpack_v(const RawV<D> &r, uint
     }
 }
 
+// mbar_wait_bounded for waits that are short and many: the clock is read only
+// once a wait has been polled for a while.
+__device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, uint32_t *status, bool &dead)
+{
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity))
+            return;
+    mbar_wait_bounded(bar, parity, status, dead);
+}
+
 struct PromptArgs {
     int layer, ratio, n_q_heads;
     const uint16_t *q;
@@ -520,9 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
     const int64_t share = sh.share;
     const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share < sh.total ? lo + share : sh.total;
     bool dead = false;
-    const auto wait = [&](uint64_t &bar, uint32_t parity) {
-        return mbar_wait_bounded(smem_addr(&bar), parity & 1u, c.status, dead);
-    };
+    const auto wait = [&](uint64_t &bar, uint32_t parity) { wait_bounded(smem_addr(&bar), parity & 1u, c.status, dead); };
     Place at = sh.start;
 
     if (warp < 8) {
@@ -843,8 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             if (more)
                 load_v<D>(rv, c.pool, place, u);
         }
-    } else if (lane == 0) {
-        // ---- the MMAs ----
+    } else {
+        // ---- the MMAs: every lane follows, lane 0 issues ----
+        const uint32_t one = lane == 0;
+        const uint32_t tmem = __reduce_max_sync(~0u, sh.tmem); // uniform
+
         uint32_t n = 0, n_p0 = 0, n_p1 = 0, piece = 0;
         const uint32_t desc0 = kDescLo | (tiles >> 4);
         const auto scores = [&](int k, uint32_t blk) { // S of tile k
@@ -854,11 +874,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    mma_ss<128>(d, q + ((g * kSub + 32 * x) >> 4), kk + ((g * kSub + 32 * x) >> 4), kIdesc<128>, g + x);
-            mma_ss<32>(d, q + ((G * kSub) >> 4), kk + ((G * kSub) >> 4), kIdesc<128>, 1);
-            commit(smem_addr(&sh.s_full[k]));
+                    mma_ss<128>(d, q + ((g * kSub + 32 * x) >> 4), kk + ((g * kSub + 32 * x) >> 4), kIdesc<128>, g + x, one);
+            mma_ss<32>(d, q + ((G * kSub) >> 4), kk + ((G * kSub) >> 4), kIdesc<128>, 1, one);
+            commit(smem_addr(&sh.s_full[k]), one);
         };
-        const auto values = [&](int k, uint32_t blk, bool accumulate) { // O of tile k
+        const auto values = [&](int k, uint32_t blk, uint32_t accumulate) { // O of tile k
             const uint32_t v = desc0 + (C::kOffV >> 4) + (blk & 1) * (C::kV >> 4);
             const uint32_t d = tmem + 256 + k * 128, p = tmem + k * 128;
 #pragma unroll
@@ -866,11 +886,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     mma_ts(d, p + 8 * (4 * h + x), v + ((h * (D * 128) + 32 * x) >> 4), kIdesc<D>,
-                           h + x > 0 ? 1u : (uint32_t)accumulate);
+                           h + x > 0 ? 1u : accumulate, one);
         };
-        for (int64_t pos = lo; pos < hi; ++piece) {
+        for (int64_t pos = lo; __any_sync(~0u, pos < hi); ++piece) {
             const Piece w = piece_at(c, b, at, pos, hi, tt);
-            const int n0 = w.n0, n1 = w.n1;
+            const int n0 = __reduce_max_sync(~0u, w.n0), n1 = __reduce_max_sync(~0u, w.n1);
+            const int nblk = __reduce_max_sync(~0u, w.nblk);
             wait(sh.q_full[0], piece);
             wait(sh.q_full[1], piece);
             wait(sh.k_full[n & 1], n >> 1);
@@ -879,16 +900,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 scores(0, n);
             if (n1 > 0)
                 scores(1, n);
-            commit(smem_addr(&sh.k_empty[n & 1]));
-            for (int i = 0; i < w.nblk; ++i, ++n) {
-                const bool more = i + 1 < w.nblk;
+            commit(smem_addr(&sh.k_empty[n & 1]), one);
+            for (int i = 0; i < nblk; ++i, ++n) {
+                const bool more = i + 1 < nblk;
                 wait(sh.v_full[n & 1], n >> 1);
                 if (i < n0) {
                     wait(sh.p_full[0], n_p0++);
                     fence_after();
                     values(0, n, i > 0);
                     if (i == n0 - 1)
-                        commit(smem_addr(&sh.o_full[0]));
+                        commit(smem_addr(&sh.o_full[0]), one);
                 }
                 if (more) {
                     wait(sh.k_full[(n + 1) & 1], (n + 1) >> 1);
@@ -901,13 +922,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     fence_after();
                     values(1, n, i > 0);
                     if (i == n1 - 1)
-                        commit(smem_addr(&sh.o_full[1]));
+                        commit(smem_addr(&sh.o_full[1]), one);
                 }
-                commit(smem_addr(&sh.v_empty[n & 1]));
+                commit(smem_addr(&sh.v_empty[n & 1]), one);
                 if (more) {
                     if (i + 1 < n1)
                         scores(1, n + 1);
-                    commit(smem_addr(&sh.k_empty[(n + 1) & 1]));
+                    commit(smem_addr(&sh.k_empty[(n + 1) & 1]), one);
                 }
             }
             pos += w.nblk;
