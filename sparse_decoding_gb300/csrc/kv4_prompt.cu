@@ -36,9 +36,13 @@
 namespace nm {
 namespace {
 
-constexpr int kSoft = 256;     // softmax threads: two tiles of 128 rows
-constexpr int kUnpack = 128;   // unpacking threads
-constexpr int kThreads = kSoft + kUnpack + 32;
+constexpr int kSoft = 256;      // softmax threads: two tiles of 128 rows
+constexpr int kUnpack = 128;    // unpacking threads
+constexpr int kMmaWarp = 12;    // (its warpgroup's other three warps idle)
+constexpr int kThreads = 512;
+// Registers of a thread in each role; 128 at launch, and 2 * 184 + 104 + 40 = 4 * 128.
+constexpr int kSoftRegs = 184, kUnpackRegs = 104, kMmaRegs = 40;
+constexpr int kSeqCache = 512;  // sequences whose descriptors are kept in shared memory
 constexpr int kBlock = 128;    // tokens of a block
 constexpr int kMinShare = 2;   // blocks of a CTA at least
 constexpr int kSub = 128 * 128; // bytes of 128 rows of 64 fp16
@@ -107,19 +111,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
                  "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi<128>), "r"(one)
                  : "memory");
 }
-// 32 columns of this thread's lane; the caller waits.
-__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-                   "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-                   "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr));
-}
+// 16 columns of this thread's lane; the caller waits.
 __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -163,6 +155,26 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r)
                  : "memory");
 }
 
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+                   "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+                   "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+template <int N> __device__ __forceinline__ void setmaxnreg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void setmaxnreg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // kind::f16, A and B fp16 and K-major, D fp32, M = 128.
 template <int N> constexpr uint32_t kIdesc = (1u << 4) | ((N >> 3) << 17) | ((128 >> 4) << 24);
 
@@ -228,14 +240,14 @@ template <int D> __device__ __forceinline__ void load_k(RawK<D> &r, const uint8_
             r.w[j][1] = x.y;
             r.w[j][2 * G - 2] = x.z;
             r.w[j][2 * G - 1] = x.w;
-            const uint2 p = have ? *(const uint2 *)(cell + Kv4Cell<D>::kKp + (row & 15) * 8) : make_uint2(0, 0);
+            const uint2 p = have ? __ldg((const uint2 *)(cell + Kv4Cell<D>::kKp + (row & 15) * 8)) : make_uint2(0, 0);
             r.p[j][0] = p.x;
             r.p[j][G - 1] = p.y;
         } else {
-            const uint2 x = have ? *(const uint2 *)src : make_uint2(0, 0);
+            const uint2 x = have ? __ldg((const uint2 *)src) : make_uint2(0, 0);
             r.w[j][0] = x.x;
             r.w[j][1] = x.y;
-            r.p[j][0] = have ? *(const uint32_t *)(cell + Kv4Cell<D>::kKp + (row & 15) * 4) : 0u;
+            r.p[j][0] = have ? __ldg((const uint32_t *)(cell + Kv4Cell<D>::kKp + (row & 15) * 4)) : 0u;
         }
     }
 }
@@ -276,9 +288,9 @@ template <int D> __device__ __forceinline__ void load_v(RawV<D> &r, const uint8_
         const bool have = where != ~0u;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            r.w[j][t] = have ? *(const uint2 *)(cell + Kv4Cell<D>::kV + g * 512 + e * 64 + t * 16 + p * 8)
+            r.w[j][t] = have ? __ldg((const uint2 *)(cell + Kv4Cell<D>::kV + g * 512 + e * 64 + t * 16 + p * 8))
                              : make_uint2(0, 0);
-            r.p[j][t] = have ? *(const uint2 *)(cell + Kv4Cell<D>::kVp + ((4 * p + t) * G + g) * 8) : make_uint2(0, 0);
+            r.p[j][t] = have ? __ldg((const uint2 *)(cell + Kv4Cell<D>::kVp + ((4 * p + t) * G + g) * 8)) : make_uint2(0, 0);
         }
     }
 }
@@ -373,32 +385,36 @@ __device__ __forceinline__ int64_t pairs_of(const Kv4Seq &s, int tt)
     return ((int64_t)s.n_new + 2 * tt - 1) / (2 * tt);
 }
 
-// A place on the line of blocks.
+// A segment takes its blocks and kOver more on the line: what starting and ending a
+// piece costs. A place before the first block of a segment is in those.
+constexpr int kOver = 3;
 struct Place {
-    int seq, head, pair, block;
+    int seq, head, pair, step;
 };
 
 // What the roles of a CTA agree on about one piece of work.
 struct Piece {
     Kv4Seq s;
     int seq, head, pair, b0, nblk, total; // blocks [b0, b0 + nblk) of the pair's total
+    int steps;                            // of the line
     int n0, n1;                           // of those, how many each tile takes
     int64_t seg_lo;                       // the segment's first place on the line
 };
 
-__device__ __forceinline__ Piece piece_at(const Kv4 &c, const Kv4Batch &b, const Place &p, int64_t pos, int64_t hi,
-                                          int tt)
+__device__ __forceinline__ Piece piece_at(const Kv4Seq &s, const Place &p, int64_t pos, int64_t hi, int tt)
 {
     Piece w;
-    w.s = kv4_seq(c, b, p.seq, false);
+    w.s = s;
     w.seq = p.seq;
     w.head = p.head;
     w.pair = p.pair;
-    w.b0 = p.block;
     w.total = pair_blocks(w.s, p.pair, tt);
-    w.seg_lo = pos - p.block;
+    w.seg_lo = pos - p.step;
     const int64_t left = hi - pos;
-    w.nblk = w.total - w.b0 < left ? w.total - w.b0 : (int)left;
+    w.steps = w.total + kOver - p.step < left ? w.total + kOver - p.step : (int)left;
+    w.b0 = p.step > kOver ? p.step - kOver : 0;
+    const int b1 = p.step + w.steps - kOver;
+    w.nblk = b1 > w.b0 ? b1 - w.b0 : 0;
     const int n0 = blocks_of(tile_limit(w.s, 2 * (int64_t)p.pair, tt)) - w.b0;
     const int n1 = blocks_of(tile_limit(w.s, 2 * (int64_t)p.pair + 1, tt)) - w.b0;
     w.n0 = n0 < 0 ? 0 : n0 > w.nblk ? w.nblk : n0;
@@ -407,9 +423,11 @@ __device__ __forceinline__ Piece piece_at(const Kv4 &c, const Kv4Batch &b, const
 }
 
 // The place after a piece that ends its segment.
-__device__ __forceinline__ void next_segment(const Kv4 &c, const Kv4Batch &b, const Piece &w, int tt, Place *p)
+template <typename SeqAt>
+__device__ __forceinline__ void next_segment(const Kv4 &c, const Kv4Batch &b, const Piece &w, int tt, const SeqAt &seq_at,
+                                             Place *p)
 {
-    p->block = 0;
+    p->step = 0;
     if (++p->pair < pairs_of(w.s, tt))
         return;
     p->pair = 0;
@@ -418,7 +436,33 @@ __device__ __forceinline__ void next_segment(const Kv4 &c, const Kv4Batch &b, co
     p->head = 0;
     do
         ++p->seq;
-    while (p->seq < b.n_seqs && kv4_seq(c, b, p->seq, false).n_new == 0);
+    while (p->seq < b.n_seqs && seq_at(p->seq).n_new == 0);
+}
+
+// The next piece with blocks, *pos past the end (hi) when there is none.
+template <typename SeqAt>
+__device__ __forceinline__ void next_piece(const Kv4 &c, const Kv4Batch &b, const SeqAt &seq_at, Piece *w, Place *at,
+                                           int64_t *pos, int64_t hi, int tt)
+{
+    *pos += w->steps;
+    if (*pos >= hi)
+        return;
+    next_segment(c, b, *w, tt, seq_at, at);
+    *w = piece_at(seq_at(at->seq), *at, *pos, hi, tt);
+    if (w->nblk == 0) // the line's end is before the segment's first block
+        *pos = hi;
+}
+template <typename SeqAt>
+__device__ __forceinline__ Piece first_piece(const Kv4 &c, const Kv4Batch &b, const SeqAt &seq_at, Place *at,
+                                             int64_t *pos, int64_t hi, int tt)
+{
+    Piece w{};
+    if (*pos < hi) {
+        w = piece_at(seq_at(at->seq), *at, *pos, hi, tt);
+        if (w.nblk == 0)
+            *pos = hi;
+    }
+    return w;
 }
 
 struct Shared {
@@ -439,7 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
     __shared__ Shared sh;
     uint8_t *const base = dsmem + ((1024u - (smem_addr(dsmem) & 1023u)) & 1023u);
     const uint32_t tiles = smem_addr(base);
-    int64_t *const pre = (int64_t *)(base + C::kTiles); // [n_seqs + 1]
+    int64_t *const pre = (int64_t *)base;                // [n_seqs + 1], before the tiles are filled
+    Kv4Seq *const seqs = (Kv4Seq *)(base + C::kTiles);   // [min(n_seqs, kSeqCache)]
+    const auto seq_at = [&](int i) { return b.n_seqs <= kSeqCache ? seqs[i] : kv4_seq(c, b, i, false); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tt = 128 / a.ratio; // tokens of a tile
 
@@ -456,15 +502,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         }
         fence_mbar_init();
     }
-    if (warp == 12)
+    if (warp == kMmaWarp)
         tmem_alloc(smem_addr(&sh.tmem), 512);
 
     // blocks of each sequence (a warp to a sequence), then where each starts on the line
     for (int i = warp; i < b.n_seqs; i += kThreads / 32) {
         const Kv4Seq s = kv4_seq(c, b, i, blockIdx.x == 0 && lane == 0);
+        if (lane == 0 && b.n_seqs <= kSeqCache)
+            seqs[i] = s;
         int64_t n = 0;
         for (int64_t j = lane; j < pairs_of(s, tt); j += 32)
-            n += pair_blocks(s, j, tt);
+            n += pair_blocks(s, j, tt) + kOver;
         for (int o = 16; o; o >>= 1)
             n += __shfl_xor_sync(~0u, n, o);
         if (lane == 0)
@@ -491,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         __syncwarp();
         const int64_t total = sum;
         int64_t share = (total + gridDim.x - 1) / gridDim.x;
-        share = share < kMinShare ? kMinShare : share;
+        share = share < kMinShare + kOver ? kMinShare + kOver : share;
         const int64_t pos = (int64_t)blockIdx.x * share;
         Place p{};
         if (pos < total) {
@@ -504,14 +552,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     h = m;
             }
             p.seq = l;
-            const Kv4Seq s = kv4_seq(c, b, l, false);
+            const Kv4Seq s = seq_at(l);
             const int64_t per = (pre[l + 1] - pre[l]) / c.n_kv_heads;
             p.head = (int)((pos - pre[l]) / per);
             int64_t left = (pos - pre[l]) % per;
             // the pair that holds block `left` of the head's line
             for (int64_t j0 = 0;; j0 += 32) {
                 const int64_t j = j0 + lane;
-                const int n = j < pairs_of(s, tt) ? pair_blocks(s, j, tt) : 0;
+                const int n = j < pairs_of(s, tt) ? pair_blocks(s, j, tt) + kOver : 0;
                 int64_t x = n;
                 for (int o = 1; o < 32; o <<= 1) {
                     const int64_t y = __shfl_up_sync(~0u, x, o);
@@ -522,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 if (in || j0 + 32 >= pairs_of(s, tt)) {
                     const int who = in ? __ffs(in) - 1 : 0;
                     p.pair = (int)(j0 + who);
-                    p.block = (int)(left - (__shfl_sync(~0u, x, who) - __shfl_sync(~0u, n, who)));
+                    p.step = (int)(left - (__shfl_sync(~0u, x, who) - __shfl_sync(~0u, n, who)));
                     break;
                 }
                 left -= __shfl_sync(~0u, x, 31);
@@ -544,175 +592,165 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
 
     if (warp < 8) {
         // ---- softmax: a row per thread ----
-        const int k = warp >> 2;          // the tile
+        setmaxnreg_inc<kSoftRegs>();
+        const int k = warp >> 2; // the tile
         const int row = tid & 127;
+        const int row_token = row / a.ratio, row_head = row % a.ratio;
         const uint32_t q_tile = tiles + k * C::kQ;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + k * 128, t_o = tmem + lanes + 256 + k * 128;
+        const auto count = [&](const Piece &w) { return k ? w.n1 : w.n0; };
+        const auto token_of = [&](const Piece &w) { return (2 * (int64_t)w.pair + k) * tt + row_token; };
+        const auto valid_in = [&](const Piece &w) { return row < tt * a.ratio && token_of(w) < w.s.n_new; };
         uint32_t n_s = 0, n_o = 0; // blocks and pieces of this tile so far
-        for (int64_t pos = lo; pos < hi;) {
-            const Piece w = piece_at(c, b, at, pos, hi, tt);
-            const int64_t tile = 2 * (int64_t)w.pair + k;
-            const int nk = k ? w.n1 : w.n0;
-            const int64_t token = tile * tt + row / a.ratio; // of the sequence's new ones
-            const bool valid = row < tt * a.ratio && token < w.s.n_new;
-            const int limit = valid ? w.s.len - w.s.n_new + (int)token + 1 : 0;
-            const int head = w.head * a.ratio + row % a.ratio;
 
-            // the row of Q: scaled by a power of two, channels in the order of the unpacked keys
-            float rs;
-            {
-                const uint16_t *q = a.q + (w.s.first + token) * a.q_stride + (int64_t)head * D;
-                uint32_t top = 0;
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 x = valid ? ldg_nc128(q + 8 * i) : make_uint4(0, 0, 0, 0);
-                    const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+        // The row of Q: scaled by a power of two, channels in the order of the unpacked
+        // keys. Returns the factor of the scores.
+        const auto load_q = [&](const Piece &w) {
+            constexpr int N = D / 8; // 16-byte pieces of a row
+            const bool valid = valid_in(w);
+            const uint16_t *q = a.q + (w.s.first + token_of(w)) * a.q_stride + ((int64_t)w.head * a.ratio + row_head) * D;
+            uint4 x[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                x[i] = valid ? ldg_nc128(q + 8 * i) : make_uint4(0, 0, 0, 0);
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    top = max(top, max(ws[n] & 0x7FFF0000u, (ws[n] << 16) & 0x7FFF0000u));
+            }
+            uint32_t e2 = top >> 23;
+            e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
+            const float up = __uint_as_float(e2 << 23);
+            const float down = a.scale < 0.0f ? -__uint_as_float((254u - e2) << 23) : __uint_as_float((254u - e2) << 23);
+            uint32_t ext[2] = {0, 0}; // the groups' sums of q, each in two parts
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 v = x[8 * g + i];
+                    const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+                    float y[8];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
-                        top = max(top, ws[n] & 0x7FFF0000u);
-                        top = max(top, (ws[n] << 16) & 0x7FFF0000u);
+                        y[2 * n] = __half2float(__float2half_rn(bf16lo_to_f32(ws[n]) * down));
+                        y[2 * n + 1] = __half2float(__float2half_rn(bf16hi_to_f32(ws[n]) * down));
+                        sum += y[2 * n] + y[2 * n + 1];
                     }
+                    sts128(q_tile + g * kSub + row * 128 + ((i ^ (row & 7)) << 4), pack_half2(y[0], y[4]),
+                           pack_half2(y[1], y[5]), pack_half2(y[2], y[6]), pack_half2(y[3], y[7]));
                 }
-                uint32_t e2 = top >> 23;
-                e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
-                const float up = __uint_as_float(e2 << 23);
-                float down = __uint_as_float((254u - e2) << 23);
-                rs = fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f); // above 0, so that masked scores stay -inf
-                if (a.scale < 0.0f)
-                    down = -down;
-                uint32_t ext[2] = {0, 0};
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    float sum = 0.0f;
-#pragma unroll 2
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 v = valid ? ldg_nc128(q + 64 * g + 8 * i) : make_uint4(0, 0, 0, 0);
-                        const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
-                        float y[8];
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            y[2 * n] = __half2float(__float2half_rn(bf16lo_to_f32(ws[n]) * down));
-                            y[2 * n + 1] = __half2float(__float2half_rn(bf16hi_to_f32(ws[n]) * down));
-                            sum += y[2 * n] + y[2 * n + 1];
-                        }
-                        sts128(q_tile + g * kSub + row * 128 + ((i ^ (row & 7)) << 4), pack_half2(y[0], y[4]),
-                               pack_half2(y[1], y[5]), pack_half2(y[2], y[6]), pack_half2(y[3], y[7]));
-                    }
-                    const float part = __half2float(__float2half_rn(sum));
-                    ext[g] = pack_half2(part, sum - part);
-                }
-                const uint32_t e_row = q_tile + G * kSub + row * 32, flip = (row >> 2) & 1;
-                sts128(e_row + (flip << 4), ext[0], ext[1], 0, 0);
-                sts128(e_row + ((flip ^ 1) << 4), 0, 0, 0, 0);
-                fence_proxy_async_smem();
-                arrive(smem_addr(&sh.q_full[k]));
+                const float part = __half2float(__float2half_rn(sum));
+                ext[g] = pack_half2(part, sum - part);
             }
+            const uint32_t e_row = q_tile + G * kSub + row * 32, flip = (row >> 2) & 1;
+            sts128(e_row + (flip << 4), ext[0], ext[1], 0, 0);
+            sts128(e_row + ((flip ^ 1) << 4), 0, 0, 0, 0);
+            fence_proxy_async_smem();
+            arrive(smem_addr(&sh.q_full[k]));
+            return fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f); // above 0, so that masked scores stay -inf
+        };
 
+        float rs = 1.0f;
+        int64_t pos = lo;
+        Piece w = first_piece(c, b, seq_at, &at, &pos, hi, tt);
+        if (pos < hi && count(w) > 0)
+            rs = load_q(w);
+        while (pos < hi) {
+            const int nk = count(w);
+            const int limit = valid_in(w) ? w.s.len - w.s.n_new + (int)token_of(w) + 1 : 0;
             // rows that see nothing of the piece need no maximum
             float m = limit > w.b0 * kBlock ? -INFINITY : 0.0f, l = 0.0f;
             for (int i = 0; i < nk; ++i, ++n_s) {
                 wait(sh.s_full[k], n_s);
                 fence_after();
                 const int vis = limit - (w.b0 + i) * kBlock; // columns this row sees
-                if (!__all_sync(~0u, vis >= kBlock)) {
-                    // the others become -inf in place: only the last blocks of a row come here
-#pragma unroll 1
-                    for (int h = 0; h < 8; ++h) {
-                        uint32_t r[16];
-                        ld16(t_s + 16 * h, r);
-                        wait_ld();
+                uint32_t r[128];
+                float mx = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            r[e] = 16 * h + e < vis ? r[e] : 0xFF800000u;
-                        st16(t_s + 16 * h, r);
-                    }
-                    wait_st();
+                for (int h = 0; h < 4; ++h)
+                    ld32(t_s + 32 * h, r + 32 * h);
+                wait_ld();
+                if (!__all_sync(~0u, vis >= kBlock)) { // only the last blocks of a row come here
+#pragma unroll
+                    for (int e = 0; e < 128; ++e)
+                        r[e] = e < vis ? r[e] : 0xFF800000u;
                 }
-                uint32_t p[64];
-                bool find = __any_sync(~0u, m == -INFINITY); // the first block: its maximum first
-                for (;;) {
-                    if (find) {
-                        float mx = -INFINITY;
+                // the maximum; it is raised when a score passes it by more than the slack
+#pragma unroll
+                for (int e = 0; e < 128; e += 2)
+                    mx = fmaxf(fmaxf(mx, __uint_as_float(r[e])), __uint_as_float(r[e + 1]));
+                mx *= rs;
+                if (__any_sync(~0u, mx > m + kSlack)) {
+                    const float mn = fmaxf(m, mx);
+                    const float f = mn == m ? 1.0f : exp2_approx(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (i > 0) {
 #pragma unroll 1
-                        for (int h = 0; h < 8; ++h) {
-                            uint32_t r[16];
-                            ld16(t_s + 16 * h, r);
+                        for (int h = 0; h < D / 16; ++h) {
+                            uint32_t o[16];
+                            ld16(t_o + 16 * h, o);
                             wait_ld();
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                mx = fmaxf(mx, __uint_as_float(r[e]));
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            st16(t_o + 16 * h, o);
                         }
-                        const float mn = fmaxf(m, mx * rs);
-                        const float f = mn == m ? 1.0f : exp2_approx(m - mn);
-                        m = mn;
-                        l *= f;
-                        if (i > 0) {
-#pragma unroll 1
-                            for (int h = 0; h < D / 16; ++h) {
-                                uint32_t r[16];
-                                ld16(t_o + 16 * h, r);
-                                wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                                st16(t_o + 16 * h, r);
-                            }
-                        }
-                    }
-                    const float off = kShift - (m == -INFINITY ? 0.0f : m);
-                    const uint64_t rs2 = pair(rs, rs), off2 = pair(off, off);
-                    uint64_t sum2 = 0;
-                    float mx = -INFINITY;
-                    uint32_t r[2][16];
-                    ld16(t_s, r[0]);
-#pragma unroll
-                    for (int h = 0; h < 8; ++h) {
-                        wait_ld();
-                        if (h < 7)
-                            ld16(t_s + 16 * (h + 1), r[(h + 1) & 1]);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float x, y;
-                            unpair(fma2(pair(__uint_as_float(r[h & 1][e]), __uint_as_float(r[h & 1][e + 1])), rs2, off2),
-                                   x, y);
-                            mx = fmaxf(fmaxf(mx, x), y);
-                            x = exp2_approx(x);
-                            y = exp2_approx(y);
-                            sum2 = add2(sum2, pair(x, y));
-                            p[8 * h + e / 2] = pack_half2(x, y);
-                        }
-                    }
-                    // a score passed the running maximum by more than the slack: raise it and take them again
-                    find = __any_sync(~0u, mx > kShift + kSlack);
-                    if (!find) {
-                        float x, y;
-                        unpair(sum2, x, y);
-                        l += x + y;
-                        break;
                     }
                 }
+                const float off = kShift - (m == -INFINITY ? 0.0f : m);
+                const uint64_t rs2 = pair(rs, rs), off2 = pair(off, off);
+                uint64_t sum2[2] = {0, 0};
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    st16(t_s + 16 * h, p + 16 * h);
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float x, y;
+                        unpair(fma2(pair(__uint_as_float(r[32 * h + e]), __uint_as_float(r[32 * h + e + 1])), rs2, off2),
+                               x, y);
+                        x = exp2_approx(x);
+                        y = exp2_approx(y);
+                        sum2[(e / 2) & 1] = add2(sum2[(e / 2) & 1], pair(x, y));
+                        p[e / 2] = pack_half2(x, y);
+                    }
+                    st16(t_s + 16 * h, p);
+                }
+                float x, y;
+                unpair(add2(sum2[0], sum2[1]), x, y);
+                l += x + y;
                 wait_st();
                 fence_before();
                 arrive(smem_addr(&sh.p_full[k]));
             }
+
+            // the next piece's Q, while the last MMAs of this one run
+            const Piece done = w;
+            next_piece(c, b, seq_at, &w, &at, &pos, hi, tt);
+            if (pos < hi && count(w) > 0)
+                rs = load_q(w);
+
+            // the row of O
             if (l == 0.0f)
                 m = -INFINITY; // nothing seen
-
-            // the tile's rows of O
             if (nk > 0) {
                 wait(sh.o_full[k], n_o);
                 ++n_o;
                 fence_after();
             }
-            const auto store = [&](int ch, const float (&x)[32], float M, float L) {
+            const int64_t token = done.s.first + token_of(done);
+            const int head = done.head * a.ratio + row_head;
+            const bool valid = valid_in(done);
+            const auto store = [&](int ch, const float *x, float M, float L) { // 16 channels
                 const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-                uint16_t *o = a.out + (w.s.first + token) * a.out_stride + (int64_t)head * D + ch;
+                uint16_t *o = a.out + token * a.out_stride + (int64_t)head * D + ch;
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
+                for (int e = 0; e < 16; e += 8) {
                     uint32_t y[4];
 #pragma unroll
                     for (int n = 0; n < 4; ++n)
@@ -721,53 +759,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     *(uint4 *)(o + e) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
                 if (a.lse && ch == 0)
-                    a.lse[(w.s.first + token) * a.n_q_heads + head] =
-                        L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * kLn2;
+                    a.lse[token * a.n_q_heads + head] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * kLn2;
             };
-            const bool whole = w.b0 == 0 && w.nblk == w.total;
+            const bool whole = done.nblk == done.total;
+            // a part: m, l of the rows, then O, four channels of the rows side by side. A CTA has at
+            // most one piece that goes on from another's (slot 0) and one that another goes on from.
+            const auto part_at = [&](int64_t cta, int slot) { return a.partials + ((cta * 2 + slot) * 2 + k) * C::kPart; };
+            const auto column = [&](int ch) { return 256 + (ch / 4) * 512 + row * 4; };
             float *part = nullptr;
             if (!whole) {
-                part = a.partials + (((int64_t)blockIdx.x * 2 + (pos == lo ? 0 : 1)) * 2 + k) * C::kPart;
+                part = part_at(blockIdx.x, done.b0 > 0 ? 0 : 1);
                 part[row] = m;
                 part[128 + row] = l;
             }
 #pragma unroll 1
-            for (int h = 0; h < D / 32; ++h) {
-                uint32_t r[32];
-                float x[32];
+            for (int h = 0; h < D / 16; ++h) {
+                uint32_t o[16];
+                float x[16];
                 if (nk > 0) {
-                    ld32(t_o + 32 * h, r);
+                    ld16(t_o + 16 * h, o);
                     wait_ld();
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    x[e] = nk > 0 ? __uint_as_float(r[e]) : 0.0f;
+                for (int e = 0; e < 16; ++e)
+                    x[e] = nk > 0 ? __uint_as_float(o[e]) : 0.0f;
                 if (whole) {
                     if (valid)
-                        store(32 * h, x, m, l);
+                        store(16 * h, x, m, l);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *(float4 *)(part + 256 + row * D + 32 * h + e) =
-                            make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                    for (int e = 0; e < 16; e += 4)
+                        *(float4 *)(part + column(16 * h + e)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
                 }
             }
+            fence_before(); // the next MMAs on O follow this thread's next arrival
             if (!whole) {
                 // the last CTA of the segment to arrive joins the parts of this tile, in CTA order
-                const int first = (int)(w.seg_lo / share), last = (int)((w.seg_lo + w.total - 1) / share);
+                const int first = (int)((done.seg_lo + kOver) / share);
+                const int last = (int)((done.seg_lo + kOver + done.total - 1) / share);
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
                 if (row == 0) {
-                    const uint32_t done = atom_add_acq_rel_gpu(a.counters + 2 * first + k, 1u);
-                    sh.last[k] = done == (uint32_t)(last - first);
+                    const uint32_t before = atom_add_acq_rel_gpu(a.counters + 2 * first + k, 1u);
+                    sh.last[k] = before == (uint32_t)(last - first);
                     if (sh.last[k])
                         a.counters[2 * first + k] = 0; // for the next launch
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
                 if (sh.last[k] && valid) {
-                    const auto of = [&](int z) {
-                        const int slot = z > first || w.seg_lo == (int64_t)first * share ? 0 : 1;
-                        return a.partials + (((int64_t)z * 2 + slot) * 2 + k) * C::kPart;
-                    };
+                    const auto of = [&](int z) { return part_at(z, z > first ? 0 : 1); };
                     float M = -INFINITY, L = 0.0f;
                     for (int z = first; z <= last; ++z)
                         M = fmaxf(M, ldcg_f32(of(z) + row));
@@ -776,31 +815,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                         L = fmaf(mz == M ? 1.0f : exp2_approx(mz - M), ldcg_f32(of(z) + 128 + row), L);
                     }
 #pragma unroll 1
-                    for (int h = 0; h < D / 32; ++h) {
-                        float x[32] = {};
+                    for (int h = 0; h < D / 16; ++h) {
+                        float x[16] = {};
                         for (int z = first; z <= last; ++z) {
                             const float mz = ldcg_f32(of(z) + row);
                             const float f = mz == M ? 1.0f : exp2_approx(mz - M);
-                            const float4 *o = (const float4 *)(of(z) + 256 + row * D + 32 * h);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 y = __ldcg(o + e);
-                                x[4 * e] = fmaf(f, y.x, x[4 * e]);
-                                x[4 * e + 1] = fmaf(f, y.y, x[4 * e + 1]);
-                                x[4 * e + 2] = fmaf(f, y.z, x[4 * e + 2]);
-                                x[4 * e + 3] = fmaf(f, y.w, x[4 * e + 3]);
+                            for (int e = 0; e < 16; e += 4) {
+                                const float4 y = __ldcg((const float4 *)(of(z) + column(16 * h + e)));
+                                x[e] = fmaf(f, y.x, x[e]);
+                                x[e + 1] = fmaf(f, y.y, x[e + 1]);
+                                x[e + 2] = fmaf(f, y.z, x[e + 2]);
+                                x[e + 3] = fmaf(f, y.w, x[e + 3]);
                             }
                         }
-                        store(32 * h, x, M, L);
+                        store(16 * h, x, M, L);
                     }
                 }
             }
-            fence_before(); // the next piece's MMAs overwrite O only after this thread's Q arrives
-            pos += w.nblk;
-            if (pos < hi)
-                next_segment(c, b, w, tt, &at);
         }
-    } else if (warp < 12) {
+    } else if (warp < kMmaWarp) {
+        setmaxnreg_dec<kUnpackRegs>();
         // ---- unpacking: 128 threads fill K and V^T of a block ----
         const int u = tid - kSoft;
         Piece w{};
@@ -809,22 +844,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         RawK<D> rk;
         RawV<D> rv;
         int len = 0, blk = 0; // of the block in rk and rv
+        // lane z < 8: the page of cell z of the block to fetch, and then its place in 128-byte
+        // units; ~0 for none. The page is asked for well before the place is needed.
+        int32_t page = -1;
         uint32_t place = ~0u;
-        // lane z < 8: the place of cell z of the block to fetch, in 128-byte units; ~0 for none
+        const int in_page = c.page_shift - 4;
+        const auto ask = [&]() {
+            const int cell = (w.b0 + i) * 8 + (lane & 7);
+            page = -2;
+            if (cell * kKv4Cell < w.s.len)
+                page = c.tables[(int64_t)w.s.row * c.max_pages + (cell >> in_page)];
+        };
         const auto find = [&]() {
             const int cell = (w.b0 + i) * 8 + (lane & 7);
             place = ~0u;
-            if (cell * kKv4Cell < w.s.len) {
-                const int page = kv4_page(c, w.s.row, cell >> (c.page_shift - 4));
-                if (page >= 0)
-                    place = (uint32_t)(kv4_cell_offset<D>(c, page, a.layer, w.head,
-                                                          cell & ((1 << (c.page_shift - 4)) - 1)) >> 7);
-                else if (u < 8)
-                    kv4_bad(c);
-            }
+            if (page >= 0 && page < c.n_pages)
+                place = (uint32_t)(kv4_cell_offset<D>(c, page, a.layer, w.head, cell & ((1 << in_page) - 1)) >> 7);
+            else if (page != -2 && u < 8)
+                kv4_bad(c);
         };
+        w = first_piece(c, b, seq_at, &at, &pos, hi, tt);
         if (pos < hi) {
-            w = piece_at(c, b, at, pos, hi, tt);
+            ask();
             find();
             load_k<D>(rk, c.pool, place, u);
             load_v<D>(rv, c.pool, place, u);
@@ -834,24 +875,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             blk = w.b0 + i;
             // the next block
             if (++i == w.nblk) {
-                pos += w.nblk;
                 i = 0;
-                if (pos < hi) {
-                    next_segment(c, b, w, tt, &at);
-                    w = piece_at(c, b, at, pos, hi, tt);
-                }
+                next_piece(c, b, seq_at, &w, &at, &pos, hi, tt);
             }
             const bool more = pos < hi;
             if (more)
-                find();
+                ask();
             const int st = n & 1;
             if (n >= 2)
                 wait(sh.k_empty[st], (n >> 1) - 1);
             unpack_k<D>(rk, tiles + C::kOffK + st * C::kQ, u);
             fence_proxy_async_smem();
             arrive(smem_addr(&sh.k_full[st]));
-            if (more)
+            if (more) {
+                find();
                 load_k<D>(rk, c.pool, place, u);
+            }
             if (n >= 2)
                 wait(sh.v_empty[st], (n >> 1) - 1);
             unpack_v<D>(rv, tiles + C::kOffV + st * C::kV, u, len - blk * kBlock);
@@ -860,12 +899,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             if (more)
                 load_v<D>(rv, c.pool, place, u);
         }
+    } else if (warp > kMmaWarp) {
+        setmaxnreg_dec<kMmaRegs>();
     } else {
+        setmaxnreg_dec<kMmaRegs>();
         // ---- the MMAs: every lane follows, lane 0 issues ----
         const uint32_t one = lane == 0;
         const uint32_t tmem = __reduce_max_sync(~0u, sh.tmem); // uniform
 
-        uint32_t n = 0, n_p0 = 0, n_p1 = 0, piece = 0;
+        uint32_t n = 0, n_p0 = 0, n_p1 = 0, n_q0 = 0, n_q1 = 0;
         const uint32_t desc0 = kDescLo | (tiles >> 4);
         const auto scores = [&](int k, uint32_t blk) { // S of tile k
             const uint32_t q = desc0 + k * (C::kQ >> 4), kk = desc0 + (C::kOffK >> 4) + (blk & 1) * (C::kQ >> 4);
@@ -885,21 +927,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    mma_ts(d, p + 8 * (4 * h + x), v + ((h * (D * 128) + 32 * x) >> 4), kIdesc<D>,
+                    mma_ts(d, p + 32 * h + 8 * x, v + ((h * (D * 128) + 32 * x) >> 4), kIdesc<D>,
                            h + x > 0 ? 1u : accumulate, one);
         };
-        for (int64_t pos = lo; __any_sync(~0u, pos < hi); ++piece) {
-            const Piece w = piece_at(c, b, at, pos, hi, tt);
+        int64_t pos = lo;
+        Piece w = first_piece(c, b, seq_at, &at, &pos, hi, tt);
+        while (__any_sync(~0u, pos < hi)) {
             const int n0 = __reduce_max_sync(~0u, w.n0), n1 = __reduce_max_sync(~0u, w.n1);
             const int nblk = __reduce_max_sync(~0u, w.nblk);
-            wait(sh.q_full[0], piece);
-            wait(sh.q_full[1], piece);
             wait(sh.k_full[n & 1], n >> 1);
-            fence_after();
-            if (n0 > 0)
+            if (n0 > 0) {
+                wait(sh.q_full[0], n_q0++);
+                fence_after();
                 scores(0, n);
-            if (n1 > 0)
+            }
+            if (n1 > 0) {
+                wait(sh.q_full[1], n_q1++);
+                fence_after();
                 scores(1, n);
+            }
             commit(smem_addr(&sh.k_empty[n & 1]), one);
             for (int i = 0; i < nblk; ++i, ++n) {
                 const bool more = i + 1 < nblk;
@@ -931,9 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     commit(smem_addr(&sh.k_empty[(n + 1) & 1]), one);
                 }
             }
-            pos += w.nblk;
-            if (pos < hi)
-                next_segment(c, b, w, tt, &at);
+            next_piece(c, b, seq_at, &w, &at, &pos, hi, tt);
         }
         // before leaving, the MMAs in flight end (bounded): the last stages are released
         if (n > 0) {
@@ -943,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
     }
     fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         __syncwarp();
         tmem_dealloc(tmem, 512);
     }
@@ -951,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
 
 template <int D> nm_status launch(const Kv4 &c, const Kv4Batch &b, const PromptArgs &a, int grid, cudaStream_t st)
 {
-    constexpr size_t kMax = Cfg<D>::kTiles + 1024 + (kKv4MaxSeqs + 1) * 8;
+    constexpr size_t kMax = Cfg<D>::kTiles + 1024 + kSeqCache * sizeof(Kv4Seq);
     static_assert(kMax + sizeof(Shared) <= 227 * 1024, "shared memory");
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
@@ -960,7 +1004,8 @@ template <int D> nm_status launch(const Kv4 &c, const Kv4Batch &b, const PromptA
     });
     if (attr != cudaSuccess)
         return NM_ERR_CUDA;
-    const size_t smem = Cfg<D>::kTiles + 1024 + (size_t)(b.n_seqs + 1) * 8;
+    const size_t smem =
+        Cfg<D>::kTiles + 1024 + (size_t)(b.n_seqs < kSeqCache ? b.n_seqs : kSeqCache) * sizeof(Kv4Seq);
     attn_prompt_kernel<D><<<grid, kThreads, smem, st>>>(c, b, a);
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
