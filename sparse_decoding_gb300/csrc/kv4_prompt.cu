@@ -340,14 +340,27 @@ template <int D> __device__ __forceinline__ void unpack_v(const RawV<D> &r, uint
     }
 }
 
-// mbar_wait_bounded for waits that are short and many: the clock is read only
-// once a wait has been polled for a while.
+// A bounded wait (about a second, then NM_ERR_TIMEOUT; `dead` threads poll once). The
+// clock is read only after some polls: reading it takes longer than most waits.
 __device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, uint32_t *status, bool &dead)
 {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity))
+    uint64_t t0 = 0;
+    uint32_t polls = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (dead)
             return;
-    mbar_wait_bounded(bar, parity, status, dead);
+        if (++polls < 64)
+            continue;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0)
+            t0 = t;
+        if (t - t0 > kWaitLimitNs) {
+            atomicOr(status, 1u << NM_ERR_TIMEOUT);
+            dead = true;
+            return;
+        }
+    }
 }
 
 struct PromptArgs {
@@ -364,114 +377,47 @@ struct PromptArgs {
 
 // Tokens that tile `tile` of a sequence sees at most (its last row's), 0 for a
 // tile without tokens; tt: tokens of a tile.
-__device__ __forceinline__ int tile_limit(const Kv4Seq &s, int64_t tile, int tt)
+__device__ __forceinline__ int tile_limit(const Kv4Seq &s, int tile, int tt)
 {
     if (tile * tt >= s.n_new)
         return 0;
-    const int64_t last = (tile + 1) * tt < s.n_new ? (tile + 1) * tt : s.n_new;
-    const int64_t n = s.len - s.n_new + last;
-    return n > 0 ? (int)n : 0;
+    const int last = (tile + 1) * tt < s.n_new ? (tile + 1) * tt : s.n_new;
+    const int n = s.len - s.n_new + last;
+    return n > 0 ? n : 0;
 }
 __device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlock - 1) / kBlock; }
 // Blocks of a pair of tiles (one at least, so that rows that see nothing are answered).
-__device__ __forceinline__ int pair_blocks(const Kv4Seq &s, int64_t pair, int tt)
+__device__ __forceinline__ int pair_blocks(const Kv4Seq &s, int pair, int tt)
 {
-    const int a = blocks_of(tile_limit(s, 2 * pair, tt)), b = blocks_of(tile_limit(s, 2 * pair + 1, tt));
-    const int n = a > b ? a : b;
+    const int a = tile_limit(s, 2 * pair, tt), b = tile_limit(s, 2 * pair + 1, tt);
+    const int n = blocks_of(a > b ? a : b);
     return n > 0 ? n : 1;
 }
-__device__ __forceinline__ int64_t pairs_of(const Kv4Seq &s, int tt)
-{
-    return ((int64_t)s.n_new + 2 * tt - 1) / (2 * tt);
-}
+__device__ __forceinline__ int pairs_of(const Kv4Seq &s, int tt) { return (s.n_new + 2 * tt - 1) / (2 * tt); }
 
 // A segment takes its blocks and kOver more on the line: what starting and ending a
-// piece costs. A place before the first block of a segment is in those.
+// piece costs. A step before the first block of a segment is in those.
 constexpr int kOver = 3;
-struct Place {
-    int seq, head, pair, step;
-};
 
-// What the roles of a CTA agree on about one piece of work.
+// One piece of a CTA's work: blocks [b0, b0 + nblk) of the total of a (sequence, kv
+// head, pair); nblk = 0 ends the work.
 struct Piece {
-    Kv4Seq s;
-    int seq, head, pair, b0, nblk, total; // blocks [b0, b0 + nblk) of the pair's total
-    int steps;                            // of the line
-    int n0, n1;                           // of those, how many each tile takes
-    int64_t seg_lo;                       // the segment's first place on the line
+    int row, len, n_new, first; // the sequence (Kv4Seq)
+    int head, pair, b0, nblk, total;
+    int n0, n1;                 // blocks that each tile takes
+    int cta0, cta1;             // the CTAs that share the segment
 };
-
-__device__ __forceinline__ Piece piece_at(const Kv4Seq &s, const Place &p, int64_t pos, int64_t hi, int tt)
-{
-    Piece w;
-    w.s = s;
-    w.seq = p.seq;
-    w.head = p.head;
-    w.pair = p.pair;
-    w.total = pair_blocks(w.s, p.pair, tt);
-    w.seg_lo = pos - p.step;
-    const int64_t left = hi - pos;
-    w.steps = w.total + kOver - p.step < left ? w.total + kOver - p.step : (int)left;
-    w.b0 = p.step > kOver ? p.step - kOver : 0;
-    const int b1 = p.step + w.steps - kOver;
-    w.nblk = b1 > w.b0 ? b1 - w.b0 : 0;
-    const int n0 = blocks_of(tile_limit(w.s, 2 * (int64_t)p.pair, tt)) - w.b0;
-    const int n1 = blocks_of(tile_limit(w.s, 2 * (int64_t)p.pair + 1, tt)) - w.b0;
-    w.n0 = n0 < 0 ? 0 : n0 > w.nblk ? w.nblk : n0;
-    w.n1 = n1 < 0 ? 0 : n1 > w.nblk ? w.nblk : n1;
-    return w;
-}
-
-// The place after a piece that ends its segment.
-template <typename SeqAt>
-__device__ __forceinline__ void next_segment(const Kv4 &c, const Kv4Batch &b, const Piece &w, int tt, const SeqAt &seq_at,
-                                             Place *p)
-{
-    p->step = 0;
-    if (++p->pair < pairs_of(w.s, tt))
-        return;
-    p->pair = 0;
-    if (++p->head < c.n_kv_heads)
-        return;
-    p->head = 0;
-    do
-        ++p->seq;
-    while (p->seq < b.n_seqs && seq_at(p->seq).n_new == 0);
-}
-
-// The next piece with blocks, *pos past the end (hi) when there is none.
-template <typename SeqAt>
-__device__ __forceinline__ void next_piece(const Kv4 &c, const Kv4Batch &b, const SeqAt &seq_at, Piece *w, Place *at,
-                                           int64_t *pos, int64_t hi, int tt)
-{
-    *pos += w->steps;
-    if (*pos >= hi)
-        return;
-    next_segment(c, b, *w, tt, seq_at, at);
-    *w = piece_at(seq_at(at->seq), *at, *pos, hi, tt);
-    if (w->nblk == 0) // the line's end is before the segment's first block
-        *pos = hi;
-}
-template <typename SeqAt>
-__device__ __forceinline__ Piece first_piece(const Kv4 &c, const Kv4Batch &b, const SeqAt &seq_at, Place *at,
-                                             int64_t *pos, int64_t hi, int tt)
-{
-    Piece w{};
-    if (*pos < hi) {
-        w = piece_at(seq_at(at->seq), *at, *pos, hi, tt);
-        if (w.nblk == 0)
-            *pos = hi;
-    }
-    return w;
-}
+constexpr int kRing = 4;        // pieces known ahead
 
 struct Shared {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem;
     uint32_t last[2];
+    uint64_t piece_full[kRing], piece_empty[kRing];
+    Piece piece[kRing];
     int64_t total, share;
-    Place start;
+    int seq, head, pair, step; // where the CTA's part of the line starts
 };
 
 template <int D>
@@ -500,6 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             mbar_init(smem_addr(&sh.s_full[i]), 1);
             mbar_init(smem_addr(&sh.o_full[i]), 1);
         }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(smem_addr(&sh.piece_full[i]), 1);
+            mbar_init(smem_addr(&sh.piece_empty[i]), 13); // a lane of each of warps 0 .. 12
+        }
         fence_mbar_init();
     }
     if (warp == kMmaWarp)
@@ -511,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         if (lane == 0 && b.n_seqs <= kSeqCache)
             seqs[i] = s;
         int64_t n = 0;
-        for (int64_t j = lane; j < pairs_of(s, tt); j += 32)
+        for (int j = lane; j < pairs_of(s, tt); j += 32)
             n += pair_blocks(s, j, tt) + kOver;
         for (int o = 16; o; o >>= 1)
             n += __shfl_xor_sync(~0u, n, o);
@@ -541,36 +491,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         int64_t share = (total + gridDim.x - 1) / gridDim.x;
         share = share < kMinShare + kOver ? kMinShare + kOver : share;
         const int64_t pos = (int64_t)blockIdx.x * share;
-        Place p{};
+        int seq = 0, head = 0, pair = 0, step = 0;
         if (pos < total) {
-            int l = 0, h = b.n_seqs;
-            while (h - l > 1) {
-                const int m = (l + h) >> 1;
+            int h = b.n_seqs;
+            while (h - seq > 1) {
+                const int m = (seq + h) >> 1;
                 if (pre[m] <= pos)
-                    l = m;
+                    seq = m;
                 else
                     h = m;
             }
-            p.seq = l;
-            const Kv4Seq s = seq_at(l);
-            const int64_t per = (pre[l + 1] - pre[l]) / c.n_kv_heads;
-            p.head = (int)((pos - pre[l]) / per);
-            int64_t left = (pos - pre[l]) % per;
-            // the pair that holds block `left` of the head's line
-            for (int64_t j0 = 0;; j0 += 32) {
-                const int64_t j = j0 + lane;
-                const int n = j < pairs_of(s, tt) ? pair_blocks(s, j, tt) + kOver : 0;
-                int64_t x = n;
+            const Kv4Seq s = seq_at(seq);
+            const int64_t per = (pre[seq + 1] - pre[seq]) / c.n_kv_heads;
+            head = (int)((pos - pre[seq]) / per);
+            int64_t left = (pos - pre[seq]) % per;
+            // the pair that holds step `left` of the head's line
+            const int pairs = pairs_of(s, tt);
+#pragma unroll 1
+            for (int j0 = 0;; j0 += 32) {
+                const int n = j0 + lane < pairs ? pair_blocks(s, j0 + lane, tt) + kOver : 0;
+                int x = n; // 32 pairs of fewer than 2^24 blocks
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(~0u, x, o);
+                    const int y = __shfl_up_sync(~0u, x, o);
                     if (lane >= o)
                         x += y;
                 }
-                const uint32_t in = __ballot_sync(~0u, left < x && left >= x - n);
-                if (in || j0 + 32 >= pairs_of(s, tt)) {
+                const uint32_t in = __ballot_sync(~0u, left < x);
+                if (in || j0 + 32 >= pairs) {
                     const int who = in ? __ffs(in) - 1 : 0;
-                    p.pair = (int)(j0 + who);
-                    p.step = (int)(left - (__shfl_sync(~0u, x, who) - __shfl_sync(~0u, n, who)));
+                    pair = j0 + who;
+                    step = (int)(left - (__shfl_sync(~0u, x, who) - __shfl_sync(~0u, n, who)));
                     break;
                 }
                 left -= __shfl_sync(~0u, x, 31);
@@ -579,16 +529,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         if (lane == 0) {
             sh.total = total;
             sh.share = share;
-            sh.start = p;
+            sh.seq = seq;
+            sh.head = head;
+            sh.pair = pair;
+            sh.step = step;
         }
     }
     __syncthreads();
     const uint32_t tmem = sh.tmem;
-    const int64_t share = sh.share;
-    const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share < sh.total ? lo + share : sh.total;
     bool dead = false;
-    const auto wait = [&](uint64_t &bar, uint32_t parity) { wait_bounded(smem_addr(&bar), parity & 1u, c.status, dead); };
-    Place at = sh.start;
+    const auto wait = [&](uint64_t &bar, uint32_t parity) {
+        wait_bounded(smem_addr(&bar), parity & 1u, c.status, dead);
+    };
+    // Piece number p of the CTA, for a whole warp.
+    const auto get_piece = [&](uint32_t p) {
+        wait(sh.piece_full[p % kRing], p / kRing);
+        const Piece w = sh.piece[p % kRing];
+        __syncwarp();
+        if (lane == 0)
+            arrive(smem_addr(&sh.piece_empty[p % kRing]));
+        return w;
+    };
 
     if (warp < 8) {
         // ---- softmax: a row per thread ----
@@ -600,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + k * 128, t_o = tmem + lanes + 256 + k * 128;
         const auto count = [&](const Piece &w) { return k ? w.n1 : w.n0; };
-        const auto token_of = [&](const Piece &w) { return (2 * (int64_t)w.pair + k) * tt + row_token; };
-        const auto valid_in = [&](const Piece &w) { return row < tt * a.ratio && token_of(w) < w.s.n_new; };
+        const auto token_of = [&](const Piece &w) { return (2 * w.pair + k) * tt + row_token; };
+        const auto valid_in = [&](const Piece &w) { return row < tt * a.ratio && token_of(w) < w.n_new; };
         uint32_t n_s = 0, n_o = 0; // blocks and pieces of this tile so far
 
         // The row of Q: scaled by a power of two, channels in the order of the unpacked
@@ -609,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         const auto load_q = [&](const Piece &w) {
             constexpr int N = D / 8; // 16-byte pieces of a row
             const bool valid = valid_in(w);
-            const uint16_t *q = a.q + (w.s.first + token_of(w)) * a.q_stride + ((int64_t)w.head * a.ratio + row_head) * D;
+            const uint16_t *q = a.q + (int64_t)(w.first + token_of(w)) * a.q_stride + ((int64_t)w.head * a.ratio + row_head) * D;
             uint4 x[N];
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -655,16 +616,132 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             return fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f); // above 0, so that masked scores stay -inf
         };
 
-        float rs = 1.0f;
-        int64_t pos = lo;
-        Piece w = first_piece(c, b, seq_at, &at, &pos, hi, tt);
-        if (pos < hi && count(w) > 0)
-            rs = load_q(w);
-        while (pos < hi) {
+        // The rows of O of a piece.
+        const auto finish = [&](const Piece &done, float m, float l) {
+            const int nk = count(done);
+            if (l == 0.0f)
+                m = -INFINITY; // nothing seen
+            if (nk > 0) {
+                wait(sh.o_full[k], n_o);
+                ++n_o;
+                fence_after();
+            }
+            const int64_t token = done.first + token_of(done);
+            const int head = done.head * a.ratio + row_head;
+            const bool valid = valid_in(done);
+            const bool whole = done.nblk == done.total;
+            // a part: m, l of the rows, then O, four channels of the rows side by side. A CTA has at
+            // most one piece that goes on from another's (slot 0) and one that another goes on from.
+            const auto part_at = [&](int cta, int slot) {
+                return a.partials + (((int64_t)cta * 2 + slot) * 2 + k) * C::kPart;
+            };
+            const auto column = [&](int ch) { return 256 + (ch / 4) * 512 + row * 4; };
+            if (!whole) {
+                float *part = part_at(blockIdx.x, done.b0 > 0 ? 0 : 1);
+                part[row] = m;
+                part[128 + row] = l;
+#pragma unroll 1
+                for (int h = 0; h < D / 16; ++h) {
+                    uint32_t o[16] = {};
+                    if (nk > 0) {
+                        ld16(t_o + 16 * h, o);
+                        wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *(uint4 *)(part + column(16 * h + e)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+                // the last CTA of the segment to arrive joins the parts of this tile, in CTA order
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
+                if (row == 0) {
+                    const uint32_t before = atom_add_acq_rel_gpu(a.counters + 2 * done.cta0 + k, 1u);
+                    sh.last[k] = before == (uint32_t)(done.cta1 - done.cta0);
+                    if (sh.last[k])
+                        a.counters[2 * done.cta0 + k] = 0; // for the next launch
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
+                if (!sh.last[k]) {
+                    fence_before(); // the next MMAs on O follow this thread's next arrival
+                    return;
+                }
+            }
+            const int z0 = done.cta0, z1 = done.cta1;
+            const auto of = [&](int z) { return part_at(z, z > z0 ? 0 : 1); };
+            float M = m, L = l;
+            if (!whole) {
+                M = -INFINITY;
+                L = 0.0f;
+                for (int z = z0; z <= z1; ++z)
+                    M = fmaxf(M, ldcg_f32(of(z) + row));
+                for (int z = z0; z <= z1; ++z) {
+                    const float mz = ldcg_f32(of(z) + row);
+                    L = fmaf(mz == M ? 1.0f : exp2_approx(mz - M), ldcg_f32(of(z) + 128 + row), L);
+                }
+            }
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            uint16_t *out = a.out + token * a.out_stride + (int64_t)head * D;
+            if (a.lse && valid)
+                a.lse[token * a.n_q_heads + head] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * kLn2;
+#pragma unroll 1
+            for (int h = 0; h < D / 16; ++h) {
+                float x[16] = {};
+                if (whole) {
+                    uint32_t o[16] = {};
+                    if (nk > 0) {
+                        ld16(t_o + 16 * h, o);
+                        wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        x[e] = __uint_as_float(o[e]);
+                } else {
+#pragma unroll 1
+                    for (int z = z0; z <= z1; ++z) {
+                        const float mz = ldcg_f32(of(z) + row);
+                        const float f = mz == M ? 1.0f : exp2_approx(mz - M);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 y = __ldcg((const float4 *)(of(z) + column(16 * h + e)));
+                            x[e] = fmaf(f, y.x, x[e]);
+                            x[e + 1] = fmaf(f, y.y, x[e + 1]);
+                            x[e + 2] = fmaf(f, y.z, x[e + 2]);
+                            x[e + 3] = fmaf(f, y.w, x[e + 3]);
+                        }
+                    }
+                }
+                if (valid) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            y[n] = f32_to_bf16_rn(x[e + 2 * n] * inv) |
+                                   ((uint32_t)f32_to_bf16_rn(x[e + 2 * n + 1] * inv) << 16);
+                        *(uint4 *)(out + 16 * h + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+            fence_before();
+        };
+
+        // Q of a piece is loaded while the last MMAs of the one before run
+        float rs = 1.0f, m = 0.0f, l = 0.0f;
+        Piece done{};
+#pragma unroll 1
+        for (uint32_t piece = 0;; ++piece) {
+            const Piece w = get_piece(piece);
+            if (count(w) > 0)
+                rs = load_q(w);
+            if (piece > 0)
+                finish(done, m, l);
+            if (w.nblk == 0)
+                break;
             const int nk = count(w);
-            const int limit = valid_in(w) ? w.s.len - w.s.n_new + (int)token_of(w) + 1 : 0;
+            const int limit = valid_in(w) ? w.len - w.n_new + token_of(w) + 1 : 0;
             // rows that see nothing of the piece need no maximum
-            float m = limit > w.b0 * kBlock ? -INFINITY : 0.0f, l = 0.0f;
+            m = limit > w.b0 * kBlock ? -INFINITY : 0.0f;
+            l = 0.0f;
+#pragma unroll 1
             for (int i = 0; i < nk; ++i, ++n_s) {
                 wait(sh.s_full[k], n_s);
                 fence_after();
@@ -729,175 +806,114 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 arrive(smem_addr(&sh.p_full[k]));
             }
 
-            // the next piece's Q, while the last MMAs of this one run
-            const Piece done = w;
-            next_piece(c, b, seq_at, &w, &at, &pos, hi, tt);
-            if (pos < hi && count(w) > 0)
-                rs = load_q(w);
-
-            // the row of O
-            if (l == 0.0f)
-                m = -INFINITY; // nothing seen
-            if (nk > 0) {
-                wait(sh.o_full[k], n_o);
-                ++n_o;
-                fence_after();
-            }
-            const int64_t token = done.s.first + token_of(done);
-            const int head = done.head * a.ratio + row_head;
-            const bool valid = valid_in(done);
-            const auto store = [&](int ch, const float *x, float M, float L) { // 16 channels
-                const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-                uint16_t *o = a.out + token * a.out_stride + (int64_t)head * D + ch;
-#pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                    uint32_t y[4];
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        y[n] = f32_to_bf16_rn(x[e + 2 * n] * inv) |
-                               ((uint32_t)f32_to_bf16_rn(x[e + 2 * n + 1] * inv) << 16);
-                    *(uint4 *)(o + e) = make_uint4(y[0], y[1], y[2], y[3]);
-                }
-                if (a.lse && ch == 0)
-                    a.lse[token * a.n_q_heads + head] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * kLn2;
-            };
-            const bool whole = done.nblk == done.total;
-            // a part: m, l of the rows, then O, four channels of the rows side by side. A CTA has at
-            // most one piece that goes on from another's (slot 0) and one that another goes on from.
-            const auto part_at = [&](int64_t cta, int slot) { return a.partials + ((cta * 2 + slot) * 2 + k) * C::kPart; };
-            const auto column = [&](int ch) { return 256 + (ch / 4) * 512 + row * 4; };
-            float *part = nullptr;
-            if (!whole) {
-                part = part_at(blockIdx.x, done.b0 > 0 ? 0 : 1);
-                part[row] = m;
-                part[128 + row] = l;
-            }
-#pragma unroll 1
-            for (int h = 0; h < D / 16; ++h) {
-                uint32_t o[16];
-                float x[16];
-                if (nk > 0) {
-                    ld16(t_o + 16 * h, o);
-                    wait_ld();
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    x[e] = nk > 0 ? __uint_as_float(o[e]) : 0.0f;
-                if (whole) {
-                    if (valid)
-                        store(16 * h, x, m, l);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        *(float4 *)(part + column(16 * h + e)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-                }
-            }
-            fence_before(); // the next MMAs on O follow this thread's next arrival
-            if (!whole) {
-                // the last CTA of the segment to arrive joins the parts of this tile, in CTA order
-                const int first = (int)((done.seg_lo + kOver) / share);
-                const int last = (int)((done.seg_lo + kOver + done.total - 1) / share);
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
-                if (row == 0) {
-                    const uint32_t before = atom_add_acq_rel_gpu(a.counters + 2 * first + k, 1u);
-                    sh.last[k] = before == (uint32_t)(last - first);
-                    if (sh.last[k])
-                        a.counters[2 * first + k] = 0; // for the next launch
-                }
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
-                if (sh.last[k] && valid) {
-                    const auto of = [&](int z) { return part_at(z, z > first ? 0 : 1); };
-                    float M = -INFINITY, L = 0.0f;
-                    for (int z = first; z <= last; ++z)
-                        M = fmaxf(M, ldcg_f32(of(z) + row));
-                    for (int z = first; z <= last; ++z) {
-                        const float mz = ldcg_f32(of(z) + row);
-                        L = fmaf(mz == M ? 1.0f : exp2_approx(mz - M), ldcg_f32(of(z) + 128 + row), L);
-                    }
-#pragma unroll 1
-                    for (int h = 0; h < D / 16; ++h) {
-                        float x[16] = {};
-                        for (int z = first; z <= last; ++z) {
-                            const float mz = ldcg_f32(of(z) + row);
-                            const float f = mz == M ? 1.0f : exp2_approx(mz - M);
-#pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                const float4 y = __ldcg((const float4 *)(of(z) + column(16 * h + e)));
-                                x[e] = fmaf(f, y.x, x[e]);
-                                x[e + 1] = fmaf(f, y.y, x[e + 1]);
-                                x[e + 2] = fmaf(f, y.z, x[e + 2]);
-                                x[e + 3] = fmaf(f, y.w, x[e + 3]);
-                            }
-                        }
-                        store(16 * h, x, M, L);
-                    }
-                }
-            }
+            done = w;
         }
     } else if (warp < kMmaWarp) {
         setmaxnreg_dec<kUnpackRegs>();
         // ---- unpacking: 128 threads fill K and V^T of a block ----
         const int u = tid - kSoft;
-        Piece w{};
-        int64_t pos = lo;
-        int i = 0; // the block being fetched: block b0 + i of the piece
+        const int in_page = c.page_shift - 4;
         RawK<D> rk;
         RawV<D> rv;
-        int len = 0, blk = 0; // of the block in rk and rv
-        // lane z < 8: the page of cell z of the block to fetch, and then its place in 128-byte
-        // units; ~0 for none. The page is asked for well before the place is needed.
-        int32_t page = -1;
-        uint32_t place = ~0u;
-        const int in_page = c.page_shift - 4;
-        const auto ask = [&]() {
+        uint32_t piece = 0;
+        Piece w = get_piece(piece);
+        int i = 0;        // the block to fetch: b0 + i of piece w
+        int left = 0;     // tokens of the fetched block's sequence from its first on
+        uint32_t n = ~0u; // the number of the fetched block; none yet
+        bool more = w.nblk > 0;
+#pragma unroll 1
+        for (;;) {
+            // Block n (fetched before) is unpacked, and the next one fetched, K and V in turn:
+            // each one's registers are free as soon as it is in shared memory. Lane z < 8 asks
+            // for the page of cell z first, and finds its place (in 128-byte units, ~0: none).
             const int cell = (w.b0 + i) * 8 + (lane & 7);
-            page = -2;
-            if (cell * kKv4Cell < w.s.len)
-                page = c.tables[(int64_t)w.s.row * c.max_pages + (cell >> in_page)];
-        };
-        const auto find = [&]() {
-            const int cell = (w.b0 + i) * 8 + (lane & 7);
-            place = ~0u;
-            if (page >= 0 && page < c.n_pages)
-                place = (uint32_t)(kv4_cell_offset<D>(c, page, a.layer, w.head, cell & ((1 << in_page) - 1)) >> 7);
-            else if (page != -2 && u < 8)
-                kv4_bad(c);
-        };
-        w = first_piece(c, b, seq_at, &at, &pos, hi, tt);
-        if (pos < hi) {
-            ask();
-            find();
-            load_k<D>(rk, c.pool, place, u);
-            load_v<D>(rv, c.pool, place, u);
-        }
-        for (uint32_t n = 0; pos < hi; ++n) {
-            len = w.s.len;
-            blk = w.b0 + i;
-            // the next block
-            if (++i == w.nblk) {
-                i = 0;
-                next_piece(c, b, seq_at, &w, &at, &pos, hi, tt);
-            }
-            const bool more = pos < hi;
-            if (more)
-                ask();
+            const bool inside = more && cell * kKv4Cell < w.len;
+            const int32_t page = inside ? c.tables[(int64_t)w.row * c.max_pages + (cell >> in_page)] : -1;
             const int st = n & 1;
-            if (n >= 2)
-                wait(sh.k_empty[st], (n >> 1) - 1);
-            unpack_k<D>(rk, tiles + C::kOffK + st * C::kQ, u);
-            fence_proxy_async_smem();
-            arrive(smem_addr(&sh.k_full[st]));
+            if (n != ~0u) {
+                if (n >= 2)
+                    wait(sh.k_empty[st], (n >> 1) - 1);
+                unpack_k<D>(rk, tiles + C::kOffK + st * C::kQ, u);
+                fence_proxy_async_smem();
+                arrive(smem_addr(&sh.k_full[st]));
+            }
+            uint32_t place = ~0u;
             if (more) {
-                find();
+                if (page >= 0 && page < c.n_pages)
+                    place = (uint32_t)(kv4_cell_offset<D>(c, page, a.layer, w.head, cell & ((1 << in_page) - 1)) >> 7);
+                else if (inside && u < 8)
+                    kv4_bad(c);
                 load_k<D>(rk, c.pool, place, u);
             }
-            if (n >= 2)
-                wait(sh.v_empty[st], (n >> 1) - 1);
-            unpack_v<D>(rv, tiles + C::kOffV + st * C::kV, u, len - blk * kBlock);
-            fence_proxy_async_smem();
-            arrive(smem_addr(&sh.v_full[st]));
-            if (more)
-                load_v<D>(rv, c.pool, place, u);
+            if (n != ~0u) {
+                if (n >= 2)
+                    wait(sh.v_empty[st], (n >> 1) - 1);
+                unpack_v<D>(rv, tiles + C::kOffV + st * C::kV, u, left);
+                fence_proxy_async_smem();
+                arrive(smem_addr(&sh.v_full[st]));
+            }
+            if (!more)
+                break;
+            load_v<D>(rv, c.pool, place, u);
+            left = w.len - (w.b0 + i) * kBlock;
+            ++n;
+            if (++i == w.nblk) {
+                i = 0;
+                w = get_piece(++piece);
+                more = w.nblk > 0;
+            }
+        }
+    } else if (warp == kMmaWarp + 1) {
+        setmaxnreg_dec<kMmaRegs>();
+        // ---- the pieces, one lane ----
+        if (lane == 0) {
+            const int64_t share = sh.share;
+            int64_t pos = (int64_t)blockIdx.x * share;
+            const int64_t hi = pos + share < sh.total ? pos + share : sh.total;
+            int seq = sh.seq, head = sh.head, pair = sh.pair, step = sh.step;
+            Kv4Seq s = pos < hi ? seq_at(seq) : Kv4Seq{};
+#pragma unroll 1
+            for (uint32_t p = 0;; ++p) {
+                Piece w{};
+                if (pos < hi) {
+                    w.row = s.row;
+                    w.len = s.len;
+                    w.n_new = s.n_new;
+                    w.first = s.first;
+                    w.head = head;
+                    w.pair = pair;
+                    w.total = pair_blocks(s, pair, tt);
+                    const int64_t seg = pos - step + kOver; // the place of the segment's first block
+                    const int all = w.total + kOver - step;
+                    const int steps = hi - pos < all ? (int)(hi - pos) : all;
+                    w.b0 = step > kOver ? step - kOver : 0;
+                    const int b1 = step + steps - kOver;
+                    w.nblk = b1 > w.b0 ? b1 - w.b0 : 0; // 0: the CTA's part ends before the first block
+                    const int n0 = blocks_of(tile_limit(s, 2 * pair, tt)) - w.b0;
+                    const int n1 = blocks_of(tile_limit(s, 2 * pair + 1, tt)) - w.b0;
+                    w.n0 = n0 < 0 ? 0 : n0 > w.nblk ? w.nblk : n0;
+                    w.n1 = n1 < 0 ? 0 : n1 > w.nblk ? w.nblk : n1;
+                    w.cta0 = (int)(seg / share);
+                    w.cta1 = (int)((seg + w.total - 1) / share);
+                    pos += steps;
+                    step = 0;
+                    if (pos < hi && ++pair == pairs_of(s, tt)) {
+                        pair = 0;
+                        if (++head == c.n_kv_heads) {
+                            head = 0;
+                            do
+                                s = seq_at(++seq);
+                            while (s.n_new == 0); // pos < hi: there is one
+                        }
+                    }
+                }
+                if (p >= kRing)
+                    wait(sh.piece_empty[p % kRing], p / kRing - 1);
+                sh.piece[p % kRing] = w;
+                arrive(smem_addr(&sh.piece_full[p % kRing]));
+                if (w.nblk == 0)
+                    break;
+            }
         }
     } else if (warp > kMmaWarp) {
         setmaxnreg_dec<kMmaRegs>();
@@ -930,54 +946,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     mma_ts(d, p + 32 * h + 8 * x, v + ((h * (D * 128) + 32 * x) >> 4), kIdesc<D>,
                            h + x > 0 ? 1u : accumulate, one);
         };
-        int64_t pos = lo;
-        Piece w = first_piece(c, b, seq_at, &at, &pos, hi, tt);
-        while (__any_sync(~0u, pos < hi)) {
+        uint32_t piece = 0;
+#pragma unroll 1
+        for (;;) {
+            const Piece w = get_piece(piece++);
+            const int nblk = __reduce_max_sync(~0u, w.nblk); // uniform, as the lanes agree
             const int n0 = __reduce_max_sync(~0u, w.n0), n1 = __reduce_max_sync(~0u, w.n1);
-            const int nblk = __reduce_max_sync(~0u, w.nblk);
-            wait(sh.k_full[n & 1], n >> 1);
-            if (n0 > 0) {
-                wait(sh.q_full[0], n_q0++);
-                fence_after();
-                scores(0, n);
-            }
-            if (n1 > 0) {
-                wait(sh.q_full[1], n_q1++);
-                fence_after();
-                scores(1, n);
-            }
-            commit(smem_addr(&sh.k_empty[n & 1]), one);
-            for (int i = 0; i < nblk; ++i, ++n) {
+            if (nblk == 0)
+                break;
+            // per step: O of block i, then S of block i + 1, tile by tile
+#pragma unroll 1
+            for (int i = -1; i < nblk; ++i) {
                 const bool more = i + 1 < nblk;
-                wait(sh.v_full[n & 1], n >> 1);
-                if (i < n0) {
+                const uint32_t cur = n + i, nxt = cur + 1;
+                if (i >= 0)
+                    wait(sh.v_full[cur & 1], cur >> 1);
+                if (i >= 0 && i < n0) {
                     wait(sh.p_full[0], n_p0++);
                     fence_after();
-                    values(0, n, i > 0);
+                    values(0, cur, i > 0);
                     if (i == n0 - 1)
                         commit(smem_addr(&sh.o_full[0]), one);
                 }
                 if (more) {
-                    wait(sh.k_full[(n + 1) & 1], (n + 1) >> 1);
-                    fence_after();
-                    if (i + 1 < n0)
-                        scores(0, n + 1);
+                    wait(sh.k_full[nxt & 1], nxt >> 1);
+                    if (i + 1 < n0) {
+                        if (i < 0)
+                            wait(sh.q_full[0], n_q0++);
+                        fence_after();
+                        scores(0, nxt);
+                    }
                 }
-                if (i < n1) {
+                if (i >= 0 && i < n1) {
                     wait(sh.p_full[1], n_p1++);
                     fence_after();
-                    values(1, n, i > 0);
+                    values(1, cur, i > 0);
                     if (i == n1 - 1)
                         commit(smem_addr(&sh.o_full[1]), one);
                 }
-                commit(smem_addr(&sh.v_empty[n & 1]), one);
+                if (i >= 0)
+                    commit(smem_addr(&sh.v_empty[cur & 1]), one);
                 if (more) {
-                    if (i + 1 < n1)
-                        scores(1, n + 1);
-                    commit(smem_addr(&sh.k_empty[(n + 1) & 1]), one);
+                    if (i + 1 < n1) {
+                        if (i < 0)
+                            wait(sh.q_full[1], n_q1++);
+                        fence_after();
+                        scores(1, nxt);
+                    }
+                    commit(smem_addr(&sh.k_empty[nxt & 1]), one);
                 }
             }
-            next_piece(c, b, seq_at, &w, &at, &pos, hi, tt);
+            n += nblk;
         }
         // before leaving, the MMAs in flight end (bounded): the last stages are released
         if (n > 0) {
