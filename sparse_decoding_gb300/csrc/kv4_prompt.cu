@@ -37,11 +37,11 @@ namespace nm {
 namespace {
 
 constexpr int kSoft = 256;      // softmax threads: two tiles of 128 rows
-constexpr int kUnpack = 128;    // unpacking threads
-constexpr int kMmaWarp = 12;    // (its warpgroup's other three warps idle)
-constexpr int kThreads = 512;
-// Registers of a thread in each role; 128 at launch, and 2 * 184 + 104 + 40 = 4 * 128.
-constexpr int kSoftRegs = 184, kUnpackRegs = 104, kMmaRegs = 40;
+constexpr int kUnpack = 256;    // unpacking threads
+constexpr int kMmaWarp = 16;    // of its warpgroup, the next one lists the pieces and two idle
+constexpr int kThreads = 640;
+// Registers of a thread in each role; 96 at launch, and 2 * 160 + 2 * 64 + 32 = 5 * 96.
+constexpr int kSoftRegs = 160, kUnpackRegs = 64, kMmaRegs = 32;
 constexpr int kSeqCache = 512;  // sequences whose descriptors are kept in shared memory
 constexpr int kBlock = 128;    // tokens of a block
 constexpr int kMinShare = 2;   // blocks of a CTA at least
@@ -209,27 +209,29 @@ template <int N> __device__ __forceinline__ __half2 nibble8(uint32_t w)
     return __hfma2(as_half2((x & 0x00F000F0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
 }
 
-// What an unpacking thread u holds of a block. K: four 16-byte pieces (8 bytes at
-// D = 64): row 32 j + u / 4, channels 16 (u % 4) .. of each group.
+// What an unpacking thread u holds of a block. K: two 16-byte pieces (8 bytes at
+// D = 64): row 64 j + u / 4, channels 16 (u % 4) .. of each group.
 template <int D> struct RawK {
-    uint32_t w[4][2 * Cfg<D>::G], p[4][Cfg<D>::G];
+    uint32_t w[2][2 * Cfg<D>::G], p[2][Cfg<D>::G];
 };
-// V: units (cell, group, e, p): channels 64 g + 8 e .., tokens 8 p .. of the cell.
-template <int D> struct RawV {
-    uint2 w[Cfg<D>::G][4], p[Cfg<D>::G][4];
+// V: a unit (cell, group, e, p): channels 64 g + 8 e .., tokens 8 p .. of the cell.
+// At D = 64 there are 128 of them, for the first 128 threads.
+struct RawV {
+    uint2 w[4], p[4];
 };
-template <int D> __device__ __forceinline__ void unit_of(int u, int j, int *cell, int *g)
+template <int D> __device__ __forceinline__ void unit_of(int u, int *cell, int *g, int *e, int *p)
 {
-    *cell = (Cfg<D>::G == 2 ? j : u >> 6) * 4 + ((u >> 1) & 3);
-    *g = Cfg<D>::G == 2 ? u >> 6 : 0;
+    *p = u & 1;
+    *e = (u >> 3) & 7;
+    *g = Cfg<D>::G == 2 ? (u >> 6) & 1 : 0;
+    *cell = (Cfg<D>::G == 2 ? u >> 7 : (u >> 6) & 1) * 4 + ((u >> 1) & 3);
 }
-
 template <int D> __device__ __forceinline__ void load_k(RawK<D> &r, const uint8_t *pool, uint32_t place, int u)
 {
     constexpr int G = Cfg<D>::G;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int row = 32 * j + (u >> 2), t = u & 3;
+    for (int j = 0; j < 2; ++j) {
+        const int row = 64 * j + (u >> 2), t = u & 3;
         const uint32_t where = __shfl_sync(~0u, place, row >> 4);
         const uint8_t *cell = pool + ((int64_t)where << 7);
         const uint8_t *src = cell + (row & 15) * (D / 2) + t * 8 * G;
@@ -256,8 +258,8 @@ template <int D> __device__ __forceinline__ void unpack_k(const RawK<D> &r, uint
     constexpr int G = Cfg<D>::G;
     const int t = u & 3;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int row = 32 * j + (u >> 2);
+    for (int j = 0; j < 2; ++j) {
+        const int row = 64 * j + (u >> 2);
         uint32_t mids[2] = {0, 0};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -275,67 +277,56 @@ template <int D> __device__ __forceinline__ void unpack_k(const RawK<D> &r, uint
             sts128(ks + G * kSub + row * 32 + ((t ^ ((row >> 2) & 1)) << 4), t ? 0 : mids[0], t ? 0 : mids[1], 0, 0);
     }
 }
-template <int D> __device__ __forceinline__ void load_v(RawV<D> &r, const uint8_t *pool, uint32_t place, int u)
+template <int D> __device__ __forceinline__ void load_v(RawV &r, const uint8_t *pool, uint32_t place, int u)
 {
     constexpr int G = Cfg<D>::G;
-    const int p = u & 1, e = (u >> 3) & 7;
+    int cell_i, g, e, p;
+    unit_of<D>(u, &cell_i, &g, &e, &p);
+    const uint32_t where = __shfl_sync(~0u, place, cell_i);
+    const uint8_t *cell = pool + ((int64_t)where << 7);
+    const bool have = where != ~0u && u < 128 * G;
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-        int cell_i, g;
-        unit_of<D>(u, j, &cell_i, &g);
-        const uint32_t where = __shfl_sync(~0u, place, cell_i);
-        const uint8_t *cell = pool + ((int64_t)where << 7);
-        const bool have = where != ~0u;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            r.w[j][t] = have ? __ldg((const uint2 *)(cell + Kv4Cell<D>::kV + g * 512 + e * 64 + t * 16 + p * 8))
-                             : make_uint2(0, 0);
-            r.p[j][t] = have ? __ldg((const uint2 *)(cell + Kv4Cell<D>::kVp + ((4 * p + t) * G + g) * 8)) : make_uint2(0, 0);
-        }
+    for (int t = 0; t < 4; ++t) {
+        r.w[t] = have ? __ldg((const uint2 *)(cell + Kv4Cell<D>::kV + g * 512 + e * 64 + t * 16 + p * 8))
+                      : make_uint2(0, 0);
+        r.p[t] = have ? __ldg((const uint2 *)(cell + Kv4Cell<D>::kVp + ((4 * p + t) * G + g) * 8)) : make_uint2(0, 0);
     }
 }
 // left: tokens of the sequence from the block's first on; past them V is 0, whatever is there.
-template <int D> __device__ __forceinline__ void unpack_v(const RawV<D> &r, uint32_t vs, int u, int left)
+template <int D> __device__ __forceinline__ void unpack_v(RawV &r, uint32_t vs, int u, int left)
 {
-    constexpr int G = Cfg<D>::G;
-    const int p = u & 1, e = (u >> 3) & 7;
+    if (u >= 128 * Cfg<D>::G)
+        return;
+    int cell_i, g, e, p;
+    unit_of<D>(u, &cell_i, &g, &e, &p);
+    const int tok = cell_i * 16 + 8 * p;
+    if (tok + 8 > left) {
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-        int cell_i, g;
-        unit_of<D>(u, j, &cell_i, &g);
-        uint2 pr[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            pr[t] = r.p[j][t];
-        const int tok = cell_i * 16 + 8 * p;
-        if (tok + 8 > left) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const uint32_t keep =
-                    (tok + 2 * t < left ? 0x0000FFFFu : 0u) | (tok + 2 * t + 1 < left ? 0xFFFF0000u : 0u);
-                pr[t].x &= keep;
-                pr[t].y &= keep;
-            }
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t keep =
+                (tok + 2 * t < left ? 0x0000FFFFu : 0u) | (tok + 2 * t + 1 < left ? 0xFFFF0000u : 0u);
+            r.p[t].x &= keep;
+            r.p[t].y &= keep;
         }
-        const uint32_t dst = vs + (cell_i >> 2) * (D * 128) + (64 * g + 8 * e) * 128;
-        const int chunk = 2 * (cell_i & 3) + p;
+    }
+    const uint32_t dst = vs + (cell_i >> 2) * (D * 128) + (64 * g + 8 * e) * 128;
+    const int chunk = 2 * (cell_i & 3) + p;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t y[4][4]; // [nibble][token pair]
+    for (int q = 0; q < 2; ++q) {
+        uint32_t y[4][4]; // [nibble][token pair]
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const uint32_t wv = q ? r.w[j][t].y : r.w[j][t].x;
-                const __half2 s = as_half2(pr[t].x), mid = as_half2(pr[t].y);
-                y[0][t] = as_u32(__hfma2(nibble8<0>(wv), s, mid));
-                y[1][t] = as_u32(__hfma2(nibble8<1>(wv), s, mid));
-                y[2][t] = as_u32(__hfma2(nibble8<2>(wv), s, mid));
-                y[3][t] = as_u32(__hfma2(nibble8<3>(wv), s, mid));
-            }
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t wv = q ? r.w[t].y : r.w[t].x;
+            const __half2 s = as_half2(r.p[t].x), mid = as_half2(r.p[t].y);
+            y[0][t] = as_u32(__hfma2(nibble8<0>(wv), s, mid));
+            y[1][t] = as_u32(__hfma2(nibble8<1>(wv), s, mid));
+            y[2][t] = as_u32(__hfma2(nibble8<2>(wv), s, mid));
+            y[3][t] = as_u32(__hfma2(nibble8<3>(wv), s, mid));
+        }
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const int rr = 4 * q + z; // row & 7
-                sts128(dst + rr * 128 + ((chunk ^ rr) << 4), y[z][0], y[z][1], y[z][2], y[z][3]);
-            }
+        for (int z = 0; z < 4; ++z) {
+            const int rr = 4 * q + z; // row & 7
+            sts128(dst + rr * 128 + ((chunk ^ rr) << 4), y[z][0], y[z][1], y[z][2], y[z][3]);
         }
     }
 }
@@ -448,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_addr(&sh.piece_full[i]), 1);
-            mbar_init(smem_addr(&sh.piece_empty[i]), 13); // a lane of each of warps 0 .. 12
+            mbar_init(smem_addr(&sh.piece_empty[i]), kMmaWarp + 1); // a lane of each warp that takes pieces
         }
         fence_mbar_init();
     }
@@ -810,11 +801,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         }
     } else if (warp < kMmaWarp) {
         setmaxnreg_dec<kUnpackRegs>();
-        // ---- unpacking: 128 threads fill K and V^T of a block ----
+        // ---- unpacking: 256 threads fill K and V^T of a block ----
         const int u = tid - kSoft;
         const int in_page = c.page_shift - 4;
         RawK<D> rk;
-        RawV<D> rv;
+        RawV rv;
         uint32_t piece = 0;
         Piece w = get_piece(piece);
         int i = 0;        // the block to fetch: b0 + i of piece w
