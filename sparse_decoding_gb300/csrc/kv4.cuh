@@ -114,7 +114,30 @@ __device__ __forceinline__ int64_t kv4_cell_offset(const Kv4 &c, int page, int l
            ((((int64_t)layer * c.n_kv_heads + head) << (c.page_shift - 4)) + cell) * Kv4Cell<D>::kBytes;
 }
 
-// 16 bytes between global memory and registers
+// A bounded wait (about a second, then NM_ERR_TIMEOUT; `dead` threads poll once). The
+// clock is read only after some polls: reading it takes longer than most waits.
+__device__ __forceinline__ void kv4_wait(uint32_t bar, uint32_t parity, uint32_t *status, bool &dead)
+{
+    uint64_t t0 = 0;
+    uint32_t polls = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (dead)
+            return;
+        if (++polls < 64)
+            continue;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0)
+            t0 = t;
+        if (t - t0 > kWaitLimitNs) {
+            atomicOr(status, 1u << NM_ERR_TIMEOUT);
+            dead = true;
+            return;
+        }
+    }
+}
+
+// 16 bytes of read-only data
 __device__ __forceinline__ uint4 ldg_nc128(const void *p)
 {
     uint4 v;

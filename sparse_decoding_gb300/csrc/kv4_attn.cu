@@ -34,6 +34,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int64_t kMinShare = 16; // cells of a CTA at least: two for each warp
+constexpr int kWholeCells = 32;   // segments of up to so many cells are not cut
 constexpr float kShift = 6.0f;    // p = 2^(s - m + kShift)
 constexpr float kSlack = 8.0f;    // a score may pass m by this much
 constexpr float kLog2e = 1.4426950408889634f;
@@ -79,53 +80,75 @@ template <int N> __device__ __forceinline__ __half2 nibble(uint32_t w, float bia
                    __float2half2_rn(-64.0f - bias));
 }
 
-// A cell in a lane's registers.
-template <int D> struct CellRegs {
+// A cell's parts in a lane's registers, from the cell in shared memory.
+template <int D> struct CellK {
     static constexpr int G = Kv4Cell<D>::G;
-    uint32_t k[2][2 * G]; // tokens g, g + 8: 16 channels of each group
-    uint32_t v[G][4];     // (quad 0, pair 0), (quad 1, pair 0), (quad 0, pair 1), (quad 1, pair 1)
-    uint32_t kp[2][G];    // tokens g, g + 8: (s, mid)
-    uint32_t vp[2][2 * G]; // token pairs t, t + 4: per group (s, s), (mid, mid)
+    uint32_t w[2][2 * G]; // tokens g, g + 8: 16 channels of each group
+    uint32_t p[2][G];     // (s, mid)
 };
-
-template <int D> __device__ __forceinline__ void load_cell(CellRegs<D> &r, const uint8_t *cell, int lane)
+template <int D> struct CellV {
+    static constexpr int G = Kv4Cell<D>::G;
+    uint32_t w[G][4];     // (quad 0, pair 0), (quad 1, pair 0), (quad 0, pair 1), (quad 1, pair 1)
+    uint32_t p[2][2 * G]; // token pairs t, t + 4: per group (s, s), (mid, mid)
+};
+template <int D> __device__ __forceinline__ void lds_k(CellK<D> &r, const uint8_t *cell, int lane)
 {
     using C = Kv4Cell<D>;
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (D == 128) {
-            const uint4 x = ldg_nc128(cell + e * 512 + lane * 16);
-            r.k[e][0] = x.x;
-            r.k[e][1] = x.y;
-            r.k[e][2 * C::G - 2] = x.z;
-            r.k[e][2 * C::G - 1] = x.w;
+            const uint4 x = *(const uint4 *)(cell + e * 512 + lane * 16);
+            r.w[e][0] = x.x;
+            r.w[e][1] = x.y;
+            r.w[e][2 * C::G - 2] = x.z;
+            r.w[e][2 * C::G - 1] = x.w;
             const uint2 p = *(const uint2 *)(cell + C::kKp + (g + 8 * e) * 8);
-            r.kp[e][0] = p.x;
-            r.kp[e][C::G - 1] = p.y;
-            const uint4 q = *(const uint4 *)(cell + C::kVp + (t + 4 * e) * 16);
-            r.vp[e][0] = q.x;
-            r.vp[e][1] = q.y;
-            r.vp[e][2 * C::G - 2] = q.z;
-            r.vp[e][2 * C::G - 1] = q.w;
+            r.p[e][0] = p.x;
+            r.p[e][C::G - 1] = p.y;
         } else {
             const uint2 x = *(const uint2 *)(cell + e * 256 + lane * 8);
-            r.k[e][0] = x.x;
-            r.k[e][1] = x.y;
-            r.kp[e][0] = *(const uint32_t *)(cell + C::kKp + (g + 8 * e) * 4);
+            r.w[e][0] = x.x;
+            r.w[e][1] = x.y;
+            r.p[e][0] = *(const uint32_t *)(cell + C::kKp + (g + 8 * e) * 4);
+        }
+    }
+}
+template <int D> __device__ __forceinline__ void lds_v(CellV<D> &r, const uint8_t *cell, int lane)
+{
+    using C = Kv4Cell<D>;
+    const int t = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (D == 128) {
+            const uint4 q = *(const uint4 *)(cell + C::kVp + (t + 4 * e) * 16);
+            r.p[e][0] = q.x;
+            r.p[e][1] = q.y;
+            r.p[e][2 * C::G - 2] = q.z;
+            r.p[e][2 * C::G - 1] = q.w;
+        } else {
             const uint2 q = *(const uint2 *)(cell + C::kVp + (t + 4 * e) * 8);
-            r.vp[e][0] = q.x;
-            r.vp[e][1] = q.y;
+            r.p[e][0] = q.x;
+            r.p[e][1] = q.y;
         }
     }
 #pragma unroll
     for (int e = 0; e < C::G; ++e) {
-        const uint4 x = ldg_nc128(cell + C::kV + e * 512 + lane * 16);
-        r.v[e][0] = x.x;
-        r.v[e][1] = x.y;
-        r.v[e][2] = x.z;
-        r.v[e][3] = x.w;
+        const uint4 x = *(const uint4 *)(cell + C::kV + e * 512 + lane * 16);
+        r.w[e][0] = x.x;
+        r.w[e][1] = x.y;
+        r.w[e][2] = x.z;
+        r.w[e][3] = x.w;
     }
+}
+
+// A copy of n bytes (a multiple of 16, 16-byte aligned ends) to shared memory,
+// counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t n, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(n), "r"(bar)
+                 : "memory");
 }
 
 struct AttnArgs {
@@ -144,11 +167,25 @@ struct AttnArgs {
 // Floats of one part in the workspace: m and l of each row, then O.
 template <int D, int NT> constexpr int part_floats() { return 8 * NT * (D + 2); }
 
+// What the scores of a row need: its factor, the sums of its q per group, and how
+// many tokens it attends.
+struct RowInfo {
+    float scale, q0, q1;
+    int limit;
+};
+
 template <int D, int NT> struct Smem {
     static constexpr int kRows = 8 * NT;
     static constexpr int kPitch = D + 4;
-    // [kWarps][kRows] m, l; [kWarps][kRows][kPitch] o
+    static constexpr int kStages = NT == 1 ? 4 : 6; // cells of a warp in flight or in use
+    static constexpr int kSteps = D / 16;
+    // the warps' rings; when a piece is done, the warps' parts (m, l, O) in their place
+    static constexpr int kRing = kWarps * kStages * Kv4Cell<D>::kBytes;
     static constexpr int kMerge = kWarps * kRows * (2 + kPitch) * 4;
+    static constexpr int kBig = kRing > kMerge ? kRing : kMerge;
+    // Q in B fragments: [n-tile][k-step][lane][2], then the rows' RowInfo
+    static constexpr int kQ = kBig, kInfo = kQ + NT * kSteps * 256, kBars = kInfo + kRows * 16;
+    static constexpr int kSeqs = kBars + kWarps * kStages * 8;
 };
 
 __device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -161,30 +198,49 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     constexpr int RT = 8 * NT;
     constexpr int KS = 4 * G; // k-steps of 16 channels
     using SM = Smem<D, NT>;
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int S = SM::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
     float *const sm_m = (float *)smem, *const sm_l = sm_m + kWarps * RT, *const sm_o = sm_l + kWarps * RT;
-    int64_t *const pre = (int64_t *)(smem + SM::kMerge);     // [n_seqs + 1]
+    uint2 *const sm_q = (uint2 *)(smem + SM::kQ);
+    RowInfo *const sm_info = (RowInfo *)(smem + SM::kInfo);
+    int64_t *const pre = (int64_t *)(smem + SM::kSeqs);      // [n_seqs + 1]
     Kv4Seq *const seqs = (Kv4Seq *)(pre + b.n_seqs + 1);     // [n_seqs]
     __shared__ uint32_t s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    uint8_t *const ring = smem + warp * S * Kv4Cell<D>::kBytes;
+    const uint32_t bars = smem_addr(smem + SM::kBars) + warp * S * 8;
 
     // the segments of each sequence, and where they start on the line of cells
+    if (lane == 0)
+        for (int i = 0; i < S; ++i)
+            mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+    int longest = 0;
     for (int i = tid; i < b.n_seqs; i += kThreads) {
         const Kv4Seq s = kv4_seq(c, b, i, blockIdx.x == 0);
         seqs[i] = s;
-        const int64_t cells = s.n_new == 0 ? 0 : s.len > 0 ? (s.len + kKv4Cell - 1) / kKv4Cell : 1;
-        pre[i + 1] = cells * ceil_div((int64_t)s.n_new * a.ratio, RT) * c.n_kv_heads;
+        const int cells = s.n_new == 0 ? 0 : s.len > 0 ? (s.len + kKv4Cell - 1) / kKv4Cell : 1;
+        longest = max(longest, cells);
+        pre[i + 1] = ceil_div((int64_t)s.n_new * a.ratio, RT) * c.n_kv_heads;
     }
-    __syncthreads();
+    // Short sequences are not cut: a segment is one step of the line, not one per cell.
+    const bool cut = __syncthreads_or(longest > kWholeCells);
     if (warp == 0) {
         int64_t sum = 0;
         for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
-            int64_t x = i0 + lane < b.n_seqs ? pre[i0 + lane + 1] : 0;
+            int64_t x = 0;
+            if (i0 + lane < b.n_seqs) {
+                x = pre[i0 + lane + 1];
+                const int len = seqs[i0 + lane].len;
+                if (cut && len > 0)
+                    x *= (len + kKv4Cell - 1) / kKv4Cell;
+            }
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(~0u, x, o);
                 if (lane >= o)
                     x += y;
             }
+            __syncwarp();
             if (i0 + lane < b.n_seqs)
                 pre[i0 + lane + 1] = sum + x;
             sum += __shfl_sync(~0u, x, 31);
@@ -195,8 +251,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     __syncthreads();
     const int64_t total = pre[b.n_seqs];
     int64_t share = ceil_div(total, gridDim.x);
-    share = share < kMinShare ? kMinShare : share;
+    if (cut && share < kMinShare)
+        share = kMinShare;
     const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share < total ? lo + share : total;
+    const int shift = c.page_shift - 4;
+    uint32_t phase = 0; // bit i: the parity of stage i's next completion
+    bool dead = false;
 
     for (int64_t pos = lo; pos < hi;) {
         int i;
@@ -213,46 +273,65 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         }
         const Kv4Seq s = seqs[i];
         const int cells = s.len > 0 ? (s.len + kKv4Cell - 1) / kKv4Cell : 1;
-        const int64_t seg = (pos - pre[i]) / cells;
-        const int64_t seg_lo = pre[i] + seg * cells, seg_hi = seg_lo + cells;
-        const int c0 = (int)(pos - seg_lo);
-        const int c1 = (int)((hi < seg_hi ? hi : seg_hi) - seg_lo);
-        const int64_t tiles = ceil_div((int64_t)s.n_new * a.ratio, RT);
-        const int head = (int)(seg / tiles);
-        const int64_t row0 = (seg % tiles) * RT;        // first row of the tile
+        const int per = cut ? cells : 1; // steps of the segment
+        const int64_t seg = (pos - pre[i]) / per;
+        const int64_t seg_lo = pre[i] + seg * per, seg_hi = seg_lo + per;
+        const int steps = (int)((hi < seg_hi ? hi : seg_hi) - pos);
+        const int c0 = cut ? (int)(pos - seg_lo) : 0, c1 = cut ? c0 + steps : cells;
         const int64_t rows = (int64_t)s.n_new * a.ratio; // rows of the sequence and kv head
+        const int64_t tiles = ceil_div(rows, RT);
+        const int head = (int)(seg / tiles);
+        const int64_t row0 = (seg % tiles) * RT; // first row of the tile
 
-        // Q as the B operand: row g of each n-tile, channels 64 grp + 16 t ..
-        uint32_t qb[NT][KS][2];
-        float rowscale[NT][2], qsum[NT][2][G];
-        int limit[NT][2]; // tokens that rows 2 t, 2 t + 1 attend
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        // The warp's cells are c0 + warp, + kWarps, ...: cell number x of them goes to stage x % S.
+        // A lane holds the page of every 32nd; `have` has a bit for each stage that was filled.
+        const int mine = s.len > 0 && c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
+        int32_t pages = -1;
+        uint32_t have = 0;
+        int stage_in = 0;
+        const auto fetch = [&](int x) {
+            if ((x & 31) == 0) {
+                const int cell = c0 + warp + (x + lane) * kWarps;
+                pages = x + lane < mine ? kv4_page(c, s.row, cell >> shift) : 0;
+                if (pages < 0)
+                    kv4_bad(c);
+            }
+            const int page = __shfl_sync(~0u, pages, x & 31);
+            const int cell = c0 + warp + x * kWarps;
+            have = page >= 0 ? have | 1u << stage_in : have & ~(1u << stage_in);
+            if (lane == 0 && page >= 0) {
+                const uint32_t bar = bars + 8 * stage_in;
+                mbar_arrive_expect_tx(bar, Kv4Cell<D>::kBytes);
+                bulk_load(smem_addr(ring + stage_in * Kv4Cell<D>::kBytes),
+                          c.pool + kv4_cell_offset<D>(c, page, a.layer, head, cell & ((1 << shift) - 1)),
+                          Kv4Cell<D>::kBytes, bar);
+            }
+            stage_in = stage_in + 1 == S ? 0 : stage_in + 1;
+        };
+        // stages start at 0 with each piece
+        for (int x = 0; x < S - 1 && x < mine; ++x)
+            fetch(x);
+
+        // Q as the B operand: warp j makes n-tile j; row g, channels 64 e + 16 t ..
+        for (int j = warp; j < NT; j += kWarps) {
             const int64_t row = row0 + 8 * j + g;
             float x[G][16];
             float top = 0.0f;
-            if (row < rows) {
-                const int64_t token = s.first + row / a.ratio;
-                const uint16_t *q = a.q + token * a.q_stride + ((int64_t)head * a.ratio + row % a.ratio) * D;
+            const bool real = row < rows;
+            const int64_t token = s.first + row / a.ratio;
+            const uint16_t *q = a.q + token * a.q_stride + ((int64_t)head * a.ratio + row % a.ratio) * D;
 #pragma unroll
-                for (int e = 0; e < G; ++e)
+            for (int e = 0; e < G; ++e)
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const uint4 w = ldg_nc128(q + 64 * e + 16 * t + 8 * f);
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                for (int f = 0; f < 2; ++f) {
+                    const uint4 w = real ? ldg_nc128(q + 64 * e + 16 * t + 8 * f) : make_uint4(0, 0, 0, 0);
+                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            x[e][8 * f + 2 * n] = bf16lo_to_f32(ws[n]);
-                            x[e][8 * f + 2 * n + 1] = bf16hi_to_f32(ws[n]);
-                        }
+                    for (int n = 0; n < 4; ++n) {
+                        x[e][8 * f + 2 * n] = bf16lo_to_f32(ws[n]);
+                        x[e][8 * f + 2 * n + 1] = bf16hi_to_f32(ws[n]);
                     }
-            } else {
-#pragma unroll
-                for (int e = 0; e < G; ++e)
-#pragma unroll
-                    for (int n = 0; n < 16; ++n)
-                        x[e][n] = 0.0f;
-            }
+                }
 #pragma unroll
             for (int e = 0; e < G; ++e)
 #pragma unroll
@@ -282,19 +361,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float *y = &x[e][8 * f + 2 * h];
-                        qb[j][4 * e + 2 * f + h][0] = pack_half2(y[0], y[4]);
-                        qb[j][4 * e + 2 * f + h][1] = pack_half2(y[1], y[5]);
+                        sm_q[(j * KS + 4 * e + 2 * f + h) * 32 + lane] =
+                            make_uint2(pack_half2(y[0], y[4]), pack_half2(y[1], y[5]));
                     }
             }
+            if (t == 0)
+                sm_info[8 * j + g] = RowInfo{up * (a.scale * kLog2e), sums[0], sums[G - 1],
+                                             real ? s.len - s.n_new + (int)(row / a.ratio) + 1 : 0};
+        }
+        __syncthreads();
+        // with few rows Q stays in registers
+        constexpr bool kKeepQ = NT <= 2;
+        uint2 qb[kKeepQ ? NT : 1][KS];
+        RowInfo info[kKeepQ ? NT : 1][2];
+        if (kKeepQ) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int from = (2 * t + n) * 4;
-                rowscale[j][n] = __shfl_sync(~0u, up, from) * (a.scale * kLog2e);
+            for (int j = 0; j < NT; ++j) {
 #pragma unroll
-                for (int e = 0; e < G; ++e)
-                    qsum[j][n][e] = __shfl_sync(~0u, sums[e], from);
-                const int64_t r = row0 + 8 * j + 2 * t + n;
-                limit[j][n] = r < rows ? s.len - s.n_new + (int)(r / a.ratio) + 1 : 0;
+                for (int x = 0; x < KS; ++x)
+                    qb[j % (kKeepQ ? NT : 1)][x] = sm_q[(j * KS + x) * 32 + lane];
+                info[j % (kKeepQ ? NT : 1)][0] = sm_info[8 * j + 2 * t];
+                info[j % (kKeepQ ? NT : 1)][1] = sm_info[8 * j + 2 * t + 1];
             }
         }
 
@@ -304,63 +391,71 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         for (int j = 0; j < NT; ++j)
             m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.0f;
 
-        const int shift = c.page_shift - 4;
-        for (int cell = c0 + warp; cell < c1; cell += kWarps) {
-            if (s.len == 0)
-                break;
-            const int page = kv4_page(c, s.row, cell >> shift);
-            if (page < 0) {
-                if (lane == 0)
-                    kv4_bad(c);
-                continue;
+        int stage = 0;
+#pragma unroll 1
+        for (int x = 0; x < mine; ++x) {
+            if (x + S - 1 < mine) {
+                __syncwarp(); // the stage that is filled now was read by all lanes
+                fetch(x + S - 1);
             }
-            CellRegs<D> r;
-            load_cell<D>(r, c.pool + kv4_cell_offset<D>(c, page, a.layer, head, cell & ((1 << shift) - 1)), lane);
-            const int tok = cell * kKv4Cell;
+            const int st = stage;
+            stage = stage + 1 == S ? 0 : stage + 1;
+            if (!(have >> st & 1))
+                continue;
+            kv4_wait(bars + 8 * st, phase >> st & 1, c.status, dead);
+            phase ^= 1u << st;
+            const uint8_t *cell_at = ring + st * Kv4Cell<D>::kBytes;
+            const int tok = (c0 + warp + x * kWarps) * kKv4Cell;
 
             // scores
-            float acc[NT][G][4] = {};
-#pragma unroll
-            for (int e = 0; e < G; ++e)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    uint32_t af[2][4];
-                    const uint32_t w0 = r.k[0][2 * e + f], w1 = r.k[1][2 * e + f];
-                    af[0][0] = as_u32(nibble<0>(w0, 8.0f));
-                    af[0][1] = as_u32(nibble<0>(w1, 8.0f));
-                    af[0][2] = as_u32(nibble<1>(w0, 8.0f));
-                    af[0][3] = as_u32(nibble<1>(w1, 8.0f));
-                    af[1][0] = as_u32(nibble<2>(w0, 8.0f));
-                    af[1][1] = as_u32(nibble<2>(w1, 8.0f));
-                    af[1][2] = as_u32(nibble<3>(w0, 8.0f));
-                    af[1][3] = as_u32(nibble<3>(w1, 8.0f));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-                            mma16816(acc[j][e], af[h], qb[j][4 * e + 2 * f + h][0], qb[j][4 * e + 2 * f + h][1]);
-                }
-            float ks[2][G], km[2][G];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
+            float sc[NT][4];
+            {
+                CellK<D> r;
+                lds_k<D>(r, cell_at, lane);
 #pragma unroll
                 for (int e = 0; e < G; ++e) {
-                    ks[u][e] = __low2float(as_half2(r.kp[u][e]));
-                    km[u][e] = __high2float(as_half2(r.kp[u][e]));
+                    float acc[NT][4] = {};
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        uint32_t af[2][4];
+                        const uint32_t w0 = r.w[0][2 * e + f], w1 = r.w[1][2 * e + f];
+                        af[0][0] = as_u32(nibble<0>(w0, 8.0f));
+                        af[0][1] = as_u32(nibble<0>(w1, 8.0f));
+                        af[0][2] = as_u32(nibble<1>(w0, 8.0f));
+                        af[0][3] = as_u32(nibble<1>(w1, 8.0f));
+                        af[1][0] = as_u32(nibble<2>(w0, 8.0f));
+                        af[1][1] = as_u32(nibble<2>(w1, 8.0f));
+                        af[1][2] = as_u32(nibble<3>(w0, 8.0f));
+                        af[1][3] = as_u32(nibble<3>(w1, 8.0f));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) {
+                                const int z = 4 * e + 2 * f + h;
+                                const uint2 q = kKeepQ ? qb[j % (kKeepQ ? NT : 1)][z] : sm_q[(j * KS + z) * 32 + lane];
+                                mma16816(acc[j], af[h], q.x, q.y);
+                            }
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int u = f >> 1, n = f & 1; // token g + 8 u, row 2 t + n
+                            const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
+                            const float ks = __low2float(as_half2(r.p[u][e])), km = __high2float(as_half2(r.p[u][e]));
+                            const float y = fmaf(ks, acc[j][f], km * (e ? in.q1 : in.q0));
+                            sc[j][f] = e ? sc[j][f] + y : y;
+                        }
                 }
-            float sc[NT][4];
+            }
             bool above = false;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
-                    const int u = f >> 1, n = f & 1; // token g + 8 u, row 2 t + n
-                    float x = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < G; ++e)
-                        x = fmaf(ks[u][e], acc[j][e][f], fmaf(km[u][e], qsum[j][n][e], x));
-                    x *= rowscale[j][n];
-                    sc[j][f] = tok + g + 8 * u < limit[j][n] ? x : -INFINITY;
+                    const int u = f >> 1, n = f & 1;
+                    const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
+                    sc[j][f] = tok + g + 8 * u < in.limit ? sc[j][f] * in.scale : -INFINITY;
                     above |= sc[j][f] > m[j][n] + kSlack;
                 }
             if (__any_sync(~0u, above)) {
@@ -368,12 +463,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        float x = fmaxf(m[j][n], fmaxf(sc[j][n], sc[j][n + 2]));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-                        const float by = x == m[j][n] ? 1.0f : exp2_approx(m[j][n] - x);
-                        m[j][n] = x;
+                        float y = fmaxf(m[j][n], fmaxf(sc[j][n], sc[j][n + 2]));
+                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
+                        const float by = y == m[j][n] ? 1.0f : exp2_approx(m[j][n] - y);
+                        m[j][n] = y;
                         l[j][n] *= by;
 #pragma unroll
                         for (int e = 0; e < G; ++e)
@@ -391,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
                     const int n = f & 1;
-                    const float x = exp2_approx(sc[j][f] - (m[j][n] - kShift));
-                    p[f] = sc[j][f] == -INFINITY ? 0.0f : x;
+                    const float y = exp2_approx(sc[j][f] - (m[j][n] - kShift));
+                    p[f] = sc[j][f] == -INFINITY ? 0.0f : y;
                     l[j][n] += p[f];
                 }
                 pb[j][0] = transpose8x8(pack_half2(p[0], p[1]));
@@ -400,6 +495,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             }
 
             // O^T += V^T P^T; tokens past the sequence's end hold anything: their V is taken as 0
+            CellV<D> r;
+            lds_v<D>(r, cell_at, lane);
             if (tok + kKv4Cell > s.len) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -407,20 +504,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                     const uint32_t keep = (first < s.len ? 0x0000FFFFu : 0u) | (first + 1 < s.len ? 0xFFFF0000u : 0u);
 #pragma unroll
                     for (int e = 0; e < 2 * G; ++e)
-                        r.vp[u][e] &= keep;
+                        r.p[u][e] &= keep;
                 }
             }
 #pragma unroll
             for (int e = 0; e < G; ++e) {
-                const __half2 s0 = as_half2(r.vp[0][2 * e]), m0 = as_half2(r.vp[0][2 * e + 1]);
-                const __half2 s1 = as_half2(r.vp[1][2 * e]), m1 = as_half2(r.vp[1][2 * e + 1]);
+                const __half2 s0 = as_half2(r.p[0][2 * e]), m0 = as_half2(r.p[0][2 * e + 1]);
+                const __half2 s1 = as_half2(r.p[1][2 * e]), m1 = as_half2(r.p[1][2 * e + 1]);
                 const auto tile = [&](auto nib) {
                     constexpr int N = decltype(nib)::value;
                     uint32_t af[4];
-                    af[0] = as_u32(__hfma2(nibble<N>(r.v[e][0], 8.0f), s0, m0));
-                    af[1] = as_u32(__hfma2(nibble<N>(r.v[e][1], 8.0f), s0, m0));
-                    af[2] = as_u32(__hfma2(nibble<N>(r.v[e][2], 8.0f), s1, m1));
-                    af[3] = as_u32(__hfma2(nibble<N>(r.v[e][3], 8.0f), s1, m1));
+                    af[0] = as_u32(__hfma2(nibble<N>(r.w[e][0], 8.0f), s0, m0));
+                    af[1] = as_u32(__hfma2(nibble<N>(r.w[e][1], 8.0f), s0, m0));
+                    af[2] = as_u32(__hfma2(nibble<N>(r.w[e][2], 8.0f), s1, m1));
+                    af[3] = as_u32(__hfma2(nibble<N>(r.w[e][3], 8.0f), s1, m1));
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
                         mma16816(o[j][e][N], af, pb[j][0], pb[j][1]);
@@ -431,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 tile(std::integral_constant<int, 3>{});
             }
         }
+        __syncthreads(); // the rings are read: the parts take their place
 
         // the warp's part to shared memory: rows 2 t, 2 t + 1, channels 64 e + 8 g ..
 #pragma unroll
@@ -515,16 +613,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             }
             __syncthreads();
             if (s_last) {
+                const auto at = [&](int k) {
+                    return a.partials + ((int64_t)k * 2 + (k > first || seg_lo == (int64_t)first * share ? 0 : 1)) *
+                                            part_floats<D, NT>();
+                };
                 for (int x = tid; x < RT * (D / 4); x += kThreads) {
                     const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
-                    const auto at = [&](int k) {
-                        return a.partials + ((int64_t)k * 2 + (k > first || seg_lo == (int64_t)first * share ? 0 : 1)) *
-                                                part_floats<D, NT>();
-                    };
                     float M = -INFINITY, L = 0.0f;
                     for (int k = first; k <= last; ++k)
                         M = fmaxf(M, ldcg_f32(at(k) + row));
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                     for (int k = first; k <= last; ++k) {
                         const float *p = at(k);
                         const float mk = ldcg_f32(p + row);
@@ -540,22 +639,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 }
             }
         }
-        __syncthreads(); // the parts' shared memory is free again
-        pos += c1 - c0;
+        // the next piece's copies overwrite the parts: they are read, and the reads come first
+        fence_proxy_async_smem();
+        __syncthreads();
+        pos += steps;
     }
 }
 
 template <int D, int NT> nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, int num_sms, cudaStream_t st)
 {
-    const size_t smem = Smem<D, NT>::kMerge + (size_t)(b.n_seqs + 1) * 8 + (size_t)b.n_seqs * sizeof(Kv4Seq);
+    constexpr size_t kMost = Smem<D, NT>::kSeqs + kKv4MaxSeqs * 24 + 8;
+    static_assert(kMost + 1024 <= 227 * 1024, "shared memory");
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(attn_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    Smem<D, NT>::kMerge + kKv4MaxSeqs * 24 + 8);
+        attr = cudaFuncSetAttribute(attn_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
     });
     if (attr != cudaSuccess)
         return NM_ERR_CUDA;
+    const size_t smem = Smem<D, NT>::kSeqs + (size_t)(b.n_seqs + 1) * 8 + (size_t)b.n_seqs * sizeof(Kv4Seq);
     const unsigned grid = (unsigned)(num_sms * (NT == 1 ? 2 : 1));
     attn_rows_kernel<D, NT><<<grid, kThreads, smem, st>>>(c, b, a);
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
@@ -563,10 +665,10 @@ template <int D, int NT> nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, 
 
 } // namespace
 
-// Parts of two CTAs to an SM with 8 rows, or of one with 16: two each.
+// Two parts of a CTA: of two CTAs to an SM with 8 rows, or of one with up to 32.
 size_t kv4_partial_bytes(int head_dim)
 {
-    const size_t rows = (size_t)kKv4Counters / 2 * 2 * 8 * (head_dim + 2) * 4;
+    const size_t rows = (size_t)kKv4Counters / 2 * 2 * 32 * (head_dim + 2) * 4;
     const size_t prompt = kv4_prompt_partial_bytes(head_dim);
     return rows > prompt ? rows : prompt;
 }
@@ -578,10 +680,14 @@ nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
                      at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials};
     if (max_new * a.ratio > 32)
         return kv4_launch_prompt(c, b, at, w, num_sms, st);
-    const bool one = max_new * a.ratio <= 8;
+    const int nt = max_new * a.ratio <= 8 ? 1 : max_new * a.ratio <= 16 ? 2 : 4;
     if (c.head_dim == 128)
-        return one ? launch_rows<128, 1>(c, b, a, num_sms, st) : launch_rows<128, 2>(c, b, a, num_sms, st);
-    return one ? launch_rows<64, 1>(c, b, a, num_sms, st) : launch_rows<64, 2>(c, b, a, num_sms, st);
+        return nt == 1   ? launch_rows<128, 1>(c, b, a, num_sms, st)
+               : nt == 2 ? launch_rows<128, 2>(c, b, a, num_sms, st)
+                         : launch_rows<128, 4>(c, b, a, num_sms, st);
+    return nt == 1   ? launch_rows<64, 1>(c, b, a, num_sms, st)
+           : nt == 2 ? launch_rows<64, 2>(c, b, a, num_sms, st)
+                     : launch_rows<64, 4>(c, b, a, num_sms, st);
 }
 
 } // namespace nm

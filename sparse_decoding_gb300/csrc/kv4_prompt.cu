@@ -331,29 +331,6 @@ template <int D> __device__ __forceinline__ void unpack_v(RawV &r, uint32_t vs, 
     }
 }
 
-// A bounded wait (about a second, then NM_ERR_TIMEOUT; `dead` threads poll once). The
-// clock is read only after some polls: reading it takes longer than most waits.
-__device__ __forceinline__ void wait_bounded(uint32_t bar, uint32_t parity, uint32_t *status, bool &dead)
-{
-    uint64_t t0 = 0;
-    uint32_t polls = 0;
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (dead)
-            return;
-        if (++polls < 64)
-            continue;
-        const uint64_t t = globaltimer_ns();
-        if (t0 == 0)
-            t0 = t;
-        if (t - t0 > kWaitLimitNs) {
-            atomicOr(status, 1u << NM_ERR_TIMEOUT);
-            dead = true;
-            return;
-        }
-    }
-}
-
 struct PromptArgs {
     int layer, ratio, n_q_heads;
     const uint16_t *q;
@@ -530,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
     const uint32_t tmem = sh.tmem;
     bool dead = false;
     const auto wait = [&](uint64_t &bar, uint32_t parity) {
-        wait_bounded(smem_addr(&bar), parity & 1u, c.status, dead);
+        kv4_wait(smem_addr(&bar), parity & 1u, c.status, dead);
     };
     // Piece number p of the CTA, for a whole warp.
     const auto get_piece = [&](uint32_t p) {
