@@ -459,6 +459,7 @@ class Kv4Cache:
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
         self.device, self.n_pages, self.page_tokens = device, n_pages, page_tokens
+        self._index, self._lib = device.index, L
         self.n_layers, self.n_kv_heads, self.head_dim = n_layers, n_kv_heads, head_dim
         ints = self.book_ints(n_pages, max_seqs, max_pages)
         fresh = book is None
@@ -489,9 +490,9 @@ class Kv4Cache:
         return 16 + _pad4(max_seqs) + _pad4(n_pages) + _pad4(max_seqs * max_pages)
 
     def _s(self) -> int:
-        if torch.cuda.current_device() != self.device.index:
+        if torch.cuda.current_device() != self._index:
             raise ValueError(f"the cache is on {self.device}: make it the current device")
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def _ids(self, t: Optional[torch.Tensor], name: str):
         if t is None:
@@ -527,29 +528,29 @@ class Kv4Cache:
         """Room for the new tokens of each sequence (``n`` sequences with both None): lens grow, pages
         are added. All or nothing; ``info[1]`` (on the device) tells."""
         p, st, m = self._batch(seqs, starts, n)
-        _check(lib().nm_kv4_reserve(self._ref, p, st, m, self._s()), "nm_kv4_reserve")
+        _check(self._lib.nm_kv4_reserve(self._ref, p, st, m, self._s()), "nm_kv4_reserve")
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor) -> None:
         """The empty sequences dst become copies of src, sharing its full pages. ``info[1]`` tells."""
         if src.numel() != dst.numel():
             raise ValueError("src and dst must have the same length")
-        _check(lib().nm_kv4_fork(self._ref, self._ids(src, "src"), self._ids(dst, "dst"), src.numel(), self._s()),
+        _check(self._lib.nm_kv4_fork(self._ref, self._ids(src, "src"), self._ids(dst, "dst"), src.numel(), self._s()),
                "nm_kv4_fork")
 
     def free(self, seqs: torch.Tensor) -> None:
         """Empties the listed sequences."""
-        _check(lib().nm_kv4_free(self._ref, self._ids(seqs, "seqs"), seqs.numel(), self._s()), "nm_kv4_free")
+        _check(self._lib.nm_kv4_free(self._ref, self._ids(seqs, "seqs"), seqs.numel(), self._s()), "nm_kv4_free")
 
     def compact(self) -> None:
         """Moves the pages in use to the front of the pool; the tables follow."""
-        _check(lib().nm_kv4_compact(self._ref, self._s()), "nm_kv4_compact")
+        _check(self._lib.nm_kv4_compact(self._ref, self._s()), "nm_kv4_compact")
 
     def copy_pages(self, src_pages: torch.Tensor, dst_pages: torch.Tensor, dst: Optional["Kv4Cache"] = None) -> None:
         """Copies whole pages of this pool to pages of ``dst``'s (default: this one)."""
         dst = self if dst is None else dst
         if src_pages.numel() != dst_pages.numel() or dst.device != self.device:
             raise ValueError("page lists must have the same length, and the caches one device")
-        _check(lib().nm_kv4_copy_pages(self._ref, self._ids(src_pages, "src_pages"), dst._ref,
+        _check(self._lib.nm_kv4_copy_pages(self._ref, self._ids(src_pages, "src_pages"), dst._ref,
                                        self._ids(dst_pages, "dst_pages"), src_pages.numel(), self._s()),
                "nm_kv4_copy_pages")
 
@@ -579,7 +580,7 @@ class Kv4Cache:
                 raise ValueError(f"rope must be [positions][{self.head_dim}] on {self.device}")
             rp, rows = rope.data_ptr(), rope.shape[0]
         sp, st, n = self._batch(seqs, starts, T if starts is None else None)
-        _check(lib().nm_kv4_append(self._ref, layer, sp, st, n, T, kp, ks, vp, vs, qp, qs, qh, op, os_, rp, rows,
+        _check(self._lib.nm_kv4_append(self._ref, layer, sp, st, n, T, kp, ks, vp, vs, qp, qs, qh, op, os_, rp, rows,
                                    self._s()), "nm_kv4_append")
         return q_out if q is not None else None
 
@@ -591,7 +592,7 @@ class Kv4Cache:
         shape = (n_tokens, self.n_kv_heads, self.head_dim)
         dt = torch.float32 if f32 else torch.bfloat16
         k, v = torch.empty(shape, dtype=dt, device=self.device), torch.empty(shape, dtype=dt, device=self.device)
-        _check(lib().nm_kv4_read(self._ref, layer, sp, st, n, n_tokens, k.data_ptr(), v.data_ptr(), int(f32),
+        _check(self._lib.nm_kv4_read(self._ref, layer, sp, st, n, n_tokens, k.data_ptr(), v.data_ptr(), int(f32),
                                  self._s()), "nm_kv4_read")
         return k, v
 
@@ -611,7 +612,7 @@ class Kv4Cache:
             raise ValueError("out must have q's tokens and heads")
         sp, st, n = self._batch(seqs, starts, T if starts is None else None)
         ls = torch.empty(T, qh, dtype=torch.float32, device=q.device) if lse else None
-        _check(lib().nm_kv4_attention(self._ref, layer, sp, st, n, T, max(T, 1) if max_new is None else max_new, qp,
+        _check(self._lib.nm_kv4_attention(self._ref, layer, sp, st, n, T, max(T, 1) if max_new is None else max_new, qp,
                                       qs, qh, self.head_dim ** -0.5 if scale is None else scale, op, os_,
                                       ls.data_ptr() if lse else None, self._s()), "nm_kv4_attention")
         return (out, ls) if lse else out

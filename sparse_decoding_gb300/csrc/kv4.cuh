@@ -137,6 +137,11 @@ __device__ __forceinline__ void kv4_wait(uint32_t bar, uint32_t parity, uint32_t
     }
 }
 
+__device__ __forceinline__ void kv4_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // 16 bytes of read-only data
 __device__ __forceinline__ uint4 ldg_nc128(const void *p)
 {

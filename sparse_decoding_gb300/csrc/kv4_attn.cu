@@ -35,8 +35,10 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int64_t kMinShare = 16; // cells of a CTA at least: two for each warp
 constexpr int kWholeCells = 32;   // segments of up to so many cells are not cut
+constexpr int kOver = 16;         // cells that starting and ending a piece costs as much as
 constexpr float kShift = 6.0f;    // p = 2^(s - m + kShift)
 constexpr float kSlack = 8.0f;    // a score may pass m by this much
+constexpr float kNone = 1e38f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -71,12 +73,18 @@ __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *(uint32_t *)&x; 
 // Nibble N (0..3) of both halves of w, minus `bias`, as two fp16 numbers: the
 // bits under an exponent of 2^10 are 1024 + n (or 1024 + 16 n), so the result is
 // exact.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 template <int N> __device__ __forceinline__ __half2 nibble(uint32_t w, float bias)
 {
     const uint32_t x = N >= 2 ? w >> 8 : w;
     if (N % 2 == 0)
-        return __hadd2(as_half2((x & 0x000F000Fu) | 0x64006400u), __float2half2_rn(-1024.0f - bias));
-    return __hfma2(as_half2((x & 0x00F000F0u) | 0x64006400u), __float2half2_rn(0.0625f),
+        return __hadd2(as_half2(and_or(x, 0x000F000Fu, 0x64006400u)), __float2half2_rn(-1024.0f - bias));
+    return __hfma2(as_half2(and_or(x, 0x00F000F0u, 0x64006400u)), __float2half2_rn(0.0625f),
                    __float2half2_rn(-64.0f - bias));
 }
 
@@ -177,7 +185,7 @@ struct RowInfo {
 template <int D, int NT> struct Smem {
     static constexpr int kRows = 8 * NT;
     static constexpr int kPitch = D + 4;
-    static constexpr int kStages = NT == 1 ? 4 : 6; // cells of a warp in flight or in use
+    static constexpr int kStages = NT == 1 ? 4 : 8; // cells of a warp in flight or in use
     static constexpr int kSteps = D / 16;
     // the warps' rings; when a piece is done, the warps' parts (m, l, O) in their place
     static constexpr int kRing = kWarps * kStages * Kv4Cell<D>::kBytes;
@@ -208,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     __shared__ uint32_t s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     uint8_t *const ring = smem + warp * S * Kv4Cell<D>::kBytes;
-    const uint32_t bars = smem_addr(smem + SM::kBars) + warp * S * 8;
+    const uint32_t rings = smem_addr(ring), bars = smem_addr(smem + SM::kBars) + warp * S * 8;
 
     // the segments of each sequence, and where they start on the line of cells
     if (lane == 0)
@@ -232,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             if (i0 + lane < b.n_seqs) {
                 x = pre[i0 + lane + 1];
                 const int len = seqs[i0 + lane].len;
-                if (cut && len > 0)
-                    x *= (len + kKv4Cell - 1) / kKv4Cell;
+                if (cut)
+                    x *= kOver + (len > 0 ? (len + kKv4Cell - 1) / kKv4Cell : 1);
             }
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(~0u, x, o);
@@ -251,11 +259,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     __syncthreads();
     const int64_t total = pre[b.n_seqs];
     int64_t share = ceil_div(total, gridDim.x);
-    if (cut && share < kMinShare)
-        share = kMinShare;
+    if (cut && share < kMinShare + kOver)
+        share = kMinShare + kOver;
     const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share < total ? lo + share : total;
     const int shift = c.page_shift - 4;
-    uint32_t phase = 0; // bit i: the parity of stage i's next completion
+    uint32_t used = 0; // cells of this warp so far: the next takes stage used % S
     bool dead = false;
 
     for (int64_t pos = lo; pos < hi;) {
@@ -273,42 +281,49 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         }
         const Kv4Seq s = seqs[i];
         const int cells = s.len > 0 ? (s.len + kKv4Cell - 1) / kKv4Cell : 1;
-        const int per = cut ? cells : 1; // steps of the segment
+        // A segment that may be cut has kOver steps of the line before its cells' own.
+        const int over = cut ? kOver : 0, per = cut ? kOver + cells : 1;
         const int64_t seg = (pos - pre[i]) / per;
         const int64_t seg_lo = pre[i] + seg * per, seg_hi = seg_lo + per;
         const int steps = (int)((hi < seg_hi ? hi : seg_hi) - pos);
-        const int c0 = cut ? (int)(pos - seg_lo) : 0, c1 = cut ? c0 + steps : cells;
+        const int from = (int)(pos - seg_lo) - over;
+        const int c0 = cut && from > 0 ? from : 0, c1 = cut ? from + steps : cells;
+        if (c1 <= c0)
+            break; // the CTA's part of the line ends before the segment's first cell
         const int64_t rows = (int64_t)s.n_new * a.ratio; // rows of the sequence and kv head
         const int64_t tiles = ceil_div(rows, RT);
         const int head = (int)(seg / tiles);
         const int64_t row0 = (seg % tiles) * RT; // first row of the tile
+        const int tile_first = s.len - s.n_new + (int)(row0 / a.ratio) + 1; // tokens that its first row attends
 
-        // The warp's cells are c0 + warp, + kWarps, ...: cell number x of them goes to stage x % S.
-        // A lane holds the page of every 32nd; `have` has a bit for each stage that was filled.
+        // The warp's cells are c0 + warp, + kWarps, ... A lane holds the address of every 32nd
+        // (0: its page is none of the pool's); `have` has a bit for each stage that was filled.
         const int mine = s.len > 0 && c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
-        int32_t pages = -1;
+        const uint8_t *const heads = c.pool + kv4_cell_offset<D>(c, 0, a.layer, head, 0);
+        uint64_t where = 0;
         uint32_t have = 0;
-        int stage_in = 0;
         const auto fetch = [&](int x) {
             if ((x & 31) == 0) {
                 const int cell = c0 + warp + (x + lane) * kWarps;
-                pages = x + lane < mine ? kv4_page(c, s.row, cell >> shift) : 0;
-                if (pages < 0)
-                    kv4_bad(c);
+                where = 0;
+                if (x + lane < mine) {
+                    const int page = kv4_page(c, s.row, cell >> shift);
+                    if (page >= 0)
+                        where = (uint64_t)(heads + page * c.page_bytes + (cell & ((1 << shift) - 1)) * Kv4Cell<D>::kBytes);
+                    else
+                        kv4_bad(c);
+                }
             }
-            const int page = __shfl_sync(~0u, pages, x & 31);
-            const int cell = c0 + warp + x * kWarps;
-            have = page >= 0 ? have | 1u << stage_in : have & ~(1u << stage_in);
-            if (lane == 0 && page >= 0) {
-                const uint32_t bar = bars + 8 * stage_in;
-                mbar_arrive_expect_tx(bar, Kv4Cell<D>::kBytes);
-                bulk_load(smem_addr(ring + stage_in * Kv4Cell<D>::kBytes),
-                          c.pool + kv4_cell_offset<D>(c, page, a.layer, head, cell & ((1 << shift) - 1)),
-                          Kv4Cell<D>::kBytes, bar);
+            const uint64_t src = __shfl_sync(~0u, where, x & 31);
+            const uint32_t st = (used + x) % S;
+            have = src ? have | 1u << st : have & ~(1u << st);
+            if (lane == 0 && src) {
+                mbar_arrive_expect_tx(bars + 8 * st, Kv4Cell<D>::kBytes);
+                bulk_load(rings + st * Kv4Cell<D>::kBytes, (const void *)src, Kv4Cell<D>::kBytes, bars + 8 * st);
+            } else if (lane == 0) {
+                kv4_arrive(bars + 8 * st);
             }
-            stage_in = stage_in + 1 == S ? 0 : stage_in + 1;
         };
-        // stages start at 0 with each piece
         for (int x = 0; x < S - 1 && x < mine; ++x)
             fetch(x);
 
@@ -343,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             // but for parts below 2^-24 of it
             uint32_t e2 = (__float_as_uint(top) >> 23) & 0xFFu;
             e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
-            const float down = __uint_as_float((254u - e2) << 23), up = __uint_as_float(e2 << 23);
+            const float up = __uint_as_float(e2 << 23); // the sign of the scale goes with q
+            const float down = a.scale < 0.0f ? -__uint_as_float((254u - e2) << 23) : __uint_as_float((254u - e2) << 23);
             float sums[G];
 #pragma unroll
             for (int e = 0; e < G; ++e) {
@@ -366,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                     }
             }
             if (t == 0)
-                sm_info[8 * j + g] = RowInfo{up * (a.scale * kLog2e), sums[0], sums[G - 1],
+                sm_info[8 * j + g] = RowInfo{fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f), sums[0], sums[G - 1],
                                              real ? s.len - s.n_new + (int)(row / a.ratio) + 1 : 0};
         }
         __syncthreads();
@@ -386,24 +402,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         }
 
         float o[NT][G][4][4] = {}; // [n-tile][group][m-tile][fragment]
-        float m[NT][2], l[NT][2];
+        // mo = kShift - m, the running maximum; before the first score so large that any raises m
+        float mo[NT][2], l[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-            m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.0f;
+            mo[j][0] = mo[j][1] = kNone, l[j][0] = l[j][1] = 0.0f;
 
-        int stage = 0;
 #pragma unroll 1
         for (int x = 0; x < mine; ++x) {
             if (x + S - 1 < mine) {
                 __syncwarp(); // the stage that is filled now was read by all lanes
                 fetch(x + S - 1);
             }
-            const int st = stage;
-            stage = stage + 1 == S ? 0 : stage + 1;
+            const uint32_t st = (used + x) % S;
+            kv4_wait(bars + 8 * st, ((used + x) / S) & 1, c.status, dead);
             if (!(have >> st & 1))
                 continue;
-            kv4_wait(bars + 8 * st, phase >> st & 1, c.status, dead);
-            phase ^= 1u << st;
             const uint8_t *cell_at = ring + st * Kv4Cell<D>::kBytes;
             const int tok = (c0 + warp + x * kWarps) * kKv4Cell;
 
@@ -448,28 +462,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                         }
                 }
             }
-            bool above = false;
+            if (tok + kKv4Cell > tile_first) { // a row of the tile may see no more than part of the cell
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][f & 1] : sm_info[8 * j + 2 * t + (f & 1)];
+                        sc[j][f] = tok + g + 8 * (f >> 1) < in.limit ? sc[j][f] : -INFINITY;
+                    }
+            }
+            float top = -INFINITY;
+            float y[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
-                    const int u = f >> 1, n = f & 1;
-                    const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
-                    sc[j][f] = tok + g + 8 * u < in.limit ? sc[j][f] * in.scale : -INFINITY;
-                    above |= sc[j][f] > m[j][n] + kSlack;
+                    const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][f & 1] : sm_info[8 * j + 2 * t + (f & 1)];
+                    y[j][f] = fmaf(sc[j][f], in.scale, mo[j][f & 1]);
+                    top = fmaxf(top, y[j][f]);
                 }
-            if (__any_sync(~0u, above)) {
+            if (__any_sync(~0u, top > kShift + kSlack)) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        float y = fmaxf(m[j][n], fmaxf(sc[j][n], sc[j][n + 2]));
-                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 4));
-                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 8));
-                        y = fmaxf(y, __shfl_xor_sync(~0u, y, 16));
-                        const float by = y == m[j][n] ? 1.0f : exp2_approx(m[j][n] - y);
-                        m[j][n] = y;
+                        const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
+                        float z = fmaxf(sc[j][n], sc[j][n + 2]);
+                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 4));
+                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 8));
+                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 16)) * in.scale;
+                        const float was = mo[j][n], now = z == -INFINITY ? was : fminf(was, kShift - z);
+                        const float by = was == now ? 1.0f : exp2_approx(now - was);
+                        mo[j][n] = now;
                         l[j][n] *= by;
+                        y[j][n] = fmaf(sc[j][n], in.scale, now);
+                        y[j][n + 2] = fmaf(sc[j][n + 2], in.scale, now);
 #pragma unroll
                         for (int e = 0; e < G; ++e)
 #pragma unroll
@@ -485,10 +512,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 float p[4];
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
-                    const int n = f & 1;
-                    const float y = exp2_approx(sc[j][f] - (m[j][n] - kShift));
-                    p[f] = sc[j][f] == -INFINITY ? 0.0f : y;
-                    l[j][n] += p[f];
+                    p[f] = exp2_approx(y[j][f]);
+                    l[j][f & 1] += p[f];
                 }
                 pb[j][0] = transpose8x8(pack_half2(p[0], p[1]));
                 pb[j][1] = transpose8x8(pack_half2(p[2], p[3]));
@@ -528,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 tile(std::integral_constant<int, 3>{});
             }
         }
+        used += mine;
         __syncthreads(); // the rings are read: the parts take their place
 
         // the warp's part to shared memory: rows 2 t, 2 t + 1, channels 64 e + 8 g ..
@@ -541,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 x += __shfl_xor_sync(~0u, x, 16);
                 const int row = 8 * j + 2 * t + n;
                 if (g == 0) {
-                    sm_m[warp * RT + row] = m[j][n];
+                    sm_m[warp * RT + row] = mo[j][n] == kNone ? -INFINITY : kShift - mo[j][n];
                     sm_l[warp * RT + row] = x;
                 }
                 float *dst = sm_o + (warp * RT + row) * SM::kPitch + 8 * g;
@@ -572,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         const bool whole = c0 == 0 && c1 == cells;
         float *part = nullptr;
         if (!whole)
-            part = a.partials + ((int64_t)blockIdx.x * 2 + (pos == lo ? 0 : 1)) * part_floats<D, NT>();
+            part = a.partials + ((int64_t)blockIdx.x * 2 + (c0 > 0 ? 0 : 1)) * part_floats<D, NT>();
         for (int x = tid; x < RT * (D / 4); x += kThreads) {
             const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
             float M = -INFINITY, L = 0.0f;
@@ -603,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         }
         if (!whole) {
             // the segment's CTAs are first .. last; the last one to arrive joins their parts in order
-            const int first = (int)(seg_lo / share), last = (int)((seg_hi - 1) / share);
+            const int first = (int)((seg_lo + over) / share), last = (int)((seg_hi - 1) / share);
             __syncthreads();
             if (tid == 0) {
                 const uint32_t n = (uint32_t)(last - first);
@@ -614,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             __syncthreads();
             if (s_last) {
                 const auto at = [&](int k) {
-                    return a.partials + ((int64_t)k * 2 + (k > first || seg_lo == (int64_t)first * share ? 0 : 1)) *
+                    return a.partials + ((int64_t)k * 2 + (k > first ? 0 : 1)) *
                                             part_floats<D, NT>();
                 };
                 for (int x = tid; x < RT * (D / 4); x += kThreads) {

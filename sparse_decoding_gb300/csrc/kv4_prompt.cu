@@ -178,10 +178,6 @@ template <int N> __device__ __forceinline__ void setmaxnreg_dec()
 // kind::f16, A and B fp16 and K-major, D fp32, M = 128.
 template <int N> constexpr uint32_t kIdesc = (1u << 4) | ((N >> 3) << 17) | ((128 >> 4) << 24);
 
-__device__ __forceinline__ void arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -515,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         const Piece w = sh.piece[p % kRing];
         __syncwarp();
         if (lane == 0)
-            arrive(smem_addr(&sh.piece_empty[p % kRing]));
+            kv4_arrive(smem_addr(&sh.piece_empty[p % kRing]));
         return w;
     };
 
@@ -580,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             sts128(e_row + (flip << 4), ext[0], ext[1], 0, 0);
             sts128(e_row + ((flip ^ 1) << 4), 0, 0, 0, 0);
             fence_proxy_async_smem();
-            arrive(smem_addr(&sh.q_full[k]));
+            kv4_arrive(smem_addr(&sh.q_full[k]));
             return fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f); // above 0, so that masked scores stay -inf
         };
 
@@ -771,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 l += x + y;
                 wait_st();
                 fence_before();
-                arrive(smem_addr(&sh.p_full[k]));
+                kv4_arrive(smem_addr(&sh.p_full[k]));
             }
 
             done = w;
@@ -803,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     wait(sh.k_empty[st], (n >> 1) - 1);
                 unpack_k<D>(rk, tiles + C::kOffK + st * C::kQ, u);
                 fence_proxy_async_smem();
-                arrive(smem_addr(&sh.k_full[st]));
+                kv4_arrive(smem_addr(&sh.k_full[st]));
             }
             uint32_t place = ~0u;
             if (more) {
@@ -818,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     wait(sh.v_empty[st], (n >> 1) - 1);
                 unpack_v<D>(rv, tiles + C::kOffV + st * C::kV, u, left);
                 fence_proxy_async_smem();
-                arrive(smem_addr(&sh.v_full[st]));
+                kv4_arrive(smem_addr(&sh.v_full[st]));
             }
             if (!more)
                 break;
@@ -878,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 if (p >= kRing)
                     wait(sh.piece_empty[p % kRing], p / kRing - 1);
                 sh.piece[p % kRing] = w;
-                arrive(smem_addr(&sh.piece_full[p % kRing]));
+                kv4_arrive(smem_addr(&sh.piece_full[p % kRing]));
                 if (w.nblk == 0)
                     break;
             }
