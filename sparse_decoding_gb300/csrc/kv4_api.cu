@@ -54,7 +54,7 @@ nm_status view(const nm_kv4_cache *k, Kv4 *c, Kv4Work *w, int *num_sms)
         sms[dev] = n;
     }
     *num_sms = sms[dev];
-    if (2 * *num_sms > (int)kKv4Counters / 2)
+    if (2 * *num_sms > (int)kKv4Counters / 4)
         return NM_ERR_UNSUPPORTED;
     c->pool = (uint8_t *)k->pool;
     c->n_pages = k->n_pages;

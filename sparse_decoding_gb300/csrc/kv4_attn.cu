@@ -2,8 +2,8 @@
 // steps and drafted tokens).
 //
 // For one sequence and kv head, the rows are its queries times the query heads
-// that share the kv head; a tile holds 8 NT of them. A warp takes the cache one
-// cell (16 tokens) at a time:
+// that share the kv head; a tile holds 8 NT of them. A warp takes the cache two
+// cells (16 tokens each) at a time:
 //
 //   S^T [16 tokens][rows] = codes(K) Q^T      m16n8k16, A = codes - 8 as fp16
 //   s = (scale_t S^T + mid_t sum(q)) per group of 64 channels, in fp32
@@ -14,12 +14,12 @@
 // scale is applied in fp32, so scores carry fp32 rounding only. V's values are
 // rounded once to fp16 (2^-11), like the weights p. m is raised only when a score
 // passes it by 2^8 (p <= 2^14 stays inside fp16, and weights down to 2^-30 of
-// the largest keep a digit): the warp votes per cell instead of reducing.
+// the largest keep a digit): the warp votes instead of reducing.
 //
 // The layout of a cell is the operands' own: lane l reads 16 bytes at 16 l, so K
 // and V need no transposition on the way to the registers.
 //
-// The cells of all (sequence, kv head, tile) segments are one line, cut evenly
+// The units (pairs of cells) of all (sequence, kv head, tile) segments are one line, cut evenly
 // over the CTAs of one wave, whatever the lengths; a CTA's warps take the cells of
 // a piece in turn and are joined in shared memory. A segment that was cut is
 // joined by the last of its CTAs, in CTA order, from the workspace.
@@ -33,9 +33,11 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int64_t kMinShare = 16; // cells of a CTA at least: two for each warp
-constexpr int kWholeCells = 32;   // segments of up to so many cells are not cut
-constexpr int kOver = 16;         // cells that starting and ending a piece costs as much as
+constexpr int kUnit = 2;          // cells that a warp takes at a time
+constexpr int kTokens = kUnit * kKv4Cell;
+constexpr int64_t kMinShare = 8;  // units of a CTA at least: one for each warp
+constexpr int kWhole = 16;        // segments of up to so many units are not cut
+constexpr int kOver = 8;          // units that starting and ending a piece costs as much as
 constexpr float kShift = 6.0f;    // p = 2^(s - m + kShift)
 constexpr float kSlack = 8.0f;    // a score may pass m by this much
 constexpr float kNone = 1e38f;
@@ -185,17 +187,22 @@ struct RowInfo {
 template <int D, int NT> struct Smem {
     static constexpr int kRows = 8 * NT;
     static constexpr int kPitch = D + 4;
-    static constexpr int kStages = NT == 1 ? 4 : 8; // cells of a warp in flight or in use
+    static constexpr int kStages = NT == 1 ? 2 : 4; // units of a warp in flight or in use
+    static constexpr int kStage = kUnit * Kv4Cell<D>::kBytes;
+    // Rows of one n-tile leave room for both cells of a unit at once; otherwise one after the other.
+    static constexpr int kAtOnce = NT == 1 ? 2 : 1;
     static constexpr int kSteps = D / 16;
     // the warps' rings; when a piece is done, the warps' parts (m, l, O) in their place
-    static constexpr int kRing = kWarps * kStages * Kv4Cell<D>::kBytes;
+    static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kMerge = kWarps * kRows * (2 + kPitch) * 4;
-    static constexpr int kBig = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kJoin = (kKv4Counters / 4 * kRows + 2 * kRows) * 4; // weights of the parts of a segment
+    static constexpr int kBig = kRing > kMerge ? (kRing > kJoin ? kRing : kJoin) : (kMerge > kJoin ? kMerge : kJoin);
     // Q in B fragments: [n-tile][k-step][lane][2], then the rows' RowInfo
     static constexpr int kQ = kBig, kInfo = kQ + NT * kSteps * 256, kBars = kInfo + kRows * 16;
     static constexpr int kSeqs = kBars + kWarps * kStages * 8;
 };
 
+__device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + kTokens - 1) / kTokens : 1; }
 __device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <int D, int NT>
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     constexpr int RT = 8 * NT;
     constexpr int KS = 4 * G; // k-steps of 16 channels
     using SM = Smem<D, NT>;
-    constexpr int S = SM::kStages;
+    constexpr int S = SM::kStages, U = SM::kAtOnce;
     extern __shared__ __align__(128) uint8_t smem[];
     float *const sm_m = (float *)smem, *const sm_l = sm_m + kWarps * RT, *const sm_o = sm_l + kWarps * RT;
     uint2 *const sm_q = (uint2 *)(smem + SM::kQ);
@@ -215,10 +222,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     Kv4Seq *const seqs = (Kv4Seq *)(pre + b.n_seqs + 1);     // [n_seqs]
     __shared__ uint32_t s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    uint8_t *const ring = smem + warp * S * Kv4Cell<D>::kBytes;
+    uint8_t *const ring = smem + warp * S * SM::kStage;
     const uint32_t rings = smem_addr(ring), bars = smem_addr(smem + SM::kBars) + warp * S * 8;
 
-    // the segments of each sequence, and where they start on the line of cells
+    // the segments of each sequence, and where they start on the line of units
     if (lane == 0)
         for (int i = 0; i < S; ++i)
             mbar_init(bars + 8 * i, 1);
@@ -227,21 +234,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     for (int i = tid; i < b.n_seqs; i += kThreads) {
         const Kv4Seq s = kv4_seq(c, b, i, blockIdx.x == 0);
         seqs[i] = s;
-        const int cells = s.n_new == 0 ? 0 : s.len > 0 ? (s.len + kKv4Cell - 1) / kKv4Cell : 1;
-        longest = max(longest, cells);
+        longest = max(longest, s.n_new == 0 ? 0 : units_of(s.len));
         pre[i + 1] = ceil_div((int64_t)s.n_new * a.ratio, RT) * c.n_kv_heads;
     }
-    // Short sequences are not cut: a segment is one step of the line, not one per cell.
-    const bool cut = __syncthreads_or(longest > kWholeCells);
+    // Short sequences are not cut: a segment is one step of the line, not one per unit.
+    const bool cut = __syncthreads_or(longest > kWhole);
     if (warp == 0) {
         int64_t sum = 0;
         for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
             int64_t x = 0;
             if (i0 + lane < b.n_seqs) {
                 x = pre[i0 + lane + 1];
-                const int len = seqs[i0 + lane].len;
                 if (cut)
-                    x *= kOver + (len > 0 ? (len + kKv4Cell - 1) / kKv4Cell : 1);
+                    x *= kOver + units_of(seqs[i0 + lane].len);
             }
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(~0u, x, o);
@@ -280,33 +285,34 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             i = l;
         }
         const Kv4Seq s = seqs[i];
-        const int cells = s.len > 0 ? (s.len + kKv4Cell - 1) / kKv4Cell : 1;
-        // A segment that may be cut has kOver steps of the line before its cells' own.
-        const int over = cut ? kOver : 0, per = cut ? kOver + cells : 1;
+        const int units = units_of(s.len);
+        // A segment that may be cut has kOver steps of the line before its units' own.
+        const int over = cut ? kOver : 0, per = cut ? kOver + units : 1;
         const int64_t seg = (pos - pre[i]) / per;
         const int64_t seg_lo = pre[i] + seg * per, seg_hi = seg_lo + per;
         const int steps = (int)((hi < seg_hi ? hi : seg_hi) - pos);
         const int from = (int)(pos - seg_lo) - over;
-        const int c0 = cut && from > 0 ? from : 0, c1 = cut ? from + steps : cells;
+        const int c0 = cut && from > 0 ? from : 0, c1 = cut ? from + steps : units;
         if (c1 <= c0)
-            break; // the CTA's part of the line ends before the segment's first cell
+            break; // the CTA's part of the line ends before the segment's first unit
         const int64_t rows = (int64_t)s.n_new * a.ratio; // rows of the sequence and kv head
         const int64_t tiles = ceil_div(rows, RT);
         const int head = (int)(seg / tiles);
         const int64_t row0 = (seg % tiles) * RT; // first row of the tile
         const int tile_first = s.len - s.n_new + (int)(row0 / a.ratio) + 1; // tokens that its first row attends
 
-        // The warp's cells are c0 + warp, + kWarps, ... A lane holds the address of every 32nd
-        // (0: its page is none of the pool's); `have` has a bit for each stage that was filled.
+        // The warp's units are c0 + warp, + kWarps, ... Lanes 2 n, 2 n + 1 hold the addresses of the
+        // cells of every 16th (0: its page is none of the pool's, or it is past the sequence's end);
+        // `have` has a bit for each cell of a stage that was filled.
         const int mine = s.len > 0 && c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
         const uint8_t *const heads = c.pool + kv4_cell_offset<D>(c, 0, a.layer, head, 0);
         uint64_t where = 0;
         uint32_t have = 0;
         const auto fetch = [&](int x) {
-            if ((x & 31) == 0) {
-                const int cell = c0 + warp + (x + lane) * kWarps;
+            if ((x & 15) == 0) {
+                const int cell = kUnit * (c0 + warp + (x + (lane >> 1)) * kWarps) + (lane & 1);
                 where = 0;
-                if (x + lane < mine) {
+                if (x + (lane >> 1) < mine && cell * kKv4Cell < s.len) {
                     const int page = kv4_page(c, s.row, cell >> shift);
                     if (page >= 0)
                         where = (uint64_t)(heads + page * c.page_bytes + (cell & ((1 << shift) - 1)) * Kv4Cell<D>::kBytes);
@@ -314,17 +320,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                         kv4_bad(c);
                 }
             }
-            const uint64_t src = __shfl_sync(~0u, where, x & 31);
-            const uint32_t st = (used + x) % S;
-            have = src ? have | 1u << st : have & ~(1u << st);
-            if (lane == 0 && src) {
-                mbar_arrive_expect_tx(bars + 8 * st, Kv4Cell<D>::kBytes);
-                bulk_load(rings + st * Kv4Cell<D>::kBytes, (const void *)src, Kv4Cell<D>::kBytes, bars + 8 * st);
-            } else if (lane == 0) {
-                kv4_arrive(bars + 8 * st);
-            }
+            const uint64_t src = __shfl_sync(~0u, where, 2 * (x & 15) + (lane & 1));
+            const uint32_t st = (used + x) % S, bar = bars + 8 * st;
+            const uint32_t both = __ballot_sync(~0u, src != 0) & 3u;
+            have = (have & ~(3u << (2 * st))) | both << (2 * st);
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, __popc(both) * Kv4Cell<D>::kBytes);
+            __syncwarp();
+            if (lane < kUnit && src)
+                bulk_load(rings + st * SM::kStage + lane * Kv4Cell<D>::kBytes, (const void *)src, Kv4Cell<D>::kBytes, bar);
         };
-        for (int x = 0; x < S - 1 && x < mine; ++x)
+        for (int x = 0; x < (S > 2 ? S - 1 : S) && x < mine; ++x)
             fetch(x);
 
         // Q as the B operand: warp j makes n-tile j; row g, channels 64 e + 16 t ..
@@ -410,147 +416,176 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 
 #pragma unroll 1
         for (int x = 0; x < mine; ++x) {
-            if (x + S - 1 < mine) {
+            if (S > 2 && x + S - 1 < mine) {
                 __syncwarp(); // the stage that is filled now was read by all lanes
                 fetch(x + S - 1);
             }
             const uint32_t st = (used + x) % S;
             kv4_wait(bars + 8 * st, ((used + x) / S) & 1, c.status, dead);
-            if (!(have >> st & 1))
-                continue;
-            const uint8_t *cell_at = ring + st * Kv4Cell<D>::kBytes;
-            const int tok = (c0 + warp + x * kWarps) * kKv4Cell;
+            const uint32_t filled = have >> (2 * st) & 3u;
+#pragma unroll 1
+            for (int v0 = 0; v0 < kUnit; v0 += U) {
+                const uint8_t *const cell_at = ring + st * SM::kStage + v0 * Kv4Cell<D>::kBytes;
+                const int tok = (c0 + warp + x * kWarps) * kTokens + v0 * kKv4Cell;
 
-            // scores
-            float sc[NT][4];
-            {
-                CellK<D> r;
-                lds_k<D>(r, cell_at, lane);
+                // scores
+                float sc[U][NT][4];
 #pragma unroll
-                for (int e = 0; e < G; ++e) {
-                    float acc[NT][4] = {};
+                for (int v = 0; v < U; ++v) {
+                    CellK<D> r;
+                    lds_k<D>(r, cell_at + v * Kv4Cell<D>::kBytes, lane);
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        uint32_t af[2][4];
-                        const uint32_t w0 = r.w[0][2 * e + f], w1 = r.w[1][2 * e + f];
-                        af[0][0] = as_u32(nibble<0>(w0, 8.0f));
-                        af[0][1] = as_u32(nibble<0>(w1, 8.0f));
-                        af[0][2] = as_u32(nibble<1>(w0, 8.0f));
-                        af[0][3] = as_u32(nibble<1>(w1, 8.0f));
-                        af[1][0] = as_u32(nibble<2>(w0, 8.0f));
-                        af[1][1] = as_u32(nibble<2>(w1, 8.0f));
-                        af[1][2] = as_u32(nibble<3>(w0, 8.0f));
-                        af[1][3] = as_u32(nibble<3>(w1, 8.0f));
+                    for (int e = 0; e < G; ++e) {
+                        float acc[NT][4] = {};
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        for (int f = 0; f < 2; ++f) {
+                            uint32_t af[2][4];
+                            const uint32_t w0 = r.w[0][2 * e + f], w1 = r.w[1][2 * e + f];
+                            af[0][0] = as_u32(nibble<0>(w0, 8.0f));
+                            af[0][1] = as_u32(nibble<0>(w1, 8.0f));
+                            af[0][2] = as_u32(nibble<1>(w0, 8.0f));
+                            af[0][3] = as_u32(nibble<1>(w1, 8.0f));
+                            af[1][0] = as_u32(nibble<2>(w0, 8.0f));
+                            af[1][1] = as_u32(nibble<2>(w1, 8.0f));
+                            af[1][2] = as_u32(nibble<3>(w0, 8.0f));
+                            af[1][3] = as_u32(nibble<3>(w1, 8.0f));
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                const int z = 4 * e + 2 * f + h;
-                                const uint2 q = kKeepQ ? qb[j % (kKeepQ ? NT : 1)][z] : sm_q[(j * KS + z) * 32 + lane];
-                                mma16816(acc[j], af[h], q.x, q.y);
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int j = 0; j < NT; ++j) {
+                                    const int z = 4 * e + 2 * f + h;
+                                    const uint2 q = kKeepQ ? qb[j % (kKeepQ ? NT : 1)][z] : sm_q[(j * KS + z) * 32 + lane];
+                                    mma16816(acc[j], af[h], q.x, q.y);
+                                }
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) {
+                                const int u = f >> 1, n = f & 1; // token g + 8 u, row 2 t + n
+                                const RowInfo &in =
+                                    kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
+                                const float ks = __low2float(as_half2(r.p[u][e])), km = __high2float(as_half2(r.p[u][e]));
+                                const float z = fmaf(km, e ? in.q1 : in.q0, e ? sc[v][j][f] : 0.0f);
+                                sc[v][j][f] = fmaf(ks, acc[j][f], z);
                             }
                     }
+                }
+                // a row may see only part of the cells, or a cell may not be there
+                if (tok + U * kKv4Cell > tile_first || filled != 3u) {
+#pragma unroll
+                    for (int v = 0; v < U; ++v)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) {
+                                const RowInfo &in =
+                                    kKeepQ ? info[j % (kKeepQ ? NT : 1)][f & 1] : sm_info[8 * j + 2 * t + (f & 1)];
+                                const bool sees = tok + v * kKv4Cell + g + 8 * (f >> 1) < in.limit && filled >> (v0 + v) & 1;
+                                sc[v][j][f] = sees ? sc[v][j][f] : -INFINITY;
+                            }
+                }
+                float top = -INFINITY;
+                float y[U][NT][4];
+#pragma unroll
+                for (int v = 0; v < U; ++v)
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int f = 0; f < 4; ++f) {
-                            const int u = f >> 1, n = f & 1; // token g + 8 u, row 2 t + n
-                            const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
-                            const float ks = __low2float(as_half2(r.p[u][e])), km = __high2float(as_half2(r.p[u][e]));
-                            const float y = fmaf(ks, acc[j][f], km * (e ? in.q1 : in.q0));
-                            sc[j][f] = e ? sc[j][f] + y : y;
+                            const RowInfo &in =
+                                kKeepQ ? info[j % (kKeepQ ? NT : 1)][f & 1] : sm_info[8 * j + 2 * t + (f & 1)];
+                            y[v][j][f] = fmaf(sc[v][j][f], in.scale, mo[j][f & 1]);
+                            top = fmaxf(top, y[v][j][f]);
                         }
-                }
-            }
-            if (tok + kKv4Cell > tile_first) { // a row of the tile may see no more than part of the cell
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][f & 1] : sm_info[8 * j + 2 * t + (f & 1)];
-                        sc[j][f] = tok + g + 8 * (f >> 1) < in.limit ? sc[j][f] : -INFINITY;
-                    }
-            }
-            float top = -INFINITY;
-            float y[NT][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][f & 1] : sm_info[8 * j + 2 * t + (f & 1)];
-                    y[j][f] = fmaf(sc[j][f], in.scale, mo[j][f & 1]);
-                    top = fmaxf(top, y[j][f]);
-                }
-            if (__any_sync(~0u, top > kShift + kSlack)) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
-                        float z = fmaxf(sc[j][n], sc[j][n + 2]);
-                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 4));
-                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 8));
-                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 16)) * in.scale;
-                        const float was = mo[j][n], now = z == -INFINITY ? was : fminf(was, kShift - z);
-                        const float by = was == now ? 1.0f : exp2_approx(now - was);
-                        mo[j][n] = now;
-                        l[j][n] *= by;
-                        y[j][n] = fmaf(sc[j][n], in.scale, now);
-                        y[j][n + 2] = fmaf(sc[j][n + 2], in.scale, now);
-#pragma unroll
-                        for (int e = 0; e < G; ++e)
-#pragma unroll
-                            for (int i4 = 0; i4 < 4; ++i4) {
-                                o[j][e][i4][n] *= by;
-                                o[j][e][i4][n + 2] *= by;
-                            }
-                    }
-            }
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float p[4];
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    p[f] = exp2_approx(y[j][f]);
-                    l[j][f & 1] += p[f];
-                }
-                pb[j][0] = transpose8x8(pack_half2(p[0], p[1]));
-                pb[j][1] = transpose8x8(pack_half2(p[2], p[3]));
-            }
-
-            // O^T += V^T P^T; tokens past the sequence's end hold anything: their V is taken as 0
-            CellV<D> r;
-            lds_v<D>(r, cell_at, lane);
-            if (tok + kKv4Cell > s.len) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int first = tok + 8 * u + 2 * t;
-                    const uint32_t keep = (first < s.len ? 0x0000FFFFu : 0u) | (first + 1 < s.len ? 0xFFFF0000u : 0u);
-#pragma unroll
-                    for (int e = 0; e < 2 * G; ++e)
-                        r.p[u][e] &= keep;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < G; ++e) {
-                const __half2 s0 = as_half2(r.p[0][2 * e]), m0 = as_half2(r.p[0][2 * e + 1]);
-                const __half2 s1 = as_half2(r.p[1][2 * e]), m1 = as_half2(r.p[1][2 * e + 1]);
-                const auto tile = [&](auto nib) {
-                    constexpr int N = decltype(nib)::value;
-                    uint32_t af[4];
-                    af[0] = as_u32(__hfma2(nibble<N>(r.w[e][0], 8.0f), s0, m0));
-                    af[1] = as_u32(__hfma2(nibble<N>(r.w[e][1], 8.0f), s0, m0));
-                    af[2] = as_u32(__hfma2(nibble<N>(r.w[e][2], 8.0f), s1, m1));
-                    af[3] = as_u32(__hfma2(nibble<N>(r.w[e][3], 8.0f), s1, m1));
+                if (__any_sync(~0u, top > kShift + kSlack)) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
-                        mma16816(o[j][e][N], af, pb[j][0], pb[j][1]);
-                };
-                tile(std::integral_constant<int, 0>{});
-                tile(std::integral_constant<int, 1>{});
-                tile(std::integral_constant<int, 2>{});
-                tile(std::integral_constant<int, 3>{});
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
+                            float z = -INFINITY;
+#pragma unroll
+                            for (int v = 0; v < U; ++v)
+                                z = fmaxf(z, fmaxf(sc[v][j][n], sc[v][j][n + 2]));
+                            z = fmaxf(z, __shfl_xor_sync(~0u, z, 4));
+                            z = fmaxf(z, __shfl_xor_sync(~0u, z, 8));
+                            z = fmaxf(z, __shfl_xor_sync(~0u, z, 16)) * in.scale;
+                            const float was = mo[j][n], now = z == -INFINITY ? was : fminf(was, kShift - z);
+                            const float by = was == now ? 1.0f : exp2_approx(now - was);
+                            mo[j][n] = now;
+                            l[j][n] *= by;
+#pragma unroll
+                            for (int v = 0; v < U; ++v) {
+                                y[v][j][n] = fmaf(sc[v][j][n], in.scale, now);
+                                y[v][j][n + 2] = fmaf(sc[v][j][n + 2], in.scale, now);
+                            }
+#pragma unroll
+                            for (int e = 0; e < G; ++e)
+#pragma unroll
+                                for (int i4 = 0; i4 < 4; ++i4) {
+                                    o[j][e][i4][n] *= by;
+                                    o[j][e][i4][n + 2] *= by;
+                                }
+                        }
+                }
+                uint32_t pb[U][NT][2];
+#pragma unroll
+                for (int v = 0; v < U; ++v)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        float p[4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            p[f] = exp2_approx(y[v][j][f]);
+                            l[j][f & 1] += p[f];
+                        }
+                        pb[v][j][0] = transpose8x8(pack_half2(p[0], p[1]));
+                        pb[v][j][1] = transpose8x8(pack_half2(p[2], p[3]));
+                    }
+
+                // O^T += V^T P^T; tokens past the sequence's end, and cells that are not there, hold
+                // anything: their V is taken as 0
+#pragma unroll
+                for (int v = 0; v < U; ++v) {
+                    CellV<D> r;
+                    lds_v<D>(r, cell_at + v * Kv4Cell<D>::kBytes, lane);
+                    const int end = filled >> (v0 + v) & 1 ? s.len - (tok + v * kKv4Cell) : 0; // tokens of the cell
+                    if (end < kKv4Cell) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int first = 8 * u + 2 * t;
+                            const uint32_t keep = (first < end ? 0x0000FFFFu : 0u) | (first + 1 < end ? 0xFFFF0000u : 0u);
+#pragma unroll
+                            for (int e = 0; e < 2 * G; ++e)
+                                r.p[u][e] &= keep;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < G; ++e) {
+                        const __half2 s0 = as_half2(r.p[0][2 * e]), m0 = as_half2(r.p[0][2 * e + 1]);
+                        const __half2 s1 = as_half2(r.p[1][2 * e]), m1 = as_half2(r.p[1][2 * e + 1]);
+                        const auto tile = [&](auto nib) {
+                            constexpr int N = decltype(nib)::value;
+                            uint32_t af[4];
+                            af[0] = as_u32(__hfma2(nibble<N>(r.w[e][0], 8.0f), s0, m0));
+                            af[1] = as_u32(__hfma2(nibble<N>(r.w[e][1], 8.0f), s0, m0));
+                            af[2] = as_u32(__hfma2(nibble<N>(r.w[e][2], 8.0f), s1, m1));
+                            af[3] = as_u32(__hfma2(nibble<N>(r.w[e][3], 8.0f), s1, m1));
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+                                mma16816(o[j][e][N], af, pb[v][j][0], pb[v][j][1]);
+                        };
+                        tile(std::integral_constant<int, 0>{});
+                        tile(std::integral_constant<int, 1>{});
+                        tile(std::integral_constant<int, 2>{});
+                        tile(std::integral_constant<int, 3>{});
+                    }
+                }
+            }
+            if (S == 2 && x + S < mine) {
+                __syncwarp(); // every lane has read the stage that is filled again
+                fetch(x + S);
             }
         }
         used += mine;
@@ -595,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             if (a.lse && ch == 0)
                 a.lse[token * a.n_q_heads + h] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * kLn2;
         };
-        const bool whole = c0 == 0 && c1 == cells;
+        const bool whole = c0 == 0 && c1 == units;
         float *part = nullptr;
         if (!whole)
             part = a.partials + ((int64_t)blockIdx.x * 2 + (c0 > 0 ? 0 : 1)) * part_floats<D, NT>();
@@ -639,29 +674,52 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             }
             __syncthreads();
             if (s_last) {
+                // weights of the parts first (a warp to a row), then their O: independent loads in a row
+                const int n = last - first + 1;
+                float *const weight = (float *)smem; // [n][RT], then [RT] M, [RT] L
+                float *const sum_m = weight + n * RT, *const sum_l = sum_m + RT;
                 const auto at = [&](int k) {
-                    return a.partials + ((int64_t)k * 2 + (k > first ? 0 : 1)) *
-                                            part_floats<D, NT>();
+                    return a.partials + ((int64_t)(first + k) * 2 + (k > 0 ? 0 : 1)) * part_floats<D, NT>();
                 };
+                for (int row = warp; row < RT; row += kWarps) {
+                    float M = -INFINITY, L = 0.0f;
+                    for (int k = lane; k < n; k += 32)
+                        M = fmaxf(M, ldcg_f32(at(k) + row));
+                    for (int z = 16; z; z >>= 1)
+                        M = fmaxf(M, __shfl_xor_sync(~0u, M, z));
+                    for (int k = lane; k < n; k += 32) {
+                        const float mk = ldcg_f32(at(k) + row);
+                        const float f = mk == M ? 1.0f : exp2_approx(mk - M);
+                        weight[k * RT + row] = f;
+                        L = fmaf(f, ldcg_f32(at(k) + RT + row), L);
+                    }
+                    for (int z = 16; z; z >>= 1)
+                        L += __shfl_xor_sync(~0u, L, z);
+                    if (lane == 0) {
+                        sum_m[row] = M;
+                        sum_l[row] = L;
+                    }
+                }
+                __syncthreads();
                 for (int x = tid; x < RT * (D / 4); x += kThreads) {
                     const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
-                    float M = -INFINITY, L = 0.0f;
-                    for (int k = first; k <= last; ++k)
-                        M = fmaxf(M, ldcg_f32(at(k) + row));
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int k = first; k <= last; ++k) {
-                        const float *p = at(k);
-                        const float mk = ldcg_f32(p + row);
-                        const float f = mk == M ? 1.0f : exp2_approx(mk - M);
-                        const float4 z = __ldcg((const float4 *)(p + 2 * RT + row * D + ch));
-                        L = fmaf(f, ldcg_f32(p + RT + row), L);
-                        y.x = fmaf(f, z.x, y.x);
-                        y.y = fmaf(f, z.y, y.y);
-                        y.z = fmaf(f, z.z, y.z);
-                        y.w = fmaf(f, z.w, y.w);
+                    for (int k0 = 0; k0 < n; k0 += 8) {
+                        float4 z[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            z[k] = k0 + k < n ? __ldcg((const float4 *)(at(k0 + k) + 2 * RT + row * D + ch))
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float f = k0 + k < n ? weight[(k0 + k) * RT + row] : 0.0f;
+                            y.x = fmaf(f, z[k].x, y.x);
+                            y.y = fmaf(f, z[k].y, y.y);
+                            y.z = fmaf(f, z[k].z, y.z);
+                            y.w = fmaf(f, z[k].w, y.w);
+                        }
                     }
-                    store(row, ch, y, M, L);
+                    store(row, ch, y, sum_m[row], sum_l[row]);
                 }
             }
         }
@@ -684,7 +742,7 @@ template <int D, int NT> nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, 
     if (attr != cudaSuccess)
         return NM_ERR_CUDA;
     const size_t smem = Smem<D, NT>::kSeqs + (size_t)(b.n_seqs + 1) * 8 + (size_t)b.n_seqs * sizeof(Kv4Seq);
-    const unsigned grid = (unsigned)(num_sms * (NT == 1 ? 2 : 1));
+    const unsigned grid = (unsigned)(num_sms * (NT == 1 ? 2 : 1)); // at most kKv4Counters / 4
     attn_rows_kernel<D, NT><<<grid, kThreads, smem, st>>>(c, b, a);
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
