@@ -6,7 +6,8 @@
 // cells (16 tokens each) at a time:
 //
 //   S^T [16 tokens][rows] = codes(K) Q^T      m16n8k16, A = codes - 8 as fp16
-//   s = (scale_t S^T + mid_t sum(q)) per group of 64 channels, in fp32
+//   s = scale_t S^T + mid_t sum(q) over the groups of 64 channels, in fp32 (the
+//                                   middles as one more product, of k = 8)
 //   p = 2^(s - m + 6)                         m: the row's running maximum
 //   O^T [channels][rows] += V^T P^T           A = V as fp16, B = P as fp16
 //
@@ -50,6 +51,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  "{%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b)
+{
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(b));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
@@ -177,17 +184,16 @@ struct AttnArgs {
 // Floats of one part in the workspace: m and l of each row, then O.
 template <int D, int NT> constexpr int part_floats() { return 8 * NT * (D + 2); }
 
-// What the scores of a row need: its factor, the sums of its q per group, and how
-// many tokens it attends.
+// What the scores of a row need: its factor, and how many tokens it attends.
 struct RowInfo {
-    float scale, q0, q1;
+    float scale;
     int limit;
 };
 
 template <int D, int NT> struct Smem {
     static constexpr int kRows = 8 * NT;
     static constexpr int kPitch = D + 4;
-    static constexpr int kStages = NT == 1 ? 2 : 4; // units of a warp in flight or in use
+    static constexpr int kStages = NT <= 2 ? 2 : 4; // units of a warp in flight or in use
     static constexpr int kStage = kUnit * Kv4Cell<D>::kBytes;
     // Rows of one n-tile leave room for both cells of a unit at once; otherwise one after the other.
     static constexpr int kAtOnce = NT == 1 ? 2 : 1;
@@ -197,8 +203,8 @@ template <int D, int NT> struct Smem {
     static constexpr int kMerge = kWarps * kRows * (2 + kPitch) * 4;
     static constexpr int kJoin = (kKv4Counters / 4 * kRows + 2 * kRows) * 4; // weights of the parts of a segment
     static constexpr int kBig = kRing > kMerge ? (kRing > kJoin ? kRing : kJoin) : (kMerge > kJoin ? kMerge : kJoin);
-    // Q in B fragments: [n-tile][k-step][lane][2], then the rows' RowInfo
-    static constexpr int kQ = kBig, kInfo = kQ + NT * kSteps * 256, kBars = kInfo + kRows * 16;
+    // Q in B fragments: [n-tile][k-step][lane][2], the sums of q as one more (of k = 8), then the rows' RowInfo
+    static constexpr int kQ = kBig, kSums = kQ + NT * kSteps * 256, kInfo = kSums + NT * 128, kBars = kInfo + kRows * 8;
     static constexpr int kSeqs = kBars + kWarps * kStages * 8;
 };
 
@@ -206,7 +212,7 @@ __device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + kToke
 __device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
     attn_rows_kernel(const Kv4 c, const Kv4Batch b, const AttnArgs a)
 {
     constexpr int G = Kv4Cell<D>::G;
@@ -217,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     extern __shared__ __align__(128) uint8_t smem[];
     float *const sm_m = (float *)smem, *const sm_l = sm_m + kWarps * RT, *const sm_o = sm_l + kWarps * RT;
     uint2 *const sm_q = (uint2 *)(smem + SM::kQ);
+    uint32_t *const sm_sums = (uint32_t *)(smem + SM::kSums);
     RowInfo *const sm_info = (RowInfo *)(smem + SM::kInfo);
     int64_t *const pre = (int64_t *)(smem + SM::kSeqs);      // [n_seqs + 1]
     Kv4Seq *const seqs = (Kv4Seq *)(pre + b.n_seqs + 1);     // [n_seqs]
@@ -387,24 +394,31 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                             make_uint2(pack_half2(y[0], y[4]), pack_half2(y[1], y[5]));
                     }
             }
+            // the middles of the groups meet the sums of q, in two fp16 parts: k = 0, 1 and k = 2, 3
+            const float h0 = __half2float(__float2half_rn(sums[0]));
+            const float h1 = G == 2 ? __half2float(__float2half_rn(sums[G - 1])) : 0.0f;
+            const float l1 = G == 2 ? sums[G - 1] - h1 : 0.0f;
+            sm_sums[32 * j + lane] = t == 0 ? pack_half2(h0, h1) : t == 1 ? pack_half2(sums[0] - h0, l1) : 0u;
             if (t == 0)
-                sm_info[8 * j + g] = RowInfo{fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f), sums[0], sums[G - 1],
+                sm_info[8 * j + g] = RowInfo{fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f),
                                              real ? s.len - s.n_new + (int)(row / a.ratio) + 1 : 0};
         }
         __syncthreads();
-        // with few rows Q stays in registers
-        constexpr bool kKeepQ = NT <= 2;
-        uint2 qb[kKeepQ ? NT : 1][KS];
-        RowInfo info[kKeepQ ? NT : 1][2];
+        // with one n-tile Q stays in registers
+        constexpr bool kKeepQ = NT == 1;
+        uint2 qb[kKeepQ ? KS : 1];
+        uint32_t qs[NT];
+        float scale[NT][2];
         if (kKeepQ) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
+            for (int x = 0; x < KS; ++x)
+                qb[x % (kKeepQ ? KS : 1)] = sm_q[x * 32 + lane];
+        }
 #pragma unroll
-                for (int x = 0; x < KS; ++x)
-                    qb[j % (kKeepQ ? NT : 1)][x] = sm_q[(j * KS + x) * 32 + lane];
-                info[j % (kKeepQ ? NT : 1)][0] = sm_info[8 * j + 2 * t];
-                info[j % (kKeepQ ? NT : 1)][1] = sm_info[8 * j + 2 * t + 1];
-            }
+        for (int j = 0; j < NT; ++j) {
+            qs[j] = sm_sums[32 * j + lane];
+            scale[j][0] = sm_info[8 * j + 2 * t].scale;
+            scale[j][1] = sm_info[8 * j + 2 * t + 1].scale;
         }
 
         float o[NT][G][4][4] = {}; // [n-tile][group][m-tile][fragment]
@@ -434,6 +448,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                 for (int v = 0; v < U; ++v) {
                     CellK<D> r;
                     lds_k<D>(r, cell_at + v * Kv4Cell<D>::kBytes, lane);
+                    const uint32_t mid0 = G == 2 ? __byte_perm(r.p[0][0], r.p[0][G - 1], 0x7632) : r.p[0][0] >> 16;
+                    const uint32_t mid1 = G == 2 ? __byte_perm(r.p[1][0], r.p[1][G - 1], 0x7632) : r.p[1][0] >> 16;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        sc[v][j][0] = sc[v][j][1] = sc[v][j][2] = sc[v][j][3] = 0.0f;
+                        mma1688(sc[v][j], mid0, mid1, qs[j]);
+                    }
 #pragma unroll
                     for (int e = 0; e < G; ++e) {
                         float acc[NT][4] = {};
@@ -454,21 +475,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
                                 for (int j = 0; j < NT; ++j) {
                                     const int z = 4 * e + 2 * f + h;
-                                    const uint2 q = kKeepQ ? qb[j % (kKeepQ ? NT : 1)][z] : sm_q[(j * KS + z) * 32 + lane];
+                                    const uint2 q = kKeepQ ? qb[z % (kKeepQ ? KS : 1)] : sm_q[(j * KS + z) * 32 + lane];
                                     mma16816(acc[j], af[h], q.x, q.y);
                                 }
                         }
+                        const float k0 = __low2float(as_half2(r.p[0][e])), k1 = __low2float(as_half2(r.p[1][e]));
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
 #pragma unroll
-                            for (int f = 0; f < 4; ++f) {
-                                const int u = f >> 1, n = f & 1; // token g + 8 u, row 2 t + n
-                                const RowInfo &in =
-                                    kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
-                                const float ks = __low2float(as_half2(r.p[u][e])), km = __high2float(as_half2(r.p[u][e]));
-                                const float z = fmaf(km, e ? in.q1 : in.q0, e ? sc[v][j][f] : 0.0f);
-                                sc[v][j][f] = fmaf(ks, acc[j][f], z);
-                            }
+                            for (int f = 0; f < 4; ++f) // token g + 8 (f / 2), row 2 t + f % 2
+                                sc[v][j][f] = fmaf(f < 2 ? k0 : k1, acc[j][f], sc[v][j][f]);
                     }
                 }
                 // a row may see only part of the cells, or a cell may not be there
@@ -479,9 +495,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                         for (int j = 0; j < NT; ++j)
 #pragma unroll
                             for (int f = 0; f < 4; ++f) {
-                                const RowInfo &in =
-                                    kKeepQ ? info[j % (kKeepQ ? NT : 1)][f & 1] : sm_info[8 * j + 2 * t + (f & 1)];
-                                const bool sees = tok + v * kKv4Cell + g + 8 * (f >> 1) < in.limit && filled >> (v0 + v) & 1;
+                                const int limit = sm_info[8 * j + 2 * t + (f & 1)].limit;
+                                const bool sees = tok + v * kKv4Cell + g + 8 * (f >> 1) < limit && filled >> (v0 + v) & 1;
                                 sc[v][j][f] = sees ? sc[v][j][f] : -INFINITY;
                             }
                 }
@@ -493,9 +508,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int f = 0; f < 4; ++f) {
-                            const RowInfo &in =
-                                kKeepQ ? info[j % (kKeepQ ? NT : 1)][f & 1] : sm_info[8 * j + 2 * t + (f & 1)];
-                            y[v][j][f] = fmaf(sc[v][j][f], in.scale, mo[j][f & 1]);
+                            y[v][j][f] = fmaf(sc[v][j][f], scale[j][f & 1], mo[j][f & 1]);
                             top = fmaxf(top, y[v][j][f]);
                         }
                 if (__any_sync(~0u, top > kShift + kSlack)) {
@@ -503,22 +516,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
-                            const RowInfo &in = kKeepQ ? info[j % (kKeepQ ? NT : 1)][n] : sm_info[8 * j + 2 * t + n];
                             float z = -INFINITY;
 #pragma unroll
                             for (int v = 0; v < U; ++v)
                                 z = fmaxf(z, fmaxf(sc[v][j][n], sc[v][j][n + 2]));
                             z = fmaxf(z, __shfl_xor_sync(~0u, z, 4));
                             z = fmaxf(z, __shfl_xor_sync(~0u, z, 8));
-                            z = fmaxf(z, __shfl_xor_sync(~0u, z, 16)) * in.scale;
+                            z = fmaxf(z, __shfl_xor_sync(~0u, z, 16)) * scale[j][n];
                             const float was = mo[j][n], now = z == -INFINITY ? was : fminf(was, kShift - z);
                             const float by = was == now ? 1.0f : exp2_approx(now - was);
                             mo[j][n] = now;
                             l[j][n] *= by;
 #pragma unroll
                             for (int v = 0; v < U; ++v) {
-                                y[v][j][n] = fmaf(sc[v][j][n], in.scale, now);
-                                y[v][j][n + 2] = fmaf(sc[v][j][n + 2], in.scale, now);
+                                y[v][j][n] = fmaf(sc[v][j][n], scale[j][n], now);
+                                y[v][j][n + 2] = fmaf(sc[v][j][n + 2], scale[j][n], now);
                             }
 #pragma unroll
                             for (int e = 0; e < G; ++e)
@@ -742,7 +754,7 @@ template <int D, int NT> nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, 
     if (attr != cudaSuccess)
         return NM_ERR_CUDA;
     const size_t smem = Smem<D, NT>::kSeqs + (size_t)(b.n_seqs + 1) * 8 + (size_t)b.n_seqs * sizeof(Kv4Seq);
-    const unsigned grid = (unsigned)(num_sms * (NT == 1 ? 2 : 1)); // at most kKv4Counters / 4
+    const unsigned grid = (unsigned)(num_sms * (NT <= 2 ? 2 : 1)); // at most kKv4Counters / 4
     attn_rows_kernel<D, NT><<<grid, kThreads, smem, st>>>(c, b, a);
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
