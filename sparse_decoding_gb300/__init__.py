@@ -504,6 +504,8 @@ class Kv4Cache:
 
     def _batch(self, seqs, starts, n_tokens=None):
         """(seqs pointer, starts pointer, n_seqs) of a call."""
+        if seqs is None and starts is None and n_tokens is not None:
+            return None, None, n_tokens
         n = starts.numel() - 1 if starts is not None else seqs.numel() if seqs is not None else n_tokens
         if n is None or n < 0 or (seqs is not None and seqs.numel() != n) or \
                 (starts is None and n_tokens is not None and n != n_tokens):
@@ -512,16 +514,17 @@ class Kv4Cache:
 
     def _tokens(self, t: torch.Tensor, name: str):
         """(pointer, token stride, heads) of a token tensor."""
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != self.device:
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda or \
+                t.get_device() != self._index:
             raise TypeError(f"{name} must be a bfloat16 tensor on {self.device}")
-        D = self.head_dim
-        if t.dim() == 3 and t.shape[2] == D and t.stride(2) == 1 and (t.stride(1) == D or t.shape[1] == 1):
-            heads = t.shape[1]
-        elif t.dim() == 2 and t.shape[1] % D == 0 and t.stride(1) == 1:
-            heads = t.shape[1] // D
+        D, shape, stride = self.head_dim, t.shape, t.stride()
+        if len(shape) == 3 and shape[2] == D and stride[2] == 1 and (stride[1] == D or shape[1] == 1):
+            heads = shape[1]
+        elif len(shape) == 2 and shape[1] % D == 0 and stride[1] == 1:
+            heads = shape[1] // D
         else:
             raise ValueError(f"{name} must be [tokens][heads][{D}] or [tokens][heads * {D}], contiguous in a token")
-        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * D, heads
+        return t.data_ptr(), stride[0] if shape[0] > 1 else heads * D, heads
 
     def reserve(self, seqs: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
                 n: Optional[int] = None) -> None:
@@ -606,13 +609,16 @@ class Kv4Cache:
         qp, qs, qh = self._tokens(q, "q")
         T = q.shape[0]
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        op, os_, oh = self._tokens(out, "out")
-        if out.shape[0] != T or oh != qh:
-            raise ValueError("out must have q's tokens and heads")
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            op, os_ = out.data_ptr(), qh * self.head_dim
+        else:
+            op, os_, oh = self._tokens(out, "out")
+            if out.shape[0] != T or oh != qh:
+                raise ValueError("out must have q's tokens and heads")
         sp, st, n = self._batch(seqs, starts, T if starts is None else None)
-        ls = torch.empty(T, qh, dtype=torch.float32, device=q.device) if lse else None
-        _check(self._lib.nm_kv4_attention(self._ref, layer, sp, st, n, T, max(T, 1) if max_new is None else max_new, qp,
-                                      qs, qh, self.head_dim ** -0.5 if scale is None else scale, op, os_,
-                                      ls.data_ptr() if lse else None, self._s()), "nm_kv4_attention")
+        ls = q.new_empty((T, qh), dtype=torch.float32) if lse else None
+        status = self._lib.nm_kv4_attention(self._ref, layer, sp, st, n, T, (T or 1) if max_new is None else max_new, qp, qs, qh,
+                                            self.head_dim ** -0.5 if scale is None else scale, op, os_,
+                                            ls.data_ptr() if lse else None, self._s())
+        _check(status, "nm_kv4_attention")
         return (out, ls) if lse else out

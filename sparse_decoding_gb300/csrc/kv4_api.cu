@@ -313,6 +313,8 @@ nm_status nm_kv4_attention(const nm_kv4_cache *cache, int layer, const int32_t *
         return NM_ERR_UNSUPPORTED;
     if (max_new < 1)
         return NM_ERR_INVALID_ARG;
+    if (n_tokens * n_q_heads > 0x3FFFFFFF)
+        return NM_ERR_SHAPE;
     if (n_seqs == 0 || n_tokens == 0)
         return NM_OK;
     const int D = cache->head_dim;

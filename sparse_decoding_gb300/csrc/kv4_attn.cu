@@ -20,10 +20,12 @@
 // The layout of a cell is the operands' own: lane l reads 16 bytes at 16 l, so K
 // and V need no transposition on the way to the registers.
 //
-// The units (pairs of cells) of all (sequence, kv head, tile) segments are one line, cut evenly
-// over the CTAs of one wave, whatever the lengths; a CTA's warps take the cells of
-// a piece in turn and are joined in shared memory. A segment that was cut is
-// joined by the last of its CTAs, in CTA order, from the workspace.
+// A (sequence, kv head, tile) is a segment. Each CTA gets one piece of one where that
+// can be balanced, else an even part of the line of all segments (see the kernel's
+// beginning): a piece costs about 5 us before and after its cells, as much as eight
+// units (pairs of cells) of each warp. A CTA's warps take the units of a piece in
+// turn and are joined in shared memory. A segment that was cut is joined by the
+// last of its CTAs, in CTA order, from the workspace.
 #include <mutex>
 #include <type_traits>
 
@@ -37,7 +39,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 2;          // cells that a warp takes at a time
 constexpr int kTokens = kUnit * kKv4Cell;
 constexpr int64_t kMinShare = 8;  // units of a CTA at least: one for each warp
-constexpr int kWhole = 16;        // segments of up to so many units are not cut
+constexpr int kWhole = 16;        // when none has more units than this, no segment is cut
+constexpr float kMoreUnits = 12.0f; // of about 0.3 us in a full CTA; a second piece costs about 4 us
 constexpr int kOver = 8;          // units that starting and ending a piece costs as much as
 constexpr float kShift = 6.0f;    // p = 2^(s - m + kShift)
 constexpr float kSlack = 8.0f;    // a score may pass m by this much
@@ -208,8 +211,15 @@ template <int D, int NT> struct Smem {
     static constexpr int kSeqs = kBars + kWarps * kStages * 8;
 };
 
+// Pieces of a segment that is cut every `chunk` units.
+__device__ __forceinline__ int pieces_of(int units, int chunk) { return (int)((uint32_t)(units + chunk - 1) / (uint32_t)chunk); }
 __device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + kTokens - 1) / kTokens : 1; }
-__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// a / b of numbers that fit 32 bits as a rule (a 64-bit division takes ten times as long).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return quotient(a + b - 1, b); }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
@@ -228,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
     int64_t *const pre = (int64_t *)(smem + SM::kSeqs);      // [n_seqs + 1]
     Kv4Seq *const seqs = (Kv4Seq *)(pre + b.n_seqs + 1);     // [n_seqs]
     __shared__ uint32_t s_last;
+    __shared__ int s_chunk;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     uint8_t *const ring = smem + warp * S * SM::kStage;
     const uint32_t rings = smem_addr(ring), bars = smem_addr(smem + SM::kBars) + warp * S * 8;
@@ -242,18 +253,48 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
         const Kv4Seq s = kv4_seq(c, b, i, blockIdx.x == 0);
         seqs[i] = s;
         longest = max(longest, s.n_new == 0 ? 0 : units_of(s.len));
-        pre[i + 1] = ceil_div((int64_t)s.n_new * a.ratio, RT) * c.n_kv_heads;
+        pre[i + 1] = (int64_t)((uint32_t)(s.n_new * a.ratio + RT - 1) / RT) * c.n_kv_heads; // segments
     }
-    // Short sequences are not cut: a segment is one step of the line, not one per unit.
-    const bool cut = __syncthreads_or(longest > kWhole);
+    const bool is_long = __syncthreads_or(longest > kWhole);
     if (warp == 0) {
+        // How the segments are cut:
+        //   chunk > 0: into pieces of so many units (a multiple of the warps), each a step of the
+        //     line; the least chunk with which all pieces fit the CTAs of one wave,
+        //   chunk = 0: the line has a step for each unit and kOver more for each segment, and is cut
+        //     evenly. Taken when there are more segments than CTAs, or when one chunk for all lengths
+        //     is over an even cut by more than a second piece costs a CTA.
+        const auto total_of = [&](const auto &f) { // counts, each cut off far above the grid
+            uint32_t x = 0;
+            for (int i = lane; i < b.n_seqs; i += 32) {
+                const int64_t y = f(i);
+                x += y < 65536 ? (uint32_t)y : 65536u;
+            }
+            return __reduce_add_sync(~0u, x);
+        };
+        int chunk = 0;
+        if (!is_long) {
+            chunk = 1 << 30;
+        } else if (total_of([&](int i) { return pre[i + 1]; }) <= gridDim.x) {
+            float work = 0.0f;
+            for (int i = lane; i < b.n_seqs; i += 32)
+                work += (float)pre[i + 1] * (float)units_of(seqs[i].len);
+            for (int z = 16; z; z >>= 1)
+                work += __shfl_xor_sync(~0u, work, z);
+            const float even = work / (float)gridDim.x;
+            const int step = (int)(even / (8 * kWarps)) * kWarps + kWarps;
+            for (int z = (int)(even / kWarps) * kWarps + kWarps; (float)z <= even + kMoreUnits; z += step) {
+                if (total_of([&](int i) { return pre[i + 1] * pieces_of(units_of(seqs[i].len), z); }) <= gridDim.x) {
+                    chunk = z;
+                    break;
+                }
+            }
+        }
         int64_t sum = 0;
         for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
             int64_t x = 0;
             if (i0 + lane < b.n_seqs) {
-                x = pre[i0 + lane + 1];
-                if (cut)
-                    x *= kOver + units_of(seqs[i0 + lane].len);
+                const int units = units_of(seqs[i0 + lane].len);
+                x = pre[i0 + lane + 1] * (chunk ? pieces_of(units, chunk) : kOver + units);
             }
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(~0u, x, o);
@@ -265,13 +306,16 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                 pre[i0 + lane + 1] = sum + x;
             sum += __shfl_sync(~0u, x, 31);
         }
-        if (lane == 0)
+        if (lane == 0) {
             pre[0] = 0;
+            s_chunk = chunk;
+        }
     }
     __syncthreads();
+    const int chunk = s_chunk;
     const int64_t total = pre[b.n_seqs];
     int64_t share = ceil_div(total, gridDim.x);
-    if (cut && share < kMinShare + kOver)
+    if (!chunk && share < kMinShare + kOver)
         share = kMinShare + kOver;
     const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share < total ? lo + share : total;
     const int shift = c.page_shift - 4;
@@ -293,20 +337,41 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
         }
         const Kv4Seq s = seqs[i];
         const int units = units_of(s.len);
-        // A segment that may be cut has kOver steps of the line before its units' own.
-        const int over = cut ? kOver : 0, per = cut ? kOver + units : 1;
-        const int64_t seg = (pos - pre[i]) / per;
+        const int over = chunk ? 0 : kOver, per = chunk ? pieces_of(units, chunk) : kOver + units; // steps of the segment
+        const int64_t seg = quotient(pos - pre[i], per);
         const int64_t seg_lo = pre[i] + seg * per, seg_hi = seg_lo + per;
-        const int steps = (int)((hi < seg_hi ? hi : seg_hi) - pos);
-        const int from = (int)(pos - seg_lo) - over;
-        const int c0 = cut && from > 0 ? from : 0, c1 = cut ? from + steps : units;
-        if (c1 <= c0)
-            break; // the CTA's part of the line ends before the segment's first unit
-        const int64_t rows = (int64_t)s.n_new * a.ratio; // rows of the sequence and kv head
-        const int64_t tiles = ceil_div(rows, RT);
-        const int head = (int)(seg / tiles);
-        const int64_t row0 = (seg % tiles) * RT; // first row of the tile
-        const int tile_first = s.len - s.n_new + (int)(row0 / a.ratio) + 1; // tokens that its first row attends
+        int steps, c0, c1;
+        if (chunk) {
+            steps = 1;
+            c0 = (int)(pos - seg_lo) * (per > 1 ? chunk : 0);
+            c1 = per > 1 && units - c0 > chunk ? c0 + chunk : units;
+        } else {
+            steps = (int)((hi < seg_hi ? hi : seg_hi) - pos);
+            const int from = (int)(pos - seg_lo) - over;
+            c0 = from > 0 ? from : 0;
+            c1 = from + steps;
+            if (c1 <= c0)
+                break; // the CTA's part of the line ends before the segment's first unit
+        }
+        const int rows = s.n_new * a.ratio; // rows of the sequence and kv head
+        const int tiles = (rows + RT - 1) / RT;
+        const int head = (int)quotient(seg, tiles);
+        const int row0 = (int)(seg - (int64_t)head * tiles) * RT; // first row of the tile
+        const int tile_first = s.len - s.n_new + row0 / a.ratio + 1; // tokens that its first row attends
+
+        // Q: warp j takes n-tile j: row g, channels 64 e + 16 t ..
+        uint4 qw[G][2];
+        const int qrow = row0 + 8 * warp + g;
+        const bool real = warp < NT && qrow < rows;
+        if (warp < NT) {
+            const uint16_t *q = a.q + (int64_t)(s.first + qrow / a.ratio) * a.q_stride +
+                                ((int64_t)head * a.ratio + qrow % a.ratio) * D + 16 * t;
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    qw[e][f] = real ? ldg_nc128(q + 64 * e + 8 * f) : make_uint4(0, 0, 0, 0);
+        }
 
         // The warp's units are c0 + warp, + kWarps, ... Lanes 2 n, 2 n + 1 hold the addresses of the
         // cells of every 16th (0: its page is none of the pool's, or it is past the sequence's end);
@@ -340,20 +405,16 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
         for (int x = 0; x < (S > 2 ? S - 1 : S) && x < mine; ++x)
             fetch(x);
 
-        // Q as the B operand: warp j makes n-tile j; row g, channels 64 e + 16 t ..
-        for (int j = warp; j < NT; j += kWarps) {
-            const int64_t row = row0 + 8 * j + g;
+        // Q as the B operand
+        if (warp < NT) {
+            const int j = warp;
             float x[G][16];
             float top = 0.0f;
-            const bool real = row < rows;
-            const int64_t token = s.first + row / a.ratio;
-            const uint16_t *q = a.q + token * a.q_stride + ((int64_t)head * a.ratio + row % a.ratio) * D;
 #pragma unroll
             for (int e = 0; e < G; ++e)
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
-                    const uint4 w = real ? ldg_nc128(q + 64 * e + 16 * t + 8 * f) : make_uint4(0, 0, 0, 0);
-                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                    const uint32_t ws[4] = {qw[e][f].x, qw[e][f].y, qw[e][f].z, qw[e][f].w};
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         x[e][8 * f + 2 * n] = bf16lo_to_f32(ws[n]);
@@ -401,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
             sm_sums[32 * j + lane] = t == 0 ? pack_half2(h0, h1) : t == 1 ? pack_half2(sums[0] - h0, l1) : 0u;
             if (t == 0)
                 sm_info[8 * j + g] = RowInfo{fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f),
-                                             real ? s.len - s.n_new + (int)(row / a.ratio) + 1 : 0};
+                                             real ? s.len - s.n_new + qrow / a.ratio + 1 : 0};
         }
         __syncthreads();
         // with one n-tile Q stays in registers
@@ -630,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
 
         // joined over the warps; four channels of a row to a thread
         const auto store = [&](int row, int ch, const float4 &x, float M, float L) {
-            const int64_t r = row0 + row;
+            const int r = row0 + row;
             if (r >= rows)
                 return;
             const int64_t token = s.first + r / a.ratio, h = (int64_t)head * a.ratio + r % a.ratio;
@@ -676,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
         }
         if (!whole) {
             // the segment's CTAs are first .. last; the last one to arrive joins their parts in order
-            const int first = (int)((seg_lo + over) / share), last = (int)((seg_hi - 1) / share);
+            const int first = (int)quotient(seg_lo + over, share), last = (int)quotient(seg_hi - 1, share);
             __syncthreads();
             if (tid == 0) {
                 const uint32_t n = (uint32_t)(last - first);
