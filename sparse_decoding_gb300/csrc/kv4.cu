@@ -1,39 +1,20 @@
 // kv4.cu -- writing tokens to the 4-bit paged KV cache (with the rotary
 // positions of q and k) and reading the values it holds back.
+//
+// A warp takes one cell (16 tokens) of one kv head, four tokens at a time with
+// eight lanes each: lane i of a token holds channels i D/16 .. of each half of the
+// vector, the two halves that a rotation turns together, so a rotation stays in the
+// lane and a group's least and greatest values take three shuffles. The four tokens
+// are 2 t, 2 t + 1, 2 t + 8, 2 t + 9 for t = 0 .. 3: together they fill 16 bytes of
+// V's codes, so a cell is written in full sectors. All loads of a cell are asked for
+// first. The q heads are turned by other warps of the same launch, four heads of a
+// token at a time with the token's angles in registers.
+//
+// Bytes bound it: k, v, q and q_out once, the angles once per SM and token.
 #include "kv4.cuh"
 
 namespace nm {
 namespace {
-
-// Channels of a lane, where a warp holds one head's vector: 2 l, 2 l + 1 and
-// D/2 + 2 l, + 1 (the two halves that a rotation turns together), l < D / 4.
-template <int D> struct Lane4 {
-    float v[4];
-};
-template <int D> __device__ __forceinline__ int lane_channel(int lane, int half) { return half * (D / 2) + 2 * lane; }
-
-template <int D> __device__ __forceinline__ Lane4<D> load_vec(const uint16_t *p, int lane)
-{
-    Lane4<D> r;
-    const uint32_t a = *(const uint32_t *)(p + lane_channel<D>(lane, 0));
-    const uint32_t b = *(const uint32_t *)(p + lane_channel<D>(lane, 1));
-    r.v[0] = bf16lo_to_f32(a);
-    r.v[1] = bf16hi_to_f32(a);
-    r.v[2] = bf16lo_to_f32(b);
-    r.v[3] = bf16hi_to_f32(b);
-    return r;
-}
-
-// (a cos - b sin, b cos + a sin), each operation rounded.
-template <int D> __device__ __forceinline__ void rotate(Lane4<D> &x, const float *row, int lane)
-{
-    const float2 c = *(const float2 *)(row + 2 * lane), s = *(const float2 *)(row + D / 2 + 2 * lane);
-    const float a0 = x.v[0], a1 = x.v[1], b0 = x.v[2], b1 = x.v[3];
-    x.v[0] = __fsub_rn(__fmul_rn(a0, c.x), __fmul_rn(b0, s.x));
-    x.v[1] = __fsub_rn(__fmul_rn(a1, c.y), __fmul_rn(b1, s.y));
-    x.v[2] = __fadd_rn(__fmul_rn(b0, c.x), __fmul_rn(a0, s.x));
-    x.v[3] = __fadd_rn(__fmul_rn(b1, c.y), __fmul_rn(a1, s.y));
-}
 
 __device__ __forceinline__ bool finite_f32(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
 __device__ __forceinline__ float saturate(float x)
@@ -41,46 +22,208 @@ __device__ __forceinline__ float saturate(float x)
     return x != x ? 0.0f : fminf(fmaxf(x, -kKv4Limit), kKv4Limit);
 }
 
-// Scale and middle of a group with least and greatest value lo and hi, as the
-// cache holds them, and the code of one value.
-__device__ __forceinline__ void group_params(float lo, float hi, __half &s, __half &mid)
+// N = D / 16 channels of each half of a vector, as bf16 pairs and in fp32.
+template <int N> struct Raw {
+    uint32_t w[2][N / 2];
+};
+template <int N> struct Vec {
+    float x[2][N];
+};
+template <int N> __device__ __forceinline__ Raw<N> load_raw(const uint16_t *p, int i, int half)
 {
-    const uint16_t sb = f32_to_bf16_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f));
-    s = __float2half_rn(bf16_to_f32(sb));
-    mid = __float2half_rn(__fadd_rn(lo, __fmul_rn(__half2float(s), 8.0f)));
+    Raw<N> r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (N == 8) {
+            const uint4 v = ldg_nc128(p + h * half + 8 * i);
+            r.w[h][0] = v.x;
+            r.w[h][1] = v.y;
+            r.w[h][N / 2 - 2] = v.z;
+            r.w[h][N / 2 - 1] = v.w;
+        } else {
+            const uint2 v = __ldg((const uint2 *)(p + h * half + 4 * i));
+            r.w[h][0] = v.x;
+            r.w[h][1] = v.y;
+        }
+    }
+    return r;
 }
-__device__ __forceinline__ uint32_t code_of(float x, float s, float mid)
+template <int N> __device__ __forceinline__ Vec<N> unpack(const Raw<N> &r)
 {
-    const float u = s > 0.0f ? rintf(__fdiv_rn(__fsub_rn(x, mid), s)) : 0.0f;
-    return (uint32_t)(int)(fminf(fmaxf(u, -8.0f), 7.0f) + 8.0f);
+    Vec<N> v;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < N / 2; ++n) {
+            v.x[h][2 * n] = bf16lo_to_f32(r.w[h][n]);
+            v.x[h][2 * n + 1] = bf16hi_to_f32(r.w[h][n]);
+        }
+    return v;
+}
+// A token's cos and sin of the lane's angles.
+template <int N> struct Turn {
+    float c[N], s[N];
+};
+template <int N> __device__ __forceinline__ Turn<N> load_turn(const float *row, int i)
+{
+    Turn<N> t;
+#pragma unroll
+    for (int n = 0; n < N; n += 4) {
+        const float4 c = __ldg((const float4 *)(row + N * i + n)), s = __ldg((const float4 *)(row + 8 * N + N * i + n));
+        t.c[n] = c.x, t.c[n + 1] = c.y, t.c[n + 2] = c.z, t.c[n + 3] = c.w;
+        t.s[n] = s.x, t.s[n + 1] = s.y, t.s[n + 2] = s.z, t.s[n + 3] = s.w;
+    }
+    return t;
+}
+// (a cos - b sin, b cos + a sin), each operation rounded.
+template <int N> __device__ __forceinline__ void rotate(Vec<N> &v, const Turn<N> &t)
+{
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const float a = v.x[0][n], b = v.x[1][n];
+        v.x[0][n] = __fsub_rn(__fmul_rn(a, t.c[n]), __fmul_rn(b, t.s[n]));
+        v.x[1][n] = __fadd_rn(__fmul_rn(b, t.c[n]), __fmul_rn(a, t.s[n]));
+    }
 }
 
-__device__ __forceinline__ float warp_min(float x)
+// The codes of N values of a group, value n in bits 4 n ..: rint((x - mid) / s), the
+// quotient rounded as fp32 division rounds it. x * (1 / s) is off by under 1e-5 here
+// (|quotient| < 16), so it decides unless it is that near to the middle between two
+// codes; then the division does.
+template <int N> __device__ __forceinline__ uint32_t codes_of(const float *x, float s, float mid)
 {
-    for (int o = 16; o; o >>= 1)
-        x = fminf(x, __shfl_xor_sync(~0u, x, o));
-    return x;
-}
-__device__ __forceinline__ float warp_max(float x)
-{
-    for (int o = 16; o; o >>= 1)
-        x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
-    return x;
+    constexpr float kMagic = 12582912.0f; // 1.5 * 2^23: adding it rounds to a whole number, ties to even
+    const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+    uint32_t r = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const float d = __fsub_rn(x[n], mid);
+        float t = fminf(fmaxf(d * inv, -8.0f), 7.0f);
+        float u = t + kMagic;
+        if (fabsf(fabsf(t - (u - kMagic)) - 0.5f) < 1e-4f) {
+            t = fminf(fmaxf(__fdiv_rn(d, s), -8.0f), 7.0f);
+            u = t + kMagic;
+        }
+        r |= ((__float_as_uint(u) + 8u) & 15u) << (4 * n);
+    }
+    return r;
 }
 
-// The byte in a cell that holds the codes of channels ch, ch + 1 (ch even) of
-// token `slot`: of K, and of V.
-template <int D> __device__ __forceinline__ int k_byte(int slot, int ch)
+// One group's parameters, from the least and greatest of its values.
+__device__ __forceinline__ __half2 params_of(float lo, float hi)
 {
-    constexpr int G = Kv4Cell<D>::G;
-    const int g = ch / kKv4Group, x = ch % kKv4Group;
-    return slot * (D / 2) + (x / 16) * (8 * G) + g * 8 + (x % 16) / 2;
+    const float s = __half2float(__float2half_rn(bf16_to_f32(f32_to_bf16_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f)))));
+    return __halves2half2(__float2half_rn(s), __float2half_rn(__fadd_rn(lo, __fmul_rn(s, 8.0f))));
 }
-template <int D> __device__ __forceinline__ int v_byte(int slot, int ch)
+
+// A token of a warp's cell, as its eight lanes hold it: K's and V's codes of the two
+// halves (8 or 4 of them each) and the parameters of the groups.
+template <int D> struct Coded {
+    uint32_t code[2][2];
+    __half2 par[2][D / 64];
+};
+template <int D> __device__ __forceinline__ Coded<D> encode(Vec<D / 16> &k, Vec<D / 16> &v)
 {
-    const int g = ch / kKv4Group, x = ch % kKv4Group;
-    return Kv4Cell<D>::kV + g * 512 + ((x / 8) * 4 + (slot / 2) % 4) * 16 + (slot / 8) * 8 + ((x / 4) % 2) * 4 +
-           (slot % 2) * 2 + (x % 4) / 2;
+    constexpr int N = D / 16, G = D / 64;
+    Coded<D> r;
+    bool fine = true;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            fine = fine && finite_f32(k.x[h][n]) && finite_f32(v.x[h][n]);
+    const uint32_t votes = __ballot_sync(~0u, fine);
+    fine = ((votes >> (threadIdx.x & 24)) & 0xFFu) == 0xFFu; // all eight lanes of the token
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+        Vec<N> &z = kv ? v : k;
+        float lo[2], hi[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            lo[h] = INFINITY;
+            hi[h] = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                z.x[h][n] = saturate(z.x[h][n]);
+                lo[h] = fminf(lo[h], z.x[h][n]);
+                hi[h] = fmaxf(hi[h], z.x[h][n]);
+            }
+        }
+        if (G == 1) {
+            lo[0] = fminf(lo[0], lo[1]);
+            hi[0] = fmaxf(hi[0], hi[1]);
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                lo[g] = fminf(lo[g], __shfl_xor_sync(~0u, lo[g], o));
+                hi[g] = fmaxf(hi[g], __shfl_xor_sync(~0u, hi[g], o));
+            }
+            r.par[kv][g] = params_of(lo[g], hi[g]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const __half2 p = r.par[kv][G == 2 ? h : 0];
+            r.code[kv][h] = codes_of<N>(z.x[h], __low2float(p), __high2float(p));
+        }
+    }
+    if (!fine) { // K poisoned, V kept finite
+        r.code[0][0] = r.code[0][1] = 0x88888888u;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            r.par[0][g] = __halves2half2(__ushort_as_half(0x7E00), __ushort_as_half(0x7E00));
+    }
+    return r;
+}
+
+// The cell that slot x of a call's work stands for. Sequence i has the slots from
+// starts[i] / 16 + 2 i on: at least as many as the cells that its new tokens lie in.
+struct CellJob {
+    Kv4Seq s;
+    int cell, from, to; // positions [from, to) of the cell's are the call's
+    int missing;        // (first slot) the first so many new tokens are at no position: len < n_new
+};
+__device__ __forceinline__ bool cell_job(const Kv4 &c, const Kv4Batch &b, int64_t x, bool report, CellJob *j)
+{
+    int i;
+    int64_t first = x;
+    j->missing = 0;
+    if (!b.starts) {
+        i = (int)x;
+        if (i >= b.n_seqs)
+            return false;
+    } else {
+        int lo = 0, hi = b.n_seqs;
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            if ((int64_t)(b.starts[m] >> 4) + 2 * m <= x)
+                lo = m;
+            else
+                hi = m;
+        }
+        i = lo;
+        first = (int64_t)(b.starts[i] >> 4) + 2 * i;
+    }
+    const int64_t nth = x - first;
+    if (nth < 0)
+        return false;
+    j->s = kv4_seq(c, b, i, report && nth == 0);
+    int begin = j->s.len - j->s.n_new;
+    if (begin < 0) {
+        if (nth == 0) {
+            j->missing = -begin;
+            if (report)
+                kv4_bad(c);
+        }
+        begin = 0;
+    }
+    if (j->s.n_new == 0 || j->s.len == 0 || nth > (j->s.len - 1) / kKv4Cell - begin / kKv4Cell)
+        return false;
+    j->cell = begin / kKv4Cell + (int)nth;
+    j->from = max(begin, j->cell * kKv4Cell);
+    j->to = min(j->s.len, (j->cell + 1) * kKv4Cell);
+    return true;
 }
 
 struct AppendArgs {
@@ -90,185 +233,255 @@ struct AppendArgs {
     int64_t k_stride, v_stride, q_stride, q_out_stride;
     const float *rope;
     int64_t rope_rows;
+    int64_t slots;      // of cells, times the kv heads: warps that write the cache
+    int64_t cell_ctas;  // the CTAs that hold those warps
+    int q_warps, q_each; // warps of a token's q heads, and how many fours of heads each turns
 };
 
-// One warp per (token, head): the kv heads are rotated, quantised and written,
-// the q heads rotated.
-template <int D> __global__ void __launch_bounds__(256) append_kernel(const Kv4 c, const Kv4Batch b, const AppendArgs a)
+template <int D> __device__ __forceinline__ void append_cell(const Kv4 &c, const Kv4Batch &b, const AppendArgs &a, int64_t w)
 {
-    constexpr int G = Kv4Cell<D>::G;
-    const int lane = threadIdx.x & 31;
-    const int jobs = c.n_kv_heads + (a.q ? a.n_q_heads : 0);
-    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t token = w / jobs;
-    const int job = (int)(w % jobs);
-    if (token >= b.n_tokens)
+    constexpr int N = D / 16, G = D / 64;
+    using C = Kv4Cell<D>;
+    const int lane = threadIdx.x & 31, i = lane & 7, part = lane >> 3; // part: r + 2 p of the token
+    const int head = (int)(w % c.n_kv_heads);
+    CellJob j;
+    if (!cell_job(c, b, w / c.n_kv_heads, head == 0 && lane == 0, &j))
         return;
-    const int i = kv4_find(b, token);
-    Kv4Seq s{};
-    int pos = -1;
-    if (i >= 0) {
-        s = kv4_seq(c, b, i, lane == 0);
-        pos = s.len - s.n_new + (int)(token - s.first);
-    }
-    bool ok = pos >= 0 && pos < s.len && (!a.rope || pos < a.rope_rows);
-    const bool mine = lane < D / 4;
-    const float *row = a.rope && ok ? a.rope + (int64_t)pos * D : nullptr;
-
-    if (job >= c.n_kv_heads) { // a q head
-        const int h = job - c.n_kv_heads;
-        if (!mine)
-            return;
-        Lane4<D> x = load_vec<D>(a.q + token * a.q_stride + (int64_t)h * D, lane);
-        if (row)
-            rotate<D>(x, row, lane);
-        uint16_t *o = a.q_out + token * a.q_out_stride + (int64_t)h * D;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t p = f32_to_bf16_rn(x.v[2 * e]) | ((uint32_t)f32_to_bf16_rn(x.v[2 * e + 1]) << 16);
-            *(uint32_t *)(o + lane_channel<D>(lane, e)) = ok ? p : 0u;
-        }
-        return;
-    }
-    const int page = ok ? kv4_page(c, s.row, pos >> c.page_shift) : -1;
+    const int page = kv4_page(c, j.s.row, (j.cell * kKv4Cell) >> c.page_shift);
     if (page < 0) {
         if (lane == 0)
             kv4_bad(c);
         return;
     }
-    const int slot = pos % kKv4Cell, cell = (pos & (c.page_tokens - 1)) / kKv4Cell;
-    uint8_t *dst = c.pool + kv4_cell_offset<D>(c, page, a.layer, job, cell);
-    Lane4<D> kx{}, vx{};
-    if (mine) {
-        kx = load_vec<D>(a.k + token * a.k_stride + (int64_t)job * D, lane);
-        vx = load_vec<D>(a.v + token * a.v_stride + (int64_t)job * D, lane);
-        if (row)
-            rotate<D>(kx, row, lane);
+    if (a.rope && j.to > a.rope_rows) {
+        if (lane == 0)
+            kv4_bad(c);
+        j.to = (int)a.rope_rows;
     }
-    bool fine = true;
+    uint8_t *const dst = c.pool + kv4_cell_offset<D>(c, page, a.layer, head, j.cell & ((c.page_tokens >> 4) - 1));
+    const int base = j.cell * kKv4Cell;
+    const auto slot_of = [&](int t) { return 2 * t + (part & 1) + 8 * (part >> 1); };
+    const auto mine = [&](int t) { return base + slot_of(t) >= j.from && base + slot_of(t) < j.to; };
+    Raw<N> rk[4], rv[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        fine = fine && finite_f32(kx.v[e]) && finite_f32(vx.v[e]);
-    fine = __all_sync(~0u, fine);
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        Lane4<D> &x = kv ? vx : kx;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            x.v[e] = saturate(x.v[e]);
-        __half sc[2], md[2];
-        float lo[2], hi[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) { // the lane's two halves
-            lo[e] = mine ? fminf(x.v[2 * e], x.v[2 * e + 1]) : INFINITY;
-            hi[e] = mine ? fmaxf(x.v[2 * e], x.v[2 * e + 1]) : -INFINITY;
+    for (int t = 0; t < 4; ++t) {
+        const int64_t token = (int64_t)j.s.first + (base + slot_of(t) - (j.s.len - j.s.n_new));
+        if (mine(t)) {
+            rk[t] = load_raw<N>(a.k + token * a.k_stride + (int64_t)head * D, i, D / 2);
+            rv[t] = load_raw<N>(a.v + token * a.v_stride + (int64_t)head * D, i, D / 2);
+        } else {
+            rk[t] = rv[t] = Raw<N>{};
         }
-        if (G == 1) {
-            lo[0] = lo[1] = fminf(lo[0], lo[1]);
-            hi[0] = hi[1] = fmaxf(hi[0], hi[1]);
-        }
+    }
 #pragma unroll
-        for (int e = 0; e < G; ++e) {
-            lo[e] = warp_min(lo[e]);
-            hi[e] = warp_max(hi[e]);
-            group_params(lo[e], hi[e], sc[e], md[e]);
-        }
-        if (G == 1) {
-            sc[1] = sc[0];
-            md[1] = md[0];
-        }
-        if (mine) {
+    for (int t = 0; t < 4; ++t) {
+        const bool ok = mine(t);
+        if (!__any_sync(~0u, ok))
+            continue;
+        const int slot = slot_of(t);
+        Vec<N> k = unpack<N>(rk[t]), v = unpack<N>(rv[t]);
+        if (a.rope && ok)
+            rotate<N>(k, load_turn<N>(a.rope + (int64_t)(base + slot) * D, i));
+        const Coded<D> e = encode<D>(k, v);
+        // K: the token's row; half h of lane i: channels h D/2 + i N ..
+        if (ok) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float fs = __half2float(sc[e]), fm = __half2float(md[e]);
-                uint32_t byte = code_of(x.v[2 * e], fs, fm) | (code_of(x.v[2 * e + 1], fs, fm) << 4);
-                const int ch = lane_channel<D>(lane, e);
-                if (!kv && !fine)
-                    byte = 0x88;
-                dst[kv ? v_byte<D>(slot, ch) : k_byte<D>(slot, ch)] = (uint8_t)byte;
+            for (int h = 0; h < 2; ++h) {
+                if (D == 128)
+                    *(uint32_t *)(dst + slot * 64 + (i >> 1) * 16 + h * 8 + (i & 1) * 4) = e.code[0][h];
+                else // four codes: channels 32 h + 4 i of the one group
+                    *(uint16_t *)(dst + slot * 32 + (2 * h + (i >> 2)) * 8 + (i & 3) * 2) = (uint16_t)e.code[0][h];
+            }
+            if (i < G)
+                *(__half2 *)(dst + C::kKp + (slot * G + i) * 4) = i == 0 ? e.par[0][0] : e.par[0][G - 1];
+        }
+        // V: a token pair's fours of channels side by side: the even token's lane stores the pair's
+        // first four of a half's channels, the odd one's the second (D = 128), or each half's (64)
+        const bool both = __shfl_xor_sync(~0u, ok, 8) && ok;
+        const int odd = part & 1;
+        uint8_t *const at = dst + C::kV + t * 16 + (part >> 1) * 8; // + group * 512 + e * 64 + f * 4 + r * 2
+        const uint32_t p0 = __shfl_xor_sync(~0u, e.code[1][0], 8), p1 = __shfl_xor_sync(~0u, e.code[1][1], 8);
+        if (D == 128) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t own = e.code[1][h], other = h ? p1 : p0;
+                uint8_t *const q = at + h * 512 + i * 64;
+                if (both)
+                    *(uint32_t *)(q + odd * 4) = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+                else if (ok) {
+                    *(uint16_t *)(q + odd * 2) = (uint16_t)own;
+                    *(uint16_t *)(q + 4 + odd * 2) = (uint16_t)(own >> 16);
+                }
+            }
+        } else {
+            // four channels 32 h + 4 i: e = 4 h + i / 2, f = i % 2; the even lane stores half 0, the odd half 1
+            const auto place = [&](int h) { return at + (4 * h + (i >> 1)) * 64 + (i & 1) * 4; };
+            if (both)
+                *(uint32_t *)place(odd) = odd ? (p1 & 0xFFFFu) | e.code[1][1] << 16 : (e.code[1][0] & 0xFFFFu) | p0 << 16;
+            else if (ok) {
+                *(uint16_t *)(place(0) + odd * 2) = (uint16_t)e.code[1][0];
+                *(uint16_t *)(place(1) + odd * 2) = (uint16_t)e.code[1][1];
             }
         }
-        if (lane < G) {
-            const __half ss = lane ? sc[G - 1] : sc[0], mm = lane ? md[G - 1] : md[0];
-            if (!kv) {
-                const __half nan = __ushort_as_half(0x7E00);
-                *(__half2 *)(dst + Kv4Cell<D>::kKp + (slot * G + lane) * 4) =
-                    fine ? __halves2half2(ss, mm) : __halves2half2(nan, nan);
-            } else {
-                __half *p = (__half *)(dst + Kv4Cell<D>::kVp + ((slot / 2) * G + lane) * 8 + (slot % 2) * 2);
-                p[0] = ss;
-                p[2] = mm;
-            }
+        if (i < G && ok) {
+            const __half2 m = i == 0 ? e.par[1][0] : e.par[1][G - 1];
+            __half *p = (__half *)(dst + C::kVp + ((t + 4 * (part >> 1)) * G + i) * 8) + odd;
+            p[0] = __low2half(m);
+            p[2] = __high2half(m);
         }
     }
 }
 
-// One warp per (token, kv head).
-template <int D, bool F32>
-__global__ void __launch_bounds__(256) read_kernel(const Kv4 c, const Kv4Batch b, int layer, void *k, void *v)
+template <int D> __device__ __forceinline__ void append_q(const Kv4 &c, const Kv4Batch &b, const AppendArgs &a, int64_t w)
 {
-    constexpr int G = Kv4Cell<D>::G;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t token = w / c.n_kv_heads;
-    const int head = (int)(w % c.n_kv_heads);
+    constexpr int N = D / 16;
+    const int lane = threadIdx.x & 31, i = lane & 7;
+    const int64_t token = w / a.q_warps;
     if (token >= b.n_tokens)
         return;
-    const int i = kv4_find(b, token);
-    Kv4Seq s{};
-    int pos = -1;
-    if (i >= 0) {
-        s = kv4_seq(c, b, i, lane == 0);
+    const int at = kv4_find(b, token);
+    int pos = -1, len = 0;
+    if (at >= 0) {
+        const Kv4Seq s = kv4_seq(c, b, at, false); // the warps of the cells report
+        len = s.len;
         pos = s.len - s.n_new + (int)(token - s.first);
     }
-    const int page = pos >= 0 && pos < s.len ? kv4_page(c, s.row, pos >> c.page_shift) : -1;
-    if (page < 0 && lane == 0)
-        kv4_bad(c);
-    if (lane >= D / 4)
-        return;
-    const int slot = pos % kKv4Cell, cell = (pos & (c.page_tokens - 1)) / kKv4Cell;
-    const uint8_t *src = page < 0 ? nullptr : c.pool + kv4_cell_offset<D>(c, page, layer, head, cell);
+    const bool ok = pos >= 0 && pos < len && (!a.rope || pos < a.rope_rows);
+    Turn<N> turn{};
+    if (a.rope && ok)
+        turn = load_turn<N>(a.rope + (int64_t)pos * D, i);
+    const int h0 = (int)(w % a.q_warps) * a.q_each * 4 + (lane >> 3);
+#pragma unroll 4
+    for (int n = 0; n < a.q_each; ++n) {
+        const int h = h0 + 4 * n;
+        if (h >= a.n_q_heads)
+            break;
+        Vec<N> v = unpack<N>(load_raw<N>(a.q + token * a.q_stride + (int64_t)h * D, i, D / 2));
+        if (a.rope)
+            rotate<N>(v, turn);
+        uint16_t *const o = a.q_out + token * a.q_out_stride + (int64_t)h * D;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        void *out = kv ? v : k;
-        if (!out)
-            continue;
+        for (int half = 0; half < 2; ++half) {
+            uint32_t y[N / 2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int ch = lane_channel<D>(lane, e), g = ch / kKv4Group;
-            float x0 = 0.0f, x1 = 0.0f;
-            if (src) {
-                float sc, md;
-                if (!kv) {
-                    const __half2 p = *(const __half2 *)(src + Kv4Cell<D>::kKp + (slot * G + g) * 4);
-                    sc = __low2float(p);
-                    md = __high2float(p);
-                } else {
-                    const __half *p = (const __half *)(src + Kv4Cell<D>::kVp + ((slot / 2) * G + g) * 8 + (slot % 2) * 2);
-                    sc = __half2float(p[0]);
-                    md = __half2float(p[2]);
-                }
-                const uint32_t by = src[kv ? v_byte<D>(slot, ch) : k_byte<D>(slot, ch)];
-                x0 = __fadd_rn(__fmul_rn((float)(int)(by & 15u) - 8.0f, sc), md);
-                x1 = __fadd_rn(__fmul_rn((float)(int)(by >> 4) - 8.0f, sc), md);
-            }
-            const int64_t at = (token * c.n_kv_heads + head) * D + ch;
-            if (F32)
-                *(float2 *)((float *)out + at) = make_float2(x0, x1);
+            for (int m = 0; m < N / 2; ++m)
+                y[m] = ok ? f32_to_bf16_rn(v.x[half][2 * m]) | ((uint32_t)f32_to_bf16_rn(v.x[half][2 * m + 1]) << 16) : 0u;
+            if (N == 8)
+                *(uint4 *)(o + half * (D / 2) + 8 * i) = make_uint4(y[0], y[1], y[N / 2 - 2], y[N / 2 - 1]);
             else
-                *(uint32_t *)((uint16_t *)out + at) = f32_to_bf16_rn(x0) | ((uint32_t)f32_to_bf16_rn(x1) << 16);
+                *(uint2 *)(o + half * (D / 2) + 4 * i) = make_uint2(y[0], y[1]);
         }
     }
 }
 
-nm_status grid_of(int64_t warps, unsigned *grid)
+template <int D> __global__ void __launch_bounds__(256) append_kernel(const Kv4 c, const Kv4Batch b, const AppendArgs a)
 {
-    const int64_t g = (warps + 7) / 8;
-    if (g > 0x7FFFFFFF)
-        return NM_ERR_SHAPE;
-    *grid = (unsigned)g;
-    return NM_OK;
+    const int warp = threadIdx.x >> 5;
+    if (blockIdx.x < a.cell_ctas) {
+        const int64_t w = (int64_t)blockIdx.x * 8 + warp;
+        if (w < a.slots)
+            append_cell<D>(c, b, a, w);
+    } else {
+        append_q<D>(c, b, a, (int64_t)(blockIdx.x - a.cell_ctas) * 8 + warp);
+    }
 }
+
+// One warp per (cell, kv head), as append.
+template <int D, bool F32>
+__global__ void __launch_bounds__(256) read_kernel(const Kv4 c, const Kv4Batch b, int layer, void *k, void *v, int64_t slots)
+{
+    constexpr int N = D / 16, G = D / 64;
+    using C = Kv4Cell<D>;
+    const int lane = threadIdx.x & 31, i = lane & 7, part = lane >> 3;
+    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (w >= slots)
+        return;
+    const int head = (int)(w % c.n_kv_heads);
+    CellJob j;
+    const bool have = cell_job(c, b, w / c.n_kv_heads, head == 0 && lane == 0, &j);
+    for (int z = 0; z < j.missing; ++z) { // rows of tokens that the sequence does not have
+        const int64_t at = ((int64_t)(j.s.first + z) * c.n_kv_heads + head) * D;
+        for (int n = lane; n < D * (F32 ? 2 : 1); n += 32) {
+            if (k)
+                ((uint16_t *)k + at * (F32 ? 2 : 1))[n] = 0;
+            if (v)
+                ((uint16_t *)v + at * (F32 ? 2 : 1))[n] = 0;
+        }
+    }
+    if (!have)
+        return;
+    const int page = kv4_page(c, j.s.row, (j.cell * kKv4Cell) >> c.page_shift);
+    if (page < 0 && lane == 0)
+        kv4_bad(c);
+    const uint8_t *const src =
+        page < 0 ? nullptr : c.pool + kv4_cell_offset<D>(c, page, layer, head, j.cell & ((c.page_tokens >> 4) - 1));
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int slot = 2 * t + (part & 1) + 8 * (part >> 1), pos = j.cell * kKv4Cell + slot;
+        if (pos < j.from || pos >= j.to)
+            continue;
+        const int64_t token = (int64_t)j.s.first + (pos - (j.s.len - j.s.n_new));
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            void *const out = kv ? v : k;
+            if (!out)
+                continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int g = G == 2 ? h : 0;
+                uint32_t code = 0;
+                float s = 0.0f, mid = 0.0f;
+                if (src) {
+                    if (kv == 0) {
+                        const __half2 p = *(const __half2 *)(src + C::kKp + (slot * G + g) * 4);
+                        s = __low2float(p);
+                        mid = __high2float(p);
+                        code = D == 128 ? *(const uint32_t *)(src + slot * 64 + (i >> 1) * 16 + h * 8 + (i & 1) * 4)
+                                        : *(const uint16_t *)(src + slot * 32 + (2 * h + (i >> 2)) * 8 + (i & 3) * 2);
+                    } else {
+                        const __half *p = (const __half *)(src + C::kVp + ((t + 4 * (part >> 1)) * G + g) * 8) + (part & 1);
+                        s = __half2float(p[0]);
+                        mid = __half2float(p[2]);
+                        const uint8_t *const at = src + C::kV + t * 16 + (part >> 1) * 8 + (part & 1) * 2;
+                        if (D == 128) {
+                            const uint8_t *const q = at + h * 512 + i * 64;
+                            code = *(const uint16_t *)q | (uint32_t)*(const uint16_t *)(q + 4) << 16;
+                        } else {
+                            code = *(const uint16_t *)(at + (4 * h + (i >> 1)) * 64 + (i & 1) * 4);
+                        }
+                    }
+                }
+                float x[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    x[n] = __fadd_rn(__fmul_rn((float)(int)((code >> (4 * n)) & 15u) - 8.0f, s), mid);
+                const int64_t o = (token * c.n_kv_heads + head) * D + h * (D / 2) + N * i;
+                if (!src) {
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+                        x[n] = 0.0f;
+                }
+                if (F32) {
+#pragma unroll
+                    for (int n = 0; n < N; n += 4)
+                        *(float4 *)((float *)out + o + n) = make_float4(x[n], x[n + 1], x[n + 2], x[n + 3]);
+                } else {
+                    uint32_t y[N / 2];
+#pragma unroll
+                    for (int n = 0; n < N / 2; ++n)
+                        y[n] = f32_to_bf16_rn(x[2 * n]) | ((uint32_t)f32_to_bf16_rn(x[2 * n + 1]) << 16);
+                    if (N == 8)
+                        *(uint4 *)((uint16_t *)out + o) = make_uint4(y[0], y[1], y[N / 2 - 2], y[N / 2 - 1]);
+                    else
+                        *(uint2 *)((uint16_t *)out + o) = make_uint2(y[0], y[1]);
+                }
+            }
+        }
+    }
+}
+
+// Slots of cells for the new tokens of a call (see cell_job).
+int64_t slots_of(const Kv4Batch &b) { return b.starts ? b.n_tokens / kKv4Cell + 2 * (int64_t)b.n_seqs : b.n_seqs; }
 
 } // namespace
 
@@ -276,35 +489,42 @@ nm_status kv4_launch_append(const Kv4 &c, const Kv4Batch &b, int layer, const vo
                             const void *v, int64_t v_stride, const void *q, int64_t q_stride, int n_q_heads,
                             void *q_out, int64_t q_out_stride, const float *rope, int64_t rope_rows, cudaStream_t st)
 {
-    const AppendArgs a{layer, n_q_heads, (const uint16_t *)k, (const uint16_t *)v, (const uint16_t *)q,
-                       (uint16_t *)q_out, k_stride, v_stride, q_stride, q_out_stride, rope, rope_rows};
-    unsigned grid;
-    nm_status s = grid_of(b.n_tokens * (c.n_kv_heads + (q ? n_q_heads : 0)), &grid);
-    if (s != NM_OK)
-        return s;
+    AppendArgs a{layer, n_q_heads, (const uint16_t *)k, (const uint16_t *)v, (const uint16_t *)q,
+                 (uint16_t *)q_out, k_stride, v_stride, q_stride, q_out_stride, rope, rope_rows, 0, 0, 1, 1};
+    a.slots = slots_of(b) * c.n_kv_heads;
+    a.cell_ctas = (a.slots + 7) / 8;
+    int64_t grid = a.cell_ctas;
+    if (q) {
+        // with many tokens a warp turns up to four fours of a token's heads, so that its angles are read once
+        const int fours = (n_q_heads + 3) / 4;
+        a.q_each = b.n_tokens * fours >= 65536 ? (fours < 4 ? fours : 4) : 1;
+        a.q_warps = (fours + a.q_each - 1) / a.q_each;
+        grid += (b.n_tokens * a.q_warps + 7) / 8;
+    }
+    if (grid > 0x7FFFFFFF)
+        return NM_ERR_SHAPE;
     if (c.head_dim == 128)
-        append_kernel<128><<<grid, 256, 0, st>>>(c, b, a);
+        append_kernel<128><<<(unsigned)grid, 256, 0, st>>>(c, b, a);
     else
-        append_kernel<64><<<grid, 256, 0, st>>>(c, b, a);
+        append_kernel<64><<<(unsigned)grid, 256, 0, st>>>(c, b, a);
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
 
 nm_status kv4_launch_read(const Kv4 &c, const Kv4Batch &b, int layer, void *k, void *v, bool f32, cudaStream_t st)
 {
-    unsigned grid;
-    nm_status s = grid_of(b.n_tokens * c.n_kv_heads, &grid);
-    if (s != NM_OK)
-        return s;
+    const int64_t slots = slots_of(b) * c.n_kv_heads, grid = (slots + 7) / 8;
+    if (grid > 0x7FFFFFFF)
+        return NM_ERR_SHAPE;
     if (c.head_dim == 128) {
         if (f32)
-            read_kernel<128, true><<<grid, 256, 0, st>>>(c, b, layer, k, v);
+            read_kernel<128, true><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots);
         else
-            read_kernel<128, false><<<grid, 256, 0, st>>>(c, b, layer, k, v);
+            read_kernel<128, false><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots);
     } else {
         if (f32)
-            read_kernel<64, true><<<grid, 256, 0, st>>>(c, b, layer, k, v);
+            read_kernel<64, true><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots);
         else
-            read_kernel<64, false><<<grid, 256, 0, st>>>(c, b, layer, k, v);
+            read_kernel<64, false><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots);
     }
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
