@@ -6,8 +6,7 @@
 // vector, the two halves that a rotation turns together, so a rotation stays in the
 // lane and a group's least and greatest values take three shuffles. The four tokens
 // are 2 t, 2 t + 1, 2 t + 8, 2 t + 9 for t = 0 .. 3: together they fill 16 bytes of
-// V's codes, so a cell is written in full sectors. All loads of a cell are asked for
-// first. The q heads are turned by other warps of the same launch, four heads of a
+// V's codes, so a cell is written in full sectors. The q heads are turned by other warps of the same launch, four heads of a
 // token at a time with the token's angles in registers.
 //
 // Bytes bound it: k, v, q and q_out once, the angles once per SM and token.
@@ -16,7 +15,6 @@
 namespace nm {
 namespace {
 
-__device__ __forceinline__ bool finite_f32(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
 __device__ __forceinline__ float saturate(float x)
 {
     return x != x ? 0.0f : fminf(fmaxf(x, -kKv4Limit), kKv4Limit);
@@ -94,17 +92,32 @@ template <int N> __device__ __forceinline__ uint32_t codes_of(const float *x, fl
 {
     constexpr float kMagic = 12582912.0f; // 1.5 * 2^23: adding it rounds to a whole number, ties to even
     const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-    uint32_t r = 0;
+    float whole[N], far = 0.0f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        const float d = __fsub_rn(x[n], mid);
-        float t = fminf(fmaxf(d * inv, -8.0f), 7.0f);
-        float u = t + kMagic;
-        if (fabsf(fabsf(t - (u - kMagic)) - 0.5f) < 1e-4f) {
-            t = fminf(fmaxf(__fdiv_rn(d, s), -8.0f), 7.0f);
-            u = t + kMagic;
+        const float t = fminf(fmaxf(__fsub_rn(x[n], mid) * inv, -8.0f), 7.0f);
+        whole[n] = (t + kMagic) - kMagic;
+        far = fmaxf(far, fabsf(t - whole[n]));
+    }
+    if (far > 0.4999f) {
+#pragma unroll 1
+        for (int n = 0; n < N; ++n) {
+            float y = x[0];
+#pragma unroll
+            for (int m = 1; m < N; ++m)
+                y = m == n ? x[m] : y;
+            const float w = rintf(fminf(fmaxf(__fdiv_rn(__fsub_rn(y, mid), s), -8.0f), 7.0f));
+#pragma unroll
+            for (int m = 0; m < N; ++m)
+                whole[m] = m == n ? w : whole[m];
         }
-        r |= ((__float_as_uint(u) + 8u) & 15u) << (4 * n);
+    }
+    // four codes to a number below 2^16: sums of code * 16^k are exact
+    uint32_t r = 0;
+#pragma unroll
+    for (int n = 0; n < N; n += 4) {
+        const float four = fmaf(whole[n + 3], 4096.0f, fmaf(whole[n + 2], 256.0f, fmaf(whole[n + 1], 16.0f, whole[n] + 34952.0f)));
+        r |= (__float_as_uint(four + 8388608.0f) & 0xFFFFu) << (4 * n); // 34952 = 8 * 0x1111
     }
     return r;
 }
@@ -126,41 +139,57 @@ template <int D> __device__ __forceinline__ Coded<D> encode(Vec<D / 16> &k, Vec<
 {
     constexpr int N = D / 16, G = D / 64;
     Coded<D> r;
-    bool fine = true;
+    float lo[2][2], hi[2][2], none = 0.0f; // [K, V][half]; 0 * x is NaN for what is not finite
+    const auto bounds = [&]() {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float *z = kv ? v.x[h] : k.x[h];
+                lo[kv][h] = hi[kv][h] = z[0];
+#pragma unroll
+                for (int n = 1; n < N; ++n) {
+                    lo[kv][h] = fminf(lo[kv][h], z[n]);
+                    hi[kv][h] = fmaxf(hi[kv][h], z[n]);
+                }
+            }
+    };
+    bounds();
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            fine = fine && finite_f32(k.x[h][n]) && finite_f32(v.x[h][n]);
+            none = fmaf(v.x[h][n], 0.0f, fmaf(k.x[h][n], 0.0f, none));
+    bool fine = none == 0.0f;
+    const float least = fminf(fminf(lo[0][0], lo[0][1]), fminf(lo[1][0], lo[1][1]));
+    const float most = fmaxf(fmaxf(hi[0][0], hi[0][1]), fmaxf(hi[1][0], hi[1][1]));
     const uint32_t votes = __ballot_sync(~0u, fine);
+    if (__any_sync(~0u, !fine || least < -kKv4Limit || most > kKv4Limit)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                k.x[h][n] = saturate(k.x[h][n]);
+                v.x[h][n] = saturate(v.x[h][n]);
+            }
+        bounds();
+    }
     fine = ((votes >> (threadIdx.x & 24)) & 0xFFu) == 0xFFu; // all eight lanes of the token
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
         Vec<N> &z = kv ? v : k;
-        float lo[2], hi[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            lo[h] = INFINITY;
-            hi[h] = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                z.x[h][n] = saturate(z.x[h][n]);
-                lo[h] = fminf(lo[h], z.x[h][n]);
-                hi[h] = fmaxf(hi[h], z.x[h][n]);
-            }
-        }
         if (G == 1) {
-            lo[0] = fminf(lo[0], lo[1]);
-            hi[0] = fmaxf(hi[0], hi[1]);
+            lo[kv][0] = fminf(lo[kv][0], lo[kv][1]);
+            hi[kv][0] = fmaxf(hi[kv][0], hi[kv][1]);
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) {
-                lo[g] = fminf(lo[g], __shfl_xor_sync(~0u, lo[g], o));
-                hi[g] = fmaxf(hi[g], __shfl_xor_sync(~0u, hi[g], o));
+                lo[kv][g] = fminf(lo[kv][g], __shfl_xor_sync(~0u, lo[kv][g], o));
+                hi[kv][g] = fmaxf(hi[kv][g], __shfl_xor_sync(~0u, hi[kv][g], o));
             }
-            r.par[kv][g] = params_of(lo[g], hi[g]);
+            r.par[kv][g] = params_of(lo[kv][g], hi[kv][g]);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -261,27 +290,25 @@ template <int D> __device__ __forceinline__ void append_cell(const Kv4 &c, const
     uint8_t *const dst = c.pool + kv4_cell_offset<D>(c, page, a.layer, head, j.cell & ((c.page_tokens >> 4) - 1));
     const int base = j.cell * kKv4Cell;
     const auto slot_of = [&](int t) { return 2 * t + (part & 1) + 8 * (part >> 1); };
-    const auto mine = [&](int t) { return base + slot_of(t) >= j.from && base + slot_of(t) < j.to; };
-    Raw<N> rk[4], rv[4];
-#pragma unroll
+    // not unrolled: a decode step's one token runs a quarter of the code, and more warps fit an SM
+#pragma unroll 1
     for (int t = 0; t < 4; ++t) {
-        const int64_t token = (int64_t)j.s.first + (base + slot_of(t) - (j.s.len - j.s.n_new));
-        if (mine(t)) {
-            rk[t] = load_raw<N>(a.k + token * a.k_stride + (int64_t)head * D, i, D / 2);
-            rv[t] = load_raw<N>(a.v + token * a.v_stride + (int64_t)head * D, i, D / 2);
-        } else {
-            rk[t] = rv[t] = Raw<N>{};
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const bool ok = mine(t);
+        const int slot = slot_of(t);
+        const bool ok = base + slot >= j.from && base + slot < j.to;
         if (!__any_sync(~0u, ok))
             continue;
-        const int slot = slot_of(t);
-        Vec<N> k = unpack<N>(rk[t]), v = unpack<N>(rv[t]);
-        if (a.rope && ok)
-            rotate<N>(k, load_turn<N>(a.rope + (int64_t)(base + slot) * D, i));
+        const int64_t token = (int64_t)j.s.first + (base + slot - (j.s.len - j.s.n_new));
+        Raw<N> rk{}, rv{};
+        Turn<N> turn{};
+        if (ok) {
+            rk = load_raw<N>(a.k + token * a.k_stride + (int64_t)head * D, i, D / 2);
+            rv = load_raw<N>(a.v + token * a.v_stride + (int64_t)head * D, i, D / 2);
+            if (a.rope)
+                turn = load_turn<N>(a.rope + (int64_t)(base + slot) * D, i);
+        }
+        Vec<N> k = unpack<N>(rk), v = unpack<N>(rv);
+        if (a.rope)
+            rotate<N>(k, turn);
         const Coded<D> e = encode<D>(k, v);
         // K: the token's row; half h of lane i: channels h D/2 + i N ..
         if (ok) {
@@ -374,7 +401,7 @@ template <int D> __device__ __forceinline__ void append_q(const Kv4 &c, const Kv
     }
 }
 
-template <int D> __global__ void __launch_bounds__(256) append_kernel(const Kv4 c, const Kv4Batch b, const AppendArgs a)
+template <int D> __global__ void __launch_bounds__(256, 4) append_kernel(const Kv4 c, const Kv4Batch b, const AppendArgs a)
 {
     const int warp = threadIdx.x >> 5;
     if (blockIdx.x < a.cell_ctas) {
@@ -415,7 +442,7 @@ __global__ void __launch_bounds__(256) read_kernel(const Kv4 c, const Kv4Batch b
         kv4_bad(c);
     const uint8_t *const src =
         page < 0 ? nullptr : c.pool + kv4_cell_offset<D>(c, page, layer, head, j.cell & ((c.page_tokens >> 4) - 1));
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 4; ++t) {
         const int slot = 2 * t + (part & 1) + 8 * (part >> 1), pos = j.cell * kKv4Cell + slot;
         if (pos < j.from || pos >= j.to)
