@@ -40,8 +40,11 @@ constexpr int kSoft = 256;      // softmax threads: two tiles of 128 rows
 constexpr int kUnpack = 256;    // unpacking threads
 constexpr int kMmaWarp = 16;    // of its warpgroup, the next one lists the pieces and two idle
 constexpr int kThreads = 640;
-// Registers of a thread in each role; 96 at launch, and 2 * 160 + 2 * 64 + 32 = 5 * 96.
-constexpr int kSoftRegs = 160, kUnpackRegs = 64, kMmaRegs = 32;
+// Registers of a thread: at launch (what 640 threads can have), and in each role.
+constexpr int kLaunchRegs = 96, kSoftRegs = 160, kUnpackRegs = 64, kMmaRegs = 32;
+static_assert(kSoftRegs >= kLaunchRegs && kUnpackRegs <= kLaunchRegs && kMmaRegs <= kLaunchRegs &&
+                  kSoft * kSoftRegs + kUnpack * kUnpackRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs,
+              "a role that takes registers waits until others have given them back");
 constexpr int kSeqCache = 512;  // sequences whose descriptors are kept in shared memory
 constexpr int kBlock = 128;    // tokens of a block
 constexpr int kMinShare = 2;   // blocks of a CTA at least
