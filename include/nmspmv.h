@@ -494,6 +494,8 @@ nm_status nm_obs_release_workspace(void);
  *     first 8192 bytes zeroed once before its first use (nm_kv4_init does). Calls with the same
  *     workspace, or that change the same bookkeeping, must not overlap on the
  *     GPU; calls with caches of their own may.
+ *   - Waits in the kernels are bounded; after an NM_ERR_TIMEOUT the workspace's first
+ *     8192 bytes are to be zeroed before its next use.
  *   - All calls are asynchronous, allocate nothing but the library's per-device
  *     scratch (for its status word), and can be captured in a CUDA graph.
  */

@@ -503,3 +503,91 @@ def test_tables_out_of_range_are_reported(nm):
     out = c.attention(1, q, starts=ints([0, 1, 3]))
     assert nm.device_status() == nm.NM_ERR_BOUNDS and torch.equal(out[0], good[0])
     assert torch.equal(c.attention(1, q), good) and nm.device_status() == nm.NM_OK
+
+
+def test_read_rows_that_are_not_there(nm):
+    """More rows asked for than a sequence has: zeros, and the status tells."""
+    c, K, V = make(nm, [5, 0, 20], seed=91)
+    k, v = c.read(1, 8 + 3 + 4, starts=starts_of([8, 3, 4]), f32=True)
+    assert nm.device_status() == nm.NM_ERR_BOUNDS
+    assert bool((k[:3] == 0).all()) and bool((v[:3] == 0).all()) and bool((k[8:11] == 0).all())
+    np.testing.assert_array_equal(f32(k[3:8]), K[0])
+    np.testing.assert_array_equal(f32(v[11:]), V[2][-4:])
+
+
+@pytest.mark.parametrize("max_new", [1, 64])
+def test_attention_nonfinite_queries_stay_in_their_rows(nm, max_new):
+    c, K, V = make(nm, [100], seed=92)
+    q = values(40, 8, 128, 93)
+    good = c.attention(1, q, starts=ints([0, 40]), max_new=max_new)
+    bad = q.clone()
+    bad[7, 3, 11], bad[20, 6, 5] = float("nan"), float("inf")
+    out = c.attention(1, bad, starts=ints([0, 40]), max_new=max_new)
+    same = torch.ones(40, 8, dtype=torch.bool, device="cuda")
+    same[7, 3] = same[20, 6] = False
+    assert torch.equal(out[same], good[same]) and bool(torch.isnan(out[7, 3]).all())
+
+
+@pytest.mark.parametrize("new,max_new", [(1, 1), (9, 9), (3, 1000)])
+def test_attention_many_sequences(nm, new, max_new):
+    """1024 sequences in a call, short ones and a long one, through each kernel."""
+    n = 1024
+    r = np.random.RandomState(new)
+    lens = (r.randint(0, 40, n) + new).tolist()
+    lens[700] = 3000
+    c, K, V = make(nm, lens, P=16, L=1, Hk=1, D=64, seed=94)
+    q = values(n * new, 4, 64, 95)
+    out, lse = c.attention(0, q, starts=starts_of([new] * n), max_new=max_new, lse=True)
+    assert nm.device_status() == nm.NM_OK
+    for s in (0, 1, 511, 512, 513, 699, 700, 701, 1023):
+        rows = slice(s * new, (s + 1) * new)
+        o, l, A, B = ref.attention(f64(q[rows]), K[s].astype(np.float64), V[s].astype(np.float64), lens[s], 0.125)
+        e = 2.0 ** -16 * B + 2.0 ** -15
+        assert np.all(np.abs(f64(lse[rows]) - l) <= e)
+        tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e[..., None] + 2.0 ** -14) * A + lens[s] * 2.0 ** -30 * 8
+        assert np.all(np.abs(f64(out[rows]) - o) <= tol)
+
+
+# --- used together -----------------------------------------------------------------------
+
+def test_example_decode_loop(nm):
+    """The example's loop: every attention result against the definition, on the q, k, v that went in."""
+    from examples import paged_decode as ex
+    d = ex.Decoder(layers=2, hidden=256, heads=8, kv_heads=2, dim=64, ffn=512, sequences=3, tokens=80, page=16, seed=5)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    prompt = torch.randn(37, 256, generator=g, device="cuda").bfloat16()
+    traces, step = [], d.step
+
+    def traced(x, seqs, starts=None):
+        t = []
+        y = step(x, seqs, starts, trace=t)
+        traces.append((seqs.tolist(), None if starts is None else starts.tolist(), t))
+        return y
+
+    d.step = traced
+    out = ex.run(d, prompt, 3, 4)
+    assert len(out) == 4 and nm.device_status() == nm.NM_OK
+    rope = d.rope.cpu().numpy()
+    held = [[([], []) for _ in range(2)] for _ in range(3)]  # [sequence][layer]: K, V as held
+    for seqs, starts, layers in traces:
+        if starts is None and len(held[1][0][0]) == 0:  # the fork came before the first joint step
+            for s in (1, 2):
+                held[s] = [(list(k), list(v)) for k, v in held[0]]
+        starts = starts or list(range(len(seqs) + 1))
+        for layer, (q, k, v, a) in enumerate(layers):
+            q, k, v = (f32(t).reshape(t.shape[0], -1, 64) for t in (q, k, v))
+            for i, s in enumerate(seqs):
+                K, V = held[s][layer]
+                rows = slice(starts[i], starts[i + 1])
+                pos = np.arange(len(K), len(K) + starts[i + 1] - starts[i])
+                cos, sin = rope[pos, :32], rope[pos, 32:]
+                rk, rv = ref.quantise(ref.rotate(k[rows], cos, sin), v[rows])
+                K.extend(rk)
+                V.extend(rv)
+                rq = ref.bf16(ref.rotate(q[rows], cos, sin)).astype(np.float64)
+                o, _, A, B = ref.attention(rq, np.array(K, np.float64), np.array(V, np.float64), len(K), 0.125)
+                e = 2.0 ** -16 * B[..., None] + 2.0 ** -15
+                tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e + 2.0 ** -14) * A + 1e-6
+                assert np.all(np.abs(f64(a[rows]).reshape(o.shape) - o) <= tol)
+    assert d.cache.lens.tolist() == [41, 0, 0] and d.cache.info.tolist()[:2] == [d.cache.n_pages - 3, 0]
+    assert d.cache.tables[0, :3].sort().values.tolist() == [0, 1, 2]
