@@ -30,6 +30,7 @@
 // All waits are bounded; one that runs out sets NM_ERR_TIMEOUT and the kernel
 // frees its tensor memory and returns.
 #include <mutex>
+#include <type_traits>
 
 #include "kv4.cuh"
 
@@ -75,10 +76,18 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols)
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// The instructions that one thread issues are predicated (on `one`) instead of
-// branched around: the MMA warp's control flow stays uniform, so that descriptors
-// live in uniform registers. In a branch of one lane each MMA waited for their
-// transfer (about 130 cycles between MMAs of 64).
+// The instructions that one thread issues are predicated on the elected lane (`one`)
+// instead of branched around, and the MMA warp's control flow and the descriptors are
+// uniform: then an MMA is few instructions. That matters because the tensor cores
+// take the next MMA only when they are done with one: with six busy warps beside it
+// on its scheduler the warp issued a 64-cycle MMA every 190 cycles from a branch of
+// one lane (or with a predicate of lane == 0), and every 88 cycles like this.
+__device__ __forceinline__ uint32_t elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+    return r;
+}
 __device__ __forceinline__ void commit(uint32_t bar, uint32_t one)
 {
     asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
@@ -169,6 +178,13 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t *r)
                    "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
                    "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(taddr));
+}
+// Keeps the uses of loaded registers behind the wait before it.
+template <int N> __device__ __forceinline__ void tie(uint32_t *r)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+r"(r[i]));
 }
 template <int N> __device__ __forceinline__ void setmaxnreg_inc()
 {
@@ -613,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     if (nk > 0) {
                         ld16(t_o + 16 * h, o);
                         wait_ld();
+                        tie<16>(o);
                     }
 #pragma unroll
                     for (int e = 0; e < 16; e += 4)
@@ -657,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     if (nk > 0) {
                         ld16(t_o + 16 * h, o);
                         wait_ld();
+                        tie<16>(o);
                     }
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -714,11 +732,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 fence_after();
                 const int vis = limit - (w.b0 + i) * kBlock; // columns this row sees
                 uint32_t r[128];
-                float mx = -INFINITY;
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
                     ld32(t_s + 32 * h, r + 32 * h);
                 wait_ld();
+                tie<128>(r);
                 if (!__all_sync(~0u, vis >= kBlock)) { // only the last blocks of a row come here
 #pragma unroll
                     for (int e = 0; e < 128; ++e)
@@ -727,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 // the maximum; it is raised when a score passes it by more than the slack
 #pragma unroll
                 for (int e = 0; e < 128; e += 2)
-                    mx = fmaxf(fmaxf(mx, __uint_as_float(r[e])), __uint_as_float(r[e + 1]));
-                mx *= rs;
+                    top[(e / 2) & 3] = fmaxf(fmaxf(top[(e / 2) & 3], __uint_as_float(r[e])), __uint_as_float(r[e + 1]));
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * rs;
                 if (__any_sync(~0u, mx > m + kSlack)) {
                     const float mn = fmaxf(m, mx);
                     const float f = mn == m ? 1.0f : exp2_approx(m - mn);
@@ -740,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                             uint32_t o[16];
                             ld16(t_o + 16 * h, o);
                             wait_ld();
+                            tie<16>(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
@@ -886,14 +906,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         setmaxnreg_dec<kMmaRegs>();
     } else {
         setmaxnreg_dec<kMmaRegs>();
-        // ---- the MMAs: every lane follows, lane 0 issues ----
-        const uint32_t one = lane == 0;
-        const uint32_t tmem = __reduce_max_sync(~0u, sh.tmem); // uniform
+        // ---- the MMAs: every lane follows, one issues ----
+        const uint32_t one = elect();
+        constexpr uint32_t tmem = 0; // all 512 columns are this kernel's: they start at 0
 
         uint32_t n = 0, n_p0 = 0, n_p1 = 0, n_q0 = 0, n_q1 = 0;
         const uint32_t desc0 = kDescLo | (tiles >> 4);
-        const auto scores = [&](int k, uint32_t blk) { // S of tile k
-            const uint32_t q = desc0 + k * (C::kQ >> 4), kk = desc0 + (C::kOffK >> 4) + (blk & 1) * (C::kQ >> 4);
+        const auto scores = [&](int k, int stage) { // S of tile k, K in `stage`
+            const uint32_t q = desc0 + k * (C::kQ >> 4), kk = desc0 + (C::kOffK >> 4) + stage * (C::kQ >> 4);
             const uint32_t d = tmem + k * 128;
 #pragma unroll
             for (int g = 0; g < G; ++g)
@@ -903,8 +923,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             mma_ss<32>(d, q + ((G * kSub) >> 4), kk + ((G * kSub) >> 4), kIdesc<128>, 1, one);
             commit(smem_addr(&sh.s_full[k]), one);
         };
-        const auto values = [&](int k, uint32_t blk, uint32_t accumulate) { // O of tile k
-            const uint32_t v = desc0 + (C::kOffV >> 4) + (blk & 1) * (C::kV >> 4);
+        const auto values = [&](int k, int stage, uint32_t accumulate) { // O of tile k, V in `stage`
+            const uint32_t v = desc0 + (C::kOffV >> 4) + stage * (C::kV >> 4);
             const uint32_t d = tmem + 256 + k * 128, p = tmem + k * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -913,57 +933,72 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     mma_ts(d, p + 32 * h + 8 * x, v + ((h * (D * 128) + 32 * x) >> 4), kIdesc<D>,
                            h + x > 0 ? 1u : accumulate, one);
         };
-        uint32_t piece = 0;
-#pragma unroll 1
-        for (;;) {
-            const Piece w = get_piece(piece++);
-            const int nblk = __reduce_max_sync(~0u, w.nblk); // uniform, as the lanes agree
-            const int n0 = __reduce_max_sync(~0u, w.n0), n1 = __reduce_max_sync(~0u, w.n1);
-            if (nblk == 0)
-                break;
-            // per step: O of block i, then S of block i + 1, tile by tile
-#pragma unroll 1
-            for (int i = -1; i < nblk; ++i) {
-                const bool more = i + 1 < nblk;
-                const uint32_t cur = n + i, nxt = cur + 1;
-                if (i >= 0)
-                    wait(sh.v_full[cur & 1], cur >> 1);
-                if (i >= 0 && i < n0) {
+        // O of block i of a piece (block n - 1 of the CTA), then S of block i + 1 (block n), tile by
+        // tile. The stages are constants of two copies of this, so that all descriptors are uniform.
+        int nblk, n0, n1;
+        const auto step = [&](auto parity, int i) {
+            constexpr int nxt = decltype(parity)::value, cur = nxt ^ 1; // n & 1, (n - 1) & 1
+            const bool more = i + 1 < nblk;
+            if (i >= 0) {
+                wait(sh.v_full[cur], (n - 1) >> 1);
+                if (i < n0) {
                     wait(sh.p_full[0], n_p0++);
                     fence_after();
                     values(0, cur, i > 0);
                     if (i == n0 - 1)
                         commit(smem_addr(&sh.o_full[0]), one);
                 }
-                if (more) {
-                    wait(sh.k_full[nxt & 1], nxt >> 1);
-                    if (i + 1 < n0) {
-                        if (i < 0)
-                            wait(sh.q_full[0], n_q0++);
-                        fence_after();
-                        scores(0, nxt);
-                    }
+            }
+            if (more) {
+                wait(sh.k_full[nxt], n >> 1);
+                if (i + 1 < n0) {
+                    if (i < 0)
+                        wait(sh.q_full[0], n_q0++);
+                    fence_after();
+                    scores(0, nxt);
                 }
-                if (i >= 0 && i < n1) {
+            }
+            if (i >= 0) {
+                if (i < n1) {
                     wait(sh.p_full[1], n_p1++);
                     fence_after();
                     values(1, cur, i > 0);
                     if (i == n1 - 1)
                         commit(smem_addr(&sh.o_full[1]), one);
                 }
-                if (i >= 0)
-                    commit(smem_addr(&sh.v_empty[cur & 1]), one);
-                if (more) {
-                    if (i + 1 < n1) {
-                        if (i < 0)
-                            wait(sh.q_full[1], n_q1++);
-                        fence_after();
-                        scores(1, nxt);
-                    }
-                    commit(smem_addr(&sh.k_empty[nxt & 1]), one);
-                }
+                commit(smem_addr(&sh.v_empty[cur]), one);
             }
-            n += nblk;
+            if (more) {
+                if (i + 1 < n1) {
+                    if (i < 0)
+                        wait(sh.q_full[1], n_q1++);
+                    fence_after();
+                    scores(1, nxt);
+                }
+                commit(smem_addr(&sh.k_empty[nxt]), one);
+                ++n;
+            }
+        };
+        uint32_t piece = 0;
+#pragma unroll 1
+        for (;;) {
+            wait(sh.piece_full[piece % kRing], piece / kRing);
+            nblk = sh.piece[piece % kRing].nblk;
+            n0 = sh.piece[piece % kRing].n0;
+            n1 = sh.piece[piece % kRing].n1;
+            __syncwarp();
+            if (one)
+                kv4_arrive(smem_addr(&sh.piece_empty[piece % kRing]));
+            ++piece;
+            if (nblk == 0)
+                break;
+#pragma unroll 1
+            for (int i = -1; i < nblk; ++i) {
+                if (n & 1)
+                    step(std::integral_constant<int, 1>{}, i);
+                else
+                    step(std::integral_constant<int, 0>{}, i);
+            }
         }
         // before leaving, the MMAs in flight end (bounded): the last stages are released
         if (n > 0) {
