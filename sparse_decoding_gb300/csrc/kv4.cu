@@ -9,7 +9,11 @@
 // V's codes, so a cell is written in full sectors. The q heads are turned by other warps of the same launch, four heads of a
 // token at a time with the token's angles in registers.
 //
-// Bytes bound it: k, v, q and q_out once, the angles once per SM and token.
+// Bytes should bound it: k, v, q and q_out once, the angles once per SM and token.
+// Measured (one GB300; 16384 tokens, 32 and 8 heads, D = 128): append 86 us (362 MB,
+// 0.62 of the measured copy rate; 90000 instructions a scheduler, half of them the
+// quantisation, waiting for each cell's loads), read 22 us. A warp per token and head
+// with a division for each value took 138 us.
 #include "kv4.cuh"
 
 namespace nm {

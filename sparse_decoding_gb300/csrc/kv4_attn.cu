@@ -26,6 +26,15 @@
 // units (pairs of cells) of each warp. A CTA's warps take the units of a piece in
 // turn and are joined in shared memory. A segment that was cut is joined by the
 // last of its CTAs, in CTA order, from the workspace.
+//
+// Measured (one GB300, D = 128): 131071 tokens, 64 query heads over 8: 43 us, 3.5 TB/s
+// (0.52 of the measured copy rate; the cache is read once): about 340 instructions a
+// cell, at 0.56 a cycle and scheduler, bound it with 8 us of start and joins; eight
+// sequences of 1 to 8191 tokens 19 us, four times five drafted tokens (25 rows) at
+// 9001 to 16385 tokens 48 us (254 registers leave two warps a scheduler), 129 tokens
+// 8.9 us. Steps on the way for the first: 67 us with loads straight to registers; 62
+// by bulk copies; 50.6 with masks at the end only and addresses a round ahead; 43.9
+// two cells at a time and a join of independent loads.
 #include <mutex>
 #include <type_traits>
 
