@@ -844,9 +844,22 @@ nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
 {
     const AttnArgs a{at.layer, at.n_q_heads / c.n_kv_heads, at.n_q_heads, (const uint16_t *)at.q, at.q_stride,
                      at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials};
-    if (max_new * a.ratio > 32)
+    // By the rows of a kv head. Measured, in us, with 8 kv heads, D = 128 (sequences x new tokens
+    // of 4 query heads, tokens in the cache):
+    //                          NT = 1    2      4    prompt
+    //    8 rows (4 x 2, 12k)     23.2   31.6   46.0    70.3
+    //   10 rows (4 x 2 of 5)     35.5   31.9   46.0    70.6
+    //   16 rows (1 x 4, 32k)     27.0   30.4   37.3    77.2   (4 x 4, 4k: 19.1 21.4 26.0 43.2)
+    //   32 rows (4 x 8, 12k)     55.7   48.0   46.0    70.6
+    //   48 rows (4 x 12, 12k)    74.7   60.3   70.3    70.6
+    //   64 rows (1 x 16, 32k)    67.2   58.0   55.2    78.8   (4 x 16, 8k: 68.5 56.5 53.9 58.0)
+    //   96 rows (4 x 24, 8k)     95.9   78.8   71.1    58.0
+    //  128 rows (1 x 32, 32k)   119.7   95.1   84.9    77.5   (8 x 32, 512: 35.2 27.3 25.2 37.8)
+    //  256 rows (4 x 64, 8k)    233.4  177.0  154.3    60.8
+    const int64_t rows = (max_new < 65 ? max_new : 65) * a.ratio;
+    if (rows > 64)
         return kv4_launch_prompt(c, b, at, w, num_sms, st);
-    const int nt = max_new * a.ratio <= 8 ? 1 : max_new * a.ratio <= 16 ? 2 : 4;
+    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     if (c.head_dim == 128)
         return nt == 1   ? launch_rows<128, 1>(c, b, a, num_sms, st)
                : nt == 2 ? launch_rows<128, 2>(c, b, a, num_sms, st)

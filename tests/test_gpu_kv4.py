@@ -219,6 +219,18 @@ def test_attention_prompts(nm, D, Hk, Hq, P, lens, new):
     assert bool(torch.isclose(lse, lf, rtol=0, atol=1e-3).all())
 
 
+@pytest.mark.parametrize("D,Hq", [(128, 1), (128, 4), (64, 7), (64, 1), (128, 64)])
+@pytest.mark.parametrize("rows", [17, 31, 33, 40, 63, 64, 65, 72])
+def test_attention_of_one_and_several_tiles(nm, D, Hq, rows):
+    new = -(-rows // Hq)
+    lens, news = [new + 5, 3001, 0, 64], [new, new, 0, 1]  # one sequence is cut over the CTAs
+    c, K, V = make(nm, lens, P=16, L=1, Hk=1, D=D, seed=rows)
+    check_attention(nm, c, K, V, lens, news, Hq, 0, max_new=new)
+    lens, news = [80] * 200, [new] * 200  # more segments than CTAs
+    c, K, V = make(nm, lens, P=16, L=1, Hk=1, D=D, seed=rows)
+    check_attention(nm, c, K, V, lens, news, Hq, 0, max_new=new)
+
+
 def test_attention_rows_with_nothing_to_attend(nm):
     """More new tokens than the sequence has, and an empty sequence: zeros and -inf."""
     lens, new = [5, 0, 20], [8, 3, 25]
