@@ -31,8 +31,8 @@
 // (0.52 of the measured copy rate; the cache is read once): about 340 instructions a
 // cell, at 0.56 a cycle and scheduler, bound it with 8 us of start and joins; eight
 // sequences of 1 to 8191 tokens 19 us, four times five drafted tokens (25 rows) at
-// 9001 to 16385 tokens 48 us (254 registers leave two warps a scheduler), 129 tokens
-// 8.9 us. Steps on the way for the first: 67 us with loads straight to registers; 62
+// 9001 to 16385 tokens 48 us (254 registers leave two warps a scheduler), 20 rows of
+// four sequences of 12288 tokens 40 us, 129 tokens 8.9 us. Steps on the way for the first: 67 us with loads straight to registers; 62
 // by bulk copies; 50.6 with masks at the end only and addresses a round ahead; 43.9
 // two cells at a time and a join of independent loads.
 #include <mutex>
@@ -844,29 +844,39 @@ nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
 {
     const AttnArgs a{at.layer, at.n_q_heads / c.n_kv_heads, at.n_q_heads, (const uint16_t *)at.q, at.q_stride,
                      at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials};
-    // By the rows of a kv head. Measured, in us, with 8 kv heads, D = 128 (sequences x new tokens
-    // of 4 query heads, tokens in the cache):
-    //                          NT = 1    2      4    prompt
-    //    8 rows (4 x 2, 12k)     23.2   31.6   46.0    70.3
-    //   10 rows (4 x 2 of 5)     35.5   31.9   46.0    70.6
-    //   16 rows (1 x 4, 32k)     27.0   30.4   37.3    77.2   (4 x 4, 4k: 19.1 21.4 26.0 43.2)
-    //   32 rows (4 x 8, 12k)     55.7   48.0   46.0    70.6
-    //   48 rows (4 x 12, 12k)    74.7   60.3   70.3    70.6
-    //   64 rows (1 x 16, 32k)    67.2   58.0   55.2    78.8   (4 x 16, 8k: 68.5 56.5 53.9 58.0)
-    //   96 rows (4 x 24, 8k)     95.9   78.8   71.1    58.0
-    //  128 rows (1 x 32, 32k)   119.7   95.1   84.9    77.5   (8 x 32, 512: 35.2 27.3 25.2 37.8)
-    //  256 rows (4 x 64, 8k)    233.4  177.0  154.3    60.8
+    // By the rows of a kv head. Measured, in us, with 8 kv heads (sequences x new tokens of 4 query
+    // heads, tokens in the cache; k: 1024):
+    //   D = 128                  NT = 1    2      3      4    prompt
+    //    8 rows (4 x 2, 12k)     23.2   31.6          46.0    70.3
+    //   12 rows (4 x 3, 12k)     35.5   32.9   39.6   45.7    70.3
+    //   16 rows (1 x 4, 32k)     27.0   30.4          37.3    77.2   (4 x 4, 12k: 35.5 33.2 39.6 45.7 69.8)
+    //   20 rows (4 x 5, 12k)     43.7   47.8   39.6   45.7    70.0   (1 x 5, 32k: 33.5 37.5 31.4 37.5 78.8)
+    //   32 rows (4 x 8, 12k)     55.5   48.0   58.0   46.0    69.8
+    //   48 rows (4 x 12, 12k)    74.4   60.1   58.0   70.3    70.3   (1 x 12, 32k: 53.9 47.8 45.7 54.4 87.7)
+    //   64 rows (4 x 16, 12k)    94.9   78.0   78.5   70.3    70.3   (1 x 16, 32k: 67.2 58.0 - 55.2 78.8)
+    //   96 rows (4 x 24, 8k)     95.9   78.8          71.1    58.0
+    //  128 rows (1 x 32, 32k)   119.7   95.1          84.9    77.5   (8 x 32, 512: 35.2 27.3 - 25.2 37.8)
+    //  256 rows (4 x 64, 8k)    233.4  177.0         154.3    60.8
+    //   D = 64
+    //   16 rows (4 x 4, 12k)     25.3   23.2   29.9   33.4    53.9
+    //   20 rows (4 x 5, 12k)     29.4   33.4   30.9   33.4    53.9
+    //   32 rows (4 x 8, 12k)     37.6   33.4   43.7   33.4    53.9
+    //   48 rows (4 x 12, 12k)    50.1   39.6   43.2   47.8    53.9
+    //   64 rows (4 x 16, 8k)     47.3   37.5          37.5    43.7
+    //  128 rows (4 x 32, 8k)     80.5   63.1          58.0    40.9
     const int64_t rows = (max_new < 65 ? max_new : 65) * a.ratio;
     if (rows > 64)
         return kv4_launch_prompt(c, b, at, w, num_sms, st);
-    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    if (c.head_dim == 128)
-        return nt == 1   ? launch_rows<128, 1>(c, b, a, num_sms, st)
-               : nt == 2 ? launch_rows<128, 2>(c, b, a, num_sms, st)
-                         : launch_rows<128, 4>(c, b, a, num_sms, st);
-    return nt == 1   ? launch_rows<64, 1>(c, b, a, num_sms, st)
-           : nt == 2 ? launch_rows<64, 2>(c, b, a, num_sms, st)
-                     : launch_rows<64, 4>(c, b, a, num_sms, st);
+    if (c.head_dim == 64)
+        return rows <= 8                 ? launch_rows<64, 1>(c, b, a, num_sms, st)
+               : rows > 16 && rows <= 24 ? launch_rows<64, 3>(c, b, a, num_sms, st)
+                                         : launch_rows<64, 2>(c, b, a, num_sms, st);
+    return rows <= 8    ? launch_rows<128, 1>(c, b, a, num_sms, st)
+           : rows <= 16 ? launch_rows<128, 2>(c, b, a, num_sms, st)
+           : rows <= 24 ? launch_rows<128, 3>(c, b, a, num_sms, st)
+           : rows <= 32 ? launch_rows<128, 4>(c, b, a, num_sms, st)
+           : rows <= 48 ? launch_rows<128, 3>(c, b, a, num_sms, st)
+                        : launch_rows<128, 4>(c, b, a, num_sms, st);
 }
 
 } // namespace nm

@@ -220,7 +220,7 @@ def test_attention_prompts(nm, D, Hk, Hq, P, lens, new):
 
 
 @pytest.mark.parametrize("D,Hq", [(128, 1), (128, 4), (64, 7), (64, 1), (128, 64)])
-@pytest.mark.parametrize("rows", [17, 31, 33, 40, 63, 64, 65, 72])
+@pytest.mark.parametrize("rows", [17, 23, 24, 25, 31, 33, 48, 49, 63, 64, 65, 72])
 def test_attention_of_one_and_several_tiles(nm, D, Hq, rows):
     new = -(-rows // Hq)
     lens, news = [new + 5, 3001, 0, 64], [new, new, 0, 1]  # one sequence is cut over the CTAs
