@@ -32,9 +32,10 @@
 // cell, at 0.56 a cycle and scheduler, bound it with 8 us of start and joins; eight
 // sequences of 1 to 8191 tokens 19 us, four times five drafted tokens (25 rows) at
 // 9001 to 16385 tokens 48 us (254 registers leave two warps a scheduler), 20 rows of
-// four sequences of 12288 tokens 40 us, 129 tokens 8.9 us. Steps on the way for the first: 67 us with loads straight to registers; 62
-// by bulk copies; 50.6 with masks at the end only and addresses a round ahead; 43.9
-// two cells at a time and a join of independent loads.
+// four sequences of 12288 tokens 40 us, 129 tokens 8.9 us. Steps on the way for the
+// first: 67 us with loads straight to registers; 62 by bulk copies; 50.6 with masks at
+// the end only and addresses a round ahead; 43.9 two cells at a time and a join of
+// independent loads.
 #include <mutex>
 #include <type_traits>
 
