@@ -441,20 +441,25 @@ __device__ __forceinline__ void kv4_store_row(uint16_t *out, const float (&x)[16
     }
 }
 
-// Joins one row's parts of CTAs z0 .. z1 (parts: this tile's slot 0 of CTA 0), several parts at a
-// time, so that their loads are in flight together. Not inlined: beside the softmax loop its
-// registers cost that loop 4% (8192 tokens 548 -> 570 us).
+// Joins a row of the parts of n CTAs of a segment, z, z + step, ... (parts: this tile's slot 0 of
+// CTA 0; cta0: the segment's first), into the first of them (final: into out and lse, where they
+// are given). Four parts at a time, so that their loads are in flight together. Not inlined: beside
+// the softmax loop its registers cost that loop 4% (8192 tokens 548 -> 570 us).
 template <int D>
-__device__ __noinline__ void kv4_join(const float *parts, int z0, int z1, int row, uint16_t *out, float *lse)
+__device__ __noinline__ void kv4_join(float *parts, int cta0, int z, int step, int n, int row, bool final, uint16_t *out,
+                                      float *lse)
 {
-    const auto of = [&](int z) { return parts + ((int64_t)z * 2 + (z > z0 ? 0 : 1)) * 2 * Cfg<D>::kPart; };
+    const auto of = [&](int i) {
+        const int cta = z + (i < n ? i : n - 1) * step;
+        return parts + ((int64_t)cta * 2 + (cta > cta0 ? 0 : 1)) * 2 * Cfg<D>::kPart;
+    };
     float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
-    for (int z = z0; z <= z1; z += 8) {
+    for (int i = 0; i < n; i += 8) {
         float mz[8], lz[8], top = m;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const float *part = of(z + u < z1 ? z + u : z1);
+            const float *part = of(i + u);
             mz[u] = __ldcg(part + row);
             lz[u] = __ldcg(part + 128 + row);
         }
@@ -464,25 +469,25 @@ __device__ __noinline__ void kv4_join(const float *parts, int z0, int z1, int ro
         l *= m == top ? 1.0f : exp2_approx(m - top);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-            if (z + u <= z1)
+            if (i + u < n)
                 l = fmaf(mz[u] == top ? 1.0f : exp2_approx(mz[u] - top), lz[u], l);
         m = top;
     }
     if (lse)
         *lse = kv4_lse(m, l);
-    if (!out)
+    if (final && !out)
         return;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
     for (int h = 0; h < D / 16; ++h) {
         float x[16] = {};
 #pragma unroll 1
-        for (int z = z0; z <= z1; z += 4) {
+        for (int i = 0; i < n; i += 4) {
             float mz[4];
             float4 y[4][4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float *part = of(z + u < z1 ? z + u : z1);
+                const float *part = of(i + u);
                 mz[u] = __ldcg(part + row);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -490,7 +495,7 @@ __device__ __noinline__ void kv4_join(const float *parts, int z0, int z1, int ro
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (z + u > z1)
+                if (i + u >= n)
                     break;
                 const float f = mz[u] == m ? 1.0f : exp2_approx(mz[u] - m);
 #pragma unroll
@@ -502,7 +507,18 @@ __device__ __noinline__ void kv4_join(const float *parts, int z0, int z1, int ro
                 }
             }
         }
-        kv4_store_row(out + 16 * h, x, inv);
+        if (final) {
+            kv4_store_row(out + 16 * h, x, inv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *(float4 *)(of(0) + kv4_part_column(row, 16 * h + 4 * e)) =
+                    make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        }
+    }
+    if (!final) {
+        of(0)[row] = m;
+        of(0)[128 + row] = l;
     }
 }
 
@@ -716,12 +732,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             const int head = done.head * a.ratio + row_head;
             const bool valid = valid_in(done);
             const bool whole = done.nblk == done.total;
+            uint16_t *out = a.out + token * a.out_stride + (int64_t)head * D;
+            float *lse = a.lse && valid ? a.lse + token * a.n_q_heads + head : nullptr;
             // a part: m, l of the rows, then O, four channels of the rows side by side. A CTA has at
             // most one piece that goes on from another's (slot 0) and one that another goes on from.
             const auto part_at = [&](int cta, int slot) {
                 return a.partials + (((int64_t)cta * 2 + slot) * 2 + k) * C::kPart;
             };
-                        if (!whole) {
+            if (!whole) {
                 float *part = part_at(blockIdx.x, done.b0 > 0 ? 0 : 1);
                 part[row] = m;
                 part[128 + row] = l;
@@ -737,25 +755,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     for (int e = 0; e < 16; e += 4)
                         *(uint4 *)(part + kv4_part_column(row, 16 * h + e)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
-                // the last CTA of the segment to arrive joins the parts of this tile, in CTA order
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
-                if (row == 0) {
-                    const uint32_t before = atom_add_acq_rel_gpu(a.counters + 2 * done.cta0 + k, 1u);
-                    sh.last[k] = before == (uint32_t)(done.cta1 - done.cta0);
-                    if (sh.last[k])
-                        a.counters[2 * done.cta0 + k] = 0; // for the next launch
+                // The parts of this tile are joined by the last CTA to arrive, in CTA order: of many,
+                // first in groups of g (at most 16 to a join), then the groups (32 new tokens after
+                // 32768 by one join of 32 parts: 77 us).
+                const auto last_of = [&](uint32_t *counter, int n) {
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
+                    if (row == 0) {
+                        const uint32_t before = n > 1 ? atom_add_acq_rel_gpu(counter, 1u) : 0;
+                        sh.last[k] = before == (uint32_t)n - 1;
+                        if (n > 1 && sh.last[k])
+                            *counter = 0; // for the next launch
+                    }
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
+                    return sh.last[k] != 0;
+                };
+                const int n = done.cta1 - done.cta0 + 1;
+                const int g = n <= 8 ? n : n <= 16 ? 4 : n <= 64 ? 8 : n <= 144 ? 12 : (n + 15) / 16;
+                const int z = (int)blockIdx.x - (int)(blockIdx.x - done.cta0) % g; // the group's first
+                const int in = g < done.cta1 - z + 1 ? g : done.cta1 - z + 1, groups = (n + g - 1) / g;
+                // a group of one has no counter: its CTA may be the first of the next segment
+                bool all = last_of(a.counters + 2 * z + k, in);
+                if (all && groups > 1) {
+                    if (in > 1)
+                        kv4_join<D>(part_at(0, 0), done.cta0, z, 1, in, row, false, nullptr, nullptr);
+                    all = last_of(a.counters + kKv4Counters / 2 + 2 * done.cta0 + k, groups);
                 }
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
-                if (!sh.last[k]) {
-                    fence_before(); // the next MMAs on O follow this thread's next arrival
-                    return;
-                }
-            }
-            uint16_t *out = a.out + token * a.out_stride + (int64_t)head * D;
-            float *lse = a.lse && valid ? a.lse + token * a.n_q_heads + head : nullptr;
-            if (!whole) {
-                kv4_join<D>(part_at(0, 0), done.cta0, done.cta1, row, valid ? out : nullptr, lse);
-                fence_before();
+                if (all)
+                    kv4_join<D>(part_at(0, 0), done.cta0, done.cta0, groups > 1 ? g : 1, groups > 1 ? groups : n, row, true,
+                                valid ? out : nullptr, lse);
+                fence_before(); // the next MMAs on O follow this thread's next arrival
                 return;
             }
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
