@@ -865,8 +865,17 @@ nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
     //   48 rows (4 x 12, 12k)    50.1   39.6   43.2   47.8    53.9
     //   64 rows (4 x 16, 8k)     47.3   37.5          37.5    43.7
     //  128 rows (4 x 32, 8k)     80.5   63.1          58.0    40.9
+    // Of all tokens' query heads together, the prompt kernel's 20 to 50 us of start, and join, against
+    // tiles that read the cache again (one sequence, 32 heads, D = 128; tokens in the cache before):
+    //                               0     1000     8000     40000
+    //   24 new,  768    few      12.5     19.1     31.9      80.6
+    //                   prompt   20.9     31.4     46.8      73.1
+    //   32 new, 1024    few      12.7     23.2     35.5      99.0
+    //                   prompt   21.2     31.7     48.3      73.1
+    //   64 new, 2048    few      12.7     25.0     53.9     177
+    //                   prompt   27.6     37.3     52.6      76.5
     const int64_t rows = (max_new < 65 ? max_new : 65) * a.ratio;
-    if (rows > 64)
+    if (rows > 64 && b.n_tokens * at.n_q_heads > 1024)
         return kv4_launch_prompt(c, b, at, w, num_sms, st);
     if (c.head_dim == 64)
         return rows <= 8                 ? launch_rows<64, 1>(c, b, a, num_sms, st)

@@ -210,7 +210,7 @@ def test_attention(nm, D, Hk, Hq, P, lens, new):
 
 @pytest.mark.parametrize("D,Hk,Hq,P", [(128, 2, 8, 64), (128, 2, 10, 16), (64, 1, 7, 32), (128, 1, 1, 64), (64, 1, 64, 128)])
 @pytest.mark.parametrize("lens,new", [([200], [200]), ([129, 64, 300], [129, 64, 100]), ([17, 0, 260, 140], [17, 0, 31, 140]),
-                                      ([700], [33])])
+                                      ([700], [33]), ([1200, 300], [1040, 30])])
 def test_attention_prompts(nm, D, Hk, Hq, P, lens, new):
     c, K, V = make(nm, lens, P=P, Hk=Hk, D=D, seed=sum(lens) + 1)
     out, lse = check_attention(nm, c, K, V, lens, new, Hq, 1, max_new=max(new))
@@ -238,10 +238,11 @@ def test_attention_rows_with_nothing_to_attend(nm):
     out, lse = check_attention(nm, c, K, V, lens, new, 8, 1, max_new=25)
     assert bool((out[:3] == 0).all()) and bool(torch.isneginf(lse[:3]).all()) and bool(torch.isneginf(lse[8:11]).all())
     check_attention(nm, c, K, V, lens, new, 8, 1, max_new=1)
+    check_attention(nm, c, K, V, lens, new, 64, 1, max_new=25)
 
 
-@pytest.mark.parametrize("max_new", [1, 64])
-def test_attention_nonfinite_tokens_stay_where_they_are(nm, max_new):
+@pytest.mark.parametrize("max_new,heads", [(1, 4), (64, 4), (64, 32)])
+def test_attention_nonfinite_tokens_stay_where_they_are(nm, max_new, heads):
     """A token with NaN in k or v makes the queries that attend it NaN, and no others."""
     for D in (64, 128):
         lens = [90]
@@ -254,29 +255,29 @@ def test_attention_nonfinite_tokens_stay_where_they_are(nm, max_new):
             c.reserve(starts=ints([0, 90]))
             c.append(0, kk, vv, starts=ints([0, 90]))
             K, V = c.read(0, 90, starts=ints([0, 90]), f32=True)
-            out, lse = check_attention(nm, c, [f32(K)], [f32(V)], lens, [40], 4, 0, max_new=max_new)
+            out, lse = check_attention(nm, c, [f32(K)], [f32(V)], lens, [40], heads, 0, max_new=max_new)
             at = first - 50
             assert bool(torch.isfinite(out[:at]).all()) and bool(torch.isnan(out[at:]).all())
 
 
-@pytest.mark.parametrize("max_new", [1, 64])
-def test_attention_sharp_and_large_scores(nm, max_new):
+@pytest.mark.parametrize("max_new,heads", [(1, 4), (64, 4), (64, 32)])
+def test_attention_sharp_and_large_scores(nm, max_new, heads):
     """Scores far apart: one token takes all, or a first token with nearly no value takes the weight."""
     c, K, V = make(nm, [333], Hk=1, seed=8)
     for qs in (0.0, 1e-20, 30.0, 1e4):
-        check_attention(nm, c, K, V, [333], [40], 4, 1, qscale=qs, max_new=max_new)
-    check_attention(nm, c, K, V, [333], [40], 4, 1, qscale=1.0, scale=-0.7, max_new=max_new)
-    check_attention(nm, c, K, V, [333], [40], 4, 1, qscale=1.0, scale=0.0, max_new=max_new)
+        check_attention(nm, c, K, V, [333], [40], heads, 1, qscale=qs, max_new=max_new)
+    check_attention(nm, c, K, V, [333], [40], heads, 1, qscale=1.0, scale=-0.7, max_new=max_new)
+    check_attention(nm, c, K, V, [333], [40], heads, 1, qscale=1.0, scale=0.0, max_new=max_new)
     # a first token along q, with a small value
     D = 128
     k, v = values(333, 1, D, 31), values(333, 1, D, 32)
-    q = torch.ones(40, 4, D, dtype=torch.bfloat16, device="cuda")
+    q = torch.ones(40, heads, D, dtype=torch.bfloat16, device="cuda")
     k[0], v[0] = 1.4, 1e-3
     c = nm.Kv4Cache(12, 32, 1, 1, D, 1, 12)
     c.reserve(starts=ints([0, 333]))
     c.append(0, k, v, starts=ints([0, 333]))
     K, V = c.read(0, 333, starts=ints([0, 333]), f32=True)
-    check_attention(nm, c, [f32(K)], [f32(V)], [333], [40], 4, 0, q=q, max_new=max_new)
+    check_attention(nm, c, [f32(K)], [f32(V)], [333], [40], heads, 0, q=q, max_new=max_new)
 
 
 def test_attention_strides_ids_and_streams(nm):
@@ -527,15 +528,15 @@ def test_read_rows_that_are_not_there(nm):
     np.testing.assert_array_equal(f32(v[11:]), V[2][-4:])
 
 
-@pytest.mark.parametrize("max_new", [1, 64])
-def test_attention_nonfinite_queries_stay_in_their_rows(nm, max_new):
+@pytest.mark.parametrize("max_new,heads", [(1, 8), (64, 8), (64, 64)])
+def test_attention_nonfinite_queries_stay_in_their_rows(nm, max_new, heads):
     c, K, V = make(nm, [100], seed=92)
-    q = values(40, 8, 128, 93)
+    q = values(40, heads, 128, 93)
     good = c.attention(1, q, starts=ints([0, 40]), max_new=max_new)
     bad = q.clone()
     bad[7, 3, 11], bad[20, 6, 5] = float("nan"), float("inf")
     out = c.attention(1, bad, starts=ints([0, 40]), max_new=max_new)
-    same = torch.ones(40, 8, dtype=torch.bool, device="cuda")
+    same = torch.ones(40, heads, dtype=torch.bool, device="cuda")
     same[7, 3] = same[20, 6] = False
     assert torch.equal(out[same], good[same]) and bool(torch.isnan(out[7, 3]).all())
 
