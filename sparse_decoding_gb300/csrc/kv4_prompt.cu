@@ -948,160 +948,161 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 more = w.nblk > 0;
             }
         }
-    } else if (warp == kMmaWarp + 1) {
+    } else {
+        // one instruction for the warpgroup: its warps have to meet in the same one
         setmaxnreg_dec<kMmaRegs>();
-        // ---- the pieces, one lane ----
-        if (lane == 0) {
-            const int64_t share = sh.share;
-            int64_t pos = (int64_t)blockIdx.x * share;
-            const int64_t hi = pos + share < sh.total ? pos + share : sh.total;
-            int seq = sh.seq, head = sh.head, pair = sh.pair, step = sh.step;
-            Kv4Seq s = pos < hi ? seq_at(seq) : Kv4Seq{};
-#pragma unroll 1
-            for (uint32_t p = 0;; ++p) {
-                Piece w{};
-                if (pos < hi) {
-                    w.row = s.row;
-                    w.len = s.len;
-                    w.n_new = s.n_new;
-                    w.first = s.first;
-                    w.head = head;
-                    w.pair = pair;
-                    w.total = pair_blocks(s, pair, tt);
-                    const int64_t seg = pos - step + kOver; // the place of the segment's first block
-                    const int all = w.total + kOver - step;
-                    const int steps = hi - pos < all ? (int)(hi - pos) : all;
-                    w.b0 = step > kOver ? step - kOver : 0;
-                    const int b1 = step + steps - kOver;
-                    w.nblk = b1 > w.b0 ? b1 - w.b0 : 0; // 0: the CTA's part ends before the first block
-                    const int n0 = blocks_of(tile_limit(s, 2 * pair, tt)) - w.b0;
-                    const int n1 = blocks_of(tile_limit(s, 2 * pair + 1, tt)) - w.b0;
-                    w.n0 = n0 < 0 ? 0 : n0 > w.nblk ? w.nblk : n0;
-                    w.n1 = n1 < 0 ? 0 : n1 > w.nblk ? w.nblk : n1;
-                    w.cta0 = (int)(seg / share);
-                    w.cta1 = (int)((seg + w.total - 1) / share);
-                    pos += steps;
-                    step = 0;
-                    if (pos < hi && ++pair == pairs_of(s, tt)) {
-                        pair = 0;
-                        if (++head == c.n_kv_heads) {
-                            head = 0;
-                            do
-                                s = seq_at(++seq);
-                            while (s.n_new == 0); // pos < hi: there is one
+        if (warp == kMmaWarp + 1) {
+            // ---- the pieces, one lane ----
+            if (lane == 0) {
+                const int64_t share = sh.share;
+                int64_t pos = (int64_t)blockIdx.x * share;
+                const int64_t hi = pos + share < sh.total ? pos + share : sh.total;
+                int seq = sh.seq, head = sh.head, pair = sh.pair, step = sh.step;
+                Kv4Seq s = pos < hi ? seq_at(seq) : Kv4Seq{};
+    #pragma unroll 1
+                for (uint32_t p = 0;; ++p) {
+                    Piece w{};
+                    if (pos < hi) {
+                        w.row = s.row;
+                        w.len = s.len;
+                        w.n_new = s.n_new;
+                        w.first = s.first;
+                        w.head = head;
+                        w.pair = pair;
+                        w.total = pair_blocks(s, pair, tt);
+                        const int64_t seg = pos - step + kOver; // the place of the segment's first block
+                        const int all = w.total + kOver - step;
+                        const int steps = hi - pos < all ? (int)(hi - pos) : all;
+                        w.b0 = step > kOver ? step - kOver : 0;
+                        const int b1 = step + steps - kOver;
+                        w.nblk = b1 > w.b0 ? b1 - w.b0 : 0; // 0: the CTA's part ends before the first block
+                        const int n0 = blocks_of(tile_limit(s, 2 * pair, tt)) - w.b0;
+                        const int n1 = blocks_of(tile_limit(s, 2 * pair + 1, tt)) - w.b0;
+                        w.n0 = n0 < 0 ? 0 : n0 > w.nblk ? w.nblk : n0;
+                        w.n1 = n1 < 0 ? 0 : n1 > w.nblk ? w.nblk : n1;
+                        w.cta0 = (int)(seg / share);
+                        w.cta1 = (int)((seg + w.total - 1) / share);
+                        pos += steps;
+                        step = 0;
+                        if (pos < hi && ++pair == pairs_of(s, tt)) {
+                            pair = 0;
+                            if (++head == c.n_kv_heads) {
+                                head = 0;
+                                do
+                                    s = seq_at(++seq);
+                                while (s.n_new == 0); // pos < hi: there is one
+                            }
                         }
                     }
+                    if (p >= kRing)
+                        wait(sh.piece_empty[p % kRing], p / kRing - 1);
+                    sh.piece[p % kRing] = w;
+                    kv4_arrive(smem_addr(&sh.piece_full[p % kRing]));
+                    if (w.nblk == 0)
+                        break;
                 }
-                if (p >= kRing)
-                    wait(sh.piece_empty[p % kRing], p / kRing - 1);
-                sh.piece[p % kRing] = w;
-                kv4_arrive(smem_addr(&sh.piece_full[p % kRing]));
-                if (w.nblk == 0)
-                    break;
             }
-        }
-    } else if (warp > kMmaWarp) {
-        setmaxnreg_dec<kMmaRegs>();
-    } else {
-        setmaxnreg_dec<kMmaRegs>();
-        // ---- the MMAs: every lane follows, one issues ----
-        const uint32_t one = elect();
-        constexpr uint32_t tmem = 0; // all 512 columns are this kernel's: they start at 0
+        } else if (warp == kMmaWarp) {
+            // ---- the MMAs: every lane follows, one issues ----
+            const uint32_t one = elect();
+            constexpr uint32_t tmem = 0; // all 512 columns are this kernel's: they start at 0
 
-        uint32_t n = 0, n_p0 = 0, n_p1 = 0, n_q0 = 0, n_q1 = 0;
-        const uint32_t desc0 = kDescLo | (tiles >> 4);
-        const auto scores = [&](int k, int stage) { // S of tile k, K in `stage`
-            const uint32_t q = desc0 + k * (C::kQ >> 4), kk = desc0 + (C::kOffK >> 4) + stage * (C::kQ >> 4);
-            const uint32_t d = tmem + k * 128;
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    mma_ss<128>(d, q + ((g * kSub + 32 * x) >> 4), kk + ((g * kSub + 32 * x) >> 4), kIdesc<128>, g + x, one);
-            mma_ss<32>(d, q + ((G * kSub) >> 4), kk + ((G * kSub) >> 4), kIdesc<128>, 1, one);
-            commit(smem_addr(&sh.s_full[k]), one);
-        };
-        const auto values = [&](int k, int stage, uint32_t accumulate) { // O of tile k, V in `stage`
-            const uint32_t v = desc0 + (C::kOffV >> 4) + stage * (C::kV >> 4);
-            const uint32_t d = tmem + 256 + k * 128, p = tmem + k * 128;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    mma_ts(d, p + 32 * h + 8 * x, v + ((h * (D * 128) + 32 * x) >> 4), kIdesc<D>,
-                           h + x > 0 ? 1u : accumulate, one);
-        };
-        // O of block i of a piece (block n - 1 of the CTA), then S of block i + 1 (block n), tile by
-        // tile. The stages are constants of two copies of this, so that all descriptors are uniform.
-        int nblk, n0, n1;
-        const auto step = [&](auto parity, int i) {
-            constexpr int nxt = decltype(parity)::value, cur = nxt ^ 1; // n & 1, (n - 1) & 1
-            const bool more = i + 1 < nblk;
-            if (i >= 0) {
-                wait(sh.v_full[cur], (n - 1) >> 1);
-                if (i < n0) {
-                    wait(sh.p_full[0], n_p0++);
-                    fence_after();
-                    values(0, cur, i > 0);
-                    if (i == n0 - 1)
-                        commit(smem_addr(&sh.o_full[0]), one);
+            uint32_t n = 0, n_p0 = 0, n_p1 = 0, n_q0 = 0, n_q1 = 0;
+            const uint32_t desc0 = kDescLo | (tiles >> 4);
+            const auto scores = [&](int k, int stage) { // S of tile k, K in `stage`
+                const uint32_t q = desc0 + k * (C::kQ >> 4), kk = desc0 + (C::kOffK >> 4) + stage * (C::kQ >> 4);
+                const uint32_t d = tmem + k * 128;
+    #pragma unroll
+                for (int g = 0; g < G; ++g)
+    #pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        mma_ss<128>(d, q + ((g * kSub + 32 * x) >> 4), kk + ((g * kSub + 32 * x) >> 4), kIdesc<128>, g + x,
+                                    one);
+                mma_ss<32>(d, q + ((G * kSub) >> 4), kk + ((G * kSub) >> 4), kIdesc<128>, 1, one);
+                commit(smem_addr(&sh.s_full[k]), one);
+            };
+            const auto values = [&](int k, int stage, uint32_t accumulate) { // O of tile k, V in `stage`
+                const uint32_t v = desc0 + (C::kOffV >> 4) + stage * (C::kV >> 4);
+                const uint32_t d = tmem + 256 + k * 128, p = tmem + k * 128;
+    #pragma unroll
+                for (int h = 0; h < 2; ++h)
+    #pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        mma_ts(d, p + 32 * h + 8 * x, v + ((h * (D * 128) + 32 * x) >> 4), kIdesc<D>,
+                               h + x > 0 ? 1u : accumulate, one);
+            };
+            // O of block i of a piece (block n - 1 of the CTA), then S of block i + 1 (block n), tile by
+            // tile. The stages are constants of two copies of this, so that all descriptors are uniform.
+            int nblk, n0, n1;
+            const auto step = [&](auto parity, int i) {
+                constexpr int nxt = decltype(parity)::value, cur = nxt ^ 1; // n & 1, (n - 1) & 1
+                const bool more = i + 1 < nblk;
+                if (i >= 0) {
+                    wait(sh.v_full[cur], (n - 1) >> 1);
+                    if (i < n0) {
+                        wait(sh.p_full[0], n_p0++);
+                        fence_after();
+                        values(0, cur, i > 0);
+                        if (i == n0 - 1)
+                            commit(smem_addr(&sh.o_full[0]), one);
+                    }
+                }
+                if (more) {
+                    wait(sh.k_full[nxt], n >> 1);
+                    if (i + 1 < n0) {
+                        if (i < 0)
+                            wait(sh.q_full[0], n_q0++);
+                        fence_after();
+                        scores(0, nxt);
+                    }
+                }
+                if (i >= 0) {
+                    if (i < n1) {
+                        wait(sh.p_full[1], n_p1++);
+                        fence_after();
+                        values(1, cur, i > 0);
+                        if (i == n1 - 1)
+                            commit(smem_addr(&sh.o_full[1]), one);
+                    }
+                    commit(smem_addr(&sh.v_empty[cur]), one);
+                }
+                if (more) {
+                    if (i + 1 < n1) {
+                        if (i < 0)
+                            wait(sh.q_full[1], n_q1++);
+                        fence_after();
+                        scores(1, nxt);
+                    }
+                    commit(smem_addr(&sh.k_empty[nxt]), one);
+                    ++n;
+                }
+            };
+            uint32_t piece = 0;
+    #pragma unroll 1
+            for (;;) {
+                wait(sh.piece_full[piece % kRing], piece / kRing);
+                nblk = sh.piece[piece % kRing].nblk;
+                n0 = sh.piece[piece % kRing].n0;
+                n1 = sh.piece[piece % kRing].n1;
+                __syncwarp();
+                if (one)
+                    kv4_arrive(smem_addr(&sh.piece_empty[piece % kRing]));
+                ++piece;
+                if (nblk == 0)
+                    break;
+    #pragma unroll 1
+                for (int i = -1; i < nblk; ++i) {
+                    if (n & 1)
+                        step(std::integral_constant<int, 1>{}, i);
+                    else
+                        step(std::integral_constant<int, 0>{}, i);
                 }
             }
-            if (more) {
-                wait(sh.k_full[nxt], n >> 1);
-                if (i + 1 < n0) {
-                    if (i < 0)
-                        wait(sh.q_full[0], n_q0++);
-                    fence_after();
-                    scores(0, nxt);
-                }
+            // before leaving, the MMAs in flight end (bounded): the last stages are released
+            if (n > 0) {
+                wait(sh.k_empty[(n - 1) & 1], (n - 1) >> 1);
+                wait(sh.v_empty[(n - 1) & 1], (n - 1) >> 1);
             }
-            if (i >= 0) {
-                if (i < n1) {
-                    wait(sh.p_full[1], n_p1++);
-                    fence_after();
-                    values(1, cur, i > 0);
-                    if (i == n1 - 1)
-                        commit(smem_addr(&sh.o_full[1]), one);
-                }
-                commit(smem_addr(&sh.v_empty[cur]), one);
-            }
-            if (more) {
-                if (i + 1 < n1) {
-                    if (i < 0)
-                        wait(sh.q_full[1], n_q1++);
-                    fence_after();
-                    scores(1, nxt);
-                }
-                commit(smem_addr(&sh.k_empty[nxt]), one);
-                ++n;
-            }
-        };
-        uint32_t piece = 0;
-#pragma unroll 1
-        for (;;) {
-            wait(sh.piece_full[piece % kRing], piece / kRing);
-            nblk = sh.piece[piece % kRing].nblk;
-            n0 = sh.piece[piece % kRing].n0;
-            n1 = sh.piece[piece % kRing].n1;
-            __syncwarp();
-            if (one)
-                kv4_arrive(smem_addr(&sh.piece_empty[piece % kRing]));
-            ++piece;
-            if (nblk == 0)
-                break;
-#pragma unroll 1
-            for (int i = -1; i < nblk; ++i) {
-                if (n & 1)
-                    step(std::integral_constant<int, 1>{}, i);
-                else
-                    step(std::integral_constant<int, 0>{}, i);
-            }
-        }
-        // before leaving, the MMAs in flight end (bounded): the last stages are released
-        if (n > 0) {
-            wait(sh.k_empty[(n - 1) & 1], (n - 1) >> 1);
-            wait(sh.v_empty[(n - 1) & 1], (n - 1) >> 1);
         }
     }
     fence_before();
