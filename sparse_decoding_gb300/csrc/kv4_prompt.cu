@@ -41,8 +41,9 @@
 // two buffers with the scores a step ahead (578: an MMA of N = 64 reads Q as often
 // for half the columns).
 //
-// All waits are bounded; one that runs out sets NM_ERR_TIMEOUT and the kernel
-// frees its tensor memory and returns.
+// All waits are bounded; one that runs out sets NM_ERR_TIMEOUT. Its thread's later waits
+// poll once and its warp takes no more pieces, so the others run out in turn, the MMAs
+// in flight end, and the kernel frees its tensor memory and returns.
 #include <mutex>
 #include <type_traits>
 
@@ -408,7 +409,7 @@ constexpr int kRing = 4;        // pieces known ahead
 
 struct Shared {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], met[2];
     uint32_t tmem;
     uint32_t last[2];
     uint64_t piece_full[kRing], piece_empty[kRing];
@@ -545,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             mbar_init(smem_addr(&sh.v_empty[i]), 1);
             mbar_init(smem_addr(&sh.q_full[i]), 128);
             mbar_init(smem_addr(&sh.p_full[i]), 128);
+            mbar_init(smem_addr(&sh.met[i]), 128);
             mbar_init(smem_addr(&sh.s_full[i]), 1);
             mbar_init(smem_addr(&sh.o_full[i]), 1);
         }
@@ -643,10 +645,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
     const auto wait = [&](uint64_t &bar, uint32_t parity) {
         kv4_wait(smem_addr(&bar), parity & 1u, c.status, dead);
     };
-    // Piece number p of the CTA, for a whole warp.
+    // Piece number p of the CTA, for a whole warp. After a wait that ran out there are no more:
+    // what stands in the ring may be no piece, or half of one.
     const auto get_piece = [&](uint32_t p) {
         wait(sh.piece_full[p % kRing], p / kRing);
-        const Piece w = sh.piece[p % kRing];
+        dead = __any_sync(~0u, dead);
+        Piece w{};
+        if (!dead)
+            w = sh.piece[p % kRing];
         __syncwarp();
         if (lane == 0)
             kv4_arrive(smem_addr(&sh.piece_empty[p % kRing]));
@@ -666,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         const auto token_of = [&](const Piece &w) { return (2 * w.pair + k) * tt + row_token; };
         const auto valid_in = [&](const Piece &w) { return row < tt * a.ratio && token_of(w) < w.n_new; };
         uint32_t n_s = 0, n_o = 0; // blocks and pieces of this tile so far
+        uint32_t n_j = 0;          // meetings of its threads
 
         // The row of Q: scaled by a power of two, channels in the order of the unpacked
         // keys. Returns the factor of the scores.
@@ -757,17 +764,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 }
                 // The parts of this tile are joined by the last CTA to arrive, in CTA order: of many,
                 // first in groups of g (at most 16 to a join), then the groups (32 new tokens after
-                // 32768 by one join of 32 parts: 77 us).
+                // 32768 by one join of 32 parts: 77 us). The tile's threads meet on an mbarrier, whose
+                // wait is bounded: after one that ran out, warps may be missing.
+                const auto meet = [&]() {
+                    kv4_arrive(smem_addr(&sh.met[k]));
+                    wait(sh.met[k], n_j++);
+                };
                 const auto last_of = [&](uint32_t *counter, int n) {
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
+                    meet();
                     if (row == 0) {
                         const uint32_t before = n > 1 ? atom_add_acq_rel_gpu(counter, 1u) : 0;
                         sh.last[k] = before == (uint32_t)n - 1;
                         if (n > 1 && sh.last[k])
                             *counter = 0; // for the next launch
                     }
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + k) : "memory");
-                    return sh.last[k] != 0;
+                    meet();
+                    dead = __any_sync(~0u, dead);
+                    return !dead && sh.last[k] != 0;
                 };
                 const int n = done.cta1 - done.cta0 + 1;
                 const int g = n <= 8 ? n : n <= 16 ? 4 : n <= 64 ? 8 : n <= 144 ? 12 : (n + 15) / 16;
@@ -959,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 const int64_t hi = pos + share < sh.total ? pos + share : sh.total;
                 int seq = sh.seq, head = sh.head, pair = sh.pair, step = sh.step;
                 Kv4Seq s = pos < hi ? seq_at(seq) : Kv4Seq{};
-    #pragma unroll 1
+#pragma unroll 1
                 for (uint32_t p = 0;; ++p) {
                     Piece w{};
                     if (pos < hi) {
@@ -996,6 +1009,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                     }
                     if (p >= kRing)
                         wait(sh.piece_empty[p % kRing], p / kRing - 1);
+                    if (dead)
+                        break; // the place may still be read
                     sh.piece[p % kRing] = w;
                     kv4_arrive(smem_addr(&sh.piece_full[p % kRing]));
                     if (w.nblk == 0)
@@ -1012,9 +1027,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             const auto scores = [&](int k, int stage) { // S of tile k, K in `stage`
                 const uint32_t q = desc0 + k * (C::kQ >> 4), kk = desc0 + (C::kOffK >> 4) + stage * (C::kQ >> 4);
                 const uint32_t d = tmem + k * 128;
-    #pragma unroll
+#pragma unroll
                 for (int g = 0; g < G; ++g)
-    #pragma unroll
+#pragma unroll
                     for (int x = 0; x < 4; ++x)
                         mma_ss<128>(d, q + ((g * kSub + 32 * x) >> 4), kk + ((g * kSub + 32 * x) >> 4), kIdesc<128>, g + x,
                                     one);
@@ -1024,9 +1039,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
             const auto values = [&](int k, int stage, uint32_t accumulate) { // O of tile k, V in `stage`
                 const uint32_t v = desc0 + (C::kOffV >> 4) + stage * (C::kV >> 4);
                 const uint32_t d = tmem + 256 + k * 128, p = tmem + k * 128;
-    #pragma unroll
+#pragma unroll
                 for (int h = 0; h < 2; ++h)
-    #pragma unroll
+#pragma unroll
                     for (int x = 0; x < 4; ++x)
                         mma_ts(d, p + 32 * h + 8 * x, v + ((h * (D * 128) + 32 * x) >> 4), kIdesc<D>,
                                h + x > 0 ? 1u : accumulate, one);
@@ -1078,10 +1093,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 }
             };
             uint32_t piece = 0;
-    #pragma unroll 1
+#pragma unroll 1
             for (;;) {
                 wait(sh.piece_full[piece % kRing], piece / kRing);
-                nblk = sh.piece[piece % kRing].nblk;
+                dead = __any_sync(~0u, dead);
+                nblk = dead ? 0 : sh.piece[piece % kRing].nblk; // as in get_piece
                 n0 = sh.piece[piece % kRing].n0;
                 n1 = sh.piece[piece % kRing].n1;
                 __syncwarp();
@@ -1090,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 ++piece;
                 if (nblk == 0)
                     break;
-    #pragma unroll 1
+#pragma unroll 1
                 for (int i = -1; i < nblk; ++i) {
                     if (n & 1)
                         step(std::integral_constant<int, 1>{}, i);
@@ -1098,8 +1114,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                         step(std::integral_constant<int, 0>{}, i);
                 }
             }
-            // before leaving, the MMAs in flight end (bounded): the last stages are released
+            // before leaving, the MMAs in flight end (bounded, after a wait that ran out too): the last
+            // stages are released
             if (n > 0) {
+                dead = false;
                 wait(sh.k_empty[(n - 1) & 1], (n - 1) >> 1);
                 wait(sh.v_empty[(n - 1) & 1], (n - 1) >> 1);
             }

@@ -31,3 +31,21 @@ def test_warpgroups_meet_in_one_register_instruction():
     assert warps and warps[0] % 4 == 0
     roles = re.findall(r"\n    (?:\} else )?(if \([^\n]*\)|else) \{\s*setmaxnreg|\n    \} (else) \{\s*setmaxnreg", kernel)
     assert [a or b for a, b in roles] == ["if (warp < 8)", "if (warp < kMmaWarp)", "else"]
+
+
+def test_prompt_roles_end_after_a_wait_that_ran_out():
+    """A thread whose wait ran out goes on with polls. It must not use a piece of work that may not be
+    there, write over one that is read, or meet others at a barrier without a bound."""
+    kernel = block(source("kv4_prompt.cu"), "attn_prompt_kernel(const Kv4 c")
+    roles = kernel[kernel.index("setmaxnreg_inc"):]
+    roles = roles[:roles.rindex("__syncthreads()")]
+    for unbounded in ("bar.sync", "barrier.sync", "__syncthreads", "while (!mbar"):
+        assert unbounded not in roles, unbounded
+    get = block(kernel, "const auto get_piece")
+    assert "dead = __any_sync(~0u, dead);" in get
+    assert re.search(r"Piece w\{\};\s*if \(!dead\)\s*w = sh\.piece", get)
+    # the other reader of the ring, and its writer
+    assert re.search(r"nblk = dead \? 0 : sh\.piece", roles)
+    assert re.search(r"if \(dead\)\s*break;\s*sh\.piece\[p % kRing\] = w;", roles)
+    # the MMAs in flight are waited for once more before the tensor memory is given back
+    assert re.search(r"if \(n > 0\) \{\s*dead = false;\s*wait\(sh\.k_empty", roles)
