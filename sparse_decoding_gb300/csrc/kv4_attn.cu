@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
         // The warp's units are c0 + warp, + kWarps, ... Lanes 2 n, 2 n + 1 hold the addresses of the
         // cells of every 16th (0: its page is none of the pool's, or it is past the sequence's end);
         // `have` has a bit for each cell of a stage that was filled.
-        const int mine = s.len > 0 && c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
+        int mine = !dead && s.len > 0 && c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
         const uint8_t *const heads = c.pool + kv4_cell_offset<D>(c, 0, a.layer, head, 0);
         uint64_t where = 0;
         uint32_t have = 0;
@@ -507,6 +507,17 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
             }
             const uint32_t st = (used + x) % S;
             kv4_wait(bars + 8 * st, ((used + x) / S) & 1, c.status, dead);
+            if (__any_sync(~0u, dead)) {
+                // Ran out: the warp asks for no more cells, in this piece or the next, and the copies in
+                // flight end (bounded) before the parts take the rings' place.
+                for (int z = x; z < x + S && z < mine; ++z) {
+                    dead = false;
+                    kv4_wait(bars + 8 * ((used + z) % S), ((used + z) / S) & 1, c.status, dead);
+                }
+                dead = true;
+                mine = x;
+                break;
+            }
             const uint32_t filled = have >> (2 * st) & 3u;
 #pragma unroll 1
             for (int v0 = 0; v0 < kUnit; v0 += U) {

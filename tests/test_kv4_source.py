@@ -49,3 +49,15 @@ def test_prompt_roles_end_after_a_wait_that_ran_out():
     assert re.search(r"if \(dead\)\s*break;\s*sh\.piece\[p % kRing\] = w;", roles)
     # the MMAs in flight are waited for once more before the tensor memory is given back
     assert re.search(r"if \(n > 0\) \{\s*dead = false;\s*wait\(sh\.k_empty", roles)
+
+
+def test_rows_kernel_waits_for_its_copies_after_a_wait_that_ran_out():
+    """No copy may be in flight when its shared memory is used for the parts or given back, and no barrier
+    may be armed again before its copy is there: after a wait that ran out the warp asks for no more cells."""
+    kernel = block(source("kv4_attn.cu"), "attn_rows_kernel(const Kv4 c")
+    assert re.search(r"int mine = !dead && ", kernel)
+    rest = kernel[kernel.index("kv4_wait(bars + 8 * st"):]
+    out = block(rest, "if (__any_sync(~0u, dead))")
+    assert rest.index("if (__any_sync(~0u, dead))") < rest.index("const uint32_t filled")
+    assert re.search(r"for \(int z = x; z < x \+ S && z < mine; \+\+z\) \{\s*dead = false;\s*kv4_wait\(", out)
+    assert re.search(r"dead = true;\s*mine = x;\s*break;", out)
