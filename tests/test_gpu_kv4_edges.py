@@ -1,0 +1,123 @@
+"""The 4-bit paged KV cache where rows, pages and parts are not the ordinary ones, on a GPU: joins of many
+parts, rows that no sequence covers, pages that are missing. Tolerances as in tests/test_gpu_kv4.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4 as ref
+from tests.test_gpu_kv4 import f32, f64, ints, make, nm, rope_table, starts_of, values  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def definition(q, K, V, limits, scale):
+    """(out, lse, A, B) as oracle.kv4.attention, one matrix product a head: q [n][H][D] (fp64); row i sees the
+    tokens of limits[i], a count or a list of truth values."""
+    n, H, D = q.shape
+    r = H // K.shape[1]
+    see = np.zeros((n, len(K)), bool)
+    for i, x in enumerate(limits):
+        see[i] = x if np.ndim(x) else np.arange(len(K)) < x
+    out, A = np.zeros((n, H, D)), np.zeros((n, H, D))
+    lse, B = np.full((n, H), -np.inf), np.zeros((n, H))
+    some = see.any(1)
+    for h in range(H):
+        k, v = K[:, h // r].astype(np.float64), V[:, h // r].astype(np.float64)
+        s = np.where(see, q[:, h] @ k.T * scale, -np.inf)[some]
+        if not len(s):
+            continue
+        top = s.max(1, keepdims=True)
+        p = np.exp(s - top)
+        z = p.sum(1, keepdims=True)
+        lse[some, h] = (top + np.log(z))[:, 0]
+        out[some, h], A[some, h] = p / z @ v, p / z @ np.abs(v)
+        B[some, h] = np.where(see, np.abs(q[:, h]) @ np.abs(k).T * abs(scale), 0.0)[some].max(1)
+    return out, lse, A, B
+
+
+def compare(out, lse, want, length, vmax):
+    o, l, A, B = want
+    e = 2.0 ** -16 * B + 2.0 ** -15
+    got, gl = f64(out), lse.cpu().numpy().astype(np.float64)
+    seen = np.isfinite(l)
+    assert np.array_equal(np.isneginf(gl), ~seen) and np.all(got[~seen] == 0)
+    assert np.all(np.abs(gl[seen] - l[seen]) <= e[seen]), np.abs(gl[seen] - l[seen]).max()
+    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e[..., None] + 2.0 ** -14) * A + length * 2.0 ** -30 * vmax + 1e-30
+    assert np.all(np.abs(got - o)[seen] <= tol[seen]), (np.abs(got - o)[seen] / tol[seen]).max()
+
+
+# --- joins of many parts ---------------------------------------------------------------
+
+BLOCK, OVER, MIN_SHARE = 128, 3, 2  # the prompt kernel's: tokens of a block, what a segment adds, blocks of a CTA
+
+
+def parts_of_first(blocks, others, ctas):
+    """CTAs that share the first segment of a line: `blocks` long, others (their blocks) behind it."""
+    total = blocks + OVER + sum(n + OVER for n in others)
+    share = max(-(-total // ctas), MIN_SHARE + OVER)
+    return (OVER + blocks - 1) // share - OVER // share + 1
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("parts", [8, 9, 13, 16, 17, 33, 64, 65, 73, 144, 145])
+def test_prompt_attention_joins_many_parts(nm, D, parts):
+    """A few new tokens behind a long context beside a short prompt: one segment is cut over 8 CTAs (one
+    join) to 145 (groups of parts, then the groups; some with a last group of one part)."""
+    H, new = 16, [9, 70]
+    others = [1] * 5  # pairs of 16 tokens of the second sequence
+    ctas = min(torch.cuda.get_device_properties(0).multi_processor_count, 160)
+    blocks = next((n for n in range(1, 2000) if parts_of_first(n, others, ctas) == parts), None)
+    if blocks is None:
+        pytest.skip(f"no length gives {parts} parts on {ctas} CTAs")
+    lens = [blocks * BLOCK - 5, 70]
+    c, K, V = make(nm, lens, P=64, L=1, Hk=1, D=D, seed=parts)
+    q = values(sum(new), H, D, 7)
+    out, lse = c.attention(0, q, starts=starts_of(new), max_new=70, lse=True)
+    assert nm.device_status() == nm.NM_OK
+    at = 0
+    for s, n in enumerate(new):
+        rows = slice(at, at + n)
+        want = definition(f64(q[rows]), K[s], V[s], [lens[s] - n + i + 1 for i in range(n)], D ** -0.5)
+        compare(out[rows], lse[rows], want, lens[s], np.abs(V[s]).max())
+        at += n
+    for _ in range(3):  # the counters are as they were, and the order of the sums is fixed
+        o2, l2 = c.attention(0, q, starts=starts_of(new), max_new=70, lse=True)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("lens,new,heads", [([30011, 17, 9000], [20, 2, 5], 64), ([30011], [40], 32)])
+def test_prompt_attention_long_cut_over_many_ctas(nm, lens, new, heads):
+    """Several long segments, each cut over tens of CTAs that end one segment and begin the next."""
+    c, K, V = make(nm, lens, P=64, L=1, Hk=1, seed=23)
+    q = values(sum(new), heads, 128, 24)
+    out, lse = c.attention(0, q, starts=starts_of(new), max_new=max(new), lse=True)
+    assert nm.device_status() == nm.NM_OK
+    at = 0
+    for s, n in enumerate(new):
+        rows = slice(at, at + n)
+        want = definition(f64(q[rows]), K[s], V[s], [lens[s] - n + i + 1 for i in range(n)], 128 ** -0.5)
+        compare(out[rows], lse[rows], want, lens[s], np.abs(V[s]).max())
+        at += n
+    o2, l2 = c.attention(0, q, starts=starts_of(new), max_new=max(new), lse=True)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_prompt_attention_past_4_gib(nm):
+    """The prompt kernel on pages whose bytes lie past 2^32 of the pool."""
+    P, L, Hk, D, H, n_new = 128, 32, 8, 128, 16, 70  # 1120 query rows
+    per = nm.lib().nm_kv4_page_bytes(P, L, Hk, D)
+    n = (1 << 32) // per + 8
+    c = nm.Kv4Cache(n, P, L, Hk, D, 1, 4)
+    c.refs.fill_(1)  # only the last three pages are free
+    c.refs[n - 3:] = 0
+    c.info[0] = 3
+    c.reserve(starts=ints([0, 300]))
+    assert int(c.tables[0, 0]) == n - 3 and (n - 3) * per > 1 << 32
+    k, v = values(300, Hk, D, 41), values(300, Hk, D, 42)
+    c.append(L - 1, k, v, starts=ints([0, 300]))
+    rk, rv = ref.quantise(f32(k), f32(v))
+    q = values(n_new, H, D, 43)
+    out, lse = c.attention(L - 1, q, starts=ints([0, n_new]), max_new=n_new, lse=True)
+    assert nm.device_status() == nm.NM_OK
+    compare(out, lse, definition(f64(q), rk, rv, [300 - n_new + i + 1 for i in range(n_new)], D ** -0.5), 300,
+            np.abs(rv).max())
