@@ -13,7 +13,8 @@
 // and a key is s (c - 8) with a scale of eight significant bits (the format's
 // reason for it), so s (c - 8) needs eleven. The groups' middles enter as one more
 // k-step of 16: [sum q of the group, in two fp16 parts] x [mid, mid]. Scores
-// then carry fp32 rounding only, as in the kernel for few rows.
+// then carry fp32 rounding only, as in the kernel for few rows. The same k-step masks
+// the tokens of missing pages: [1] x [0, or -inf].
 //
 // Roles (20 warps): two softmax warpgroups, one per tile (a thread owns a row: no
 // reductions across threads; it also loads and scales its row of Q, rescales and
@@ -241,9 +242,11 @@ template <int N> __device__ __forceinline__ __half2 nibble8(uint32_t w)
 
 // What an unpacking thread u holds of a block. K: two 16-byte pieces (8 bytes at
 // D = 64): row 64 j + u / 4, channels 16 (u % 4) .. of each group.
+// The first parameters of a cell that is not there are kNoCell: a scale of -0, which no token has.
 template <int D> struct RawK {
     uint32_t w[2][2 * Cfg<D>::G], p[2][Cfg<D>::G];
 };
+constexpr uint32_t kNoCell = 0x8000u;
 // V: a unit (cell, group, e, p): channels 64 g + 8 e .., tokens 8 p .. of the cell.
 // At D = 64 there are 128 of them, for the first 128 threads.
 struct RawV {
@@ -272,14 +275,14 @@ template <int D> __device__ __forceinline__ void load_k(RawK<D> &r, const uint8_
             r.w[j][1] = x.y;
             r.w[j][2 * G - 2] = x.z;
             r.w[j][2 * G - 1] = x.w;
-            const uint2 p = have ? __ldg((const uint2 *)(cell + Kv4Cell<D>::kKp + (row & 15) * 8)) : make_uint2(0, 0);
+            const uint2 p = have ? __ldg((const uint2 *)(cell + Kv4Cell<D>::kKp + (row & 15) * 8)) : make_uint2(kNoCell, 0);
             r.p[j][0] = p.x;
             r.p[j][G - 1] = p.y;
         } else {
             const uint2 x = have ? __ldg((const uint2 *)src) : make_uint2(0, 0);
             r.w[j][0] = x.x;
             r.w[j][1] = x.y;
-            r.p[j][0] = have ? __ldg((const uint32_t *)(cell + Kv4Cell<D>::kKp + (row & 15) * 4)) : 0u;
+            r.p[j][0] = have ? __ldg((const uint32_t *)(cell + Kv4Cell<D>::kKp + (row & 15) * 4)) : kNoCell;
         }
     }
 }
@@ -303,8 +306,11 @@ template <int D> __device__ __forceinline__ void unpack_k(const RawK<D> &r, uint
                        as_u32(__hmul2(nibble8<3>(x), s)));
             }
         }
-        if (t < 2) // the k-step of the middles: two 16-byte halves of the row
-            sts128(ks + G * kSub + row * 32 + ((t ^ ((row >> 2) & 1)) << 4), t ? 0 : mids[0], t ? 0 : mids[1], 0, 0);
+        // the k-step of the middles: two 16-byte halves of the row. Where Q has its one, a token whose
+        // cell is not there has -inf: then so is its score, and nothing of it is attended.
+        if (t < 2)
+            sts128(ks + G * kSub + row * 32 + ((t ^ ((row >> 2) & 1)) << 4), t ? 0 : mids[0], t ? 0 : mids[1],
+                   t == 0 && r.p[j][0] == kNoCell ? 0xFC00u : 0, 0);
     }
 }
 template <int D> __device__ __forceinline__ void load_v(RawV &r, const uint8_t *pool, uint32_t place, int u)
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 ext[g] = pack_half2(part, sum - part);
             }
             const uint32_t e_row = q_tile + G * kSub + row * 32, flip = (row >> 2) & 1;
-            sts128(e_row + (flip << 4), ext[0], ext[1], 0, 0);
+            sts128(e_row + (flip << 4), ext[0], ext[1], 0x3C00, 0); // and a one (see unpack_k)
             sts128(e_row + ((flip ^ 1) << 4), 0, 0, 0, 0);
             fence_proxy_async_smem();
             kv4_arrive(smem_addr(&sh.q_full[k]));

@@ -121,3 +121,28 @@ def test_prompt_attention_past_4_gib(nm):
     assert nm.device_status() == nm.NM_OK
     compare(out, lse, definition(f64(q), rk, rv, [300 - n_new + i + 1 for i in range(n_new)], D ** -0.5), 300,
             np.abs(rv).max())
+
+
+# --- pages that are missing ----------------------------------------------------------------
+
+@pytest.mark.parametrize("D,heads", [(128, 32), (64, 64)])
+@pytest.mark.parametrize("max_new", [1, 64])
+def test_attention_skips_tokens_of_missing_pages(nm, D, heads, max_new):
+    """A token whose page the table does not name is not attended, by either kernel: it adds nothing to the
+    sums, and a row that sees no other gives zeros."""
+    lens, new, P = [300, 70], [40, 40], 32
+    c, K, V = make(nm, lens, P=P, Hk=1, D=D, seed=101)
+    q = values(80, heads, D, 102)
+    for gone in ([4], [9], [0, 3, 8], list(range(9)), list(range(10))):
+        saved = c.book.clone()
+        for i, page in enumerate(gone):
+            c.tables[0, page] = -1 if i % 2 else c.n_pages
+        out, lse = c.attention(1, q, starts=starts_of(new), max_new=max_new, lse=True)
+        assert nm.device_status() == nm.NM_ERR_BOUNDS
+        c.book.copy_(saved)
+        there = ~np.isin(np.arange(300) // P, gone)
+        limits = [there & (np.arange(300) < 261 + i) for i in range(40)]
+        compare(out[:40], lse[:40], definition(f64(q[:40]), K[0], V[0], limits, D ** -0.5), 300, np.abs(V[0]).max())
+        want = definition(f64(q[40:]), K[1], V[1], [31 + i for i in range(40)], D ** -0.5)
+        compare(out[40:], lse[40:], want, 70, np.abs(V[1]).max())
+    assert nm.device_status() == nm.NM_OK
