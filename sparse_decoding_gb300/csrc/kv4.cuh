@@ -49,8 +49,9 @@ __device__ __forceinline__ void kv4_bad(const Kv4 &c) { atomicOr(c.status, 1u <<
 
 // One listed sequence: its row of the tables, its length, and its new tokens
 // [first, first + n_new) of the token arrays. Anything out of range is reported
-// and leaves it without tokens (len 0, but its rows, where starts names rows of
-// the arrays, are still there to be answered with zeros).
+// and leaves it without tokens: len 0, but its rows, where starts names rows of
+// the arrays, are still there to be answered with zeros; where it does not, n_new
+// is 0 and first -1.
 struct Kv4Seq {
     int row, len, first, n_new;
 };
@@ -64,7 +65,7 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4 &c, const Kv4Batch &b, int i
         e = b.starts[i + 1];
     }
     bool ok = a >= 0 && e >= a && e <= b.n_tokens;
-    s.first = ok ? (int)a : 0;
+    s.first = ok ? (int)a : -1;
     s.n_new = ok ? (int)(e - a) : 0;
     s.row = b.seqs ? b.seqs[i] : i;
     s.len = 0;
@@ -98,6 +99,42 @@ __device__ __forceinline__ int kv4_find(const Kv4Batch &b, int64_t i)
             hi = m;
     }
     return (i >= b.starts[lo] && i < b.starts[lo + 1]) ? lo : -1;
+}
+
+// Rows of the token arrays that no sequence covers: before starts[0], past the last end (padding), or
+// left by starts that are out of range. There are none when the starts rise from 0 to the number of
+// tokens, that is when all sequences are in range (no first is -1) and kv4_ends holds.
+__device__ __forceinline__ bool kv4_ends(const Kv4Batch &b)
+{
+    return !b.starts || (b.starts[0] == 0 && b.starts[b.n_seqs] == b.n_tokens);
+}
+// f(row) for those rows, a warp to each.
+template <class F>
+__device__ __forceinline__ void kv4_uncovered(const Kv4Batch &b, int64_t warp, int64_t warps, const F &f)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int64_t row = warp; row < b.n_tokens; row += warps) {
+        bool covered = false;
+#pragma unroll 1
+        for (int i = lane; i < b.n_seqs; i += 32) {
+            const int64_t a = b.starts[i], e = b.starts[i + 1];
+            covered |= a >= 0 && a <= row && row < e && e <= b.n_tokens;
+        }
+        if (!__any_sync(~0u, covered))
+            f(row);
+    }
+}
+// What attention answers there: width channels of out 0, lse -inf.
+__device__ __forceinline__ void kv4_answer_uncovered(const Kv4Batch &b, uint16_t *out, int64_t out_stride, int width,
+                                                     float *lse, int n_q_heads, int64_t warp, int64_t warps)
+{
+    kv4_uncovered(b, warp, warps, [&](int64_t row) {
+        for (int i = threadIdx.x & 31; i < width / 8; i += 32)
+            *(uint4 *)(out + row * out_stride + 8 * i) = make_uint4(0, 0, 0, 0);
+        for (int h = threadIdx.x & 31; lse && h < n_q_heads; h += 32)
+            lse[row * n_q_heads + h] = -INFINITY;
+    });
 }
 
 // The cell that holds position `pos` of table row `row`, for one layer and kv

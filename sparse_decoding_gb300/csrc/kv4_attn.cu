@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
     Kv4Seq *const seqs = (Kv4Seq *)(pre + b.n_seqs + 1);     // [n_seqs]
     __shared__ uint32_t s_last;
     __shared__ int s_chunk;
+    __shared__ bool s_rest; // some rows belong to no sequence
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     uint8_t *const ring = smem + warp * S * SM::kStage;
     const uint32_t rings = smem_addr(ring), bars = smem_addr(smem + SM::kBars) + warp * S * 8;
@@ -300,9 +301,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
             }
         }
         int64_t sum = 0;
+        bool rest = !kv4_ends(b);
         for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
             int64_t x = 0;
             if (i0 + lane < b.n_seqs) {
+                rest |= seqs[i0 + lane].first < 0;
                 const int units = units_of(seqs[i0 + lane].len);
                 x = pre[i0 + lane + 1] * (chunk ? pieces_of(units, chunk) : kOver + units);
             }
@@ -316,9 +319,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                 pre[i0 + lane + 1] = sum + x;
             sum += __shfl_sync(~0u, x, 31);
         }
+        rest = __any_sync(~0u, rest);
         if (lane == 0) {
             pre[0] = 0;
             s_chunk = chunk;
+            s_rest = rest;
         }
     }
     __syncthreads();
@@ -822,6 +827,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
         __syncthreads();
         pos += steps;
     }
+    if (s_rest)
+        kv4_answer_uncovered(b, a.out, a.out_stride, a.n_q_heads * D, a.lse, a.n_q_heads,
+                             (int64_t)blockIdx.x * kWarps + warp, (int64_t)gridDim.x * kWarps);
 }
 
 template <int D, int NT> nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, int num_sms, cudaStream_t st)

@@ -422,6 +422,7 @@ struct Shared {
     Piece piece[kRing];
     int64_t total, share;
     int seq, head, pair, step; // where the CTA's part of the line starts
+    bool rest;                 // some rows belong to no sequence
 };
 
 // A part of a tile: m and l of its 128 rows, then O, four channels of the rows side by side.
@@ -576,15 +577,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         for (int o = 16; o; o >>= 1)
             n += __shfl_xor_sync(~0u, n, o);
         if (lane == 0)
-            pre[i + 1] = n * c.n_kv_heads;
+            pre[i + 1] = s.first < 0 ? -1 : n * c.n_kv_heads; // -1: starts out of range, no blocks
     }
     fence_before();
     __syncthreads();
     fence_after();
     if (warp == 0) {
         int64_t sum = 0;
+        bool rest = !kv4_ends(b);
         for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
             int64_t x = i0 + lane < b.n_seqs ? pre[i0 + lane + 1] : 0;
+            rest |= x < 0;
+            x = x < 0 ? 0 : x;
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(~0u, x, o);
                 if (lane >= o)
@@ -636,7 +640,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 left -= __shfl_sync(~0u, x, 31);
             }
         }
+        rest = __any_sync(~0u, rest);
         if (lane == 0) {
+            sh.rest = rest;
             sh.total = total;
             sh.share = share;
             sh.seq = seq;
@@ -647,6 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
     }
     __syncthreads();
     const uint32_t tmem = sh.tmem;
+    if (sh.rest)
+        kv4_answer_uncovered(b, a.out, a.out_stride, a.n_q_heads * D, a.lse, a.n_q_heads,
+                             (int64_t)blockIdx.x * (kThreads / 32) + warp, (int64_t)gridDim.x * (kThreads / 32));
     bool dead = false;
     const auto wait = [&](uint64_t &bar, uint32_t parity) {
         kv4_wait(smem_addr(&bar), parity & 1u, c.status, dead);

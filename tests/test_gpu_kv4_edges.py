@@ -146,3 +146,59 @@ def test_attention_skips_tokens_of_missing_pages(nm, D, heads, max_new):
         want = definition(f64(q[40:]), K[1], V[1], [31 + i for i in range(40)], D ** -0.5)
         compare(out[40:], lse[40:], want, 70, np.abs(V[1]).max())
     assert nm.device_status() == nm.NM_OK
+
+
+# --- rows that no sequence covers -------------------------------------------------------------
+
+# starts, the tokens of the arrays, which rows have a sequence (its index), the status
+COVERS = [
+    ([0, 20, 30], 40, [(0, 20, 0), (20, 30, 1)], "NM_OK"),           # padding behind the last sequence
+    ([3, 20, 40], 40, [(3, 20, 0), (20, 40, 1)], "NM_OK"),           # and before the first
+    ([0, 20, 41], 40, [(0, 20, 0)], "NM_ERR_BOUNDS"),                # an end past the arrays
+    ([-1, 20, 40], 40, [(20, 40, 1)], "NM_ERR_BOUNDS"),              # a start before them
+    ([0, 30, 20], 40, [(0, 30, 0)], "NM_ERR_BOUNDS"),                # an end before its start
+    ([0, 100, 200], 40, [], "NM_ERR_BOUNDS"),
+    ([0, 0, 0], 40, [], "NM_OK"),
+]
+
+
+def attend_into(nm, c, layer, q, starts, max_new):
+    """attention with out and lse full of NaN before the call."""
+    T, H, D = q.shape
+    out = torch.full((T, H * D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), float("nan"), device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    assert nm.lib().nm_kv4_attention(c._ref, layer, None, starts.data_ptr(), starts.numel() - 1, T, max_new, q.data_ptr(),
+                                     H * D, H, D ** -0.5, out.data_ptr(), H * D, lse.data_ptr(), s) == nm.NM_OK
+    return out.view(T, H, D), lse
+
+
+@pytest.mark.parametrize("D,heads,max_new", [(128, 2, 1), (64, 8, 8), (128, 64, 64), (64, 64, 64)])
+@pytest.mark.parametrize("starts,T,rows,status", COVERS)
+def test_attention_rows_of_no_sequence_are_zero(nm, D, heads, max_new, starts, T, rows, status):
+    c, K, V = make(nm, [50, 90], Hk=2, D=D, seed=111)
+    q = values(T, heads, D, 112)
+    out, lse = attend_into(nm, c, 1, q, ints(starts), max_new)
+    assert nm.device_status() == getattr(nm, status)
+    none = np.ones(T, bool)
+    for a, b, s in rows:
+        none[a:b] = False
+        n = b - a
+        want = definition(f64(q[a:b]), K[s], V[s], [len(K[s]) - n + i + 1 for i in range(n)], D ** -0.5)
+        compare(out[a:b], lse[a:b], want, len(K[s]), np.abs(V[s]).max())
+    none = torch.from_numpy(none).cuda()
+    assert bool((out[none] == 0).all()) and bool(torch.isneginf(lse[none]).all())
+
+
+@pytest.mark.parametrize("heads,max_new", [(2, 1), (2, 9), (4, 1000)])
+def test_attention_padding_behind_many_sequences(nm, heads, max_new):
+    n, T = 700, 700 + 61
+    lens = [1 + i % 37 for i in range(n)]
+    c, K, V = make(nm, lens, P=16, L=1, Hk=1, D=64, seed=113)
+    q = values(T, heads, 64, 114)
+    out, lse = attend_into(nm, c, 0, q, ints(range(n + 1)), max_new)
+    assert nm.device_status() == nm.NM_OK
+    assert bool((out[n:] == 0).all()) and bool(torch.isneginf(lse[n:]).all())
+    for s in (0, 1, 511, 512, 699):
+        compare(out[s:s + 1], lse[s:s + 1], definition(f64(q[s:s + 1]), K[s], V[s], [lens[s]], 0.125), lens[s],
+                np.abs(V[s]).max())
