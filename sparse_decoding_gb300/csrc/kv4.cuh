@@ -153,12 +153,12 @@ __device__ __forceinline__ int64_t kv4_cell_offset(const Kv4 &c, int page, int l
 
 // A bounded wait (about a second, then NM_ERR_TIMEOUT; `dead` threads poll once). The
 // clock is read only after some polls: reading it takes longer than most waits.
-__device__ __forceinline__ void kv4_wait(uint32_t bar, uint32_t parity, uint32_t *status, bool &dead)
+template <class F> __device__ __forceinline__ void kv4_until(const F &there, uint32_t *status, bool &dead)
 {
     uint64_t t0 = 0;
     uint32_t polls = 0;
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
+    while (!there()) {
         if (dead)
             return;
         if (++polls < 64)
@@ -173,10 +173,30 @@ __device__ __forceinline__ void kv4_wait(uint32_t bar, uint32_t parity, uint32_t
         }
     }
 }
+__device__ __forceinline__ void kv4_wait(uint32_t bar, uint32_t parity, uint32_t *status, bool &dead)
+{
+    kv4_until([&]() { return mbar_try_wait(bar, parity); }, status, dead);
+}
 
 __device__ __forceinline__ void kv4_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Arrives and waits for the others of the barrier's count: a __syncthreads() of some threads that is
+// bounded as above.
+__device__ __forceinline__ void kv4_meet(uint32_t bar, uint32_t *status, bool &dead)
+{
+    uint64_t phase;
+    asm volatile("mbarrier.arrive.shared::cta.b64 %0, [%1];" : "=l"(phase) : "r"(bar) : "memory");
+    kv4_until([&]() {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "l"(phase)
+                     : "memory");
+        return ok != 0;
+    }, status, dead);
 }
 
 // 16 bytes of read-only data

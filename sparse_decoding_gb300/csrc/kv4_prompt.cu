@@ -665,9 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
     const auto get_piece = [&](uint32_t p) {
         wait(sh.piece_full[p % kRing], p / kRing);
         dead = __any_sync(~0u, dead);
-        Piece w{};
-        if (!dead)
-            w = sh.piece[p % kRing];
+        Piece w = sh.piece[p % kRing];
+        if (dead)
+            w.nblk = w.n0 = w.n1 = 0;
         __syncwarp();
         if (lane == 0)
             kv4_arrive(smem_addr(&sh.piece_empty[p % kRing]));
@@ -687,7 +687,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
         const auto token_of = [&](const Piece &w) { return (2 * w.pair + k) * tt + row_token; };
         const auto valid_in = [&](const Piece &w) { return row < tt * a.ratio && token_of(w) < w.n_new; };
         uint32_t n_s = 0, n_o = 0; // blocks and pieces of this tile so far
-        uint32_t n_j = 0;          // meetings of its threads
 
         // The row of Q: scaled by a power of two, channels in the order of the unpacked
         // keys. Returns the factor of the scores.
@@ -781,10 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
                 // first in groups of g (at most 16 to a join), then the groups (32 new tokens after
                 // 32768 by one join of 32 parts: 77 us). The tile's threads meet on an mbarrier, whose
                 // wait is bounded: after one that ran out, warps may be missing.
-                const auto meet = [&]() {
-                    kv4_arrive(smem_addr(&sh.met[k]));
-                    wait(sh.met[k], n_j++);
-                };
+                const auto meet = [&]() { kv4_meet(smem_addr(&sh.met[k]), c.status, dead); };
                 const auto last_of = [&](uint32_t *counter, int n) {
                     meet();
                     if (row == 0) {
