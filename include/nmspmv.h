@@ -584,7 +584,8 @@ nm_status nm_kv4_append(const nm_kv4_cache *cache, int layer, const int32_t *seq
 /*
  * nm_kv4_read -- the values that the cache holds for the last tokens of each
  * sequence (as many as starts says), k and v each [n_tokens][n_kv_heads]
- * [head_dim] contiguous in bf16, or fp32 with f32 != 0; either may be NULL.
+ * [head_dim] contiguous in bf16, or fp32 with f32 != 0; either may be NULL. Rows of
+ * tokens that a sequence does not have, or that belong to no listed sequence, are 0.
  */
 nm_status nm_kv4_read(const nm_kv4_cache *cache, int layer, const int32_t *seqs, const int32_t *starts, int n_seqs,
                       int64_t n_tokens, void *k, void *v, int f32, void *stream);

@@ -417,13 +417,36 @@ template <int D> __global__ void __launch_bounds__(256, 4) append_kernel(const K
     }
 }
 
-// One warp per (cell, kv head), as append.
+// One row of read's results (n bytes of each) becomes zeros, a warp to it.
+__device__ __forceinline__ void zero_row(void *k, void *v, int64_t row, int64_t n)
+{
+    for (int64_t i = threadIdx.x & 31; i < n / 16; i += 32) {
+        if (k)
+            ((uint4 *)((uint8_t *)k + row * n))[i] = make_uint4(0, 0, 0, 0);
+        if (v)
+            ((uint4 *)((uint8_t *)v + row * n))[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+constexpr int kRestCtas = 16; // CTAs that look for rows of no sequence: there are few as a rule
+
+// One warp per (cell, kv head), as append; the last CTAs see to the rows that belong to no sequence.
 template <int D, bool F32>
-__global__ void __launch_bounds__(256) read_kernel(const Kv4 c, const Kv4Batch b, int layer, void *k, void *v, int64_t slots)
+__global__ void __launch_bounds__(256)
+    read_kernel(const Kv4 c, const Kv4Batch b, int layer, void *k, void *v, int64_t slots, int64_t cell_ctas)
 {
     constexpr int N = D / 16, G = D / 64;
     using C = Kv4Cell<D>;
     const int lane = threadIdx.x & 31, i = lane & 7, part = lane >> 3;
+    if (blockIdx.x >= cell_ctas) {
+        bool rest = !kv4_ends(b);
+        for (int x = threadIdx.x; x < b.n_seqs; x += blockDim.x)
+            rest |= kv4_seq(c, b, x, blockIdx.x == cell_ctas).first < 0;
+        if (__syncthreads_or(rest))
+            kv4_uncovered(b, (blockIdx.x - cell_ctas) * 8 + (threadIdx.x >> 5), kRestCtas * 8,
+                          [&](int64_t row) { zero_row(k, v, row, (int64_t)c.n_kv_heads * D * (F32 ? 4 : 2)); });
+        return;
+    }
     const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (w >= slots)
         return;
@@ -543,19 +566,20 @@ nm_status kv4_launch_append(const Kv4 &c, const Kv4Batch &b, int layer, const vo
 
 nm_status kv4_launch_read(const Kv4 &c, const Kv4Batch &b, int layer, void *k, void *v, bool f32, cudaStream_t st)
 {
-    const int64_t slots = slots_of(b) * c.n_kv_heads, grid = (slots + 7) / 8;
+    const int64_t slots = slots_of(b) * c.n_kv_heads, ctas = (slots + 7) / 8;
+    const int64_t grid = ctas + (b.starts ? kRestCtas : 0);
     if (grid > 0x7FFFFFFF)
         return NM_ERR_SHAPE;
     if (c.head_dim == 128) {
         if (f32)
-            read_kernel<128, true><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots);
+            read_kernel<128, true><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots, ctas);
         else
-            read_kernel<128, false><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots);
+            read_kernel<128, false><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots, ctas);
     } else {
         if (f32)
-            read_kernel<64, true><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots);
+            read_kernel<64, true><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots, ctas);
         else
-            read_kernel<64, false><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots);
+            read_kernel<64, false><<<(unsigned)grid, 256, 0, st>>>(c, b, layer, k, v, slots, ctas);
     }
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }

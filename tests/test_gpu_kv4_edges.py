@@ -202,3 +202,33 @@ def test_attention_padding_behind_many_sequences(nm, heads, max_new):
     for s in (0, 1, 511, 512, 699):
         compare(out[s:s + 1], lse[s:s + 1], definition(f64(q[s:s + 1]), K[s], V[s], [lens[s]], 0.125), lens[s],
                 np.abs(V[s]).max())
+
+
+def read_into(nm, c, layer, T, starts, f32=True, k=True, v=True):
+    """read with both results full of NaN before the call; None for one that is not asked for."""
+    shape = (T, c.n_kv_heads, c.head_dim)
+    res = [torch.full(shape, float("nan"), dtype=torch.float32 if f32 else torch.bfloat16, device="cuda") if x else None
+           for x in (k, v)]
+    s = torch.cuda.current_stream().cuda_stream
+    assert nm.lib().nm_kv4_read(c._ref, layer, None, starts.data_ptr(), starts.numel() - 1, T,
+                                *[None if x is None else x.data_ptr() for x in res], int(f32), s) == nm.NM_OK
+    return res
+
+
+@pytest.mark.parametrize("D,f32_", [(128, True), (128, False), (64, True), (64, False)])
+@pytest.mark.parametrize("starts,T,rows,status", COVERS)
+def test_read_rows_of_no_sequence_are_zero(nm, D, f32_, starts, T, rows, status):
+    c, K, V = make(nm, [50, 90], Hk=3, D=D, seed=115)
+    k, v = read_into(nm, c, 1, T, ints(starts), f32=f32_)
+    assert nm.device_status() == getattr(nm, status)
+    none = np.ones(T, bool)
+    for a, b, s in rows:
+        none[a:b] = False
+        for got, held in ((k, K[s]), (v, V[s])):
+            want = held[len(held) - (b - a):]
+            np.testing.assert_array_equal(f32(got[a:b]), want if f32_ else ref.bf16(want))
+    none = torch.from_numpy(none).cuda()
+    assert bool((k[none] == 0).all()) and bool((v[none] == 0).all())
+    only, _ = read_into(nm, c, 1, T, ints(starts), f32=f32_, v=False)
+    assert torch.equal(only, k)
+    nm.device_status()
