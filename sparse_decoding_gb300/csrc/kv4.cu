@@ -268,6 +268,7 @@ struct AppendArgs {
     int64_t rope_rows;
     int64_t slots;      // of cells, times the kv heads: warps that write the cache
     int64_t cell_ctas;  // the CTAs that hold those warps
+    int64_t q_ctas;     // and the ones that turn q
     int q_warps, q_each; // warps of a token's q heads, and how many fours of heads each turns
 };
 
@@ -412,8 +413,11 @@ template <int D> __global__ void __launch_bounds__(256, 4) append_kernel(const K
         const int64_t w = (int64_t)blockIdx.x * 8 + warp;
         if (w < a.slots)
             append_cell<D>(c, b, a, w);
-    } else {
+    } else if (blockIdx.x < a.cell_ctas + a.q_ctas) {
         append_q<D>(c, b, a, (int64_t)(blockIdx.x - a.cell_ctas) * 8 + warp);
+    } else { // starts out of range need not have a cell of their own: one CTA looks at all of them
+        for (int i = threadIdx.x; i < b.n_seqs; i += blockDim.x)
+            kv4_seq(c, b, i, true);
     }
 }
 
@@ -544,17 +548,17 @@ nm_status kv4_launch_append(const Kv4 &c, const Kv4Batch &b, int layer, const vo
                             void *q_out, int64_t q_out_stride, const float *rope, int64_t rope_rows, cudaStream_t st)
 {
     AppendArgs a{layer, n_q_heads, (const uint16_t *)k, (const uint16_t *)v, (const uint16_t *)q,
-                 (uint16_t *)q_out, k_stride, v_stride, q_stride, q_out_stride, rope, rope_rows, 0, 0, 1, 1};
+                 (uint16_t *)q_out, k_stride, v_stride, q_stride, q_out_stride, rope, rope_rows, 0, 0, 0, 1, 1};
     a.slots = slots_of(b) * c.n_kv_heads;
     a.cell_ctas = (a.slots + 7) / 8;
-    int64_t grid = a.cell_ctas;
     if (q) {
         // with many tokens a warp turns up to four fours of a token's heads, so that its angles are read once
         const int fours = (n_q_heads + 3) / 4;
         a.q_each = b.n_tokens * fours >= 65536 ? (fours < 4 ? fours : 4) : 1;
         a.q_warps = (fours + a.q_each - 1) / a.q_each;
-        grid += (b.n_tokens * a.q_warps + 7) / 8;
+        a.q_ctas = (b.n_tokens * a.q_warps + 7) / 8;
     }
+    const int64_t grid = a.cell_ctas + a.q_ctas + (b.starts ? 1 : 0);
     if (grid > 0x7FFFFFFF)
         return NM_ERR_SHAPE;
     if (c.head_dim == 128)

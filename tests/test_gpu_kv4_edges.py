@@ -232,3 +232,18 @@ def test_read_rows_of_no_sequence_are_zero(nm, D, f32_, starts, T, rows, status)
     only, _ = read_into(nm, c, 1, T, ints(starts), f32=f32_, v=False)
     assert torch.equal(only, k)
     nm.device_status()
+
+
+@pytest.mark.parametrize("starts,T", [([-1, 1, 2], 2), ([-5, -5, 2], 2), ([0, 50, 3, 8], 60), ([0, 1, 1 << 30], 2),
+                                      ([0, 2, 3], 2)])
+def test_append_and_read_report_starts_out_of_range(nm, starts, T):
+    c, _, _ = make(nm, [60] * (len(starts) - 1), seed=116)
+    k = values(T, 2, 128, 117)
+    c.append(1, k, k, starts=ints(starts))
+    assert nm.device_status() == nm.NM_ERR_BOUNDS
+    c.read(1, T, starts=ints(starts))
+    assert nm.device_status() == nm.NM_ERR_BOUNDS
+    good = [0] * (len(starts) - 1) + [T]
+    c.append(1, k, k, starts=ints(good))
+    c.read(1, T, starts=ints(good))
+    assert nm.device_status() == nm.NM_OK
