@@ -6,6 +6,7 @@
 
 #include "kernels.h"
 #include "nm_common.cuh"
+#include "per_device.h"
 
 namespace nm {
 
@@ -215,6 +216,7 @@ struct Kv4Work {
     uint32_t *counters;  // [kKv4Counters], zero between launches
     int32_t *list;       // [64 + 2 n_pages]: page lists of the table calls
     float *partials;     // attention parts
+    int device, num_sms;
 };
 size_t kv4_partial_bytes(int head_dim);
 
@@ -235,10 +237,9 @@ struct Kv4Attn {
 };
 constexpr int kKv4PromptCtas = 160; // CTAs of the prompt kernel at most
 size_t kv4_prompt_partial_bytes(int head_dim);
-nm_status kv4_launch_prompt(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a, const Kv4Work &w, int num_sms,
-                            cudaStream_t st);
+nm_status kv4_launch_prompt(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a, const Kv4Work &w, cudaStream_t st);
 nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a, int64_t max_new, const Kv4Work &w,
-                               int num_sms, cudaStream_t st);
+                               cudaStream_t st);
 
 nm_status kv4_launch_reserve(const Kv4 &c, const int32_t *seqs, const int32_t *starts, int n, const Kv4Work &w,
                              cudaStream_t st);

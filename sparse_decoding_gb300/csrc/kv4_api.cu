@@ -5,8 +5,6 @@
 namespace nm {
 namespace {
 
-constexpr int kMaxDevices = 64;
-
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 bool sizes_ok(int page_tokens, int n_layers, int n_kv_heads, int head_dim)
@@ -43,17 +41,18 @@ nm_status view(const nm_kv4_cache *k, Kv4 *c, Kv4Work *w, int *num_sms)
     nm_status s = library_status_word(&c->status);
     if (s != NM_OK)
         return s;
-    static int sms[kMaxDevices] = {};
+    static std::atomic<int> sms[kMaxDevices] = {}; // 0: not asked for yet; threads that ask at once get the same
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
         return NM_ERR_CUDA;
-    if (!sms[dev]) {
-        int n = 0;
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (!n) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
             return NM_ERR_CUDA;
-        sms[dev] = n;
+        sms[dev].store(n, std::memory_order_relaxed);
     }
-    *num_sms = sms[dev];
+    w->device = dev;
+    w->num_sms = *num_sms = n;
     if (2 * *num_sms > (int)kKv4Counters / 4)
         return NM_ERR_UNSUPPORTED;
     c->pool = (uint8_t *)k->pool;
@@ -330,7 +329,7 @@ nm_status nm_kv4_attention(const nm_kv4_cache *cache, int layer, const int32_t *
         return s;
     const Kv4Batch b{seqs, starts, n_seqs, n_tokens};
     const Kv4Attn a{layer, q_bf16, q_stride, n_q_heads, scale, out_bf16, out_stride, lse};
-    return kv4_launch_attention(c, b, a, starts ? max_new : 1, w, sms, (cudaStream_t)stream);
+    return kv4_launch_attention(c, b, a, starts ? max_new : 1, w, (cudaStream_t)stream);
 }
 
 } // extern "C"

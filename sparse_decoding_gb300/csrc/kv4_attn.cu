@@ -36,7 +36,6 @@
 // first: 67 us with loads straight to registers; 62 by bulk copies; 50.6 with masks at
 // the end only and addresses a round ahead; 43.9 two cells at a time and a join of
 // independent loads.
-#include <mutex>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -832,19 +831,19 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                              (int64_t)blockIdx.x * kWarps + warp, (int64_t)gridDim.x * kWarps);
 }
 
-template <int D, int NT> nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, int num_sms, cudaStream_t st)
+template <int D, int NT>
+nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, const Kv4Work &w, cudaStream_t st)
 {
     constexpr size_t kMost = Smem<D, NT>::kSeqs + kKv4MaxSeqs * 24 + 8;
     static_assert(kMost + 1024 <= 227 * 1024, "shared memory");
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(attn_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
-    });
-    if (attr != cudaSuccess)
+    static OncePerDevice once;
+    if (!once(w.device, [] {
+            return cudaFuncSetAttribute(attn_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost) ==
+                   cudaSuccess;
+        }))
         return NM_ERR_CUDA;
     const size_t smem = Smem<D, NT>::kSeqs + (size_t)(b.n_seqs + 1) * 8 + (size_t)b.n_seqs * sizeof(Kv4Seq);
-    const unsigned grid = (unsigned)(num_sms * (NT <= 2 ? 2 : 1)); // at most kKv4Counters / 4
+    const unsigned grid = (unsigned)(w.num_sms * (NT <= 2 ? 2 : 1)); // at most kKv4Counters / 4
     attn_rows_kernel<D, NT><<<grid, kThreads, smem, st>>>(c, b, a);
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
@@ -860,7 +859,7 @@ size_t kv4_partial_bytes(int head_dim)
 }
 
 nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &at, int64_t max_new, const Kv4Work &w,
-                               int num_sms, cudaStream_t st)
+                               cudaStream_t st)
 {
     const AttnArgs a{at.layer, at.n_q_heads / c.n_kv_heads, at.n_q_heads, (const uint16_t *)at.q, at.q_stride,
                      at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials};
@@ -895,17 +894,17 @@ nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
     //                   prompt   27.6     37.3     52.6      76.5
     const int64_t rows = (max_new < 65 ? max_new : 65) * a.ratio;
     if (rows > 64 && b.n_tokens * at.n_q_heads > 1024)
-        return kv4_launch_prompt(c, b, at, w, num_sms, st);
+        return kv4_launch_prompt(c, b, at, w, st);
     if (c.head_dim == 64)
-        return rows <= 8                 ? launch_rows<64, 1>(c, b, a, num_sms, st)
-               : rows > 16 && rows <= 24 ? launch_rows<64, 3>(c, b, a, num_sms, st)
-                                         : launch_rows<64, 2>(c, b, a, num_sms, st);
-    return rows <= 8    ? launch_rows<128, 1>(c, b, a, num_sms, st)
-           : rows <= 16 ? launch_rows<128, 2>(c, b, a, num_sms, st)
-           : rows <= 24 ? launch_rows<128, 3>(c, b, a, num_sms, st)
-           : rows <= 32 ? launch_rows<128, 4>(c, b, a, num_sms, st)
-           : rows <= 48 ? launch_rows<128, 3>(c, b, a, num_sms, st)
-                        : launch_rows<128, 4>(c, b, a, num_sms, st);
+        return rows <= 8                 ? launch_rows<64, 1>(c, b, a, w, st)
+               : rows > 16 && rows <= 24 ? launch_rows<64, 3>(c, b, a, w, st)
+                                         : launch_rows<64, 2>(c, b, a, w, st);
+    return rows <= 8    ? launch_rows<128, 1>(c, b, a, w, st)
+           : rows <= 16 ? launch_rows<128, 2>(c, b, a, w, st)
+           : rows <= 24 ? launch_rows<128, 3>(c, b, a, w, st)
+           : rows <= 32 ? launch_rows<128, 4>(c, b, a, w, st)
+           : rows <= 48 ? launch_rows<128, 3>(c, b, a, w, st)
+                        : launch_rows<128, 4>(c, b, a, w, st);
 }
 
 } // namespace nm

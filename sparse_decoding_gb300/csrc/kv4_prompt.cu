@@ -45,7 +45,6 @@
 // All waits are bounded; one that runs out sets NM_ERR_TIMEOUT. Its thread's later waits
 // poll once and its warp takes no more pieces, so the others run out in turn, the MMAs
 // in flight end, and the kernel frees its tensor memory and returns.
-#include <mutex>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -1142,19 +1141,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const Kv4 c, c
     }
 }
 
-template <int D> nm_status launch(const Kv4 &c, const Kv4Batch &b, const PromptArgs &a, int grid, cudaStream_t st)
+template <int D> nm_status launch(const Kv4 &c, const Kv4Batch &b, const PromptArgs &a, const Kv4Work &w, cudaStream_t st)
 {
     constexpr size_t kMax = Cfg<D>::kTiles + 1024 + kSeqCache * sizeof(Kv4Seq);
     static_assert(kMax + sizeof(Shared) <= 227 * 1024, "shared memory");
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMax);
-    });
-    if (attr != cudaSuccess)
+    static OncePerDevice once;
+    if (!once(w.device, [] {
+            return cudaFuncSetAttribute(attn_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMax) ==
+                   cudaSuccess;
+        }))
         return NM_ERR_CUDA;
     const size_t smem =
         Cfg<D>::kTiles + 1024 + (size_t)(b.n_seqs < kSeqCache ? b.n_seqs : kSeqCache) * sizeof(Kv4Seq);
+    const int grid = w.num_sms < kKv4PromptCtas ? w.num_sms : kKv4PromptCtas;
     attn_prompt_kernel<D><<<grid, kThreads, smem, st>>>(c, b, a);
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
@@ -1163,13 +1162,11 @@ template <int D> nm_status launch(const Kv4 &c, const Kv4Batch &b, const PromptA
 
 size_t kv4_prompt_partial_bytes(int head_dim) { return (size_t)kKv4PromptCtas * 4 * 128 * (head_dim + 2) * 4; }
 
-nm_status kv4_launch_prompt(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &at, const Kv4Work &w, int num_sms,
-                            cudaStream_t st)
+nm_status kv4_launch_prompt(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &at, const Kv4Work &w, cudaStream_t st)
 {
     const PromptArgs a{at.layer, at.n_q_heads / c.n_kv_heads, at.n_q_heads, (const uint16_t *)at.q, at.q_stride,
                        at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials};
-    const int grid = num_sms < kKv4PromptCtas ? num_sms : kKv4PromptCtas;
-    return c.head_dim == 128 ? launch<128>(c, b, a, grid, st) : launch<64>(c, b, a, grid, st);
+    return c.head_dim == 128 ? launch<128>(c, b, a, w, st) : launch<64>(c, b, a, w, st);
 }
 
 } // namespace nm

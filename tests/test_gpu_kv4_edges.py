@@ -247,3 +247,26 @@ def test_append_and_read_report_starts_out_of_range(nm, starts, T):
     c.append(1, k, k, starts=ints(good))
     c.read(1, T, starts=ints(good))
     assert nm.device_status() == nm.NM_OK
+
+
+# --- a second device ----------------------------------------------------------------------------
+
+def test_attention_on_a_second_device(nm):
+    """Both attention kernels on one device, then on another, in one process."""
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one device")
+    results = []
+    for d in (0, 1):
+        torch.cuda.set_device(d)
+        try:
+            nm.init()
+            c = nm.Kv4Cache(8, 32, 1, 1, 128, 1, 8, device=f"cuda:{d}")
+            st = torch.tensor([0, 100], dtype=torch.int32, device=f"cuda:{d}")
+            k, q = (values(100, h, 128, 131).cpu().to(f"cuda:{d}") for h in (1, 16))
+            c.reserve(starts=st)
+            c.append(0, k, k, starts=st)
+            results.append([c.attention(0, q, starts=st, max_new=m).cpu() for m in (1, 100)])
+            assert nm.device_status() == nm.NM_OK
+        finally:
+            torch.cuda.set_device(0)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
