@@ -50,6 +50,26 @@ template <int N> __device__ __forceinline__ Raw<N> load_raw(const uint16_t *p, i
     }
     return r;
 }
+// The same of memory that the kernel may write too (q in place): not by the read-only path.
+template <int N> __device__ __forceinline__ Raw<N> load_own(const uint16_t *p, int i, int half)
+{
+    Raw<N> r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (N == 8) {
+            const uint4 v = *(const uint4 *)(p + h * half + 8 * i);
+            r.w[h][0] = v.x;
+            r.w[h][1] = v.y;
+            r.w[h][N / 2 - 2] = v.z;
+            r.w[h][N / 2 - 1] = v.w;
+        } else {
+            const uint2 v = *(const uint2 *)(p + h * half + 4 * i);
+            r.w[h][0] = v.x;
+            r.w[h][1] = v.y;
+        }
+    }
+    return r;
+}
 template <int N> __device__ __forceinline__ Vec<N> unpack(const Raw<N> &r)
 {
     Vec<N> v;
@@ -259,6 +279,7 @@ __device__ __forceinline__ bool cell_job(const Kv4 &c, const Kv4Batch &b, int64_
     return true;
 }
 
+constexpr int kFours = 4; // fours of heads that a warp turns at most
 struct AppendArgs {
     int layer, n_q_heads;
     const uint16_t *k, *v, *q;
@@ -383,12 +404,18 @@ template <int D> __device__ __forceinline__ void append_q(const Kv4 &c, const Kv
     if (a.rope && ok)
         turn = load_turn<N>(a.rope + (int64_t)pos * D, i);
     const int h0 = (int)(w % a.q_warps) * a.q_each * 4 + (lane >> 3);
-#pragma unroll 4
-    for (int n = 0; n < a.q_each; ++n) {
+    // all of the warp's heads are asked for before the first is written
+    Raw<N> raw[kFours];
+#pragma unroll
+    for (int n = 0; n < kFours; ++n)
+        if (n < a.q_each && h0 + 4 * n < a.n_q_heads)
+            raw[n] = load_own<N>(a.q + token * a.q_stride + (int64_t)(h0 + 4 * n) * D, i, D / 2);
+#pragma unroll
+    for (int n = 0; n < kFours; ++n) {
         const int h = h0 + 4 * n;
-        if (h >= a.n_q_heads)
+        if (n >= a.q_each || h >= a.n_q_heads)
             break;
-        Vec<N> v = unpack<N>(load_raw<N>(a.q + token * a.q_stride + (int64_t)h * D, i, D / 2));
+        Vec<N> v = unpack<N>(raw[n]);
         if (a.rope)
             rotate<N>(v, turn);
         uint16_t *const o = a.q_out + token * a.q_out_stride + (int64_t)h * D;
@@ -554,7 +581,7 @@ nm_status kv4_launch_append(const Kv4 &c, const Kv4Batch &b, int layer, const vo
     if (q) {
         // with many tokens a warp turns up to four fours of a token's heads, so that its angles are read once
         const int fours = (n_q_heads + 3) / 4;
-        a.q_each = b.n_tokens * fours >= 65536 ? (fours < 4 ? fours : 4) : 1;
+        a.q_each = b.n_tokens * fours >= 65536 ? (fours < kFours ? fours : kFours) : 1;
         a.q_warps = (fours + a.q_each - 1) / a.q_each;
         a.q_ctas = (b.n_tokens * a.q_warps + 7) / 8;
     }

@@ -249,6 +249,40 @@ def test_append_and_read_report_starts_out_of_range(nm, starts, T):
     assert nm.device_status() == nm.NM_OK
 
 
+# --- append ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D,heads,T", [(128, 32, 8192), (64, 17, 16384), (128, 6, 50)])
+def test_append_turns_q_in_place_as_it_does_beside(nm, D, heads, T):
+    """q_out may be q itself, with many tokens (a warp turns several heads) and few."""
+    c = nm.Kv4Cache(T // 128 + 1, 128, 1, 1, D, 1, T // 128 + 1)
+    c.reserve(starts=ints([0, T]))
+    k, q, rope = values(T, 1, D, 121), values(T, heads, D, 122), rope_table(T, D)
+    beside = c.append(0, k, k, q=q, rope=rope, starts=ints([0, T]))
+    c.append(0, k, k, q=q, rope=rope, starts=ints([0, T]), q_out=q)
+    assert torch.equal(q, beside) and nm.device_status() == nm.NM_OK
+
+
+def test_append_past_the_rope_table_and_again(nm):
+    """Tokens past the rope table are not written and the status tells; appended again with a table that
+    reaches them, the sequence is as if it had always been."""
+    D, T = 128, 70
+    c, K, V = make(nm, [30], P=64, Hk=1, seed=123, max_seqs=2)
+    c.reserve(seqs=ints([1]), starts=ints([0, T]))
+    k, v = values(T, 1, D, 124), values(T, 1, D, 125)
+    rope = rope_table(T, D)
+    c.append(1, k, v, rope=rope[:50].contiguous(), seqs=ints([1]), starts=ints([0, T]))
+    assert nm.device_status() == nm.NM_ERR_BOUNDS
+    q = values(20, 64, D, 126)
+    out, lse = c.attention(1, q, seqs=ints([0]), starts=ints([0, 20]), max_new=20, lse=True)
+    compare(out, lse, definition(f64(q), K[0], V[0], [11 + i for i in range(20)], D ** -0.5), 30, np.abs(V[0]).max())
+    c.append(1, k, v, rope=rope, seqs=ints([1]), starts=ints([0, T]))
+    cs = rope.cpu().numpy()
+    rk, rv = ref.quantise(ref.rotate(f32(k), cs[:, :64], cs[:, 64:]), f32(v))
+    out, lse = c.attention(1, q, seqs=ints([1]), starts=ints([0, 20]), max_new=20, lse=True)
+    compare(out, lse, definition(f64(q), rk, rv, [51 + i for i in range(20)], D ** -0.5), T, np.abs(rv).max())
+    assert nm.device_status() == nm.NM_OK
+
+
 # --- a second device ----------------------------------------------------------------------------
 
 def test_attention_on_a_second_device(nm):

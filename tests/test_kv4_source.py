@@ -61,3 +61,12 @@ def test_rows_kernel_waits_for_its_copies_after_a_wait_that_ran_out():
     assert rest.index("if (__any_sync(~0u, dead))") < rest.index("const uint32_t filled")
     assert re.search(r"for \(int z = x; z < x \+ S && z < mine; \+\+z\) \{\s*dead = false;\s*kv4_wait\(", out)
     assert re.search(r"dead = true;\s*mine = x;\s*break;", out)
+
+
+def test_append_reads_q_as_memory_that_it_writes():
+    """q_out may be q: loads by the read-only path are for memory that no thread of the kernel writes."""
+    text = source("kv4.cu")
+    turn = block(text, "void append_q(")
+    assert re.findall(r"(\w+)<N>\(a\.q \+", turn) == ["load_own"]
+    own = block(text, "Raw<N> load_own(")
+    assert "ldg" not in own and ".nc" not in own
