@@ -566,7 +566,10 @@ __global__ void __launch_bounds__(256)
 }
 
 // Slots of cells for the new tokens of a call (see cell_job).
-int64_t slots_of(const Kv4Batch &b) { return b.starts ? b.n_tokens / kKv4Cell + 2 * (int64_t)b.n_seqs : b.n_seqs; }
+int64_t slots_of(const Kv4Batch &b)
+{
+    return b.starts && b.n_seqs > 0 ? b.n_tokens / kKv4Cell + 2 * (int64_t)b.n_seqs : b.n_seqs;
+}
 
 } // namespace
 

@@ -89,7 +89,7 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4 &c, const Kv4Batch &b, int i
 // cover it). starts is nondecreasing; any values end the search.
 __device__ __forceinline__ int kv4_find(const Kv4Batch &b, int64_t i)
 {
-    if (!b.starts)
+    if (!b.starts || b.n_seqs == 0)
         return i < b.n_seqs ? (int)i : -1;
     int lo = 0, hi = b.n_seqs; // starts[lo] <= i < starts[hi], if it is covered at all
     while (hi - lo > 1) {

@@ -252,7 +252,7 @@ nm_status nm_kv4_append(const nm_kv4_cache *cache, int layer, const int32_t *seq
         return s;
     if (layer < 0 || layer >= cache->n_layers || n_q_heads < 0 || n_q_heads > 65536 || rope_rows < 0)
         return NM_ERR_SHAPE;
-    if (n_seqs == 0 || n_tokens == 0)
+    if (n_tokens == 0)
         return NM_OK;
     const int D = cache->head_dim;
     if ((s = check_tokens(k_bf16, k_stride, cache->n_kv_heads, D)) != NM_OK ||
@@ -285,7 +285,7 @@ nm_status nm_kv4_read(const nm_kv4_cache *cache, int layer, const int32_t *seqs,
         return s;
     if (layer < 0 || layer >= cache->n_layers)
         return NM_ERR_SHAPE;
-    if (n_seqs == 0 || n_tokens == 0 || (!k && !v))
+    if (n_tokens == 0 || (!k && !v))
         return NM_OK;
     if (!aligned(k, 16) || !aligned(v, 16))
         return NM_ERR_ALIGN;
@@ -314,7 +314,7 @@ nm_status nm_kv4_attention(const nm_kv4_cache *cache, int layer, const int32_t *
         return NM_ERR_INVALID_ARG;
     if (n_tokens * n_q_heads > 0x3FFFFFFF)
         return NM_ERR_SHAPE;
-    if (n_seqs == 0 || n_tokens == 0)
+    if (n_tokens == 0)
         return NM_OK;
     const int D = cache->head_dim;
     if ((s = check_tokens(q_bf16, q_stride, n_q_heads, D)) != NM_OK ||

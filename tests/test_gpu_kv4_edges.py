@@ -249,6 +249,22 @@ def test_append_and_read_report_starts_out_of_range(nm, starts, T):
     assert nm.device_status() == nm.NM_OK
 
 
+@pytest.mark.parametrize("D,heads,max_new", [(128, 2, 1), (64, 64, 64)])
+def test_calls_with_tokens_and_no_sequence(nm, D, heads, max_new):
+    """No sequence is listed: every row belongs to none."""
+    T = 40
+    c, _, _ = make(nm, [50, 90], Hk=2, D=D, seed=118)
+    pool = c.pool.clone()
+    q = values(T, heads, D, 119)
+    out, lse = attend_into(nm, c, 1, q, ints([0]), max_new)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    k, v = read_into(nm, c, 1, T, ints([0]))
+    assert bool((k == 0).all()) and bool((v == 0).all())
+    k = values(T, 2, D, 120)
+    qo = c.append(1, k, k, q=q, rope=rope_table(100, D), starts=ints([0]), q_out=torch.full_like(q, float("nan")))
+    assert bool((qo == 0).all()) and torch.equal(c.pool, pool) and nm.device_status() == nm.NM_OK
+
+
 # --- append ---------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("D,heads,T", [(128, 32, 8192), (64, 17, 16384), (128, 6, 50)])
