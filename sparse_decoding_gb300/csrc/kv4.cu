@@ -303,7 +303,9 @@ template <int D> __device__ __forceinline__ void append_cell(const Kv4 &c, const
     if (!cell_job(c, b, w / c.n_kv_heads, head == 0 && lane == 0, &j))
         return;
     const int page = kv4_page(c, j.s.row, (j.cell * kKv4Cell) >> c.page_shift);
-    if (page < 0) {
+    // A page that another sequence reads is not written: tokens fall there only when reserve did not make
+    // room for them.
+    if (page < 0 || c.refs[page] > 1) {
         if (lane == 0)
             kv4_bad(c);
         return;

@@ -299,6 +299,31 @@ def test_append_past_the_rope_table_and_again(nm):
     assert nm.device_status() == nm.NM_OK
 
 
+@pytest.mark.parametrize("D", [128, 64])
+def test_append_leaves_pages_that_are_shared(nm, D):
+    """A reserve that finds no page refuses; an append all the same would fall on the sequence's last tokens,
+    in a page that a fork reads. It is not written there, and the status tells."""
+    P = 16
+    c, K, V = make(nm, [32], P=P, Hk=2, D=D, extra=0, seed=141, max_seqs=3)
+    c.fork(ints([0, 0]), ints([1, 2]))
+    c.reserve(ints([0, 1]))
+    assert c.info.tolist()[:2] == [0, 2] and c.lens.tolist() == [32, 32, 32]
+    pool = c.pool.clone()
+    k = values(2, 2, D, 142)
+    c.append(1, k, k, seqs=ints([0, 1]))
+    assert nm.device_status() == nm.NM_ERR_BOUNDS and torch.equal(c.pool, pool)
+    c.append(1, values(5, 2, D, 143), values(5, 2, D, 144), seqs=ints([2]), starts=ints([0, 5]))
+    assert nm.device_status() == nm.NM_ERR_BOUNDS and torch.equal(c.pool, pool)
+    # with a page of its own a sequence is written as ever
+    c.free(ints([1, 2]))
+    c.append(1, k[:1], k[:1], seqs=ints([0]))
+    kk, vv = c.read(1, 1, seqs=ints([0]), f32=True)
+    rk, rv = ref.quantise(f32(k[:1]), f32(k[:1]))
+    assert nm.device_status() == nm.NM_OK
+    np.testing.assert_array_equal(f32(kk), rk)
+    np.testing.assert_array_equal(f32(vv), rv)
+
+
 # --- a second device ----------------------------------------------------------------------------
 
 def test_attention_on_a_second_device(nm):
