@@ -61,8 +61,9 @@ typedef enum nm_status {
     NM_ERR_CUDA = 6,        /* a CUDA runtime call or kernel launch failed */
     NM_ERR_TIMEOUT = 7,     /* a kernel's bounded wait ran out */
     NM_ERR_NOT_PD = 8,      /* nm_obs_prune: the damped Hessian is not positive definite */
-    NM_ERR_BOUNDS = 9       /* reported only by the bounds-checking build (NM_BOUNDS_CHECK): a
-                               kernel found an index outside its buffer and skipped the access */
+    NM_ERR_BOUNDS = 9       /* a kernel found an index outside its buffer and skipped the access: a
+                               table or list of the KV cache (nm_kv4_*), or, in the
+                               bounds-checking build (NM_BOUNDS_CHECK), any data-dependent index */
 } nm_status;
 
 /* Version of this ABI (bumped on any incompatible change). */
@@ -473,13 +474,22 @@ nm_status nm_obs_release_workspace(void);
  *   refs   [n_pages]: how many table entries name the page (0: free).
  *   tables [max_seqs][max_pages]: the pages of each sequence in order; -1 beyond.
  * Only full pages are shared between sequences, so an append never writes a
- * page that another sequence reads.
+ * page that another sequence reads. Lengths are changed by the calls only: one
+ * lowered by hand leaves pages behind that no call gives back, and where it ends
+ * in a shared page the next tokens have no place to go.
+ * A reserve that was refused leaves the lengths as they were. Appending all the
+ * same would put the new tokens over the sequence's last ones: look at info[1]
+ * first. Where those lie in a page of other sequences too, nothing is written and
+ * NM_ERR_BOUNDS is reported.
  *
  * Conventions, beside those at the top of this file:
  *   - seqs: device int32 [n_seqs], rows of `tables`; NULL: 0 .. n_seqs - 1.
  *   - starts: device int32 [n_seqs + 1], starts[0] = 0: the new tokens of the
  *     i-th listed sequence are rows starts[i] .. starts[i+1] - 1 of the token
- *     arrays; NULL: one token each (n_tokens = n_seqs).
+ *     arrays; NULL: one token each (n_tokens = n_seqs). Rows that belong to no
+ *     sequence (padding past starts[n_seqs]) are allowed: results are zero there,
+ *     lse -inf.
+ *   - seqs, starts and page lists need an int32's alignment only.
  *   - Token arrays are bf16 [n_tokens][heads][head_dim] with a token stride in
  *     elements (a multiple of 8, at least heads * head_dim), so that slices of a
  *     fused row can be passed. n_seqs is at most 1024; heads, pages and layers
@@ -489,8 +499,14 @@ nm_status nm_obs_release_workspace(void);
  *     lens - n_new + j.
  *   - The tables are checked on the device: an id, length, start or page out
  *     of range is not followed (a token at such a place is neither written nor
- *     attended, its row gives zeros) and nm_device_status reports NM_ERR_BOUNDS.
- *   - workspace: device memory of nm_kv4_workspace_bytes(), 256-byte aligned, its
+ *     attended, and reads as zeros; rows that starts out of range would have named
+ *     are rows of no sequence) and nm_device_status reports NM_ERR_BOUNDS.
+ *   - A token that room was made for but that was never appended in a layer holds
+ *     what its page held before. Queries of its sequence in that layer then have no
+ *     defined values, earlier ones of the same call included (what stands there may
+ *     be NaN, and 0 NaN is NaN).
+ *   - workspace: device memory of nm_kv4_workspace_bytes() (the parts of attention: 42.6
+ *     MB at head_dim 128, 21.6 MB at 64, and 8 bytes a page), 256-byte aligned, its
  *     first 8192 bytes zeroed once before its first use (nm_kv4_init does). Calls with the same
  *     workspace, or that change the same bookkeeping, must not overlap on the
  *     GPU; calls with caches of their own may.
@@ -574,7 +590,8 @@ nm_status nm_kv4_copy_pages(const nm_kv4_cache *src, const int32_t *src_pages, c
  *          (a cos - b sin, b cos + a sin), each operation rounded to fp32. k goes
  *          into the codes from fp32; q is rounded to bf16.
  * A position at or past rope_rows is reported as NM_ERR_BOUNDS; its token is not
- * written and its q_out row is zero.
+ * written (see above: attention over it is undefined until it is appended again
+ * with a longer table) and its q_out row is zero.
  */
 nm_status nm_kv4_append(const nm_kv4_cache *cache, int layer, const int32_t *seqs, const int32_t *starts, int n_seqs,
                         int64_t n_tokens, const void *k_bf16, int64_t k_stride, const void *v_bf16, int64_t v_stride,
@@ -602,9 +619,12 @@ nm_status nm_kv4_read(const nm_kv4_cache *cache, int layer, const int32_t *seqs,
  *   that belongs to no listed sequence.
  *   max_new: a bound on the new tokens of one sequence that the caller expects; it
  *   chooses the kernel, any value >= 1 gives the same results to rounding.
- * Scores are exact products with fp32 sums; the softmax statistics, its sums
- * and the output are held in fp32, the weights are rounded to fp16 for the
- * product with v. The order of the sums depends on the lengths and the device
+ * q is scaled by a power of two for each row and held in fp16: exact for what is at
+ * least 2^-17 of the row's largest; what is smaller is rounded to a multiple of
+ * 2^-24 of that power. Scores are exact products of it with the keys as held,
+ * summed in fp32; the softmax statistics, its sums and the output are held in
+ * fp32; for the product with v the weights and the values of v are each rounded to
+ * fp16 (2^-11). The order of the sums depends on the lengths and the device
  * alone: results repeat bit for bit.
  */
 nm_status nm_kv4_attention(const nm_kv4_cache *cache, int layer, const int32_t *seqs, const int32_t *starts,

@@ -444,7 +444,8 @@ class Kv4Cache:
     overlap on the GPU. ``seqs`` (int32, CUDA) names the sequences of a call, None: 0, 1, ...;
     ``starts`` (int32 [n + 1], CUDA) bounds each one's new tokens in the token tensors, None: one
     token each. Token tensors are bf16 [tokens][heads][head_dim] or [tokens][heads * head_dim];
-    the token stride is free.
+    the token stride is free. After an NM_ERR_TIMEOUT, go on with a new Kv4Cache over this one's
+    ``pool`` and ``book`` (its workspace starts clean).
     """
 
     def __init__(self, n_pages: int, page_tokens: int, n_layers: int, n_kv_heads: int, head_dim: int, max_seqs: int,
@@ -529,7 +530,8 @@ class Kv4Cache:
     def reserve(self, seqs: Optional[torch.Tensor] = None, starts: Optional[torch.Tensor] = None,
                 n: Optional[int] = None) -> None:
         """Room for the new tokens of each sequence (``n`` sequences with both None): lens grow, pages
-        are added. All or nothing; ``info[1]`` (on the device) tells."""
+        are added. All or nothing; ``info[1]`` (on the device) tells. After a refusal nothing may be
+        appended: the tokens would fall on the sequences' last ones."""
         p, st, m = self._batch(seqs, starts, n)
         _check(self._lib.nm_kv4_reserve(self._ref, p, st, m, self._s()), "nm_kv4_reserve")
 
@@ -604,7 +606,9 @@ class Kv4Cache:
                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse: bool = False):
         """Causal attention of the new tokens' q over the cache of one layer; bf16, shaped as q.
 
-        ``max_new``: the most new tokens a sequence has, where the caller knows (it chooses the kernel only).
+        ``max_new``: the most new tokens a sequence has, where the caller knows. It chooses the kernel only,
+        but without it (and with ``starts``) all tokens count as one sequence's: eight sequences of five
+        drafted tokens then take the kernel for prompts, which is slower for them.
         ``scale`` defaults to head_dim ** -0.5. lse=True: (out, lse), lse fp32 [tokens][heads]."""
         qp, qs, qh = self._tokens(q, "q")
         T = q.shape[0]

@@ -10,10 +10,11 @@
 // token at a time with the token's angles in registers.
 //
 // Bytes should bound it: k, v, q and q_out once, the angles once per SM and token.
-// Measured (one GB300; 16384 tokens, 32 and 8 heads, D = 128): append 86 us (362 MB,
-// 0.62 of the measured copy rate; 90000 instructions a scheduler, half of them the
-// quantisation, waiting for each cell's loads), read 22 us. A warp per token and head
-// with a division for each value took 138 us.
+// Measured (one GB300; 16384 tokens, 32 and 8 heads, D = 128): append 80 us (362 MB,
+// 0.67 of the measured copy rate; 101000 instructions a scheduler, half of them the
+// quantisation, waiting for each cell's loads), 86 while a warp asked for its q heads one
+// by one; read 22 us, of which its 86 MB take 13: it waits for one token's codes and
+// parameters at a time. A warp per token and head with a division for each value took 138 us.
 #include "kv4.cuh"
 
 namespace nm {

@@ -28,11 +28,13 @@
 // last of its CTAs, in CTA order, from the workspace.
 //
 // Measured (one GB300, D = 128): 131071 tokens, 64 query heads over 8: 43 us, 3.5 TB/s
-// (0.52 of the measured copy rate; the cache is read once): about 340 instructions a
-// cell, at 0.56 a cycle and scheduler, bound it with 8 us of start and joins; eight
-// sequences of 1 to 8191 tokens 19 us, four times five drafted tokens (25 rows) at
-// 9001 to 16385 tokens 48 us (254 registers leave two warps a scheduler), 20 rows of
-// four sequences of 12288 tokens 40 us, 129 tokens 8.9 us. Steps on the way for the
+// (0.52 of the measured copy rate; the cache is read once). What bounds it is a unit's
+// chain in its warp, scores, weights, values, with four warps a scheduler to hide it:
+// 345 instructions a cell issue at 0.56 a cycle and scheduler, and a warp waits most for
+// results of fixed latency, then for the tensor pipe (active 22%); 8 us are start and
+// joins. Eight sequences of 1 to 8191 tokens 19 us, four times five drafted tokens (25
+// rows) at 9001 to 16385 tokens 47 us (248 registers leave two warps a scheduler), 20
+// rows of four sequences of 12288 tokens 40 us, 129 tokens 8.9 us. Steps on the way for the
 // first: 67 us with loads straight to registers; 62 by bulk copies; 50.6 with masks at
 // the end only and addresses a round ahead; 43.9 two cells at a time and a join of
 // independent loads.
@@ -442,8 +444,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                     top = fmaxf(top, fabsf(x[e][n]));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            // 2^-e brings the row's largest magnitude into [1, 2): exact in fp16
-            // but for parts below 2^-24 of it
+            // 2^-e brings the row's largest magnitude into [1, 2): what is at least 2^-17 of it is
+            // exact in fp16 (eight bits above 2^-24), the rest is rounded to 2^-24
             uint32_t e2 = (__float_as_uint(top) >> 23) & 0xFFu;
             e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
             const float up = __uint_as_float(e2 << 23); // the sign of the scale goes with q
@@ -850,7 +852,8 @@ nm_status launch_rows(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, const 
 
 } // namespace
 
-// Two parts of a CTA: of two CTAs to an SM with 8 rows, or of one with up to 32.
+// Two parts of a CTA: of two CTAs to an SM with up to 16 rows, or of one with up to 32; here for 32 rows
+// and as many CTAs as the counters could serve, which is still less than the prompt kernel's parts.
 size_t kv4_partial_bytes(int head_dim)
 {
     const size_t rows = (size_t)kKv4Counters / 2 * 2 * 32 * (head_dim + 2) * 4;
@@ -866,32 +869,35 @@ nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
     // By the rows of a kv head. Measured, in us, with 8 kv heads (sequences x new tokens of 4 query
     // heads, tokens in the cache; k: 1024):
     //   D = 128                  NT = 1    2      3      4    prompt
-    //    8 rows (4 x 2, 12k)     23.2   31.6          46.0    70.3
-    //   12 rows (4 x 3, 12k)     35.5   32.9   39.6   45.7    70.3
-    //   16 rows (1 x 4, 32k)     27.0   30.4          37.3    77.2   (4 x 4, 12k: 35.5 33.2 39.6 45.7 69.8)
-    //   20 rows (4 x 5, 12k)     43.7   47.8   39.6   45.7    70.0   (1 x 5, 32k: 33.5 37.5 31.4 37.5 78.8)
-    //   32 rows (4 x 8, 12k)     55.5   48.0   58.0   46.0    69.8
-    //   48 rows (4 x 12, 12k)    74.4   60.1   58.0   70.3    70.3   (1 x 12, 32k: 53.9 47.8 45.7 54.4 87.7)
-    //   64 rows (4 x 16, 12k)    94.9   78.0   78.5   70.3    70.3   (1 x 16, 32k: 67.2 58.0 - 55.2 78.8)
-    //   96 rows (4 x 24, 8k)     95.9   78.8          71.1    58.0
-    //  128 rows (1 x 32, 32k)   119.7   95.1          84.9    77.5   (8 x 32, 512: 35.2 27.3 - 25.2 37.8)
-    //  256 rows (4 x 64, 8k)    233.4  177.0         154.3    60.8
+    //    8 rows (4 x 2, 12k)     23.5   31.6   39.8   45.5    68.5
+    //   12 rows (4 x 3, 12k)     35.2   31.4   39.8   45.7    68.3
+    //   16 rows (4 x 4, 12k)     35.2   31.6   39.8   45.7    68.5   (1 x 4, 32k: 27.3 29.3 31.4 35.5 66.2)
+    //   20 rows (4 x 5, 12k)     43.7   47.5   39.8   46.0    68.5   (1 x 5, 32k: 33.7 36.8 31.6 35.7 66.5)
+    //   32 rows (4 x 8, 12k)     55.5   47.8   58.3   46.0    68.5
+    //   48 rows (4 x 12, 12k)    74.4   60.1   58.3   66.7    68.5   (1 x 12, 32k: 53.9 47.3 46.8 53.9 65.7)
+    //   64 rows (4 x 16, 12k)    94.9   76.5   78.5   67.0    69.5   (1 x 16, 32k: 67.5 57.8 58.3 54.2 66.0)
+    //   96 rows (4 x 24, 8k)     95.9   76.7   72.6   68.3    56.2
+    //  128 rows (1 x 32, 32k)   119.7   93.3   96.9   80.6    63.4   (8 x 32, 512: 35.0 27.3 31.1 25.5 37.8)
+    //  256 rows (4 x 64, 8k)    232.9  174.0  168.9  144.0    58.3
     //   D = 64
-    //   16 rows (4 x 4, 12k)     25.3   23.2   29.9   33.4    53.9
-    //   20 rows (4 x 5, 12k)     29.4   33.4   30.9   33.4    53.9
-    //   32 rows (4 x 8, 12k)     37.6   33.4   43.7   33.4    53.9
-    //   48 rows (4 x 12, 12k)    50.1   39.6   43.2   47.8    53.9
-    //   64 rows (4 x 16, 8k)     47.3   37.5          37.5    43.7
-    //  128 rows (4 x 32, 8k)     80.5   63.1          58.0    40.9
+    //    8 rows (4 x 2, 12k)     18.9   23.2   31.1   34.0    56.2
+    //   16 rows (4 x 4, 12k)     26.5   23.2   31.1   33.7    56.2
+    //   20 rows (4 x 5, 12k)     30.4   33.4   31.4   34.7    56.2
+    //   32 rows (4 x 8, 12k)     39.3   33.7   43.7   34.7    56.2
+    //   48 rows (4 x 12, 12k)    51.4   39.8   43.7   49.8    56.0
+    //   64 rows (4 x 16, 8k)     47.8   39.3   43.7   39.6    45.7
+    //  128 rows (4 x 32, 8k)     82.4   64.2   70.8   60.3    41.6
     // Of all tokens' query heads together, the prompt kernel's 20 to 50 us of start, and join, against
     // tiles that read the cache again (one sequence, 32 heads, D = 128; tokens in the cache before):
-    //                               0     1000     8000     40000
-    //   24 new,  768    few      12.5     19.1     31.9      80.6
-    //                   prompt   20.9     31.4     46.8      73.1
-    //   32 new, 1024    few      12.7     23.2     35.5      99.0
-    //                   prompt   21.2     31.7     48.3      73.1
-    //   64 new, 2048    few      12.7     25.0     53.9     177
-    //                   prompt   27.6     37.3     52.6      76.5
+    //                               0     1000     8000    32000    40000
+    //   24 new,  768    few      12.4     19.1     31.4     66.2     76.4
+    //                   prompt   19.6     31.1     46.5     76.4     72.4
+    //   32 new, 1024    few      12.4     22.2     35.5     80.5     94.9
+    //                   prompt   21.2     31.4     47.8     73.6     68.5
+    //   64 new, 2048    few      12.5     23.2     51.9    135.8    164.8
+    //                   prompt   25.2     36.0     50.8     78.5     73.1
+    // The lengths are on the device, so the choice cannot go by them: up to 1024 rows short contexts
+    // gain up to a quarter, and from some 30000 tokens on the other kernel would.
     const int64_t rows = (max_new < 65 ? max_new : 65) * a.ratio;
     if (rows > 64 && b.n_tokens * at.n_q_heads > 1024)
         return kv4_launch_prompt(c, b, at, w, st);

@@ -31,14 +31,15 @@
 // CTAs to arrive of groups of its parts and then of the groups, in CTA order.
 //
 // Measured (one GB300; 32 query heads, 8 kv heads, D = 128): a prompt of 8192 tokens
-// 548 us, 1.0 PFLOP/s, 0.52 of a measured bf16 matrix product; the tensor cores are
-// active half the cycles, DRAM idles. What bounds it is a tile's own chain, S to
-// softmax to P to O (about 3700 cycles a block, of which 1088 are MMAs), with 16
-// unpacking and softmax warps sharing the issue slots (2340 of a block's 4400 cycles).
+// 507 us, 1.08 PFLOP/s, 0.57 of a measured bf16 matrix product; the tensor cores are
+// active 55% of the cycles, DRAM idles. What bounds it is a tile's own chain, S to
+// softmax to P to O (1088 cycles of it MMAs, where a block takes 4000), with 16
+// unpacking and softmax warps sharing the issue slots (2200 of those cycles).
 // Steps on the way: 1337 us with one pass per role; 884 the scores read once; 733 the
 // line weighted, Q ahead, registers split by role; 596 one site per step (the code
 // shrank from 202 to 118 KB: instruction fetches had stalled every role); 553 eight
-// unpacking warps. Tried and not kept: two threads to a row (564), S of half blocks in
+// unpacking warps; 507 fewer registers held across the softmax loop (168 bytes spilled, not 256).
+// Tried and not kept: two threads to a row (564), S of half blocks in
 // two buffers with the scores a step ahead (578: an MMA of N = 64 reads Q as often
 // for half the columns).
 //
