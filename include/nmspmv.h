@@ -615,6 +615,7 @@ nm_status nm_kv4_read(const nm_kv4_cache *cache, int layer, const int32_t *seqs,
  *   A query at position p attends positions 0 .. p of its sequence:
  *     out = sum_t e^(scale q.k_t) v_t / sum_t e^(scale q.k_t),
  *     lse = log sum_t e^(scale q.k_t).
+ *   scale: any finite number (NM_ERR_INVALID_ARG otherwise).
  *   A query with nothing to attend gives out 0 and lse -inf, and so does a row
  *   that belongs to no listed sequence.
  *   max_new: a bound on the new tokens of one sequence that the caller expects; it

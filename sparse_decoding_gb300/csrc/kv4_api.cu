@@ -1,5 +1,7 @@
 // kv4_api.cu -- the C entry points of the 4-bit paged KV cache (declared in
 // include/nmspmv.h): argument checks and dispatch.
+#include <cmath>
+
 #include "kv4.cuh"
 
 namespace nm {
@@ -310,7 +312,7 @@ nm_status nm_kv4_attention(const nm_kv4_cache *cache, int layer, const int32_t *
         return NM_ERR_SHAPE;
     if (n_q_heads / cache->n_kv_heads > 64)
         return NM_ERR_UNSUPPORTED;
-    if (max_new < 1)
+    if (max_new < 1 || !std::isfinite(scale))
         return NM_ERR_INVALID_ARG;
     if (n_tokens * n_q_heads > 0x3FFFFFFF)
         return NM_ERR_SHAPE;
