@@ -243,8 +243,8 @@ nm_status kv4_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
 
 nm_status kv4_launch_reserve(const Kv4 &c, const int32_t *seqs, const int32_t *starts, int n, const Kv4Work &w,
                              cudaStream_t st);
-nm_status kv4_launch_fork(const Kv4 &c, const int32_t *src, const int32_t *dst, int n, const Kv4Work &w, int num_sms,
-                          cudaStream_t st);
+nm_status kv4_launch_fork(const Kv4 &c, const int32_t *src, const int32_t *dst, int n, const Kv4Work &w, int cell_bytes,
+                          int num_sms, cudaStream_t st);
 nm_status kv4_launch_free(const Kv4 &c, const int32_t *seqs, int n, cudaStream_t st);
 nm_status kv4_launch_compact(const Kv4 &c, const Kv4Work &w, int num_sms, cudaStream_t st);
 nm_status kv4_launch_copy(const uint8_t *src, int64_t src_pages_n, const int32_t *src_pages, uint8_t *dst,

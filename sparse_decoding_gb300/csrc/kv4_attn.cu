@@ -41,6 +41,7 @@
 #include <type_traits>
 
 #include "kv4.cuh"
+#include "kv_ops.cuh"
 
 namespace nm {
 namespace {
@@ -59,40 +60,12 @@ constexpr float kNone = 1e38f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                 "{%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b)
 {
     asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(b));
 }
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
-{
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *(__half2 *)&x; }
-__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *(uint32_t *)&x; }
-
 // Nibble N (0..3) of both halves of w, minus `bias`, as two fp16 numbers: the
 // bits under an exponent of 2^10 are 1024 + n (or 1024 + 16 n), so the result is
 // exact.
@@ -173,15 +146,6 @@ template <int D> __device__ __forceinline__ void lds_v(CellV<D> &r, const uint8_
     }
 }
 
-// A copy of n bytes (a multiple of 16, 16-byte aligned ends) to shared memory,
-// counted on an mbarrier.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t n, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(n), "r"(bar)
-                 : "memory");
-}
-
 struct AttnArgs {
     int layer, ratio; // ratio: query heads of one kv head
     int n_q_heads;
@@ -225,13 +189,6 @@ template <int D, int NT> struct Smem {
 // Pieces of a segment that is cut every `chunk` units.
 __device__ __forceinline__ int pieces_of(int units, int chunk) { return (int)((uint32_t)(units + chunk - 1) / (uint32_t)chunk); }
 __device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + kTokens - 1) / kTokens : 1; }
-// a / b of numbers that fit 32 bits as a rule (a 64-bit division takes ten times as long).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
-{
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return quotient(a + b - 1, b); }
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
     attn_rows_kernel(const Kv4 c, const Kv4Batch b, const AttnArgs a)

@@ -418,11 +418,11 @@ nm_status kv4_launch_reserve(const Kv4 &c, const int32_t *seqs, const int32_t *s
     return done();
 }
 
-nm_status kv4_launch_fork(const Kv4 &c, const int32_t *src, const int32_t *dst, int n, const Kv4Work &w, int num_sms,
-                          cudaStream_t st)
+nm_status kv4_launch_fork(const Kv4 &c, const int32_t *src, const int32_t *dst, int n, const Kv4Work &w, int cell_bytes,
+                          int num_sms, cudaStream_t st)
 {
     fork_kernel<<<1, kT, 0, st>>>(c, src, dst, n, w.list);
-    fork_copy_kernel<<<num_sms * 8, 256, 0, st>>>(c, w.list, 16 * c.head_dim + c.head_dim * 2);
+    fork_copy_kernel<<<num_sms * 8, 256, 0, st>>>(c, w.list, cell_bytes);
     return done();
 }
 
