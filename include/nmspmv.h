@@ -62,7 +62,7 @@ typedef enum nm_status {
     NM_ERR_TIMEOUT = 7,     /* a kernel's bounded wait ran out */
     NM_ERR_NOT_PD = 8,      /* nm_obs_prune: the damped Hessian is not positive definite */
     NM_ERR_BOUNDS = 9       /* a kernel found an index outside its buffer and skipped the access: a
-                               table or list of the KV cache (nm_kv4_*), or, in the
+                               table or list of a KV cache (nm_kv4_*, nm_kv8_*), or, in the
                                bounds-checking build (NM_BOUNDS_CHECK), any data-dependent index */
 } nm_status;
 
@@ -631,6 +631,116 @@ nm_status nm_kv4_read(const nm_kv4_cache *cache, int layer, const int32_t *seqs,
 nm_status nm_kv4_attention(const nm_kv4_cache *cache, int layer, const int32_t *seqs, const int32_t *starts,
                            int n_seqs, int64_t n_tokens, int64_t max_new, const void *q_bf16, int64_t q_stride,
                            int n_q_heads, float scale, void *out_bf16, int64_t out_stride, float *lse, void *stream);
+
+/*
+ * ---- A paged KV cache in 8 bits, and attention over selected pages of it ----
+ *
+ * For models whose attention does not stand 4 bits, and for contexts that are too long to read
+ * in full at every step: the cache above with 8-bit codes, a scale for each block of 16 tokens and kv
+ * head, and bounds of each full page's keys, by which the pages that matter to a query are found.
+ *
+ * Values: a block is 16 tokens (positions 16 i .. 16 i + 15 of a sequence) of one kv head. K and V of
+ * it have a scale each, a power of two:
+ *     s = 2^e, e the least number with max |x| <= 448 2^e, at least -24 and at most 7
+ *     c = x / s as an 8-bit float (e4m3: 4 exponent and 3 mantissa bits), nearest, ties to even
+ *     the value it stands for: s c
+ * so a value is off by at most 2^-4 of itself, or by 2^-10 s where it is below 2^-6 s. The maximum is over the
+ * block's tokens. A token that needs a larger scale than the block has moves the
+ * codes held there to it: they are rounded again, which changes only those that fall below 2^-6
+ * of the new scale. A scale never shrinks, until its block's first position is written again. So
+ * what is held depends on how a block's tokens were divided into calls, by such roundings alone.
+ * Finite |x| above 32768 saturates. When k or v of a token holds a NaN or an infinity in one kv head, that
+ * head's K of the token becomes NaN (so every query that attends it gives NaN), its V is held as
+ * zeros, and neither counts for the scales and bounds.
+ *
+ * Bounds of a full page, per kv head, over the keys as held (NaN ones left out, 0 where there are no others):
+ *     w = 2^b, b the least number with max |k| <= 127 2^b, at least -30
+ *     upper[d] = ceil(max_t k_td / w), lower[d] = floor(min_t k_td / w)    (whole numbers, exact)
+ * nm_kv8_append writes them when it fills a page.
+ *
+ * Layout: the pool is [n_pages] pages; a page is [n_layers][n_kv_heads] shares of page_tokens / 16
+ * cells of 32 D + 16 bytes (D = head_dim) and the bounds, 2 D + 16 bytes:
+ *     K codes [2 halves][D / 64][8 tokens][64 channels]
+ *     V codes [D / 4 channels' fours][4 t][4 channels][tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9]
+ *     fp32 scale of K, of V, eight bytes unused
+ *     bounds: int8 upper [D], int8 lower [D], fp32 w, twelve bytes unused
+ *
+ * Bookkeeping, conventions and workspace are those of the 4-bit cache (nm_kv4_cache, with page and
+ * workspace bytes from the two calls below): the tables are kept by the same rules. Beside them:
+ *   - A fork copies the cells of the partial last page; full pages are shared with their bounds.
+ *   - A sequence listed twice in one nm_kv8_append gets no defined values there.
+ */
+typedef nm_kv4_cache nm_kv8_cache;
+
+int64_t nm_kv8_page_bytes(int page_tokens, int n_layers, int n_kv_heads, int head_dim);
+int64_t nm_kv8_workspace_bytes(int64_t n_pages, int head_dim);
+
+/* As the calls nm_kv4_* of these names. */
+nm_status nm_kv8_init(const nm_kv8_cache *cache, void *stream);
+nm_status nm_kv8_reserve(const nm_kv8_cache *cache, const int32_t *seqs, const int32_t *starts, int n_seqs,
+                         void *stream);
+nm_status nm_kv8_fork(const nm_kv8_cache *cache, const int32_t *src, const int32_t *dst, int n, void *stream);
+nm_status nm_kv8_free(const nm_kv8_cache *cache, const int32_t *seqs, int n, void *stream);
+nm_status nm_kv8_compact(const nm_kv8_cache *cache, void *stream);
+nm_status nm_kv8_copy_pages(const nm_kv8_cache *src, const int32_t *src_pages, const nm_kv8_cache *dst,
+                            const int32_t *dst_pages, int64_t n, void *stream);
+
+/*
+ * nm_kv8_append -- writes the new tokens' k and v to the cache of one layer, rotating k, and rotates
+ * q. Arguments, the rotation and what is reported are nm_kv4_append's; k goes into the codes from fp32.
+ */
+nm_status nm_kv8_append(const nm_kv8_cache *cache, int layer, const int32_t *seqs, const int32_t *starts, int n_seqs,
+                        int64_t n_tokens, const void *k_bf16, int64_t k_stride, const void *v_bf16, int64_t v_stride,
+                        const void *q_bf16, int64_t q_stride, int n_q_heads, void *q_out_bf16, int64_t q_out_stride,
+                        const float *rope, int64_t rope_rows, void *stream);
+
+/* nm_kv8_read -- the values held, as nm_kv4_read returns them (bf16 holds them exactly). */
+nm_status nm_kv8_read(const nm_kv8_cache *cache, int layer, const int32_t *seqs, const int32_t *starts, int n_seqs,
+                      int64_t n_tokens, void *k, void *v, int f32, void *stream);
+
+/*
+ * nm_kv8_attention -- attention of the new tokens over the cache of one layer, all of it or listed
+ * pages. Arguments, formulas and results are nm_kv4_attention's, beside:
+ *   pages: NULL, or device int32 [n_tokens][n_kv_heads][n_list]: for each new token and kv head the
+ *          pages of its sequence that its query heads attend, as indices into the sequence's table
+ *          row, ascending, -1 behind the last. Positions past the query's own are not attended, whatever is listed.
+ *          An entry that is out of range of the sequence, or does not ascend, is passed over and
+ *          reported (NM_ERR_BOUNDS). A query with nothing listed gives out 0 and lse -inf.
+ *   n_list: 1 .. 49152 (with pages; NM_ERR_UNSUPPORTED above). max_new is not used then.
+ * q is scaled by a power of two for each row and held in fp16, as there. Scores are exact products of it with
+ * the keys as held, summed in fp32; weights are rounded to fp16 (2^-11) for the product with V, whose codes
+ * are exact; statistics, sums and the output are held in fp32. Results repeat bit for bit.
+ */
+nm_status nm_kv8_attention(const nm_kv8_cache *cache, int layer, const int32_t *seqs, const int32_t *starts,
+                           int n_seqs, int64_t n_tokens, int64_t max_new, const void *q_bf16, int64_t q_stride,
+                           int n_q_heads, float scale, const int32_t *pages, int n_list, void *out_bf16,
+                           int64_t out_stride, float *lse, void *stream);
+
+/*
+ * nm_kv8_select -- the pages that nm_kv8_attention is to read: for each new token and kv head the
+ * n_list pages (of those up to its own position's) that can hold its largest scores.
+ *   q     : bf16 [n_tokens][n_q_heads][head_dim] (read), as nm_kv8_attention will get it.
+ *   pages : device int32 [n_tokens][n_kv_heads][n_list] (written): ascending, -1 behind; all -1 for
+ *           rows that belong to no listed sequence and tokens at no position.
+ *   first, last: so many of the sequence's first pages and of the last up to the query's own are
+ *           always taken; first >= 0, last >= 1, first + last <= n_list (NM_ERR_INVALID_ARG).
+ * When there are more than n_list pages, the others go by their scores, largest first, equal ones
+ * lowest page first:
+ *     p_d = sum_h max(q_hd, 0), m_d = sum_h min(q_hd, 0)  over the query heads h of the kv head, in
+ *           order, in fp32 (what is not finite counts as 0, magnitudes above 2^100 as that)
+ *     a_d = rint(p_d 2^-u), c_d = rint(m_d 2^-u), u the least number with max(p, -m) <= 127 2^u,
+ *           at least -100
+ *     score = w sum_d (a_d upper_d + c_d lower_d)
+ * 2^u score is, up to the rounding of a and c, a bound of the sum over the heads of their largest q.k in
+ * the page. The sum is a whole number below 2^23 and w a power of two: the score is exact, and so the lists
+ * are the same however they are computed. The softmax scale is taken as positive.
+ * A table entry that names no page is taken last and reported. max_pages of the cache: at most 49152
+ * (NM_ERR_UNSUPPORTED). Bounds of a page that was never filled through nm_kv8_append are undefined,
+ * and so is the choice then.
+ */
+nm_status nm_kv8_select(const nm_kv8_cache *cache, int layer, const int32_t *seqs, const int32_t *starts, int n_seqs,
+                        int64_t n_tokens, const void *q_bf16, int64_t q_stride, int n_q_heads, int n_list, int first,
+                        int last, int32_t *pages, void *stream);
 
 #ifdef __cplusplus
 }

@@ -46,7 +46,10 @@ EXPORTS = ("nm_abi_version", "nm_status_str", "nm_pack_host", "nm_select", "nm_p
            "nm_spmv_f32out_atomic", "nm_select_pack", "nm_spmv_qkv", "nm_obs_release_workspace",
            "nm_kv4_page_bytes", "nm_kv4_workspace_bytes", "nm_kv4_init", "nm_kv4_reserve", "nm_kv4_fork",
            "nm_kv4_free", "nm_kv4_compact", "nm_kv4_copy_pages", "nm_kv4_append", "nm_kv4_read",
-           "nm_kv4_attention")
+           "nm_kv4_attention",
+           "nm_kv8_page_bytes", "nm_kv8_workspace_bytes", "nm_kv8_init", "nm_kv8_reserve", "nm_kv8_fork",
+           "nm_kv8_free", "nm_kv8_compact", "nm_kv8_copy_pages", "nm_kv8_append", "nm_kv8_read",
+           "nm_kv8_attention", "nm_kv8_select")
 
 
 class NmError(RuntimeError):
@@ -122,6 +125,10 @@ def lib() -> ctypes.CDLL:
         "nm_kv4_read": ([p, i32, p, p, i32, i64, p, p, i32, p], i32),
         "nm_kv4_attention": ([p, i32, p, p, i32, i64, i64, p, i64, i32, ctypes.c_float, p, i64, p, p], i32),
     }
+    for call in ("page_bytes", "workspace_bytes", "init", "reserve", "fork", "free", "compact", "copy_pages", "append", "read"):
+        sig["nm_kv8_" + call] = sig["nm_kv4_" + call]
+    sig["nm_kv8_attention"] = ([p, i32, p, p, i32, i64, i64, p, i64, i32, ctypes.c_float, p, i32, p, i64, p, p], i32)
+    sig["nm_kv8_select"] = ([p, i32, p, p, i32, i64, p, i64, i32, i32, i32, i32, p, p], i32)
     for name, (args, res) in sig.items():
         f = getattr(L, name)
         f.argtypes = args
@@ -427,7 +434,7 @@ def obs_release_workspace():
     _check(lib().nm_obs_release_workspace(), "nm_obs_release_workspace")
 
 
-# --- the 4-bit paged KV cache ---------------------------------------------------------
+# --- the paged KV caches --------------------------------------------------------------
 
 def _pad4(n: int) -> int:
     return (n + 3) // 4 * 4
@@ -448,19 +455,23 @@ class Kv4Cache:
     ``pool`` and ``book`` (its workspace starts clean).
     """
 
+    _calls = "nm_kv4_"  # the C calls of the format
+
     def __init__(self, n_pages: int, page_tokens: int, n_layers: int, n_kv_heads: int, head_dim: int, max_seqs: int,
                  max_pages: int, device: Optional[torch.device] = None, pool: Optional[torch.Tensor] = None,
                  book: Optional[torch.Tensor] = None):
         L = lib()
-        per = L.nm_kv4_page_bytes(page_tokens, n_layers, n_kv_heads, head_dim)
+        per = getattr(L, self._calls + "page_bytes")(page_tokens, n_layers, n_kv_heads, head_dim)
         if per == 0 or n_pages < 0 or max_seqs < 0 or max_pages < 0:
-            raise NmError(NM_ERR_UNSUPPORTED, "Kv4Cache")
+            raise NmError(NM_ERR_UNSUPPORTED, type(self).__name__)
         given = pool if pool is not None else book
         device = given.device if given is not None else torch.device(device if device is not None else "cuda")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
         self.device, self.n_pages, self.page_tokens = device, n_pages, page_tokens
-        self._index, self._lib = device.index, L
+        self._index = device.index
+        self._f = {x: getattr(L, self._calls + x) for x in ("init", "reserve", "fork", "free", "compact", "copy_pages", "append",
+                                                            "read", "attention")}
         self.n_layers, self.n_kv_heads, self.head_dim = n_layers, n_kv_heads, head_dim
         ints = self.book_ints(n_pages, max_seqs, max_pages)
         fresh = book is None
@@ -475,7 +486,7 @@ class Kv4Cache:
         b = a + _pad4(n_pages)
         self.info, self.lens, self.refs = self.book[:16], self.book[16:16 + max_seqs], self.book[a:a + n_pages]
         self.tables = self.book[b:b + max_seqs * max_pages].view(max_seqs, max_pages)
-        self._work = torch.empty(L.nm_kv4_workspace_bytes(n_pages, head_dim), dtype=torch.uint8, device=device)
+        self._work = torch.empty(getattr(L, self._calls + "workspace_bytes")(n_pages, head_dim), dtype=torch.uint8, device=device)
         self._work[:8192].zero_()  # the join counters
         base = self.book.data_ptr()
         self._c = NmKv4Cache(self.pool.data_ptr(), n_pages, page_tokens, n_layers, n_kv_heads, head_dim, max_seqs,
@@ -483,12 +494,16 @@ class Kv4Cache:
                              self._work.numel())
         self._ref = ctypes.byref(self._c)
         if fresh:
-            _check(L.nm_kv4_init(self._ref, self._s()), "nm_kv4_init")
+            self._ok(self._f["init"](self._ref, self._s()), "init")
 
     @staticmethod
     def book_ints(n_pages: int, max_seqs: int, max_pages: int) -> int:
         """Ints of ``book``: info, lens, refs and tables, each padded to a multiple of four."""
         return 16 + _pad4(max_seqs) + _pad4(n_pages) + _pad4(max_seqs * max_pages)
+
+    def _ok(self, status: int, call: str):
+        if status != NM_OK:
+            raise NmError(status, self._calls + call)
 
     def _s(self) -> int:
         if torch.cuda.current_device() != self._index:
@@ -533,31 +548,29 @@ class Kv4Cache:
         are added. All or nothing; ``info[1]`` (on the device) tells. After a refusal nothing may be
         appended: the tokens would fall on the sequences' last ones."""
         p, st, m = self._batch(seqs, starts, n)
-        _check(self._lib.nm_kv4_reserve(self._ref, p, st, m, self._s()), "nm_kv4_reserve")
+        self._ok(self._f["reserve"](self._ref, p, st, m, self._s()), "reserve")
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor) -> None:
         """The empty sequences dst become copies of src, sharing its full pages. ``info[1]`` tells."""
         if src.numel() != dst.numel():
             raise ValueError("src and dst must have the same length")
-        _check(self._lib.nm_kv4_fork(self._ref, self._ids(src, "src"), self._ids(dst, "dst"), src.numel(), self._s()),
-               "nm_kv4_fork")
+        self._ok(self._f["fork"](self._ref, self._ids(src, "src"), self._ids(dst, "dst"), src.numel(), self._s()), "fork")
 
     def free(self, seqs: torch.Tensor) -> None:
         """Empties the listed sequences."""
-        _check(self._lib.nm_kv4_free(self._ref, self._ids(seqs, "seqs"), seqs.numel(), self._s()), "nm_kv4_free")
+        self._ok(self._f["free"](self._ref, self._ids(seqs, "seqs"), seqs.numel(), self._s()), "free")
 
     def compact(self) -> None:
         """Moves the pages in use to the front of the pool; the tables follow."""
-        _check(self._lib.nm_kv4_compact(self._ref, self._s()), "nm_kv4_compact")
+        self._ok(self._f["compact"](self._ref, self._s()), "compact")
 
     def copy_pages(self, src_pages: torch.Tensor, dst_pages: torch.Tensor, dst: Optional["Kv4Cache"] = None) -> None:
         """Copies whole pages of this pool to pages of ``dst``'s (default: this one)."""
         dst = self if dst is None else dst
-        if src_pages.numel() != dst_pages.numel() or dst.device != self.device:
-            raise ValueError("page lists must have the same length, and the caches one device")
-        _check(self._lib.nm_kv4_copy_pages(self._ref, self._ids(src_pages, "src_pages"), dst._ref,
-                                       self._ids(dst_pages, "dst_pages"), src_pages.numel(), self._s()),
-               "nm_kv4_copy_pages")
+        if src_pages.numel() != dst_pages.numel() or dst.device != self.device or dst._calls != self._calls:
+            raise ValueError("page lists must have the same length, and the caches one device and format")
+        self._ok(self._f["copy_pages"](self._ref, self._ids(src_pages, "src_pages"), dst._ref,
+                                       self._ids(dst_pages, "dst_pages"), src_pages.numel(), self._s()), "copy_pages")
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, q: Optional[torch.Tensor] = None,
                rope: Optional[torch.Tensor] = None, seqs: Optional[torch.Tensor] = None,
@@ -585,8 +598,8 @@ class Kv4Cache:
                 raise ValueError(f"rope must be [positions][{self.head_dim}] on {self.device}")
             rp, rows = rope.data_ptr(), rope.shape[0]
         sp, st, n = self._batch(seqs, starts, T if starts is None else None)
-        _check(self._lib.nm_kv4_append(self._ref, layer, sp, st, n, T, kp, ks, vp, vs, qp, qs, qh, op, os_, rp, rows,
-                                   self._s()), "nm_kv4_append")
+        self._ok(self._f["append"](self._ref, layer, sp, st, n, T, kp, ks, vp, vs, qp, qs, qh, op, os_, rp, rows,
+                                   self._s()), "append")
         return q_out if q is not None else None
 
     def read(self, layer: int, n_tokens: int, seqs: Optional[torch.Tensor] = None,
@@ -597,8 +610,8 @@ class Kv4Cache:
         shape = (n_tokens, self.n_kv_heads, self.head_dim)
         dt = torch.float32 if f32 else torch.bfloat16
         k, v = torch.empty(shape, dtype=dt, device=self.device), torch.empty(shape, dtype=dt, device=self.device)
-        _check(self._lib.nm_kv4_read(self._ref, layer, sp, st, n, n_tokens, k.data_ptr(), v.data_ptr(), int(f32),
-                                 self._s()), "nm_kv4_read")
+        self._ok(self._f["read"](self._ref, layer, sp, st, n, n_tokens, k.data_ptr(), v.data_ptr(), int(f32),
+                                 self._s()), "read")
         return k, v
 
     def attention(self, layer: int, q: torch.Tensor, seqs: Optional[torch.Tensor] = None,
@@ -610,6 +623,9 @@ class Kv4Cache:
         but without it (and with ``starts``) all tokens count as one sequence's: eight sequences of five
         drafted tokens then take the kernel for prompts, which is slower for them.
         ``scale`` defaults to head_dim ** -0.5. lse=True: (out, lse), lse fp32 [tokens][heads]."""
+        return self._attend(layer, q, seqs, starts, max_new, scale, out, lse)
+
+    def _attend(self, layer, q, seqs, starts, max_new, scale, out, lse, *listed):
         qp, qs, qh = self._tokens(q, "q")
         T = q.shape[0]
         if out is None:
@@ -621,8 +637,51 @@ class Kv4Cache:
                 raise ValueError("out must have q's tokens and heads")
         sp, st, n = self._batch(seqs, starts, T if starts is None else None)
         ls = q.new_empty((T, qh), dtype=torch.float32) if lse else None
-        status = self._lib.nm_kv4_attention(self._ref, layer, sp, st, n, T, (T or 1) if max_new is None else max_new, qp, qs, qh,
-                                            self.head_dim ** -0.5 if scale is None else scale, op, os_,
-                                            ls.data_ptr() if lse else None, self._s())
-        _check(status, "nm_kv4_attention")
+        status = self._f["attention"](self._ref, layer, sp, st, n, T, (T or 1) if max_new is None else max_new, qp, qs, qh,
+                                      self.head_dim ** -0.5 if scale is None else scale, *listed, op, os_,
+                                      ls.data_ptr() if lse else None, self._s())
+        self._ok(status, "attention")
         return (out, ls) if lse else out
+
+
+class Kv8Cache(Kv4Cache):
+    """A paged KV cache in 8 bits (``nm_kv8_*``), used as a ``Kv4Cache``: 8-bit floats with a power of two for
+    each 16 tokens and kv head (see include/nmspmv.h).
+
+    A full page holds bounds of its keys, from which ``select`` finds the pages that matter to each new
+    token; ``attention`` reads the whole cache or the pages listed for each token."""
+
+    _calls = "nm_kv8_"
+
+    def attention(self, layer: int, q: torch.Tensor, seqs: Optional[torch.Tensor] = None,
+                  starts: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
+                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse: bool = False,
+                  pages: Optional[torch.Tensor] = None):
+        """Causal attention of the new tokens' q over the cache of one layer; bf16, shaped as q.
+
+        ``pages`` (int32 [tokens][n_kv_heads][n], from ``select`` or of the caller's own): the pages of its
+        sequence that each token attends, ascending, -1 behind; None: all. The rest as ``Kv4Cache.attention``."""
+        if pages is None:
+            return self._attend(layer, q, seqs, starts, max_new, scale, out, lse, None, 0)
+        _cuda(pages, torch.int32, "pages")
+        if pages.device != self.device or pages.dim() != 3 or pages.shape[:2] != (q.shape[0], self.n_kv_heads) or \
+                pages.shape[2] < 1:
+            raise ValueError(f"pages must be [tokens][{self.n_kv_heads}][n], n >= 1, on {self.device}")
+        return self._attend(layer, q, seqs, starts, max_new, scale, out, lse, pages.data_ptr(), pages.shape[2])
+
+    def select(self, layer: int, q: torch.Tensor, n: int, seqs: Optional[torch.Tensor] = None,
+               starts: Optional[torch.Tensor] = None, first: int = 1, last: int = 1,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The n pages of each new token and kv head (int32 [tokens][n_kv_heads][n], ascending, -1 behind) whose
+        keys can have the largest scores with its query heads; the ``first`` pages of the sequence and the
+        ``last`` up to the token's own are always among them."""
+        qp, qs, qh = self._tokens(q, "q")
+        shape = (q.shape[0], self.n_kv_heads, n)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.int32, device=self.device)
+        elif tuple(_cuda(out, torch.int32, "out").shape) != shape or out.device != self.device:
+            raise ValueError(f"out must be {list(shape)} on {self.device}")
+        sp, st, m = self._batch(seqs, starts, shape[0] if starts is None else None)
+        self._ok(lib().nm_kv8_select(self._ref, layer, sp, st, m, shape[0], qp, qs, qh, n, first, last, out.data_ptr(), self._s()),
+                 "select")
+        return out

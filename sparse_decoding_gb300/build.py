@@ -23,7 +23,8 @@ BUILD_CHECK = os.path.join(HERE, "_build_check")
 LIB_CHECK = os.path.join(HERE, "libnmspmv_check.so")
 
 SOURCES = ["api.cu", "spmv.cu", "gemv.cu", "pack.cu", "noalloc.cu", "obs.cu", "tc_gemm.cu", "kv4_api.cu",
-           "kv4.cu", "kv4_attn.cu", "kv4_prompt.cu", "kv4_pages.cu", "pack_host.cpp"]
+           "kv4.cu", "kv4_attn.cu", "kv4_prompt.cu", "kv4_pages.cu", "kv8_api.cu", "kv8.cu", "kv8_attn.cu",
+           "kv8_prompt.cu", "kv8_select.cu", "pack_host.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

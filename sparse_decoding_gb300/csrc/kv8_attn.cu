@@ -1,0 +1,735 @@
+// kv8_attn.cu -- attention of few queries over the 8-bit paged cache (decode steps and
+// drafted tokens), and of any queries over the pages that were selected for each.
+//
+// For one sequence and kv head, the rows are its queries times the query heads that share the kv
+// head (with lists of pages: one query's); a tile holds 8 NT of them. A warp takes the cache a
+// cell (16 tokens) at a time:
+//
+//   S^T [16 tokens][rows] = codes(K) Q^T      m16n8k16, the codes and q as fp16
+//   s = scale_K S^T                           fp32
+//   p = 2^(s + e - m + 6)                     2^e: V's scale; m: the row's running maximum of s + e
+//   O^T [channels][rows] += codes(V)^T P^T    m16n8k16, P as fp16
+//   l += 2^-e p
+//
+// The codes are exact in fp16, q is made so by a power of two per row, so scores carry fp32
+// rounding only. V's scale is a power of two too: as an exponent of the weights it costs an addition,
+// V's codes are exact operands, and only the weights are rounded (2^-11). m is raised only when a
+// score passes it by 2^8: the warp votes instead of reducing.
+//
+// The layout of a cell is the operands' own: lane l reads 16 bytes at 16 l, so K and V need no
+// transposition on the way to the registers, and an instruction makes two codes fp16.
+//
+// A (sequence, kv head, tile) is a segment. Each CTA gets one piece of one where that can be
+// balanced, else an even part of the line of all segments. A CTA's warps take the cells of a piece
+// in turn and are joined in shared memory. A segment that was cut is joined by the last of its
+// CTAs, in CTA order, from the workspace.
+#include "kv8.cuh"
+#include "kv_ops.cuh"
+
+namespace nm {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int64_t kMinShare = 8;  // cells of a CTA at least: one for each warp
+constexpr int kWhole = 32;        // when none has more cells than this, no segment is cut
+constexpr float kMoreUnits = 24.0f; // a second piece costs about as many cells
+constexpr int kOver = 16;         // cells that starting and ending a piece costs as much as
+constexpr float kShift = 6.0f;    // p = 2^(s + e - m + kShift)
+constexpr float kSlack = 8.0f;    // a score may pass m by this much
+constexpr float kNone = 1e38f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnArgs {
+    int layer, ratio; // ratio: query heads of one kv head
+    int n_q_heads;
+    const uint16_t *q;
+    int64_t q_stride;
+    float scale;
+    uint16_t *out;
+    int64_t out_stride;
+    float *lse;
+    uint32_t *counters;
+    float *partials;
+    const int32_t *pages; // of a selection: [n_tokens][n_kv_heads][n_list]
+    int n_list;
+};
+
+// Floats of one part in the workspace: m and l of each row, then O.
+template <int D, int NT> constexpr int part_floats() { return 8 * NT * (D + 2); }
+
+// What the scores of a row need: its factor, and how many tokens it attends.
+struct RowInfo {
+    float scale;
+    int limit;
+};
+
+template <int D, int NT> struct Smem {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kPitch = D + 4;
+    static constexpr int kStage = Kv8Cell<D>::kBytes;
+    // cells of a warp in flight or in use: what two CTAs (up to 16 rows) or one leave room for
+    static constexpr int kStages = D == 128 ? (NT <= 2 ? 3 : 5) : (NT <= 2 ? 5 : 8);
+    static constexpr int kSteps = D / 16;
+    // the warps' rings; when a piece is done, the warps' parts (m, l, O) in their place
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kMerge = kWarps * kRows * (2 + kPitch) * 4;
+    static constexpr int kJoin = (kKv4Counters / 4 * kRows + 2 * kRows) * 4; // weights of the parts of a segment
+    static constexpr int kMost = kRing > kMerge ? (kRing > kJoin ? kRing : kJoin) : (kMerge > kJoin ? kMerge : kJoin);
+    static constexpr int kBig = (kMost + 127) / 128 * 128;
+    // Q in B fragments: [n-tile][k-step][lane][2], then the rows' RowInfo, the rings' barriers and the
+    // first tokens of their cells
+    static constexpr int kQ = kBig, kInfo = kQ + NT * kSteps * 256, kBars = kInfo + kRows * 8;
+    static constexpr int kFirst = kBars + kWarps * kStages * 8, kSeqs = kFirst + (kWarps * kStages * 4 + 15) / 16 * 16;
+};
+
+// The last i with pre[i] <= x, of n entries that do not fall; -1: none.
+__device__ __forceinline__ int find(const int64_t *pre, int n, int64_t x)
+{
+    int lo = -1, hi = n;
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (pre[m] <= x)
+            lo = m;
+        else
+            hi = m;
+    }
+    return lo;
+}
+
+// Pieces of a segment that is cut every `chunk` units.
+__device__ __forceinline__ int pieces_of(int units, int chunk) { return (int)((uint32_t)(units + chunk - 1) / (uint32_t)chunk); }
+__device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + kKv4Cell - 1) / kKv4Cell : 1; }
+
+template <int D, int NT, bool kListed>
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
+    kv8_rows_kernel(const Kv4 c, const Kv4Batch b, const AttnArgs a)
+{
+    constexpr int G = D / 64;
+    constexpr int RT = 8 * NT;
+    constexpr int KS = 4 * G; // k-steps of 16 channels
+    using SM = Smem<D, NT>;
+    constexpr int S = SM::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float *const sm_m = (float *)smem, *const sm_l = sm_m + kWarps * RT, *const sm_o = sm_l + kWarps * RT;
+    uint2 *const sm_q = (uint2 *)(smem + SM::kQ);
+    RowInfo *const sm_info = (RowInfo *)(smem + SM::kInfo);
+    int64_t *const pre = (int64_t *)(smem + SM::kSeqs);      // [n_seqs + 1]
+    Kv4Seq *const seqs = (Kv4Seq *)(pre + b.n_seqs + 1);     // [n_seqs]
+    __shared__ uint32_t s_last;
+    __shared__ int s_chunk;
+    __shared__ bool s_rest; // some rows belong to no sequence
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    uint8_t *const ring = smem + warp * S * SM::kStage;
+    int *const sm_first = (int *)(smem + SM::kFirst) + warp * S;
+    const uint32_t rings = smem_addr(ring), bars = smem_addr(smem + SM::kBars) + warp * S * 8;
+
+    // the segments of each sequence, and where they start on the line of units
+    if (lane == 0)
+        for (int i = 0; i < S; ++i)
+            mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+    int longest = 0;
+    for (int i = tid; i < b.n_seqs; i += kThreads) {
+        const Kv4Seq s = kv4_seq(c, b, i, blockIdx.x == 0);
+        seqs[i] = s;
+        if (kListed) {
+            pre[i] = b.starts ? b.starts[i] : i;
+            continue;
+        }
+        longest = max(longest, s.n_new == 0 ? 0 : units_of(s.len));
+        pre[i + 1] = (int64_t)((uint32_t)(s.n_new * a.ratio + RT - 1) / RT) * c.n_kv_heads; // segments
+    }
+    const bool is_long = __syncthreads_or(longest > kWhole);
+    // Lists: a token, kv head and tile is a segment, all of one length
+    const int list_tiles = (a.ratio + RT - 1) / RT, list_units = a.n_list << (c.page_shift - 4);
+    const int64_t list_segments = kListed ? b.n_tokens * c.n_kv_heads * list_tiles : 0;
+    if constexpr (kListed) {
+        if (tid == 0) {
+            int z = 0; // an even cut of the line, as below
+            if (list_units <= kWhole || list_segments >= 4 * (int64_t)gridDim.x)
+                z = 1 << 30;
+            else if (list_segments <= gridDim.x)
+                z = (int)ceil_div(ceil_div(list_units, gridDim.x / list_segments), kWarps) * kWarps;
+            s_chunk = z;
+            s_rest = false;
+        }
+    } else if (warp == 0) {
+        // How the segments are cut:
+        //   chunk > 0: into pieces of so many units (a multiple of the warps), each a step of the
+        //     line; the least chunk with which all pieces fit the CTAs of one wave,
+        //   chunk = 0: the line has a step for each unit and kOver more for each segment, and is cut
+        //     evenly. Taken when there are more segments than CTAs, or when one chunk for all lengths
+        //     is over an even cut by more than a second piece costs a CTA.
+        const auto total_of = [&](const auto &f) { // counts, each cut off far above the grid
+            uint32_t x = 0;
+            for (int i = lane; i < b.n_seqs; i += 32) {
+                const int64_t y = f(i);
+                x += y < 65536 ? (uint32_t)y : 65536u;
+            }
+            return __reduce_add_sync(~0u, x);
+        };
+        int chunk = 0;
+        if (!is_long) {
+            chunk = 1 << 30;
+        } else if (total_of([&](int i) { return pre[i + 1]; }) <= gridDim.x) {
+            float work = 0.0f;
+            for (int i = lane; i < b.n_seqs; i += 32)
+                work += (float)pre[i + 1] * (float)units_of(seqs[i].len);
+            for (int z = 16; z; z >>= 1)
+                work += __shfl_xor_sync(~0u, work, z);
+            const float even = work / (float)gridDim.x;
+            const int step = (int)(even / (8 * kWarps)) * kWarps + kWarps;
+            for (int z = (int)(even / kWarps) * kWarps + kWarps; (float)z <= even + kMoreUnits; z += step) {
+                if (total_of([&](int i) { return pre[i + 1] * pieces_of(units_of(seqs[i].len), z); }) <= gridDim.x) {
+                    chunk = z;
+                    break;
+                }
+            }
+        }
+        int64_t sum = 0;
+        bool rest = !kv4_ends(b);
+        for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
+            int64_t x = 0;
+            if (i0 + lane < b.n_seqs) {
+                rest |= seqs[i0 + lane].first < 0;
+                const int units = units_of(seqs[i0 + lane].len);
+                x = pre[i0 + lane + 1] * (chunk ? pieces_of(units, chunk) : kOver + units);
+            }
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            __syncwarp();
+            if (i0 + lane < b.n_seqs)
+                pre[i0 + lane + 1] = sum + x;
+            sum += __shfl_sync(~0u, x, 31);
+        }
+        rest = __any_sync(~0u, rest);
+        if (lane == 0) {
+            pre[0] = 0;
+            s_chunk = chunk;
+            s_rest = rest;
+        }
+    }
+    __syncthreads();
+    const int chunk = s_chunk;
+    const int list_per = chunk ? pieces_of(list_units, chunk) : kOver + list_units;
+    const int64_t total = kListed ? list_segments * list_per : pre[b.n_seqs];
+    int64_t share = ceil_div(total, gridDim.x);
+    if (!chunk && share < kMinShare + kOver)
+        share = kMinShare + kOver;
+    const int64_t lo = (int64_t)blockIdx.x * share, hi = lo + share < total ? lo + share : total;
+    const int shift = c.page_shift - 4;
+    uint32_t used = 0; // cells of this warp so far: the next takes stage used % S
+    bool dead = false;
+
+    for (int64_t pos = lo; pos < hi;) {
+        int most = 0; // (lists) tokens of the sequence
+        int i, units, per, head, row0;
+        int64_t seg_lo, list = 0;
+        Kv4Seq s{};
+        if (kListed) {
+            const int64_t seg = quotient(pos, list_per), token = quotient(seg, c.n_kv_heads * list_tiles);
+            const int rest = (int)(seg - token * c.n_kv_heads * list_tiles);
+            head = rest / list_tiles;
+            row0 = rest % list_tiles * RT;
+            units = list_units;
+            per = list_per;
+            seg_lo = seg * list_per;
+            list = (token * c.n_kv_heads + head) * a.n_list;
+            i = find(pre, b.n_seqs, token);
+            if (i >= 0)
+                s = seqs[i];
+            // the token's own position is the last that it sees; a row of no sequence sees nothing
+            const int64_t seen = i >= 0 && s.first >= 0 && token - s.first < s.n_new ? s.len - s.n_new + (token - s.first) + 1 : 0;
+            most = s.len;
+            s.len = seen > 0 && s.len > 0 ? (int)seen : 0;
+            s.first = (int)token;
+            s.n_new = 1;
+        } else {
+            i = find(pre, b.n_seqs, pos);
+            s = seqs[i];
+            units = units_of(s.len);
+            per = chunk ? pieces_of(units, chunk) : kOver + units; // steps of the segment
+            const int64_t seg = quotient(pos - pre[i], per);
+            seg_lo = pre[i] + seg * per;
+            const int tiles = (s.n_new * a.ratio + RT - 1) / RT;
+            head = (int)quotient(seg, tiles);
+            row0 = (int)(seg - (int64_t)head * tiles) * RT; // first row of the tile
+        }
+        const int over = chunk ? 0 : kOver;
+        const int64_t seg_hi = seg_lo + per;
+        int steps, c0, c1;
+        if (chunk) {
+            steps = 1;
+            c0 = (int)(pos - seg_lo) * (per > 1 ? chunk : 0);
+            c1 = per > 1 && units - c0 > chunk ? c0 + chunk : units;
+        } else {
+            steps = (int)((hi < seg_hi ? hi : seg_hi) - pos);
+            const int from = (int)(pos - seg_lo) - over;
+            c0 = from > 0 ? from : 0;
+            c1 = from + steps;
+            if (c1 <= c0)
+                break; // the CTA's part of the line ends before the segment's first unit
+        }
+        const int rows = s.n_new * a.ratio; // rows of the sequence and kv head
+        const int tile_first = s.len - s.n_new + row0 / a.ratio + 1; // tokens that its first row attends
+
+        // Q: warp j takes n-tile j: row g, channels 64 e + 16 t ..
+        uint4 qw[G][2];
+        const int qrow = row0 + 8 * warp + g;
+        const bool real = warp < NT && qrow < rows;
+        if (warp < NT) {
+            const uint16_t *q = a.q + (int64_t)(s.first + qrow / a.ratio) * a.q_stride +
+                                ((int64_t)head * a.ratio + qrow % a.ratio) * D + 16 * t;
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    qw[e][f] = real ? ldg_nc128(q + 64 * e + 8 * f) : make_uint4(0, 0, 0, 0);
+        }
+
+        // The warp's cells are c0 + warp, + kWarps, ... Lane n holds the address of every 32nd (0: its page
+        // is none of the pool's, or it is past the tokens that are seen) and the position it begins at;
+        // `have` has a bit for each stage that was filled.
+        int mine = !dead && s.len > 0 && c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
+        const uint8_t *const heads = c.pool + kv8_head_offset<D>(c, 0, a.layer, head);
+        uint64_t where = 0;
+        int begins = 0;
+        uint32_t have = 0;
+        const auto fetch = [&](int x) {
+            if ((x & 31) == 0) {
+                const int cell = c0 + warp + (x + lane) * kWarps;
+                where = 0;
+                if (x + lane < mine) {
+                    int index = cell >> shift;
+                    bool seen = true;
+                    if (kListed) { // ascending, -1 only behind; what is listed beyond the query is not seen
+                        const int32_t *const at = a.pages + list + index;
+                        const bool rises = index == 0 || (at[-1] >= 0 && at[-1] < at[0]);
+                        index = at[0];
+                        seen = index >= 0 && rises && (int64_t)index << c.page_shift < most;
+                        if (!seen && index != -1)
+                            kv4_bad(c);
+                    }
+                    begins = seen ? (index << c.page_shift) + ((cell & ((1 << shift) - 1)) << 4) : 0;
+                    if (seen && begins < s.len) {
+                        const int page = kv4_page(c, s.row, index);
+                        if (page >= 0)
+                            where = (uint64_t)(heads + page * c.page_bytes + (cell & ((1 << shift) - 1)) * Kv8Cell<D>::kBytes);
+                        else
+                            kv4_bad(c);
+                    }
+                }
+            }
+            const uint64_t src = __shfl_sync(~0u, where, x & 31);
+            const int first = __shfl_sync(~0u, begins, x & 31);
+            const uint32_t st = (used + x) % S, bar = bars + 8 * st;
+            have = (have & ~(1u << st)) | (uint32_t)(src != 0) << st;
+            if (lane == 0) {
+                sm_first[st] = first;
+                mbar_arrive_expect_tx(bar, src ? Kv8Cell<D>::kBytes : 0u);
+                if (src)
+                    bulk_load(rings + st * SM::kStage, (const void *)src, Kv8Cell<D>::kBytes, bar);
+            }
+            __syncwarp();
+        };
+        for (int x = 0; x < S - 1 && x < mine; ++x)
+            fetch(x);
+
+        // Q as the B operand
+        if (warp < NT) {
+            const int j = warp;
+            float x[G][16];
+            float top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const uint32_t ws[4] = {qw[e][f].x, qw[e][f].y, qw[e][f].z, qw[e][f].w};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        x[e][8 * f + 2 * n] = bf16lo_to_f32(ws[n]);
+                        x[e][8 * f + 2 * n + 1] = bf16hi_to_f32(ws[n]);
+                    }
+                }
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+                    top = fmaxf(top, fabsf(x[e][n]));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            // 2^-e brings the row's largest magnitude into [1, 2): what is at least 2^-17 of it is
+            // exact in fp16 (eight bits above 2^-24), the rest is rounded to 2^-24
+            uint32_t e2 = (__float_as_uint(top) >> 23) & 0xFFu;
+            e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
+            const float up = __uint_as_float(e2 << 23); // the sign of the scale goes with q
+            const float down = a.scale < 0.0f ? -__uint_as_float((254u - e2) << 23) : __uint_as_float((254u - e2) << 23);
+#pragma unroll
+            for (int e = 0; e < G; ++e) {
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+                    x[e][n] *= down;
+                // word f of a lane's 16 channels is a k-step of 16
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                    sm_q[(j * KS + 4 * e + f) * 32 + lane] =
+                        make_uint2(pack_half2(x[e][4 * f], x[e][4 * f + 1]), pack_half2(x[e][4 * f + 2], x[e][4 * f + 3]));
+            }
+            if (t == 0)
+                sm_info[8 * j + g] = RowInfo{fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f),
+                                             real ? s.len - s.n_new + qrow / a.ratio + 1 : 0};
+        }
+        __syncthreads();
+        // with one n-tile Q stays in registers
+        constexpr bool kKeepQ = NT == 1;
+        uint2 qb[kKeepQ ? KS : 1];
+        float scale[NT][2];
+        if (kKeepQ) {
+#pragma unroll
+            for (int x = 0; x < KS; ++x)
+                qb[x % (kKeepQ ? KS : 1)] = sm_q[x * 32 + lane];
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            scale[j][0] = sm_info[8 * j + 2 * t].scale;
+            scale[j][1] = sm_info[8 * j + 2 * t + 1].scale;
+        }
+
+        float o[NT][D / 16][4] = {}; // [n-tile][m-tile][fragment]
+        // mo = kShift - m, the running maximum; before the first score so large that any raises m
+        float mo[NT][2], l[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            mo[j][0] = mo[j][1] = kNone, l[j][0] = l[j][1] = 0.0f;
+
+#pragma unroll 1
+        for (int x = 0; x < mine; ++x) {
+            if (x + S - 1 < mine) {
+                __syncwarp(); // the stage that is filled now was read by all lanes
+                fetch(x + S - 1);
+            }
+            const uint32_t st = (used + x) % S;
+            kv4_wait(bars + 8 * st, ((used + x) / S) & 1, c.status, dead);
+            if (__any_sync(~0u, dead)) {
+                // Ran out: the warp asks for no more cells, in this piece or the next, and the copies in
+                // flight end (bounded) before the parts take the rings' place.
+                for (int z = x; z < x + S && z < mine; ++z) {
+                    dead = false;
+                    kv4_wait(bars + 8 * ((used + z) % S), ((used + z) / S) & 1, c.status, dead);
+                }
+                dead = true;
+                mine = x;
+                break;
+            }
+            if (!(have >> st & 1u))
+                continue;
+            const uint8_t *const cell = ring + st * SM::kStage;
+            const int tok = sm_first[st];
+            const float2 scales = *(const float2 *)(cell + Kv8Cell<D>::kScales);
+            // V's scale goes with the weights, as an exponent; the sums are freed of it again
+            const float ev = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);
+            const float iv = __uint_as_float((254u << 23) - __float_as_uint(scales.y));
+
+            // scores
+            float sc[NT][4];
+            {
+                float acc[G][NT][4] = {};
+#pragma unroll
+                for (int e = 0; e < G; ++e) {
+                    const uint4 x0 = *((const uint4 *)(cell + e * 512) + lane);
+                    const uint4 x1 = *((const uint4 *)(cell + 8 * D + e * 512) + lane);
+                    const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        const uint32_t af[4] = {kv8_decode(w0[f]), kv8_decode(w1[f]), kv8_decode(w0[f] >> 16),
+                                                kv8_decode(w1[f] >> 16)};
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const int z = 4 * e + f;
+                            const uint2 q = kKeepQ ? qb[z % (kKeepQ ? KS : 1)] : sm_q[(j * KS + z) * 32 + lane];
+                            mma16816(acc[e][j], af, q.x, q.y);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) // token g + 8 (f / 2), row 2 t + f % 2
+                        sc[j][f] = (G == 2 ? acc[0][j][f] + acc[G - 1][j][f] : acc[0][j][f]) * scales.x;
+            }
+            // a row may see only part of the cell
+            if (tok + kKv4Cell > tile_first) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        sc[j][f] = tok + g + 8 * (f >> 1) < sm_info[8 * j + 2 * t + (f & 1)].limit ? sc[j][f] : -INFINITY;
+            }
+            float top = -INFINITY;
+            float y[NT][4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    y[j][f] = fmaf(sc[j][f], scale[j][f & 1], mo[j][f & 1] + ev);
+                    top = fmaxf(top, y[j][f]);
+                }
+            if (__any_sync(~0u, top > kShift + kSlack)) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        float z = fmaxf(sc[j][n], sc[j][n + 2]);
+                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 4));
+                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 8));
+                        z = fmaf(fmaxf(z, __shfl_xor_sync(~0u, z, 16)), scale[j][n], ev);
+                        const float was = mo[j][n], now = z == -INFINITY ? was : fminf(was, kShift - z);
+                        const float by = was == now ? 1.0f : exp2_approx(now - was);
+                        mo[j][n] = now;
+                        l[j][n] *= by;
+                        y[j][n] = fmaf(sc[j][n], scale[j][n], now + ev);
+                        y[j][n + 2] = fmaf(sc[j][n + 2], scale[j][n], now + ev);
+#pragma unroll
+                        for (int z4 = 0; z4 < D / 16; ++z4) {
+                            o[j][z4][n] *= by;
+                            o[j][z4][n + 2] *= by;
+                        }
+                    }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float p[4];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    p[f] = exp2_approx(y[j][f]);
+                    l[j][f & 1] = fmaf(p[f], iv, l[j][f & 1]);
+                }
+                pb[j][0] = transpose8x8(pack_half2(p[0], p[1]));
+                pb[j][1] = transpose8x8(pack_half2(p[2], p[3]));
+            }
+
+            // O^T += V^T P^T; tokens past the last that is seen hold anything: their V is taken as 0
+            const int end = s.len - tok;
+            uint32_t keep = ~0u;
+            if (end < kKv4Cell)
+                keep = (2 * t < end ? 0xFFu : 0u) | (2 * t + 1 < end ? 0xFF00u : 0u) | (2 * t + 8 < end ? 0xFF0000u : 0u) |
+                       (2 * t + 9 < end ? 0xFF000000u : 0u);
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                const uint4 x4 = *((const uint4 *)(cell + Kv8Cell<D>::kV + q * 512) + lane);
+                const uint32_t w[4] = {x4.x & keep, x4.y & keep, x4.z & keep, x4.w & keep};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t af[4] = {kv8_decode(w[2 * h]), kv8_decode(w[2 * h + 1]), kv8_decode(w[2 * h] >> 16),
+                                            kv8_decode(w[2 * h + 1] >> 16)};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        mma16816(o[j][2 * q + h], af, pb[j][0], pb[j][1]);
+                }
+            }
+        }
+        used += mine;
+        __syncthreads(); // the rings are read: the parts take their place
+
+        // the warp's part to shared memory: rows 2 t, 2 t + 1, channels 32 q + 4 g ..
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float x = l[j][n];
+                x += __shfl_xor_sync(~0u, x, 4);
+                x += __shfl_xor_sync(~0u, x, 8);
+                x += __shfl_xor_sync(~0u, x, 16);
+                const int row = 8 * j + 2 * t + n;
+                if (g == 0) {
+                    sm_m[warp * RT + row] = mo[j][n] == kNone ? -INFINITY : kShift - mo[j][n];
+                    sm_l[warp * RT + row] = x;
+                }
+                float *dst = sm_o + (warp * RT + row) * SM::kPitch + 4 * g;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q)
+                    *(float4 *)(dst + 32 * q) =
+                        make_float4(o[j][2 * q][n], o[j][2 * q][n + 2], o[j][2 * q + 1][n], o[j][2 * q + 1][n + 2]);
+            }
+        __syncthreads();
+
+        // joined over the warps; four channels of a row to a thread
+        const auto store = [&](int row, int ch, const float4 &x, float M, float L) {
+            const int r = row0 + row;
+            if (r >= rows)
+                return;
+            const int64_t token = s.first + r / a.ratio, h = (int64_t)head * a.ratio + r % a.ratio;
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            uint2 w;
+            w.x = f32_to_bf16_rn(x.x * inv) | ((uint32_t)f32_to_bf16_rn(x.y * inv) << 16);
+            w.y = f32_to_bf16_rn(x.z * inv) | ((uint32_t)f32_to_bf16_rn(x.w * inv) << 16);
+            *(uint2 *)(a.out + token * a.out_stride + h * D + ch) = w;
+            if (a.lse && ch == 0)
+                a.lse[token * a.n_q_heads + h] = L == 0.0f ? -INFINITY : (M - kShift + log2f(L)) * kLn2;
+        };
+        const bool whole = c0 == 0 && c1 == units;
+        float *part = nullptr;
+        if (!whole)
+            part = a.partials + ((int64_t)blockIdx.x * 2 + (c0 > 0 ? 0 : 1)) * part_floats<D, NT>();
+        for (int x = tid; x < RT * (D / 4); x += kThreads) {
+            const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
+            float M = -INFINITY, L = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                M = fmaxf(M, sm_m[w * RT + row]);
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = sm_m[w * RT + row];
+                const float f = mw == M ? 1.0f : exp2_approx(mw - M);
+                const float4 z = *(const float4 *)(sm_o + (w * RT + row) * SM::kPitch + ch);
+                L = fmaf(f, sm_l[w * RT + row], L);
+                y.x = fmaf(f, z.x, y.x);
+                y.y = fmaf(f, z.y, y.y);
+                y.z = fmaf(f, z.z, y.z);
+                y.w = fmaf(f, z.w, y.w);
+            }
+            if (whole) {
+                store(row, ch, y, M, L);
+            } else {
+                if (ch == 0) {
+                    part[row] = M;
+                    part[RT + row] = L;
+                }
+                *(float4 *)(part + 2 * RT + row * D + ch) = y;
+            }
+        }
+        if (!whole) {
+            // the segment's CTAs are first .. last; the last one to arrive joins their parts in order
+            const int first = (int)quotient(seg_lo + over, share), last = (int)quotient(seg_hi - 1, share);
+            __syncthreads();
+            if (tid == 0) {
+                const uint32_t n = (uint32_t)(last - first);
+                s_last = atom_add_acq_rel_gpu(a.counters + first, 1u) == n;
+                if (s_last)
+                    a.counters[first] = 0; // for the next launch
+            }
+            __syncthreads();
+            if (s_last) {
+                // weights of the parts first (a warp to a row), then their O: independent loads in a row
+                const int n = last - first + 1;
+                float *const weight = (float *)smem; // [n][RT], then [RT] M, [RT] L
+                float *const sum_m = weight + n * RT, *const sum_l = sum_m + RT;
+                const auto at = [&](int k) {
+                    return a.partials + ((int64_t)(first + k) * 2 + (k > 0 ? 0 : 1)) * part_floats<D, NT>();
+                };
+                for (int row = warp; row < RT; row += kWarps) {
+                    float M = -INFINITY, L = 0.0f;
+                    for (int k = lane; k < n; k += 32)
+                        M = fmaxf(M, ldcg_f32(at(k) + row));
+                    for (int z = 16; z; z >>= 1)
+                        M = fmaxf(M, __shfl_xor_sync(~0u, M, z));
+                    for (int k = lane; k < n; k += 32) {
+                        const float mk = ldcg_f32(at(k) + row);
+                        const float f = mk == M ? 1.0f : exp2_approx(mk - M);
+                        weight[k * RT + row] = f;
+                        L = fmaf(f, ldcg_f32(at(k) + RT + row), L);
+                    }
+                    for (int z = 16; z; z >>= 1)
+                        L += __shfl_xor_sync(~0u, L, z);
+                    if (lane == 0) {
+                        sum_m[row] = M;
+                        sum_l[row] = L;
+                    }
+                }
+                __syncthreads();
+                for (int x = tid; x < RT * (D / 4); x += kThreads) {
+                    const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k0 = 0; k0 < n; k0 += 8) {
+                        float4 z[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            z[k] = k0 + k < n ? __ldcg((const float4 *)(at(k0 + k) + 2 * RT + row * D + ch))
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float f = k0 + k < n ? weight[(k0 + k) * RT + row] : 0.0f;
+                            y.x = fmaf(f, z[k].x, y.x);
+                            y.y = fmaf(f, z[k].y, y.y);
+                            y.z = fmaf(f, z[k].z, y.z);
+                            y.w = fmaf(f, z[k].w, y.w);
+                        }
+                    }
+                    store(row, ch, y, sum_m[row], sum_l[row]);
+                }
+            }
+        }
+        // the next piece's copies overwrite the parts: they are read, and the reads come first
+        fence_proxy_async_smem();
+        __syncthreads();
+        pos += steps;
+    }
+    if (!kListed && s_rest)
+        kv4_answer_uncovered(b, a.out, a.out_stride, a.n_q_heads * D, a.lse, a.n_q_heads,
+                             (int64_t)blockIdx.x * kWarps + warp, (int64_t)gridDim.x * kWarps);
+}
+
+template <int D, int NT, bool kListed>
+nm_status launch(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, const Kv4Work &w, cudaStream_t st)
+{
+    constexpr size_t kMost = Smem<D, NT>::kSeqs + kKv4MaxSeqs * 24 + 8;
+    static_assert(kMost + 1024 <= 227 * 1024, "shared memory");
+    static OncePerDevice once;
+    if (!once(w.device, [] {
+            return cudaFuncSetAttribute(kv8_rows_kernel<D, NT, kListed>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost) ==
+                   cudaSuccess;
+        }))
+        return NM_ERR_CUDA;
+    const size_t smem = Smem<D, NT>::kSeqs + (size_t)(b.n_seqs + 1) * 8 + (size_t)b.n_seqs * sizeof(Kv4Seq);
+    const unsigned grid = (unsigned)(w.num_sms * (NT <= 2 ? 2 : 1)); // at most kKv4Counters / 4
+    kv8_rows_kernel<D, NT, kListed><<<grid, kThreads, smem, st>>>(c, b, a);
+    return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
+}
+
+} // namespace
+
+// Two parts of a CTA: of two CTAs to an SM with up to 16 rows, or of one with up to 32; here for 32 rows
+// and as many CTAs as the counters could serve.
+size_t kv8_partial_bytes(int head_dim)
+{
+    const size_t rows = (size_t)kKv4Counters / 2 * 2 * 32 * (head_dim + 2) * 4;
+    const size_t prompt = kv8_prompt_partial_bytes(head_dim);
+    return rows > prompt ? rows : prompt;
+}
+
+nm_status kv8_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &at, int64_t max_new, const int32_t *pages,
+                               int n_list, const Kv4Work &w, cudaStream_t st)
+{
+    const AttnArgs a{at.layer, at.n_q_heads / c.n_kv_heads, at.n_q_heads, (const uint16_t *)at.q, at.q_stride,
+                     at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials, pages, n_list};
+    if (pages) {
+        const int rows = a.ratio;
+        if (c.head_dim == 64)
+            return rows <= 8 ? launch<64, 1, true>(c, b, a, w, st) : launch<64, 2, true>(c, b, a, w, st);
+        return rows <= 8    ? launch<128, 1, true>(c, b, a, w, st)
+               : rows <= 16 ? launch<128, 2, true>(c, b, a, w, st)
+                            : launch<128, 4, true>(c, b, a, w, st);
+    }
+    const int64_t rows = (max_new < 65 ? max_new : 65) * a.ratio;
+    if (rows > 64 && b.n_tokens * at.n_q_heads > 1024)
+        return kv8_launch_prompt(c, b, at, w, st);
+    if (c.head_dim == 64)
+        return rows <= 8                 ? launch<64, 1, false>(c, b, a, w, st)
+               : rows > 16 && rows <= 24 ? launch<64, 3, false>(c, b, a, w, st)
+                                         : launch<64, 2, false>(c, b, a, w, st);
+    return rows <= 8    ? launch<128, 1, false>(c, b, a, w, st)
+           : rows <= 16 ? launch<128, 2, false>(c, b, a, w, st)
+           : rows <= 24 ? launch<128, 3, false>(c, b, a, w, st)
+           : rows <= 32 ? launch<128, 4, false>(c, b, a, w, st)
+           : rows <= 48 ? launch<128, 3, false>(c, b, a, w, st)
+                        : launch<128, 4, false>(c, b, a, w, st);
+}
+
+} // namespace nm
