@@ -141,11 +141,7 @@ nm_status kv_append_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache
         return NM_ERR_SHAPE;
     if (rope && !aligned(rope, 16))
         return NM_ERR_ALIGN;
-    int sms;
-    if ((s = view(f, cache, &o->c, &o->w, &sms)) != NM_OK)
-        return s;
-    o->b = Kv4Batch{seqs, starts, n_seqs, n_tokens};
-    return NM_OK;
+    return kv_open(f, o, cache, seqs, starts, n_seqs, n_tokens);
 }
 
 nm_status kv_read_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, int layer, const int32_t *seqs,
@@ -161,15 +157,11 @@ nm_status kv_read_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, 
         return NM_OK;
     if (!aligned(k, 16) || !aligned(v, 16))
         return NM_ERR_ALIGN;
-    int sms;
-    if ((s = view(f, cache, &o->c, &o->w, &sms)) != NM_OK)
-        return s;
-    o->b = Kv4Batch{seqs, starts, n_seqs, n_tokens};
-    return NM_OK;
+    return kv_open(f, o, cache, seqs, starts, n_seqs, n_tokens);
 }
 
-nm_status kv_attention_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, int layer, const int32_t *seqs,
-                            const int32_t *starts, int n_seqs, int64_t n_tokens, int64_t max_new, const void *q,
+nm_status kv_attention_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, int layer, const int32_t *starts,
+                            int n_seqs, int64_t n_tokens, int64_t max_new, const void *q,
                             int64_t q_stride, int n_q_heads, float scale, const void *out, int64_t out_stride,
                             const float *lse)
 {
@@ -193,11 +185,16 @@ nm_status kv_attention_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *ca
         return s;
     if (lse && !aligned(lse, 16))
         return NM_ERR_ALIGN;
-    int sms;
-    if ((s = view(f, cache, &o->c, &o->w, &sms)) != NM_OK)
-        return s;
-    o->b = Kv4Batch{seqs, starts, n_seqs, n_tokens};
     return NM_OK;
+}
+
+nm_status kv_open(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, const int32_t *seqs, const int32_t *starts,
+                  int n_seqs, int64_t n_tokens)
+{
+    int sms;
+    const nm_status s = view(f, cache, &o->c, &o->w, &sms);
+    o->b = Kv4Batch{seqs, starts, n_seqs, n_tokens};
+    return s;
 }
 
 } // namespace nm
@@ -283,9 +280,9 @@ nm_status nm_kv4_attention(const nm_kv4_cache *cache, int layer, const int32_t *
 {
     NvtxRange nvtx_("nm_kv4_attention");
     KvCall o;
-    const nm_status s = kv_attention_args(kFormat, &o, cache, layer, seqs, starts, n_seqs, n_tokens, max_new, q_bf16,
-                                          q_stride, n_q_heads, scale, out_bf16, out_stride, lse);
-    if (s != NM_OK || o.done)
+    nm_status s = kv_attention_args(kFormat, &o, cache, layer, starts, n_seqs, n_tokens, max_new, q_bf16, q_stride,
+                                    n_q_heads, scale, out_bf16, out_stride, lse);
+    if (s != NM_OK || o.done || (s = kv_open(kFormat, &o, cache, seqs, starts, n_seqs, n_tokens)) != NM_OK)
         return s;
     const Kv4Attn a{layer, q_bf16, q_stride, n_q_heads, scale, out_bf16, out_stride, lse};
     return kv4_launch_attention(o.c, o.b, a, starts ? max_new : 1, o.w, (cudaStream_t)stream);

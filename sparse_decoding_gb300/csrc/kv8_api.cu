@@ -103,11 +103,10 @@ nm_status nm_kv8_attention(const nm_kv8_cache *cache, int layer, const int32_t *
 {
     NvtxRange nvtx_("nm_kv8_attention");
     KvCall o;
-    nm_status s = kv_attention_args(kFormat, &o, cache, layer, seqs, starts, n_seqs, n_tokens, max_new, q_bf16, q_stride,
+    nm_status s = kv_attention_args(kFormat, &o, cache, layer, starts, n_seqs, n_tokens, max_new, q_bf16, q_stride,
                                     n_q_heads, scale, out_bf16, out_stride, lse);
-    if (s != NM_OK || o.done)
-        return s;
-    if (pages && (s = check_pages(cache, pages, n_list)) != NM_OK)
+    if (s != NM_OK || o.done || (pages && (s = check_pages(cache, pages, n_list)) != NM_OK) ||
+        (s = kv_open(kFormat, &o, cache, seqs, starts, n_seqs, n_tokens)) != NM_OK)
         return s;
     const Kv4Attn a{layer, q_bf16, q_stride, n_q_heads, scale, out_bf16, out_stride, lse};
     return kv8_launch_attention(o.c, o.b, a, starts ? max_new : 1, pages, n_list, o.w, (cudaStream_t)stream);
@@ -120,8 +119,8 @@ nm_status nm_kv8_select(const nm_kv8_cache *cache, int layer, const int32_t *seq
     NvtxRange nvtx_("nm_kv8_select");
     KvCall o;
     // q alone is read: its checks are attention's
-    nm_status s = kv_attention_args(kFormat, &o, cache, layer, seqs, starts, n_seqs, n_tokens, 1, q_bf16, q_stride,
-                                    n_q_heads, 1.0f, q_bf16, q_stride, nullptr);
+    nm_status s = kv_attention_args(kFormat, &o, cache, layer, starts, n_seqs, n_tokens, 1, q_bf16, q_stride, n_q_heads,
+                                    1.0f, q_bf16, q_stride, nullptr);
     if (s != NM_OK || o.done)
         return s;
     if (!pages || first < 0 || last < 1)
@@ -132,6 +131,8 @@ nm_status nm_kv8_select(const nm_kv8_cache *cache, int layer, const int32_t *seq
         return NM_ERR_INVALID_ARG;
     if (cache->max_pages > kKv8SelectPages)
         return NM_ERR_UNSUPPORTED;
+    if ((s = kv_open(kFormat, &o, cache, seqs, starts, n_seqs, n_tokens)) != NM_OK)
+        return s;
     const Kv8Select a{layer, n_q_heads, n_list, first, last, q_bf16, q_stride, pages};
     return kv8_launch_select(o.c, o.b, a, o.w, (cudaStream_t)stream);
 }

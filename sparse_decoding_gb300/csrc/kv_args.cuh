@@ -146,22 +146,24 @@ nm_status kv_compact(const KvFormat &f, const nm_kv4_cache *cache, cudaStream_t 
 nm_status kv_copy_pages(const KvFormat &f, const nm_kv4_cache *src, const int32_t *src_pages, const nm_kv4_cache *dst,
                         const int32_t *dst_pages, int64_t n, cudaStream_t st);
 
-// Of append, read and attention: their arguments checked, *c, *w and *b filled in. *done: there is
-// nothing to do.
+// Of append, read and attention: their arguments checked. done: there is nothing to do. kv_open fills
+// in the rest; it asks CUDA first, so it comes after every refusal (append's and read's checks end with it).
 struct KvCall {
     Kv4 c;
     Kv4Work w;
     Kv4Batch b;
     bool done;
 };
+nm_status kv_open(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, const int32_t *seqs, const int32_t *starts,
+                  int n_seqs, int64_t n_tokens);
 nm_status kv_append_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, int layer, const int32_t *seqs,
                          const int32_t *starts, int n_seqs, int64_t n_tokens, const void *k, int64_t k_stride,
                          const void *v, int64_t v_stride, const void *q, int64_t q_stride, int n_q_heads,
                          const void *q_out, int64_t q_out_stride, const float *rope, int64_t rope_rows);
 nm_status kv_read_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, int layer, const int32_t *seqs,
                        const int32_t *starts, int n_seqs, int64_t n_tokens, const void *k, const void *v);
-nm_status kv_attention_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, int layer, const int32_t *seqs,
-                            const int32_t *starts, int n_seqs, int64_t n_tokens, int64_t max_new, const void *q,
+nm_status kv_attention_args(const KvFormat &f, KvCall *o, const nm_kv4_cache *cache, int layer, const int32_t *starts,
+                            int n_seqs, int64_t n_tokens, int64_t max_new, const void *q,
                             int64_t q_stride, int n_q_heads, float scale, const void *out, int64_t out_stride,
                             const float *lse);
 
