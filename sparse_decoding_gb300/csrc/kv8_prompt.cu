@@ -608,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
 #pragma unroll 1
             for (int i = 0; i < nk; ++i, ++n_s) {
                 const uint32_t n_blk = n_first + i;
-                wait(sh.scales_full[n_blk & 3], n_blk >> 2);
                 wait(sh.s_full[k], n_s);
+                wait(sh.scales_full[n_blk & 3], n_blk >> 2); // they are there: their K was unpacked
                 fence_after();
                 const int vis = limit - (w.b0 + i) * kBlock; // columns this row sees
                 const CellScales *const cells = sh.scales[n_blk & 3];
@@ -617,8 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                 const bool masked = !__all_sync(~0u, vis >= kBlock) || sh.gaps[n_blk & 3];
                 const auto mask = [&](uint32_t *r, int h) { // columns 32 h ..
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        r[e] = 32 * h + e < vis && cells[2 * h + e / 16].k >= 0.0f ? r[e] : 0xFF800000u;
+                    for (int z = 0; z < 2; ++z) {
+                        const int end = cells[2 * h + z].k < 0.0f ? 0 : vis - 32 * h - 16 * z;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            r[16 * z + e] = e < end ? r[16 * z + e] : 0xFF800000u;
+                    }
                 };
                 // S is read twice, 64 columns at a time: for the maximum, then for the weights. The maximum is
                 // raised when a score passes it by more than the slack.
