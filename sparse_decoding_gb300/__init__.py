@@ -636,7 +636,7 @@ class Kv4Cache:
             if out.shape[0] != T or oh != qh:
                 raise ValueError("out must have q's tokens and heads")
         sp, st, n = self._batch(seqs, starts, T if starts is None else None)
-        ls = q.new_empty((T, qh), dtype=torch.float32) if lse else None
+        ls = torch.empty((T, qh), dtype=torch.float32, device=self.device) if lse else None
         status = self._f["attention"](self._ref, layer, sp, st, n, T, (T or 1) if max_new is None else max_new, qp, qs, qh,
                                       self.head_dim ** -0.5 if scale is None else scale, *listed, op, os_,
                                       ls.data_ptr() if lse else None, self._s())

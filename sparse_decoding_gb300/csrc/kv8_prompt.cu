@@ -14,9 +14,9 @@
 // softmax, V's (2^e) is an exponent of the weights, and the sums of the weights are freed of it
 // again, sixteen columns at a time. Scores carry fp32 rounding only, as in the kernel for few rows.
 //
-// Roles (20 warps): two softmax warpgroups, one per tile (a thread owns a row: no
+// Roles (16 warps): two softmax warpgroups, one per tile (a thread owns a row: no
 // reductions across threads; it also loads and scales its row of Q, rescales and
-// stores its row of O); two warpgroups that make the codes fp16 in two stages of K
+// stores its row of O); a warpgroup that makes the codes fp16 in two stages of K
 // and of V^T (both tiles use them); one warp that issues the MMAs; one that lists
 // the pieces of work. While one tile is in its softmax, the other's MMAs run. The
 // running maximum is raised only when a score passes it by 2^8, so O is rarely
@@ -40,98 +40,114 @@ namespace nm {
 namespace {
 
 constexpr int kSoft = 256;      // softmax threads: two tiles of 128 rows
-constexpr int kUnpack = 256;    // unpacking threads
-constexpr int kMmaWarp = 16;    // of its warpgroup, the next one lists the pieces and two idle
-constexpr int kThreads = 640;
-// Registers of a thread: at launch (what 640 threads can have), and in each role.
-constexpr int kLaunchRegs = 96, kSoftRegs = 160, kUnpackRegs = 64, kMmaRegs = 32;
+constexpr int kUnpack = 128;    // unpacking threads
+constexpr int kMmaWarp = 12;    // of its warpgroup, the next one lists the pieces and two copy K
+constexpr int kLoad = 64;       // the threads of those
+constexpr int kThreads = 512;
+// Registers of a thread: at launch (what 512 threads can have), and in each role.
+constexpr int kLaunchRegs = 128, kSoftRegs = 184, kUnpackRegs = 104, kMmaRegs = 40;
 static_assert(kSoftRegs >= kLaunchRegs && kUnpackRegs <= kLaunchRegs && kMmaRegs <= kLaunchRegs &&
                   kSoft * kSoftRegs + kUnpack * kUnpackRegs + 128 * kMmaRegs <= kThreads * kLaunchRegs,
               "a role that takes registers waits until others have given them back");
 constexpr int kSeqCache = 512;  // sequences whose descriptors are kept in shared memory
 constexpr int kBlock = 128;    // tokens of a block
 constexpr int kMinShare = 2;   // blocks of a CTA at least
-constexpr int kSub = 128 * 128; // bytes of 128 rows of 64 fp16
 constexpr float kShift = 6.0f, kSlack = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D> struct Cfg {
-    static constexpr int G = D / 64;
-    static constexpr int kQ = G * kSub;          // a tile of Q, and a stage of K
-    static constexpr int kV = 2 * D * 128;       // a stage of V^T: two halves of 64 tokens
-    static constexpr int kOffK = 2 * kQ, kOffV = kOffK + 2 * kQ, kTiles = kOffV + 2 * kV;
-    static constexpr int kPart = 128 * (D + 2);  // floats of a tile's part
+    static constexpr int kK = 128 * D;      // one part of a tile of Q, a stage of K, of V's codes
+    static constexpr int kV = 2 * D * 128;  // a stage of V^T: two halves of 64 tokens
+    static constexpr int kOffK = 4 * kK, kOffV = kOffK + 2 * kK, kOffRaw = kOffV + 2 * kV, kTiles = kOffRaw + 2 * kK;
+    static constexpr int kPart = 128 * (D + 2); // floats of a tile's part
+    // where in a row of D bytes (under the D-byte swizzle) its c-th 16 bytes are
+    static __device__ __forceinline__ uint32_t piece(int row, int c) { return (c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4; }
 };
 
-// What an unpacking thread u holds of a block. K: 64 channels of row u / G (at D = 64 of the first 128
-// threads). V: the cell u / (D / 4), channels 4 (u % (D / 4)) .. of its 16 tokens (at D = 64, of the first
-// 128 threads too). Both are 64 bytes side by side.
-struct Codes {
-    uint4 w[4];
+// The scales of a block, in shared memory: K's of each cell (1 where there is none), the exponent of
+// V's largest and 2^-that, and which cells are not there.
+struct BlockScales {
+    float k[8];
+    float ev, iv;
+    uint32_t gaps, pad;
 };
-// The scales of a block's cells, in shared memory: of K, V's exponent, and 2^-that. Cells that are not
-// there have the factor -1.
-struct CellScales {
-    float k, ev, iv, pad;
-};
-template <int D> __device__ __forceinline__ bool unpacks(int u) { return u < 128 * Cfg<D>::G; }
-template <int D> __device__ __forceinline__ void load_k(Codes &r, uint64_t where, int u)
+// Two codes as fp16, times a power of two of at most 1: V's scale in its cell over the block's largest. Exact
+// down to 2^-15 of that; beyond, what is below 2^-24 of it is rounded.
+__device__ __forceinline__ uint32_t decode_by(uint32_t two, __half2 by) { return as_u32(__hmul2(as_half2(kv8_decode(two)), by)); }
+// The largest of the scales of V that lanes 0 .. 7 have (0: none; 1 if all are).
+__device__ __forceinline__ float largest_of(float v)
 {
-    constexpr int G = Cfg<D>::G;
-    const int row = u / G, j = u % G;
-    const uint64_t cell = __shfl_sync(~0u, where, (row >> 4) & 7);
-    const uint8_t *const src = (const uint8_t *)cell + ((row >> 3) & 1) * 8 * D + j * 512 + (row & 7) * 64;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        r.w[i] = cell && unpacks<D>(u) ? ldg_nc128(src + 16 * i) : make_uint4(0, 0, 0, 0);
+    for (int o = 1; o < 8; o <<= 1)
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+    return v > 0.0f ? v : 1.0f;
 }
-template <int D> __device__ __forceinline__ void unpack_k(const Codes &r, uint32_t ks, int u)
+__device__ __forceinline__ float pow2_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
+// Codes of a block go to shared memory 16 bytes at a time: K to its rows, by 64 threads; V as they
+// are, by 128, where piece (cell, four channels, t) is the t ^ (cell % 4)th of its four.
+// where: lane z < 8's, the address of cell z (0: it is not there, and reads as zeros).
+template <int D> __device__ __forceinline__ void copy_k(uint64_t where, const void *pool, uint32_t ks, int u)
 {
-    constexpr int G = Cfg<D>::G;
-    if (!unpacks<D>(u))
-        return;
-    const int row = u / G, j = u % G;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-            sts128(ks + j * kSub + row * 128 + (((2 * i + f) ^ (row & 7)) << 4), kv8_decode(w[2 * f]),
-                   kv8_decode(w[2 * f] >> 16), kv8_decode(w[2 * f + 1]), kv8_decode(w[2 * f + 1] >> 16));
+    // piece [2 halves][D / 64][8 tokens][4] of a cell, in order
+    const int g = (u >> 2) & 7, c = D == 128 ? ((u >> 5) & 1) * 4 + (u & 3) : u & 3, row = D == 128 ? g : (u >> 5) * 8 + g;
+    const uint32_t dst = ks + row * D + Cfg<D>::piece(row, c);
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+        const uint64_t cell = __shfl_sync(~0u, where, i / (D / 64));
+        async_copy16(dst + i * 1024, cell ? (const uint8_t *)cell + (i % (D / 64)) * 1024 + u * 16 : pool, cell != 0);
     }
 }
-template <int D> __device__ __forceinline__ void load_v(Codes &r, uint64_t where, int u)
+template <int D> __device__ __forceinline__ void copy_v(uint64_t where, const void *pool, uint32_t raw, int u)
 {
-    const uint64_t cell = __shfl_sync(~0u, where, (u / (D / 4)) & 7);
-    const uint8_t *const src = (const uint8_t *)cell + Kv8Cell<D>::kV + (u % (D / 4)) * 64;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-        r.w[t] = cell && unpacks<D>(u) ? ldg_nc128(src + 16 * t) : make_uint4(0, 0, 0, 0);
+    const int first = D == 128 ? 0 : u >> 6, piece = u & (D - 1);
+#pragma unroll 4
+    for (int i = 0; i < D / 16; ++i) {
+        const int z = D == 128 ? i : 2 * i + first;
+        const uint64_t cell = __shfl_sync(~0u, where, z);
+        async_copy16(raw + z * 16 * D + (piece >> 2) * 64 + (((piece & 3) ^ (z & 3)) << 4),
+                     cell ? (const uint8_t *)cell + Kv8Cell<D>::kV + piece * 16 : pool, cell != 0);
+    }
 }
-// left: tokens of the sequence from the block's first on; past them V is 0, whatever is there.
-template <int D> __device__ __forceinline__ void unpack_v(const Codes &r, uint32_t vs, int u, int left)
+// V^T as fp16 from V's codes: a thread takes four channels of a cell at a time, 16 tokens of each.
+// by: lane z < 8's, the factor of cell z. left: tokens of the sequence from the block's first on; past them V is 0,
+// whatever is there.
+template <int D> __device__ __forceinline__ void unpack_v(uint32_t raw, uint32_t vs, float by, int u, int left)
 {
-    if (!unpacks<D>(u))
-        return;
-    const int cell = u / (D / 4), ch0 = 4 * (u % (D / 4)), tok = cell * 16;
-    const uint32_t dst = vs + (cell >> 2) * (D * 128) + ch0 * 128;
-    uint32_t keep[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-        keep[t] = tok + 16 <= left ? ~0u
-                                   : (tok + 2 * t < left ? 0xFFu : 0u) | (tok + 2 * t + 1 < left ? 0xFF00u : 0u) |
-                                         (tok + 2 * t + 8 < left ? 0xFF0000u : 0u) | (tok + 2 * t + 9 < left ? 0xFF000000u : 0u);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int ch = ch0 + c; // of its row's 16-byte pieces (8 tokens), 2 (cell % 4) + p
-        uint32_t w[4];
+    // lanes that store together differ in the cell (of four) and in the channels' parity, and
+    // then in which half of the cell's tokens they store first: no two in one bank
+    const int odd = u & 1;
+#pragma unroll 1
+    for (int i = 0; i < D / 64; ++i) {
+        const int four = odd + 2 * ((u >> 3) & 3) + 8 * ((u >> 5) & (D / 32 - 1)); // channels 4 four ..
+        const int cell = ((u >> 1) & 3) + 4 * (D == 128 ? i : u >> 6);
+        const __half2 f = __float2half2_rn(__shfl_sync(~0u, by, cell));
+        uint32_t w[4][4]; // [t][channel]
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            w[t] = (c == 0 ? r.w[t].x : c == 1 ? r.w[t].y : c == 2 ? r.w[t].z : r.w[t].w) & keep[t];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[t][0]), "=r"(w[t][1]), "=r"(w[t][2]), "=r"(w[t][3])
+                         : "r"(raw + cell * 16 * D + four * 64 + ((t ^ (cell & 3)) << 4)));
+        const int end = left - cell * 16;
+        if (end < 16) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-            sts128(dst + c * 128 + (((2 * (cell & 3) + p) ^ (ch & 7)) << 4), kv8_decode(w[0] >> (16 * p)),
-                   kv8_decode(w[1] >> (16 * p)), kv8_decode(w[2] >> (16 * p)), kv8_decode(w[3] >> (16 * p)));
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t keep = (2 * t < end ? 0xFFu : 0u) | (2 * t + 1 < end ? 0xFF00u : 0u) |
+                                      (2 * t + 8 < end ? 0xFF0000u : 0u) | (2 * t + 9 < end ? 0xFF000000u : 0u);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    w[t][c] &= keep;
+            }
+        }
+        const uint32_t rows = vs + (cell >> 2) * (D * 128) + four * 512;
+#pragma unroll 1
+        for (int p = 0; p < 2; ++p) {
+            const int half = p ^ odd; // tokens 8 half ..
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sts128(rows + c * 128 + (((2 * (cell & 3) + half) ^ (4 * odd + c)) << 4), decode_by(w[0][c] >> (16 * half), f),
+                       decode_by(w[1][c] >> (16 * half), f), decode_by(w[2][c] >> (16 * half), f), decode_by(w[3][c] >> (16 * half), f));
+        }
     }
 }
 
@@ -182,14 +198,13 @@ struct Piece {
 constexpr int kRing = 4;        // pieces known ahead
 
 struct Shared {
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], raw_full[2];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], met[2], scales_full[4];
     uint32_t tmem;
     uint32_t last[2];
     uint64_t piece_full[kRing], piece_empty[kRing];
     Piece piece[kRing];
-    CellScales scales[4][8]; // of the last blocks' cells: block n's are overwritten by n + 4's, when n + 1 is done
-    bool gaps[4];            // whether some of a block's cells are not there
+    BlockScales scales[4]; // of the last blocks: block n's are overwritten by n + 4's, when n + 1 is done
     int64_t total, share;
     int seq, head, pair, step; // where the CTA's part of the line starts
     bool rest;                 // some rows belong to no sequence
@@ -304,7 +319,6 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, const Kv4Batch b, const PromptArgs a)
 {
     using C = Cfg<D>;
-    constexpr int G = C::G;
     extern __shared__ __align__(1024) uint8_t dsmem[];
     __shared__ Shared sh;
     uint8_t *const base = dsmem + ((1024u - (smem_addr(dsmem) & 1023u)) & 1023u);
@@ -317,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sh.k_full[i]), kUnpack);
+            mbar_init(smem_addr(&sh.k_full[i]), kLoad);
+            mbar_init(smem_addr(&sh.raw_full[i]), kUnpack);
             mbar_init(smem_addr(&sh.v_full[i]), kUnpack);
             mbar_init(smem_addr(&sh.k_empty[i]), 1);
             mbar_init(smem_addr(&sh.v_empty[i]), 1);
@@ -331,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
             mbar_init(smem_addr(&sh.scales_full[i]), 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_addr(&sh.piece_full[i]), 1);
-            mbar_init(smem_addr(&sh.piece_empty[i]), kMmaWarp + 1); // a lane of each warp that takes pieces
+            mbar_init(smem_addr(&sh.piece_empty[i]), kMmaWarp + 3); // a lane of each warp that takes pieces
         }
         fence_mbar_init();
     }
@@ -446,13 +461,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
         return w;
     };
 
+    // f(addresses of the cells, piece, block, scales of the cells, more) for the blocks of all pieces, and
+    // once more without one, for a whole warp: lane z < 8's cell z (0: it is not there, and its scales are 0).
+    // The pages of a block are asked for before the block ahead of it is worked on.
+    const auto walk = [&](const auto &f) {
+        const int in_page = c.page_shift - 4;
+        uint32_t piece = 0;
+        Piece w{};
+        int i = -1, page = -2;
+        bool more;
+#pragma unroll 1
+        do {
+            const Piece now = w;
+            const int b = w.b0 + i, cell = b * 8 + (lane & 7);
+            more = i >= 0 && w.nblk > 0;
+            uint64_t where = 0;
+            if (page >= 0 && page < c.n_pages)
+                where = (uint64_t)(c.pool + kv8_head_offset<D>(c, page, a.layer, w.head) +
+                                   (cell & ((1 << in_page) - 1)) * Kv8Cell<D>::kBytes);
+            else if (page != -2 && tid < kSoft + 8)
+                kv4_bad(c);
+            const float2 scales =
+                where ? __ldg((const float2 *)((const uint8_t *)where + Kv8Cell<D>::kScales)) : make_float2(0.0f, 0.0f);
+            if (++i == w.nblk) { // at first there is no piece
+                i = 0;
+                w = get_piece(piece++);
+            }
+            page = -2; // nothing to find
+            const int next = (w.b0 + i) * 8 + (lane & 7);
+            if (w.nblk > 0 && next * kKv4Cell < w.len)
+                page = max(c.tables[(int64_t)w.row * c.max_pages + (next >> in_page)], -1);
+            if (more || w.nblk == 0)
+                f(where, now, b, scales, more);
+        } while (w.nblk > 0 || more);
+    };
+
     if (warp < 8) {
         // ---- softmax: a row per thread ----
         setmaxnreg_inc<kSoftRegs>();
         const int k = warp >> 2; // the tile
         const int row = tid & 127;
         const int row_token = row / a.ratio, row_head = row % a.ratio;
-        const uint32_t q_tile = tiles + k * C::kQ;
+        const uint32_t q_tile = tiles + 2 * k * C::kK;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + k * 128, t_o = tmem + lanes + 256 + k * 128;
         const auto count = [&](const Piece &w) { return k ? w.n1 : w.n0; };
@@ -461,7 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
         uint32_t n_s = 0, n_o = 0; // blocks and pieces of this tile so far
         uint32_t n_first = 0;      // blocks of the CTA before the piece
 
-        // The row of Q, scaled by a power of two. Returns the factor of the scores.
+        // The row of Q, scaled by a power of two to below 2^8, in two parts: the first four significant
+        // bits (e4m3), and what is left (e5m2). Returns the factor of the scores.
         const auto load_q = [&](const Piece &w) {
             constexpr int N = D / 8; // 16-byte pieces of a row
             const bool valid = valid_in(w);
@@ -478,27 +529,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                 for (int n = 0; n < 4; ++n)
                     top = max(top, max(ws[n] & 0x7FFF0000u, (ws[n] << 16) & 0x7FFF0000u));
             }
-            uint32_t e2 = top >> 23;
-            e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
-            const float up = __uint_as_float(e2 << 23);
-            const float down = a.scale < 0.0f ? -__uint_as_float((254u - e2) << 23) : __uint_as_float((254u - e2) << 23);
+            const uint32_t field = top >> 23;
+            const uint32_t e2 = field == 0xFFu || field == 0 ? 127u : field > 250u ? 250u : field < 8u ? 8u : field;
+            const float up = __uint_as_float((e2 - 7u) << 23);
+            const float down = a.scale < 0.0f ? -__uint_as_float((261u - e2) << 23) : __uint_as_float((261u - e2) << 23);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                uint32_t y[4];
+            for (int i = 0; i < N; i += 2) {
+                uint32_t hi[4], lo[4]; // of 16 channels
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    y[n] = pack_half2(bf16lo_to_f32(ws[n]) * down, bf16hi_to_f32(ws[n]) * down);
-                sts128(q_tile + (i >> 3) * kSub + row * 128 + (((i & 7) ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t ws[4] = {x[i + h].x, x[i + h].y, x[i + h].z, x[i + h].w};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const uint32_t y = pack_half2(bf16lo_to_f32(ws[n]) * down, bf16hi_to_f32(ws[n]) * down);
+                        uint16_t p, r;
+                        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(y));
+                        const uint32_t left = as_u32(__hsub2(as_half2(y), as_half2(kv8_decode(p))));
+                        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(left));
+                        hi[2 * h + n / 2] = n & 1 ? hi[2 * h + n / 2] | (uint32_t)p << 16 : p;
+                        lo[2 * h + n / 2] = n & 1 ? lo[2 * h + n / 2] | (uint32_t)r << 16 : r;
+                    }
+                }
+                const uint32_t at = q_tile + row * D + C::piece(row, i / 2);
+                sts128(at, hi[0], hi[1], hi[2], hi[3]);
+                sts128(at + C::kK, lo[0], lo[1], lo[2], lo[3]);
             }
             fence_proxy_async_smem();
             kv4_arrive(smem_addr(&sh.q_full[k]));
+            if (field == 0xFFu && w.len - w.n_new + token_of(w) >= 0) // something that is not finite meets a token
+                return __uint_as_float(0x7FC00000u);
             return fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f); // above 0, so that masked scores stay -inf
         };
 
         // The rows of O of a piece.
-        const auto finish = [&](const Piece &done, float m, float l) {
-            const int nk = count(done);
+        const auto finish = [&](const Piece &done, int nk, float m, float l) {
             if (l == 0.0f)
                 m = -INFINITY; // nothing seen
             if (nk > 0) {
@@ -588,19 +652,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
             fence_before();
         };
 
-        // Q of a piece is loaded while the last MMAs of the one before run
+        // Q of a piece is loaded while the last MMAs of the one before run. Pieces stay in the ring until they
+        // are finished, and are read there: in registers they would be held across the softmax.
         float rs = 1.0f, m = 0.0f, l = 0.0f;
-        Piece done{};
+        int nk = 0;
 #pragma unroll 1
         for (uint32_t piece = 0;; ++piece) {
-            const Piece w = get_piece(piece);
-            if (count(w) > 0)
+            wait(sh.piece_full[piece % kRing], piece / kRing);
+            dead = __any_sync(~0u, dead);
+            const Piece &w = sh.piece[piece % kRing];
+            const bool none = dead || w.nblk == 0; // as in get_piece
+            const int n_done = nk;
+            nk = none ? 0 : count(w);
+            if (nk > 0)
                 rs = load_q(w);
-            if (piece > 0)
-                finish(done, m, l);
-            if (w.nblk == 0)
+            if (piece > 0) {
+                finish(sh.piece[(piece - 1) % kRing], n_done, m, l);
+                __syncwarp();
+                if (lane == 0)
+                    kv4_arrive(smem_addr(&sh.piece_empty[(piece - 1) % kRing]));
+            }
+            if (none)
                 break;
-            const int nk = count(w);
             const int limit = valid_in(w) ? w.len - w.n_new + token_of(w) + 1 : 0;
             // rows that see nothing of the piece need no maximum
             m = limit > w.b0 * kBlock ? -INFINITY : 0.0f;
@@ -612,51 +685,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                 wait(sh.scales_full[n_blk & 3], n_blk >> 2); // they are there: their K was unpacked
                 fence_after();
                 const int vis = limit - (w.b0 + i) * kBlock; // columns this row sees
-                const CellScales *const cells = sh.scales[n_blk & 3];
-                // only the last blocks of a row are masked, and blocks with cells that are not there
-                const bool masked = !__all_sync(~0u, vis >= kBlock) || sh.gaps[n_blk & 3];
-                const auto mask = [&](uint32_t *r, int h) { // columns 32 h ..
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int end = cells[2 * h + z].k < 0.0f ? 0 : vis - 32 * h - 16 * z;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            r[16 * z + e] = e < end ? r[16 * z + e] : 0xFF800000u;
-                    }
-                };
-                // S is read twice, 64 columns at a time: for the maximum, then for the weights. The maximum is
-                // raised when a score passes it by more than the slack.
-                uint32_t r[2][32];
-                const auto read = [&](int h) { // columns 32 h .. 32 h + 63
-                    ld32(t_s + 32 * h, r[0]);
-                    ld32(t_s + 32 * h + 32, r[1]);
+                const BlockScales &bs = sh.scales[n_blk & 3];
+                const float ev = bs.ev;
+                const uint32_t gaps = bs.gaps;
+                // Only the last blocks of a row are masked, as a rule, and blocks with cells that are not there.
+                const bool masked = !__all_sync(~0u, vis >= kBlock && gaps == 0);
+                uint32_t r[32];
+                const auto read = [&](int h) { // columns 32 h ..
+                    ld32(t_s + 32 * h, r);
                     wait_ld();
-                    tie<32>(r[0]);
-                    tie<32>(r[1]);
+                    tie<32>(r);
                     if (masked) {
-                        mask(r[0], h);
-                        mask(r[1], h + 1);
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const int end = gaps >> (2 * h + z) & 1u ? 0 : vis - 32 * h - 16 * z;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                r[16 * z + e] = e < end ? r[16 * z + e] : 0xFF800000u;
+                        }
                     }
                 };
+                // S is read twice, 32 columns at a time: for the maximum, which is raised when a score passes
+                // it by more than the slack, and for the weights. Loops, so that the code stays in the
+                // instruction caches beside the other roles'.
                 float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
-                    if (h % 2 == 0)
-                        read(h);
+                    read(h);
+                    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const uint32_t *const x = r[h & 1] + 16 * z;
-                        float top[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
-#pragma unroll
-                        for (int e = 2; e < 14; e += 4) {
-                            top[0] = fmaxf(fmaxf(top[0], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
-                            top[1] = fmaxf(fmaxf(top[1], __uint_as_float(x[e + 2])), __uint_as_float(x[e + 3]));
-                        }
-                        top[0] = fmaxf(fmaxf(top[0], __uint_as_float(x[14])), __uint_as_float(x[15]));
-                        const CellScales &cs = cells[2 * h + z];
-                        mx = fmaxf(mx, fmaf(fmaxf(top[0], top[1]), rs * fabsf(cs.k), cs.ev));
-                    }
+                    for (int e = 0; e < 32; e += 2)
+                        top[e / 16] = fmaxf(fmaxf(top[e / 16], __uint_as_float(r[e])), __uint_as_float(r[e + 1]));
+                    mx = fmaxf(mx, fmaxf(top[0] * bs.k[2 * h], top[1] * bs.k[2 * h + 1]));
                 }
+                mx = fmaf(mx, rs, ev);
                 if (__any_sync(~0u, mx > m + kSlack)) {
                     const float mn = fmaxf(m, mx);
                     const float f = mn == m ? 1.0f : exp2_approx(m - mn);
@@ -676,111 +738,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                         }
                     }
                 }
-                const float off = kShift - (m == -INFINITY ? 0.0f : m);
-#pragma unroll
+                const float off = kShift - (m == -INFINITY ? 0.0f : m) + ev;
+                const uint64_t off2 = pair(off, off);
+                uint64_t sum2[2] = {0, 0};
+#pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
-                    if (h % 2 == 0)
-                        read(h);
+                    const float f[2] = {rs * bs.k[2 * h], rs * bs.k[2 * h + 1]};
+                    read(h);
                     uint32_t p[16];
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const uint32_t *const s = r[h & 1] + 16 * z;
-                        const CellScales cs = cells[2 * h + z];
-                        const float rk = rs * fabsf(cs.k), at = off + cs.ev;
-                        const uint64_t rk2 = pair(rk, rk), at2 = pair(at, at);
-                        uint64_t sum2[2] = {0, 0};
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float x, y;
-                            unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), rk2, at2), x, y);
-                            x = exp2_approx(x);
-                            y = exp2_approx(y);
-                            sum2[(e / 2) & 1] = add2(sum2[(e / 2) & 1], pair(x, y));
-                            p[8 * z + e / 2] = pack_half2(x, y);
-                        }
+                    for (int e = 0; e < 32; e += 2) {
                         float x, y;
-                        unpair(add2(sum2[0], sum2[1]), x, y);
-                        l = fmaf(x + y, cs.iv, l);
+                        unpair(fma2(pair(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), pair(f[e / 16], f[e / 16]), off2), x, y);
+                        x = exp2_approx(x);
+                        y = exp2_approx(y);
+                        sum2[(e / 2) & 1] = add2(sum2[(e / 2) & 1], pair(x, y));
+                        p[e / 2] = pack_half2(x, y);
                     }
                     st16(t_s + 16 * h, p);
                 }
+                float x, y;
+                unpair(add2(sum2[0], sum2[1]), x, y);
+                l = fmaf(x + y, bs.iv, l);
                 wait_st();
                 fence_before();
                 kv4_arrive(smem_addr(&sh.p_full[k]));
             }
 
             n_first += w.nblk;
-            done = w;
         }
     } else if (warp < kMmaWarp) {
         setmaxnreg_dec<kUnpackRegs>();
-        // ---- unpacking: 256 threads fill K and V^T of a block ----
+        // ---- V^T: block n's codes are asked for while block n - 1's become fp16 ----
         const int u = tid - kSoft;
-        const int in_page = c.page_shift - 4;
-        Codes rk, rv;
-        float2 scales = make_float2(-1.0f, 1.0f); // lane z < 8 of the first warp: cell z's
-        uint32_t piece = 0;
-        Piece w = get_piece(piece);
-        int i = 0;        // the block to fetch: b0 + i of piece w
-        int left = 0;     // tokens of the fetched block's sequence from its first on
-        uint32_t n = ~0u; // the number of the fetched block; none yet
-        bool more = w.nblk > 0;
-#pragma unroll 1
-        for (;;) {
-            // Block n (fetched before) is unpacked, and the next one fetched, K and V in turn:
-            // each one's registers are free as soon as it is in shared memory. Lane z < 8 asks
-            // for the page of cell z first, and finds where it is (0: nowhere).
-            const int cell = (w.b0 + i) * 8 + (lane & 7);
-            const bool inside = more && cell * kKv4Cell < w.len;
-            const int32_t page = inside ? c.tables[(int64_t)w.row * c.max_pages + (cell >> in_page)] : -1;
-            const int st = n & 1;
-            if (n != ~0u) {
-                if (n >= 2)
-                    wait(sh.k_empty[st], (n >> 1) - 1);
-                unpack_k<D>(rk, tiles + C::kOffK + st * C::kQ, u);
-                if (u < 32) {
-                    if (u < 8) {
-                        const uint32_t e = __float_as_uint(scales.y);
-                        sh.scales[n & 3][u] = CellScales{scales.x, (float)((int)(e >> 23) - 127), __uint_as_float((254u << 23) - e), 0.0f};
-                    }
-                    const bool gaps = __any_sync(~0u, u < 8 && scales.x < 0.0f);
-                    __syncwarp();
-                    if (u == 0) {
-                        sh.gaps[n & 3] = gaps;
-                        kv4_arrive(smem_addr(&sh.scales_full[n & 3]));
-                    }
-                }
-                fence_proxy_async_smem();
-                kv4_arrive(smem_addr(&sh.k_full[st]));
-            }
-            uint64_t where = 0;
+        uint32_t n = 0;  // blocks asked for
+        int left = 0;    // tokens of the last one's sequence from its first on
+        float by = 0.0f; // lane z < 8: its cell z's factor of V
+        walk([&](uint64_t where, const Piece &w, int b, float2 scales, bool more) {
             if (more) {
-                if (page >= 0 && page < c.n_pages)
-                    where = (uint64_t)(c.pool + kv8_head_offset<D>(c, page, a.layer, w.head) +
-                                       (cell & ((1 << in_page) - 1)) * Kv8Cell<D>::kBytes);
-                else if (inside && u < 8)
-                    kv4_bad(c);
-                scales = where ? __ldg((const float2 *)((const uint8_t *)where + Kv8Cell<D>::kScales)) : make_float2(-1.0f, 1.0f);
-                load_k<D>(rk, where, u);
-            }
-            if (n != ~0u) {
+                // its place was read when all had written block n - 2's V^T
                 if (n >= 2)
-                    wait(sh.v_empty[st], (n >> 1) - 1);
-                unpack_v<D>(rv, tiles + C::kOffV + st * C::kV, u, left);
+                    wait(sh.v_full[n & 1], (n >> 1) - 1);
+                copy_v<D>(where, c.pool, tiles + C::kOffRaw + (n & 1) * C::kK, u);
+                async_copies_arrive(smem_addr(&sh.raw_full[n & 1]));
+            }
+            if (n >= 1) {
+                const uint32_t st = (n - 1) & 1;
+                wait(sh.raw_full[st], (n - 1) >> 1);
+                if (n >= 3)
+                    wait(sh.v_empty[st], ((n - 1) >> 1) - 1);
+                unpack_v<D>(tiles + C::kOffRaw + st * C::kK, tiles + C::kOffV + st * C::kV, by, u, left);
                 fence_proxy_async_smem();
                 kv4_arrive(smem_addr(&sh.v_full[st]));
             }
-            if (!more)
-                break;
-            load_v<D>(rv, where, u);
-            left = w.len - (w.b0 + i) * kBlock;
+            left = w.len - b * kBlock;
+            by = scales.y * pow2_inverse(largest_of(scales.y));
             ++n;
-            if (++i == w.nblk) {
-                i = 0;
-                w = get_piece(++piece);
-                more = w.nblk > 0;
-            }
-        }
+        });
+        async_copies_wait(); // there are some in flight only after a wait that ran out
     } else {
         // one instruction for the warpgroup: its warps have to meet in the same one
         setmaxnreg_dec<kMmaRegs>();
@@ -837,6 +852,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                         break;
                 }
             }
+        } else if (warp > kMmaWarp + 1) {
+            // ---- K: two warps copy block n's codes and publish them ----
+            const int u = tid - (kMmaWarp + 2) * 32;
+            uint32_t n = 0;
+            walk([&](uint64_t where, const Piece &, int, float2 scales, bool more) {
+                if (!more)
+                    return;
+                const int st = n & 1;
+                if (n >= 2)
+                    wait(sh.k_empty[st], (n >> 1) - 1);
+                copy_k<D>(where, c.pool, tiles + C::kOffK + st * C::kK, u);
+                if (u < 32) {
+                    BlockScales &bs = sh.scales[n & 3];
+                    const float v = largest_of(scales.y);
+                    const uint32_t gaps = __ballot_sync(~0u, scales.x == 0.0f) & 0xFFu;
+                    if (u < 8)
+                        bs.k[u] = scales.x == 0.0f ? 1.0f : scales.x;
+                    __syncwarp();
+                    if (u == 0) {
+                        bs.ev = (float)((int)(__float_as_uint(v) >> 23) - 127);
+                        bs.iv = pow2_inverse(v);
+                        bs.gaps = gaps;
+                        kv4_arrive(smem_addr(&sh.scales_full[n & 3]));
+                    }
+                }
+                async_copies_wait();
+                fence_proxy_async_smem();
+                kv4_arrive(smem_addr(&sh.k_full[st]));
+                ++n;
+            });
         } else if (warp == kMmaWarp) {
             // ---- the MMAs: every lane follows, one issues ----
             const uint32_t one = elect();
@@ -845,14 +890,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
             uint32_t n = 0, n_p0 = 0, n_p1 = 0, n_q0 = 0, n_q1 = 0;
             const uint32_t desc0 = kDescLo | (tiles >> 4);
             const auto scores = [&](int k, int stage) { // S of tile k, K in `stage`
-                const uint32_t q = desc0 + k * (C::kQ >> 4), kk = desc0 + (C::kOffK >> 4) + stage * (C::kQ >> 4);
+                const uint32_t q = desc0 + k * (2 * C::kK >> 4), kk = desc0 + (C::kOffK >> 4) + stage * (C::kK >> 4);
                 const uint32_t d = tmem + k * 128;
 #pragma unroll
-                for (int g = 0; g < G; ++g)
+                for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_ss<128>(d, q + ((g * kSub + 32 * x) >> 4), kk + ((g * kSub + 32 * x) >> 4), kIdesc<128>, g + x,
-                                    one);
+                    for (int x = 0; x < D / 32; ++x)
+                        mma_ss_f8<D>(d, q + ((part * C::kK + 32 * x) >> 4), kk + ((32 * x) >> 4),
+                                     kIdesc<128> | (part ? kE5m2A : 0u), part + x, one);
                 commit(smem_addr(&sh.s_full[k]), one);
             };
             const auto values = [&](int k, int stage, uint32_t accumulate) { // O of tile k, V in `stage`

@@ -13,16 +13,16 @@
 // A CTA takes one token and kv head, or, of prompts, a tile of eight tokens of a sequence, whose
 // bounds it then reads once: eight lanes share a page, 16 bytes of each bound to a lane, four products to an
 // instruction. With few tokens and many pages the CTAs of a cluster share the pages and write the
-// scores to the first one's shared memory. There the want-th largest is found two bits at a time
-// (counts of three borders in a pass over the scores), and the pages above it, with the lowest of
-// those equal to it, are written in order.
+// scores to the first one's shared memory. There the want-th largest is found by counting the
+// scores in bins of their range (2048 bins, of a tile 256 for each token), then of the bin that it lies
+// in, until a bin is one number; the pages above it, with the lowest of those equal to it, are
+// written in order.
 #include "kv8.cuh"
 
 namespace nm {
 namespace {
 
 constexpr int kTile = 8;  // tokens of a tile of prompts
-constexpr int kAhead = 4; // pages whose bounds a group of lanes asks for together
 
 struct SelectArgs {
     int layer, ratio, want, first, last;
@@ -32,6 +32,10 @@ struct SelectArgs {
     int64_t units; // tiles (at most) times the kv heads
     int cluster;
 };
+
+// The two halves of cluster_sync, apart.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // An order of fp32 numbers as unsigned ones.
 __device__ __forceinline__ uint32_t key_of(float x)
@@ -124,103 +128,146 @@ template <int D> __device__ __forceinline__ Words<D> words_at(const void *p)
     return r;
 }
 
-// A group of W warps (the CTA, or one): sums of a thread's numbers over the group.
+// A group of W warps that chooses the pages of one query: the CTA, or a warp. Of few warps, since what takes
+// the time is the shuffles (with 32 warps to the CTA choosing took 8000 cycles).
 template <int W> struct Group {
-    uint32_t (*part)[2][32]; // (W > 1) two buffers in shared memory, used in turn
+    static constexpr int kThreads = 32 * W, kEach = 8, kBins = kThreads * kEach, kBits = W == 1 ? 8 : 11;
+    static_assert(kBins == 1 << kBits, "bins");
+    uint32_t *bins;   // [kBins] of shared memory
+    uint32_t *parts;  // [2][32]: the warps' sums, in turn
+    uint32_t *found;  // [2]
     int turn = 0;
     __device__ int thread() const { return W == 1 ? threadIdx.x & 31 : threadIdx.x; }
-    __device__ void sums(uint32_t &x, uint32_t &y)
+    __device__ void sync()
     {
-        x = __reduce_add_sync(~0u, x);
-        y = __reduce_add_sync(~0u, y);
         if (W == 1)
-            return;
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        if (lane == 0) {
-            part[turn][0][warp] = x;
-            part[turn][1][warp] = y;
-        }
-        __syncthreads();
-        x = __reduce_add_sync(~0u, lane < W ? part[turn][0][lane] : 0u);
-        y = __reduce_add_sync(~0u, lane < W ? part[turn][1][lane] : 0u);
-        turn ^= 1;
+            __syncwarp();
+        else
+            __syncthreads();
     }
-    // Sum over the threads before this one, and over all.
-    __device__ uint32_t scan(uint32_t x, uint32_t *total)
+    // Sum over the threads before this one, and over all; x is the warp's scan already (its lanes up to this one).
+    __device__ uint32_t before(uint32_t upto, uint32_t x, uint32_t *total)
     {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        uint32_t y = x;
+        if (W == 1) {
+            *total = __shfl_sync(~0u, upto, 31);
+            return upto - x;
+        }
+        uint32_t *const part = parts + 32 * turn;
+        turn ^= 1;
+        if (lane == 31)
+            part[warp] = upto;
+        __syncthreads();
+        const uint32_t all = scan32(lane < W ? part[lane] : 0u);
+        *total = __shfl_sync(~0u, all, 31);
+        const uint32_t prior = __shfl_sync(~0u, all, warp > 0 ? warp - 1 : 0);
+        return (warp > 0 ? prior : 0u) + upto - x;
+    }
+    static __device__ uint32_t scan32(uint32_t x)
+    {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t z = __shfl_up_sync(~0u, y, o);
-            if (lane >= o)
-                y += z;
+            const uint32_t z = __shfl_up_sync(~0u, x, o);
+            if ((int)(threadIdx.x & 31) >= o)
+                x += z;
         }
-        if (W == 1) {
-            *total = __shfl_sync(~0u, y, 31);
-            return y - x;
-        }
-        if (lane == 31)
-            part[turn][0][warp] = y;
-        __syncthreads();
-        const uint32_t s = lane < W ? part[turn][0][lane] : 0u;
-        *total = __reduce_add_sync(~0u, s);
-        const uint32_t before = __reduce_add_sync(~0u, lane < warp ? s : 0u);
-        turn ^= 1;
-        return before + y - x;
+        return x;
     }
 };
 
-// The list of one query: the first and last pages, and of the others those with the largest keys.
-template <int W> __device__ __forceinline__ void choose(const SelectArgs &a, Group<W> &g, const uint32_t *keys, int count, int32_t *out)
+// The least and the greatest over a warp.
+__device__ __forceinline__ void range_of(uint32_t &least, uint32_t &most)
 {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        least = min(least, __shfl_xor_sync(~0u, least, o));
+        most = max(most, __shfl_xor_sync(~0u, most, o));
+    }
+}
+
+// The list of one query: the first and last pages, and of the others those with the largest keys, which are
+// within least .. most.
+template <int W>
+__device__ __forceinline__ void choose(const SelectArgs &a, Group<W> &g, const uint32_t *keys, int count, uint32_t least,
+                                       uint32_t most, int32_t *out)
+{
+    using G = Group<W>;
     const int me = g.thread();
-    constexpr int kThreads = 32 * W;
     if (count <= a.want) {
-        for (int j = me; j < a.want; j += kThreads)
+        for (int j = me; j < a.want; j += G::kThreads)
             out[j] = j < count ? j : -1;
         return;
     }
     const int lo = a.first, hi = count - a.last; // the others: lo < hi, since first + last <= want < count
-    const uint32_t need = (uint32_t)(a.want - a.first - a.last);
-    // the largest border with at least `need` keys at or above it
-    uint32_t border = need ? 0u : ~0u, above = 0; // above: keys over it
-    if (need) {
-#pragma unroll 1
-        for (int bit = 30; bit >= 0; bit -= 2) {
-            const uint32_t step = 1u << bit;
-            uint32_t n12 = 0, n3 = 0; // counts of at most 2^16 - 1
-            for (int z = lo + me; z < hi; z += kThreads) {
-                const uint32_t k = keys[z];
-                n12 += (k >= border + step ? 1u : 0u) + (k >= border + 2 * step ? 65536u : 0u);
-                n3 += k >= border + 3 * step ? 1u : 0u;
-            }
-            g.sums(n12, n3);
-            const uint32_t n1 = n12 & 0xFFFFu, n2 = n12 >> 16;
-            if (n3 >= need)
-                border += 3 * step;
-            else if (n2 >= need)
-                border += 2 * step, above = n3;
-            else if (n1 >= need)
-                border += step, above = n2;
-            else
-                above = n1;
+    uint32_t need = (uint32_t)(a.want - a.first - a.last); // of the keys within the border's bin still to take
+    // each thread's keys lie side by side, four to a load
+    const int per = ((count + G::kThreads - 1) / G::kThreads + 3) / 4 * 4;
+    const int from = min(me * per, count), to = min(from + per, count);
+    const auto each = [&](const auto &f) {
+        for (int z = from; z < to; z += 4) {
+            const uint4 k = *(const uint4 *)(keys + z);
+            f(z, k.x);
+            f(z + 1, k.y);
+            f(z + 2, k.z);
+            f(z + 3, k.w);
         }
+    };
+    // The border: keys above it are taken, and of those equal to it the lowest pages. The range of
+    // the keys is divided into bins, then the bin that the need-th largest lies in, until a bin is one number.
+    uint32_t border = ~0u;
+    if (need) {
+        uint32_t width = most - least; // the keys in question: least .. least + width
+#pragma unroll 1
+        while (width) {
+            const int shift = max(0, 32 - __clz(width) - G::kBits);
+            uint4 *const mine = (uint4 *)(g.bins + 8 * (G::kThreads - 1 - me)); // thread 0 has the largest
+            mine[0] = mine[1] = make_uint4(0, 0, 0, 0);
+            g.sync();
+            each([&](int z, uint32_t k) {
+                if (z >= lo && z < hi && k - least <= width)
+                    atomicAdd(g.bins + ((k - least) >> shift), 1u);
+            });
+            g.sync();
+            const uint4 x = mine[1], y = mine[0];
+            const uint32_t n[8] = {x.w, x.z, x.y, x.x, y.w, y.z, y.y, y.x};
+            const uint32_t sum = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
+            uint32_t total, above = g.before(G::scan32(sum), sum, &total);
+            if (above < need && above + sum >= need) {
+                int b = 0;
+                bool there = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    there = there || above + n[i] >= need;
+                    above += there ? 0 : n[i];
+                    b += there ? 0 : 1;
+                }
+                g.found[0] = (uint32_t)(8 * (G::kThreads - 1 - me) + 7 - b);
+                g.found[1] = need - above;
+            }
+            g.sync();
+            const uint32_t bin = g.found[0] << shift;
+            need = g.found[1];
+            least += bin;
+            width = min(width - bin, (1u << shift) - 1);
+        }
+        border = least;
     }
-    const uint32_t ties = need - above; // of the keys equal to the border, the lowest pages
-    uint32_t done = 0;                  // above the border, and (times 65536) equal to it
-    for (int z0 = 0; z0 < count; z0 += kThreads) {
-        const int z = z0 + me;
-        const bool forced = z < lo || (z >= hi && z < count), other = z >= lo && z < hi;
-        const uint32_t k = other ? keys[z] : 0u;
-        const bool over = forced || (other && need && k > border), tie = other && need && k == border;
-        uint32_t total;
-        const uint32_t before = done + g.scan((over ? 1u : 0u) + (tie ? 65536u : 0u), &total);
-        const uint32_t n_over = before & 0xFFFFu, n_tie = before >> 16;
-        if (over || (tie && n_tie < ties))
-            out[n_over + (n_tie < ties ? n_tie : ties)] = z;
-        done += total;
-    }
+    const auto is_over = [&](int z, uint32_t k) {
+        return z < count && (z < lo || z >= hi || (need && k > border));
+    };
+    const auto is_tie = [&](int z, uint32_t k) { return z >= lo && z < hi && need && k == border; };
+    uint32_t mine = 0, total; // keys above the border, and (times 65536) equal to it
+    each([&](int z, uint32_t k) { mine += is_over(z, k) ? 1u : is_tie(z, k) ? 65536u : 0u; });
+    const uint32_t before = g.before(G::scan32(mine), mine, &total);
+    uint32_t n_over = before & 0xFFFFu, n_tie = before >> 16;
+    if (mine)
+        each([&](int z, uint32_t k) {
+            const bool over = is_over(z, k), tie = is_tie(z, k);
+            if (over || (tie && n_tie < need))
+                out[n_over + min(n_tie, need)] = z;
+            n_over += over;
+            n_tie += tie;
+        });
 }
 
 // T tokens of a sequence and one kv head; W warps choose the pages of one token.
@@ -230,10 +277,17 @@ __global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const 
     constexpr int kThreads = T == 1 ? 32 * W : 32 * T;
     extern __shared__ __align__(16) uint32_t keys[]; // [T][the table's width]
     __shared__ __align__(16) int8_t sq[T][2][D];
-    __shared__ uint32_t parts[2][2][32];
+    constexpr int kGroups = T == 1 ? 1 : T;
+    __shared__ __align__(16) uint32_t bins[kGroups * Group<T == 1 ? W : 1>::kBins];
+    __shared__ uint32_t parts[64], found[kGroups][2];
+    // the ranges of the keys that the warps scored: of every CTA's of a cluster (in its first CTA), or of each token
+    constexpr int kWarps = kThreads / 32, kRanges = T == 1 ? 8 * kWarps : kWarps * T;
+    __shared__ uint32_t ranges[kRanges][2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t unit = blockIdx.x / a.cluster;
     const int rank = (int)(blockIdx.x - unit * a.cluster);
+    if (a.cluster > 1)
+        cluster_arrive();
 
     if (b.starts) { // rows that belong to no sequence: no pages
         bool rest = !kv4_ends(b);
@@ -264,6 +318,8 @@ __global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const 
         i = lo;
         nth = (int)(slot - ((int64_t)(b.starts[i] / T) + i));
     }
+    if (a.cluster > 1)
+        cluster_wait(); // the first CTA's shared memory is there from here on
     if (unit >= a.units || i >= b.n_seqs || nth < 0)
         return; // with the whole cluster
     const Kv4Seq s = kv4_seq(c, b, i, !b.starts && head == 0 && rank == 0 && tid == 0);
@@ -275,40 +331,26 @@ __global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const 
         return pos < 0 ? 0 : (pos >> c.page_shift) + 1;
     };
     const int most = count_of(nt - 1);
-    const int width = c.max_pages;
+    const int width = (c.max_pages + 3) / 4 * 4;
 
     if (most > a.want) {
-        if (warp < nt)
-            query_sums<D>(a, a.q + (int64_t)(s.first + t0 + warp) * a.q_stride + (int64_t)head * a.ratio * D, sq[warp % T][0],
-                          sq[warp % T][1]);
-        __syncthreads();
-        const int n = lane & 7, group = tid >> 3;
-        Words<D> up[T], down[T];
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            up[t] = words_at<D>(&sq[t][0][n * (D / 8)]);
-            down[t] = words_at<D>(&sq[t][1][n * (D / 8)]);
-        }
-        // pages up to the last query's own (which needs no score) are full
+        // Pages up to the last query's own (which needs no score) are full. A group of eight lanes
+        // asks for the bounds of kAhead of them together, the first ones before the queries' sums.
+        constexpr int kAhead = T == 1 ? 8 : 4, kStride = kThreads / 8;
         const int per = (most - 1 + a.cluster - 1) / a.cluster;
         const int z0 = rank * per, z1 = min(most - 1, z0 + per);
-        const uint8_t *const tails = c.pool + kv8_head_offset<D>(c, 0, a.layer, head) + ((int64_t)Kv8Cell<D>::kBytes << (c.page_shift - 4));
-        uint32_t to = smem_addr(keys);
-        if (a.cluster > 1) {
-            to = cluster_map(to, 0);
-            cluster_sync(); // the first CTA's shared memory is there from here on
-        }
-#pragma unroll 1
-        for (int z = z0 + group; z - group < z1; z += kAhead * (kThreads / 8)) {
-            Words<D> hi[kAhead], lo[kAhead];
-            float step[kAhead];
-            const uint8_t *at[kAhead];
+        const int n = lane & 7, group = tid >> 3;
+        const uint8_t *const tails = c.pool + kv8_head_offset<D>(c, 0, a.layer, head) +
+                                     ((int64_t)Kv8Cell<D>::kBytes << (c.page_shift - 4)) + n * (D / 8);
+        Words<D> hi[kAhead], lo[kAhead];
+        float step[kAhead];
+        const auto ask = [&](int z) {
+            int page[kAhead];
 #pragma unroll
             for (int x = 0; x < kAhead; ++x) {
-                const int zx = z + x * (kThreads / 8);
-                const int page = zx < z1 ? kv4_page(c, s.row, zx) : -1;
-                at[x] = page < 0 ? nullptr : tails + page * c.page_bytes;
-                if (zx < z1 && page < 0)
+                const bool in = z + x * kStride < z1;
+                page[x] = in ? kv4_page(c, s.row, z + x * kStride) : -1;
+                if (in && page[x] < 0)
                     kv4_bad(c);
             }
 #pragma unroll
@@ -316,12 +358,35 @@ __global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const 
                 hi[x] = Words<D>{};
                 lo[x] = Words<D>{};
                 step[x] = -INFINITY; // a page that is none of the pool's is the last choice
-                if (at[x]) {
-                    hi[x] = words_at<D>(at[x] + n * (D / 8));
-                    lo[x] = words_at<D>(at[x] + Kv8Cell<D>::kLower + n * (D / 8));
-                    step[x] = *(const float *)(at[x] + Kv8Cell<D>::kStep);
+                if (page[x] >= 0) {
+                    const uint8_t *const at = tails + page[x] * c.page_bytes;
+                    hi[x] = words_at<D>(at);
+                    lo[x] = words_at<D>(at + Kv8Cell<D>::kLower);
+                    step[x] = *(const float *)(at + Kv8Cell<D>::kStep - n * (D / 8));
                 }
             }
+        };
+        ask(z0 + group);
+        if (warp < nt)
+            query_sums<D>(a, a.q + (int64_t)(s.first + t0 + warp) * a.q_stride + (int64_t)head * a.ratio * D, sq[warp % T][0],
+                          sq[warp % T][1]);
+        __syncthreads();
+        Words<D> up[T], down[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            up[t] = words_at<D>(&sq[t][0][n * (D / 8)]);
+            down[t] = words_at<D>(&sq[t][1][n * (D / 8)]);
+        }
+        uint32_t to = smem_addr(keys), to_range = smem_addr(ranges);
+        if (a.cluster > 1) {
+            to = cluster_map(to, 0);
+            to_range = cluster_map(to_range, 0);
+        }
+        uint32_t least = ~0u, largest = 0;
+#pragma unroll 1
+        for (int z = z0 + group; z - group < z1; z += kAhead * kStride) {
+            if (z != z0 + group)
+                ask(z);
 #pragma unroll
             for (int x = 0; x < kAhead; ++x) {
                 int sum[8];
@@ -340,12 +405,25 @@ __global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const 
                 } else {
                     mine = sum_across(sum, n);
                 }
-                const int zx = z + x * (kThreads / 8);
+                const int zx = z + x * kStride;
                 if (zx < z1 && n < T) {
-                    const uint32_t key = key_of(at[x] ? (float)mine * step[x] : -INFINITY);
+                    const uint32_t key = key_of(step[x] == -INFINITY ? -INFINITY : (float)mine * step[x]);
                     st_cluster_f32(to + 4 * (n * width + zx), __uint_as_float(key));
+                    least = min(least, key);
+                    largest = max(largest, key);
                 }
             }
+        }
+        // over the four groups of a warp (each lane of a group has a token's, or the first has all)
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+            least = min(least, __shfl_xor_sync(~0u, least, o));
+            largest = max(largest, __shfl_xor_sync(~0u, largest, o));
+        }
+        if (lane < T) {
+            const uint32_t at = to_range + 8 * (T == 1 ? rank * kWarps + warp : warp * T + lane);
+            st_cluster_f32(at, __uint_as_float(least));
+            st_cluster_f32(at + 4, __uint_as_float(largest));
         }
     }
     if (a.cluster > 1) {
@@ -357,11 +435,25 @@ __global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const 
     }
     const auto out_of = [&](int t) { return a.pages + ((int64_t)(s.first + t0 + t) * c.n_kv_heads + head) * a.want; };
     if (T == 1) {
-        Group<W> g{parts};
-        choose(a, g, keys, most, out_of(0));
+        Group<W> g{bins, parts, found[0]};
+        uint32_t least = ~0u, largest = 0;
+        if (most > a.want) {
+            for (int x = lane; x < a.cluster * kWarps; x += 32) {
+                least = min(least, ranges[x][0]);
+                largest = max(largest, ranges[x][1]);
+            }
+            range_of(least, largest);
+        }
+        choose(a, g, keys, most, least, largest, out_of(0));
     } else if (warp < nt) {
-        Group<1> g{parts};
-        choose(a, g, keys + warp * width, count_of(warp), out_of(warp));
+        Group<1> g{bins + warp % kGroups * Group<1>::kBins, nullptr, found[warp % kGroups]};
+        uint32_t least = ~0u, largest = 0;
+        if (most > a.want && lane < kWarps) {
+            least = ranges[(lane % kWarps) * T + warp % T][0];
+            largest = ranges[(lane % kWarps) * T + warp % T][1];
+        }
+        range_of(least, largest);
+        choose(a, g, keys + warp * width, count_of(warp), least, largest, out_of(warp));
     }
 }
 
@@ -384,7 +476,7 @@ nm_status launch(const Kv4 &c, const Kv4Batch &b, SelectArgs a, int cluster, con
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(T == 1 ? 32 * W : 32 * T);
-    cfg.dynamicSmemBytes = (size_t)T * c.max_pages * 4;
+    cfg.dynamicSmemBytes = (size_t)T * ((c.max_pages + 3) / 4 * 4) * 4;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -401,12 +493,12 @@ nm_status kv8_launch_select(const Kv4 &c, const Kv4Batch &b, const Kv8Select &x,
 {
     const SelectArgs a{x.layer, x.n_q_heads / c.n_kv_heads, x.count, x.first, x.last, (const uint16_t *)x.q, x.q_stride, x.pages, 0, 1};
     // tiles of tokens when there are several for each SM, and their scores fit
-    if (b.starts && b.n_tokens * c.n_kv_heads >= 4 * (int64_t)w.num_sms && (int64_t)kTile * c.max_pages <= kKv8SelectPages)
+    if (b.starts && b.n_tokens * c.n_kv_heads >= 4 * (int64_t)w.num_sms && (int64_t)kTile * (c.max_pages + 3) <= kKv8SelectPages)
         return c.head_dim == 128 ? launch<128, kTile, 1>(c, b, a, 1, w, st) : launch<64, kTile, 1>(c, b, a, 1, w, st);
     int cluster = 1;
     while (cluster < 8 && 2 * cluster * b.n_tokens * c.n_kv_heads <= w.num_sms && c.max_pages >= 256 * cluster)
         cluster *= 2;
-    return c.head_dim == 128 ? launch<128, 1, 32>(c, b, a, cluster, w, st) : launch<64, 1, 32>(c, b, a, cluster, w, st);
+    return c.head_dim == 128 ? launch<128, 1, 8>(c, b, a, cluster, w, st) : launch<64, 1, 8>(c, b, a, cluster, w, st);
 }
 
 } // namespace nm

@@ -87,10 +87,10 @@ __device__ __forceinline__ void commit(uint32_t bar, uint32_t one)
                  : "memory");
 }
 // Shared-memory descriptor of a K-major tile with rows of SW bytes under the
-// SW-byte swizzle, 8-row groups 8 SW bytes apart (layout type 2: 128 bytes, 6: 32):
+// SW-byte swizzle, 8-row groups 8 SW bytes apart (layout type 2: 128 bytes, 4: 64, 6: 32):
 // its high word, and its low word without the address (in 16-byte units).
 template <int SW>
-constexpr uint32_t kDescHi = ((8 * SW) >> 4) | (1u << 14) | ((SW == 128 ? 2u : SW == 32 ? 6u : 8u) << 29);
+constexpr uint32_t kDescHi = ((8 * SW) >> 4) | (1u << 14) | ((SW == 128 ? 2u : SW == 64 ? 4u : 6u) << 29);
 constexpr uint32_t kDescLo = 1u << 16;
 
 // D (tensor memory) (+)= A (shared memory) B (shared memory)^T; a, b: the low words
@@ -101,6 +101,18 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint3
     asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %6, 0;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
                  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi<SW>), "r"(one)
+                 : "memory");
+}
+// The same of 8-bit floats: e4m3, or with kE5m2A in the descriptor A e5m2.
+constexpr uint32_t kE5m2A = 1u << 7;
+template <int SW>
+__device__ __forceinline__ void mma_ss_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                          uint32_t one)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %6, 0;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}" ::"r"(d),
                  "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi<SW>), "r"(one)
                  : "memory");
 }
@@ -185,8 +197,19 @@ template <int N> __device__ __forceinline__ void setmaxnreg_dec()
 {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// kind::f16, A and B fp16 and K-major, D fp32, M = 128.
+// kind::f16, A and B fp16 and K-major, D fp32, M = 128; the same bits say e4m3 in kind::f8f6f4.
 template <int N> constexpr uint32_t kIdesc = (1u << 4) | ((N >> 3) << 17) | ((128 >> 4) << 24);
+
+// 16 bytes to shared memory in the background (zeros if there is no source); done: all of this thread's arrive.
+__device__ __forceinline__ void async_copy16(uint32_t dst, const void *src, bool have)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void async_copies_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void async_copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
