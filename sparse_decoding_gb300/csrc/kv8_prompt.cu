@@ -41,8 +41,7 @@ namespace {
 
 constexpr int kSoft = 256;      // softmax threads: two tiles of 128 rows
 constexpr int kUnpack = 128;    // unpacking threads
-constexpr int kMmaWarp = 12;    // of its warpgroup, the next one lists the pieces and two copy K
-constexpr int kLoad = 64;       // the threads of those
+constexpr int kMmaWarp = 12;    // of its warpgroup, the next one lists the pieces and two idle
 constexpr int kThreads = 512;
 // Registers of a thread: at launch (what 512 threads can have), and in each role.
 constexpr int kLaunchRegs = 128, kSoftRegs = 184, kUnpackRegs = 104, kMmaRegs = 40;
@@ -84,29 +83,22 @@ __device__ __forceinline__ float largest_of(float v)
 }
 __device__ __forceinline__ float pow2_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
-// Codes of a block go to shared memory 16 bytes at a time: K to its rows, by 64 threads; V as they
-// are, by 128, where piece (cell, four channels, t) is the t ^ (cell % 4)th of its four.
-// where: lane z < 8's, the address of cell z (0: it is not there, and reads as zeros).
-template <int D> __device__ __forceinline__ void copy_k(uint64_t where, const void *pool, uint32_t ks, int u)
+// The codes of a block go to shared memory 16 bytes at a time: K to its rows, V as they are, where piece
+// (cell, four channels, t) is the t ^ (cell % 4)th of its four. where: lane z < 8's, the address of cell z
+// (0: it is not there, and reads as zeros).
+template <int D> __device__ __forceinline__ void copy_block(uint64_t where, const void *pool, uint32_t ks, uint32_t raw, int u)
 {
-    // piece [2 halves][D / 64][8 tokens][4] of a cell, in order
-    const int g = (u >> 2) & 7, c = D == 128 ? ((u >> 5) & 1) * 4 + (u & 3) : u & 3, row = D == 128 ? g : (u >> 5) * 8 + g;
-    const uint32_t dst = ks + row * D + Cfg<D>::piece(row, c);
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-        const uint64_t cell = __shfl_sync(~0u, where, i / (D / 64));
-        async_copy16(dst + i * 1024, cell ? (const uint8_t *)cell + (i % (D / 64)) * 1024 + u * 16 : pool, cell != 0);
-    }
-}
-template <int D> __device__ __forceinline__ void copy_v(uint64_t where, const void *pool, uint32_t raw, int u)
-{
+    // of K piece [2 halves][D / 64][8 tokens][4] of a cell, of V piece [D / 4][4]; at D = 64 two cells at once
     const int first = D == 128 ? 0 : u >> 6, piece = u & (D - 1);
-#pragma unroll 4
+    const int g = (piece >> 2) & 7, c = D == 128 ? ((piece >> 5) & 1) * 4 + (piece & 3) : piece & 3, row = (piece / (D / 2)) * 8 + g;
+    const uint32_t to_k = ks + row * D + Cfg<D>::piece(row, c), to_v = raw + (piece >> 2) * 64;
+#pragma unroll 2
     for (int i = 0; i < D / 16; ++i) {
         const int z = D == 128 ? i : 2 * i + first;
         const uint64_t cell = __shfl_sync(~0u, where, z);
-        async_copy16(raw + z * 16 * D + (piece >> 2) * 64 + (((piece & 3) ^ (z & 3)) << 4),
-                     cell ? (const uint8_t *)cell + Kv8Cell<D>::kV + piece * 16 : pool, cell != 0);
+        const uint8_t *const from = cell ? (const uint8_t *)cell + piece * 16 : (const uint8_t *)pool;
+        async_copy16(to_k + z * 16 * D, from, cell != 0);
+        async_copy16(to_v + z * 16 * D + (((piece & 3) ^ (z & 3)) << 4), cell ? from + Kv8Cell<D>::kV : from, cell != 0);
     }
 }
 // V^T as fp16 from V's codes: a thread takes four channels of a cell at a time, 16 tokens of each.
@@ -331,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sh.k_full[i]), kLoad);
+            mbar_init(smem_addr(&sh.k_full[i]), kUnpack);
             mbar_init(smem_addr(&sh.raw_full[i]), kUnpack);
             mbar_init(smem_addr(&sh.v_full[i]), kUnpack);
             mbar_init(smem_addr(&sh.k_empty[i]), 1);
@@ -346,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
             mbar_init(smem_addr(&sh.scales_full[i]), 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_addr(&sh.piece_full[i]), 1);
-            mbar_init(smem_addr(&sh.piece_empty[i]), kMmaWarp + 3); // a lane of each warp that takes pieces
+            mbar_init(smem_addr(&sh.piece_empty[i]), kMmaWarp + 1); // a lane of each warp that takes pieces
         }
         fence_mbar_init();
     }
@@ -459,41 +451,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
         if (lane == 0)
             kv4_arrive(smem_addr(&sh.piece_empty[p % kRing]));
         return w;
-    };
-
-    // f(addresses of the cells, piece, block, scales of the cells, more) for the blocks of all pieces, and
-    // once more without one, for a whole warp: lane z < 8's cell z (0: it is not there, and its scales are 0).
-    // The pages of a block are asked for before the block ahead of it is worked on.
-    const auto walk = [&](const auto &f) {
-        const int in_page = c.page_shift - 4;
-        uint32_t piece = 0;
-        Piece w{};
-        int i = -1, page = -2;
-        bool more;
-#pragma unroll 1
-        do {
-            const Piece now = w;
-            const int b = w.b0 + i, cell = b * 8 + (lane & 7);
-            more = i >= 0 && w.nblk > 0;
-            uint64_t where = 0;
-            if (page >= 0 && page < c.n_pages)
-                where = (uint64_t)(c.pool + kv8_head_offset<D>(c, page, a.layer, w.head) +
-                                   (cell & ((1 << in_page) - 1)) * Kv8Cell<D>::kBytes);
-            else if (page != -2 && tid < kSoft + 8)
-                kv4_bad(c);
-            const float2 scales =
-                where ? __ldg((const float2 *)((const uint8_t *)where + Kv8Cell<D>::kScales)) : make_float2(0.0f, 0.0f);
-            if (++i == w.nblk) { // at first there is no piece
-                i = 0;
-                w = get_piece(piece++);
-            }
-            page = -2; // nothing to find
-            const int next = (w.b0 + i) * 8 + (lane & 7);
-            if (w.nblk > 0 && next * kKv4Cell < w.len)
-                page = max(c.tables[(int64_t)w.row * c.max_pages + (next >> in_page)], -1);
-            if (more || w.nblk == 0)
-                f(where, now, b, scales, more);
-        } while (w.nblk > 0 || more);
     };
 
     if (warp < 8) {
@@ -695,15 +652,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                     ld32(t_s + 32 * h, r);
                     wait_ld();
                     tie<32>(r);
-                    if (masked) {
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const int end = gaps >> (2 * h + z) & 1u ? 0 : vis - 32 * h - 16 * z;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                r[16 * z + e] = e < end ? r[16 * z + e] : 0xFF800000u;
-                        }
-                    }
                 };
                 // S is read twice, 32 columns at a time: for the maximum, which is raised when a score passes
                 // it by more than the slack, and for the weights. Loops, so that the code stays in the
@@ -712,6 +660,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     read(h);
+                    if (masked) { // once: they are written back
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const int end = gaps >> (2 * h + z) & 1u ? 0 : vis - 32 * h - 16 * z;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                r[16 * z + e] = e < end ? r[16 * z + e] : 0xFF800000u;
+                            st16(t_s + 32 * h + 16 * z, r + 16 * z);
+                        }
+                        wait_st();
+                    }
                     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
@@ -769,32 +728,79 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
         }
     } else if (warp < kMmaWarp) {
         setmaxnreg_dec<kUnpackRegs>();
-        // ---- V^T: block n's codes are asked for while block n - 1's become fp16 ----
+        // ---- the codes: block n's are asked for, and block n - 1's V^T made, a round ----
         const int u = tid - kSoft;
-        uint32_t n = 0;  // blocks asked for
+        const int in_page = c.page_shift - 4;
+        uint32_t piece = 0, n = 0; // n: blocks asked for
+        Piece w{};
+        int i = -1, page = -2; // the block to ask for next, and its pages (lane z < 8's: that of cell z; -2: none)
         int left = 0;    // tokens of the last one's sequence from its first on
         float by = 0.0f; // lane z < 8: its cell z's factor of V
-        walk([&](uint64_t where, const Piece &w, int b, float2 scales, bool more) {
+        bool more;
+#pragma unroll 1
+        do {
+            more = w.nblk > 0 && i >= 0;
+            uint64_t where = 0;
+            if (page >= 0 && page < c.n_pages)
+                where = (uint64_t)(c.pool + kv8_head_offset<D>(c, page, a.layer, w.head) +
+                                   (((w.b0 + i) * 8 + (lane & 7)) & ((1 << in_page) - 1)) * Kv8Cell<D>::kBytes);
+            else if (page != -2 && u < 8)
+                kv4_bad(c);
+            // 0: the cell is not there
+            const float2 scales =
+                where ? __ldg((const float2 *)((const uint8_t *)where + Kv8Cell<D>::kScales)) : make_float2(0.0f, 0.0f);
+            const int now_left = w.len - (w.b0 + i) * kBlock;
+            // the pages of the next block are asked for before this one is worked on
+            if (++i == w.nblk) { // at first there is no piece
+                i = 0;
+                w = get_piece(piece++);
+            }
+            page = -2;
+            const int next = (w.b0 + i) * 8 + (lane & 7);
+            if (w.nblk > 0 && next * kKv4Cell < w.len)
+                page = max(c.tables[(int64_t)w.row * c.max_pages + (next >> in_page)], -1);
+            const uint32_t st = n & 1;
+            float next_by = 0.0f;
             if (more) {
-                // its place was read when all had written block n - 2's V^T
-                if (n >= 2)
-                    wait(sh.v_full[n & 1], (n >> 1) - 1);
-                copy_v<D>(where, c.pool, tiles + C::kOffRaw + (n & 1) * C::kK, u);
-                async_copies_arrive(smem_addr(&sh.raw_full[n & 1]));
+                // K's place is free when S has been computed of block n - 2, V's when all have made its V^T
+                if (n >= 2) {
+                    wait(sh.k_empty[st], (n >> 1) - 1);
+                    wait(sh.v_full[st], (n >> 1) - 1);
+                }
+                copy_block<D>(where, c.pool, tiles + C::kOffK + st * C::kK, tiles + C::kOffRaw + st * C::kK, u);
+                async_copies_arrive(smem_addr(&sh.k_full[st]));
+                async_copies_arrive(smem_addr(&sh.raw_full[st]));
+                const float v = largest_of(scales.y);
+                if (u < 32) {
+                    BlockScales &bs = sh.scales[n & 3];
+                    const uint32_t gaps = __ballot_sync(~0u, scales.x == 0.0f) & 0xFFu;
+                    if (u < 8)
+                        bs.k[u] = scales.x == 0.0f ? 1.0f : scales.x;
+                    __syncwarp();
+                    if (u == 0) {
+                        bs.ev = (float)((int)(__float_as_uint(v) >> 23) - 127);
+                        bs.iv = pow2_inverse(v);
+                        bs.gaps = gaps;
+                        kv4_arrive(smem_addr(&sh.scales_full[n & 3]));
+                    }
+                }
+                next_by = scales.y * pow2_inverse(v);
             }
-            if (n >= 1) {
-                const uint32_t st = (n - 1) & 1;
-                wait(sh.raw_full[st], (n - 1) >> 1);
+            if (n >= 1 && (more || w.nblk == 0)) {
+                const uint32_t was = st ^ 1;
+                wait(sh.raw_full[was], (n - 1) >> 1);
                 if (n >= 3)
-                    wait(sh.v_empty[st], ((n - 1) >> 1) - 1);
-                unpack_v<D>(tiles + C::kOffRaw + st * C::kK, tiles + C::kOffV + st * C::kV, by, u, left);
+                    wait(sh.v_empty[was], ((n - 1) >> 1) - 1);
+                unpack_v<D>(tiles + C::kOffRaw + was * C::kK, tiles + C::kOffV + was * C::kV, by, u, left);
                 fence_proxy_async_smem();
-                kv4_arrive(smem_addr(&sh.v_full[st]));
+                kv4_arrive(smem_addr(&sh.v_full[was]));
             }
-            left = w.len - b * kBlock;
-            by = scales.y * pow2_inverse(largest_of(scales.y));
-            ++n;
-        });
+            if (more) {
+                by = next_by;
+                left = now_left;
+                ++n;
+            }
+        } while (w.nblk > 0 || more);
         async_copies_wait(); // there are some in flight only after a wait that ran out
     } else {
         // one instruction for the warpgroup: its warps have to meet in the same one
@@ -852,36 +858,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                         break;
                 }
             }
-        } else if (warp > kMmaWarp + 1) {
-            // ---- K: two warps copy block n's codes and publish them ----
-            const int u = tid - (kMmaWarp + 2) * 32;
-            uint32_t n = 0;
-            walk([&](uint64_t where, const Piece &, int, float2 scales, bool more) {
-                if (!more)
-                    return;
-                const int st = n & 1;
-                if (n >= 2)
-                    wait(sh.k_empty[st], (n >> 1) - 1);
-                copy_k<D>(where, c.pool, tiles + C::kOffK + st * C::kK, u);
-                if (u < 32) {
-                    BlockScales &bs = sh.scales[n & 3];
-                    const float v = largest_of(scales.y);
-                    const uint32_t gaps = __ballot_sync(~0u, scales.x == 0.0f) & 0xFFu;
-                    if (u < 8)
-                        bs.k[u] = scales.x == 0.0f ? 1.0f : scales.x;
-                    __syncwarp();
-                    if (u == 0) {
-                        bs.ev = (float)((int)(__float_as_uint(v) >> 23) - 127);
-                        bs.iv = pow2_inverse(v);
-                        bs.gaps = gaps;
-                        kv4_arrive(smem_addr(&sh.scales_full[n & 3]));
-                    }
-                }
-                async_copies_wait();
-                fence_proxy_async_smem();
-                kv4_arrive(smem_addr(&sh.k_full[st]));
-                ++n;
-            });
         } else if (warp == kMmaWarp) {
             // ---- the MMAs: every lane follows, one issues ----
             const uint32_t one = elect();
@@ -892,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
             const auto scores = [&](int k, int stage) { // S of tile k, K in `stage`
                 const uint32_t q = desc0 + k * (2 * C::kK >> 4), kk = desc0 + (C::kOffK >> 4) + stage * (C::kK >> 4);
                 const uint32_t d = tmem + k * 128;
-#pragma unroll
+#pragma unroll 1
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int x = 0; x < D / 32; ++x)
@@ -903,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
             const auto values = [&](int k, int stage, uint32_t accumulate) { // O of tile k, V in `stage`
                 const uint32_t v = desc0 + (C::kOffV >> 4) + stage * (C::kV >> 4);
                 const uint32_t d = tmem + 256 + k * 128, p = tmem + k * 128;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
@@ -913,45 +889,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
             // O of block i of a piece (block n - 1 of the CTA), then S of block i + 1 (block n), tile by
             // tile. The stages are constants of two copies of this, so that all descriptors are uniform.
             int nblk, n0, n1;
-            const auto step = [&](auto parity, int i) {
-                constexpr int nxt = decltype(parity)::value, cur = nxt ^ 1; // n & 1, (n - 1) & 1
+            const auto step = [&](int i) {
+                const int nxt = __shfl_sync(~0u, n & 1, 0), cur = nxt ^ 1;
                 const bool more = i + 1 < nblk;
-                if (i >= 0) {
+                if (i >= 0)
                     wait(sh.v_full[cur], (n - 1) >> 1);
-                    if (i < n0) {
-                        wait(sh.p_full[0], n_p0++);
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    const int nk = k ? n1 : n0;
+                    if (i >= 0 && i < nk) {
+                        wait(sh.p_full[k], k ? n_p1 : n_p0);
+                        n_p0 += 1 - k;
+                        n_p1 += k;
                         fence_after();
-                        values(0, cur, i > 0);
-                        if (i == n0 - 1)
-                            commit(smem_addr(&sh.o_full[0]), one);
+                        values(k, cur, i > 0);
+                        if (i == nk - 1)
+                            commit(smem_addr(&sh.o_full[k]), one);
+                    }
+                    if (more) {
+                        if (k == 0) {
+                            wait(sh.k_full[nxt], n >> 1);
+                            fence_proxy_async_smem(); // copies wrote K: the threads that asked for them have gone on
+                        }
+                        if (i + 1 < nk) {
+                            if (i < 0) {
+                                wait(sh.q_full[k], k ? n_q1 : n_q0);
+                                n_q0 += 1 - k;
+                                n_q1 += k;
+                            }
+                            fence_after();
+                            scores(k, nxt);
+                        }
                     }
                 }
-                if (more) {
-                    wait(sh.k_full[nxt], n >> 1);
-                    if (i + 1 < n0) {
-                        if (i < 0)
-                            wait(sh.q_full[0], n_q0++);
-                        fence_after();
-                        scores(0, nxt);
-                    }
-                }
-                if (i >= 0) {
-                    if (i < n1) {
-                        wait(sh.p_full[1], n_p1++);
-                        fence_after();
-                        values(1, cur, i > 0);
-                        if (i == n1 - 1)
-                            commit(smem_addr(&sh.o_full[1]), one);
-                    }
+                if (i >= 0)
                     commit(smem_addr(&sh.v_empty[cur]), one);
-                }
                 if (more) {
-                    if (i + 1 < n1) {
-                        if (i < 0)
-                            wait(sh.q_full[1], n_q1++);
-                        fence_after();
-                        scores(1, nxt);
-                    }
                     commit(smem_addr(&sh.k_empty[nxt]), one);
                     ++n;
                 }
@@ -972,10 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                     break;
 #pragma unroll 1
                 for (int i = -1; i < nblk; ++i) {
-                    if (n & 1)
-                        step(std::integral_constant<int, 1>{}, i);
-                    else
-                        step(std::integral_constant<int, 0>{}, i);
+                    step(i);
                 }
             }
             // before leaving, the MMAs in flight end (bounded, after a wait that ran out too): the last
