@@ -98,6 +98,209 @@ __device__ __forceinline__ int find(const int64_t *pre, int n, int64_t x)
     return lo;
 }
 
+// The cell that entry x of a list's cells names: its address, or 0, and the position it begins at. Lists ascend,
+// with -1 only behind; what is listed beyond the query is not seen. most: tokens of the sequence.
+template <int D>
+__device__ __forceinline__ uint64_t listed_cell(const Kv4 &c, int row, const uint8_t *heads, const int32_t *list, int x,
+                                                int most, int limit, int *begins)
+{
+    const int shift = c.page_shift - 4, cell = x & ((1 << shift) - 1);
+    const int32_t *const at = list + (x >> shift);
+    const int index = at[0];
+    const bool rises = x >> shift == 0 || (at[-1] >= 0 && at[-1] < index);
+    if (index < 0 || !rises || (int64_t)index << c.page_shift >= most) {
+        if (index != -1)
+            kv4_bad(c);
+        return 0;
+    }
+    *begins = (index << c.page_shift) + (cell << 4);
+    if (*begins >= limit)
+        return 0;
+    const int page = kv4_page(c, row, index);
+    if (page < 0) {
+        kv4_bad(c);
+        return 0;
+    }
+    return (uint64_t)(heads + page * c.page_bytes + cell * Kv8Cell<D>::kBytes);
+}
+
+// A row of q as the B operand: the lane's channels 64 e + 16 t .. are words of four k-steps (put(step, word)).
+// Returns the factor of the row's scores.
+template <int D, class F> __device__ __forceinline__ float split_q(const uint4 (&qw)[D / 64][2], float scale, const F &put)
+{
+    constexpr int G = D / 64;
+    float x[G][16];
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < G; ++e)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const uint32_t ws[4] = {qw[e][f].x, qw[e][f].y, qw[e][f].z, qw[e][f].w};
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                x[e][8 * f + 2 * n] = bf16lo_to_f32(ws[n]);
+                x[e][8 * f + 2 * n + 1] = bf16hi_to_f32(ws[n]);
+            }
+        }
+#pragma unroll
+    for (int e = 0; e < G; ++e)
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+            top = fmaxf(top, fabsf(x[e][n]));
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+    // 2^-e brings the row's largest magnitude into [1, 2): what is at least 2^-17 of it is
+    // exact in fp16 (eight bits above 2^-24), the rest is rounded to 2^-24
+    uint32_t e2 = (__float_as_uint(top) >> 23) & 0xFFu;
+    e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
+    const float up = __uint_as_float(e2 << 23); // the sign of the scale goes with q
+    const float down = scale < 0.0f ? -__uint_as_float((254u - e2) << 23) : __uint_as_float((254u - e2) << 23);
+#pragma unroll
+    for (int e = 0; e < G; ++e)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const float *const y = &x[e][4 * f];
+            put(4 * e + f, make_uint2(pack_half2(y[0] * down, y[1] * down), pack_half2(y[2] * down, y[3] * down)));
+        }
+    return fmaxf(up * (fabsf(scale) * kLog2e), 1e-30f);
+}
+
+// What a warp keeps of its rows (lane (g, t): rows 8 j + 2 t + n), and a cell's part in it.
+template <int D, int NT> struct Rows {
+    float o[NT][D / 16][4]; // [n-tile][m-tile][fragment]
+    float mo[NT][2];        // kShift - m, m the running maximum; before the first score so large that any raises m
+    float l[NT][2], scale[NT][2];
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int z = 0; z < D / 16; ++z)
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                    o[j][z][f] = 0.0f;
+            mo[j][0] = mo[j][1] = kNone, l[j][0] = l[j][1] = 0.0f;
+        }
+    }
+    // channels 32 q + 4 g .. of row 8 j + 2 t + n
+    __device__ __forceinline__ float4 four(int j, int n, int q) const
+    {
+        return make_float4(o[j][2 * q][n], o[j][2 * q][n + 2], o[j][2 * q + 1][n], o[j][2 * q + 1][n + 2]);
+    }
+    // A cell in shared memory whose tokens begin at position tok. all: positions that every row sees;
+    // end: positions that hold tokens; q(j, z): B operands; limit(j, n): positions that a row sees.
+    template <class Q, class L>
+    __device__ __forceinline__ void take(const uint8_t *cell, int tok, int all, int end, int lane, const Q &qop, const L &limit)
+    {
+        constexpr int G = D / 64;
+        const int g = lane >> 2, t = lane & 3;
+        const float2 scales = *(const float2 *)(cell + Kv8Cell<D>::kScales);
+        // V's scale goes with the weights, as an exponent; the sums are freed of it again
+        const float ev = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);
+        const float iv = __uint_as_float((254u << 23) - __float_as_uint(scales.y));
+
+        // scores
+        float sc[NT][4];
+        {
+            float acc[G][NT][4] = {};
+#pragma unroll
+            for (int e = 0; e < G; ++e) {
+                const uint4 x0 = *((const uint4 *)(cell + e * 512) + lane);
+                const uint4 x1 = *((const uint4 *)(cell + 8 * D + e * 512) + lane);
+                const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const uint32_t af[4] = {kv8_decode(w0[f]), kv8_decode(w1[f]), kv8_decode(w0[f] >> 16),
+                                            kv8_decode(w1[f] >> 16)};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const int z = 4 * e + f;
+                        const uint2 q = qop(j, z);
+                        mma16816(acc[e][j], af, q.x, q.y);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int f = 0; f < 4; ++f) // token g + 8 (f / 2), row 2 t + f % 2
+                    sc[j][f] = (G == 2 ? acc[0][j][f] + acc[G - 1][j][f] : acc[0][j][f]) * scales.x;
+        }
+        // a row may see only part of the cell
+        if (tok + kKv4Cell > all) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                    sc[j][f] = tok + g + 8 * (f >> 1) < limit(j, f & 1) ? sc[j][f] : -INFINITY;
+        }
+        float top = -INFINITY;
+        float y[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                y[j][f] = fmaf(sc[j][f], scale[j][f & 1], mo[j][f & 1] + ev);
+                top = fmaxf(top, y[j][f]);
+            }
+        if (__any_sync(~0u, top > kShift + kSlack)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    float z = fmaxf(sc[j][n], sc[j][n + 2]);
+                    z = fmaxf(z, __shfl_xor_sync(~0u, z, 4));
+                    z = fmaxf(z, __shfl_xor_sync(~0u, z, 8));
+                    z = fmaf(fmaxf(z, __shfl_xor_sync(~0u, z, 16)), scale[j][n], ev);
+                    const float was = mo[j][n], now = z == -INFINITY ? was : fminf(was, kShift - z);
+                    const float by = was == now ? 1.0f : exp2_approx(now - was);
+                    mo[j][n] = now;
+                    l[j][n] *= by;
+                    y[j][n] = fmaf(sc[j][n], scale[j][n], now + ev);
+                    y[j][n + 2] = fmaf(sc[j][n + 2], scale[j][n], now + ev);
+#pragma unroll
+                    for (int z4 = 0; z4 < D / 16; ++z4) {
+                        o[j][z4][n] *= by;
+                        o[j][z4][n + 2] *= by;
+                    }
+                }
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float p[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                p[f] = exp2_approx(y[j][f]);
+                l[j][f & 1] = fmaf(p[f], iv, l[j][f & 1]);
+            }
+            pb[j][0] = transpose8x8(pack_half2(p[0], p[1]));
+            pb[j][1] = transpose8x8(pack_half2(p[2], p[3]));
+        }
+
+        // O^T += V^T P^T; tokens past the last that is seen hold anything: their V is taken as 0
+        const int left = end - tok;
+        uint32_t keep = ~0u;
+        if (left < kKv4Cell)
+            keep = (2 * t < left ? 0xFFu : 0u) | (2 * t + 1 < left ? 0xFF00u : 0u) | (2 * t + 8 < left ? 0xFF0000u : 0u) |
+                   (2 * t + 9 < left ? 0xFF000000u : 0u);
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+            const uint4 x4 = *((const uint4 *)(cell + Kv8Cell<D>::kV + q * 512) + lane);
+            const uint32_t w[4] = {x4.x & keep, x4.y & keep, x4.z & keep, x4.w & keep};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t af[4] = {kv8_decode(w[2 * h]), kv8_decode(w[2 * h + 1]), kv8_decode(w[2 * h] >> 16),
+                                        kv8_decode(w[2 * h + 1] >> 16)};
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    mma16816(o[j][2 * q + h], af, pb[j][0], pb[j][1]);
+            }
+        }
+    }
+};
+
 // Pieces of a segment that is cut every `chunk` units.
 __device__ __forceinline__ int pieces_of(int units, int chunk) { return (int)((uint32_t)(units + chunk - 1) / (uint32_t)chunk); }
 __device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + kKv4Cell - 1) / kKv4Cell : 1; }
@@ -305,19 +508,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                 const int cell = c0 + warp + (x + lane) * kWarps;
                 where = 0;
                 if (x + lane < mine) {
-                    int index = cell >> shift;
-                    bool seen = true;
-                    if (kListed) { // ascending, -1 only behind; what is listed beyond the query is not seen
-                        const int32_t *const at = a.pages + list + index;
-                        const bool rises = index == 0 || (at[-1] >= 0 && at[-1] < at[0]);
-                        index = at[0];
-                        seen = index >= 0 && rises && (int64_t)index << c.page_shift < most;
-                        if (!seen && index != -1)
-                            kv4_bad(c);
-                    }
-                    begins = seen ? (index << c.page_shift) + ((cell & ((1 << shift) - 1)) << 4) : 0;
-                    if (seen && begins < s.len) {
-                        const int page = kv4_page(c, s.row, index);
+                    if (kListed) {
+                        where = listed_cell<D>(c, s.row, heads, a.pages + list, cell, most, s.len, &begins);
+                    } else if (cell * kKv4Cell < s.len) {
+                        begins = cell * kKv4Cell;
+                        const int page = kv4_page(c, s.row, cell >> shift);
                         if (page >= 0)
                             where = (uint64_t)(heads + page * c.page_bytes + (cell & ((1 << shift) - 1)) * Kv8Cell<D>::kBytes);
                         else
@@ -342,53 +537,15 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
 
         // Q as the B operand
         if (warp < NT) {
-            const int j = warp;
-            float x[G][16];
-            float top = 0.0f;
-#pragma unroll
-            for (int e = 0; e < G; ++e)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const uint32_t ws[4] = {qw[e][f].x, qw[e][f].y, qw[e][f].z, qw[e][f].w};
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        x[e][8 * f + 2 * n] = bf16lo_to_f32(ws[n]);
-                        x[e][8 * f + 2 * n + 1] = bf16hi_to_f32(ws[n]);
-                    }
-                }
-#pragma unroll
-            for (int e = 0; e < G; ++e)
-#pragma unroll
-                for (int n = 0; n < 16; ++n)
-                    top = fmaxf(top, fabsf(x[e][n]));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            // 2^-e brings the row's largest magnitude into [1, 2): what is at least 2^-17 of it is
-            // exact in fp16 (eight bits above 2^-24), the rest is rounded to 2^-24
-            uint32_t e2 = (__float_as_uint(top) >> 23) & 0xFFu;
-            e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
-            const float up = __uint_as_float(e2 << 23); // the sign of the scale goes with q
-            const float down = a.scale < 0.0f ? -__uint_as_float((254u - e2) << 23) : __uint_as_float((254u - e2) << 23);
-#pragma unroll
-            for (int e = 0; e < G; ++e) {
-#pragma unroll
-                for (int n = 0; n < 16; ++n)
-                    x[e][n] *= down;
-                // word f of a lane's 16 channels is a k-step of 16
-#pragma unroll
-                for (int f = 0; f < 4; ++f)
-                    sm_q[(j * KS + 4 * e + f) * 32 + lane] =
-                        make_uint2(pack_half2(x[e][4 * f], x[e][4 * f + 1]), pack_half2(x[e][4 * f + 2], x[e][4 * f + 3]));
-            }
+            const float factor = split_q<D>(qw, a.scale, [&](int z, uint2 v) { sm_q[(warp * KS + z) * 32 + lane] = v; });
             if (t == 0)
-                sm_info[8 * j + g] = RowInfo{fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f),
-                                             real ? s.len - s.n_new + qrow / a.ratio + 1 : 0};
+                sm_info[8 * warp + g] = RowInfo{factor, real ? s.len - s.n_new + qrow / a.ratio + 1 : 0};
         }
         __syncthreads();
         // with one n-tile Q stays in registers
         constexpr bool kKeepQ = NT == 1;
         uint2 qb[kKeepQ ? KS : 1];
-        float scale[NT][2];
+        Rows<D, NT> r;
         if (kKeepQ) {
 #pragma unroll
             for (int x = 0; x < KS; ++x)
@@ -396,16 +553,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            scale[j][0] = sm_info[8 * j + 2 * t].scale;
-            scale[j][1] = sm_info[8 * j + 2 * t + 1].scale;
+            r.scale[j][0] = sm_info[8 * j + 2 * t].scale;
+            r.scale[j][1] = sm_info[8 * j + 2 * t + 1].scale;
         }
 
-        float o[NT][D / 16][4] = {}; // [n-tile][m-tile][fragment]
-        // mo = kShift - m, the running maximum; before the first score so large that any raises m
-        float mo[NT][2], l[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            mo[j][0] = mo[j][1] = kNone, l[j][0] = l[j][1] = 0.0f;
+        r.clear();
 
 #pragma unroll 1
         for (int x = 0; x < mine; ++x) {
@@ -426,113 +578,10 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                 mine = x;
                 break;
             }
-            if (!(have >> st & 1u))
-                continue;
-            const uint8_t *const cell = ring + st * SM::kStage;
-            const int tok = sm_first[st];
-            const float2 scales = *(const float2 *)(cell + Kv8Cell<D>::kScales);
-            // V's scale goes with the weights, as an exponent; the sums are freed of it again
-            const float ev = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);
-            const float iv = __uint_as_float((254u << 23) - __float_as_uint(scales.y));
-
-            // scores
-            float sc[NT][4];
-            {
-                float acc[G][NT][4] = {};
-#pragma unroll
-                for (int e = 0; e < G; ++e) {
-                    const uint4 x0 = *((const uint4 *)(cell + e * 512) + lane);
-                    const uint4 x1 = *((const uint4 *)(cell + 8 * D + e * 512) + lane);
-                    const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const uint32_t af[4] = {kv8_decode(w0[f]), kv8_decode(w1[f]), kv8_decode(w0[f] >> 16),
-                                                kv8_decode(w1[f] >> 16)};
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const int z = 4 * e + f;
-                            const uint2 q = kKeepQ ? qb[z % (kKeepQ ? KS : 1)] : sm_q[(j * KS + z) * 32 + lane];
-                            mma16816(acc[e][j], af, q.x, q.y);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) // token g + 8 (f / 2), row 2 t + f % 2
-                        sc[j][f] = (G == 2 ? acc[0][j][f] + acc[G - 1][j][f] : acc[0][j][f]) * scales.x;
-            }
-            // a row may see only part of the cell
-            if (tok + kKv4Cell > tile_first) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        sc[j][f] = tok + g + 8 * (f >> 1) < sm_info[8 * j + 2 * t + (f & 1)].limit ? sc[j][f] : -INFINITY;
-            }
-            float top = -INFINITY;
-            float y[NT][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    y[j][f] = fmaf(sc[j][f], scale[j][f & 1], mo[j][f & 1] + ev);
-                    top = fmaxf(top, y[j][f]);
-                }
-            if (__any_sync(~0u, top > kShift + kSlack)) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        float z = fmaxf(sc[j][n], sc[j][n + 2]);
-                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 4));
-                        z = fmaxf(z, __shfl_xor_sync(~0u, z, 8));
-                        z = fmaf(fmaxf(z, __shfl_xor_sync(~0u, z, 16)), scale[j][n], ev);
-                        const float was = mo[j][n], now = z == -INFINITY ? was : fminf(was, kShift - z);
-                        const float by = was == now ? 1.0f : exp2_approx(now - was);
-                        mo[j][n] = now;
-                        l[j][n] *= by;
-                        y[j][n] = fmaf(sc[j][n], scale[j][n], now + ev);
-                        y[j][n + 2] = fmaf(sc[j][n + 2], scale[j][n], now + ev);
-#pragma unroll
-                        for (int z4 = 0; z4 < D / 16; ++z4) {
-                            o[j][z4][n] *= by;
-                            o[j][z4][n + 2] *= by;
-                        }
-                    }
-            }
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float p[4];
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    p[f] = exp2_approx(y[j][f]);
-                    l[j][f & 1] = fmaf(p[f], iv, l[j][f & 1]);
-                }
-                pb[j][0] = transpose8x8(pack_half2(p[0], p[1]));
-                pb[j][1] = transpose8x8(pack_half2(p[2], p[3]));
-            }
-
-            // O^T += V^T P^T; tokens past the last that is seen hold anything: their V is taken as 0
-            const int end = s.len - tok;
-            uint32_t keep = ~0u;
-            if (end < kKv4Cell)
-                keep = (2 * t < end ? 0xFFu : 0u) | (2 * t + 1 < end ? 0xFF00u : 0u) | (2 * t + 8 < end ? 0xFF0000u : 0u) |
-                       (2 * t + 9 < end ? 0xFF000000u : 0u);
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                const uint4 x4 = *((const uint4 *)(cell + Kv8Cell<D>::kV + q * 512) + lane);
-                const uint32_t w[4] = {x4.x & keep, x4.y & keep, x4.z & keep, x4.w & keep};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t af[4] = {kv8_decode(w[2 * h]), kv8_decode(w[2 * h + 1]), kv8_decode(w[2 * h] >> 16),
-                                            kv8_decode(w[2 * h + 1] >> 16)};
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        mma16816(o[j][2 * q + h], af, pb[j][0], pb[j][1]);
-                }
-            }
+            if (have >> st & 1u)
+                r.take(ring + st * SM::kStage, sm_first[st], tile_first, s.len, lane,
+                       [&](int j, int z) { return kKeepQ ? qb[z % (kKeepQ ? KS : 1)] : sm_q[(j * KS + z) * 32 + lane]; },
+                       [&](int j, int n) { return sm_info[8 * j + 2 * t + n].limit; });
         }
         used += mine;
         __syncthreads(); // the rings are read: the parts take their place
@@ -542,20 +591,19 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                float x = l[j][n];
+                float x = r.l[j][n];
                 x += __shfl_xor_sync(~0u, x, 4);
                 x += __shfl_xor_sync(~0u, x, 8);
                 x += __shfl_xor_sync(~0u, x, 16);
                 const int row = 8 * j + 2 * t + n;
                 if (g == 0) {
-                    sm_m[warp * RT + row] = mo[j][n] == kNone ? -INFINITY : kShift - mo[j][n];
+                    sm_m[warp * RT + row] = r.mo[j][n] == kNone ? -INFINITY : kShift - r.mo[j][n];
                     sm_l[warp * RT + row] = x;
                 }
                 float *dst = sm_o + (warp * RT + row) * SM::kPitch + 4 * g;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q)
-                    *(float4 *)(dst + 32 * q) =
-                        make_float4(o[j][2 * q][n], o[j][2 * q][n + 2], o[j][2 * q + 1][n], o[j][2 * q + 1][n + 2]);
+                    *(float4 *)(dst + 32 * q) = r.four(j, n, q);
             }
         __syncthreads();
 
@@ -676,6 +724,149 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                              (int64_t)blockIdx.x * kWarps + warp, (int64_t)gridDim.x * kWarps);
 }
 
+// With lists and many of them: a warp takes a token's kv head by itself, all of its list, so that no threads
+// meet. Q is in its registers, and a lane has two rows' output of four channels in 32.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv8_lists_kernel(const Kv4 c, const Kv4Batch b, const AttnArgs a)
+{
+    constexpr int G = D / 64, KS = 4 * G;
+    using SM = Smem<D, 1>;
+    constexpr int S = NT == 1 ? SM::kStages : 2 * SM::kStages - 1;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t s_bars[kWarps * S];
+    __shared__ int s_first[kWarps * S];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    uint8_t *const ring = smem + warp * S * SM::kStage;
+    int *const first_of = s_first + warp * S;
+    const uint32_t rings = smem_addr(ring), bars = smem_addr(s_bars) + warp * S * 8;
+    if (lane == 0)
+        for (int i = 0; i < S; ++i)
+            mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+    __syncwarp();
+    if (blockIdx.x == 0)
+        for (int i = tid; i < b.n_seqs; i += kThreads)
+            kv4_seq(c, b, i, true);
+    const int shift = c.page_shift - 4, mask = (1 << shift) - 1;
+    const int64_t segments = b.n_tokens * c.n_kv_heads;
+    uint32_t used = 0;
+    bool dead = false;
+#pragma unroll 1
+    for (int64_t seg = (int64_t)blockIdx.x * kWarps + warp; seg < segments; seg += (int64_t)gridDim.x * kWarps) {
+        const int64_t token = quotient(seg, c.n_kv_heads);
+        const int head = (int)(seg - token * c.n_kv_heads);
+        // the rows of Q: row 8 j + g, channels 64 e + 16 t ..
+        uint4 qw[NT][G][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const bool real = 8 * j + g < a.ratio;
+            const uint16_t *q = a.q + token * a.q_stride + ((int64_t)head * a.ratio + 8 * j + g) * D + 16 * t;
+#pragma unroll
+            for (int e = 0; e < G; ++e)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    qw[j][e][f] = real ? ldg_nc128(q + 64 * e + 8 * f) : make_uint4(0, 0, 0, 0);
+        }
+        const int i = kv4_find(b, token);
+        Kv4Seq s{};
+        if (i >= 0)
+            s = kv4_seq(c, b, i, false);
+        const int64_t seen = i >= 0 && s.first >= 0 && token - s.first < s.n_new ? s.len - s.n_new + (token - s.first) + 1 : 0;
+        const int most = s.len, limit = seen > 0 && s.len > 0 ? (int)seen : 0;
+        const int32_t *const list = a.pages + seg * a.n_list;
+        int mine = dead || limit == 0 ? 0 : a.n_list << shift;
+        const uint8_t *const heads = c.pool + kv8_head_offset<D>(c, 0, a.layer, head);
+        uint64_t where = 0;
+        int begins = 0;
+        uint32_t have = 0;
+        const auto fetch = [&](int x) {
+            if ((x & 31) == 0) {
+                where = 0;
+                if (x + lane < mine)
+                    where = listed_cell<D>(c, s.row, heads, list, x + lane, most, limit, &begins);
+                // nothing is listed from here on
+                if (x > 0 && !__any_sync(~0u, where != 0)) {
+                    const bool rest = x + lane < mine && list[(x + lane) >> shift] != -1;
+                    if (!__any_sync(~0u, rest))
+                        mine = x;
+                }
+            }
+            if (x >= mine)
+                return;
+            const uint64_t src = __shfl_sync(~0u, where, x & 31);
+            const int first = __shfl_sync(~0u, begins, x & 31);
+            const uint32_t st = (used + x) % S, bar = bars + 8 * st;
+            have = (have & ~(1u << st)) | (uint32_t)(src != 0) << st;
+            if (lane == 0) {
+                first_of[st] = first;
+                mbar_arrive_expect_tx(bar, src ? Kv8Cell<D>::kBytes : 0u);
+                if (src)
+                    bulk_load(rings + st * SM::kStage, (const void *)src, Kv8Cell<D>::kBytes, bar);
+            }
+            __syncwarp();
+        };
+        for (int x = 0; x < S - 1 && x < mine; ++x)
+            fetch(x);
+
+        uint2 qb[NT][KS];
+        float factor[NT]; // of row 8 j + g
+        Rows<D, NT> r;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            factor[j] = split_q<D>(qw[j], a.scale, [&](int z, uint2 v) { qb[j][z] = v; });
+            r.scale[j][0] = __shfl_sync(~0u, factor[j], 8 * t);
+            r.scale[j][1] = __shfl_sync(~0u, factor[j], 8 * t + 4);
+        }
+        r.clear();
+#pragma unroll 1
+        for (int x = 0; x < mine; ++x) {
+            if (x + S - 1 < mine) {
+                __syncwarp(); // the stage that is filled now was read by all lanes
+                fetch(x + S - 1);
+            }
+            const uint32_t st = (used + x) % S;
+            kv4_wait(bars + 8 * st, ((used + x) / S) & 1, c.status, dead);
+            if (__any_sync(~0u, dead)) { // as in kv8_rows_kernel
+                for (int z = x; z < x + S && z < mine; ++z) {
+                    dead = false;
+                    kv4_wait(bars + 8 * ((used + z) % S), ((used + z) / S) & 1, c.status, dead);
+                }
+                dead = true;
+                mine = x;
+                break;
+            }
+            if (have >> st & 1u)
+                r.take(ring + st * SM::kStage, first_of[st], limit, limit, lane, [&](int j, int z) { return qb[j][z]; },
+                       [&](int, int) { return limit; });
+        }
+        used += mine;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float l = r.l[j][n];
+                l += __shfl_xor_sync(~0u, l, 4);
+                l += __shfl_xor_sync(~0u, l, 8);
+                l += __shfl_xor_sync(~0u, l, 16);
+                const int row = 8 * j + 2 * t + n;
+                if (row >= a.ratio)
+                    continue;
+                const int64_t h = (int64_t)head * a.ratio + row;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                uint16_t *const out = a.out + token * a.out_stride + h * D + 4 * g;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    const float4 y = r.four(j, n, q);
+                    *(uint2 *)(out + 32 * q) = make_uint2(f32_to_bf16_rn(y.x * inv) | ((uint32_t)f32_to_bf16_rn(y.y * inv) << 16),
+                                                          f32_to_bf16_rn(y.z * inv) | ((uint32_t)f32_to_bf16_rn(y.w * inv) << 16));
+                }
+                if (a.lse && g == 0)
+                    a.lse[token * a.n_q_heads + h] = l == 0.0f ? -INFINITY : (log2f(l) - r.mo[j][n]) * kLn2;
+            }
+        __syncwarp(); // the stages are read before the next list's cells overwrite them
+    }
+}
+
 template <int D, int NT, bool kListed>
 nm_status launch(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, const Kv4Work &w, cudaStream_t st)
 {
@@ -690,6 +881,21 @@ nm_status launch(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, const Kv4Wo
     const size_t smem = Smem<D, NT>::kSeqs + (size_t)(b.n_seqs + 1) * 8 + (size_t)b.n_seqs * sizeof(Kv4Seq);
     const unsigned grid = (unsigned)(w.num_sms * (NT <= 2 ? 2 : 1)); // at most kKv4Counters / 4
     kv8_rows_kernel<D, NT, kListed><<<grid, kThreads, smem, st>>>(c, b, a);
+    return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
+}
+
+template <int D, int NT>
+nm_status launch_lists(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, const Kv4Work &w, cudaStream_t st)
+{
+    constexpr int kStages = NT == 1 ? Smem<D, 1>::kStages : 2 * Smem<D, 1>::kStages - 1;
+    constexpr int kBytes = kWarps * kStages * Smem<D, 1>::kStage;
+    static OncePerDevice once;
+    if (!once(w.device, [] {
+            return cudaFuncSetAttribute(kv8_lists_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) ==
+                   cudaSuccess;
+        }))
+        return NM_ERR_CUDA;
+    kv8_lists_kernel<D, NT><<<(unsigned)(w.num_sms * (NT == 1 ? 2 : 1)), kThreads, kBytes, st>>>(c, b, a);
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
 
@@ -711,11 +917,14 @@ nm_status kv8_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
                      at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials, pages, n_list};
     if (pages) {
         const int rows = a.ratio;
+        if (rows <= 16 && b.n_tokens * c.n_kv_heads >= 8 * (int64_t)w.num_sms) {
+            if (c.head_dim == 64)
+                return rows <= 8 ? launch_lists<64, 1>(c, b, a, w, st) : launch_lists<64, 2>(c, b, a, w, st);
+            return rows <= 8 ? launch_lists<128, 1>(c, b, a, w, st) : launch_lists<128, 2>(c, b, a, w, st);
+        }
         if (c.head_dim == 64)
             return rows <= 8 ? launch<64, 1, true>(c, b, a, w, st) : launch<64, 2, true>(c, b, a, w, st);
-        return rows <= 8    ? launch<128, 1, true>(c, b, a, w, st)
-               : rows <= 16 ? launch<128, 2, true>(c, b, a, w, st)
-                            : launch<128, 4, true>(c, b, a, w, st);
+        return rows <= 8 ? launch<128, 1, true>(c, b, a, w, st) : launch<128, 2, true>(c, b, a, w, st);
     }
     const int64_t rows = (max_new < 65 ? max_new : 65) * a.ratio;
     if (rows > 64 && b.n_tokens * at.n_q_heads > 1024)
@@ -724,12 +933,9 @@ nm_status kv8_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
         return rows <= 8                 ? launch<64, 1, false>(c, b, a, w, st)
                : rows > 16 && rows <= 24 ? launch<64, 3, false>(c, b, a, w, st)
                                          : launch<64, 2, false>(c, b, a, w, st);
-    return rows <= 8    ? launch<128, 1, false>(c, b, a, w, st)
-           : rows <= 16 ? launch<128, 2, false>(c, b, a, w, st)
-           : rows <= 24 ? launch<128, 3, false>(c, b, a, w, st)
-           : rows <= 32 ? launch<128, 4, false>(c, b, a, w, st)
-           : rows <= 48 ? launch<128, 3, false>(c, b, a, w, st)
-                        : launch<128, 4, false>(c, b, a, w, st);
+    return rows <= 8                 ? launch<128, 1, false>(c, b, a, w, st)
+           : rows > 16 && rows <= 24 ? launch<128, 3, false>(c, b, a, w, st)
+                                     : launch<128, 2, false>(c, b, a, w, st);
 }
 
 } // namespace nm

@@ -715,3 +715,38 @@ def test_fork_decode_compact(nm):
         tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2.0 ** -13 + 2.0 ** -15 * B[..., None]) * A + 1e-6
         assert np.all(np.abs(f64(out[i:i + 1]) - o) <= tol)
     assert nm.device_status() == nm.NM_OK
+
+
+@pytest.mark.parametrize("D,Hq", [(128, 4), (64, 8), (128, 13), (64, 16)])
+def test_many_lists_a_warp_each(nm, D, Hq):
+    """So many tokens that each list is one warp's: sequences that end and begin, padding, empty lists."""
+    P = 16
+    lens, new = [3000, 900, 40], [900, 400, 40]
+    c, held = make(nm, lens, P=P, L=1, Hk=1, D=D, seed=37)
+    q = values(1400, Hq, D, 38)
+    starts = starts_of(new)  # 60 rows belong to no sequence
+    pages = c.select(0, q, 9, starts=starts)
+    pages[5] = -1
+    pages[950, 0, 3:] = -1
+    out, lse = c.attention(0, q, starts=starts, pages=pages, lse=True, out=torch.full_like(q, 7.0))
+    assert nm.device_status() == nm.NM_OK
+    assert bool((out[1340:] == 0).all()) and bool(torch.isneginf(lse[1340:]).all())
+    assert bool((out[5] == 0).all()) and bool(torch.isneginf(lse[5]).all())
+    for t in (0, 1, 31, 899, 900, 950, 1299, 1300, 1301, 1339):
+        s, m = (0, 2101 + t) if t < 900 else (1, 501 + t - 900) if t < 1300 else (2, 1 + t - 1300)
+        o, l, A, B = ref.attention(f64(q[t:t + 1]), held[s].k[:m].astype(np.float64), held[s].v[:m].astype(np.float64), m,
+                                   D ** -0.5, pages[t:t + 1].cpu().numpy(), P)
+        e = 2.0 ** -16 * B + 2.0 ** -15
+        assert np.all(np.abs(f64(lse[t:t + 1]) - l) <= e)
+        tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e[..., None] + 2.0 ** -14) * A + m * 2.0 ** -27
+        assert np.all(np.abs(f64(out[t:t + 1]) - o) <= tol)
+    # each list by itself gives the same to rounding, and calls repeat
+    few = torch.cat([c.attention(0, q[t:t + 1], seqs=ints([0]), starts=ints([0, 1]), pages=pages[t:t + 1]) for t in (899,)])
+    assert float((few[0].float() - out[899].float()).abs().max()) < 0.05
+    o2, l2 = c.attention(0, q, starts=starts, pages=pages, lse=True)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+    # entries out of order or range are passed over and reported
+    bad = pages.clone()
+    bad[7, 0, 4], bad[8, 0, 8] = 1 << 20, 0
+    c.attention(0, q, starts=starts, pages=bad)
+    assert nm.device_status() == nm.NM_ERR_BOUNDS
