@@ -10,8 +10,7 @@
 // A block's scale is a power of two, so a value is its code exactly, and a token that
 // needs a larger one moves the codes held there by whole exponents: they are rounded
 // again only where they leave the codes' normal range. The greatest magnitude of the
-// new tokens decides before any is written, so they wait in registers (K in fp32, V as it
-// came).
+// new tokens decides before any is written.
 //
 // The warps of a page's blocks stand side by side in a CTA. When a call fills a page its
 // keys' bounds are taken from the codes just written and those held before.
@@ -245,33 +244,40 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, const Kv4Seq &
     constexpr int N = D / 16;
     using C = Kv8Cell<D>;
     const int lane = threadIdx.x & 31, i = lane & 7, part = lane >> 3;
-    Vec<N> k[4];
-    Raw<N> v[4];
-    uint32_t most_k = 0, most_v = 0, ok_bits = 0, bad_bits = 0;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    // The four tokens t of the lanes: K rotated, V as it came. The tokens are read twice, for the scale and for the
+    // codes (the second time from L1): held in registers they leave room for half as many warps.
+    const auto token_at = [&](int t, Vec<N> *k, Raw<N> *v) {
         const int pos = base + slot_of(t, part);
         const bool ok = pos >= from && pos < to;
-        ok_bits |= (uint32_t)ok << t;
-        if (!__any_sync(~0u, ok))
-            continue;
         Raw<N> rk{};
-        v[t] = Raw<N>{};
+        *v = Raw<N>{};
         if (ok) {
             const int64_t token = (int64_t)s.first + (pos - (s.len - s.n_new));
             rk = load_raw<N, false>(a.k + token * a.k_stride + (int64_t)head * D, i, D / 2);
-            v[t] = load_raw<N, false>(a.v + token * a.v_stride + (int64_t)head * D, i, D / 2);
+            *v = load_raw<N, false>(a.v + token * a.v_stride + (int64_t)head * D, i, D / 2);
         }
-        k[t] = unpack<N>(rk);
+        *k = unpack<N>(rk);
         if (a.rope && ok)
-            rotate<N>(k[t], a.rope + (int64_t)pos * D, i);
-        const Vec<N> w = unpack<N>(v[t]);
+            rotate<N>(*k, a.rope + (int64_t)pos * D, i);
+        return ok;
+    };
+    uint32_t most_k = 0, most_v = 0, bad_bits = 0;
+    // not unrolled: a decode step's one token runs a quarter of the code
+#pragma unroll 1
+    for (int t = 0; t < 4; ++t) {
+        const int first = base + 2 * t;
+        if (first + 9 < from || first >= to)
+            continue; // none of the four is the call's
+        Vec<N> k;
+        Raw<N> v;
+        token_at(t, &k, &v);
+        const Vec<N> w = unpack<N>(v);
         uint32_t mk = 0, mv = 0; // magnitudes as whole numbers: what is not finite is at least 0x7F800000
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                mk = max(mk, __float_as_uint(k[t].x[h][n]) & 0x7FFFFFFFu);
+                mk = max(mk, __float_as_uint(k.x[h][n]) & 0x7FFFFFFFu);
                 mv = max(mv, __float_as_uint(w.x[h][n]) & 0x7FFFFFFFu);
             }
         const uint32_t votes = __ballot_sync(~0u, max(mk, mv) < 0x7F800000u);
@@ -314,18 +320,21 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, const Kv4Seq &
         *(float2 *)(cell + C::kScales) = make_float2(sk, sv);
     const float ik = pow2_inverse(sk), iv = pow2_inverse(sv);
     const bool large = max(most_k, most_v) > __float_as_uint(kKv4Limit);
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 4; ++t) {
-        const bool ok = ok_bits >> t & 1u, bad = bad_bits >> t & 1u;
-        const uint32_t votes = __ballot_sync(~0u, ok);
-        if (!votes)
+        const int first = base + 2 * t;
+        if (first + 9 < from || first >= to)
             continue;
-        const Vec<N> w = unpack<N>(v[t]);
+        Vec<N> k;
+        Raw<N> v;
+        const bool ok = token_at(t, &k, &v), bad = bad_bits >> t & 1u;
+        const uint32_t votes = __ballot_sync(~0u, ok);
+        const Vec<N> w = unpack<N>(v);
         uint32_t cv[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int p = 0; p < N / 2; ++p) {
             const int h = p / (N / 4), n = 4 * (p % (N / 4));
-            const uint32_t ck = bad ? 0x7F7F7F7Fu : encode4(&k[t].x[h][n], ik, large); // a NaN for each query
+            const uint32_t ck = bad ? 0x7F7F7F7Fu : encode4(&k.x[h][n], ik, large); // a NaN for each query
             if (ok)
                 *(uint32_t *)(cell + k_at<D>(slot_of(t, part), channel_of<D>(p, i))) = ck;
             cv[p] = bad ? 0u : encode4(&w.x[h][n], iv, large);
@@ -514,7 +523,7 @@ template <int D> __device__ __forceinline__ void append_q(const Kv4 &c, const Kv
     }
 }
 
-template <int D> __global__ void __launch_bounds__(256, 2) append_kernel(const Kv4 c, const Kv4Batch b, const AppendArgs a)
+template <int D> __global__ void __launch_bounds__(256, 4) append_kernel(const Kv4 c, const Kv4Batch b, const AppendArgs a)
 {
     if (blockIdx.x < a.unit_ctas) {
         append_pages<D>(c, b, a);
