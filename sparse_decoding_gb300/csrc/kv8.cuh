@@ -39,6 +39,57 @@ __device__ __forceinline__ uint32_t kv8_decode(uint32_t two)
     return r;
 }
 
+// q in 8-bit floats (for prompts). A row is scaled by a power of two that brings its largest magnitude into [2^7, 2^8), and
+// a bf16 number (eight significant bits) is split into its first four (e4m3, nearest) and what is left: at most
+// eight units of the last place, which e5m2 holds exactly. That is so down to 2^-6, 2^-13 of the row's
+// largest at least. Below, the first part is a multiple of 2^-9 and what is left is rounded: by at most 2^-14,
+// 2^-21 of the row's largest.
+__device__ __forceinline__ uint32_t kv8_magnitude(const uint4 &x) // the largest of eight, as fp32 bits
+{
+    const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+        top = max(top, max(ws[n] & 0x7FFF0000u, (ws[n] << 16) & 0x7FFF0000u));
+    return top;
+}
+struct Kv8Row {
+    float down, factor; // of q, with the sign of the scale; of the scores, to the base 2
+};
+// sees: whether the row sees any token: something that is not finite then makes its result NaN.
+__device__ __forceinline__ Kv8Row kv8_row(uint32_t top, float scale, bool sees)
+{
+    const uint32_t field = top >> 23;
+    const uint32_t e = field == 0xFFu || field == 0 ? 127u : field > 250u ? 250u : field < 8u ? 8u : field;
+    const float up = __uint_as_float((e - 7u) << 23), down = __uint_as_float((261u - e) << 23);
+    Kv8Row r;
+    r.down = scale < 0.0f ? -down : down;
+    // above 0, so that masked scores stay -inf
+    r.factor = field == 0xFFu && sees ? __uint_as_float(0x7FC00000u) : fmaxf(up * (fabsf(scale) * 1.4426950408889634f), 1e-30f);
+    return r;
+}
+// Eight channels: two words of each part.
+__device__ __forceinline__ void kv8_split(const uint4 &x, float down, uint2 &hi, uint2 &lo)
+{
+    const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        uint32_t y, z;
+        uint16_t p, r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(bf16hi_to_f32(ws[n]) * down), "f"(bf16lo_to_f32(ws[n]) * down));
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(y));
+        const uint32_t back = kv8_decode(p);
+        const __half2 left = __hsub2(*(const __half2 *)&y, *(const __half2 *)&back);
+        z = *(const uint32_t *)&left;
+        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(z));
+        h[n] = p;
+        l[n] = r;
+    }
+    hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
 // A selection: count pages of each token and kv head, the first and last of them always.
 struct Kv8Select {
     int layer, n_q_heads, count, first, last;

@@ -125,16 +125,19 @@ __device__ __forceinline__ uint64_t listed_cell(const Kv4 &c, int row, const uin
 }
 
 // A row of q as the B operand: the lane's channels 64 e + 16 t .. are words of four k-steps (put(step, word)).
-// Returns the factor of the row's scores.
-template <int D, class F> __device__ __forceinline__ float split_q(const uint4 (&qw)[D / 64][2], float scale, const F &put)
+// Returns the factor of the row's scores. sees: whether the row sees any token, which something that is not finite
+// in it then meets.
+template <int D, class F>
+__device__ __forceinline__ float split_q(const uint4 (&qw)[D / 64][2], float scale, bool sees, const F &put)
 {
     constexpr int G = D / 64;
     float x[G][16];
-    float top = 0.0f;
+    uint32_t top = 0; // the largest magnitude, as fp32 bits
 #pragma unroll
     for (int e = 0; e < G; ++e)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
+            top = max(top, kv8_magnitude(qw[e][f]));
             const uint32_t ws[4] = {qw[e][f].x, qw[e][f].y, qw[e][f].z, qw[e][f].w};
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -142,17 +145,11 @@ template <int D, class F> __device__ __forceinline__ float split_q(const uint4 (
                 x[e][8 * f + 2 * n + 1] = bf16hi_to_f32(ws[n]);
             }
         }
-#pragma unroll
-    for (int e = 0; e < G; ++e)
-#pragma unroll
-        for (int n = 0; n < 16; ++n)
-            top = fmaxf(top, fabsf(x[e][n]));
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+    top = max(top, __shfl_xor_sync(~0u, top, 1));
+    top = max(top, __shfl_xor_sync(~0u, top, 2));
     // 2^-e brings the row's largest magnitude into [1, 2): what is at least 2^-17 of it is
     // exact in fp16 (eight bits above 2^-24), the rest is rounded to 2^-24
-    uint32_t e2 = (__float_as_uint(top) >> 23) & 0xFFu;
-    e2 = e2 == 0xFFu || e2 == 0 ? 127u : e2 > 253u ? 253u : e2;
+    const uint32_t field = top >> 23, e2 = field == 0xFFu || field == 0 ? 127u : field > 253u ? 253u : field;
     const float up = __uint_as_float(e2 << 23); // the sign of the scale goes with q
     const float down = scale < 0.0f ? -__uint_as_float((254u - e2) << 23) : __uint_as_float((254u - e2) << 23);
 #pragma unroll
@@ -162,7 +159,8 @@ template <int D, class F> __device__ __forceinline__ float split_q(const uint4 (
             const float *const y = &x[e][4 * f];
             put(4 * e + f, make_uint2(pack_half2(y[0] * down, y[1] * down), pack_half2(y[2] * down, y[3] * down)));
         }
-    return fmaxf(up * (fabsf(scale) * kLog2e), 1e-30f);
+    // above 0, so that masked scores stay -inf
+    return field == 0xFFu && sees ? __uint_as_float(0x7FC00000u) : fmaxf(up * (fabsf(scale) * kLog2e), 1e-30f);
 }
 
 // What a warp keeps of its rows (lane (g, t): rows 8 j + 2 t + n), and a cell's part in it.
@@ -537,9 +535,10 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
 
         // Q as the B operand
         if (warp < NT) {
-            const float factor = split_q<D>(qw, a.scale, [&](int z, uint2 v) { sm_q[(warp * KS + z) * 32 + lane] = v; });
+            const int limit = real ? s.len - s.n_new + qrow / a.ratio + 1 : 0;
+            const float factor = split_q<D>(qw, a.scale, limit > 0, [&](int z, uint2 v) { sm_q[(warp * KS + z) * 32 + lane] = v; });
             if (t == 0)
-                sm_info[8 * warp + g] = RowInfo{factor, real ? s.len - s.n_new + qrow / a.ratio + 1 : 0};
+                sm_info[8 * warp + g] = RowInfo{factor, limit};
         }
         __syncthreads();
         // with one n-tile Q stays in registers
@@ -813,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv8_lists_kernel(co
         Rows<D, NT> r;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            factor[j] = split_q<D>(qw[j], a.scale, [&](int z, uint2 v) { qb[j][z] = v; });
+            factor[j] = split_q<D>(qw[j], a.scale, true, [&](int z, uint2 v) { qb[j][z] = v; });
             r.scale[j][0] = __shfl_sync(~0u, factor[j], 8 * t);
             r.scale[j][1] = __shfl_sync(~0u, factor[j], 8 * t + 4);
         }

@@ -468,8 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
         uint32_t n_s = 0, n_o = 0; // blocks and pieces of this tile so far
         uint32_t n_first = 0;      // blocks of the CTA before the piece
 
-        // The row of Q, scaled by a power of two to below 2^8, in two parts: the first four significant
-        // bits (e4m3), and what is left (e5m2). Returns the factor of the scores.
+        // The row of Q in its two parts. Returns the factor of the scores.
         const auto load_q = [&](const Piece &w) {
             constexpr int N = D / 8; // 16-byte pieces of a row
             const bool valid = valid_in(w);
@@ -480,42 +479,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                 x[i] = valid ? ldg_nc128(q + 8 * i) : make_uint4(0, 0, 0, 0);
             uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    top = max(top, max(ws[n] & 0x7FFF0000u, (ws[n] << 16) & 0x7FFF0000u));
-            }
-            const uint32_t field = top >> 23;
-            const uint32_t e2 = field == 0xFFu || field == 0 ? 127u : field > 250u ? 250u : field < 8u ? 8u : field;
-            const float up = __uint_as_float((e2 - 7u) << 23);
-            const float down = a.scale < 0.0f ? -__uint_as_float((261u - e2) << 23) : __uint_as_float((261u - e2) << 23);
+            for (int i = 0; i < N; ++i)
+                top = max(top, kv8_magnitude(x[i]));
+            const Kv8Row of = kv8_row(top, a.scale, w.len - w.n_new + token_of(w) >= 0);
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                uint32_t hi[4], lo[4]; // of 16 channels
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t ws[4] = {x[i + h].x, x[i + h].y, x[i + h].z, x[i + h].w};
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const uint32_t y = pack_half2(bf16lo_to_f32(ws[n]) * down, bf16hi_to_f32(ws[n]) * down);
-                        uint16_t p, r;
-                        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(y));
-                        const uint32_t left = as_u32(__hsub2(as_half2(y), as_half2(kv8_decode(p))));
-                        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(left));
-                        hi[2 * h + n / 2] = n & 1 ? hi[2 * h + n / 2] | (uint32_t)p << 16 : p;
-                        lo[2 * h + n / 2] = n & 1 ? lo[2 * h + n / 2] | (uint32_t)r << 16 : r;
-                    }
-                }
+                uint2 hi[2], lo[2]; // of 16 channels
+                kv8_split(x[i], of.down, hi[0], lo[0]);
+                kv8_split(x[i + 1], of.down, hi[1], lo[1]);
                 const uint32_t at = q_tile + row * D + C::piece(row, i / 2);
-                sts128(at, hi[0], hi[1], hi[2], hi[3]);
-                sts128(at + C::kK, lo[0], lo[1], lo[2], lo[3]);
+                sts128(at, hi[0].x, hi[0].y, hi[1].x, hi[1].y);
+                sts128(at + C::kK, lo[0].x, lo[0].y, lo[1].x, lo[1].y);
             }
             fence_proxy_async_smem();
             kv4_arrive(smem_addr(&sh.q_full[k]));
-            if (field == 0xFFu && w.len - w.n_new + token_of(w) >= 0) // something that is not finite meets a token
-                return __uint_as_float(0x7FC00000u);
-            return fmaxf(up * (fabsf(a.scale) * kLog2e), 1e-30f); // above 0, so that masked scores stay -inf
+            return of.factor;
         };
 
         // The rows of O of a piece.

@@ -750,3 +750,48 @@ def test_many_lists_a_warp_each(nm, D, Hq):
     bad[7, 0, 4], bad[8, 0, 8] = 1 << 20, 0
     c.attention(0, q, starts=starts, pages=bad)
     assert nm.device_status() == nm.NM_ERR_BOUNDS
+
+
+@pytest.mark.parametrize("max_new,heads", [(1, 8), (64, 8), (64, 64), (0, 8)])
+def test_attention_nonfinite_queries_stay_in_their_rows(nm, max_new, heads):
+    """NaN and infinities in q: NaN in that row and no other, in each kernel (0: over lists), and nothing in a row that
+    sees no token."""
+    c, held = make(nm, [100], seed=92)
+    q = values(40, heads, 128, 93)
+    kw = dict(pages=c.select(1, q, 3, starts=ints([0, 40]))) if max_new == 0 else dict(max_new=max_new)
+    good, gl = c.attention(1, q, starts=ints([0, 40]), lse=True, **kw)
+    bad = q.clone()
+    bad[7, 3, 11], bad[20, 6, 5], bad[21, 0, 0] = float("nan"), float("inf"), float("-inf")
+    out, lse = c.attention(1, bad, starts=ints([0, 40]), lse=True, **kw)
+    same = torch.ones(40, heads, dtype=torch.bool, device="cuda")
+    for t, h in ((7, 3), (20, 6), (21, 0)):
+        same[t, h] = False
+        assert bool(torch.isnan(out[t, h]).all()) and bool(torch.isnan(lse[t, h]))
+    assert torch.equal(out[same], good[same]) and torch.equal(lse[same], gl[same])
+    short = nm.Kv8Cache(3, 16, 1, 2, 128, 1, 3)
+    short.reserve(starts=ints([0, 30]))
+    k = values(30, 2, 128, 94)
+    short.append(0, k, k, starts=ints([0, 30]))
+    kw = dict(pages=torch.zeros(40, 2, 1, dtype=torch.int32, device="cuda")) if max_new == 0 else dict(max_new=max_new)
+    out, lse = short.attention(0, bad, starts=ints([0, 40]), lse=True, **kw)  # the first ten rows see nothing
+    assert bool((out[:10] == 0).all()) and bool(torch.isneginf(lse[:10]).all())
+    assert bool(torch.isnan(out[20, 6]).all()) and bool(torch.isfinite(out[19]).all())
+
+
+@pytest.mark.parametrize("max_new,heads", [(1, 8), (64, 64), (0, 8)])
+def test_attention_queries_of_wide_range(nm, max_new, heads):
+    """Channels of q from the row's largest down to 2^-24 of it, in an order that meets large keys: q is exact
+    above 2^-13 of the largest and off by at most 2^-21 of it below, so scores are off by at most 2^-21 max |q| sum |k| more."""
+    c, held = make(nm, [300], Hk=2, seed=95)
+    g = torch.Generator().manual_seed(96)
+    q = (torch.randn(30, heads, 128, generator=g) * torch.exp2(-24 * torch.rand(30, heads, 128, generator=g)) * 30).bfloat16().cuda()
+    kw = dict(pages=c.select(1, q, 5, starts=ints([0, 30]))) if max_new == 0 else dict(max_new=max_new)
+    out, lse = c.attention(1, q, starts=ints([0, 30]), lse=True, **kw)
+    K, V = held[0].k.astype(np.float64), held[0].v.astype(np.float64)
+    lists = kw["pages"].cpu().numpy() if max_new == 0 else None
+    o, l, A, B = ref.attention(f64(q), K, V, 300, 128 ** -0.5, lists, 32)
+    e = 2.0 ** -16 * B + 2.0 ** -15 + 2.0 ** -21 * np.abs(f64(q)).max(-1) * np.abs(K).sum(-1).max() * 128 ** -0.5
+    assert np.all(np.abs(f64(lse) - l) <= e)
+    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e[..., None] + 2.0 ** -14) * A + 300 * 2.0 ** -27
+    assert np.all(np.abs(f64(out) - o) <= tol)
+    assert nm.device_status() == nm.NM_OK
