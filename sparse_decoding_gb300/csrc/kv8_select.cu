@@ -272,7 +272,7 @@ __device__ __forceinline__ void choose(const SelectArgs &a, Group<W> &g, const u
 
 // T tokens of a sequence and one kv head; W warps choose the pages of one token.
 template <int D, int T, int W>
-__global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const Kv4 c, const Kv4Batch b, const SelectArgs a)
+__global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T, T == 1 ? 1 : 3) select_kernel(const Kv4 c, const Kv4Batch b, const SelectArgs a)
 {
     constexpr int kThreads = T == 1 ? 32 * W : 32 * T;
     extern __shared__ __align__(16) uint32_t keys[]; // [T][the table's width]
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const 
     if (most > a.want) {
         // Pages up to the last query's own (which needs no score) are full. A group of eight lanes
         // asks for the bounds of kAhead of them together, the first ones before the queries' sums.
-        constexpr int kAhead = T == 1 ? 8 : 4, kStride = kThreads / 8;
+        constexpr int kAhead = T == 1 ? 8 : 2, kStride = kThreads / 8;
         const int per = (most - 1 + a.cluster - 1) / a.cluster;
         const int z0 = rank * per, z1 = min(most - 1, z0 + per);
         const int n = lane & 7, group = tid >> 3;
@@ -371,12 +371,6 @@ __global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const 
             query_sums<D>(a, a.q + (int64_t)(s.first + t0 + warp) * a.q_stride + (int64_t)head * a.ratio * D, sq[warp % T][0],
                           sq[warp % T][1]);
         __syncthreads();
-        Words<D> up[T], down[T];
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            up[t] = words_at<D>(&sq[t][0][n * (D / 8)]);
-            down[t] = words_at<D>(&sq[t][1][n * (D / 8)]);
-        }
         uint32_t to = smem_addr(keys), to_range = smem_addr(ranges);
         if (a.cluster > 1) {
             to = cluster_map(to, 0);
@@ -387,23 +381,27 @@ __global__ void __launch_bounds__(T == 1 ? 32 * W : 32 * T) select_kernel(const 
         for (int z = z0 + group; z - group < z1; z += kAhead * kStride) {
             if (z != z0 + group)
                 ask(z);
+            int sum[kAhead][8];
 #pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                int sum[8];
+            for (int t = 0; t < T; ++t) {
+                const Words<D> up = words_at<D>(&sq[t][0][n * (D / 8)]), down = words_at<D>(&sq[t][1][n * (D / 8)]);
 #pragma unroll
-                for (int t = 0; t < T; ++t) {
-                    sum[t] = 0;
+                for (int x = 0; x < kAhead; ++x) {
+                    sum[x][t] = 0;
 #pragma unroll
                     for (int w = 0; w < D / 32; ++w)
-                        sum[t] = __dp4a(up[t].w[w], hi[x].w[w], __dp4a(down[t].w[w], lo[x].w[w], sum[t]));
+                        sum[x][t] = __dp4a(up.w[w], hi[x].w[w], __dp4a(down.w[w], lo[x].w[w], sum[x][t]));
                 }
-                int mine = sum[0];
+            }
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                int mine = sum[x][0];
                 if (T == 1) {
 #pragma unroll
                     for (int o = 4; o; o >>= 1)
                         mine += __shfl_xor_sync(~0u, mine, o);
                 } else {
-                    mine = sum_across(sum, n);
+                    mine = sum_across(sum[x], n);
                 }
                 const int zx = z + x * kStride;
                 if (zx < z1 && n < T) {
