@@ -491,10 +491,10 @@ nm_status kv8_launch_select(const Kv4 &c, const Kv4Batch &b, const Kv8Select &x,
 {
     const SelectArgs a{x.layer, x.n_q_heads / c.n_kv_heads, x.count, x.first, x.last, (const uint16_t *)x.q, x.q_stride, x.pages, 0, 1};
     // tiles of tokens when there are several for each SM, and their scores fit
-    if (b.starts && b.n_tokens * c.n_kv_heads >= 4 * (int64_t)w.num_sms && (int64_t)kTile * (c.max_pages + 3) <= kKv8SelectPages)
+    if (b.starts && b.n_tokens * c.n_kv_heads >= 2 * (int64_t)w.num_sms && (int64_t)kTile * (c.max_pages + 3) <= kKv8SelectPages)
         return c.head_dim == 128 ? launch<128, kTile, 1>(c, b, a, 1, w, st) : launch<64, kTile, 1>(c, b, a, 1, w, st);
     int cluster = 1;
-    while (cluster < 8 && 2 * cluster * b.n_tokens * c.n_kv_heads <= w.num_sms && c.max_pages >= 256 * cluster)
+    while (cluster < 8 && cluster * b.n_tokens * c.n_kv_heads <= w.num_sms && c.max_pages >= 256 * cluster)
         cluster *= 2;
     return c.head_dim == 128 ? launch<128, 1, 8>(c, b, a, cluster, w, st) : launch<64, 1, 8>(c, b, a, cluster, w, st);
 }
