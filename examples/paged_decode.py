@@ -1,13 +1,14 @@
-"""A decode loop over pruned linears and the 4-bit paged KV cache.
+"""A decode loop over pruned linears and a paged KV cache, in 4 or 8 bits.
 
 A few decoder layers with random weights: the linears are pruned to 2:4 and run as the
 bitmask SpMV, the attention between qkv and o reads the paged cache. A prompt goes in
 eight tokens at a time (the largest batch of the SpMV), is forked into several
 continuations that share its full pages, and these are decoded together; then all but
 one are dropped and the pool is compacted. The "sampling" takes the next input from the
-last hidden state, so no vocabulary is needed.
+last hidden state, so no vocabulary is needed. With the 8-bit cache and --pages a step
+attends only the pages whose keys can have the largest scores.
 
-    python examples/paged_decode.py [--layers 2 --hidden 1024 --prompt 100 --steps 20]
+    python examples/paged_decode.py [--layers 2 --hidden 1024 --prompt 100 --steps 20 --bits 8 --pages 4]
 """
 from __future__ import annotations
 
@@ -32,10 +33,12 @@ class Decoder:
     """Decoder layers over one cache. ``step`` runs all of them on up to eight tokens."""
 
     def __init__(self, layers=2, hidden=1024, heads=8, kv_heads=2, dim=128, ffn=2048, sequences=4, tokens=512, page=16,
-                 seed=0, device="cuda"):
-        self.heads, self.kv_heads, self.dim = heads, kv_heads, dim
+                 seed=0, device="cuda", bits=4, pages=0):
+        if pages and bits != 8:
+            raise ValueError("pages are selected in the 8-bit cache")
+        self.heads, self.kv_heads, self.dim, self.pages = heads, kv_heads, dim, pages
         max_pages = -(-tokens // page)
-        self.cache = nm.Kv4Cache(sequences * max_pages, page, layers, kv_heads, dim, sequences, max_pages, device=device)
+        self.cache = (nm.Kv8Cache if bits == 8 else nm.Kv4Cache)(sequences * max_pages, page, layers, kv_heads, dim, sequences, max_pages, device=device)
         self.rope = rope_table(tokens, dim, device=device)
         g = torch.Generator(device=device).manual_seed(seed)
 
@@ -68,7 +71,8 @@ class Decoder:
             if trace is not None:
                 trace.append([q.clone(), k.clone(), v.clone()])
             c.append(i, k, v, q=q, rope=self.rope, seqs=seqs, starts=starts, q_out=q)
-            a = c.attention(i, q, seqs=seqs, starts=starts, max_new=1 if starts is None else x.shape[0])
+            part = {"pages": c.select(i, q, self.pages, seqs=seqs, starts=starts)} if self.pages else {}
+            a = c.attention(i, q, seqs=seqs, starts=starts, max_new=1 if starts is None else x.shape[0], **part)
             if trace is not None:
                 trace[-1].append(a)
             x = x + nm.spmv(*w["o"], a)
@@ -104,11 +108,12 @@ def run(decoder: Decoder, prompt: torch.Tensor, branches: int, steps: int):
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    for name, value in (("layers", 2), ("hidden", 1024), ("prompt", 100), ("branches", 3), ("steps", 20)):
+    for name, value in (("layers", 2), ("hidden", 1024), ("prompt", 100), ("branches", 3), ("steps", 20), ("bits", 4), ("pages", 0)):
         ap.add_argument(f"--{name}", type=int, default=value)
     a = ap.parse_args()
     nm.init()
-    d = Decoder(layers=a.layers, hidden=a.hidden, sequences=max(a.branches, 1), tokens=a.prompt + a.steps + 1)
+    d = Decoder(layers=a.layers, hidden=a.hidden, sequences=max(a.branches, 1), tokens=a.prompt + a.steps + 1,
+                bits=a.bits, pages=a.pages)
     prompt = torch.randn(a.prompt, a.hidden, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
     out = run(d, prompt, a.branches, a.steps)
     free, refused, moved = d.cache.info.tolist()[:3]

@@ -914,7 +914,11 @@ nm_status kv8_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
 {
     const AttnArgs a{at.layer, at.n_q_heads / c.n_kv_heads, at.n_q_heads, (const uint16_t *)at.q, at.q_stride,
                      at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials, pages, n_list};
+    // Figures: head size 128, 8 kv heads, us.
     if (pages) {
+        // 16 pages of 64 tokens, 32 heads: a warp per list against a CTA per piece of one. 20 tokens: 23 against 14, 140:
+        // 57 against 54, 160: 63 against 65, 512: 123 against 166. Eight lists an SM are a list for half of the warps.
+        // More than 16 query heads to a kv head are several tiles, which that kernel does not cut.
         const int rows = a.ratio;
         if (rows <= 16 && b.n_tokens * c.n_kv_heads >= 8 * (int64_t)w.num_sms) {
             if (c.head_dim == 64)
@@ -925,6 +929,18 @@ nm_status kv8_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
             return rows <= 8 ? launch<64, 1, true>(c, b, a, w, st) : launch<64, 2, true>(c, b, a, w, st);
         return rows <= 8 ? launch<128, 1, true>(c, b, a, w, st) : launch<128, 2, true>(c, b, a, w, st);
     }
+    // A sequence's rows and this kernel with 1, 2, 3 n-tiles, kv8_prompt.cu:
+    //   4 x 2 new tokens of 32 heads (8 rows), after 12288:    22, 28, 37,  77
+    //   4 x 4 of 32 heads (16 rows), after 12288:              33, 28, 38,  77
+    //   4 x 5 of 32 heads (20 rows), after 12288:              42, 41, 38,  76
+    //   8 x 3 of 64 heads (24 rows), after 8192:               55, 52, 46,  93
+    //   4 x 5 of 40 heads (25 rows), after 12288:              53, 42, 57,  78
+    //   1 x 16 of 32 heads (64 rows), after 32768:             65, 50, 55,  69
+    //   4 x 24 of 32 heads (96 rows), after 8192:              93, 68, 70,  61
+    //   4 x 64 of 32 heads (256 rows), after 8192:            231, 155, 167, 59
+    //   2 x 20 of 32 heads (80 rows), 1024 in all:             18, 17, 17,  30
+    //   1 x 32 of 32 heads (128 rows), 1032 in all:            14, 17, 17,  28, but after 32768 118, 83, 94, 63
+    // Lengths are on the device: a few rows of one sequence, which may be short, stay here.
     const int64_t rows = (max_new < 65 ? max_new : 65) * a.ratio;
     if (rows > 64 && b.n_tokens * at.n_q_heads > 1024)
         return kv8_launch_prompt(c, b, at, w, st);

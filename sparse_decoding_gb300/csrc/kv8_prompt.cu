@@ -5,23 +5,31 @@
 // share the kv head. A CTA works on a pair of 128-row tiles at a time and walks the
 // tokens they see in blocks of 128:
 //
-//   S = Q codes(K)^T    tcgen05.mma, Q and K in shared memory, S in tensor memory
+//   S = (Qh + Ql) codes(K)^T   tcgen05.mma kind::f8f6f4, both operands in shared memory, S in tensor memory
 //   P = 2^(S r s_K + e - m + 6)  one row per thread, written back to tensor memory as fp16
-//   O += P codes(V)     tcgen05.mma, P from tensor memory, V^T in shared memory
+//   O += P codes(V) 2^-d       tcgen05.mma kind::f16, P from tensor memory, V^T in shared memory
 //
-// Both operands of S are exact in fp16: the codes, and q scaled by a power of two per row.
-// The scales are powers of two of each cell (16 tokens): K's multiplies the scores in the
-// softmax, V's (2^e) is an exponent of the weights, and the sums of the weights are freed of it
-// again, sixteen columns at a time. Scores carry fp32 rounding only, as in the kernel for few rows.
+// Each row of q is scaled by a power of two and split into an e4m3 and an e5m2 part, whose sum it is (exactly,
+// down to 2^-13 of the row's largest): K's codes are an operand as they are stored, at the 8-bit rate, and no thread
+// has to make them fp16. S carries the fp32 rounding of the sums, as in the kernel for few rows.
+// The scales are powers of two of each cell (16 tokens). K's multiplies the scores in the softmax. V's codes are
+// made fp16 and brought to the largest of the block's eight scales, 2^e (d: how many binary places a cell's scale is
+// below it; exact down to 2^-15 of that), which is an exponent of the weights; the sums of the weights are freed of it
+// a block at a time.
 //
 // Roles (16 warps): two softmax warpgroups, one per tile (a thread owns a row: no
-// reductions across threads; it also loads and scales its row of Q, rescales and
-// stores its row of O); a warpgroup that makes the codes fp16 in two stages of K
-// and of V^T (both tiles use them); one warp that issues the MMAs; one that lists
-// the pieces of work. While one tile is in its softmax, the other's MMAs run. The
-// running maximum is raised only when a score passes it by 2^8, so O is rarely
-// rescaled. The next block's bytes are in the unpacking threads' registers before
-// the current one is written.
+// reductions across threads; it also loads and splits its row of Q, rescales and
+// stores its row of O); a warpgroup that copies the codes of K and V to shared memory, two blocks ahead, and makes V^T (both
+// tiles use them); one warp that issues the MMAs; one that lists the pieces of work. While one tile is in its
+// softmax, the other's MMAs run. The running maximum is raised only when a score passes it by 2^8, so O is rarely
+// rescaled.
+//
+// What bounds it: the softmax warpgroups' instructions and their fetch. The exponentials alone (16 a clock and SM)
+// take 230 us of the case below, its products 273 us at the measured bf16 rate, and the roles' loops together have to
+// stay in the instruction caches, so they are rolled. One sequence of 8192 new tokens, 32 query heads on 8 (0.55
+// TFLOP): K made fp16 beside V by 640 threads 705 us; K as an 8-bit operand 521; one copy of the MMA
+// step and masks written back once 502, 1.1 PFLOP/s. Not kept: the softmax unrolled 740, its maximum in steps of 64
+// columns 537, P passed on in halves 547.
 //
 // The blocks of all (sequence, kv head, pair) segments are one line, on which a
 // segment takes kOver blocks more (what starting and ending a piece costs), cut evenly
@@ -31,8 +39,6 @@
 // All waits are bounded; one that runs out sets NM_ERR_TIMEOUT. Its thread's later waits
 // poll once and its warp takes no more pieces, so the others run out in turn, the MMAs
 // in flight end, and the kernel frees its tensor memory and returns.
-#include <type_traits>
-
 #include "kv8.cuh"
 #include "kv_ops.cuh"
 
@@ -865,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                                h + x > 0 ? 1u : accumulate, one);
             };
             // O of block i of a piece (block n - 1 of the CTA), then S of block i + 1 (block n), tile by
-            // tile. The stages are constants of two copies of this, so that all descriptors are uniform.
+            // tile: one copy of this for both (two, and two of each for the stages: 521 against 502 us at 8192 tokens).
             int nblk, n0, n1;
             const auto step = [&](int i) {
                 const int nxt = __shfl_sync(~0u, n & 1, 0), cur = nxt ^ 1;

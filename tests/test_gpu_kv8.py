@@ -795,3 +795,101 @@ def test_attention_queries_of_wide_range(nm, max_new, heads):
     tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e[..., None] + 2.0 ** -14) * A + 300 * 2.0 ** -27
     assert np.all(np.abs(f64(out) - o) <= tol)
     assert nm.device_status() == nm.NM_OK
+
+
+@pytest.mark.parametrize("n", [0, 2, 100])
+def test_example_decode_loop(nm, n):
+    """The example's loop over the 8-bit cache, all of it (0), two selected pages, and more pages than there are:
+    every attention result against the definition, on the q, k, v that went in."""
+    from examples import paged_decode as ex
+    P = 16
+    d = ex.Decoder(layers=2, hidden=256, heads=8, kv_heads=2, dim=64, ffn=512, sequences=3, tokens=80, page=P, seed=5, bits=8, pages=n)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    prompt = torch.randn(53, 256, generator=g, device="cuda").bfloat16()
+    traces, step = [], d.step
+
+    def traced(x, seqs, starts=None):
+        t = []
+        y = step(x, seqs, starts, trace=t)
+        traces.append((seqs.tolist(), None if starts is None else starts.tolist(), t))
+        return y
+
+    d.step = traced
+    out = ex.run(d, prompt, 3, 14)
+    assert len(out) == 14 and nm.device_status() == nm.NM_OK
+    rope = d.rope.cpu().numpy()
+    held = [[ref.Sequence(2, 64) for _ in range(2)] for _ in range(3)]  # [sequence][layer]
+    for seqs, starts, layers in traces:
+        if starts is None and len(held[1][0].k) == 0:  # the fork came before the first joint step
+            for s in (1, 2):
+                held[s] = [h.copy() for h in held[0]]
+        starts = starts or list(range(len(seqs) + 1))
+        for layer, (q, k, v, a) in enumerate(layers):
+            q, k, v = (f32(t).reshape(t.shape[0], -1, 64) for t in (q, k, v))
+            for i, s in enumerate(seqs):
+                h = held[s][layer]
+                rows = slice(starts[i], starts[i + 1])
+                pos = np.arange(len(h.k), len(h.k) + starts[i + 1] - starts[i])
+                cos, sin = rope[pos, :32], rope[pos, 32:]
+                h.append(ref.rotate(k[rows], cos, sin), v[rows])
+                rq = ref.bf16(ref.rotate(q[rows], cos, sin))
+                m = len(h.k) - len(rq)
+                lists = np.array([ref.select(rq[j], h.k[:m + j + 1], P, n, 1, 1) for j in range(len(rq))]) if n else None
+                o, _, A, B = ref.attention(rq.astype(np.float64), h.k.astype(np.float64), h.v.astype(np.float64), len(h.k), 0.125, lists, P)
+                e = 2.0 ** -16 * B[..., None] + 2.0 ** -15
+                tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e + 2.0 ** -14) * A + 1e-6
+                assert np.all(np.abs(f64(a[rows]).reshape(o.shape) - o) <= tol)
+    assert d.cache.lens.tolist() == [67, 0, 0] and d.cache.info.tolist()[:2] == [d.cache.n_pages - 5, 0]
+
+
+def test_two_caches_on_two_streams(nm):
+    """Calls with caches of their own may overlap: each on a stream, alternating, as often as it takes to meet."""
+    D, P, H = 128, 64, 8
+    both = [make(nm, [3000, 700], P=P, Hk=2, D=D, seed=61 + i) for i in range(2)]
+    q = [values(2, H, D, 63 + i) for i in range(2)]
+    many = [values(300, H, D, 65 + i) for i in range(2)]
+    st = starts_of([250, 50])
+    want = [(c.attention(1, q[i]), c.select(1, q[i], 9), c.attention(1, many[i], starts=st)) for i, (c, _) in enumerate(both)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i, (c, _) in enumerate(both):
+            with torch.cuda.stream(streams[i]):
+                got[i].append((c.attention(1, q[i]), c.select(1, q[i], 9), c.attention(1, many[i], starts=st)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for x in got[i]:
+            for a, b in zip(x, want[i]):
+                assert torch.equal(a, b)
+    assert nm.device_status() == nm.NM_OK
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_page_filled_and_selected_in_one_call(nm, D):
+    """Drafted tokens that fill a page and go on: later ones of the call select it by its new bounds; appended again
+    (after a rejection the tokens are written anew) the bounds follow."""
+    P, Hk, H = 16, 1, 4
+    c, held = make(nm, [205, 260], P=P, L=1, Hk=Hk, D=D, extra=4, seed=97)  # the second: for a table of more pages
+    one = ints([0])
+    rope = rope_table(230, D)
+    cs = rope.cpu().numpy()
+    c.reserve(one, ints([0, 20]))
+    for seed in (1, 2):
+        h = held[0].copy()
+        k, v, q = values(20, Hk, D, 100 * seed, 2.0 * seed), values(20, Hk, D, 100 * seed + 1), values(20, H, D, 100 * seed + 2)
+        q = c.append(0, k, v, q=q, rope=rope, seqs=one, starts=ints([0, 20]))
+        cos, sin = cs[205:225, :D // 2], cs[205:225, D // 2:]
+        if seed == 2:  # a scale does not shrink until its block's first position is written again
+            h.e[12] = e_before
+            h.k[192:205], h.v[192:205] = kept
+        h.append(ref.rotate(f32(k), cos, sin), f32(v))
+        e_before, kept = h.e[12].copy(), (h.k[192:205].copy(), h.v[192:205].copy())
+        kk, vv = c.read(0, 225, one, ints([0, 225]), f32=True)
+        np.testing.assert_array_equal(f32(kk), h.k)
+        np.testing.assert_array_equal(f32(vv), h.v)
+        for n in (3, 6):
+            pages = c.select(0, q, n, one, ints([0, 20]))
+            for t in range(20):
+                np.testing.assert_array_equal(pages[t].cpu().numpy(), ref.select(f32(q[t]), h.k[:206 + t], P, n, 1, 1))
+    assert nm.device_status() == nm.NM_OK
