@@ -186,77 +186,105 @@ template <int D, int NT> struct Rows {
     {
         return make_float4(o[j][2 * q][n], o[j][2 * q][n + 2], o[j][2 * q + 1][n], o[j][2 * q + 1][n + 2]);
     }
-    // A cell in shared memory whose tokens begin at position tok. all: positions that every row sees;
-    // end: positions that hold tokens; q(j, z): B operands; limit(j, n): positions that a row sees.
-    template <class Q, class L>
-    __device__ __forceinline__ void take(const uint8_t *cell, int tok, int all, int end, int lane, const Q &qop, const L &limit)
+    // C cells in shared memory, one behind the other, whose tokens begin at positions tok. all: positions that every row
+    // sees; end: positions that hold tokens (a cell that begins there or beyond may hold anything); q(j, z): B operands;
+    // limit(j, n): positions that a row sees.
+    template <int C, class Q, class L>
+    __device__ __forceinline__ void take(const uint8_t *cells, const int (&tok)[C], int all, int end, int lane, const Q &qop,
+                                         const L &limit)
     {
         constexpr int G = D / 64;
         const int g = lane >> 2, t = lane & 3;
-        const float2 scales = *(const float2 *)(cell + Kv8Cell<D>::kScales);
-        // V's scale goes with the weights, as an exponent; the sums are freed of it again
-        const float ev = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);
-        const float iv = __uint_as_float((254u << 23) - __float_as_uint(scales.y));
+        float ks[C], ev[C], iv[C];
+        bool part = false;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float2 scales = *(const float2 *)(cells + c * Kv8Cell<D>::kBytes + Kv8Cell<D>::kScales);
+            if (C > 1 && tok[c] >= end)
+                scales = make_float2(1.0f, 1.0f);
+            ks[c] = scales.x;
+            // V's scale goes with the weights, as an exponent; the sums are freed of it again
+            ev[c] = (float)((int)(__float_as_uint(scales.y) >> 23) - 127);
+            iv[c] = __uint_as_float((254u << 23) - __float_as_uint(scales.y));
+            part |= tok[c] + kKv4Cell > all;
+        }
 
         // scores
-        float sc[NT][4];
+        float sc[C][NT][4];
         {
-            float acc[G][NT][4] = {};
+            float acc[C][G][NT][4] = {};
 #pragma unroll
             for (int e = 0; e < G; ++e) {
-                const uint4 x0 = *((const uint4 *)(cell + e * 512) + lane);
-                const uint4 x1 = *((const uint4 *)(cell + 8 * D + e * 512) + lane);
-                const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+                uint4 x0[C], x1[C];
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const uint32_t af[4] = {kv8_decode(w0[f]), kv8_decode(w1[f]), kv8_decode(w0[f] >> 16),
-                                            kv8_decode(w1[f] >> 16)};
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const int z = 4 * e + f;
-                        const uint2 q = qop(j, z);
-                        mma16816(acc[e][j], af, q.x, q.y);
-                    }
+                for (int c = 0; c < C; ++c) {
+                    x0[c] = *((const uint4 *)(cells + c * Kv8Cell<D>::kBytes + e * 512) + lane);
+                    x1[c] = *((const uint4 *)(cells + c * Kv8Cell<D>::kBytes + 8 * D + e * 512) + lane);
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int f = 0; f < 4; ++f) // token g + 8 (f / 2), row 2 t + f % 2
-                    sc[j][f] = (G == 2 ? acc[0][j][f] + acc[G - 1][j][f] : acc[0][j][f]) * scales.x;
-        }
-        // a row may see only part of the cell
-        if (tok + kKv4Cell > all) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int f = 0; f < 4; ++f)
-                    sc[j][f] = tok + g + 8 * (f >> 1) < limit(j, f & 1) ? sc[j][f] : -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const uint32_t w0 = f == 0 ? x0[c].x : f == 1 ? x0[c].y : f == 2 ? x0[c].z : x0[c].w;
+                        const uint32_t w1 = f == 0 ? x1[c].x : f == 1 ? x1[c].y : f == 2 ? x1[c].z : x1[c].w;
+                        const uint32_t af[4] = {kv8_decode(w0), kv8_decode(w1), kv8_decode(w0 >> 16), kv8_decode(w1 >> 16)};
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const uint2 q = qop(j, 4 * e + f);
+                            mma16816(acc[c][e][j], af, q.x, q.y);
+                        }
+                    }
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) // token g + 8 (f / 2), row 2 t + f % 2
+                        sc[c][j][f] = (G == 2 ? acc[c][0][j][f] + acc[c][G - 1][j][f] : acc[c][0][j][f]) * ks[c];
+        }
+        // a row may see only part of a cell
+        if (part) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        sc[c][j][f] = tok[c] + g + 8 * (f >> 1) < limit(j, f & 1) ? sc[c][j][f] : -INFINITY;
         }
         float top = -INFINITY;
-        float y[NT][4];
+        float y[C][NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                y[j][f] = fmaf(sc[j][f], scale[j][f & 1], mo[j][f & 1] + ev);
-                top = fmaxf(top, y[j][f]);
-            }
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    y[c][j][f] = fmaf(sc[c][j][f], scale[j][f & 1], mo[j][f & 1] + ev[c]);
+                    top = fmaxf(top, y[c][j][f]);
+                }
         if (__any_sync(~0u, top > kShift + kSlack)) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    float z = fmaxf(sc[j][n], sc[j][n + 2]);
+                    float z = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        z = fmaxf(z, fmaf(fmaxf(sc[c][j][n], sc[c][j][n + 2]), scale[j][n], ev[c]));
                     z = fmaxf(z, __shfl_xor_sync(~0u, z, 4));
                     z = fmaxf(z, __shfl_xor_sync(~0u, z, 8));
-                    z = fmaf(fmaxf(z, __shfl_xor_sync(~0u, z, 16)), scale[j][n], ev);
+                    z = fmaxf(z, __shfl_xor_sync(~0u, z, 16));
                     const float was = mo[j][n], now = z == -INFINITY ? was : fminf(was, kShift - z);
                     const float by = was == now ? 1.0f : exp2_approx(now - was);
                     mo[j][n] = now;
                     l[j][n] *= by;
-                    y[j][n] = fmaf(sc[j][n], scale[j][n], now + ev);
-                    y[j][n + 2] = fmaf(sc[j][n + 2], scale[j][n], now + ev);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        y[c][j][n] = fmaf(sc[c][j][n], scale[j][n], now + ev[c]);
+                        y[c][j][n + 2] = fmaf(sc[c][j][n + 2], scale[j][n], now + ev[c]);
+                    }
 #pragma unroll
                     for (int z4 = 0; z4 < D / 16; ++z4) {
                         o[j][z4][n] *= by;
@@ -264,36 +292,41 @@ template <int D, int NT> struct Rows {
                     }
                 }
         }
-        uint32_t pb[NT][2];
+        uint32_t pb[C][NT][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            float p[4];
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                p[f] = exp2_approx(y[j][f]);
-                l[j][f & 1] = fmaf(p[f], iv, l[j][f & 1]);
+            for (int j = 0; j < NT; ++j) {
+                float p[4];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    p[f] = exp2_approx(y[c][j][f]);
+                    l[j][f & 1] = fmaf(p[f], iv[c], l[j][f & 1]);
+                }
+                pb[c][j][0] = transpose8x8(pack_half2(p[0], p[1]));
+                pb[c][j][1] = transpose8x8(pack_half2(p[2], p[3]));
             }
-            pb[j][0] = transpose8x8(pack_half2(p[0], p[1]));
-            pb[j][1] = transpose8x8(pack_half2(p[2], p[3]));
-        }
 
         // O^T += V^T P^T; tokens past the last that is seen hold anything: their V is taken as 0
-        const int left = end - tok;
-        uint32_t keep = ~0u;
-        if (left < kKv4Cell)
-            keep = (2 * t < left ? 0xFFu : 0u) | (2 * t + 1 < left ? 0xFF00u : 0u) | (2 * t + 8 < left ? 0xFF0000u : 0u) |
-                   (2 * t + 9 < left ? 0xFF000000u : 0u);
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-            const uint4 x4 = *((const uint4 *)(cell + Kv8Cell<D>::kV + q * 512) + lane);
-            const uint32_t w[4] = {x4.x & keep, x4.y & keep, x4.z & keep, x4.w & keep};
+        for (int c = 0; c < C; ++c) {
+            const int left = end - tok[c];
+            uint32_t keep = ~0u;
+            if (left < kKv4Cell)
+                keep = (2 * t < left ? 0xFFu : 0u) | (2 * t + 1 < left ? 0xFF00u : 0u) | (2 * t + 8 < left ? 0xFF0000u : 0u) |
+                       (2 * t + 9 < left ? 0xFF000000u : 0u);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t af[4] = {kv8_decode(w[2 * h]), kv8_decode(w[2 * h + 1]), kv8_decode(w[2 * h] >> 16),
-                                        kv8_decode(w[2 * h + 1] >> 16)};
+            for (int q = 0; q < D / 32; ++q) {
+                const uint4 x4 = *((const uint4 *)(cells + c * Kv8Cell<D>::kBytes + Kv8Cell<D>::kV + q * 512) + lane);
+                const uint32_t w[4] = {x4.x & keep, x4.y & keep, x4.z & keep, x4.w & keep};
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    mma16816(o[j][2 * q + h], af, pb[j][0], pb[j][1]);
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t af[4] = {kv8_decode(w[2 * h]), kv8_decode(w[2 * h + 1]), kv8_decode(w[2 * h] >> 16),
+                                            kv8_decode(w[2 * h + 1] >> 16)};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        mma16816(o[j][2 * q + h], af, pb[c][j][0], pb[c][j][1]);
+                }
             }
         }
     }
@@ -578,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                 break;
             }
             if (have >> st & 1u)
-                r.take(ring + st * SM::kStage, sm_first[st], tile_first, s.len, lane,
+                r.template take<1>(ring + st * SM::kStage, {sm_first[st]}, tile_first, s.len, lane,
                        [&](int j, int z) { return kKeepQ ? qb[z % (kKeepQ ? KS : 1)] : sm_q[(j * KS + z) * 32 + lane]; },
                        [&](int j, int n) { return sm_info[8 * j + 2 * t + n].limit; });
         }
@@ -724,19 +757,32 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
 }
 
 // With lists and many of them: a warp takes a token's kv head by itself, all of its list, so that no threads
-// meet. Q is in its registers, and a lane has two rows' output of four channels in 32.
+// meet, two cells at a time, whose chains of instructions overlap: 12 warps of two cells have as much under way as 24 of
+// one, for whose registers and rings there is no room. Q is in its registers, and a lane has two rows' output of four
+// channels in 32. Lists are dealt over the SMs before their warps, so that a last round is spread evenly. 512 tokens
+// of 16 pages of 64 tokens, 32 heads on 8: 116 us (a cell at a time by 16 warps 123), 9.3 TB/s of cells, most of them
+// from L2; what bounds it is the latency of a warp's chain: it issues an instruction in 60% of the cycles.
+template <int D, int NT> struct Lists {
+    static constexpr int kWarps = NT == 1 ? 12 : 8, kThreads = 32 * kWarps;
+    static constexpr int kCells = 2; // of a stage: those of one copy, which a cell of its own page is not part of
+    static constexpr int kStages = (NT == 1 ? 2 : 3) * (128 / D), kStage = kCells * Kv8Cell<D>::kBytes;
+    static constexpr int kBytes = kWarps * kStages * kStage;
+    static_assert(kBytes <= 200 * 1024, "shared memory");
+};
+constexpr int kAbsent = 0x7FFFFF00; // the first token of a cell that is not there: seen by no row
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv8_lists_kernel(const Kv4 c, const Kv4Batch b, const AttnArgs a)
+__global__ void __launch_bounds__(Lists<D, NT>::kThreads, 1) kv8_lists_kernel(const Kv4 c, const Kv4Batch b, const AttnArgs a)
 {
+    using LS = Lists<D, NT>;
+    constexpr int kWarps = LS::kWarps, kThreads = LS::kThreads, S = LS::kStages, C = LS::kCells;
     constexpr int G = D / 64, KS = 4 * G;
-    using SM = Smem<D, 1>;
-    constexpr int S = NT == 1 ? SM::kStages : 2 * SM::kStages - 1;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_bars[kWarps * S];
-    __shared__ int s_first[kWarps * S];
+    __shared__ int s_first[kWarps * S][C];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    uint8_t *const ring = smem + warp * S * SM::kStage;
-    int *const first_of = s_first + warp * S;
+    uint8_t *const ring = smem + warp * S * LS::kStage;
+    int(*const first_of)[C] = s_first + warp * S;
     const uint32_t rings = smem_addr(ring), bars = smem_addr(s_bars) + warp * S * 8;
     if (lane == 0)
         for (int i = 0; i < S; ++i)
@@ -751,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv8_lists_kernel(co
     uint32_t used = 0;
     bool dead = false;
 #pragma unroll 1
-    for (int64_t seg = (int64_t)blockIdx.x * kWarps + warp; seg < segments; seg += (int64_t)gridDim.x * kWarps) {
+    for (int64_t seg = (int64_t)warp * gridDim.x + blockIdx.x; seg < segments; seg += (int64_t)gridDim.x * kWarps) {
         const int64_t token = quotient(seg, c.n_kv_heads);
         const int head = (int)(seg - token * c.n_kv_heads);
         // the rows of Q: row 8 j + g, channels 64 e + 16 t ..
@@ -773,34 +819,47 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv8_lists_kernel(co
         const int64_t seen = i >= 0 && s.first >= 0 && token - s.first < s.n_new ? s.len - s.n_new + (token - s.first) + 1 : 0;
         const int most = s.len, limit = seen > 0 && s.len > 0 ? (int)seen : 0;
         const int32_t *const list = a.pages + seg * a.n_list;
-        int mine = dead || limit == 0 ? 0 : a.n_list << shift;
+        const int cells = a.n_list << shift;
+        int mine = dead || limit == 0 ? 0 : (cells + C - 1) / C; // stages
         const uint8_t *const heads = c.pool + kv8_head_offset<D>(c, 0, a.layer, head);
         uint64_t where = 0;
-        int begins = 0;
+        int begins = kAbsent;
         uint32_t have = 0;
         const auto fetch = [&](int x) {
-            if ((x & 31) == 0) {
+            const int z = C * x;
+            if ((z & 31) == 0) {
                 where = 0;
-                if (x + lane < mine)
-                    where = listed_cell<D>(c, s.row, heads, list, x + lane, most, limit, &begins);
+                begins = kAbsent;
+                if (z + lane < cells)
+                    where = listed_cell<D>(c, s.row, heads, list, z + lane, most, limit, &begins);
+                if (where == 0)
+                    begins = kAbsent;
                 // nothing is listed from here on
                 if (x > 0 && !__any_sync(~0u, where != 0)) {
-                    const bool rest = x + lane < mine && list[(x + lane) >> shift] != -1;
+                    const bool rest = z + lane < cells && list[(z + lane) >> shift] != -1;
                     if (!__any_sync(~0u, rest))
                         mine = x;
                 }
             }
             if (x >= mine)
                 return;
-            const uint64_t src = __shfl_sync(~0u, where, x & 31);
-            const int first = __shfl_sync(~0u, begins, x & 31);
             const uint32_t st = (used + x) % S, bar = bars + 8 * st;
-            have = (have & ~(1u << st)) | (uint32_t)(src != 0) << st;
-            if (lane == 0) {
-                first_of[st] = first;
-                mbar_arrive_expect_tx(bar, src ? Kv8Cell<D>::kBytes : 0u);
-                if (src)
-                    bulk_load(rings + st * SM::kStage, (const void *)src, Kv8Cell<D>::kBytes, bar);
+            const uint32_t there = __ballot_sync(~0u, where != 0) >> (z & 31) & ((1u << C) - 1);
+            have = (have & ~(1u << st)) | (uint32_t)(there != 0) << st;
+            // the lanes of the stage's cells; of cells side by side the first one copies both
+            static_assert(C == 2, "the second lane tells whether they are");
+            const int who = lane - (z & 31);
+            const uint64_t before = __shfl_up_sync(~0u, where, 1);
+            const bool joined = where != 0 && who == 1 && where == before + Kv8Cell<D>::kBytes && before != 0;
+            const uint32_t pair = __ballot_sync(~0u, joined);
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, __popc(there) * Kv8Cell<D>::kBytes);
+            __syncwarp();
+            if (who >= 0 && who < C) {
+                first_of[st][who] = begins;
+                if (where != 0 && !joined)
+                    bulk_load(rings + st * LS::kStage + who * Kv8Cell<D>::kBytes, (const void *)where,
+                              Kv8Cell<D>::kBytes << (who == 0 && pair != 0), bar);
             }
             __syncwarp();
         };
@@ -835,8 +894,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv8_lists_kernel(co
                 break;
             }
             if (have >> st & 1u)
-                r.take(ring + st * SM::kStage, first_of[st], limit, limit, lane, [&](int j, int z) { return qb[j][z]; },
-                       [&](int, int) { return limit; });
+                r.template take<C>(ring + st * LS::kStage, {first_of[st][0], first_of[st][1]}, limit, limit, lane,
+                                   [&](int j, int z) { return qb[j][z]; }, [&](int, int) { return limit; });
         }
         used += mine;
 #pragma unroll
@@ -886,15 +945,14 @@ nm_status launch(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, const Kv4Wo
 template <int D, int NT>
 nm_status launch_lists(const Kv4 &c, const Kv4Batch &b, const AttnArgs &a, const Kv4Work &w, cudaStream_t st)
 {
-    constexpr int kStages = NT == 1 ? Smem<D, 1>::kStages : 2 * Smem<D, 1>::kStages - 1;
-    constexpr int kBytes = kWarps * kStages * Smem<D, 1>::kStage;
+    using LS = Lists<D, NT>;
     static OncePerDevice once;
     if (!once(w.device, [] {
-            return cudaFuncSetAttribute(kv8_lists_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) ==
+            return cudaFuncSetAttribute(kv8_lists_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, LS::kBytes) ==
                    cudaSuccess;
         }))
         return NM_ERR_CUDA;
-    kv8_lists_kernel<D, NT><<<(unsigned)(w.num_sms * (NT == 1 ? 2 : 1)), kThreads, kBytes, st>>>(c, b, a);
+    kv8_lists_kernel<D, NT><<<(unsigned)w.num_sms, LS::kThreads, LS::kBytes, st>>>(c, b, a);
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
 
@@ -916,11 +974,11 @@ nm_status kv8_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
                      at.scale, (uint16_t *)at.out, at.out_stride, at.lse, w.counters, w.partials, pages, n_list};
     // Figures: head size 128, 8 kv heads, us.
     if (pages) {
-        // 16 pages of 64 tokens, 32 heads: a warp per list against a CTA per piece of one. 20 tokens: 23 against 14, 140:
-        // 57 against 54, 160: 63 against 65, 512: 123 against 166. Eight lists an SM are a list for half of the warps.
+        // 16 pages of 64 tokens, a CTA per piece of a list against a warp per list. 32 heads: 20 tokens 14 against 23; 80: 35,
+        // 37; 110: 43, 38; 160: 60, 45; 512: 166, 116. 128 heads: 40 tokens 31 against 37; 80: 48, 47; 110: 61, 48; 512: 226, 172.
         // More than 16 query heads to a kv head are several tiles, which that kernel does not cut.
         const int rows = a.ratio;
-        if (rows <= 16 && b.n_tokens * c.n_kv_heads >= 8 * (int64_t)w.num_sms) {
+        if (rows <= 16 && b.n_tokens * c.n_kv_heads >= 5 * (int64_t)w.num_sms) {
             if (c.head_dim == 64)
                 return rows <= 8 ? launch_lists<64, 1>(c, b, a, w, st) : launch_lists<64, 2>(c, b, a, w, st);
             return rows <= 8 ? launch_lists<128, 1>(c, b, a, w, st) : launch_lists<128, 2>(c, b, a, w, st);

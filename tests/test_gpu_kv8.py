@@ -893,3 +893,41 @@ def test_page_filled_and_selected_in_one_call(nm, D):
             for t in range(20):
                 np.testing.assert_array_equal(pages[t].cpu().numpy(), ref.select(f32(q[t]), h.k[:206 + t], P, n, 1, 1))
     assert nm.device_status() == nm.NM_OK
+
+
+@pytest.mark.parametrize("D,P,Hq", [(128, 64, 8), (64, 32, 10), (128, 32, 3)])
+def test_many_lists_of_pages_of_several_cells(nm, D, P, Hq):
+    """A warp's cells come two at a time: lists of odd and even length, pages that end inside a pair, a page that the
+    table does not name, and NaN in whatever lies behind the last token."""
+    c, held = make(nm, [1200, 2 * P + 17], P=P, L=1, Hk=1, D=D, extra=1, seed=41)
+    new = [1000, 2 * P + 17]
+    T = sum(new)
+    q = values(T, Hq, D, 42)
+    starts = starts_of(new)
+    pages = c.select(0, q, 5, starts=starts)
+    pages[10:200, 0, 3:] = -1
+    pages[200:300, 0, 1:] = -1
+    q[40, 1, 3] = float("inf")
+    out, lse = c.attention(0, q, starts=starts, pages=pages, lse=True)
+    assert nm.device_status() == nm.NM_OK
+    assert bool(torch.isnan(out[40, 1]).all()) and int(torch.isnan(out).sum()) == D
+    q[40, 1, 3] = 0.0
+
+    def right(t, s, m, listed, out, lse):
+        o, l, A, B = ref.attention(f64(q[t:t + 1]), held[s].k[:m].astype(np.float64), held[s].v[:m].astype(np.float64), m,
+                                   D ** -0.5, listed, P)
+        e = 2.0 ** -16 * B + 2.0 ** -15
+        tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e[..., None] + 2.0 ** -14) * A + m * 2.0 ** -27
+        return np.all(np.abs(f64(lse[t:t + 1]) - l) <= e) and np.all(np.abs(f64(out[t:t + 1]) - o) <= tol)
+
+    for t in [0, 9, 10, 41, 199, 200, 299, 300, 999] + list(range(1000, T)):
+        s, m = (0, 201 + t) if t < 1000 else (1, t - 999)
+        assert right(t, s, m, pages[t:t + 1].cpu().numpy(), out, lse), t
+    c.tables[0, 0] = -1  # as if page 0 were not listed
+    o2, l2 = c.attention(0, q, starts=starts, pages=pages, lse=True)
+    assert nm.device_status() == nm.NM_ERR_BOUNDS
+    assert torch.equal(o2[1000:], out[1000:])
+    for t in (0, 10, 300, 999):
+        rest = pages[t:t + 1].cpu().numpy()
+        rest = np.concatenate([rest[..., 1:], np.full_like(rest[..., :1], -1)], -1) if rest[0, 0, 0] == 0 else rest
+        assert right(t, 0, 201 + t, rest, o2, l2), t
