@@ -669,6 +669,8 @@ nm_status nm_kv4_attention(const nm_kv4_cache *cache, int layer, const int32_t *
  * workspace bytes from the two calls below): the tables are kept by the same rules. Beside them:
  *   - A fork copies the cells of the partial last page; full pages are shared with their bounds.
  *   - A sequence listed twice in one nm_kv8_append gets no defined values there.
+ *   - The struct does not tell the format. A cache is used with the calls of one of the two only, and
+ *     nm_kv8_copy_pages copies between caches that both are in 8 bits.
  */
 typedef nm_kv4_cache nm_kv8_cache;
 
@@ -707,9 +709,13 @@ nm_status nm_kv8_read(const nm_kv8_cache *cache, int layer, const int32_t *seqs,
  *          An entry that is out of range of the sequence, or does not ascend, is passed over and
  *          reported (NM_ERR_BOUNDS). A query with nothing listed gives out 0 and lse -inf.
  *   n_list: 1 .. 49152 (with pages; NM_ERR_UNSUPPORTED above). max_new is not used then.
- * q is scaled by a power of two for each row and held in fp16, as there. Scores are exact products of it with
- * the keys as held, summed in fp32; weights are rounded to fp16 (2^-11) for the product with V, whose codes
- * are exact; statistics, sums and the output are held in fp32. Results repeat bit for bit.
+ * q is scaled by a power of two for each row. For few query rows and over listed pages it is held in fp16: exact down
+ * to 2^-17 of the row's largest magnitude, off by at most 2^-25 of it below. For prompts it is held in two 8-bit
+ * parts: exact down to 2^-13 of the row's largest, off by at most 2^-21 of it below. Scores are exact products of
+ * that with the keys as held, summed in fp32. Weights are rounded to fp16 (2^-11) for the product with V, whose codes are
+ * exact; for prompts they are brought to the largest scale S of 128 tokens, which takes away what is below 2^-25 S.
+ * Statistics and sums are held in fp32. A query row with a NaN or an infinity that sees any token gives NaN in its out and
+ * lse and in no others. Results repeat bit for bit.
  */
 nm_status nm_kv8_attention(const nm_kv8_cache *cache, int layer, const int32_t *seqs, const int32_t *starts,
                            int n_seqs, int64_t n_tokens, int64_t max_new, const void *q_bf16, int64_t q_stride,
