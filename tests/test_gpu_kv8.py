@@ -931,3 +931,98 @@ def test_many_lists_of_pages_of_several_cells(nm, D, P, Hq):
         rest = pages[t:t + 1].cpu().numpy()
         rest = np.concatenate([rest[..., 1:], np.full_like(rest[..., :1], -1)], -1) if rest[0, 0, 0] == 0 else rest
         assert right(t, 0, 201 + t, rest, o2, l2), t
+
+
+def test_a_thousand_sequences_and_one_listed_often(nm):
+    """1024 sequences in one call of each kind and kernel, and a sequence that a call lists more than once: each
+    listing is answered as by itself."""
+    D, P, Hk, H, S = 64, 16, 1, 8, 1024
+    r = np.random.RandomState(7)
+    lens = [int(x) for x in r.randint(0, 40, S)]
+    c, held = make(nm, lens, P=P, L=1, Hk=Hk, D=D, extra=S, seed=101, max_seqs=S)  # a page more for each
+    k, v, q = values(S, Hk, D, 102), values(S, Hk, D, 103), values(S, H, D, 104)
+    c.reserve(n=S)
+    assert c.info[1] == 0
+    c.append(0, k, v)
+    for i, h in enumerate(held):
+        h.append(f32(k[i:i + 1]), f32(v[i:i + 1]))
+    lists = c.select(0, q, 2)
+    out, part = c.attention(0, q), c.attention(0, q, pages=lists)
+    kk, vv = c.read(0, S, f32=True)
+    long = [i for i in range(S) if lens[i] >= 3]
+    starts = starts_of([3 if n >= 3 else 0 for n in lens])  # drafted tokens of most of them
+    q3 = values(int(starts[-1]), H, D, 105)
+    few = c.attention(0, q3, starts=starts, max_new=3)
+    lists3 = c.select(0, q3, 2, starts=starts)
+    part3 = c.attention(0, q3, starts=starts, pages=lists3)
+    q9 = q3.repeat(1, 6, 1)  # 48 heads and no bound on the new tokens: the kernel for prompts
+    many = c.attention(0, q9, starts=starts)
+    assert nm.device_status() == nm.NM_OK
+
+    def right(got, q, i, m, listed=None):
+        o, _, A, B = ref.attention(f64(q), held[i].k[:m].astype(np.float64), held[i].v[:m].astype(np.float64), m, D ** -0.5,
+                                   listed, P)
+        e = 2.0 ** -16 * B + 2.0 ** -15
+        return np.all(np.abs(f64(got) - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e[..., None] + 2.0 ** -14) * A + m * 2.0 ** -27)
+
+    for i in r.choice(S, 60, replace=False).tolist() + [0, S - 1]:
+        n = lens[i] + 1
+        np.testing.assert_array_equal(f32(kk[i]), held[i].k[-1])
+        np.testing.assert_array_equal(f32(vv[i]), held[i].v[-1])
+        np.testing.assert_array_equal(lists[i].cpu().numpy(), ref.select(f32(q[i]), held[i].k, P, 2, 1, 1))
+        assert right(out[i:i + 1], q[i:i + 1], i, n) and right(part[i:i + 1], q[i:i + 1], i, n, lists[i:i + 1].cpu().numpy())
+        for t in range(int(starts[i]), int(starts[i + 1])):
+            m = n - 2 + t - int(starts[i])
+            np.testing.assert_array_equal(lists3[t].cpu().numpy(), ref.select(f32(q3[t]), held[i].k[:m], P, 2, 1, 1))
+            assert right(few[t:t + 1], q3[t:t + 1], i, m) and right(many[t:t + 1], q9[t:t + 1], i, m)
+            assert right(part3[t:t + 1], q3[t:t + 1], i, m, lists3[t:t + 1].cpu().numpy())
+    ids = [long[0], long[1], long[0], long[0], long[2]]  # one sequence three times
+    again = c.attention(0, q[:5], seqs=ints(ids))
+    la = c.select(0, q[:5], 2, seqs=ints(ids))
+    pa = c.attention(0, q[:5], seqs=ints(ids), pages=la)
+    ka, _ = c.read(0, 5, seqs=ints(ids), f32=True)
+    for j, i in enumerate(ids):
+        n = lens[i] + 1
+        assert right(again[j:j + 1], q[j:j + 1], i, n) and right(pa[j:j + 1], q[j:j + 1], i, n, la[j:j + 1].cpu().numpy())
+        np.testing.assert_array_equal(f32(ka[j]), held[i].k[-1])
+    q5 = values(15, 48, D, 106)
+    m5 = c.attention(0, q5, seqs=ints(ids), starts=ints([0, 3, 6, 9, 12, 15]))
+    for j, i in enumerate(ids):
+        assert right(m5[3 * j + 2:3 * j + 3], q5[3 * j + 2:3 * j + 3], i, lens[i] + 1)
+    assert nm.device_status() == nm.NM_OK
+
+
+def test_prompt_and_lists_captured_and_replayed(nm):
+    """The kernels for prompts and for many lists in one graph, replayed while the lengths and the rows' cuts change."""
+    D, P, Hk, H = 128, 16, 2, 32
+    c, held = make(nm, [700, 300], P=P, L=1, Hk=Hk, D=D, seed=111)
+    q = values(900, H, D, 112)
+    starts, pages = starts_of([700, 200]), torch.empty(900, Hk, 7, dtype=torch.int32, device="cuda")
+    out, part = torch.empty_like(q), torch.empty_like(q)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        c.attention(0, q, starts=starts, out=out)
+        c.select(0, q, 7, starts=starts, out=pages)
+        c.attention(0, q, starts=starts, pages=pages, out=part)
+    for new, drop in (([700, 200], 0), ([1, 300], 0), ([600, 300], 100), ([0, 0], 0), ([650, 250], 0)):
+        c.lens[0] = 700 - drop
+        starts.copy_(starts_of(new))
+        out.fill_(3.0), part.fill_(3.0), pages.fill_(9)
+        g.replay()
+        assert nm.device_status() == nm.NM_OK
+        n = sum(new)
+        assert bool((out[n:] == 0).all()) and bool((part[n:] == 0).all()) and bool((pages[n:] == -1).all())
+        at = 0
+        for i, m in enumerate(new):
+            L = len(held[i].k) - (drop if i == 0 else 0)
+            for t in sorted({0, 1, m // 2, m - 1} & set(range(m))):
+                pos, x = L - m + t, at + t
+                for got, listed in ((out, None), (part, pages[x:x + 1].cpu().numpy())):
+                    o, _, A, B = ref.attention(f64(q[x:x + 1]), held[i].k[:pos + 1].astype(np.float64),
+                                               held[i].v[:pos + 1].astype(np.float64), pos + 1, D ** -0.5, listed, P)
+                    e = 2.0 ** -16 * B + 2.0 ** -15
+                    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e[..., None] + 2.0 ** -14) * A + (pos + 1) * 2.0 ** -27
+                    assert np.all(np.abs(f64(got[x:x + 1]) - o) <= tol)
+                np.testing.assert_array_equal(listed[0], ref.select(f32(q[x]), held[i].k[:pos + 1], P, 7, 1, 1))
+            at += m
