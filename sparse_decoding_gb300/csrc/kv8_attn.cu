@@ -34,7 +34,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int64_t kMinShare = 8;  // cells of a CTA at least: one for each warp
 constexpr int kWhole = 32;        // when none has more cells than this, no segment is cut
 constexpr float kMoreUnits = 24.0f; // a second piece costs about as many cells
-constexpr int kOver = 16;         // cells that starting and ending a piece costs as much as
+constexpr int kOver = 32;         // cells that starting and ending a piece costs as much as (4 x 5 tokens: 42.4 us, with 16 44.1)
 constexpr float kShift = 6.0f;    // p = 2^(s + e - m + kShift)
 constexpr float kSlack = 8.0f;    // a score may pass m by this much
 constexpr float kNone = 1e38f;
@@ -704,18 +704,43 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                 const auto at = [&](int k) {
                     return a.partials + ((int64_t)(first + k) * 2 + (k > 0 ? 0 : 1)) * part_floats<D, NT>();
                 };
+                // O of the first parts is asked for before the weights, 16 parts at a time (8 at a time and after the weights:
+                // 131071 tokens, 38 parts 55.0 us, now 54.5; one token of 32 pages 21.2, 19.8 with its selection)
+                constexpr int kBatch = 16;
+                float4 z[kBatch];
+                const auto ask = [&](int x, int k0) {
+                    const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        z[k] = k0 + k < n ? __ldcg((const float4 *)(at(k0 + k) + 2 * RT + row * D + ch))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                };
+                if (tid < RT * (D / 4))
+                    ask(tid, 0);
                 for (int row = warp; row < RT; row += kWarps) {
-                    float M = -INFINITY, L = 0.0f;
-                    for (int k = lane; k < n; k += 32)
+                    float mk[2], lk[2], M = -INFINITY, L = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int k = lane + 32 * u;
+                        mk[u] = k < n ? ldcg_f32(at(k) + row) : -INFINITY;
+                        lk[u] = k < n ? ldcg_f32(at(k) + RT + row) : 0.0f;
+                        M = fmaxf(M, mk[u]);
+                    }
+                    for (int k = lane + 64; k < n; k += 32)
                         M = fmaxf(M, ldcg_f32(at(k) + row));
                     for (int z = 16; z; z >>= 1)
                         M = fmaxf(M, __shfl_xor_sync(~0u, M, z));
-                    for (int k = lane; k < n; k += 32) {
-                        const float mk = ldcg_f32(at(k) + row);
-                        const float f = mk == M ? 1.0f : exp2_approx(mk - M);
+                    const auto weigh = [&](int k, float m, float l) {
+                        const float f = m == M ? 1.0f : exp2_approx(m - M);
                         weight[k * RT + row] = f;
-                        L = fmaf(f, ldcg_f32(at(k) + RT + row), L);
-                    }
+                        L = fmaf(f, l, L);
+                    };
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (lane + 32 * u < n)
+                            weigh(lane + 32 * u, mk[u], lk[u]);
+                    for (int k = lane + 64; k < n; k += 32)
+                        weigh(k, ldcg_f32(at(k) + row), ldcg_f32(at(k) + RT + row));
                     for (int z = 16; z; z >>= 1)
                         L += __shfl_xor_sync(~0u, L, z);
                     if (lane == 0) {
@@ -727,14 +752,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
                 for (int x = tid; x < RT * (D / 4); x += kThreads) {
                     const int row = x / (D / 4), ch = (x % (D / 4)) * 4;
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k0 = 0; k0 < n; k0 += 8) {
-                        float4 z[8];
+                    for (int k0 = 0; k0 < n; k0 += kBatch) {
+                        if (x != tid || k0 > 0)
+                            ask(x, k0);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            z[k] = k0 + k < n ? __ldcg((const float4 *)(at(k0 + k) + 2 * RT + row * D + ch))
-                                              : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < kBatch; ++k) {
                             const float f = k0 + k < n ? weight[(k0 + k) * RT + row] : 0.0f;
                             y.x = fmaf(f, z[k].x, y.x);
                             y.y = fmaf(f, z[k].y, y.y);
