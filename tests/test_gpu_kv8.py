@@ -1026,3 +1026,23 @@ def test_prompt_and_lists_captured_and_replayed(nm):
                     assert np.all(np.abs(f64(got[x:x + 1]) - o) <= tol)
                 np.testing.assert_array_equal(listed[0], ref.select(f32(q[x]), held[i].k[:pos + 1], P, 7, 1, 1))
             at += m
+
+
+def test_prompts_and_many_lists_past_4_gib(nm):
+    """The kernels for prompts, for tiles of tokens and for many lists over pages whose bytes lie past 2^32 of the pool."""
+    P, L, Hk, D = 128, 32, 8, 128
+    per = nm.lib().nm_kv8_page_bytes(P, L, Hk, D)
+    n = (1 << 32) // per + 8
+    c = nm.Kv8Cache(n, P, L, Hk, D, 1, 4)
+    c.refs.fill_(1)  # only the last four pages are free
+    c.refs[n - 4:] = 0
+    c.info[0] = 4
+    c.reserve(starts=ints([0, 500]))
+    k, v = values(500, Hk, D, 141), values(500, Hk, D, 142)
+    c.append(L - 1, k, v, starts=ints([0, 500]))
+    h = ref.Sequence(Hk, D)
+    h.append(f32(k), f32(v))
+    check(nm, c, [h], [120], 16, L - 1, max_new=120)  # 240 rows, 1920 in all
+    q, pages = check_select(nm, c, [h], [120], 16, L - 1, 3)
+    check(nm, c, [h], [120], 16, L - 1, q=q, pages=pages)
+    assert int(c.tables[0, 0]) == n - 4 and (n - 4) * per > 1 << 32
