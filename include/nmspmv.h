@@ -706,8 +706,9 @@ nm_status nm_kv8_read(const nm_kv8_cache *cache, int layer, const int32_t *seqs,
  *   pages: NULL, or device int32 [n_tokens][n_kv_heads][n_list]: for each new token and kv head the
  *          pages of its sequence that its query heads attend, as indices into the sequence's table
  *          row, ascending, -1 behind the last. Positions past the query's own are not attended, whatever is listed.
- *          An entry that is out of range of the sequence, or does not ascend, is passed over and
- *          reported (NM_ERR_BOUNDS). A query with nothing listed gives out 0 and lse -inf.
+ *          The first -1 ends a list: what stands behind it is neither attended nor reported. Before the end an entry
+ *          that is out of range of the sequence, or not above every entry before it that is in range, is passed over
+ *          and reported (NM_ERR_BOUNDS). A query with nothing listed gives out 0 and lse -inf.
  *   n_list: 1 .. 49152 (with pages; NM_ERR_UNSUPPORTED above). max_new is not used then.
  * q is scaled by a power of two for each row. For few query rows and over listed pages it is held in fp16: exact down
  * to 2^-17 of the row's largest magnitude, off by at most 2^-25 of it below. For prompts it is held in two 8-bit

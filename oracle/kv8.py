@@ -146,3 +146,17 @@ def attention(q, K, V, length, scale, pages=None, P=0):
             out[i, h * r:(h + 1) * r], lse[i, h * r:(h + 1) * r] = o[0], l[0]
             A[i, h * r:(h + 1) * r], B[i, h * r:(h + 1) * r] = a[0], b[0]
     return out, lse, A, B
+
+
+def listed(entries, count):
+    """The entries of one list that count, for a sequence of `count` pages, and whether others are reported: the first -1
+    ends it; before that, those in range and above all in range before them."""
+    taken, faults = [], False
+    for e in entries:
+        if e == -1:
+            break
+        if 0 <= e < count and (not taken or e > taken[-1]):
+            taken.append(int(e))
+        else:
+            faults = True
+    return taken, faults

@@ -98,21 +98,54 @@ __device__ __forceinline__ int find(const int64_t *pre, int n, int64_t x)
     return lo;
 }
 
-// The cell that entry x of a list's cells names: its address, or 0, and the position it begins at. Lists ascend,
-// with -1 only behind; what is listed beyond the query is not seen. most: tokens of the sequence.
-template <int D>
+// Which entries of a list count: the first -1 ends it; before that, those that are pages of the sequence (of `most`
+// tokens) and above all that count before them. Others before the end are passed over and reported.
+__device__ __forceinline__ bool is_page(const Kv4 &c, int index, int most)
+{
+    return index >= 0 && (int64_t)index << c.page_shift < most;
+}
+// Entry j (`index`) is as it should be behind an entry that is. If all up to j are, j counts unless it is -1.
+__device__ __forceinline__ bool in_order(const Kv4 &c, const int32_t *list, int j, int index, int most)
+{
+    const int before = j > 0 ? list[j - 1] : -1;
+    return index == -1 || (is_page(c, index, most) && (j == 0 || (before >= 0 && before < index)));
+}
+// Whether entry j of any list counts, from the entries before it: for lists that are not in order.
+__device__ __forceinline__ bool counts(const Kv4 &c, const int32_t *list, int j, int most)
+{
+    int top = -1; // the last one that counts
+#pragma unroll 1
+    for (int x = 0; x < j; ++x) {
+        const int index = list[x];
+        if (index == -1)
+            return false;
+        if (is_page(c, index, most))
+            top = max(top, index);
+    }
+    const int index = list[j];
+    const bool yes = index > top && is_page(c, index, most);
+    if (!yes && index != -1)
+        kv4_bad(c);
+    return yes;
+}
+// The same as a call: in the kernel for many lists it costs fewer registers of the loop (512 tokens with their selection
+// 139.5 us, inlined 142.6), in the one for few rows more (80 tokens of 128 heads 50.5, inlined 49.5).
+__device__ __noinline__ bool counts_apart(const Kv4 &c, const int32_t *list, int j, int most)
+{
+    return counts(c, list, j, most);
+}
+
+// The cell that entry x of a list's cells names (in entry `index` of the list): its address, or 0, and the position it
+// begins at. What is listed beyond the query is not seen. most: tokens of the sequence; ordered: in_order holds up to the entry.
+template <int D, bool kApart>
 __device__ __forceinline__ uint64_t listed_cell(const Kv4 &c, int row, const uint8_t *heads, const int32_t *list, int x,
-                                                int most, int limit, int *begins)
+                                                int index, bool ordered, int most, int limit, int *begins)
 {
     const int shift = c.page_shift - 4, cell = x & ((1 << shift) - 1);
-    const int32_t *const at = list + (x >> shift);
-    const int index = at[0];
-    const bool rises = x >> shift == 0 || (at[-1] >= 0 && at[-1] < index);
-    if (index < 0 || !rises || (int64_t)index << c.page_shift >= most) {
-        if (index != -1)
-            kv4_bad(c);
+    if (index == -1)
         return 0;
-    }
+    if (!ordered && !(kApart ? counts_apart(c, list, x >> shift, most) : counts(c, list, x >> shift, most)))
+        return 0;
     *begins = (index << c.page_shift) + (cell << 4);
     if (*begins >= limit)
         return 0;
@@ -534,13 +567,22 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
         uint64_t where = 0;
         int begins = 0;
         uint32_t have = 0;
+        bool ordered = true; // (lists) the entries up to the piece's last one: of a few each warp looks at all of them
+        if constexpr (kListed) {
+            const int n = ((c1 - 1) >> shift) + 1, step = n > 32 ? kThreads : 32;
+            bool odd = false;
+            for (int j = tid & (step - 1); s.len > 0 && j < n; j += step)
+                odd |= !in_order(c, a.pages + list, j, a.pages[list + j], most);
+            ordered = !(n > 32 ? __syncthreads_or(odd) : __any_sync(~0u, odd));
+        }
         const auto fetch = [&](int x) {
             if ((x & 31) == 0) {
                 const int cell = c0 + warp + (x + lane) * kWarps;
                 where = 0;
                 if (x + lane < mine) {
                     if (kListed) {
-                        where = listed_cell<D>(c, s.row, heads, a.pages + list, cell, most, s.len, &begins);
+                        where = listed_cell<D, false>(c, s.row, heads, a.pages + list, cell, a.pages[list + (cell >> shift)],
+                                                      ordered, most, s.len, &begins);
                     } else if (cell * kKv4Cell < s.len) {
                         begins = cell * kKv4Cell;
                         const int page = kv4_page(c, s.row, cell >> shift);
@@ -847,13 +889,16 @@ __global__ void __launch_bounds__(Lists<D, NT>::kThreads, 1) kv8_lists_kernel(co
         uint64_t where = 0;
         int begins = kAbsent;
         uint32_t have = 0;
+        bool ordered = true; // the list's entries so far
         const auto fetch = [&](int x) {
             const int z = C * x;
             if ((z & 31) == 0) {
                 where = 0;
                 begins = kAbsent;
+                const int j = min(z + lane, cells - 1) >> shift, index = list[j];
+                ordered = !__any_sync(~0u, !ordered || !in_order(c, list, j, index, most));
                 if (z + lane < cells)
-                    where = listed_cell<D>(c, s.row, heads, list, z + lane, most, limit, &begins);
+                    where = listed_cell<D, true>(c, s.row, heads, list, z + lane, index, ordered, most, limit, &begins);
                 if (where == 0)
                     begins = kAbsent;
                 // nothing is listed from here on

@@ -1,0 +1,90 @@
+"""Calls of the 8-bit paged cache at the edges of what its header allows, on a GPU: lists of pages that are not in order,
+selection over many pages, values far below their neighbours' and queries far above. Tolerances as in test_gpu_kv8.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv8 as ref
+from tests.test_gpu_kv4 import f32, f64, ints, starts_of, values
+from tests.test_gpu_kv8 import make, nm  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def right(got, lse, q, K, V, scale, listed=None, P=0, more=0.0):
+    """One token's out [H][D] and lse [H] over positions 0 .. len(K) - 1 (those in the listed pages alone): within
+    the tolerances; more: what else a channel of out may be off by."""
+    K, V = K.astype(np.float64), V.astype(np.float64)
+    lists = None if listed is None else np.array(listed, dtype=int).reshape(1, K.shape[1], -1)
+    o, l, A, B = ref.attention(f64(q[None]), K, V, len(K), scale, lists, P)
+    e = 2.0 ** -16 * B + 2.0 ** -15
+    # weights below fp16's normal range: 2^-25 of codes up to 448 under a weight of at least 2^6, with the scale of the heaviest block
+    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e[..., None] + 2.0 ** -14) * A + len(K) * (2.0 ** -30 * np.abs(V).max() + 2.0 ** -46) + more
+    seen = np.isfinite(l)
+    gl, go = f64(lse[None]), f64(got[None])
+    return np.array_equal(np.isneginf(gl), np.isneginf(l)) and np.all(go[~seen] == 0) and \
+        np.all(np.abs(gl[seen] - l[seen]) <= e[seen]) and np.all(np.abs(go - o)[seen] <= tol[seen])
+
+
+def many(Hk):
+    """So many tokens that a warp takes each list by itself (kv8_launch_attention: from five lists an SM on)."""
+    return -(-5 * torch.cuda.get_device_properties(0).multi_processor_count // Hk) + 3
+
+
+LISTS = [[0, 3, 9], [1, 4, 2, 4], [1, 1 << 20, 5], [1, -2, 5], [0, -1, 7, 9], [9, 3, 5, 9, 10], [2, 2, 2, 3], [7, "end", 8],
+         [-1, 3], [5, 1 << 30, -(1 << 31), 6], [-7, 2, 3], ["last", 3], [0, 1, "last", 2, "last", "end"], [3] + [-1] * 10 + [4]]
+
+
+@pytest.mark.parametrize("D,P,Hq", [(128, 64, 8), (64, 16, 4), (128, 16, 13)])
+@pytest.mark.parametrize("each", [False, True])
+def test_entries_that_count(nm, D, P, Hq, each):
+    """Lists out of order and range, with good entries behind bad ones and entries behind the end: what counts, and what
+    is reported, is the same in the kernel for few lists and in that for many."""
+    n, m = 20 * P + 5, 12
+    T = many(1) if each else 5
+    if n < T + 4 * P:
+        n = T + 20 * P
+    count = -(-n // P)
+    c, held = make(nm, [n], P=P, L=1, Hk=1, D=D, seed=n)
+    q = values(T, Hq, D, 7)
+    starts = starts_of([T])
+    for x in LISTS:
+        bad = [{"last": count - 1, "end": count}.get(e, e) for e in x] + [-1] * (m - len(x))
+        taken, faults = ref.listed(bad, count)
+        pages = torch.full((T, 1, m), -1, dtype=torch.int32, device="cuda")
+        pages[:, 0, :3] = ints([0, 1, 2])
+        at = [0, T - 1]
+        for t in at:
+            pages[t, 0] = ints(bad)
+        out, lse = c.attention(0, q, starts=starts, pages=pages, lse=True)
+        assert nm.device_status() == (nm.NM_ERR_BOUNDS if faults else nm.NM_OK), x
+        for t in at:
+            k = n - T + t + 1
+            assert right(out[t], lse[t], q[t], held[0].k[:k], held[0].v[:k], D ** -0.5, taken or [-1], P), (x, t)
+        k = n - T + 2
+        assert right(out[1], lse[1], q[1], held[0].k[:k], held[0].v[:k], D ** -0.5, [0, 1, 2], P), x
+
+
+@pytest.mark.parametrize("D,P,Hk,Hq", [(128, 16, 1, 8), (64, 32, 1, 16)])
+@pytest.mark.parametrize("each", [False, True])
+def test_long_lists_out_of_order(nm, D, P, Hk, Hq, each):
+    """Hundreds of entries, of which an early one decides what counts much later (in another piece of the list)."""
+    m = 300
+    n = m * P - 3
+    T = many(Hk) if each else 3
+    c, held = make(nm, [n], P=P, L=1, Hk=Hk, D=D, seed=P)
+    q = values(T, Hq, D, 8)
+    starts = starts_of([T])
+    for at, value in ((40, 250), (0, 299), (299, 298), (170, -5), (100, -1), (250, 3)):
+        bad = np.arange(m)
+        bad[at] = value
+        taken, faults = ref.listed(bad, m)
+        pages = torch.zeros(T, Hk, m, dtype=torch.int32, device="cuda")
+        pages[:, :, 1:] = -1
+        pages[T - 1] = torch.from_numpy(bad.astype(np.int32)).cuda()
+        out, lse = c.attention(0, q, starts=starts, pages=pages, lse=True)
+        assert nm.device_status() == (nm.NM_ERR_BOUNDS if faults else nm.NM_OK), (at, value)
+        assert right(out[T - 1], lse[T - 1], q[T - 1], held[0].k, held[0].v, D ** -0.5, taken, P), (at, value)
+        o2, l2 = c.attention(0, q, starts=starts, pages=pages, lse=True)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+        nm.device_status()
