@@ -103,8 +103,8 @@ nm_status nm_kv8_attention(const nm_kv8_cache *cache, int layer, const int32_t *
 {
     NvtxRange nvtx_("nm_kv8_attention");
     KvCall o;
-    nm_status s = kv_attention_args(kFormat, &o, cache, layer, starts, n_seqs, n_tokens, max_new, q_bf16, q_stride,
-                                    n_q_heads, scale, out_bf16, out_stride, lse);
+    nm_status s = kv_attention_args(kFormat, &o, cache, layer, starts, n_seqs, n_tokens, pages ? 1 : max_new, q_bf16,
+                                    q_stride, n_q_heads, scale, out_bf16, out_stride, lse);
     if (s != NM_OK || o.done || (pages && (s = check_pages(cache, pages, n_list)) != NM_OK) ||
         (s = kv_open(kFormat, &o, cache, seqs, starts, n_seqs, n_tokens)) != NM_OK)
         return s;

@@ -146,3 +146,13 @@ def test_reference_selection_bounds_the_scores():
         assert bound >= (K.k[16 * z:16 * z + 16, 0] @ q.T).max(0).sum()
     got = ref.select(q.astype(np.float32), K.k, 16, 6, 1, 2)
     assert got.shape == (1, 6) and got[0, 0] == 0 and list(got[0, -2:]) == [18, 19] and np.all(np.diff(got[0]) > 0)
+
+
+def test_max_new_is_not_looked_at_with_pages(nm):
+    """What such a call is refused for is something else of it."""
+    c = cache(nm)
+    for most in (0, -1, 1):
+        assert attend(nm, c, most=most, pages=P + 2, m=1) == nm.NM_ERR_ALIGN
+        assert attend(nm, c, most=most, pages=P, m=0) == nm.NM_ERR_INVALID_ARG
+        assert attend(nm, c, most=most, pages=P, m=49153) == nm.NM_ERR_UNSUPPORTED
+    assert attend(nm, c, most=0, m=1) == nm.NM_ERR_INVALID_ARG
