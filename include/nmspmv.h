@@ -713,8 +713,9 @@ nm_status nm_kv8_read(const nm_kv8_cache *cache, int layer, const int32_t *seqs,
  * q is scaled by a power of two for each row. For few query rows and over listed pages it is held in fp16: exact down
  * to 2^-17 of the row's largest magnitude, off by at most 2^-25 of it below. For prompts it is held in two 8-bit
  * parts: exact down to 2^-13 of the row's largest, off by at most 2^-21 of it below. Scores are exact products of
- * that with the keys as held, summed in fp32. Weights are rounded to fp16 (2^-11) for the product with V, whose codes are
- * exact; for prompts they are brought to the largest scale S of 128 tokens, which takes away what is below 2^-25 S.
+ * that with the keys as held, summed in fp32. Weights, times their block's scale of V, are rounded to fp16 for the product
+ * with V's codes (2^-11 of them, or 2^-31 of the row's largest), which are exact; for prompts V is exact down to 2^-22 of
+ * the largest scale S of the 128 tokens it lies in (positions 128 i .. 128 i + 127), and off by at most 2^-32 S below.
  * Statistics and sums are held in fp32. A query row with a NaN or an infinity that sees any token gives NaN in its out and
  * lse and in no others. Results repeat bit for bit.
  */

@@ -13,9 +13,10 @@
 // down to 2^-13 of the row's largest): K's codes are an operand as they are stored, at the 8-bit rate, and no thread
 // has to make them fp16. S carries the fp32 rounding of the sums, as in the kernel for few rows.
 // The scales are powers of two of each cell (16 tokens). K's multiplies the scores in the softmax. V's codes are
-// made fp16 and brought to the largest of the block's eight scales, 2^e (d: how many binary places a cell's scale is
-// below it; exact down to 2^-15 of that), which is an exponent of the weights; the sums of the weights are freed of it
-// a block at a time.
+// made fp16 and brought to one scale for the block, 2^e, a 128th of the largest of its eight (which keeps them below
+// 448 * 2^7, in fp16's range; d: how many binary places a cell's scale is below it), which is an exponent of the weights; the
+// sums of the weights are freed of it a block at a time. A row may see only tokens whose scales are far below that of a later
+// one: codes are exact down to 2^-22 of the block's largest scale, and off by at most 2^-32 of it beyond.
 //
 // Roles (16 warps): two softmax warpgroups, one per tile (a thread owns a row: no
 // reductions across threads; it also loads and splits its row of Q, rescales and
@@ -70,22 +71,22 @@ template <int D> struct Cfg {
 };
 
 // The scales of a block, in shared memory: K's of each cell (1 where there is none), the exponent of
-// V's largest and 2^-that, and which cells are not there.
+// V's one and 2^-that, and which cells are not there.
 struct BlockScales {
     float k[8];
     float ev, iv;
     uint32_t gaps, pad;
 };
-// Two codes as fp16, times a power of two of at most 1: V's scale in its cell over the block's largest. Exact
-// down to 2^-15 of that; beyond, what is below 2^-24 of it is rounded.
+// Two codes as fp16, times a power of two of at most 2^7: V's scale in its cell over the block's one. Exact
+// down to 2^-15 of that; beyond, it is rounded to 2^-24 of it.
 __device__ __forceinline__ uint32_t decode_by(uint32_t two, __half2 by) { return as_u32(__hmul2(as_half2(kv8_decode(two)), by)); }
-// The largest of the scales of V that lanes 0 .. 7 have (0: none; 1 if all are).
-__device__ __forceinline__ float largest_of(float v)
+// V's one scale of a block: a 128th of the largest that lanes 0 .. 7 have (0: none; 1 if all are).
+__device__ __forceinline__ float common_scale(float v)
 {
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1)
         v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-    return v > 0.0f ? v : 1.0f;
+    return v > 0.0f ? v * 0x1p-7f : 1.0f;
 }
 __device__ __forceinline__ float pow2_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prompt_kernel(const Kv4 c, co
                 copy_block<D>(where, c.pool, tiles + C::kOffK + st * C::kK, tiles + C::kOffRaw + st * C::kK, u);
                 async_copies_arrive(smem_addr(&sh.k_full[st]));
                 async_copies_arrive(smem_addr(&sh.raw_full[st]));
-                const float v = largest_of(scales.y);
+                const float v = common_scale(scales.y);
                 if (u < 32) {
                     BlockScales &bs = sh.scales[n & 3];
                     const uint32_t gaps = __ballot_sync(~0u, scales.x == 0.0f) & 0xFFu;

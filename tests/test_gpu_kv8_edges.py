@@ -88,3 +88,34 @@ def test_long_lists_out_of_order(nm, D, P, Hk, Hq, each):
         o2, l2 = c.attention(0, q, starts=starts, pages=pages, lse=True)
         assert torch.equal(o2, out) and torch.equal(l2, lse)
         nm.device_status()
+
+
+def held_cache(nm, k, v, P, extra=1):
+    """A cache of one sequence and layer that holds k and v: (cache, ref.Sequence)."""
+    n, Hk, D = k.shape
+    c = nm.Kv8Cache(-(-n // P) + extra, P, 1, Hk, D, 1, -(-n // P) + extra)
+    c.pool.fill_(0xFF)
+    c.reserve(starts=ints([0, n]))
+    c.append(0, k, v, starts=ints([0, n]))
+    h = ref.Sequence(Hk, D)
+    h.append(f32(k), f32(v))
+    return c, h
+
+
+@pytest.mark.parametrize("D,small", [(128, 1e-4), (64, 1e-4), (128, 3e-6)])
+@pytest.mark.parametrize("max_new", [1, 160])
+def test_values_far_below_later_ones(nm, D, small, max_new):
+    """The first 64 tokens have small values, the next ones, of the same 128, the largest there are: rows that see the first
+    alone are right all the same. Off by at most 2^-32 of the largest scale more in the kernel for prompts."""
+    n, H, P = 200, 16, 16
+    k, v = values(n, 1, D, 1), values(n, 1, D, 2)
+    v[:64] = (v[:64].float() * small).bfloat16()
+    v[64:] = (v[64:].float() * 8000).bfloat16()
+    c, h = held_cache(nm, k, v, P)
+    assert h.e[4, 0, 1] == 7
+    q = values(160, H, D, 3)
+    out, lse = c.attention(0, q, starts=ints([0, 160]), max_new=max_new, lse=True)
+    assert nm.device_status() == nm.NM_OK
+    for t in (0, 5, 22, 23, 24, 60, 159):
+        m = n - 160 + t + 1
+        assert right(out[t], lse[t], q[t], h.k[:m], h.v[:m], D ** -0.5, more=2.0 ** -32 * 128 if max_new > 1 else 0.0), t
