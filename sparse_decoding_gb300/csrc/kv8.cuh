@@ -60,7 +60,7 @@ struct Kv8Row {
 __device__ __forceinline__ Kv8Row kv8_row(uint32_t top, float scale, bool sees)
 {
     const uint32_t field = top >> 23;
-    const uint32_t e = field == 0xFFu || field == 0 ? 127u : field > 250u ? 250u : field < 8u ? 8u : field;
+    const uint32_t e = field == 0xFFu || field == 0 ? 127u : field < 8u ? 8u : field;
     const float up = __uint_as_float((e - 7u) << 23), down = __uint_as_float((261u - e) << 23);
     Kv8Row r;
     r.down = scale < 0.0f ? -down : down;

@@ -119,3 +119,21 @@ def test_values_far_below_later_ones(nm, D, small, max_new):
     for t in (0, 5, 22, 23, 24, 60, 159):
         m = n - 160 + t + 1
         assert right(out[t], lse[t], q[t], h.k[:m], h.v[:m], D ** -0.5, more=2.0 ** -32 * 128 if max_new > 1 else 0.0), t
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("max_new", [1, 100, 0])
+def test_queries_up_to_the_largest_number(nm, D, max_new):
+    """q up to 2^128 with a scale that makes its scores ordinary, in each kernel (0: over lists)."""
+    n, H, P = 150, 16, 16
+    k, v = values(n, 1, D, 4, 0.01), values(n, 1, D, 5)
+    c, h = held_cache(nm, k, v, P)
+    g = torch.Generator().manual_seed(6)
+    q = (torch.randn(100, H, D, generator=g) * 2.0 ** 126).clamp(-3.3e38, 3.3e38).bfloat16().cuda()
+    pages = torch.arange(10, dtype=torch.int32, device="cuda").expand(100, 1, 10).contiguous()
+    kw = dict(pages=pages) if max_new == 0 else dict(max_new=max_new)
+    out, lse = c.attention(0, q, starts=ints([0, 100]), scale=2.0 ** -126, lse=True, **kw)
+    assert nm.device_status() == nm.NM_OK and bool((q.float().abs() > 2.0 ** 127).any())
+    for t in (0, 50, 99):
+        m = n - 100 + t + 1
+        assert right(out[t], lse[t], q[t], h.k[:m], h.v[:m], 2.0 ** -126), t
