@@ -64,8 +64,9 @@ __device__ __forceinline__ Kv8Row kv8_row(uint32_t top, float scale, bool sees)
     const float up = __uint_as_float((e - 7u) << 23), down = __uint_as_float((261u - e) << 23);
     Kv8Row r;
     r.down = scale < 0.0f ? -down : down;
-    // above 0, so that masked scores stay -inf
-    r.factor = field == 0xFFu && sees ? __uint_as_float(0x7FC00000u) : fmaxf(up * (fabsf(scale) * 1.4426950408889634f), 1e-30f);
+    // above 0, so that masked scores stay -inf; finite, K's scale of up to 2^7 with it, so that scores of 0 stay 0
+    r.factor = field == 0xFFu && sees ? __uint_as_float(0x7FC00000u)
+                                      : fminf(fmaxf(up * (fabsf(scale) * 1.4426950408889634f), 1e-30f), 0x1.fffffep120f);
     return r;
 }
 // Eight channels: two words of each part.

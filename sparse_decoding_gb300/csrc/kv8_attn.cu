@@ -192,8 +192,9 @@ __device__ __forceinline__ float split_q(const uint4 (&qw)[D / 64][2], float sca
             const float *const y = &x[e][4 * f];
             put(4 * e + f, make_uint2(pack_half2(y[0] * down, y[1] * down), pack_half2(y[2] * down, y[3] * down)));
         }
-    // above 0, so that masked scores stay -inf
-    return field == 0xFFu && sees ? __uint_as_float(0x7FC00000u) : fmaxf(up * (fabsf(scale) * kLog2e), 1e-30f);
+    // above 0, so that masked scores stay -inf; finite, so that scores of 0 stay 0
+    return field == 0xFFu && sees ? __uint_as_float(0x7FC00000u)
+                                  : fminf(fmaxf(up * (fabsf(scale) * kLog2e), 1e-30f), 0x1.fffffep127f);
 }
 
 // What a warp keeps of its rows (lane (g, t): rows 8 j + 2 t + n), and a cell's part in it.

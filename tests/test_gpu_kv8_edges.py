@@ -137,3 +137,21 @@ def test_queries_up_to_the_largest_number(nm, D, max_new):
     for t in (0, 50, 99):
         m = n - 100 + t + 1
         assert right(out[t], lse[t], q[t], h.k[:m], h.v[:m], 2.0 ** -126), t
+
+
+@pytest.mark.parametrize("max_new", [1, 100, 0])
+def test_large_scales_of_scores_that_are_zero(nm, max_new):
+    """Keys of zeros: any finite q and scale give even weights."""
+    n, H, D, P = 150, 16, 128, 16
+    v = values(n, 1, D, 5)
+    c, h = held_cache(nm, torch.zeros_like(v), v, P)
+    q = (values(100, H, D, 6).float() * 2.0 ** 120).bfloat16()
+    q[:, ::2] *= 2.0 ** -130
+    pages = torch.arange(10, dtype=torch.int32, device="cuda").expand(100, 1, 10).contiguous()
+    kw = dict(pages=pages) if max_new == 0 else dict(max_new=max_new)
+    for scale in (2.0 ** 100, -2.0 ** 127, 1.0):
+        out, lse = c.attention(0, q, starts=ints([0, 100]), scale=scale, lse=True, **kw)
+        for t in (0, 99):
+            m = n - 100 + t + 1
+            assert right(out[t], lse[t], q[t] * 0, h.k[:m], h.v[:m], 1.0), (scale, t)
+    assert nm.device_status() == nm.NM_OK
