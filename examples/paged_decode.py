@@ -34,8 +34,8 @@ class Decoder:
 
     def __init__(self, layers=2, hidden=1024, heads=8, kv_heads=2, dim=128, ffn=2048, sequences=4, tokens=512, page=16,
                  seed=0, device="cuda", bits=4, pages=0):
-        if pages and bits != 8:
-            raise ValueError("pages are selected in the 8-bit cache")
+        if pages < 0 or (pages and bits != 8):
+            raise ValueError("pages are selected in the 8-bit cache, at least one")
         self.heads, self.kv_heads, self.dim, self.pages = heads, kv_heads, dim, pages
         max_pages = -(-tokens // page)
         self.cache = (nm.Kv8Cache if bits == 8 else nm.Kv4Cache)(sequences * max_pages, page, layers, kv_heads, dim, sequences, max_pages, device=device)
@@ -71,7 +71,8 @@ class Decoder:
             if trace is not None:
                 trace.append([q.clone(), k.clone(), v.clone()])
             c.append(i, k, v, q=q, rope=self.rope, seqs=seqs, starts=starts, q_out=q)
-            part = {"pages": c.select(i, q, self.pages, seqs=seqs, starts=starts)} if self.pages else {}
+            # of a single page the token's own, else the first one too
+            part = {"pages": c.select(i, q, self.pages, seqs=seqs, starts=starts, first=min(1, self.pages - 1))} if self.pages else {}
             a = c.attention(i, q, seqs=seqs, starts=starts, max_new=1 if starts is None else x.shape[0], **part)
             if trace is not None:
                 trace[-1].append(a)

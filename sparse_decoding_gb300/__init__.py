@@ -674,7 +674,7 @@ class Kv8Cache(Kv4Cache):
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """The n pages of each new token and kv head (int32 [tokens][n_kv_heads][n], ascending, -1 behind) whose
         keys can have the largest scores with its query heads; the ``first`` pages of the sequence and the
-        ``last`` up to the token's own are always among them."""
+        ``last`` (at least one) up to the token's own are always among them: n >= first + last."""
         qp, qs, qh = self._tokens(q, "q")
         shape = (q.shape[0], self.n_kv_heads, n)
         if out is None:

@@ -155,3 +155,35 @@ def test_large_scales_of_scores_that_are_zero(nm, max_new):
             m = n - 100 + t + 1
             assert right(out[t], lse[t], q[t] * 0, h.k[:m], h.v[:m], 1.0), (scale, t)
     assert nm.device_status() == nm.NM_OK
+
+
+@pytest.mark.parametrize("pages", [1, 2])
+def test_example_with_few_pages(nm, pages):
+    """The example's loop with a single page a step, its last one, or the first and the last."""
+    from examples import paged_decode as ex
+    d = ex.Decoder(layers=1, hidden=256, heads=8, kv_heads=2, dim=64, ffn=512, sequences=2, tokens=80, page=16, seed=5, bits=8, pages=pages)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(8, 256, generator=g, device="cuda").bfloat16()
+    trace, one = [], ints([0])
+    for _ in range(5):
+        trace.append([])
+        d.step(x, one, starts=ints([0, 8]), trace=trace[-1])
+    rope = d.rope.cpu().numpy()
+    h = ref.Sequence(2, 64)
+    for step in trace:
+        (q, k, v, a), = step
+        q, k, v = (f32(t).reshape(8, -1, 64) for t in (q, k, v))
+        pos = np.arange(len(h.k), len(h.k) + 8)
+        cos, sin = rope[pos, :32], rope[pos, 32:]
+        h.append(ref.rotate(k, cos, sin), v)
+        q = torch.from_numpy(ref.bf16(ref.rotate(q, cos, sin)))
+    for t in range(8):  # of the last step: pages 0 .. 2
+        m = len(h.k) - 7 + t
+        last = (m - 1) // 16
+        K, V = h.k[:m].astype(np.float64), h.v[:m].astype(np.float64)
+        lists = np.array([[[last]] * 2 if pages == 1 else [[0, last]] * 2])
+        o, _, A, B = ref.attention(f64(q[t:t + 1]), K, V, m, 0.125, lists, 16)
+        e = 2.0 ** -16 * B[..., None] + 2.0 ** -15
+        tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e + 2.0 ** -14) * A + 1e-6
+        assert np.all(np.abs(f64(a[t]).reshape(o.shape) - o) <= tol), t
+    assert nm.device_status() == nm.NM_OK

@@ -156,3 +156,11 @@ def test_max_new_is_not_looked_at_with_pages(nm):
         assert attend(nm, c, most=most, pages=P, m=0) == nm.NM_ERR_INVALID_ARG
         assert attend(nm, c, most=most, pages=P, m=49153) == nm.NM_ERR_UNSUPPORTED
     assert attend(nm, c, most=0, m=1) == nm.NM_ERR_INVALID_ARG
+
+
+def test_example_refuses_pages_that_it_cannot_select():
+    """Before anything is put on a device."""
+    from examples import paged_decode as ex
+    for kw in (dict(bits=4, pages=2), dict(bits=8, pages=-1)):
+        with pytest.raises(ValueError):
+            ex.Decoder(**kw)
