@@ -187,3 +187,89 @@ def test_example_with_few_pages(nm, pages):
         tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * e + 2.0 ** -14) * A + 1e-6
         assert np.all(np.abs(f64(a[t]).reshape(o.shape) - o) <= tol), t
     assert nm.device_status() == nm.NM_OK
+# --- selection over many pages, whole lists of many query heads, tables ---------------------
+
+@pytest.mark.parametrize("new", [[1], [2], [5]])
+def test_select_many_pages_by_a_cluster(nm, new):
+    """Head size 128: more pages than the CTAs of a cluster score in one turn of their loop."""
+    D, P, n = 128, 16, 40000
+    c, held = make(nm, [n], P=P, L=1, Hk=1, D=D, seed=60)
+    q = values(new[0], 4, D, 61)
+    for m, first, last in ((100, 2, 3), (1999, 0, 1), (2, 1, 1)):
+        pages = c.select(0, q, m, starts=starts_of(new), first=first, last=last)
+        for t in {0, new[0] - 1}:
+            want = ref.select(f32(q[t]), held[0].k[:n - new[0] + t + 1], P, m, first, last)
+            np.testing.assert_array_equal(pages[t].cpu().numpy(), want)
+    assert nm.device_status() == nm.NM_OK
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_select_many_pages_by_a_cta(nm, D):
+    """So many tokens and kv heads that each has one CTA, with more pages than it scores in one turn of its loop."""
+    P, Hk, n, S = 16, 8, 9000, 40
+    c, held = make(nm, [n], P=P, L=1, Hk=Hk, D=D, seed=62)
+    q = values(S, 16, D, 63)
+    seqs = torch.zeros(S, dtype=torch.int32, device="cuda")  # one sequence, listed often
+    for m in (2, 150):
+        pages = c.select(0, q, m, seqs=seqs)
+        for t in (0, 39):
+            np.testing.assert_array_equal(pages[t].cpu().numpy(), ref.select(f32(q[t]), held[0].k, P, m, 1, 1))
+    assert nm.device_status() == nm.NM_OK
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 3], [200, 100]])
+def test_select_long_sequences(nm, new):
+    """Head size 128 and hundreds of pages, by clusters, CTAs and tiles of tokens."""
+    D, P, Hk, n = 128, 16, 2, 150
+    lens = [9000, 8000]
+    c, held = make(nm, lens, P=P, L=1, Hk=Hk, D=D, seed=64)
+    q = values(sum(new), 8, D, 65)
+    pages = c.select(0, q, n, starts=starts_of(new))
+    at = 0
+    for s, w in enumerate(new):
+        for t in sorted({0, w // 2, w - 1}):
+            want = ref.select(f32(q[at + t]), held[s].k[:lens[s] - w + t + 1], P, n, 1, 1)
+            np.testing.assert_array_equal(pages[at + t].cpu().numpy(), want)
+        at += w
+    assert nm.device_status() == nm.NM_OK
+
+
+@pytest.mark.parametrize("D,tokens,Hq", [(128, 700, 32), (64, 700, 40), (128, 250, 64)])
+def test_lists_of_many_query_heads(nm, D, tokens, Hq):
+    """More than 16 query heads to a kv head: tiles of a list's rows, more tiles than CTAs, and lists of more than 32
+    cells: whole ones, or ones that an even cut goes through."""
+    P, n, m = 64, 1500, 9
+    c, held = make(nm, [n], P=P, L=1, Hk=1, D=D, seed=66)
+    q = values(tokens, Hq, D, 67)
+    pages = c.select(0, q, m, starts=starts_of([tokens]))
+    pages[3, 0, 1:] = -1
+    pages[tokens - 1] = -1
+    out, lse = c.attention(0, q, starts=starts_of([tokens]), pages=pages, lse=True)
+    for t in (0, 1, 3, tokens // 2, tokens - 2, tokens - 1):
+        k = n - tokens + t + 1
+        assert right(out[t], lse[t], q[t], held[0].k[:k], held[0].v[:k], D ** -0.5, pages[t].cpu().numpy(), P), t
+    o2, l2 = c.attention(0, q, starts=starts_of([tokens]), pages=pages, lse=True)
+    assert torch.equal(out, o2) and torch.equal(lse, l2) and nm.device_status() == nm.NM_OK
+
+
+def test_damaged_tables_are_reported_by_each_kernel(nm):
+    """A page that is none of the pool's: each of the attention's kernels reports it and answers another sequence as before."""
+    D, P, H = 128, 16, 8
+    c, held = make(nm, [1200, 300], P=P, L=1, Hk=1, D=D, seed=68)
+    few, some, each = values(2, H, D, 69), values(300, H, D, 70), values(many(1), H, D, 71)
+    calls = {"rows": lambda: c.attention(0, few, max_new=1),
+             "prompt": lambda: c.attention(0, some, starts=starts_of([200, 100])),
+             "lists of few": lambda: c.attention(0, few, pages=lists[:2]),
+             "lists of many": lambda: c.attention(0, each, starts=starts_of([each.shape[0] - 100, 100]), pages=lists[2:])}
+    lists = torch.cat([c.select(0, few, 5), c.select(0, each, 5, starts=starts_of([each.shape[0] - 100, 100]))])
+    good = {x: f() for x, f in calls.items()}
+    assert nm.device_status() == nm.NM_OK
+    c.tables[1, 18], c.tables[1, 0] = -7, c.n_pages
+    for x, f in calls.items():
+        bad = f()
+        assert nm.device_status() == nm.NM_ERR_BOUNDS, x
+        first = 1 if bad.shape[0] == 2 else bad.shape[0] - 100  # rows of sequence 0
+        assert torch.equal(bad[:first], good[x][:first]) and bool(torch.isfinite(bad).all()), x
+        assert not torch.equal(bad[first:], good[x][first:]), x
+    c.select(0, few, 5)
+    assert nm.device_status() == nm.NM_ERR_BOUNDS
