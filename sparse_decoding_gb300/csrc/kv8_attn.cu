@@ -1043,8 +1043,13 @@ nm_status kv8_launch_attention(const Kv4 &c, const Kv4Batch &b, const Kv4Attn &a
     // Figures: head size 128, 8 kv heads, us.
     if (pages) {
         // 16 pages of 64 tokens, a CTA per piece of a list against a warp per list. 32 heads: 20 tokens 14 against 23; 80: 35,
-        // 37; 110: 43, 38; 160: 60, 45; 512: 166, 116. 128 heads: 40 tokens 31 against 37; 80: 48, 47; 110: 61, 48; 512: 226, 172.
-        // More than 16 query heads to a kv head are several tiles, which that kernel does not cut.
+        // 37; 112: 44, 37; 160: 61, 44; 512: 164, 113. 128 heads: 40 tokens 32 against 36; 96: 56, 47; 112: 65, 48; 512: 234, 172.
+        // Head size 64, 32 heads: 80 tokens 32 against 30; 112: 41, 30; 512: 145, 91. Other lists of 32 heads at 112 tokens: 8 pages
+        // of 16 tokens 16 against 9; 64 of 16 46, 38; 4 of 64 19, 13; 8 of 128 44, 36; where half of the lists have two pages of
+        // 16, at 160 tokens 59, 44. Lists of more than a hundred cells would stay with CTAs a little longer: 64 pages of 64 tokens
+        // at 112 tokens 114 against 136; 160: 178, 162; 512: 494, 427; of 128 heads 160: 239, 301; 512: 665, 648.
+        // More than 16 query heads to a kv head are several tiles, which that kernel does not cut (512 tokens of 256 heads:
+        // 9, 16, 64 pages of 64 tokens 333, 450, 1282).
         const int rows = a.ratio;
         if (rows <= 16 && b.n_tokens * c.n_kv_heads >= 5 * (int64_t)w.num_sms) {
             if (c.head_dim == 64)

@@ -496,7 +496,9 @@ nm_status kv8_launch_select(const Kv4 &c, const Kv4Batch &b, const Kv8Select &x,
     const SelectArgs a{x.layer, x.n_q_heads / c.n_kv_heads, x.count, x.first, x.last, (const uint16_t *)x.q, x.q_stride, x.pages, 0, 1};
     // Tiles of tokens when there are two tokens and kv heads to an SM, and their scores fit. A CTA each against tiles, us,
     // 8 kv heads: 20 tokens (256 pages) 9.8, 12.2; 4 x 5 tokens (up to 512) 14.7, 17.5; 40 tokens (256) 15.8, 12.1; 8 x 5 (32)
-    // 15.1, 8.8.
+    // 15.1, 8.8. The scores of a tile stand in shared memory by the table's width, not the lengths: 512 tokens of 264 pages take
+    // 27 us in tables of up to 3200, 43 from there (one CTA an SM) and 121 above 6141 pages, where there are no tiles; of 6000 pages
+    // 522 in a table of 6141, 1112 in one of 6142.
     if (b.starts && b.n_tokens * c.n_kv_heads >= 2 * (int64_t)w.num_sms && (int64_t)kTile * (c.max_pages + 3) <= kKv8SelectPages)
         return c.head_dim == 128 ? launch<128, kTile, 1>(c, b, a, 1, w, st) : launch<64, kTile, 1>(c, b, a, 1, w, st);
     // The CTAs of a cluster share a token's pages while they are at most two to an SM and have 128 pages each. At most one to
