@@ -90,6 +90,22 @@ def test_long_lists_out_of_order(nm, D, P, Hk, Hq, each):
         nm.device_status()
 
 
+def test_lists_of_thousands(nm):
+    """A token's list of 3000 pages: in order, and with one entry that decides what counts a thousand later."""
+    D, P, m = 64, 16, 3000
+    n = m * P
+    c, held = make(nm, [n], P=P, L=1, Hk=1, D=D, seed=9)
+    q = values(1, 8, D, 10)
+    for at, value in ((0, 0), (100, 1500), (1100, 2), (2999, 2998), (2500, -1)):
+        bad = np.arange(m)
+        bad[at] = value
+        taken, faults = ref.listed(bad, m)
+        pages = torch.from_numpy(bad.astype(np.int32)).cuda().view(1, 1, m)
+        out, lse = c.attention(0, q, pages=pages, lse=True)
+        assert nm.device_status() == (nm.NM_ERR_BOUNDS if faults else nm.NM_OK), (at, value)
+        assert right(out[0], lse[0], q[0], held[0].k, held[0].v, D ** -0.5, taken, P), (at, value)
+
+
 def held_cache(nm, k, v, P, extra=1):
     """A cache of one sequence and layer that holds k and v: (cache, ref.Sequence)."""
     n, Hk, D = k.shape
