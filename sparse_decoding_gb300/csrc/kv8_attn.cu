@@ -109,42 +109,43 @@ __device__ __forceinline__ bool in_order(const Kv4 &c, int j, int before, int in
 {
     return index == -1 || (is_page(c, index, most) && (j == 0 || (before >= 0 && before < index)));
 }
-// Whether entry j of any list counts, from the entries before it: for lists that are not in order.
-__device__ __forceinline__ bool counts(const Kv4 &c, const int32_t *list, int j, int most)
+// Whether entry j counts (another j in each lane of a warp, up to `last`), of a list that need not be in order: it is followed from
+// entry `from` on, behind entries of which `top` is the last one that counts (-1: none, kEnded: the list has ended).
+constexpr int kEnded = 0x7FFFFFFF;
+__device__ __forceinline__ bool follow(const Kv4 &c, const int32_t *list, int from, int &top, int j, int last, int most)
 {
-    int top = -1; // the last one that counts
+    const int lane = threadIdx.x & 31;
+    bool yes = false;
 #pragma unroll 1
-    for (int x = 0; x < j; ++x) {
-        const int index = list[x];
-        if (index == -1)
-            return false;
-        if (is_page(c, index, most))
-            top = max(top, index);
+    for (int b = from; b <= last; b += 32) {
+        const int index = list[min(b + lane, last)];
+        const uint32_t ends = __ballot_sync(~0u, index == -1);
+        const bool open = b + lane <= last && top != kEnded && lane < (ends ? __ffs(ends) - 1 : 32);
+        int upto = open && is_page(c, index, most) ? index : -1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(~0u, upto, o);
+            upto = lane >= o ? max(upto, x) : upto;
+        }
+        const int x = __shfl_up_sync(~0u, upto, 1), before = lane > 0 ? max(top, x) : top;
+        const bool counts = open && index > before && is_page(c, index, most);
+        if (open && !counts)
+            kv4_bad(c);
+        const uint32_t all = __ballot_sync(~0u, counts);
+        yes = j >= b && j < b + 32 ? (all >> (j - b) & 1u) != 0 : yes;
+        const int most_here = __shfl_sync(~0u, upto, 31);
+        top = ends ? kEnded : max(top, most_here);
     }
-    const int index = list[j];
-    const bool yes = index > top && is_page(c, index, most);
-    if (!yes && index != -1)
-        kv4_bad(c);
     return yes;
 }
-// The same as a call: in the kernel for many lists it costs fewer registers of the loop (512 tokens with their selection
-// 139.5 us, inlined 142.6), in the one for few rows more (80 tokens of 128 heads 50.5, inlined 49.5).
-__device__ __noinline__ bool counts_apart(const Kv4 &c, const int32_t *list, int j, int most)
-{
-    return counts(c, list, j, most);
-}
 
-// The cell that entry x of a list's cells names (in entry `index` of the list): its address, or 0, and the position it
-// begins at. What is listed beyond the query is not seen. most: tokens of the sequence; ordered: in_order holds up to the entry.
-template <int D, bool kApart>
-__device__ __forceinline__ uint64_t listed_cell(const Kv4 &c, int row, const uint8_t *heads, const int32_t *list, int x,
-                                                int index, bool ordered, int most, int limit, int *begins)
+// The cell that entry x of a list's cells names, in its entry `index`, which counts: its address, or 0, and the position it
+// begins at. What is listed beyond the query is not seen.
+template <int D>
+__device__ __forceinline__ uint64_t listed_cell(const Kv4 &c, int row, const uint8_t *heads, int x, int index, int limit,
+                                                int *begins)
 {
-    const int shift = c.page_shift - 4, cell = x & ((1 << shift) - 1);
-    if (index == -1)
-        return 0;
-    if (!ordered && !(kApart ? counts_apart(c, list, x >> shift, most) : counts(c, list, x >> shift, most)))
-        return 0;
+    const int cell = x & ((1 << (c.page_shift - 4)) - 1);
     *begins = (index << c.page_shift) + (cell << 4);
     if (*begins >= limit)
         return 0;
@@ -601,11 +602,19 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
             if ((x & 31) == 0) {
                 const int cell = c0 + warp + (x + lane) * kWarps;
                 where = 0;
-                if (x + lane < mine) {
-                    if (kListed) {
-                        where = listed_cell<D, false>(c, s.row, heads, a.pages + list, cell, a.pages[list + (cell >> shift)],
-                                                      ordered, most, s.len, &begins);
-                    } else if (cell * kKv4Cell < s.len) {
+                if constexpr (kListed) {
+                    const int32_t *const l = a.pages + list;
+                    bool counts = x + lane < mine;
+                    const int j = counts ? cell >> shift : 0, index = l[j];
+                    counts &= index != -1;
+                    if (!ordered) {
+                        int top = -1;
+                        counts &= follow(c, l, 0, top, j, __reduce_max_sync(~0u, j), most);
+                    }
+                    if (counts)
+                        where = listed_cell<D>(c, s.row, heads, cell, index, s.len, &begins);
+                } else if (x + lane < mine) {
+                    if (cell * kKv4Cell < s.len) {
                         begins = cell * kKv4Cell;
                         const int page = kv4_page(c, s.row, cell >> shift);
                         if (page >= 0)
@@ -911,16 +920,27 @@ __global__ void __launch_bounds__(Lists<D, NT>::kThreads, 1) kv8_lists_kernel(co
         uint64_t where = 0;
         int begins = kAbsent;
         uint32_t have = 0;
+        int top = -1;        // of a list that is not in order, the last entry so far that counts
         bool ordered = true; // the list's entries so far
         const auto fetch = [&](int x) {
             const int z = C * x;
             if ((z & 31) == 0) {
                 where = 0;
                 begins = kAbsent;
-                const int j = min(z + lane, cells - 1) >> shift, index = list[j];
-                ordered = !__any_sync(~0u, !ordered || !in_order(c, j, list[max(j - 1, 0)], index, most));
-                if (z + lane < cells)
-                    where = listed_cell<D, true>(c, s.row, heads, list, z + lane, index, ordered, most, limit, &begins);
+                const int j = min(z + lane, cells - 1) >> shift, index = list[j], before = list[max(j - 1, 0)];
+                bool counts = z + lane < cells && index != -1;
+                const bool odd = __any_sync(~0u, !in_order(c, j, before, index, most));
+                if (odd || !ordered) {
+                    const int from = z >> shift, last = __shfl_sync(~0u, j, 31);
+                    if (ordered && from > 0) { // up to here it is in order
+                        top = __shfl_sync(~0u, before, 0);
+                        top = top == -1 ? kEnded : top;
+                    }
+                    ordered = false;
+                    counts &= follow(c, list, from, top, j, last, most);
+                }
+                if (counts)
+                    where = listed_cell<D>(c, s.row, heads, z + lane, index, limit, &begins);
                 if (where == 0)
                     begins = kAbsent;
                 // nothing is listed from here on
